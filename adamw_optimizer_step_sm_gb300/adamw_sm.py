@@ -1,4 +1,5 @@
-"""Python binding of the adamw_sm C ABI (include/adamw_sm.h).
+"""Python binding of the adamw_sm C ABI (include/adamw_sm.h and
+include/adamw_losses.h).
 
 Argument marshalling only: every step of the optimizer runs in the library's
 CUDA kernels.  The functions keep the C names; a non-zero status raises
@@ -16,6 +17,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 from . import build as _build
 
@@ -49,6 +51,18 @@ ADAMW_ERR_NO_NORM = -4
 ADAMW_ERR_TOO_LARGE = -5
 ADAMW_ERR_NOT_ACCESSIBLE = -6
 
+# the fine-tuning operators (include/adamw_losses.h)
+DTYPE_BF16 = 0
+DTYPE_FP16 = 1
+DTYPE_FP32 = 2
+KL = {"k1": 1, "k2": 2, "k3": 3}
+REDUCE = {"token": 0, "sequence": 1, "fixed": 2}
+PREFERENCE = {"sigmoid": 0, "hinge": 1, "ipo": 2}
+REF_NONE = 0
+REF_TOKEN = 1
+REF_SEQUENCE = 2
+NORM = {"l2": 0, "max": 1}
+
 
 class AdamWError(RuntimeError):
     def __init__(self, status: int, where: str):
@@ -81,6 +95,37 @@ class adamw_chunk_t(ctypes.Structure):
     _fields_ = [("tensor", ctypes.c_int32), ("vec", ctypes.c_int32),
                 ("offset", ctypes.c_int64), ("len", ctypes.c_int64),
                 ("cta", ctypes.c_int32), ("pad_", ctypes.c_int32)]
+
+
+class adamw_rows_t(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("inner", ctypes.c_int64),
+                ("outer_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+                ("cols", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class adamw_tokens_t(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("sequences", ctypes.c_int64),
+                ("offsets", ctypes.c_void_p), ("mask", ctypes.c_void_p)]
+
+
+class adamw_policy_t(ctypes.Structure):
+    _fields_ = [("clip_low", ctypes.c_float), ("clip_high", ctypes.c_float),
+                ("dual_clip", ctypes.c_float), ("kl_coef", ctypes.c_float),
+                ("entropy_coef", ctypes.c_float), ("divisor", ctypes.c_float),
+                ("grad_scale", ctypes.c_float), ("kl", ctypes.c_int32),
+                ("reduce", ctypes.c_int32), ("advantage_per_token", ctypes.c_int32)]
+
+
+class adamw_preference_t(ctypes.Structure):
+    _fields_ = [("beta", ctypes.c_float), ("margin", ctypes.c_float),
+                ("label_smoothing", ctypes.c_float), ("grad_scale", ctypes.c_float),
+                ("kind", ctypes.c_int32), ("length_average", ctypes.c_int32),
+                ("ref", ctypes.c_int32)]
+
+
+class adamw_grad_t(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("src_dtype", ctypes.c_int32), ("dst_dtype", ctypes.c_int32)]
 
 
 _lock = threading.Lock()
@@ -120,6 +165,22 @@ def load() -> ctypes.CDLL:
             L.adamw_step_table.argtypes = [vp, i32, i32, ctypes.POINTER(adamw_hparams_t), i64,
                                            vp, vp, vp]
             L.adamw_step_table_cache_clear.argtypes = []
+            f32, P = ctypes.c_float, ctypes.POINTER
+            rows, tokens, policy = P(adamw_rows_t), P(adamw_tokens_t), P(adamw_policy_t)
+            L.adamw_token_logprob.argtypes = [rows, vp, i64, f32, vp, vp, vp, vp]
+            L.adamw_token_logprob_backward.argtypes = [rows, vp, i64, f32, vp, vp, vp, vp, rows, vp]
+            L.adamw_policy_loss.argtypes = [tokens, policy, *([vp] * 11)]
+            L.adamw_policy_loss_logits.argtypes = [rows, vp, i64, f32, tokens, policy,
+                                                   *([vp] * 7), rows, vp, vp]
+            L.adamw_preference_loss.argtypes = [tokens, P(adamw_preference_t), *([vp] * 8)]
+            L.adamw_clip_plan_create.argtypes = [P(adamw_grad_t), i32, P(vp)]
+            L.adamw_clip_grads.argtypes = [vp, f32, i32, vp, vp]
+            L.adamw_clip_plan_destroy.argtypes = [vp]
+            for name in ("adamw_policy_workspace", "adamw_policy_logits_workspace"):
+                getattr(L, name).argtypes = [i64, i64]
+                getattr(L, name).restype = i64
+            L.adamw_preference_workspace.argtypes = [i64]
+            L.adamw_preference_workspace.restype = i64
             L.adamw_status_string.argtypes = [ctypes.c_int]
             L.adamw_status_string.restype = ctypes.c_char_p
             for name in ("adamw_plan_create", "adamw_step", "adamw_grad_norm", "adamw_step_device",
@@ -127,7 +188,10 @@ def load() -> ctypes.CDLL:
                          "adamw_step_scalars", "adamw_copy_probe", "adamw_grad_norm_noalloc",
                          "adamw_step_table", "adamw_step_table_cache_clear",
                          "adamw_plan_device_status", "adamw_lr_linear_warmup_device",
-                         "adamw_plan_test_skew_barrier", "adamw_plan_test_corrupt_chunk"):
+                         "adamw_plan_test_skew_barrier", "adamw_plan_test_corrupt_chunk",
+                         "adamw_token_logprob", "adamw_token_logprob_backward",
+                         "adamw_policy_loss", "adamw_policy_loss_logits", "adamw_preference_loss",
+                         "adamw_clip_plan_create", "adamw_clip_grads", "adamw_clip_plan_destroy"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
         return _lib
@@ -272,6 +336,87 @@ def adamw_copy_probe(dst: int, src: int, nbytes: int, stream: int = 0) -> None:
     _check(load().adamw_copy_probe(dst, src, nbytes, stream or None), "adamw_copy_probe")
 
 
+# The C functions of adamw_losses.h.  rows, tokens, policy and pref are the
+# structures above; every other argument is a device address (0: NULL), a
+# number or a stream.  losses.py has them over torch tensors.
+
+def adamw_token_logprob(logits: adamw_rows_t, targets: int, ignore_index: int, scale: float, logp: int,
+                        entropy: int = 0, stats: int = 0, stream: int = 0) -> None:
+    rc = load().adamw_token_logprob(ctypes.byref(logits), targets, ignore_index, scale, logp,
+                                    entropy or None, stats or None, stream or None)
+    _check(rc, "adamw_token_logprob")
+
+
+def adamw_token_logprob_backward(logits: adamw_rows_t, targets: int, ignore_index: int, scale: float,
+                                 stats: int, entropy: int, d_logp: int, d_entropy: int,
+                                 d_logits: adamw_rows_t, stream: int = 0) -> None:
+    rc = load().adamw_token_logprob_backward(ctypes.byref(logits), targets, ignore_index, scale, stats,
+                                             entropy or None, d_logp, d_entropy or None,
+                                             ctypes.byref(d_logits), stream or None)
+    _check(rc, "adamw_token_logprob_backward")
+
+
+def adamw_policy_workspace(n: int, sequences: int) -> int:
+    return load().adamw_policy_workspace(n, sequences)
+
+
+def adamw_policy_logits_workspace(n: int, sequences: int) -> int:
+    return load().adamw_policy_logits_workspace(n, sequences)
+
+
+def adamw_preference_workspace(pairs: int) -> int:
+    return load().adamw_preference_workspace(pairs)
+
+
+def adamw_policy_loss(tokens: adamw_tokens_t, policy: adamw_policy_t, logp: int, old_logp: int,
+                      ref_logp: int, advantages: int, entropy: int, stats: int, counts: int, d_logp: int,
+                      d_entropy: int, workspace: int, stream: int = 0) -> None:
+    rc = load().adamw_policy_loss(ctypes.byref(tokens), ctypes.byref(policy), logp, old_logp,
+                                  ref_logp or None, advantages, entropy or None, stats, counts, d_logp,
+                                  d_entropy or None, workspace, stream or None)
+    _check(rc, "adamw_policy_loss")
+
+
+def adamw_policy_loss_logits(logits: adamw_rows_t, targets: int, ignore_index: int, scale: float,
+                             tokens: adamw_tokens_t, policy: adamw_policy_t, old_logp: int, ref_logp: int,
+                             advantages: int, stats: int, counts: int, logp: int, entropy: int,
+                             d_logits: adamw_rows_t, workspace: int, stream: int = 0) -> None:
+    rc = load().adamw_policy_loss_logits(ctypes.byref(logits), targets, ignore_index, scale,
+                                         ctypes.byref(tokens), ctypes.byref(policy), old_logp,
+                                         ref_logp or None, advantages, stats, counts, logp, entropy or None,
+                                         ctypes.byref(d_logits), workspace, stream or None)
+    _check(rc, "adamw_policy_loss_logits")
+
+
+def adamw_preference_loss(tokens: adamw_tokens_t, pref: adamw_preference_t, logp: int, ref_logp: int,
+                          stats: int, losses: int, rewards: int, d_logp: int, workspace: int,
+                          stream: int = 0) -> None:
+    rc = load().adamw_preference_loss(ctypes.byref(tokens), ctypes.byref(pref), logp, ref_logp or None,
+                                      stats, losses, rewards, d_logp, workspace, stream or None)
+    _check(rc, "adamw_preference_loss")
+
+
+def adamw_clip_plan_create(entries) -> int:
+    """entries: adamw_grad_t or (src, dst, numel, src_dtype, dst_dtype)
+    tuples.  Returns the plan handle."""
+    entries = list(entries)
+    arr = (adamw_grad_t * max(1, len(entries)))()
+    for i, e in enumerate(entries):
+        arr[i] = e if isinstance(e, adamw_grad_t) else adamw_grad_t(*e)
+    out = ctypes.c_void_p()
+    _check(load().adamw_clip_plan_create(arr, len(entries), ctypes.byref(out)), "adamw_clip_plan_create")
+    return out.value
+
+
+def adamw_clip_grads(plan: int, max_norm: float, norm: int, result: int, stream: int = 0) -> None:
+    rc = load().adamw_clip_grads(plan, max_norm, norm, result, stream or None)
+    _check(rc, "adamw_clip_grads")
+
+
+def adamw_clip_plan_destroy(plan: int) -> None:
+    _check(load().adamw_clip_plan_destroy(plan), "adamw_clip_plan_destroy")
+
+
 def hparams(lr=2e-4, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1,
             max_grad_norm=0.0) -> adamw_hparams_t:
     return adamw_hparams_t(lr, beta1, beta2, eps, weight_decay, max_grad_norm)
@@ -394,3 +539,84 @@ def device_hparams(hp: adamw_hparams_t, device="cuda"):
     import torch
     raw = bytes(hp)
     return torch.frombuffer(bytearray(raw), dtype=torch.uint8).to(device)
+
+
+def dtype_code(dtype) -> int:
+    """The library's code of a torch dtype of logits or gradients."""
+    import torch
+    codes = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32}
+    if dtype not in codes:
+        raise TypeError(f"want bfloat16, float16 or float32, not {dtype}")
+    return codes[dtype]
+
+
+class ClipResult(NamedTuple):
+    """The plan's own device tensors, overwritten by its next ``clip``."""
+    norm: object       # fp32, the global norm
+    coef: object       # fp32, what the gradients were multiplied by
+    nonfinite: object  # int32, 1: a gradient was inf or NaN (then coef is 1)
+
+
+class ClipPlan:
+    """Clips a list of gradients by their global norm, over every parameter
+    group and optimizer and over bf16, fp16 and fp32 tensors alike.
+
+    ``grads``: contiguous CUDA tensors of one device.  ``outs``: where the
+    clipped gradients go, tensors of the same sizes and any of the three
+    types (for example the bf16 gradients that an optimizer reads, from fp32
+    accumulators); None clips in place.  ``norm_only``: nothing is written
+    but the result.  The tensors must stay alive and in place for the plan's
+    lifetime (the plan holds references to them); calls on one plan must not
+    overlap on the GPU."""
+
+    def __init__(self, grads, outs=None, norm_only: bool = False):
+        import torch
+        grads = list(grads)
+        if norm_only and outs is not None:
+            raise ValueError("norm_only writes no outs")
+        outs = list(outs) if outs is not None else grads
+        if len(outs) != len(grads):
+            raise ValueError("tensor lists differ in length")
+        if not grads:
+            raise ValueError("empty gradient list")
+        dev = grads[0].device
+        entries = []
+        for k, (g, o) in enumerate(zip(grads, outs)):
+            for t in (g, o):
+                if not t.is_cuda or t.device != dev or not t.is_contiguous() or t.numel() != g.numel():
+                    raise TypeError(f"tensor {k}: want contiguous CUDA tensors of one device and of equal sizes")
+            entries.append(adamw_grad_t(g.data_ptr() or None, None if norm_only else o.data_ptr() or None,
+                                        g.numel(), dtype_code(g.dtype), dtype_code(o.dtype)))
+        self._keep = (grads, outs)
+        self.device = dev
+        with torch.cuda.device(dev):
+            self.handle = adamw_clip_plan_create(entries)
+        self._result = torch.zeros(4, dtype=torch.float32, device=dev)
+        self._at = self._result.data_ptr()
+        self.result = ClipResult(self._result[0], self._result[1], self._result.view(torch.int32)[2])
+
+    def clip(self, max_norm: float, norm: str = "l2", stream=None) -> ClipResult:
+        """One clip to ``max_norm`` (infinity: only copies or converts) by the
+        l2 norm of all elements or their largest magnitude ("max"); returns
+        ``self.result`` without waiting for the GPU.  With a non-finite
+        gradient nothing is scaled: the values reach the optimizer, which
+        skips or reports the step."""
+        import torch
+        if norm not in NORM:
+            raise ValueError('norm must be "l2" or "max"')
+        if not max_norm > 0:
+            raise ValueError("want max_norm > 0")
+        st = stream.cuda_stream if stream is not None else torch.cuda.current_stream(self.device).cuda_stream
+        adamw_clip_grads(self.handle, max_norm, NORM[norm], self._at, st)
+        return self.result
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            adamw_clip_plan_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass

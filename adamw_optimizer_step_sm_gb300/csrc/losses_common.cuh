@@ -1,0 +1,519 @@
+// losses_common.cuh -- device building blocks of the fine-tuning operators:
+// element types, 16-byte vectors, the online softmax record and its joins, the
+// error-free running sum, cluster access, token weights and the policy loss of
+// one token; and the host helpers of their entry points.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <limits>
+
+#include "adamw_internal.h"
+#include "adamw_losses.h"
+
+// Internal linkage, as in device_common.cuh.
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kInf = std::numeric_limits<float>::infinity();
+
+// ------------------------------------------------------- element types ----
+
+template <int DT>
+struct Elem;
+
+template <>
+struct Elem<ADAMW_DTYPE_BF16> {
+    static constexpr int kSize = 2, kVec = 8;
+    static constexpr uint32_t kNegInf = 0xff80ff80u;   // two elements of -inf
+    static constexpr uint32_t kSigns = 0x80008000u;
+    __device__ static float load(const void* p, int64_t i) {
+        return __uint_as_float(uint32_t(static_cast<const uint16_t*>(p)[i]) << 16);
+    }
+    __device__ static void store(void* p, int64_t i, float x) {
+        static_cast<uint16_t*>(p)[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+    }
+    __device__ static void unpack(uint4 v, float* x) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    __device__ static uint4 pack(const float* x) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 r = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            memcpy(&w[i], &r, 4);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+template <>
+struct Elem<ADAMW_DTYPE_FP16> {
+    static constexpr int kSize = 2, kVec = 8;
+    static constexpr uint32_t kNegInf = 0xfc00fc00u;
+    static constexpr uint32_t kSigns = 0x80008000u;
+    __device__ static float load(const void* p, int64_t i) {
+        return __half2float(static_cast<const __half*>(p)[i]);
+    }
+    __device__ static void store(void* p, int64_t i, float x) {
+        static_cast<__half*>(p)[i] = __float2half_rn(x);
+    }
+    __device__ static void unpack(uint4 v, float* x) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            __half2 h;
+            memcpy(&h, &w[i], 4);
+            const float2 f = __half22float2(h);
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
+    }
+    __device__ static uint4 pack(const float* x) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2 r = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+            memcpy(&w[i], &r, 4);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+template <>
+struct Elem<ADAMW_DTYPE_FP32> {
+    static constexpr int kSize = 4, kVec = 4;
+    static constexpr uint32_t kNegInf = 0xff800000u;
+    static constexpr uint32_t kSigns = 0x80000000u;
+    __device__ static float load(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
+    __device__ static void store(void* p, int64_t i, float x) { static_cast<float*>(p)[i] = x; }
+    __device__ static void unpack(uint4 v, float* x) {
+        x[0] = __uint_as_float(v.x);
+        x[1] = __uint_as_float(v.y);
+        x[2] = __uint_as_float(v.z);
+        x[3] = __uint_as_float(v.w);
+    }
+    __device__ static uint4 pack(const float* x) {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                          __float_as_uint(x[3]));
+    }
+};
+
+__device__ __forceinline__ uint4 load16(const void* p) { return *static_cast<const uint4*>(p); }
+__device__ __forceinline__ void store16(void* p, uint4 v) { *static_cast<uint4*>(p) = v; }
+
+// 2^x, results below the smallest normal number flushed to 0 (a probability
+// that small is 0 in every output type but fp32, where it is below 1.2e-38).
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Programmatic dependent launch: every kernel here is launched with the
+// attribute, reads nothing before the wait and lets the next kernel of the
+// stream be set up from its start (it waits in turn).
+__device__ __forceinline__ void dependency_wait() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void dependency_trigger() {
+    asm volatile("griddepcontrol.launch_dependents;");
+}
+
+// -------------------------------------------------------------- clusters --
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+// A barrier of every thread of the cluster; memory written before it is
+// visible to the cluster after it.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+                 ::: "memory");
+}
+// The float at the same shared address in the cluster's CTA `rank`.
+__device__ __forceinline__ float load_remote(const float* smem, uint32_t rank) {
+    const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    float v;
+    asm volatile("{\n\t.reg .b32 ra;\n\tmapa.shared::cluster.u32 ra, %1, %2;\n\t"
+                 "ld.shared::cluster.f32 %0, [ra];\n\t}"
+                 : "=f"(v) : "r"(a), "r"(rank) : "memory");
+    return v;
+}
+
+// ------------------------------------------------- error-free running sum --
+
+// hi + lo, the rounding error of every addition found exactly (Knuth's TwoSum)
+// and kept in lo: about 46 bits, at fp32's speed (fp64 additions are slow on
+// this GPU).  A non-finite term makes hi or lo non-finite; value() is then
+// NaN or the infinity.
+struct Sum2 {
+    float hi, lo;
+    __device__ __forceinline__ void add(float x) {
+        const float s = __fadd_rn(hi, x);
+        const float b = __fsub_rn(s, hi);
+        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)));
+        hi = s;
+    }
+    __device__ __forceinline__ void join(float h, float l) {
+        add(h);
+        lo = __fadd_rn(lo, l);
+    }
+    __device__ __forceinline__ float value() const {
+        return isfinite(hi) ? __fadd_rn(hi, lo) : hi;
+    }
+};
+
+// Sum over the warp, the same in every lane.
+__device__ __forceinline__ Sum2 warp_sum(Sum2 a) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        const float h = __shfl_xor_sync(0xffffffffu, a.hi, d);
+        const float l = __shfl_xor_sync(0xffffffffu, a.lo, d);
+        // both lanes add in the same order, so that they agree bit for bit
+        const bool low = (threadIdx.x & d) == 0;
+        Sum2 s = low ? a : Sum2{h, l};
+        s.join(low ? h : a.hi, low ? l : a.lo);
+        a = s;
+    }
+    return a;
+}
+
+// -------------------------------------------------------- online softmax --
+
+// Over the elements x seen so far: m their largest, s = sum exp(scale(x - m)),
+// t = sum exp(scale(x - m)) (x - m) (for the entropy).  -inf elements (and an
+// empty record) leave m at -inf and add nothing.
+struct Online {
+    float m, s, t;
+};
+
+// The largest element, or 0 where there is none: what exponents are taken
+// relative to, so that -inf - (-inf) does not arise.
+__device__ __forceinline__ float reference_of(float m) { return m == -kInf ? 0.0f : m; }
+
+// Moves a record's reference to M >= o.m.  c = scale * log2(e).
+template <bool ENT>
+__device__ __forceinline__ void rebase(Online& o, float M, float c) {
+    if (o.m == M) return;
+    const float d = o.m - M;  // < 0; -inf for an empty record
+    const float f = exp2_fast(d * c);
+    // d f before s: both d s and f's smallness may pass fp32's range
+    if (ENT) o.t = o.m == -kInf ? 0.0f : fmaf(d * f, o.s, o.t * f);
+    // an empty record holds s = 0, or NaN when it saw a NaN, which stays
+    o.s = o.m == -kInf ? o.s : o.s * f;
+    o.m = M;
+}
+
+template <bool ENT>
+__device__ __forceinline__ void join(Online& a, Online b, float c) {
+    const float M = fmaxf(a.m, b.m);
+    rebase<ENT>(a, M, c);
+    rebase<ENT>(b, M, c);
+    a.s += b.s;
+    if (ENT) a.t += b.t;
+}
+
+// Adds N elements.
+template <bool ENT, int N>
+__device__ __forceinline__ void absorb(Online& o, const float* x, float c) {
+    float m = x[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) m = fmaxf(m, x[i]);
+    if (m > o.m) rebase<ENT>(o, m, c);
+    const float ref = reference_of(o.m);
+    float s0 = 0.0f, s1 = 0.0f, t0 = 0.0f, t1 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const float d0 = x[i] - ref, d1 = x[i + 1] - ref;
+        const float e0 = exp2_fast(d0 * c), e1 = exp2_fast(d1 * c);
+        s0 += e0;
+        s1 += e1;
+        if (ENT) {  // a -inf element: 0 * (large), not 0 * inf
+            t0 = fmaf(e0, fmaxf(d0, -1e30f), t0);
+            t1 = fmaf(e1, fmaxf(d1, -1e30f), t1);
+        }
+    }
+    o.s += s0 + s1;
+    if (ENT) o.t += t0 + t1;
+}
+
+template <bool ENT>
+__device__ __forceinline__ Online warp_join(Online o, float c) {
+    float M = o.m;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    rebase<ENT>(o, M, c);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        o.s += __shfl_xor_sync(0xffffffffu, o.s, d);
+        if (ENT) o.t += __shfl_xor_sync(0xffffffffu, o.t, d);
+    }
+    return o;
+}
+
+// What the row's softmax comes to.
+struct RowStats {
+    float m;      // its largest logit (0 where it has no distribution)
+    float log_s;  // log of the sum; +inf: no distribution, or not read
+    float entropy;
+};
+
+template <bool ENT>
+__device__ __forceinline__ RowStats row_stats(const Online& o, float scale) {
+    RowStats r;
+    if (o.m == -kInf && o.s == 0.0f) {
+        r.m = 0.0f;
+        r.log_s = kInf;
+        r.entropy = 0.0f;
+        return r;
+    }
+    r.m = reference_of(o.m);
+    r.log_s = logf(o.s);
+    r.entropy = ENT ? r.log_s - scale * (o.t / o.s) : 0.0f;
+    return r;
+}
+
+// log-probability of a logit x under the row.
+__device__ __forceinline__ float logp_of(const RowStats& r, float x, float scale) {
+    if (r.log_s == kInf) return -kInf;
+    return (x - r.m) * scale - r.log_s;
+}
+
+// The gradient of one element, without the target's term:
+//   -p (a + b (log p + H)),  a = scale d_logp, b = scale d_entropy
+template <bool ENT>
+__device__ __forceinline__ float logit_grad(float x, float m, float log_s, float log2_s, float scale,
+                                            float c, float a, float b, float H) {
+    const float d = x - m;
+    const float p = exp2_fast(fmaf(d, c, -log2_s));
+    if (!ENT) return -a * p;
+    const float lp = fmaxf(fmaf(d, scale, -log_s), -1e30f);
+    return -p * fmaf(b, lp + H, a);
+}
+
+// ----------------------------------------------------------------- rows ----
+
+// adamw_rows_t for a kernel: byte strides.
+struct Rows {
+    char* data;
+    int64_t outer, row;
+    uint32_t inner;
+    __device__ __forceinline__ char* at(uint32_t r) const {
+        const uint32_t o = r / inner;
+        return data + int64_t(o) * outer + int64_t(r - o * inner) * row;
+    }
+};
+
+// A row as a few leading elements up to the first 16-byte boundary, whole
+// vectors, and a few trailing elements.
+template <int DT>
+struct RowSplit {
+    int head, vecs, tail;
+    __device__ __forceinline__ RowSplit(const char* row, int cols) {
+        using E = Elem<DT>;
+        const int off = int((16u - (uint32_t(reinterpret_cast<uintptr_t>(row)) & 15u)) & 15u) / E::kSize;
+        head = off < cols ? off : cols;
+        vecs = (cols - head) / E::kVec;
+        tail = cols - head - vecs * E::kVec;
+    }
+};
+
+// ----------------------------------------------------------------- tokens --
+
+// adamw_tokens_t for a kernel.  Tokens count by a byte mask, or by their
+// target (not `ignore`), or all.
+struct Tokens {
+    uint32_t n, sequences, length;  // length: of each, without offsets
+    const int64_t* offsets;
+    const uint8_t* mask;
+    const int64_t* targets;
+    int64_t ignore;
+
+    // The sequence of token i, or -1 outside of them all.  With offsets by
+    // bisection, which stays inside the array whatever it holds.
+    __device__ __forceinline__ int32_t sequence(uint32_t i) const {
+        if (!offsets) return int32_t(i / length);
+        uint32_t lo = 0, hi = sequences;  // the last start <= i is in [lo, hi)
+        while (hi - lo > 1) {
+            const uint32_t mid = lo + (hi - lo) / 2;
+            if (offsets[mid] <= int64_t(i)) lo = mid; else hi = mid;
+        }
+        return int64_t(i) >= offsets[lo] && int64_t(i) < offsets[lo + 1] ? int32_t(lo) : -1;
+    }
+    __device__ __forceinline__ bool counts(uint32_t i) const {
+        if (mask) return mask[i] != 0;
+        if (targets) return targets[i] != ignore;
+        return true;
+    }
+};
+
+// Token counts, in the workspace: tokens and non-empty sequences first, then
+// each sequence's tokens.
+struct Counts {
+    uint32_t tokens, filled, ticket, pad_;
+    uint32_t sequence[1];
+};
+
+// The weight of a token of a sequence with `in_sequence` tokens that count.
+__device__ __forceinline__ float token_weight(int32_t reduce, float inv_divisor, uint32_t tokens,
+                                              uint32_t filled, uint32_t in_sequence) {
+    if (reduce == ADAMW_REDUCE_FIXED) return inv_divisor;
+    if (reduce == ADAMW_REDUCE_TOKEN) return 1.0f / float(tokens);
+    return 1.0f / (float(in_sequence) * float(filled));
+}
+
+// ------------------------------------------------------------ policy loss --
+
+// adamw_policy_t with the thresholds of d = logp - old_logp worked out.
+struct Policy {
+    float r_low, r_high, d_low, d_high, dual, d_dual;  // d_dual +inf: off
+    float kl_coef, entropy_coef, inv_divisor, grad_scale;
+    int32_t kl, reduce, per_token;
+};
+
+struct PolicyToken {
+    float pg, kl, off, old_kl, grad;
+};
+
+// The loss terms of one token and the derivative of pg + kl_coef KL with
+// respect to its log-probability (weights left out).
+__device__ __forceinline__ PolicyToken policy_token(const Policy& P, float logp, float old, bool has_ref,
+                                                    float ref, float A) {
+    PolicyToken o;
+    const float d = logp - old;
+    const float r = expf(d);
+    const float rc = d > P.d_high ? P.r_high : d < P.d_low ? P.r_low : r;
+    const bool capped = A < 0.0f && d > P.d_dual;
+    const bool off = capped || (A > 0.0f && d > P.d_high) || (A < 0.0f && d < P.d_low);
+    // fmaxf would drop a NaN: the two agree in their NaN (both hold A, r)
+    const float u = -A * r, v = -A * rc;
+    o.pg = capped ? -A * P.dual : (u < v ? v : u);
+    o.off = off ? 1.0f : 0.0f;
+    o.old_kl = expm1f(d) - d;
+    o.grad = off ? 0.0f : u;
+    o.kl = 0.0f;
+    if (has_ref) {
+        const float k = logp - ref;
+        float dk;
+        if (P.kl == ADAMW_KL_K1) {
+            o.kl = k;
+            dk = 1.0f;
+        } else if (P.kl == ADAMW_KL_K2) {
+            o.kl = 0.5f * k * k;
+            dk = k;
+        } else {
+            const float e = expm1f(-k);
+            o.kl = e + k;
+            dk = -e;
+        }
+        // without a coefficient the estimate is reported only, and a
+        // reference that is -inf somewhere does not reach the gradient
+        if (P.kl_coef != 0.0f) o.grad = fmaf(P.kl_coef, dk, o.grad);
+    }
+    return o;
+}
+
+// ---------------------------------------------------------- host helpers --
+
+inline bool launched(cudaError_t e, const char* what) {
+    if (e == cudaSuccess) return true;
+    cudaGetLastError();  // not the next caller's error
+    adamw::set_cuda_error(what, cudaGetErrorString(e));
+    return false;
+}
+
+// One launch with programmatic stream serialization, in clusters of `cluster`
+// CTAs, with `smem` bytes of dynamic shared memory.
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*kernel)(KArgs...), uint32_t grid, int block, int cluster, size_t smem,
+                   cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(unsigned(block));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+inline bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+constexpr int64_t kMaxCount = 2147483647;
+
+inline Tokens tokens_of(const adamw_tokens_t* t, const int64_t* targets, int64_t ignore) {
+    Tokens k = {};
+    k.n = uint32_t(t->n);
+    k.sequences = uint32_t(t->sequences);
+    k.length = t->offsets || t->n == 0 ? 1u : uint32_t(t->n / t->sequences);
+    k.offsets = t->offsets;
+    k.mask = t->mask;
+    k.targets = targets;
+    k.ignore = ignore;
+    return k;
+}
+
+inline Policy policy_of(const adamw_policy_t* p) {
+    Policy k;
+    k.r_low = 1.0f - p->clip_low;
+    k.r_high = 1.0f + p->clip_high;
+    k.d_low = float(std::log1p(-double(p->clip_low)));
+    k.d_high = float(std::log1p(double(p->clip_high)));
+    k.dual = p->dual_clip;
+    k.d_dual = p->dual_clip > 0.0f ? float(std::log(double(p->dual_clip))) : kInf;
+    k.kl_coef = p->kl_coef;
+    k.entropy_coef = p->entropy_coef;
+    k.inv_divisor = p->reduce == ADAMW_REDUCE_FIXED ? 1.0f / p->divisor : 0.0f;
+    k.grad_scale = p->grad_scale;
+    k.kl = p->kl;
+    k.reduce = p->reduce;
+    k.per_token = p->advantage_per_token;
+    return k;
+}
+
+inline int dtype_size(int32_t dt) {
+    return dt == ADAMW_DTYPE_FP32 ? 4 : dt == ADAMW_DTYPE_BF16 || dt == ADAMW_DTYPE_FP16 ? 2 : 0;
+}
+
+}  // namespace
+
+namespace adamw {
+
+// Shared by the entry points' files (policy_loss.cu, token_logprob.cu).
+int check_tokens(const adamw_tokens_t* t);
+int check_policy(const adamw_policy_t* p);
+// Counts the tokens of `targets` (or of the tokens' mask, or all) into the
+// workspace's Counts, and zeroes its ticket.
+int launch_counts(const adamw_tokens_t* t, const int64_t* targets, int64_t ignore, void* workspace,
+                  cudaStream_t st);
+int launch_policy(const adamw_tokens_t* t, const adamw_policy_t* p, const int64_t* targets,
+                  int64_t ignore, const float* logp, const float* old_logp, const float* ref_logp,
+                  const float* advantages, const float* entropy, float* stats, int64_t* counts,
+                  float* d_logp, float* d_entropy, void* workspace, cudaStream_t st);
+
+}  // namespace adamw

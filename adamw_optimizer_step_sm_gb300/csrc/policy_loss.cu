@@ -1,0 +1,408 @@
+// policy_loss.cu -- the token losses: the clipped policy loss with its KL
+// term, and the preference loss over pairs of sequences, with the gradients
+// of the log-probabilities.
+//
+// Both touch a few floats per token (policy 12 to 28 bytes, preference 9 to
+// 13): bound by launches below about a million tokens and by HBM above.
+#include "losses_common.cuh"
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxGrid = 608;  // 4 CTAs on each of 152 SMs
+constexpr int kSums = 5;       // pg, KL, entropy, clipped, old KL
+
+uint32_t token_grid(int64_t n) {
+    const int64_t g = (n + kThreads - 1) / kThreads;
+    return uint32_t(g < 1 ? 1 : g > kMaxGrid ? kMaxGrid : g);
+}
+
+int64_t counts_bytes(int64_t sequences) { return (16 + 4 * sequences + 15) / 16 * 16; }
+
+// Counts tokens by sequence, warp by warp (integers: any order gives the same).
+__global__ void __launch_bounds__(kThreads) count_kernel(Tokens t, Counts* out) {
+    dependency_trigger();
+    dependency_wait();
+    const uint32_t lane = threadIdx.x % 32;
+    uint32_t tokens = 0, filled = 0;
+    const uint64_t step = uint64_t(gridDim.x) * kThreads;
+    // whole warps take part in every round
+    for (uint64_t base = uint64_t(blockIdx.x) * kThreads + threadIdx.x - lane; base < t.n; base += step) {
+        const uint32_t i = uint32_t(base) + lane;
+        int32_t seq = -1;
+        if (base + lane < t.n && t.counts(i)) seq = t.sequence(i);
+        const uint32_t peers = __match_any_sync(0xffffffffu, seq);
+        if (seq >= 0 && (peers & ((1u << lane) - 1)) == 0) {
+            const uint32_t k = __popc(peers);
+            tokens += k;
+            filled += atomicAdd(&out->sequence[seq], k) == 0;
+        }
+    }
+    tokens = __reduce_add_sync(0xffffffffu, tokens);
+    filled = __reduce_add_sync(0xffffffffu, filled);
+    if (lane == 0 && tokens) atomicAdd(&out->tokens, tokens);
+    if (lane == 0 && filled) atomicAdd(&out->filled, filled);
+}
+
+struct PolicyTokens {
+    const float *logp, *old_logp, *ref_logp, *advantages, *entropy;
+    float *d_logp, *d_entropy, *stats;
+    int64_t* counts;
+};
+
+// Loss terms and gradients, token by token; each CTA leaves its five sums and
+// the last one to finish adds them up in the CTAs' order.
+__global__ void __launch_bounds__(kThreads)
+policy_kernel(Tokens t, Policy P, PolicyTokens a, Counts* counts, float2* partial) {
+    dependency_trigger();
+    dependency_wait();
+    const uint32_t tokens = counts->tokens, filled = counts->filled;
+    Sum2 sum[kSums] = {};
+    const uint64_t step = uint64_t(gridDim.x) * kThreads;
+    for (uint64_t at = uint64_t(blockIdx.x) * kThreads + threadIdx.x; at < t.n; at += step) {
+        const uint32_t i = uint32_t(at);
+        float g = 0.0f, gh = 0.0f;
+        if (t.counts(i)) {
+            const int32_t seq = t.sequence(i);
+            if (seq >= 0) {
+                const float w = token_weight(P.reduce, P.inv_divisor, tokens, filled, counts->sequence[seq]);
+                const float A = a.advantages[P.per_token ? i : uint32_t(seq)];
+                const PolicyToken k = policy_token(P, a.logp[i], a.old_logp[i], a.ref_logp != nullptr,
+                                                   a.ref_logp ? a.ref_logp[i] : 0.0f, A);
+                sum[0].add(w * k.pg);
+                sum[1].add(w * k.kl);
+                if (a.entropy) sum[2].add(w * a.entropy[i]);
+                sum[3].add(w * k.off);
+                sum[4].add(w * k.old_kl);
+                g = w * P.grad_scale * k.grad;
+                gh = -w * P.grad_scale * P.entropy_coef;
+            }
+        }
+        if (a.d_logp) a.d_logp[i] = g;
+        if (a.d_entropy) a.d_entropy[i] = gh;
+    }
+    __shared__ float2 part[kSums][kWarps];
+    __shared__ bool last;
+    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+#pragma unroll
+    for (int k = 0; k < kSums; ++k) {
+        const Sum2 s = warp_sum(sum[k]);
+        if (lane == 0) part[k][warp] = make_float2(s.hi, s.lo);
+    }
+    __syncthreads();
+    if (threadIdx.x < kSums) {
+        Sum2 s = {};
+        for (int w = 0; w < kWarps; ++w) s.join(part[threadIdx.x][w].x, part[threadIdx.x][w].y);
+        partial[blockIdx.x * kSums + threadIdx.x] = make_float2(s.hi, s.lo);
+        __threadfence();
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(&counts->ticket, 1) == gridDim.x - 1;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    __shared__ float mean[kSums];
+    if (warp < kSums) {
+        Sum2 s = {};
+        for (uint32_t b = lane; b < gridDim.x; b += 32) {
+            const float2 p = __ldcg(&partial[b * kSums + warp]);
+            s.join(p.x, p.y);
+        }
+        s = warp_sum(s);
+        if (lane == 0) mean[warp] = s.value();
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float loss = mean[0];
+        if (P.kl_coef != 0.0f) loss = fmaf(P.kl_coef, mean[1], loss);
+        if (P.entropy_coef != 0.0f) loss = fmaf(-P.entropy_coef, mean[2], loss);
+        a.stats[0] = loss;
+        for (int k = 0; k < kSums; ++k) a.stats[k + 1] = mean[k];
+        a.counts[0] = tokens;
+        a.counts[1] = filled;
+    }
+}
+
+// ------------------------------------------------------------- preference --
+
+struct Preference {
+    float beta, margin, smoothing, grad_scale;
+    int32_t kind, average, ref;
+};
+
+// log(1 + exp(x)) and sigmoid(x), without overflow.
+__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))); }
+__device__ __forceinline__ float sigmoid(float x) {
+    const float e = expf(-fabsf(x));
+    return x >= 0.0f ? 1.0f / (1.0f + e) : e / (1.0f + e);
+}
+
+// One pair per cluster of CTAs: each CTA sums its share of the two
+// sequences' log ratios, the cluster joins them, and every CTA writes its
+// share of the gradient.
+__global__ void __launch_bounds__(kThreads)
+preference_kernel(Tokens t, Preference P, const float* logp, const float* ref, float* losses,
+                  float* rewards, float* d_logp, float* difference) {
+    dependency_trigger();
+    dependency_wait();
+    const uint32_t size = cluster_size(), rank = cluster_rank();
+    const uint32_t pair = blockIdx.x / size, pairs = t.sequences / 2;
+    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const uint32_t width = size * kThreads, me = rank * kThreads + threadIdx.x;
+    __shared__ float part[2][3][kWarps];
+    __shared__ float whole[2][3];
+    int64_t begin[2], end[2];
+    for (int side = 0; side < 2; ++side) {
+        const uint32_t seq = pair + (side ? pairs : 0);
+        int64_t b = t.offsets ? t.offsets[seq] : int64_t(seq) * t.length;
+        int64_t e = t.offsets ? t.offsets[seq + 1] : b + t.length;
+        // inside the tokens, whatever the offsets hold
+        b = b < 0 ? 0 : b > int64_t(t.n) ? int64_t(t.n) : b;
+        e = e < b ? b : e > int64_t(t.n) ? int64_t(t.n) : e;
+        begin[side] = b;
+        end[side] = e;
+        Sum2 sum = {};
+        uint32_t tokens = 0;
+        for (int64_t i = b + me; i < e; i += width) {
+            if (t.mask && t.mask[i] == 0) continue;
+            sum.add(logp[i]);
+            if (P.ref == ADAMW_REF_TOKEN) sum.add(-ref[i]);  // the difference unrounded
+            ++tokens;
+        }
+        sum = warp_sum(sum);
+        tokens = __reduce_add_sync(0xffffffffu, tokens);
+        if (lane == 0) {
+            part[side][0][warp] = sum.hi;
+            part[side][1][warp] = sum.lo;
+            part[side][2][warp] = __uint_as_float(tokens);
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < 2) {
+        Sum2 s = {};
+        uint32_t k = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            s.join(part[threadIdx.x][0][w], part[threadIdx.x][1][w]);
+            k += __float_as_uint(part[threadIdx.x][2][w]);
+        }
+        whole[threadIdx.x][0] = s.hi;
+        whole[threadIdx.x][1] = s.lo;
+        whole[threadIdx.x][2] = __uint_as_float(k);
+    }
+    if (size > 1) cluster_sync(); else __syncthreads();
+    float S[2], share[2];
+    for (int side = 0; side < 2; ++side) {
+        Sum2 s = {};
+        uint32_t k = 0;
+        if (size == 1) {
+            s = {whole[side][0], whole[side][1]};
+            k = __float_as_uint(whole[side][2]);
+        }
+        for (uint32_t c = 0; size > 1 && c < size; ++c) {
+            s.join(load_remote(&whole[side][0], c), load_remote(&whole[side][1], c));
+            k += __float_as_uint(load_remote(&whole[side][2], c));
+        }
+        if (P.ref == ADAMW_REF_SEQUENCE) s.add(-ref[pair + (side ? pairs : 0)]);
+        share[side] = P.average ? 1.0f / float(k > 0 ? k : 1) : 1.0f;
+        S[side] = P.average ? s.value() / float(k > 0 ? k : 1) : s.value();
+    }
+    if (size > 1) cluster_sync();  // the records stay until all have read them
+    const float D = S[0] - S[1];
+    const float h = P.beta * D - P.margin;
+    float loss, dD;
+    if (P.kind == ADAMW_PREF_SIGMOID) {
+        loss = (1.0f - P.smoothing) * softplus(-h) + P.smoothing * softplus(h);
+        dD = P.beta * (P.smoothing * sigmoid(h) - (1.0f - P.smoothing) * sigmoid(-h));
+    } else if (P.kind == ADAMW_PREF_HINGE) {
+        const float u = 1.0f - h;
+        loss = u < 0.0f ? 0.0f : u;  // NaN stays
+        dD = h < 1.0f ? -P.beta : h >= 1.0f ? 0.0f : h;
+    } else {
+        const float u = D - 0.5f / P.beta;
+        loss = u * u;
+        dD = 2.0f * u;
+    }
+    if (rank == 0 && threadIdx.x == 0) {
+        losses[pair] = loss;
+        rewards[pair] = P.beta * S[0];
+        rewards[pairs + pair] = P.beta * S[1];
+        difference[pair] = D;
+    }
+    const float g = P.grad_scale * dD / float(pairs);
+    for (int side = 0; side < 2; ++side) {
+        const float v = (side ? -g : g) * share[side];
+        for (int64_t i = begin[side] + me; i < end[side]; i += width)
+            d_logp[i] = !t.mask || t.mask[i] != 0 ? v : 0.0f;
+    }
+    // tokens outside every sequence
+    if (t.offsets && pair == 0) {
+        for (int64_t i = me; i < begin[0]; i += width) d_logp[i] = 0.0f;
+    }
+    if (t.offsets && pair == pairs - 1) {
+        for (int64_t i = end[1] + me; i < int64_t(t.n); i += width) d_logp[i] = 0.0f;
+    }
+}
+
+// The statistics over the pairs.
+__global__ void __launch_bounds__(kThreads)
+preference_stats_kernel(uint32_t pairs, Preference P, const float* losses, const float* difference,
+                        float* stats) {
+    dependency_trigger();
+    dependency_wait();
+    Sum2 loss = {}, h = {};
+    uint32_t right = 0;
+    for (uint32_t i = threadIdx.x; i < pairs; i += kThreads) {
+        const float D = difference[i];
+        loss.add(losses[i]);
+        h.add(P.beta * D - P.margin);
+        right += D > 0.0f;
+    }
+    __shared__ float2 part[2][kWarps];
+    __shared__ uint32_t rights[kWarps];
+    loss = warp_sum(loss);
+    h = warp_sum(h);
+    right = __reduce_add_sync(0xffffffffu, right);
+    if (threadIdx.x % 32 == 0) {
+        part[0][threadIdx.x / 32] = make_float2(loss.hi, loss.lo);
+        part[1][threadIdx.x / 32] = make_float2(h.hi, h.lo);
+        rights[threadIdx.x / 32] = right;
+    }
+    __syncthreads();
+    if (threadIdx.x < 2) {
+        Sum2 s = {};
+        for (int w = 0; w < kWarps; ++w) s.join(part[threadIdx.x][w].x, part[threadIdx.x][w].y);
+        stats[threadIdx.x * 2] = s.value() / float(pairs);
+    }
+    if (threadIdx.x == 2) {
+        uint32_t k = 0;
+        for (int w = 0; w < kWarps; ++w) k += rights[w];
+        stats[1] = float(k) / float(pairs);
+    }
+}
+
+}  // namespace
+
+namespace adamw {
+
+int check_tokens(const adamw_tokens_t* t) {
+    if (!t || t->n < 0 || t->sequences < 0) return ADAMW_ERR_INVALID_ARG;
+    if (t->n > kMaxCount || t->sequences > kMaxCount) return ADAMW_ERR_TOO_LARGE;
+    if (t->sequences == 0) return t->n == 0 ? ADAMW_OK : ADAMW_ERR_INVALID_ARG;
+    if (!t->offsets && t->n % t->sequences != 0) return ADAMW_ERR_INVALID_ARG;
+    if (!aligned(t->offsets, 8)) return ADAMW_ERR_MISALIGNED;
+    return ADAMW_OK;
+}
+
+int check_policy(const adamw_policy_t* p) {
+    if (!p) return ADAMW_ERR_INVALID_ARG;
+    const bool ok = p->clip_low >= 0.0f && p->clip_low <= 1.0f && p->clip_high >= 0.0f &&
+                    std::isfinite(p->clip_high) &&
+                    (p->dual_clip == 0.0f || (p->dual_clip > 1.0f && std::isfinite(p->dual_clip))) &&
+                    std::isfinite(p->kl_coef) && std::isfinite(p->entropy_coef) &&
+                    std::isfinite(p->grad_scale) && p->kl >= ADAMW_KL_K1 && p->kl <= ADAMW_KL_K3 &&
+                    p->reduce >= ADAMW_REDUCE_TOKEN && p->reduce <= ADAMW_REDUCE_FIXED &&
+                    (p->reduce != ADAMW_REDUCE_FIXED || (p->divisor > 0.0f && std::isfinite(p->divisor))) &&
+                    (p->advantage_per_token == 0 || p->advantage_per_token == 1);
+    return ok ? ADAMW_OK : ADAMW_ERR_INVALID_ARG;
+}
+
+int launch_counts(const adamw_tokens_t* t, const int64_t* targets, int64_t ignore, void* workspace,
+                  cudaStream_t st) {
+    Counts* c = static_cast<Counts*>(workspace);
+    if (!launched(cudaMemsetAsync(c, 0, size_t(counts_bytes(t->sequences)), st), "counts memset"))
+        return ADAMW_ERR_CUDA;
+    if (t->n == 0) return ADAMW_OK;
+    return launched(launch(count_kernel, token_grid(t->n), kThreads, 1, 0, st,
+                           tokens_of(t, targets, ignore), c), "count launch")
+               ? ADAMW_OK : ADAMW_ERR_CUDA;
+}
+
+int launch_policy(const adamw_tokens_t* t, const adamw_policy_t* p, const int64_t* targets,
+                  int64_t ignore, const float* logp, const float* old_logp, const float* ref_logp,
+                  const float* advantages, const float* entropy, float* stats, int64_t* counts,
+                  float* d_logp, float* d_entropy, void* workspace, cudaStream_t st) {
+    const Policy P = policy_of(p);
+    const PolicyTokens a = {logp, old_logp, ref_logp, advantages, entropy, d_logp, d_entropy, stats, counts};
+    float2* partial = reinterpret_cast<float2*>(static_cast<char*>(workspace) + counts_bytes(t->sequences));
+    return launched(launch(policy_kernel, token_grid(t->n), kThreads, 1, 0, st,
+                           tokens_of(t, targets, ignore), P, a, static_cast<Counts*>(workspace), partial),
+                    "policy launch")
+               ? ADAMW_OK : ADAMW_ERR_CUDA;
+}
+
+}  // namespace adamw
+
+extern "C" int64_t adamw_policy_workspace(int64_t n, int64_t sequences) {
+    if (n < 0 || sequences < 0 || n > kMaxCount || sequences > kMaxCount) return 0;
+    return counts_bytes(sequences) + int64_t(kMaxGrid) * kSums * int64_t(sizeof(float2));
+}
+
+extern "C" int adamw_policy_loss(const adamw_tokens_t* tokens, const adamw_policy_t* policy,
+                                 const float* logp, const float* old_logp, const float* ref_logp,
+                                 const float* advantages, const float* entropy, float* stats,
+                                 int64_t* counts, float* d_logp, float* d_entropy, void* workspace,
+                                 adamw_stream_t stream) {
+    int rc = adamw::check_tokens(tokens);
+    if (rc != ADAMW_OK) return rc;
+    rc = adamw::check_policy(policy);
+    if (rc != ADAMW_OK) return rc;
+    if (!stats || !counts || !workspace || (policy->kl_coef != 0.0f && !ref_logp) ||
+        (policy->entropy_coef != 0.0f && (!entropy || !d_entropy)))
+        return ADAMW_ERR_INVALID_ARG;
+    if (tokens->n > 0 && (!logp || !old_logp || !advantages || !d_logp)) return ADAMW_ERR_INVALID_ARG;
+    const void* floats[] = {logp, old_logp, ref_logp, advantages, entropy, stats, d_logp, d_entropy};
+    for (const void* p : floats)
+        if (!aligned(p, 4)) return ADAMW_ERR_MISALIGNED;
+    if (!aligned(counts, 8) || !aligned(workspace, 16)) return ADAMW_ERR_MISALIGNED;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    rc = adamw::launch_counts(tokens, nullptr, 0, workspace, st);
+    if (rc != ADAMW_OK) return rc;
+    return adamw::launch_policy(tokens, policy, nullptr, 0, logp, old_logp, ref_logp, advantages, entropy,
+                                stats, counts, d_logp, d_entropy, workspace, st);
+}
+
+extern "C" int64_t adamw_preference_workspace(int64_t pairs) {
+    return pairs < 1 || pairs > kMaxCount / 2 ? 0 : (4 * pairs + 15) / 16 * 16;
+}
+
+extern "C" int adamw_preference_loss(const adamw_tokens_t* tokens, const adamw_preference_t* pref,
+                                     const float* logp, const float* ref_logp, float* stats,
+                                     float* losses, float* rewards, float* d_logp, void* workspace,
+                                     adamw_stream_t stream) {
+    const int rc = adamw::check_tokens(tokens);
+    if (rc != ADAMW_OK) return rc;
+    if (!pref || tokens->sequences < 2 || tokens->sequences % 2 != 0) return ADAMW_ERR_INVALID_ARG;
+    if (!(pref->beta > 0.0f) || !std::isfinite(pref->beta) || !std::isfinite(0.5f / pref->beta) ||
+        !std::isfinite(pref->margin) || !std::isfinite(pref->grad_scale) ||
+        !(pref->label_smoothing >= 0.0f && pref->label_smoothing <= 0.5f) ||
+        pref->kind < ADAMW_PREF_SIGMOID || pref->kind > ADAMW_PREF_IPO ||
+        (pref->kind != ADAMW_PREF_SIGMOID && pref->label_smoothing != 0.0f) ||
+        (pref->kind == ADAMW_PREF_IPO && pref->margin != 0.0f) || pref->ref < ADAMW_REF_NONE ||
+        pref->ref > ADAMW_REF_SEQUENCE)
+        return ADAMW_ERR_INVALID_ARG;
+    if (!stats || !losses || !rewards || !workspace || (pref->ref != ADAMW_REF_NONE && !ref_logp) ||
+        (tokens->n > 0 && (!logp || !d_logp)))
+        return ADAMW_ERR_INVALID_ARG;
+    const void* floats[] = {logp, ref_logp, stats, losses, rewards, d_logp};
+    for (const void* p : floats)
+        if (!aligned(p, 4)) return ADAMW_ERR_MISALIGNED;
+    if (!aligned(workspace, 16)) return ADAMW_ERR_MISALIGNED;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t pairs = tokens->sequences / 2;
+    // CTAs per pair: more where pairs are few and long
+    int cluster = 1;
+    while (cluster < 8 && pairs * cluster < 304 && tokens->n >= pairs * cluster * 4 * kThreads) cluster *= 2;
+    const Preference P = {pref->beta, pref->margin, pref->label_smoothing, pref->grad_scale,
+                          pref->kind, pref->length_average, pref->ref};
+    float* difference = static_cast<float*>(workspace);
+    if (pairs * cluster > kMaxCount) return ADAMW_ERR_TOO_LARGE;
+    if (!launched(launch(preference_kernel, uint32_t(pairs * cluster), kThreads, cluster, 0, st,
+                         tokens_of(tokens, nullptr, 0), P, logp, ref_logp, losses, rewards, d_logp,
+                         difference), "preference launch"))
+        return ADAMW_ERR_CUDA;
+    return launched(launch(preference_stats_kernel, 1u, kThreads, 1, 0, st, uint32_t(pairs), P,
+                           static_cast<const float*>(losses), static_cast<const float*>(difference), stats),
+                    "preference statistics launch")
+               ? ADAMW_OK : ADAMW_ERR_CUDA;
+}

@@ -1,0 +1,627 @@
+// token_logprob.cu -- per-token log-probabilities from logits over the
+// vocabulary, their gradient, and the policy loss fused with both.
+//
+// All three are bound by HBM: a bf16 logit costs about six instructions and
+// one exponential against two bytes.
+#include <atomic>
+
+#include "losses_common.cuh"
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+// Rows of up to this many elements are taken by a warp each, eight to a CTA;
+// longer ones by a CTA or a cluster of them.
+constexpr int kWarpCols = 1024;
+// 16-byte vectors in flight per thread.
+constexpr int kUnroll = 4;
+
+// The elements of the row outside its vectors, at most one per thread of the
+// group: the head's by threads 0.. of the first CTA, the tail's by threads
+// 8.. of the last one.  -1: none.
+template <int DT>
+__device__ __forceinline__ int extra_element(const RowSplit<DT>& sp, int lane, bool first, bool last) {
+    if (first && lane < sp.head) return lane;
+    if (last && lane >= 8 && lane < 8 + sp.tail) return sp.head + sp.vecs * Elem<DT>::kVec + lane - 8;
+    return -1;
+}
+
+// Joins the records of a group of threads: a warp, or a cluster of CTAs (one
+// or more).  Every thread gets the same record.
+template <bool ENT, bool WARP>
+__device__ __forceinline__ Online group_join(Online o, float c) {
+    o = warp_join<ENT>(o, c);
+    if (WARP) {
+        __syncwarp();
+        return o;
+    }
+    __shared__ Online part[kWarps];
+    __shared__ Online whole;
+    const int warp = threadIdx.x / 32;
+    if (threadIdx.x % 32 == 0) part[warp] = o;
+    __syncthreads();
+    o = part[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) join<ENT>(o, part[w], c);
+    const uint32_t size = cluster_size();
+    if (size > 1) {
+        if (threadIdx.x == 0) whole = o;
+        cluster_sync();
+        for (uint32_t k = 0; k < size; ++k) {
+            Online b;
+            b.m = load_remote(&whole.m, k);
+            b.s = load_remote(&whole.s, k);
+            b.t = ENT ? load_remote(&whole.t, k) : 0.0f;
+            if (k == 0) o = b; else join<ENT>(o, b, c);
+        }
+        // no CTA may end, or write its record again, while another reads it
+        cluster_sync();
+    }
+    return o;
+}
+
+// ---------------------------------------------------------------- forward --
+
+// Log-probability and entropy of one row per group (a warp; or a cluster of
+// CTAs, each streaming its share of the row once, with the running maximum
+// and sums in registers).
+template <int DT, bool ENT, bool WARP>
+__global__ void __launch_bounds__(kThreads)
+logprob_kernel(Rows logits, uint32_t rows, int cols, const int64_t* targets, int64_t ignore,
+               float scale, float* logp, float* entropy, float* stats) {
+    using E = Elem<DT>;
+    dependency_trigger();
+    dependency_wait();
+    const uint32_t size = WARP ? 1 : cluster_size();
+    const uint32_t rank = WARP ? 0 : cluster_rank();
+    const int lane = WARP ? threadIdx.x % 32 : threadIdx.x;
+    constexpr int width = WARP ? 32 : kThreads;
+    const uint32_t r = WARP ? blockIdx.x * kWarps + threadIdx.x / 32 : blockIdx.x / size;
+    if (r >= rows) return;  // whole warps only: the CTA form's grid is exact
+    const int64_t t = targets[r];
+    const bool writer = lane == 0 && rank == 0;
+    if (t == ignore) {
+        if (writer) {
+            logp[r] = 0.0f;
+            if (entropy) entropy[r] = 0.0f;
+            if (stats) reinterpret_cast<float2*>(stats)[r] = make_float2(0.0f, kInf);
+        }
+        return;  // the whole group
+    }
+    const char* row = logits.at(r);
+    const RowSplit<DT> sp(row, cols);
+    const float c = scale * kLog2e;
+    const uint4* body = reinterpret_cast<const uint4*>(row + int64_t(sp.head) * E::kSize);
+    const int first = int(int64_t(sp.vecs) * rank / size);
+    const int end = int(int64_t(sp.vecs) * (rank + 1) / size);
+
+    Online o = {-kInf, 0.0f, 0.0f};
+    const int extra = extra_element<DT>(sp, lane, rank == 0, rank == size - 1);
+    float x2[2] = {extra >= 0 ? E::load(row, extra) : -kInf, -kInf};
+    for (int base = first + lane; base < end; base += kUnroll * width) {
+        uint4 v[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            v[u] = base + u * width < end
+                       ? load16(body + base + u * width)
+                       : make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf);
+        float x[kUnroll * E::kVec];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) E::unpack(v[u], x + u * E::kVec);
+        absorb<ENT, kUnroll * E::kVec>(o, x, c);
+    }
+    absorb<ENT, 2>(o, x2, c);
+    o = group_join<ENT, WARP>(o, c);
+    if (!writer) return;
+    const bool bad = t < 0 || t >= cols;
+    RowStats rs = row_stats<ENT>(o, scale);
+    if (bad) rs.m = rs.log_s = rs.entropy = __int_as_float(0x7fc00000);
+    logp[r] = logp_of(rs, bad ? 0.0f : E::load(row, t), scale);
+    if (entropy) entropy[r] = rs.entropy;
+    if (stats) reinterpret_cast<float2*>(stats)[r] = make_float2(rs.m, rs.log_s);
+}
+
+// --------------------------------------------------------------- backward --
+
+// Writes the gradients of the vector at `elem` (its first element's index).
+template <int DT, bool ENT>
+__device__ __forceinline__ void grad_vector(uint4 v, char* out, bool vector_out, int elem, int64_t t,
+                                            float m, float log_s, float log2_s, float scale, float c,
+                                            float a, float b, float H) {
+    using E = Elem<DT>;
+    float x[E::kVec];
+    E::unpack(v, x);
+#pragma unroll
+    for (int j = 0; j < E::kVec; ++j) x[j] = logit_grad<ENT>(x[j], m, log_s, log2_s, scale, c, a, b, H);
+    const int64_t at = t - elem;
+    if (at >= 0 && at < E::kVec) {
+#pragma unroll
+        for (int j = 0; j < E::kVec; ++j)
+            if (j == at) x[j] += a;
+    }
+    if (vector_out) {
+        store16(out + int64_t(elem) * E::kSize, E::pack(x));
+    } else {
+#pragma unroll
+        for (int j = 0; j < E::kVec; ++j) E::store(out, elem + j, x[j]);
+    }
+}
+
+// Zeros in the vectors [first, end) and the extra element of a row.
+template <int DT>
+__device__ __forceinline__ void zero_row(char* out, bool vector_out, const RowSplit<DT>& sp, int first,
+                                         int end, int lane, int width, int extra) {
+    using E = Elem<DT>;
+    for (int i = first + lane; i < end; i += width) {
+        const int elem = sp.head + i * E::kVec;
+        if (vector_out) {
+            store16(out + int64_t(elem) * E::kSize, make_uint4(0, 0, 0, 0));
+        } else {
+            for (int j = 0; j < E::kVec; ++j) E::store(out, elem + j, 0.0f);
+        }
+    }
+    if (extra >= 0) E::store(out, extra, 0.0f);
+}
+
+// One CTA per piece of a row (or a warp per row): elementwise.
+template <int DT, bool ENT, bool WARP>
+__global__ void __launch_bounds__(kThreads)
+logprob_backward_kernel(Rows logits, Rows grad, uint32_t rows, uint32_t pieces, int cols,
+                        const int64_t* targets, float scale, const float* stats, const float* entropy,
+                        const float* d_logp, const float* d_entropy) {
+    using E = Elem<DT>;
+    dependency_trigger();
+    dependency_wait();
+    const int lane = WARP ? threadIdx.x % 32 : threadIdx.x;
+    constexpr int width = WARP ? 32 : kThreads;
+    const uint32_t r = WARP ? blockIdx.x * kWarps + threadIdx.x / 32 : blockIdx.x / pieces;
+    const uint32_t piece = WARP ? 0 : blockIdx.x - r * pieces;
+    if (r >= rows) return;
+    const char* row = logits.at(r);
+    char* out = grad.at(r);
+    const RowSplit<DT> sp(row, cols);
+    const bool vector_out = ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
+    const int first = int(int64_t(sp.vecs) * piece / pieces);
+    const int end = int(int64_t(sp.vecs) * (piece + 1) / pieces);
+    const int extra = extra_element<DT>(sp, lane, piece == 0, piece == pieces - 1);
+
+    const float2 st = reinterpret_cast<const float2*>(stats)[r];
+    if (st.y == kInf) {  // ignored, or without a distribution
+        zero_row<DT>(out, vector_out, sp, first, end, lane, width, extra);
+        return;
+    }
+    const int64_t t = targets[r];
+    const float c = scale * kLog2e, log2_s = st.y * kLog2e;
+    const float a = scale * d_logp[r];
+    const float b = ENT ? scale * d_entropy[r] : 0.0f;
+    const float H = ENT ? entropy[r] : 0.0f;
+    const uint4* body = reinterpret_cast<const uint4*>(row + int64_t(sp.head) * E::kSize);
+    const float xe = extra >= 0 ? E::load(row, extra) : 0.0f;
+    for (int base = first + lane; base < end; base += kUnroll * width) {
+        uint4 v[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            if (base + u * width < end) v[u] = load16(body + base + u * width);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            if (base + u * width < end)
+                grad_vector<DT, ENT>(v[u], out, vector_out, sp.head + (base + u * width) * E::kVec, t, st.x,
+                                     st.y, log2_s, scale, c, a, b, H);
+    }
+    if (extra >= 0)
+        E::store(out, extra,
+                 logit_grad<ENT>(xe, st.x, st.y, log2_s, scale, c, a, b, H) + (extra == t ? a : 0.0f));
+}
+
+// ------------------------------------------------------ fused policy loss --
+
+struct PolicyRows {
+    const int64_t* targets;
+    int64_t ignore;
+    const float *old_logp, *ref_logp, *advantages;
+    const Counts* counts;
+    float *logp, *entropy;
+};
+
+__device__ __forceinline__ void copy_async16(uint4* smem, const uint4* global) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                 :: "r"(static_cast<uint32_t>(__cvta_generic_to_shared(smem))), "l"(global) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
+}
+
+// Groups of kUnroll vectors per thread that are on their way at a time.
+constexpr int kDepth = 4;
+
+// The policy loss of one token per group, from its row of logits to their
+// gradient: the row (each CTA's share of it) is copied to shared memory with
+// the maximum and sums taken as it arrives, the group joins them, every
+// thread works out the token's loss, and the gradient is written from the
+// copy: one read and one write of HBM.  A thread reads only the vectors that
+// it copied itself, so the copies need no barrier.
+template <int DT, bool ENT, bool WARP>
+__global__ void __launch_bounds__(kThreads)
+policy_rows_kernel(Rows logits, Rows grad, Tokens tokens, int cols, float scale, Policy P, PolicyRows a) {
+    using E = Elem<DT>;
+    extern __shared__ uint4 slices[];
+    dependency_trigger();
+    dependency_wait();
+    const uint32_t size = WARP ? 1 : cluster_size();
+    const uint32_t rank = WARP ? 0 : cluster_rank();
+    const int lane = WARP ? threadIdx.x % 32 : threadIdx.x;
+    constexpr int width = WARP ? 32 : kThreads;
+    const uint32_t r = WARP ? blockIdx.x * kWarps + threadIdx.x / 32 : blockIdx.x / size;
+    if (r >= tokens.n) return;
+    const char* row = logits.at(r);
+    char* out = grad.at(r);
+    const RowSplit<DT> sp(row, cols);
+    const bool vector_out = ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
+    const int first = int(int64_t(sp.vecs) * rank / size);
+    const int end = int(int64_t(sp.vecs) * (rank + 1) / size);
+    const int extra = extra_element<DT>(sp, lane, rank == 0, rank == size - 1);
+    const bool writer = lane == 0 && rank == 0;
+
+    const int64_t t = a.targets[r];
+    if (t == a.ignore) {
+        zero_row<DT>(out, vector_out, sp, first, end, lane, width, extra);
+        if (writer) {
+            a.logp[r] = 0.0f;
+            if (a.entropy) a.entropy[r] = 0.0f;
+        }
+        return;  // the whole group
+    }
+    uint4* slice = slices + (WARP ? (threadIdx.x / 32) * (cols / E::kVec) : 0);
+    const uint4* body = reinterpret_cast<const uint4*>(row + int64_t(sp.head) * E::kSize) + first;
+    const int n = end - first;
+    int asked = lane;
+    auto ask = [&] {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            if (asked + u * width < n) copy_async16(slice + asked + u * width, body + asked + u * width);
+        asked += kUnroll * width;
+        copy_commit();
+    };
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) ask();
+
+    const float c = scale * kLog2e;
+    const bool bad = t < 0 || t >= cols;
+    const float xt = bad ? 0.0f : E::load(row, t);
+    const float xe = extra >= 0 ? E::load(row, extra) : -kInf;
+    const float old = a.old_logp[r];
+    const float ref = a.ref_logp ? a.ref_logp[r] : 0.0f;
+    const int32_t seq = tokens.sequence(r);
+    const float A = seq < 0 ? 0.0f : a.advantages[P.per_token ? r : uint32_t(seq)];
+    const float w = seq < 0 ? 0.0f
+                            : token_weight(P.reduce, P.inv_divisor, a.counts->tokens, a.counts->filled,
+                                           a.counts->sequence[seq]) * P.grad_scale;
+
+    Online o = {-kInf, 0.0f, 0.0f};
+    for (int base = lane; base < n; base += kUnroll * width) {
+        copy_wait<kDepth - 1>();
+        float x[kUnroll * E::kVec];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            E::unpack(base + u * width < n ? slice[base + u * width]
+                                           : make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf),
+                      x + u * E::kVec);
+        absorb<ENT, kUnroll * E::kVec>(o, x, c);
+        ask();
+    }
+    const float x2[2] = {xe, -kInf};
+    absorb<ENT, 2>(o, x2, c);
+    o = group_join<ENT, WARP>(o, c);
+
+    RowStats rs = row_stats<ENT>(o, scale);
+    if (bad) rs.m = rs.log_s = rs.entropy = __int_as_float(0x7fc00000);
+    const float lp = logp_of(rs, xt, scale);
+    if (writer) {
+        a.logp[r] = lp;
+        if (a.entropy) a.entropy[r] = rs.entropy;
+    }
+    const PolicyToken k = policy_token(P, lp, old, a.ref_logp != nullptr, ref, A);
+    if (rs.log_s == kInf || seq < 0) {
+        zero_row<DT>(out, vector_out, sp, first, end, lane, width, extra);
+        return;
+    }
+    const float ga = scale * w * k.grad, gb = ENT ? -scale * w * P.entropy_coef : 0.0f;
+    const float log2_s = rs.log_s * kLog2e;
+#pragma unroll 4
+    for (int i = lane; i < n; i += width)
+        grad_vector<DT, ENT>(slice[i], out, vector_out, sp.head + (first + i) * E::kVec, t, rs.m, rs.log_s,
+                             log2_s, scale, c, ga, gb, rs.entropy);
+    if (extra >= 0)
+        E::store(out, extra,
+                 logit_grad<ENT>(xe, rs.m, rs.log_s, log2_s, scale, c, ga, gb, rs.entropy) +
+                     (extra == t ? ga : 0.0f));
+}
+
+// ------------------------------------------------------------------- host --
+
+// Fewest CTAs that keep the GPU busy: rows below it are split over clusters.
+constexpr int64_t kBusyCtas = 304;
+constexpr int kMaxCluster = 8;
+constexpr int64_t kMaxSmem = 200 * 1024;    // a CTA's share of a row, at most
+constexpr int64_t kWantSmem = 108 * 1024;   // two CTAs to an SM
+
+int vec_of(int32_t dt) { return dt == ADAMW_DTYPE_FP32 ? 4 : 8; }
+
+bool same_rows(const adamw_rows_t* a, const adamw_rows_t* b) {
+    return a->data == b->data && a->inner == b->inner &&
+           (a->inner == 1 || a->row_stride == b->row_stride) &&
+           (a->rows == a->inner || a->outer_stride == b->outer_stride);
+}
+
+// Elements from the first of `data` to one past the last.
+int64_t extent(const adamw_rows_t* m) {
+    if (m->rows == 0) return 0;
+    return (m->rows / m->inner - 1) * m->outer_stride + (m->inner - 1) * m->row_stride + m->cols;
+}
+
+int check_rows(const adamw_rows_t* m, bool written) {
+    if (!m || m->rows < 0 || m->cols < 0 || m->inner < 1 || m->outer_stride < 0 || m->row_stride < 0)
+        return ADAMW_ERR_INVALID_ARG;
+    const int size = dtype_size(m->dtype);
+    if (size == 0) return ADAMW_ERR_INVALID_ARG;
+    if (m->rows == 0) return ADAMW_OK;
+    if (!m->data || m->cols < 1 || m->rows % m->inner != 0) return ADAMW_ERR_INVALID_ARG;
+    if (m->rows > kMaxCount) return ADAMW_ERR_TOO_LARGE;
+    // offsets stay far inside 64 bits
+    constexpr int64_t kMaxStride = int64_t(1) << 40;
+    if (m->outer_stride > kMaxStride || m->row_stride > kMaxStride) return ADAMW_ERR_TOO_LARGE;
+    const int64_t outer = m->rows / m->inner;
+    if ((outer > 1 && m->outer_stride > (int64_t(1) << 60) / outer) ||
+        (m->inner > 1 && m->row_stride > (int64_t(1) << 60) / m->inner))
+        return ADAMW_ERR_TOO_LARGE;
+    if (!aligned(m->data, uintptr_t(size))) return ADAMW_ERR_MISALIGNED;
+    if (written) {
+        // rows apart from one another, the smaller stride's run inside the larger
+        const bool in = m->inner > 1, out = outer > 1;
+        const int64_t small = in && out ? (m->row_stride < m->outer_stride ? m->row_stride : m->outer_stride)
+                              : in ? m->row_stride : m->outer_stride;
+        if ((in || out) && small < m->cols) return ADAMW_ERR_INVALID_ARG;
+        if (in && out) {
+            const bool rows_inside = m->row_stride <= m->outer_stride;
+            const int64_t run = rows_inside ? (m->inner - 1) * m->row_stride : (outer - 1) * m->outer_stride;
+            if ((rows_inside ? m->outer_stride : m->row_stride) < run + m->cols) return ADAMW_ERR_INVALID_ARG;
+        }
+    }
+    return ADAMW_OK;
+}
+
+int check_gradient(const adamw_rows_t* x, const adamw_rows_t* d) {
+    int rc = check_rows(d, true);
+    if (rc != ADAMW_OK) return rc;
+    if (d->rows != x->rows || d->cols != x->cols || d->dtype != x->dtype) return ADAMW_ERR_INVALID_ARG;
+    if (x->rows == 0 || same_rows(x, d)) return ADAMW_OK;
+    const uintptr_t size = uintptr_t(dtype_size(x->dtype));
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x->data), b = reinterpret_cast<uintptr_t>(d->data);
+    const bool apart = a + uintptr_t(extent(x)) * size <= b || b + uintptr_t(extent(d)) * size <= a;
+    return apart ? ADAMW_OK : ADAMW_ERR_INVALID_ARG;
+}
+
+Rows rows_of(const adamw_rows_t* m) {
+    Rows r;
+    const int64_t size = dtype_size(m->dtype);
+    r.data = static_cast<char*>(m->data);
+    r.outer = m->outer_stride * size;
+    r.row = m->row_stride * size;
+    r.inner = uint32_t(m->inner);
+    return r;
+}
+
+bool good_scale(float s) { return s > 0.0f && std::isfinite(s * kLog2e); }
+
+// CTAs per row: one where there are rows enough to keep the GPU busy, else up
+// to eight, each with at least two turns of its threads' vectors.
+int cluster_for(int64_t rows, int64_t vecs, int at_least) {
+    int c = at_least;
+    while (c < kMaxCluster && rows * c < kBusyCtas && vecs >= int64_t(2) * c * 2 * kThreads) c *= 2;
+    return c;
+}
+
+uint32_t grid_of(int64_t groups) { return groups > 0 && groups <= kMaxCount ? uint32_t(groups) : 0; }
+
+template <int DT>
+cudaError_t forward(const adamw_rows_t* x, const int64_t* targets, int64_t ignore, float scale,
+                    float* logp, float* entropy, float* stats, cudaStream_t st) {
+    const Rows rows = rows_of(x);
+    const uint32_t n = uint32_t(x->rows);
+    if (x->cols <= kWarpCols) {
+        auto k = entropy ? logprob_kernel<DT, true, true> : logprob_kernel<DT, false, true>;
+        return launch(k, (n + kWarps - 1) / kWarps, kThreads, 1, 0, st, rows, n, x->cols, targets, ignore,
+                      scale, logp, entropy, stats);
+    }
+    const int c = cluster_for(x->rows, x->cols / Elem<DT>::kVec, 1);
+    auto k = entropy ? logprob_kernel<DT, true, false> : logprob_kernel<DT, false, false>;
+    const uint32_t grid = grid_of(x->rows * c);
+    if (!grid) return cudaErrorInvalidConfiguration;
+    return launch(k, grid, kThreads, c, 0, st, rows, n, x->cols, targets, ignore, scale, logp, entropy, stats);
+}
+
+template <int DT>
+cudaError_t backward(const adamw_rows_t* x, const int64_t* targets, float scale, const float* stats,
+                     const float* entropy, const float* d_logp, const float* d_entropy,
+                     const adamw_rows_t* dx, cudaStream_t st) {
+    const Rows in = rows_of(x), out = rows_of(dx);
+    const uint32_t n = uint32_t(x->rows);
+    if (x->cols <= kWarpCols) {
+        auto k = d_entropy ? logprob_backward_kernel<DT, true, true> : logprob_backward_kernel<DT, false, true>;
+        return launch(k, (n + kWarps - 1) / kWarps, kThreads, 1, 0, st, in, out, n, 1u, x->cols, targets,
+                      scale, stats, entropy, d_logp, d_entropy);
+    }
+    const int64_t per = int64_t(kThreads) * kUnroll * Elem<DT>::kVec;
+    const uint32_t pieces = uint32_t((x->cols + per - 1) / per);
+    auto k = d_entropy ? logprob_backward_kernel<DT, true, false> : logprob_backward_kernel<DT, false, false>;
+    const uint32_t grid = grid_of(x->rows * pieces);
+    if (!grid) return cudaErrorInvalidConfiguration;
+    return launch(k, grid, kThreads, 1, 0, st, in, out, n, pieces, x->cols, targets, scale, stats, entropy,
+                  d_logp, d_entropy);
+}
+
+// Allows a kernel its dynamic shared memory, once per device.
+cudaError_t allow_smem(const void* kernel, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMaxSmem));
+    if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
+// A row's vectors in shared memory fit a cluster.
+bool fits_cluster(const adamw_rows_t* x) {
+    return int64_t(x->cols / vec_of(x->dtype)) * 16 <= int64_t(kMaxCluster) * (kMaxSmem - 16);
+}
+
+template <int DT, bool ENT>
+cudaError_t policy_rows(const adamw_rows_t* x, const adamw_rows_t* dx, const Tokens& tokens, float scale,
+                        const Policy& P, const PolicyRows& a, cudaStream_t st) {
+    const Rows in = rows_of(x), out = rows_of(dx);
+    const int64_t vecs = x->cols / Elem<DT>::kVec;
+    if (x->cols <= kWarpCols) {
+        // a CTA's eight rows: at most 8 * 1024 * 4 bytes
+        return launch(policy_rows_kernel<DT, ENT, true>, (tokens.n + kWarps - 1) / kWarps, kThreads, 1,
+                      size_t(vecs) * 16 * kWarps, st, in, out, tokens, x->cols, scale, P, a);
+    }
+    auto k = policy_rows_kernel<DT, ENT, false>;
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), done);
+    if (e != cudaSuccess) return e;
+    int c = 1;
+    while (c < kMaxCluster && (vecs + c - 1) / c * 16 > kWantSmem) c *= 2;
+    c = cluster_for(x->rows, vecs, c);
+    const uint32_t grid = grid_of(x->rows * c);
+    if (!grid) return cudaErrorInvalidConfiguration;
+    return launch(k, grid, kThreads, c, size_t((vecs + c - 1) / c) * 16, st, in, out, tokens, x->cols,
+                  scale, P, a);
+}
+
+template <int DT>
+cudaError_t policy_rows(const adamw_rows_t* x, const adamw_rows_t* dx, const Tokens& tokens, float scale,
+                        const Policy& P, const PolicyRows& a, cudaStream_t st) {
+    return a.entropy ? policy_rows<DT, true>(x, dx, tokens, scale, P, a, st)
+                     : policy_rows<DT, false>(x, dx, tokens, scale, P, a, st);
+}
+
+int64_t round16(int64_t x) { return (x + 15) / 16 * 16; }
+
+}  // namespace
+
+extern "C" int adamw_token_logprob(const adamw_rows_t* logits, const int64_t* targets,
+                                   int64_t ignore_index, float scale, float* logp, float* entropy,
+                                   float* stats, adamw_stream_t stream) {
+    const int rc = check_rows(logits, false);
+    if (rc != ADAMW_OK) return rc;
+    if (!good_scale(scale)) return ADAMW_ERR_INVALID_ARG;
+    if (logits->rows == 0) return ADAMW_OK;
+    if (!targets || !logp) return ADAMW_ERR_INVALID_ARG;
+    if (!aligned(targets, 8) || !aligned(logp, 4) || !aligned(entropy, 4) || !aligned(stats, 8))
+        return ADAMW_ERR_MISALIGNED;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    switch (logits->dtype) {
+        case ADAMW_DTYPE_BF16: e = forward<ADAMW_DTYPE_BF16>(logits, targets, ignore_index, scale, logp, entropy, stats, st); break;
+        case ADAMW_DTYPE_FP16: e = forward<ADAMW_DTYPE_FP16>(logits, targets, ignore_index, scale, logp, entropy, stats, st); break;
+        default: e = forward<ADAMW_DTYPE_FP32>(logits, targets, ignore_index, scale, logp, entropy, stats, st); break;
+    }
+    return launched(e, "token_logprob launch") ? ADAMW_OK : ADAMW_ERR_CUDA;
+}
+
+extern "C" int adamw_token_logprob_backward(const adamw_rows_t* logits, const int64_t* targets,
+                                            int64_t ignore_index, float scale, const float* stats,
+                                            const float* entropy, const float* d_logp,
+                                            const float* d_entropy, const adamw_rows_t* d_logits,
+                                            adamw_stream_t stream) {
+    (void)ignore_index;  // the forward call marked those rows in stats
+    int rc = check_rows(logits, false);
+    if (rc != ADAMW_OK) return rc;
+    if (!d_logits) return ADAMW_ERR_INVALID_ARG;
+    rc = check_gradient(logits, d_logits);
+    if (rc != ADAMW_OK) return rc;
+    if (!good_scale(scale)) return ADAMW_ERR_INVALID_ARG;
+    if (logits->rows == 0) return ADAMW_OK;
+    if (!targets || !stats || !d_logp || (d_entropy && !entropy)) return ADAMW_ERR_INVALID_ARG;
+    if (!aligned(targets, 8) || !aligned(stats, 8) || !aligned(d_logp, 4) || !aligned(d_entropy, 4) ||
+        !aligned(entropy, 4))
+        return ADAMW_ERR_MISALIGNED;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    switch (logits->dtype) {
+        case ADAMW_DTYPE_BF16: e = backward<ADAMW_DTYPE_BF16>(logits, targets, scale, stats, entropy, d_logp, d_entropy, d_logits, st); break;
+        case ADAMW_DTYPE_FP16: e = backward<ADAMW_DTYPE_FP16>(logits, targets, scale, stats, entropy, d_logp, d_entropy, d_logits, st); break;
+        default: e = backward<ADAMW_DTYPE_FP32>(logits, targets, scale, stats, entropy, d_logp, d_entropy, d_logits, st); break;
+    }
+    return launched(e, "token_logprob_backward launch") ? ADAMW_OK : ADAMW_ERR_CUDA;
+}
+
+// The workspace: the policy loss's, then (used for rows too long for a
+// cluster) the forward pass's stats and the gradients of logp and entropy.
+extern "C" int64_t adamw_policy_logits_workspace(int64_t n, int64_t sequences) {
+    const int64_t base = adamw_policy_workspace(n, sequences);
+    return base == 0 ? 0 : round16(base) + round16(8 * n) + 2 * round16(4 * n);
+}
+
+extern "C" int adamw_policy_loss_logits(const adamw_rows_t* logits, const int64_t* targets,
+                                        int64_t ignore_index, float scale, const adamw_tokens_t* tokens,
+                                        const adamw_policy_t* policy, const float* old_logp,
+                                        const float* ref_logp, const float* advantages, float* stats,
+                                        int64_t* counts, float* logp, float* entropy,
+                                        const adamw_rows_t* d_logits, void* workspace,
+                                        adamw_stream_t stream) {
+    int rc = check_rows(logits, false);
+    if (rc != ADAMW_OK) return rc;
+    if (!d_logits) return ADAMW_ERR_INVALID_ARG;
+    rc = check_gradient(logits, d_logits);
+    if (rc != ADAMW_OK) return rc;
+    rc = adamw::check_tokens(tokens);
+    if (rc != ADAMW_OK) return rc;
+    rc = adamw::check_policy(policy);
+    if (rc != ADAMW_OK) return rc;
+    if (!good_scale(scale) || tokens->mask || tokens->n != logits->rows) return ADAMW_ERR_INVALID_ARG;
+    if (!stats || !counts || !workspace || (policy->entropy_coef != 0.0f && !entropy) ||
+        (policy->kl_coef != 0.0f && !ref_logp))
+        return ADAMW_ERR_INVALID_ARG;
+    if (tokens->n > 0 && (!targets || !old_logp || !advantages || !logp)) return ADAMW_ERR_INVALID_ARG;
+    if (!aligned(targets, 8) || !aligned(old_logp, 4) || !aligned(ref_logp, 4) || !aligned(advantages, 4) ||
+        !aligned(stats, 4) || !aligned(counts, 8) || !aligned(logp, 4) || !aligned(entropy, 4) ||
+        !aligned(workspace, 16))
+        return ADAMW_ERR_MISALIGNED;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    rc = adamw::launch_counts(tokens, targets, ignore_index, workspace, st);
+    if (rc != ADAMW_OK) return rc;
+    if (tokens->n == 0 || fits_cluster(logits)) {
+        if (tokens->n > 0) {
+            const Tokens t = tokens_of(tokens, targets, ignore_index);
+            const Policy P = policy_of(policy);
+            const PolicyRows a = {targets, ignore_index, old_logp, ref_logp, advantages,
+                                  static_cast<const Counts*>(workspace), logp, entropy};
+            cudaError_t e;
+            switch (logits->dtype) {
+                case ADAMW_DTYPE_BF16: e = policy_rows<ADAMW_DTYPE_BF16>(logits, d_logits, t, scale, P, a, st); break;
+                case ADAMW_DTYPE_FP16: e = policy_rows<ADAMW_DTYPE_FP16>(logits, d_logits, t, scale, P, a, st); break;
+                default: e = policy_rows<ADAMW_DTYPE_FP32>(logits, d_logits, t, scale, P, a, st); break;
+            }
+            if (!launched(e, "policy_loss_logits launch")) return ADAMW_ERR_CUDA;
+        }
+        return adamw::launch_policy(tokens, policy, targets, ignore_index, logp, old_logp, ref_logp,
+                                    advantages, entropy, stats, counts, nullptr, nullptr, workspace, st);
+    }
+    char* w = static_cast<char*>(workspace) + round16(adamw_policy_workspace(tokens->n, tokens->sequences));
+    float* row_stats = reinterpret_cast<float*>(w);
+    float* d_logp = reinterpret_cast<float*>(w + round16(8 * tokens->n));
+    float* d_entropy = entropy ? reinterpret_cast<float*>(w + round16(8 * tokens->n) + round16(4 * tokens->n)) : nullptr;
+    rc = adamw_token_logprob(logits, targets, ignore_index, scale, logp, entropy, row_stats, stream);
+    if (rc != ADAMW_OK) return rc;
+    rc = adamw::launch_policy(tokens, policy, targets, ignore_index, logp, old_logp, ref_logp, advantages,
+                              entropy, stats, counts, d_logp, d_entropy, workspace, st);
+    if (rc != ADAMW_OK) return rc;
+    return adamw_token_logprob_backward(logits, targets, ignore_index, scale, row_stats, entropy, d_logp,
+                                        d_entropy, d_logits, stream);
+}

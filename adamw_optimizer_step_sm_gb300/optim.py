@@ -209,6 +209,16 @@ class _FlatAdamW(torch.optim.Optimizer):
                 self._sync_master(b, k, p, force=True)
 
     # -- the step -----------------------------------------------------------
+    def _gather(self, group, b: _GroupBuffers) -> None:
+        """Brings gradients found outside the group's buffer into it."""
+        for k, (p, g) in enumerate(zip(group["params"], b.grads)):
+            if p.grad is None:
+                raise RuntimeError(f"parameter {k} of a group has no gradient; "
+                                   f"{type(self).__name__} steps every parameter")
+            if p.grad.data_ptr() != g.data_ptr():
+                g.copy_(p.grad)
+                p.grad = g
+
     @torch.no_grad()
     def step(self, closure=None):
         loss = None
@@ -218,13 +228,7 @@ class _FlatAdamW(torch.optim.Optimizer):
         for group in self.param_groups:
             b = self._buffers_of(group)
             self._check_masters(group, b)
-            for k, (p, g) in enumerate(zip(group["params"], b.grads)):
-                if p.grad is None:
-                    raise RuntimeError(f"parameter {k} of a group has no gradient; "
-                                       f"{type(self).__name__} steps every parameter")
-                if p.grad.data_ptr() != g.data_ptr():
-                    g.copy_(p.grad)
-                    p.grad = g
+            self._gather(group, b)
             beta1, beta2 = group["betas"]
             # plain floats (a scheduler may keep lr as a tensor)
             key = tuple(float(x) for x in (group["lr"], beta1, beta2, group["eps"],
@@ -357,3 +361,35 @@ class MasterWeightAdamW(_FlatAdamW):
         self._aux_name = "remainder"
         super().__init__(params, modes[master], lr, betas, eps, weight_decay, max_grad_norm,
                          track_grad_norm)
+
+
+class GlobalClip:
+    """Clips the gradients of every parameter group of one or more of this
+    module's optimizers by one norm over them all, in place, before their
+    steps (a group's own ``max_grad_norm`` knows that group's gradients
+    only):
+
+        clip = GlobalClip(optimizer)              # or several
+        loss.backward(); clip(1.0); optimizer.step()
+
+    Returns the library's ``ClipResult`` (norm, coefficient, non-finite flag,
+    device tensors of the plan).  Non-finite gradients are passed on
+    unscaled: the optimizers report them (``last_nonfinite``)."""
+
+    def __init__(self, *optimizers: _FlatAdamW):
+        if not optimizers or not all(isinstance(o, _FlatAdamW) for o in optimizers):
+            raise TypeError("want one or more optimizers of this module")
+        self.optimizers = optimizers
+        self._plan, self._of = None, None
+
+    @torch.no_grad()
+    def __call__(self, max_norm: float, norm: str = "l2") -> A.ClipResult:
+        groups = [(o, g, o._buffers_of(g)) for o in self.optimizers for g in o.param_groups]
+        for o, group, b in groups:
+            o._gather(group, b)
+        flat = [b.grad for _, _, b in groups]
+        if self._of is None or len(flat) != len(self._of) or any(x is not y for x, y in zip(flat, self._of)):
+            if self._plan is not None:
+                self._plan.close()
+            self._plan, self._of = A.ClipPlan(flat), flat   # rebuilt when a group was added
+        return self._plan.clip(max_norm, norm=norm)
