@@ -13,10 +13,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-// Elements of a tile, the piece of a tensor that a CTA takes at a time.
-constexpr int kTile = 16384;
+// Elements of a tile, the piece of a tensor that a CTA takes at a time: the
+// largest that gives every resident CTA one, in [2048, 16384].
+constexpr int kMaxTile = 16384, kMinTile = 2048;
 constexpr int kNormUnroll = 8;   // 16-byte vectors in flight per thread
-constexpr int kScaleVecs = 4;    // likewise, when scaling
+constexpr int kScaleVecs = 8;    // likewise, when scaling
 constexpr int kMaxGrid = 1216;   // CTAs of the norm pass at most: its partials
 
 struct alignas(16) Tile {
@@ -24,8 +25,8 @@ struct alignas(16) Tile {
     char* dst;
     int32_t len;
     int32_t src_type;
-    int32_t dst_type;
     int32_t vector;   // both 16-byte aligned
+    int32_t pad_;
 };
 static_assert(sizeof(Tile) == 32, "tile layout");
 
@@ -45,8 +46,9 @@ struct ClipState {
 struct SquareSum {
     Sum2 sum;
     double rare;
+    // false: the group has to be summed by add_rare
     template <typename E, int U>
-    __device__ __forceinline__ void add(const uint4 (&v)[U]) {
+    __device__ __forceinline__ bool add(const uint4 (&v)[U]) {
         float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -58,19 +60,12 @@ struct SquareSum {
         const float g = (s[0] + s[1]) + (s[2] + s[3]);
         if (g >= 0x1p-100f && g <= 0x1p100f) {
             sum.add(g);
-        } else {
-            uint32_t any = 0;
-#pragma unroll
-            for (int u = 0; u < U; ++u) any |= v[u].x | v[u].y | v[u].z | v[u].w;
-            if ((any & ~E::kSigns) != 0) {   // not all zeros
-#pragma unroll 1
-                for (int u = 0; u < U; ++u) {
-                    float x[E::kVec];
-                    E::unpack(v[u], x);
-                    for (int i = 0; i < E::kVec; ++i) add_rare(x[i]);
-                }
-            }
+            return true;
         }
+        uint32_t any = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) any |= v[u].x | v[u].y | v[u].z | v[u].w;
+        return (any & ~E::kSigns) == 0;   // zeros
     }
     __device__ __forceinline__ void add(float x) {
         const float g = x * x;
@@ -84,7 +79,7 @@ struct SquareSum {
 struct MaxBits {
     uint32_t bits;
     template <typename E, int U>
-    __device__ __forceinline__ void add(const uint4 (&v)[U]) {
+    __device__ __forceinline__ bool add(const uint4 (&v)[U]) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float x[E::kVec];
@@ -92,7 +87,9 @@ struct MaxBits {
 #pragma unroll
             for (int i = 0; i < E::kVec; ++i) add(x[i]);
         }
+        return true;
     }
+    __device__ __forceinline__ void add_rare(float) {}
     __device__ __forceinline__ void add(float x) {
         const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
         bits = b > bits ? b : bits;
@@ -105,13 +102,33 @@ __device__ __forceinline__ void norm_tile(const Tile& t, Acc& acc) {
     int done = 0;
     if (t.vector) {
         const int vecs = t.len / E::kVec;
-        for (int base = threadIdx.x; base < vecs; base += kNormUnroll * kThreads) {
+        constexpr int kBatch = kNormUnroll * kThreads;
+        const char* src = t.src + threadIdx.x * 16;
+        int base = 0;
+        // the batch again, from L2, element by element
+        auto again = [&] {
+#pragma unroll 1
+            for (int u = 0; u < kNormUnroll; ++u) {
+                if (base + u * kThreads + int(threadIdx.x) >= vecs) break;
+                float x[E::kVec];
+                E::unpack(load16(src + (base + u * kThreads) * 16), x);
+#pragma unroll
+                for (int i = 0; i < E::kVec; ++i) acc.add_rare(x[i]);
+            }
+        };
+        for (; base + kBatch <= vecs; base += kBatch) {
+            uint4 v[kNormUnroll];
+#pragma unroll
+            for (int u = 0; u < kNormUnroll; ++u) v[u] = load16(src + (base + u * kThreads) * 16);
+            if (!acc.template add<E, kNormUnroll>(v)) again();
+        }
+        if (base < vecs) {
             uint4 v[kNormUnroll];
 #pragma unroll
             for (int u = 0; u < kNormUnroll; ++u)
-                v[u] = base + u * kThreads < vecs
-                           ? load16(t.src + int64_t(base + u * kThreads) * 16) : make_uint4(0, 0, 0, 0);
-            acc.template add<E, kNormUnroll>(v);
+                v[u] = base + u * kThreads + int(threadIdx.x) < vecs
+                           ? load16(src + (base + u * kThreads) * 16) : make_uint4(0, 0, 0, 0);
+            if (!acc.template add<E, kNormUnroll>(v)) again();
         }
         done = vecs * E::kVec;
     }
@@ -197,70 +214,76 @@ grad_norm_kernel(const Tile* tiles, int32_t n, float max_norm, double* partial, 
     }
 }
 
-// Not inlined: the nine pairs of types in one kernel would share, and spill,
-// its registers.
+// dst = coef * src for the tiles [first, first + n), all of the kernel's pair
+// of types.  In reverse: those that the norm pass read last are the likeliest
+// to be in L2 still.
 template <int SRC, int DST>
-__device__ __noinline__ void scale_tile(const char* src, char* dst, int len, bool vector, float2 coef) {
+__global__ void __launch_bounds__(kThreads, 4)
+grad_scale_kernel(const Tile* tiles, int32_t n, const ClipState* state) {
     using S = Elem<SRC>;
     using D = Elem<DST>;
     // elements per step: whole 16-byte vectors on both sides
     constexpr int K = S::kVec > D::kVec ? S::kVec : D::kVec;
     constexpr int kIn = K / S::kVec, kOut = K / D::kVec;
     constexpr int U = kScaleVecs / kIn;
-    int done = 0;
-    if (vector) {
-        const int steps = len / K;
-        for (int base = threadIdx.x; base < steps; base += U * kThreads) {
-            uint4 v[U][kIn];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (base + u * kThreads < steps) {
-#pragma unroll
-                    for (int j = 0; j < kIn; ++j)
-                        v[u][j] = load16(src + (int64_t(base + u * kThreads) * kIn + j) * 16);
-                }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (base + u * kThreads < steps) {
-                    float x[K];
-#pragma unroll
-                    for (int j = 0; j < kIn; ++j) S::unpack(v[u][j], x + j * S::kVec);
-#pragma unroll
-                    for (int j = 0; j < K; ++j) x[j] = x[j] * coef.x * coef.y;
-#pragma unroll
-                    for (int j = 0; j < kOut; ++j)
-                        store16(dst + (int64_t(base + u * kThreads) * kOut + j) * 16, D::pack(x + j * D::kVec));
-                }
-        }
-        done = steps * K;
-    }
-    for (int i = done + threadIdx.x; i < len; i += kThreads) D::store(dst, i, S::load(src, i) * coef.x * coef.y);
-}
-
-template <int SRC>
-__device__ __forceinline__ void scale_tile(const Tile& t, float2 coef) {
-    switch (t.dst_type) {
-        case ADAMW_DTYPE_BF16: scale_tile<SRC, ADAMW_DTYPE_BF16>(t.src, t.dst, t.len, t.vector, coef); break;
-        case ADAMW_DTYPE_FP16: scale_tile<SRC, ADAMW_DTYPE_FP16>(t.src, t.dst, t.len, t.vector, coef); break;
-        default: scale_tile<SRC, ADAMW_DTYPE_FP32>(t.src, t.dst, t.len, t.vector, coef); break;
-    }
-}
-
-// dst = coef * src.  The tiles in reverse: those that the norm pass read last
-// are the likeliest to be in L2 still.
-__global__ void __launch_bounds__(kThreads, 4)
-grad_scale_kernel(const Tile* tiles, int32_t n, const ClipState* state) {
     dependency_trigger();
     dependency_wait();
     const float2 coef = state->coef;
+    auto scaled = [&](uint4 (&v)[kIn], char* dst) {
+        float x[K];
+#pragma unroll
+        for (int j = 0; j < kIn; ++j) S::unpack(v[j], x + j * S::kVec);
+#pragma unroll
+        for (int j = 0; j < K; ++j) x[j] = x[j] * coef.x * coef.y;
+#pragma unroll
+        for (int j = 0; j < kOut; ++j) store16(dst + j * 16, D::pack(x + j * D::kVec));
+    };
     for (int32_t k = n - 1 - int32_t(blockIdx.x); k >= 0; k -= gridDim.x) {
         const Tile t = tiles[k];
-        if (!t.dst || (coef.x == 1.0f && t.dst == t.src)) continue;
-        switch (t.src_type) {
-            case ADAMW_DTYPE_BF16: scale_tile<ADAMW_DTYPE_BF16>(t, coef); break;
-            case ADAMW_DTYPE_FP16: scale_tile<ADAMW_DTYPE_FP16>(t, coef); break;
-            default: scale_tile<ADAMW_DTYPE_FP32>(t, coef); break;
+        if (coef.x == 1.0f && t.dst == t.src) continue;
+        int done = 0;
+        if (t.vector) {
+            const int steps = t.len / K;
+            int base = threadIdx.x;
+            for (; base + (U - 1) * kThreads < steps; base += U * kThreads) {
+                uint4 v[U][kIn];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int j = 0; j < kIn; ++j)
+                        v[u][j] = load16(t.src + ((base + u * kThreads) * kIn + j) * 16);
+#pragma unroll
+                for (int u = 0; u < U; ++u) scaled(v[u], t.dst + (base + u * kThreads) * kOut * 16);
+            }
+            for (; base < steps; base += kThreads) {
+                uint4 v[kIn];
+#pragma unroll
+                for (int j = 0; j < kIn; ++j) v[j] = load16(t.src + (base * kIn + j) * 16);
+                scaled(v, t.dst + base * kOut * 16);
+            }
+            done = steps * K;
         }
+        for (int i = done + threadIdx.x; i < t.len; i += kThreads)
+            D::store(t.dst, i, S::load(t.src, i) * coef.x * coef.y);
+    }
+}
+
+using ScaleKernel = void (*)(const Tile*, int32_t, const ClipState*);
+
+template <int SRC>
+ScaleKernel scale_kernel(int32_t dst) {
+    switch (dst) {
+        case ADAMW_DTYPE_BF16: return grad_scale_kernel<SRC, ADAMW_DTYPE_BF16>;
+        case ADAMW_DTYPE_FP16: return grad_scale_kernel<SRC, ADAMW_DTYPE_FP16>;
+        default: return grad_scale_kernel<SRC, ADAMW_DTYPE_FP32>;
+    }
+}
+
+ScaleKernel scale_kernel(int32_t src, int32_t dst) {
+    switch (src) {
+        case ADAMW_DTYPE_BF16: return scale_kernel<ADAMW_DTYPE_BF16>(dst);
+        case ADAMW_DTYPE_FP16: return scale_kernel<ADAMW_DTYPE_FP16>(dst);
+        default: return scale_kernel<ADAMW_DTYPE_FP32>(dst);
     }
 }
 
@@ -321,7 +344,12 @@ struct adamw_clip_plan {
     int device = 0;
     int32_t n_tiles = 0;
     int32_t norm_grid[2] = {0, 0};   // by ADAMW_NORM_*
-    int32_t scale_grid = 0;
+    // the tiles to scale, by their pair of types
+    struct Group {
+        ScaleKernel kernel;
+        int32_t first, n, grid;
+    };
+    std::vector<Group> groups;
     void* block = nullptr;           // tiles, then partials, then the state
     Tile* tiles = nullptr;
     double* partial = nullptr;
@@ -336,38 +364,55 @@ int create(const adamw_grad_t* table, int32_t n, adamw_clip_plan* P) {
     if (!launched(cudaDeviceGetAttribute(&pageable, cudaDevAttrPageableMemoryAccess, P->device), "cudaDeviceGetAttribute") ||
         !launched(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, P->device), "cudaDeviceGetAttribute"))
         return ADAMW_ERR_CUDA;
-    std::vector<Tile> tiles;
+    int64_t total = 0;
     for (int32_t k = 0; k < n; ++k) {
         const adamw_grad_t& g = table[k];
         if (g.numel == 0) continue;
         int rc = check_access(g.src, P->device, pageable);
         if (rc == ADAMW_OK && g.dst) rc = check_access(g.dst, P->device, pageable);
         if (rc != ADAMW_OK) return rc;
-        const int s = dtype_size(g.src_dtype), d = g.dst ? dtype_size(g.dst_dtype) : 0;
-        Tile t = {};
-        t.src_type = g.src_dtype;
-        t.dst_type = g.dst ? g.dst_dtype : 0;
-        t.vector = aligned(g.src, 16) && aligned(g.dst, 16);
-        for (int64_t at = 0; at < g.numel; at += kTile) {
-            t.src = static_cast<const char*>(g.src) + at * s;
-            t.dst = g.dst ? static_cast<char*>(g.dst) + at * d : nullptr;
-            t.len = int32_t(g.numel - at < kTile ? g.numel - at : kTile);
-            tiles.push_back(t);
-        }
+        total += g.numel;
     }
-    if (int64_t(tiles.size()) > kMaxCount - kMaxGrid) return ADAMW_ERR_TOO_LARGE;
+    int64_t tile = kMaxTile;
+    while (tile > kMinTile && total < tile * sms * 4) tile /= 2;
+    // pair by pair of types, tensors that are only read first
+    std::vector<Tile> tiles;
+    for (int pair = -1; pair < 9; ++pair) {
+        const size_t first = tiles.size();
+        for (int32_t k = 0; k < n; ++k) {
+            const adamw_grad_t& g = table[k];
+            if (g.numel == 0 || (g.dst ? g.src_dtype * 3 + g.dst_dtype : -1) != pair) continue;
+            const int s = dtype_size(g.src_dtype), d = g.dst ? dtype_size(g.dst_dtype) : 0;
+            Tile t = {};
+            t.src_type = g.src_dtype;
+            t.vector = aligned(g.src, 16) && aligned(g.dst, 16);
+            for (int64_t at = 0; at < g.numel; at += tile) {
+                t.src = static_cast<const char*>(g.src) + at * s;
+                t.dst = g.dst ? static_cast<char*>(g.dst) + at * d : nullptr;
+                t.len = int32_t(g.numel - at < tile ? g.numel - at : tile);
+                tiles.push_back(t);
+            }
+        }
+        if (int64_t(tiles.size()) > kMaxCount - kMaxGrid) return ADAMW_ERR_TOO_LARGE;
+        const int32_t count = int32_t(tiles.size() - first);
+        if (pair < 0 || count == 0) continue;
+        ScaleKernel kernel = scale_kernel(pair / 3, pair % 3);
+        int occ = 0;
+        if (!launched(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, kThreads, 0), "occupancy"))
+            return ADAMW_ERR_CUDA;
+        const int32_t grid = sms * (occ > 0 ? occ : 1);
+        P->groups.push_back({kernel, int32_t(first), count, grid < count ? grid : count});
+    }
     P->n_tiles = int32_t(tiles.size());
-    int occ[3] = {0, 0, 0};
+    int occ[2] = {0, 0};
     if (!launched(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ[0], grad_norm_kernel<false>, kThreads, 0), "occupancy") ||
-        !launched(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ[1], grad_norm_kernel<true>, kThreads, 0), "occupancy") ||
-        !launched(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ[2], grad_scale_kernel, kThreads, 0), "occupancy"))
+        !launched(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ[1], grad_norm_kernel<true>, kThreads, 0), "occupancy"))
         return ADAMW_ERR_CUDA;
-    int32_t* grids[3] = {&P->norm_grid[0], &P->norm_grid[1], &P->scale_grid};
-    for (int k = 0; k < 3; ++k) {
+    for (int k = 0; k < 2; ++k) {
         int64_t g = int64_t(sms) * (occ[k] > 0 ? occ[k] : 1);
-        if (k < 2 && g > kMaxGrid) g = kMaxGrid;
+        if (g > kMaxGrid) g = kMaxGrid;
         // one CTA at least: an empty list's norm is 0
-        *grids[k] = int32_t(g < P->n_tiles ? g : P->n_tiles > 0 ? P->n_tiles : 1);
+        P->norm_grid[k] = int32_t(g < P->n_tiles ? g : P->n_tiles > 0 ? P->n_tiles : 1);
     }
     const size_t tile_bytes = sizeof(Tile) * tiles.size();
     if (!launched(cudaMalloc(&P->block, tile_bytes + kMaxGrid * sizeof(double) + sizeof(ClipState)), "cudaMalloc"))
@@ -419,10 +464,12 @@ extern "C" int adamw_clip_grads(adamw_clip_plan_t plan, float max_norm, int32_t 
     if (!launched(launch(kernel, uint32_t(plan->norm_grid[norm]), kThreads, 1, 0, st, static_cast<const Tile*>(plan->tiles), plan->n_tiles,
                          max_norm, plan->partial, plan->state, result), "grad_norm launch"))
         return ADAMW_ERR_CUDA;
-    return launched(launch(grad_scale_kernel, uint32_t(plan->scale_grid), kThreads, 1, 0, st,
-                           static_cast<const Tile*>(plan->tiles), plan->n_tiles,
-                           static_cast<const ClipState*>(plan->state)), "grad_scale launch")
-               ? ADAMW_OK : ADAMW_ERR_CUDA;
+    for (auto g = plan->groups.rbegin(); g != plan->groups.rend(); ++g)
+        if (!launched(launch(g->kernel, uint32_t(g->grid), kThreads, 1, 0, st,
+                             static_cast<const Tile*>(plan->tiles + g->first), g->n,
+                             static_cast<const ClipState*>(plan->state)), "grad_scale launch"))
+            return ADAMW_ERR_CUDA;
+    return ADAMW_OK;
 }
 
 extern "C" int adamw_clip_plan_destroy(adamw_clip_plan_t plan) {

@@ -263,7 +263,8 @@ int adamw_clip_plan_create(const adamw_grad_t* host_table, int32_t n, adamw_clip
  * it reaches the optimizer, whose step reports it or is skipped.
  * max_norm > 0 (infinity: no clipping).  norm: ADAMW_NORM_*.
  * result: device adamw_clip_result_t, 16-byte aligned.
- * Two launches, no host synchronisation; sums run in a fixed order.
+ * A launch for the norm and one for each pair of types in the list; no host
+ * synchronisation; sums run in a fixed order.
  * Errors: INVALID_ARG, MISALIGNED, CUDA. */
 int adamw_clip_grads(adamw_clip_plan_t plan, float max_norm, int32_t norm,
                      adamw_clip_result_t* result, adamw_stream_t stream);
