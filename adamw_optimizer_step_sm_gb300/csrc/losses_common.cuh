@@ -358,10 +358,80 @@ struct Tokens {
         }
         return int64_t(i) >= offsets[lo] && int64_t(i) < offsets[lo + 1] ? int32_t(lo) : -1;
     }
-    __device__ __forceinline__ bool counts(uint32_t i) const {
-        if (mask) return mask[i] != 0;
-        if (targets) return targets[i] != ignore;
-        return true;
+
+    // The sequences of the N tokens from `first` on, for every lane of a warp
+    // whose lane 0 starts at `base` and which covers [base, base + 32 N).
+    // Called by whole warps.
+    template <int N>
+    __device__ __forceinline__ void sequences_of(uint32_t base, uint32_t first, int32_t (&seq)[N]) const {
+        if (!offsets) {
+            uint32_t q = first / length, r = first - q * length;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                seq[j] = int32_t(q);
+                if (++r == length) { r = 0; ++q; }
+            }
+            return;
+        }
+        // how many of the sequences + 1 offsets are <= base: each round the
+        // lanes probe 32 points of what is left, so 2048 take three loads
+        const uint32_t lane = threadIdx.x % 32;
+        uint32_t lo = 0, hi = sequences + 1;  // offsets[0, lo) <= base < offsets[hi, ..)
+        while (lo < hi) {
+            const uint32_t step = (hi - lo + 31) / 32;
+            const uint32_t at = lo + lane * step;
+            const bool below = at < hi && offsets[at] <= int64_t(base);
+            // ascending offsets: the lanes below are the first ones
+            const uint32_t k = __popc(__ballot_sync(0xffffffffu, below));
+            if (k == 0) break;
+            const uint32_t next = lo + k * step;
+            lo = lo + (k - 1) * step + 1;
+            hi = next < hi ? next : hi;
+        }
+        // the offsets inside the warp's tokens, in the lanes
+        const uint32_t at = lo + lane;
+        const int64_t past = int64_t(base) + 32 * N;
+        const int64_t mine = at <= sequences ? offsets[at] : past;
+        const int count = __popc(__ballot_sync(0xffffffffu, mine < past));
+        const int32_t near = int32_t(mine < past ? mine - base : 32 * N), me = int32_t(first - base);
+#pragma unroll
+        for (int j = 0; j < N; ++j) seq[j] = int32_t(lo) - 1;
+        if (count < 32) {
+            for (int k = 0; k < count; ++k) {
+                const int32_t b = __shfl_sync(0xffffffffu, near, k);
+#pragma unroll
+                for (int j = 0; j < N; ++j) seq[j] += b <= me + j;
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (seq[j] >= int32_t(sequences)) seq[j] = -1;
+        } else {  // more sequences here than lanes
+#pragma unroll
+            for (int j = 0; j < N; ++j) seq[j] = first + j < n ? sequence(first + j) : -1;
+        }
+    }
+
+    // Which of the N <= 4 tokens from `first` on count, as bits.
+    template <int N>
+    __device__ __forceinline__ uint32_t counting(uint32_t first) const {
+        const uint32_t left = first < n ? n - first : 0;
+        uint32_t bits = left >= N ? (1u << N) - 1 : (1u << left) - 1;
+        if (mask) {
+            if (N == 4 && left >= 4 && (reinterpret_cast<uintptr_t>(mask) + first) % 4 == 0) {
+                // bytes to 0 / 1, then their bits next to one another
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(mask + first);
+                bits = ((__vcmpne4(w, 0) & 0x01010101u) * 0x01020408u) >> 24;
+            } else {
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (j < int(left) && mask[first + j] == 0) bits &= ~(1u << j);
+            }
+        } else if (targets) {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (j < int(left) && targets[first + j] == ignore) bits &= ~(1u << j);
+        }
+        return bits;
     }
 };
 
@@ -372,12 +442,19 @@ struct Counts {
     uint32_t sequence[1];
 };
 
+// 1 / x for 1 <= x < 2^126, within an ulp.
+__device__ __forceinline__ float reciprocal(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // The weight of a token of a sequence with `in_sequence` tokens that count.
 __device__ __forceinline__ float token_weight(int32_t reduce, float inv_divisor, uint32_t tokens,
                                               uint32_t filled, uint32_t in_sequence) {
     if (reduce == ADAMW_REDUCE_FIXED) return inv_divisor;
-    if (reduce == ADAMW_REDUCE_TOKEN) return 1.0f / float(tokens);
-    return 1.0f / (float(in_sequence) * float(filled));
+    if (reduce == ADAMW_REDUCE_TOKEN) return reciprocal(float(tokens));
+    return reciprocal(float(in_sequence) * float(filled));
 }
 
 // ------------------------------------------------------------ policy loss --
@@ -393,6 +470,22 @@ struct PolicyToken {
     float pg, kl, off, old_kl, grad;
 };
 
+// exp(x) - 1 - x, from x and e = exp(x).  Below 0.7 by its series, whose terms
+// after x^9 are below 1e-8 of the first; above, the subtraction loses no more
+// than three bits.
+__device__ __forceinline__ float exp_beyond_linear(float x, float e) {
+    float s = 1.0f / 362880.0f;
+    s = fmaf(s, x, 1.0f / 40320.0f);
+    s = fmaf(s, x, 1.0f / 5040.0f);
+    s = fmaf(s, x, 1.0f / 720.0f);
+    s = fmaf(s, x, 1.0f / 120.0f);
+    s = fmaf(s, x, 1.0f / 24.0f);
+    s = fmaf(s, x, 1.0f / 6.0f);
+    s = fmaf(s, x, 0.5f);
+    const float far = (e - 1.0f) - x;
+    return fabsf(x) < 0.7f ? s * x * x : far;
+}
+
 // The loss terms of one token and the derivative of pg + kl_coef KL with
 // respect to its log-probability (weights left out).
 __device__ __forceinline__ PolicyToken policy_token(const Policy& P, float logp, float old, bool has_ref,
@@ -407,7 +500,7 @@ __device__ __forceinline__ PolicyToken policy_token(const Policy& P, float logp,
     const float u = -A * r, v = -A * rc;
     o.pg = capped ? -A * P.dual : (u < v ? v : u);
     o.off = off ? 1.0f : 0.0f;
-    o.old_kl = expm1f(d) - d;
+    o.old_kl = exp_beyond_linear(d, r);
     o.grad = off ? 0.0f : u;
     o.kl = 0.0f;
     if (has_ref) {
@@ -420,9 +513,8 @@ __device__ __forceinline__ PolicyToken policy_token(const Policy& P, float logp,
             o.kl = 0.5f * k * k;
             dk = k;
         } else {
-            const float e = expm1f(-k);
-            o.kl = e + k;
-            dk = -e;
+            o.kl = exp_beyond_linear(-k, expf(-k));
+            dk = k - o.kl;   // 1 - exp(-k)
         }
         // without a coefficient the estimate is reported only, and a
         // reference that is -inf somewhere does not reach the gradient

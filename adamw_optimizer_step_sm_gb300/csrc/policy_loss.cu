@@ -10,39 +10,78 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxGrid = 608;  // 4 CTAs on each of 152 SMs
+constexpr int kPerLane = 4;    // consecutive tokens of a lane
+constexpr int kChunk = 32 * kPerLane;  // and of a warp
+constexpr int kMaxGrid = 1216; // 8 CTAs for each of 152 SMs
+constexpr int kCountGrid = 608;
 constexpr int kSums = 5;       // pg, KL, entropy, clipped, old KL
 
-uint32_t token_grid(int64_t n) {
-    const int64_t g = (n + kThreads - 1) / kThreads;
-    return uint32_t(g < 1 ? 1 : g > kMaxGrid ? kMaxGrid : g);
+uint32_t token_grid(int64_t n, int64_t most) {
+    const int64_t g = (n + kWarps * kChunk - 1) / (kWarps * kChunk);
+    return uint32_t(g < 1 ? 1 : g > most ? most : g);
 }
 
 int64_t counts_bytes(int64_t sequences) { return (16 + 4 * sequences + 15) / 16 * 16; }
 
-// Counts tokens by sequence, warp by warp (integers: any order gives the same).
+// Counts tokens by sequence (integers: any order gives the same).  A warp
+// takes 128 consecutive tokens, four to a lane.
 __global__ void __launch_bounds__(kThreads) count_kernel(Tokens t, Counts* out) {
     dependency_trigger();
     dependency_wait();
     const uint32_t lane = threadIdx.x % 32;
     uint32_t tokens = 0, filled = 0;
-    const uint64_t step = uint64_t(gridDim.x) * kThreads;
-    // whole warps take part in every round
-    for (uint64_t base = uint64_t(blockIdx.x) * kThreads + threadIdx.x - lane; base < t.n; base += step) {
-        const uint32_t i = uint32_t(base) + lane;
-        int32_t seq = -1;
-        if (base + lane < t.n && t.counts(i)) seq = t.sequence(i);
-        const uint32_t peers = __match_any_sync(0xffffffffu, seq);
-        if (seq >= 0 && (peers & ((1u << lane) - 1)) == 0) {
-            const uint32_t k = __popc(peers);
-            tokens += k;
-            filled += atomicAdd(&out->sequence[seq], k) == 0;
+    const uint64_t step = uint64_t(gridDim.x) * kWarps * kChunk;
+    for (uint64_t at = (uint64_t(blockIdx.x) * kWarps + threadIdx.x / 32) * kChunk; at < t.n; at += step) {
+        const uint32_t base = uint32_t(at), first = base + lane * kPerLane;
+        uint32_t bits = t.counting<kPerLane>(first);
+        int32_t seq[kPerLane];
+        t.sequences_of<kPerLane>(base, first, seq);
+        // run by run of the lane's tokens; one atomic where the whole warp is
+        // in one sequence
+        const int32_t s0 = __shfl_sync(0xffffffffu, seq[0], 0);
+        const bool one = seq[0] == s0 && seq[kPerLane - 1] == s0;
+        if (__all_sync(0xffffffffu, one || bits == 0)) {
+            const uint32_t k = __reduce_add_sync(0xffffffffu, uint32_t(__popc(bits)));
+            if (lane == 0 && k && s0 >= 0) {
+                tokens += k;
+                filled += atomicAdd(&out->sequence[s0], k) == 0;
+            }
+            continue;
+        }
+        while (bits) {
+            const int j = __ffs(bits) - 1;
+            int32_t s = -1;
+            uint32_t k = 0;
+#pragma unroll
+            for (int i = 0; i < kPerLane; ++i)
+                if (i == j) s = seq[i];
+#pragma unroll
+            for (int i = 0; i < kPerLane; ++i)
+                if ((bits >> i & 1) && seq[i] == s) {
+                    ++k;
+                    bits &= ~(1u << i);
+                }
+            if (s >= 0) {
+                tokens += k;
+                filled += atomicAdd(&out->sequence[s], k) == 0;
+            }
         }
     }
+    // one atomic per CTA: thousands on one address would wait for one another
+    __shared__ uint32_t part[2];
+    if (threadIdx.x < 2) part[threadIdx.x] = 0;
+    __syncthreads();
     tokens = __reduce_add_sync(0xffffffffu, tokens);
     filled = __reduce_add_sync(0xffffffffu, filled);
-    if (lane == 0 && tokens) atomicAdd(&out->tokens, tokens);
-    if (lane == 0 && filled) atomicAdd(&out->filled, filled);
+    if (lane == 0) {
+        atomicAdd(&part[0], tokens);
+        atomicAdd(&part[1], filled);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && part[0]) {
+        atomicAdd(&out->tokens, part[0]);
+        atomicAdd(&out->filled, part[1]);
+    }
 }
 
 struct PolicyTokens {
@@ -51,44 +90,87 @@ struct PolicyTokens {
     int64_t* counts;
 };
 
-// Loss terms and gradients, token by token; each CTA leaves its five sums and
-// the last one to finish adds them up in the CTAs' order.
+// Four tokens of an array from `first` on, those past n as 0.
+__device__ __forceinline__ void load4(const float* p, uint32_t first, uint32_t n, bool vector, float (&x)[kPerLane]) {
+    if (vector) {
+        const float4 v = *reinterpret_cast<const float4*>(p + first);
+        x[0] = v.x;
+        x[1] = v.y;
+        x[2] = v.z;
+        x[3] = v.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < kPerLane; ++j) x[j] = first + j < n ? p[first + j] : 0.0f;
+    }
+}
+__device__ __forceinline__ void store4(float* p, uint32_t first, uint32_t n, bool vector, const float (&x)[kPerLane]) {
+    if (vector) {
+        *reinterpret_cast<float4*>(p + first) = make_float4(x[0], x[1], x[2], x[3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kPerLane; ++j)
+            if (first + j < n) p[first + j] = x[j];
+    }
+}
+
+// Loss terms and gradients, 128 tokens to a warp: a lane's loads are all on
+// their way before it looks for its tokens' sequences.  Each CTA leaves its
+// five sums and the last one to finish adds them up in the CTAs' order.
+// aligned: every array is 16-byte aligned.
 __global__ void __launch_bounds__(kThreads)
-policy_kernel(Tokens t, Policy P, PolicyTokens a, Counts* counts, float2* partial) {
+policy_kernel(Tokens t, Policy P, PolicyTokens a, Counts* counts, float2* partial, bool aligned) {
     dependency_trigger();
     dependency_wait();
+    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const uint32_t tokens = counts->tokens, filled = counts->filled;
     Sum2 sum[kSums] = {};
-    const uint64_t step = uint64_t(gridDim.x) * kThreads;
-    for (uint64_t at = uint64_t(blockIdx.x) * kThreads + threadIdx.x; at < t.n; at += step) {
-        const uint32_t i = uint32_t(at);
-        float g = 0.0f, gh = 0.0f;
-        if (t.counts(i)) {
-            const int32_t seq = t.sequence(i);
-            if (seq >= 0) {
-                const float w = token_weight(P.reduce, P.inv_divisor, tokens, filled, counts->sequence[seq]);
-                const float A = a.advantages[P.per_token ? i : uint32_t(seq)];
-                const PolicyToken k = policy_token(P, a.logp[i], a.old_logp[i], a.ref_logp != nullptr,
-                                                   a.ref_logp ? a.ref_logp[i] : 0.0f, A);
-                sum[0].add(w * k.pg);
-                sum[1].add(w * k.kl);
-                if (a.entropy) sum[2].add(w * a.entropy[i]);
-                sum[3].add(w * k.off);
-                sum[4].add(w * k.old_kl);
-                g = w * P.grad_scale * k.grad;
-                gh = -w * P.grad_scale * P.entropy_coef;
-            }
+    const uint64_t step = uint64_t(gridDim.x) * kWarps * kChunk;
+    for (uint64_t at = (uint64_t(blockIdx.x) * kWarps + warp) * kChunk; at < t.n; at += step) {
+        const uint32_t base = uint32_t(at), first = base + lane * kPerLane;
+        const bool vector = aligned && uint64_t(first) + kPerLane <= t.n;
+        float logp[kPerLane], old[kPerLane], ref[kPerLane] = {}, ent[kPerLane] = {}, adv[kPerLane] = {};
+        load4(a.logp, first, t.n, vector, logp);
+        load4(a.old_logp, first, t.n, vector, old);
+        if (a.ref_logp) load4(a.ref_logp, first, t.n, vector, ref);
+        if (a.entropy) load4(a.entropy, first, t.n, vector, ent);
+        if (P.per_token) load4(a.advantages, first, t.n, vector, adv);
+        const uint32_t bits = t.counting<kPerLane>(first);
+        int32_t seq[kPerLane];
+        t.sequences_of<kPerLane>(base, first, seq);
+        float g[kPerLane], gh[kPerLane], v[kSums] = {};
+        // every token alike, whether it counts or not: its results are then
+        // taken or left, never multiplied (they may be anything)
+#pragma unroll
+        for (int j = 0; j < kPerLane; ++j) {
+            const bool on = (bits >> j & 1) && seq[j] >= 0;
+            const uint32_t q = on ? uint32_t(seq[j]) : 0u;
+            const uint32_t in_sequence = P.reduce == ADAMW_REDUCE_SEQUENCE && on ? counts->sequence[q] : 1u;
+            const float w = on ? token_weight(P.reduce, P.inv_divisor, tokens, filled, in_sequence) : 0.0f;
+            const float A = P.per_token ? adv[j] : on ? a.advantages[q] : 0.0f;
+            const PolicyToken k = policy_token(P, logp[j], old[j], a.ref_logp != nullptr, ref[j], A);
+            v[0] = fmaf(w, on ? k.pg : 0.0f, v[0]);
+            v[1] = fmaf(w, on ? k.kl : 0.0f, v[1]);
+            v[2] = fmaf(w, on ? ent[j] : 0.0f, v[2]);
+            v[3] = fmaf(w, k.off, v[3]);
+            v[4] = fmaf(w, on ? k.old_kl : 0.0f, v[4]);
+            g[j] = on ? w * P.grad_scale * k.grad : 0.0f;
+            gh[j] = on ? -w * P.grad_scale * P.entropy_coef : 0.0f;
         }
-        if (a.d_logp) a.d_logp[i] = g;
-        if (a.d_entropy) a.d_entropy[i] = gh;
+#pragma unroll
+        for (int k = 0; k < kSums; ++k) sum[k].add(v[k]);
+        if (a.d_logp) store4(a.d_logp, first, t.n, vector, g);
+        if (a.d_entropy) store4(a.d_entropy, first, t.n, vector, gh);
     }
+    // the lanes' sums as a tree in fp32 (five roundings), the warps' and the
+    // CTAs' error-free
     __shared__ float2 part[kSums][kWarps];
     __shared__ bool last;
-    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
 #pragma unroll
     for (int k = 0; k < kSums; ++k) {
-        const Sum2 s = warp_sum(sum[k]);
-        if (lane == 0) part[k][warp] = make_float2(s.hi, s.lo);
+        float s = sum[k].value();
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+        if (lane == 0) part[k][warp] = make_float2(s, 0.0f);
     }
     __syncthreads();
     if (threadIdx.x < kSums) {
@@ -103,14 +185,23 @@ policy_kernel(Tokens t, Policy P, PolicyTokens a, Counts* counts, float2* partia
     if (!last) return;
     __threadfence();
     __shared__ float mean[kSums];
-    if (warp < kSums) {
-        Sum2 s = {};
-        for (uint32_t b = lane; b < gridDim.x; b += 32) {
-            const float2 p = __ldcg(&partial[b * kSums + warp]);
-            s.join(p.x, p.y);
+    Sum2 all[kSums] = {};
+    for (uint32_t b = threadIdx.x; b < gridDim.x; b += kThreads)
+#pragma unroll
+        for (int k = 0; k < kSums; ++k) {
+            const float2 p = __ldcg(&partial[b * kSums + k]);
+            all[k].join(p.x, p.y);
         }
-        s = warp_sum(s);
-        if (lane == 0) mean[warp] = s.value();
+#pragma unroll
+    for (int k = 0; k < kSums; ++k) {
+        const Sum2 s = warp_sum(all[k]);
+        if (lane == 0) part[k][warp] = make_float2(s.hi, s.lo);
+    }
+    __syncthreads();
+    if (threadIdx.x < kSums) {
+        Sum2 s = {};
+        for (int w = 0; w < kWarps; ++w) s.join(part[threadIdx.x][w].x, part[threadIdx.x][w].y);
+        mean[threadIdx.x] = s.value();
     }
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -313,7 +404,7 @@ int launch_counts(const adamw_tokens_t* t, const int64_t* targets, int64_t ignor
     if (!launched(cudaMemsetAsync(c, 0, size_t(counts_bytes(t->sequences)), st), "counts memset"))
         return ADAMW_ERR_CUDA;
     if (t->n == 0) return ADAMW_OK;
-    return launched(launch(count_kernel, token_grid(t->n), kThreads, 1, 0, st,
+    return launched(launch(count_kernel, token_grid(t->n, kCountGrid), kThreads, 1, 0, st,
                            tokens_of(t, targets, ignore), c), "count launch")
                ? ADAMW_OK : ADAMW_ERR_CUDA;
 }
@@ -325,8 +416,13 @@ int launch_policy(const adamw_tokens_t* t, const adamw_policy_t* p, const int64_
     const Policy P = policy_of(p);
     const PolicyTokens a = {logp, old_logp, ref_logp, advantages, entropy, d_logp, d_entropy, stats, counts};
     float2* partial = reinterpret_cast<float2*>(static_cast<char*>(workspace) + counts_bytes(t->sequences));
-    return launched(launch(policy_kernel, token_grid(t->n), kThreads, 1, 0, st,
-                           tokens_of(t, targets, ignore), P, a, static_cast<Counts*>(workspace), partial),
+    bool all_aligned = true;
+    const void* arrays[] = {logp, old_logp, ref_logp, p->advantage_per_token ? advantages : nullptr, entropy,
+                            d_logp, d_entropy};
+    for (const void* x : arrays) all_aligned = all_aligned && aligned(x, 16);
+    return launched(launch(policy_kernel, token_grid(t->n, kMaxGrid), kThreads, 1, 0, st,
+                           tokens_of(t, targets, ignore), P, a, static_cast<Counts*>(workspace), partial,
+                           all_aligned),
                     "policy launch")
                ? ADAMW_OK : ADAMW_ERR_CUDA;
 }
