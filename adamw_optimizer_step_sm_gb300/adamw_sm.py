@@ -135,6 +135,8 @@ _lib: ctypes.CDLL | None = None
 def load() -> ctypes.CDLL:
     """Build if needed and load the shared library (raises on failure)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = os.environ.get("ADAMW_SM_LIBRARY") or _build.build()
@@ -172,15 +174,13 @@ def load() -> ctypes.CDLL:
             L.adamw_policy_loss.argtypes = [tokens, policy, *([vp] * 11)]
             L.adamw_policy_loss_logits.argtypes = [rows, vp, i64, f32, tokens, policy,
                                                    *([vp] * 7), rows, vp, vp]
-            L.adamw_preference_loss.argtypes = [tokens, P(adamw_preference_t), *([vp] * 8)]
+            L.adamw_preference_loss.argtypes = [tokens, P(adamw_preference_t), *([vp] * 7)]
             L.adamw_clip_plan_create.argtypes = [P(adamw_grad_t), i32, P(vp)]
             L.adamw_clip_grads.argtypes = [vp, f32, i32, vp, vp]
             L.adamw_clip_plan_destroy.argtypes = [vp]
             for name in ("adamw_policy_workspace", "adamw_policy_logits_workspace"):
                 getattr(L, name).argtypes = [i64, i64]
                 getattr(L, name).restype = i64
-            L.adamw_preference_workspace.argtypes = [i64]
-            L.adamw_preference_workspace.restype = i64
             L.adamw_status_string.argtypes = [ctypes.c_int]
             L.adamw_status_string.restype = ctypes.c_char_p
             for name in ("adamw_plan_create", "adamw_step", "adamw_grad_norm", "adamw_step_device",
@@ -364,10 +364,6 @@ def adamw_policy_logits_workspace(n: int, sequences: int) -> int:
     return load().adamw_policy_logits_workspace(n, sequences)
 
 
-def adamw_preference_workspace(pairs: int) -> int:
-    return load().adamw_preference_workspace(pairs)
-
-
 def adamw_policy_loss(tokens: adamw_tokens_t, policy: adamw_policy_t, logp: int, old_logp: int,
                       ref_logp: int, advantages: int, entropy: int, stats: int, counts: int, d_logp: int,
                       d_entropy: int, workspace: int, stream: int = 0) -> None:
@@ -389,10 +385,9 @@ def adamw_policy_loss_logits(logits: adamw_rows_t, targets: int, ignore_index: i
 
 
 def adamw_preference_loss(tokens: adamw_tokens_t, pref: adamw_preference_t, logp: int, ref_logp: int,
-                          stats: int, losses: int, rewards: int, d_logp: int, workspace: int,
-                          stream: int = 0) -> None:
+                          stats: int, losses: int, rewards: int, d_logp: int, stream: int = 0) -> None:
     rc = load().adamw_preference_loss(ctypes.byref(tokens), ctypes.byref(pref), logp, ref_logp or None,
-                                      stats, losses, rewards, d_logp, workspace, stream or None)
+                                      stats, losses, rewards, d_logp, stream or None)
     _check(rc, "adamw_preference_loss")
 
 

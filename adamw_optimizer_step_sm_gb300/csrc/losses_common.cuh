@@ -603,9 +603,10 @@ int check_policy(const adamw_policy_t* p);
 // workspace's Counts, and zeroes its ticket.
 int launch_counts(const adamw_tokens_t* t, const int64_t* targets, int64_t ignore, void* workspace,
                   cudaStream_t st);
+// counted: launch_counts has run on this workspace, and nothing since.
 int launch_policy(const adamw_tokens_t* t, const adamw_policy_t* p, const int64_t* targets,
-                  int64_t ignore, const float* logp, const float* old_logp, const float* ref_logp,
-                  const float* advantages, const float* entropy, float* stats, int64_t* counts,
+                  int64_t ignore, bool counted, const float* logp, const float* old_logp,
+                  const float* ref_logp, const float* advantages, const float* entropy, float* stats, int64_t* counts,
                   float* d_logp, float* d_entropy, void* workspace, cudaStream_t st);
 
 }  // namespace adamw

@@ -21,17 +21,26 @@ uint32_t token_grid(int64_t n, int64_t most) {
     return uint32_t(g < 1 ? 1 : g > most ? most : g);
 }
 
+// Up to here one cluster does a whole call in one launch.
+constexpr int64_t kClusterTokens = 32768, kClusterSequences = 8192, kClusterPairs = 16;
+bool in_one_cluster(const adamw_tokens_t* t) {
+    return t->n <= kClusterTokens && t->sequences <= kClusterSequences;
+}
+uint32_t cluster_ctas(int64_t n) {
+    uint32_t c = 1;
+    while (c < 8 && n > int64_t(c) * kWarps * kChunk) c *= 2;
+    return c;
+}
+
 int64_t counts_bytes(int64_t sequences) { return (16 + 4 * sequences + 15) / 16 * 16; }
 
-// Counts tokens by sequence (integers: any order gives the same).  A warp
-// takes 128 consecutive tokens, four to a lane.
-__global__ void __launch_bounds__(kThreads) count_kernel(Tokens t, Counts* out) {
-    dependency_trigger();
-    dependency_wait();
+// Counts tokens by sequence (integers: any order gives the same), CTA `cta`
+// of `ctas`.  A warp takes 128 consecutive tokens, four to a lane.
+__device__ __forceinline__ void count_tokens(const Tokens& t, Counts* out, uint32_t cta, uint32_t ctas) {
     const uint32_t lane = threadIdx.x % 32;
     uint32_t tokens = 0, filled = 0;
-    const uint64_t step = uint64_t(gridDim.x) * kWarps * kChunk;
-    for (uint64_t at = (uint64_t(blockIdx.x) * kWarps + threadIdx.x / 32) * kChunk; at < t.n; at += step) {
+    const uint64_t step = uint64_t(ctas) * kWarps * kChunk;
+    for (uint64_t at = (uint64_t(cta) * kWarps + threadIdx.x / 32) * kChunk; at < t.n; at += step) {
         const uint32_t base = uint32_t(at), first = base + lane * kPerLane;
         uint32_t bits = t.counting<kPerLane>(first);
         int32_t seq[kPerLane];
@@ -84,6 +93,27 @@ __global__ void __launch_bounds__(kThreads) count_kernel(Tokens t, Counts* out) 
     }
 }
 
+__global__ void __launch_bounds__(kThreads) count_kernel(Tokens t, Counts* out) {
+    dependency_trigger();
+    dependency_wait();
+    count_tokens(t, out, blockIdx.x, gridDim.x);
+}
+
+// The same by one cluster, which zeroes the counts first.
+__device__ __forceinline__ void count_in_cluster(const Tokens& t, Counts* out, uint32_t rank, uint32_t size) {
+    uint32_t* words = reinterpret_cast<uint32_t*>(out);
+    const uint32_t n = 4 + t.sequences;
+    for (uint32_t i = rank * kThreads + threadIdx.x; i < n; i += size * kThreads) words[i] = 0;
+    cluster_sync();
+    count_tokens(t, out, rank, size);
+    cluster_sync();
+}
+__global__ void __launch_bounds__(kThreads) count_cluster_kernel(Tokens t, Counts* out) {
+    dependency_trigger();
+    dependency_wait();
+    count_in_cluster(t, out, cluster_rank(), cluster_size());
+}
+
 struct PolicyTokens {
     const float *logp, *old_logp, *ref_logp, *advantages, *entropy;
     float *d_logp, *d_entropy, *stats;
@@ -113,19 +143,17 @@ __device__ __forceinline__ void store4(float* p, uint32_t first, uint32_t n, boo
     }
 }
 
-// Loss terms and gradients, 128 tokens to a warp: a lane's loads are all on
-// their way before it looks for its tokens' sequences.  Each CTA leaves its
-// five sums and the last one to finish adds them up in the CTAs' order.
-// aligned: every array is 16-byte aligned.
-__global__ void __launch_bounds__(kThreads)
-policy_kernel(Tokens t, Policy P, PolicyTokens a, Counts* counts, float2* partial, bool aligned) {
-    dependency_trigger();
-    dependency_wait();
+// Loss terms and gradients of CTA `cta` of `ctas`, 128 tokens to a warp: a
+// lane's loads are all on their way before it looks for its tokens'
+// sequences.  Threads below kSums return the CTA's sums.  aligned: every
+// array is 16-byte aligned.
+__device__ __forceinline__ Sum2 policy_tokens(const Tokens& t, const Policy& P, const PolicyTokens& a,
+                                              const Counts* counts, uint32_t tokens, uint32_t filled,
+                                              bool aligned, uint32_t cta, uint32_t ctas) {
     const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const uint32_t tokens = counts->tokens, filled = counts->filled;
     Sum2 sum[kSums] = {};
-    const uint64_t step = uint64_t(gridDim.x) * kWarps * kChunk;
-    for (uint64_t at = (uint64_t(blockIdx.x) * kWarps + warp) * kChunk; at < t.n; at += step) {
+    const uint64_t step = uint64_t(ctas) * kWarps * kChunk;
+    for (uint64_t at = (uint64_t(cta) * kWarps + warp) * kChunk; at < t.n; at += step) {
         const uint32_t base = uint32_t(at), first = base + lane * kPerLane;
         const bool vector = aligned && uint64_t(first) + kPerLane <= t.n;
         float logp[kPerLane], old[kPerLane], ref[kPerLane] = {}, ent[kPerLane] = {}, adv[kPerLane] = {};
@@ -144,7 +172,7 @@ policy_kernel(Tokens t, Policy P, PolicyTokens a, Counts* counts, float2* partia
         for (int j = 0; j < kPerLane; ++j) {
             const bool on = (bits >> j & 1) && seq[j] >= 0;
             const uint32_t q = on ? uint32_t(seq[j]) : 0u;
-            const uint32_t in_sequence = P.reduce == ADAMW_REDUCE_SEQUENCE && on ? counts->sequence[q] : 1u;
+            const uint32_t in_sequence = P.reduce == ADAMW_REDUCE_SEQUENCE && on ? __ldcg(&counts->sequence[q]) : 1u;
             const float w = on ? token_weight(P.reduce, P.inv_divisor, tokens, filled, in_sequence) : 0.0f;
             const float A = P.per_token ? adv[j] : on ? a.advantages[q] : 0.0f;
             const PolicyToken k = policy_token(P, logp[j], old[j], a.ref_logp != nullptr, ref[j], A);
@@ -163,20 +191,44 @@ policy_kernel(Tokens t, Policy P, PolicyTokens a, Counts* counts, float2* partia
     }
     // the lanes' sums as a tree in fp32 (five roundings), the warps' and the
     // CTAs' error-free
-    __shared__ float2 part[kSums][kWarps];
-    __shared__ bool last;
+    __shared__ float part[kSums][kWarps];
 #pragma unroll
     for (int k = 0; k < kSums; ++k) {
         float s = sum[k].value();
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        if (lane == 0) part[k][warp] = make_float2(s, 0.0f);
+        if (lane == 0) part[k][warp] = s;
     }
     __syncthreads();
+    Sum2 s = {};
+    if (threadIdx.x < kSums)
+        for (int w = 0; w < kWarps; ++w) s.add(part[threadIdx.x][w]);
+    return s;
+}
+
+__device__ __forceinline__ void policy_result(const Policy& P, const PolicyTokens& a, const float* mean,
+                                              uint32_t tokens, uint32_t filled) {
+    float loss = mean[0];
+    if (P.kl_coef != 0.0f) loss = fmaf(P.kl_coef, mean[1], loss);
+    if (P.entropy_coef != 0.0f) loss = fmaf(-P.entropy_coef, mean[2], loss);
+    a.stats[0] = loss;
+    for (int k = 0; k < kSums; ++k) a.stats[k + 1] = mean[k];
+    a.counts[0] = tokens;
+    a.counts[1] = filled;
+}
+
+// Over a grid: each CTA leaves its five sums and the last one to finish adds
+// them up in the CTAs' order.
+__global__ void __launch_bounds__(kThreads)
+policy_kernel(Tokens t, Policy P, PolicyTokens a, Counts* counts, float2* partial, bool aligned) {
+    dependency_trigger();
+    dependency_wait();
+    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const uint32_t tokens = counts->tokens, filled = counts->filled;
+    const Sum2 mine = policy_tokens(t, P, a, counts, tokens, filled, aligned, blockIdx.x, gridDim.x);
+    __shared__ bool last;
     if (threadIdx.x < kSums) {
-        Sum2 s = {};
-        for (int w = 0; w < kWarps; ++w) s.join(part[threadIdx.x][w].x, part[threadIdx.x][w].y);
-        partial[blockIdx.x * kSums + threadIdx.x] = make_float2(s.hi, s.lo);
+        partial[blockIdx.x * kSums + threadIdx.x] = make_float2(mine.hi, mine.lo);
         __threadfence();
     }
     __syncthreads();
@@ -184,6 +236,7 @@ policy_kernel(Tokens t, Policy P, PolicyTokens a, Counts* counts, float2* partia
     __syncthreads();
     if (!last) return;
     __threadfence();
+    __shared__ float2 part[kSums][kWarps];
     __shared__ float mean[kSums];
     Sum2 all[kSums] = {};
     for (uint32_t b = threadIdx.x; b < gridDim.x; b += kThreads)
@@ -204,15 +257,34 @@ policy_kernel(Tokens t, Policy P, PolicyTokens a, Counts* counts, float2* partia
         mean[threadIdx.x] = s.value();
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        float loss = mean[0];
-        if (P.kl_coef != 0.0f) loss = fmaf(P.kl_coef, mean[1], loss);
-        if (P.entropy_coef != 0.0f) loss = fmaf(-P.entropy_coef, mean[2], loss);
-        a.stats[0] = loss;
-        for (int k = 0; k < kSums; ++k) a.stats[k + 1] = mean[k];
-        a.counts[0] = tokens;
-        a.counts[1] = filled;
+    if (threadIdx.x == 0) policy_result(P, a, mean, tokens, filled);
+}
+
+// Few tokens: one cluster counts (COUNT), computes and adds up in one launch.
+template <bool COUNT>
+__global__ void __launch_bounds__(kThreads)
+policy_cluster_kernel(Tokens t, Policy P, PolicyTokens a, Counts* counts, bool aligned) {
+    dependency_trigger();
+    dependency_wait();
+    const uint32_t rank = cluster_rank(), size = cluster_size();
+    if (COUNT) count_in_cluster(t, counts, rank, size);
+    const uint32_t tokens = __ldcg(&counts->tokens), filled = __ldcg(&counts->filled);
+    const Sum2 mine = policy_tokens(t, P, a, counts, tokens, filled, aligned, rank, size);
+    __shared__ float whole[kSums][2];
+    __shared__ float mean[kSums];
+    if (threadIdx.x < kSums) {
+        whole[threadIdx.x][0] = mine.hi;
+        whole[threadIdx.x][1] = mine.lo;
     }
+    cluster_sync();
+    if (rank == 0 && threadIdx.x < kSums) {
+        Sum2 s = mine;
+        for (uint32_t k = 1; k < size; ++k)
+            s.join(load_remote(&whole[threadIdx.x][0], k), load_remote(&whole[threadIdx.x][1], k));
+        mean[threadIdx.x] = s.value();
+    }
+    cluster_sync();   // no CTA ends while its sums are read
+    if (rank == 0 && threadIdx.x == 0) policy_result(P, a, mean, tokens, filled);
 }
 
 // ------------------------------------------------------------- preference --
@@ -229,51 +301,83 @@ __device__ __forceinline__ float sigmoid(float x) {
     return x >= 0.0f ? 1.0f / (1.0f + e) : e / (1.0f + e);
 }
 
-// One pair per cluster of CTAs: each CTA sums its share of the two
-// sequences' log ratios, the cluster joins them, and every CTA writes its
-// share of the gradient.
-__global__ void __launch_bounds__(kThreads)
-preference_kernel(Tokens t, Preference P, const float* logp, const float* ref, float* losses,
-                  float* rewards, float* d_logp, float* difference) {
-    dependency_trigger();
-    dependency_wait();
-    const uint32_t size = cluster_size(), rank = cluster_rank();
-    const uint32_t pair = blockIdx.x / size, pairs = t.sequences / 2;
-    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const uint32_t width = size * kThreads, me = rank * kThreads + threadIdx.x;
-    __shared__ float part[2][3][kWarps];
-    __shared__ float whole[2][3];
-    int64_t begin[2], end[2];
-    for (int side = 0; side < 2; ++side) {
-        const uint32_t seq = pair + (side ? pairs : 0);
-        int64_t b = t.offsets ? t.offsets[seq] : int64_t(seq) * t.length;
-        int64_t e = t.offsets ? t.offsets[seq + 1] : b + t.length;
-        // inside the tokens, whatever the offsets hold
-        b = b < 0 ? 0 : b > int64_t(t.n) ? int64_t(t.n) : b;
-        e = e < b ? b : e > int64_t(t.n) ? int64_t(t.n) : e;
-        begin[side] = b;
-        end[side] = e;
-        Sum2 sum = {};
-        uint32_t tokens = 0;
-        for (int64_t i = b + me; i < e; i += width) {
-            if (t.mask && t.mask[i] == 0) continue;
-            sum.add(logp[i]);
-            if (P.ref == ADAMW_REF_TOKEN) sum.add(-ref[i]);  // the difference unrounded
+constexpr int kMaxWarps = 32;
+
+// The sum of logp (less the reference's) over the tokens [b, e) that count, a
+// thread's share: every width-th from `me` on, four on their way at a time.
+__device__ __forceinline__ void sum_side(const Tokens& t, bool has_ref, const float* logp, const float* ref,
+                                         int64_t b, int64_t e, uint32_t me, uint32_t width, Sum2& sum,
+                                         uint32_t& tokens) {
+    for (int64_t i = b + me; i < e; i += 4 * int64_t(width)) {
+        float x[4], r[4];
+        bool on[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t at = i + u * int64_t(width);
+            const bool in = at < e;
+            on[u] = in && (!t.mask || t.mask[at] != 0);
+            x[u] = in ? logp[at] : 0.0f;
+            r[u] = in && has_ref ? ref[at] : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (!on[u]) continue;
+            sum.add(x[u]);
+            if (has_ref) sum.add(-r[u]);  // the difference unrounded
             ++tokens;
         }
-        sum = warp_sum(sum);
-        tokens = __reduce_add_sync(0xffffffffu, tokens);
+    }
+}
+
+// h without the margin, from the rewards, which also order the pair.
+struct PairResult {
+    float loss, h;
+};
+
+// One pair by a group of CTAs (SHARED: a cluster; else one): each sums its
+// share of the two sequences' log ratios, the group joins them, and every CTA
+// writes its share of the gradient.
+template <bool SHARED>
+__device__ __forceinline__ PairResult preference_pair(const Tokens& t, const Preference& P, const float* logp,
+                                                      const float* ref, float* losses, float* rewards,
+                                                      float* d_logp, uint32_t pair, uint32_t rank,
+                                                      uint32_t size) {
+    const uint32_t pairs = t.sequences / 2;
+    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+    const uint32_t width = size * blockDim.x, me = rank * blockDim.x + threadIdx.x;
+    __shared__ float part[2][3][kMaxWarps];
+    __shared__ float whole[2][3];
+    int64_t begin[2], end[2];
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+        const uint32_t seq = pair + (side ? pairs : 0);
+        const int64_t b = t.offsets ? t.offsets[seq] : int64_t(seq) * t.length;
+        const int64_t e = t.offsets ? t.offsets[seq + 1] : b + t.length;
+        // inside the tokens, whatever the offsets hold
+        begin[side] = b < 0 ? 0 : b > int64_t(t.n) ? int64_t(t.n) : b;
+        end[side] = e < begin[side] ? begin[side] : e > int64_t(t.n) ? int64_t(t.n) : e;
+    }
+    Sum2 sum[2] = {};
+    uint32_t tokens[2] = {};
+#pragma unroll
+    for (int side = 0; side < 2; ++side)
+        sum_side(t, P.ref == ADAMW_REF_TOKEN, logp, ref, begin[side], end[side], me, width, sum[side],
+                 tokens[side]);
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+        const Sum2 s = warp_sum(sum[side]);
+        const uint32_t k = __reduce_add_sync(0xffffffffu, tokens[side]);
         if (lane == 0) {
-            part[side][0][warp] = sum.hi;
-            part[side][1][warp] = sum.lo;
-            part[side][2][warp] = __uint_as_float(tokens);
+            part[side][0][warp] = s.hi;
+            part[side][1][warp] = s.lo;
+            part[side][2][warp] = __uint_as_float(k);
         }
     }
     __syncthreads();
     if (threadIdx.x < 2) {
         Sum2 s = {};
         uint32_t k = 0;
-        for (int w = 0; w < kWarps; ++w) {
+        for (uint32_t w = 0; w < warps; ++w) {
             s.join(part[threadIdx.x][0][w], part[threadIdx.x][1][w]);
             k += __float_as_uint(part[threadIdx.x][2][w]);
         }
@@ -281,24 +385,27 @@ preference_kernel(Tokens t, Preference P, const float* logp, const float* ref, f
         whole[threadIdx.x][1] = s.lo;
         whole[threadIdx.x][2] = __uint_as_float(k);
     }
-    if (size > 1) cluster_sync(); else __syncthreads();
+    if (SHARED) cluster_sync(); else __syncthreads();
     float S[2], share[2];
+#pragma unroll
     for (int side = 0; side < 2; ++side) {
         Sum2 s = {};
         uint32_t k = 0;
-        if (size == 1) {
+        if (SHARED) {
+            for (uint32_t c = 0; c < size; ++c) {
+                s.join(load_remote(&whole[side][0], c), load_remote(&whole[side][1], c));
+                k += __float_as_uint(load_remote(&whole[side][2], c));
+            }
+        } else {
             s = {whole[side][0], whole[side][1]};
             k = __float_as_uint(whole[side][2]);
-        }
-        for (uint32_t c = 0; size > 1 && c < size; ++c) {
-            s.join(load_remote(&whole[side][0], c), load_remote(&whole[side][1], c));
-            k += __float_as_uint(load_remote(&whole[side][2], c));
         }
         if (P.ref == ADAMW_REF_SEQUENCE) s.add(-ref[pair + (side ? pairs : 0)]);
         share[side] = P.average ? 1.0f / float(k > 0 ? k : 1) : 1.0f;
         S[side] = P.average ? s.value() / float(k > 0 ? k : 1) : s.value();
     }
-    if (size > 1) cluster_sync();  // the records stay until all have read them
+    // the records stay until all have read them
+    if (SHARED) cluster_sync(); else __syncthreads();
     const float D = S[0] - S[1];
     const float h = P.beta * D - P.margin;
     float loss, dD;
@@ -318,11 +425,12 @@ preference_kernel(Tokens t, Preference P, const float* logp, const float* ref, f
         losses[pair] = loss;
         rewards[pair] = P.beta * S[0];
         rewards[pairs + pair] = P.beta * S[1];
-        difference[pair] = D;
     }
     const float g = P.grad_scale * dD / float(pairs);
+#pragma unroll
     for (int side = 0; side < 2; ++side) {
         const float v = (side ? -g : g) * share[side];
+#pragma unroll 4
         for (int64_t i = begin[side] + me; i < end[side]; i += width)
             d_logp[i] = !t.mask || t.mask[i] != 0 ? v : 0.0f;
     }
@@ -333,21 +441,33 @@ preference_kernel(Tokens t, Preference P, const float* logp, const float* ref, f
     if (t.offsets && pair == pairs - 1) {
         for (int64_t i = end[1] + me; i < int64_t(t.n); i += width) d_logp[i] = 0.0f;
     }
+    return {loss, P.beta * S[0] - P.beta * S[1]};
+}
+
+// A cluster (or CTA) per pair.
+template <bool SHARED>
+__global__ void __launch_bounds__(1024)
+preference_kernel(Tokens t, Preference P, const float* logp, const float* ref, float* losses,
+                  float* rewards, float* d_logp) {
+    dependency_trigger();
+    dependency_wait();
+    const uint32_t size = SHARED ? cluster_size() : 1, rank = SHARED ? cluster_rank() : 0;
+    preference_pair<SHARED>(t, P, logp, ref, losses, rewards, d_logp, blockIdx.x / size, rank, size);
 }
 
 // The statistics over the pairs.
 __global__ void __launch_bounds__(kThreads)
-preference_stats_kernel(uint32_t pairs, Preference P, const float* losses, const float* difference,
+preference_stats_kernel(uint32_t pairs, Preference P, const float* losses, const float* rewards,
                         float* stats) {
     dependency_trigger();
     dependency_wait();
     Sum2 loss = {}, h = {};
     uint32_t right = 0;
     for (uint32_t i = threadIdx.x; i < pairs; i += kThreads) {
-        const float D = difference[i];
+        const float d = rewards[i] - rewards[pairs + i];
         loss.add(losses[i]);
-        h.add(P.beta * D - P.margin);
-        right += D > 0.0f;
+        h.add(d - P.margin);
+        right += d > 0.0f;
     }
     __shared__ float2 part[2][kWarps];
     __shared__ uint32_t rights[kWarps];
@@ -370,6 +490,44 @@ preference_stats_kernel(uint32_t pairs, Preference P, const float* losses, const
         for (int w = 0; w < kWarps; ++w) k += rights[w];
         stats[1] = float(k) / float(pairs);
     }
+}
+
+// Few pairs: one cluster takes them, a CTA each (in turns), and their
+// statistics, in one launch.
+__global__ void __launch_bounds__(1024)
+preference_cluster_kernel(Tokens t, Preference P, const float* logp, const float* ref, float* losses,
+                          float* rewards, float* d_logp, float* stats) {
+    dependency_trigger();
+    dependency_wait();
+    const uint32_t size = cluster_size(), rank = cluster_rank(), pairs = t.sequences / 2;
+    Sum2 loss = {}, h = {};
+    uint32_t right = 0;
+    for (uint32_t pair = rank; pair < pairs; pair += size) {
+        const PairResult r = preference_pair<false>(t, P, logp, ref, losses, rewards, d_logp, pair, 0, 1);
+        loss.add(r.loss);
+        h.add(r.h - P.margin);
+        right += r.h > 0.0f;
+    }
+    __shared__ float mine[5];
+    if (threadIdx.x == 0) {
+        mine[0] = loss.hi;
+        mine[1] = loss.lo;
+        mine[2] = h.hi;
+        mine[3] = h.lo;
+        mine[4] = float(right);
+    }
+    cluster_sync();
+    if (rank == 0 && threadIdx.x == 0) {
+        for (uint32_t k = 1; k < size; ++k) {
+            loss.join(load_remote(&mine[0], k), load_remote(&mine[1], k));
+            h.join(load_remote(&mine[2], k), load_remote(&mine[3], k));
+            right += uint32_t(load_remote(&mine[4], k));
+        }
+        stats[0] = loss.value() / float(pairs);
+        stats[1] = float(right) / float(pairs);
+        stats[2] = h.value() / float(pairs);
+    }
+    cluster_sync();   // no CTA ends while its record is read
 }
 
 }  // namespace
@@ -401,29 +559,42 @@ int check_policy(const adamw_policy_t* p) {
 int launch_counts(const adamw_tokens_t* t, const int64_t* targets, int64_t ignore, void* workspace,
                   cudaStream_t st) {
     Counts* c = static_cast<Counts*>(workspace);
+    const Tokens k = tokens_of(t, targets, ignore);
+    if (in_one_cluster(t))
+        return launched(launch(count_cluster_kernel, cluster_ctas(t->n), kThreads, int(cluster_ctas(t->n)), 0, st,
+                               k, c), "count launch")
+                   ? ADAMW_OK : ADAMW_ERR_CUDA;
     if (!launched(cudaMemsetAsync(c, 0, size_t(counts_bytes(t->sequences)), st), "counts memset"))
         return ADAMW_ERR_CUDA;
-    if (t->n == 0) return ADAMW_OK;
-    return launched(launch(count_kernel, token_grid(t->n, kCountGrid), kThreads, 1, 0, st,
-                           tokens_of(t, targets, ignore), c), "count launch")
+    return launched(launch(count_kernel, token_grid(t->n, kCountGrid), kThreads, 1, 0, st, k, c), "count launch")
                ? ADAMW_OK : ADAMW_ERR_CUDA;
 }
 
 int launch_policy(const adamw_tokens_t* t, const adamw_policy_t* p, const int64_t* targets,
-                  int64_t ignore, const float* logp, const float* old_logp, const float* ref_logp,
-                  const float* advantages, const float* entropy, float* stats, int64_t* counts,
-                  float* d_logp, float* d_entropy, void* workspace, cudaStream_t st) {
+                  int64_t ignore, bool counted, const float* logp, const float* old_logp,
+                  const float* ref_logp, const float* advantages, const float* entropy, float* stats,
+                  int64_t* counts, float* d_logp, float* d_entropy, void* workspace, cudaStream_t st) {
     const Policy P = policy_of(p);
     const PolicyTokens a = {logp, old_logp, ref_logp, advantages, entropy, d_logp, d_entropy, stats, counts};
-    float2* partial = reinterpret_cast<float2*>(static_cast<char*>(workspace) + counts_bytes(t->sequences));
+    const Tokens k = tokens_of(t, targets, ignore);
+    Counts* c = static_cast<Counts*>(workspace);
     bool all_aligned = true;
     const void* arrays[] = {logp, old_logp, ref_logp, p->advantage_per_token ? advantages : nullptr, entropy,
                             d_logp, d_entropy};
     for (const void* x : arrays) all_aligned = all_aligned && aligned(x, 16);
-    return launched(launch(policy_kernel, token_grid(t->n, kMaxGrid), kThreads, 1, 0, st,
-                           tokens_of(t, targets, ignore), P, a, static_cast<Counts*>(workspace), partial,
-                           all_aligned),
-                    "policy launch")
+    if (in_one_cluster(t)) {
+        auto kernel = counted ? policy_cluster_kernel<false> : policy_cluster_kernel<true>;
+        return launched(launch(kernel, cluster_ctas(t->n), kThreads, int(cluster_ctas(t->n)), 0, st, k, P, a, c,
+                               all_aligned), "policy launch")
+                   ? ADAMW_OK : ADAMW_ERR_CUDA;
+    }
+    if (!counted) {
+        const int rc = launch_counts(t, targets, ignore, workspace, st);
+        if (rc != ADAMW_OK) return rc;
+    }
+    float2* partial = reinterpret_cast<float2*>(static_cast<char*>(workspace) + counts_bytes(t->sequences));
+    return launched(launch(policy_kernel, token_grid(t->n, kMaxGrid), kThreads, 1, 0, st, k, P, a, c, partial,
+                           all_aligned), "policy launch")
                ? ADAMW_OK : ADAMW_ERR_CUDA;
 }
 
@@ -452,20 +623,13 @@ extern "C" int adamw_policy_loss(const adamw_tokens_t* tokens, const adamw_polic
         if (!aligned(p, 4)) return ADAMW_ERR_MISALIGNED;
     if (!aligned(counts, 8) || !aligned(workspace, 16)) return ADAMW_ERR_MISALIGNED;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    rc = adamw::launch_counts(tokens, nullptr, 0, workspace, st);
-    if (rc != ADAMW_OK) return rc;
-    return adamw::launch_policy(tokens, policy, nullptr, 0, logp, old_logp, ref_logp, advantages, entropy,
+    return adamw::launch_policy(tokens, policy, nullptr, 0, false, logp, old_logp, ref_logp, advantages, entropy,
                                 stats, counts, d_logp, d_entropy, workspace, st);
-}
-
-extern "C" int64_t adamw_preference_workspace(int64_t pairs) {
-    return pairs < 1 || pairs > kMaxCount / 2 ? 0 : (4 * pairs + 15) / 16 * 16;
 }
 
 extern "C" int adamw_preference_loss(const adamw_tokens_t* tokens, const adamw_preference_t* pref,
                                      const float* logp, const float* ref_logp, float* stats,
-                                     float* losses, float* rewards, float* d_logp, void* workspace,
-                                     adamw_stream_t stream) {
+                                     float* losses, float* rewards, float* d_logp, adamw_stream_t stream) {
     const int rc = adamw::check_tokens(tokens);
     if (rc != ADAMW_OK) return rc;
     if (!pref || tokens->sequences < 2 || tokens->sequences % 2 != 0) return ADAMW_ERR_INVALID_ARG;
@@ -477,28 +641,37 @@ extern "C" int adamw_preference_loss(const adamw_tokens_t* tokens, const adamw_p
         (pref->kind == ADAMW_PREF_IPO && pref->margin != 0.0f) || pref->ref < ADAMW_REF_NONE ||
         pref->ref > ADAMW_REF_SEQUENCE)
         return ADAMW_ERR_INVALID_ARG;
-    if (!stats || !losses || !rewards || !workspace || (pref->ref != ADAMW_REF_NONE && !ref_logp) ||
+    if (!stats || !losses || !rewards || (pref->ref != ADAMW_REF_NONE && !ref_logp) ||
         (tokens->n > 0 && (!logp || !d_logp)))
         return ADAMW_ERR_INVALID_ARG;
     const void* floats[] = {logp, ref_logp, stats, losses, rewards, d_logp};
     for (const void* p : floats)
         if (!aligned(p, 4)) return ADAMW_ERR_MISALIGNED;
-    if (!aligned(workspace, 16)) return ADAMW_ERR_MISALIGNED;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int64_t pairs = tokens->sequences / 2;
-    // CTAs per pair: more where pairs are few and long
-    int cluster = 1;
-    while (cluster < 8 && pairs * cluster < 304 && tokens->n >= pairs * cluster * 4 * kThreads) cluster *= 2;
     const Preference P = {pref->beta, pref->margin, pref->label_smoothing, pref->grad_scale,
                           pref->kind, pref->length_average, pref->ref};
-    float* difference = static_cast<float*>(workspace);
+    const Tokens k = tokens_of(tokens, nullptr, 0);
+    const int64_t per_pair = tokens->n / pairs;
+    int block = kThreads;
+    while (block < 1024 && per_pair >= 8 * block) block *= 2;
+    if (pairs <= kClusterPairs && tokens->n <= kClusterTokens) {
+        int ctas = 1;
+        while (ctas < 8 && ctas < pairs) ctas *= 2;
+        return launched(launch(preference_cluster_kernel, uint32_t(ctas), block, ctas, 0, st, k, P, logp, ref_logp,
+                               losses, rewards, d_logp, stats), "preference launch")
+                   ? ADAMW_OK : ADAMW_ERR_CUDA;
+    }
+    // CTAs per pair: more where pairs are few and long
+    int cluster = 1;
+    while (cluster < 8 && pairs * cluster < 304 && per_pair >= cluster * 4 * block) cluster *= 2;
     if (pairs * cluster > kMaxCount) return ADAMW_ERR_TOO_LARGE;
-    if (!launched(launch(preference_kernel, uint32_t(pairs * cluster), kThreads, cluster, 0, st,
-                         tokens_of(tokens, nullptr, 0), P, logp, ref_logp, losses, rewards, d_logp,
-                         difference), "preference launch"))
+    auto kernel = cluster > 1 ? preference_kernel<true> : preference_kernel<false>;
+    if (!launched(launch(kernel, uint32_t(pairs * cluster), block, cluster, 0, st, k, P, logp, ref_logp, losses,
+                         rewards, d_logp), "preference launch"))
         return ADAMW_ERR_CUDA;
     return launched(launch(preference_stats_kernel, 1u, kThreads, 1, 0, st, uint32_t(pairs), P,
-                           static_cast<const float*>(losses), static_cast<const float*>(difference), stats),
+                           static_cast<const float*>(losses), static_cast<const float*>(rewards), stats),
                     "preference statistics launch")
                ? ADAMW_OK : ADAMW_ERR_CUDA;
 }

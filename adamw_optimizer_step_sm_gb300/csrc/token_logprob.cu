@@ -610,7 +610,7 @@ extern "C" int adamw_policy_loss_logits(const adamw_rows_t* logits, const int64_
             }
             if (!launched(e, "policy_loss_logits launch")) return ADAMW_ERR_CUDA;
         }
-        return adamw::launch_policy(tokens, policy, targets, ignore_index, logp, old_logp, ref_logp,
+        return adamw::launch_policy(tokens, policy, targets, ignore_index, true, logp, old_logp, ref_logp,
                                     advantages, entropy, stats, counts, nullptr, nullptr, workspace, st);
     }
     char* w = static_cast<char*>(workspace) + round16(adamw_policy_workspace(tokens->n, tokens->sequences));
@@ -619,7 +619,7 @@ extern "C" int adamw_policy_loss_logits(const adamw_rows_t* logits, const int64_
     float* d_entropy = entropy ? reinterpret_cast<float*>(w + round16(8 * tokens->n) + round16(4 * tokens->n)) : nullptr;
     rc = adamw_token_logprob(logits, targets, ignore_index, scale, logp, entropy, row_stats, stream);
     if (rc != ADAMW_OK) return rc;
-    rc = adamw::launch_policy(tokens, policy, targets, ignore_index, logp, old_logp, ref_logp, advantages,
+    rc = adamw::launch_policy(tokens, policy, targets, ignore_index, true, logp, old_logp, ref_logp, advantages,
                               entropy, stats, counts, d_logp, d_entropy, workspace, st);
     if (rc != ADAMW_OK) return rc;
     return adamw_token_logprob_backward(logits, targets, ignore_index, scale, row_stats, entropy, d_logp,

@@ -35,6 +35,7 @@ import torch
 from . import adamw_sm as A
 
 _byref = ctypes.byref
+_F32 = torch.float32
 _CODES = {torch.bfloat16: A.DTYPE_BF16, torch.float16: A.DTYPE_FP16, torch.float32: A.DTYPE_FP32}
 
 
@@ -68,21 +69,17 @@ class PreferenceLoss(NamedTuple):
 
 # ---------------------------------------------------------------- checking --
 
-def _on(device: torch.device):
-    """The device guard and the raw current stream of a call."""
-    if device.index != torch.cuda.current_device():
-        return torch.cuda.device(device), torch.cuda.current_stream(device).cuda_stream
-    return None, torch._C._cuda_getCurrentRawStream(device.index)
+# A call on small arrays is mostly host time: the checks below take the usual
+# case first, in one condition.
 
-
-def _call(name: str, device: torch.device, *args) -> None:
-    guard, stream = _on(device)
-    f = getattr(A.load(), name)
-    if guard is None:
-        rc = f(*args, stream)
+def _call(f, name: str, device: torch.device, *args) -> None:
+    """One library call on the device's current stream."""
+    index = device.index
+    if index == torch._C._cuda_getDevice():
+        rc = f(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with guard:
-            rc = f(*args, stream)
+        with torch.cuda.device(index):
+            rc = f(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc:
         raise A.AdamWError(rc, name)
 
@@ -135,6 +132,8 @@ def _targets(t: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
 
 
 def _floats(name: str, t: torch.Tensor, shape, device) -> torch.Tensor:
+    if t.dtype is _F32 and t.shape == shape and t.device == device and t.is_contiguous():
+        return t
     if t.dtype != torch.float32 or t.device != device:
         raise TypeError(f"want fp32 {name} on the same device")
     if t.shape != shape:
@@ -187,10 +186,10 @@ def _scale(temperature: float) -> float:
 def _token_logprob(logits, targets, ignore_index, temperature, entropy) -> TokenLogprob:
     rows, t = _rows(logits), _targets(targets, logits)
     dev, shape = logits.device, targets.shape
-    logp = torch.empty(shape, dtype=torch.float32, device=dev)
-    ent = torch.empty(shape, dtype=torch.float32, device=dev) if entropy else None
-    stats = torch.empty((*shape, 2), dtype=torch.float32, device=dev)
-    _call("adamw_token_logprob", dev, _byref(rows), t.data_ptr(), ignore_index, _scale(temperature),
+    logp = torch.empty(shape, dtype=_F32, device=dev)
+    ent = torch.empty(shape, dtype=_F32, device=dev) if entropy else None
+    stats = torch.empty((*shape, 2), dtype=_F32, device=dev)
+    _call(A.load().adamw_token_logprob, "adamw_token_logprob", dev, _byref(rows), t.data_ptr(), ignore_index, _scale(temperature),
           logp.data_ptr(), _ptr(ent), stats.data_ptr())
     return TokenLogprob(logp, ent, stats)
 
@@ -246,7 +245,7 @@ def token_logprob_backward(logits: torch.Tensor, targets: torch.Tensor, result: 
         dh = _floats("d_entropy", d_entropy, shape, dev)
         ent = _floats("entropy", result.entropy, shape, dev)
     d = _out_rows(out, logits)
-    _call("adamw_token_logprob_backward", dev, _byref(rows), t.data_ptr(), ignore_index, _scale(temperature),
+    _call(A.load().adamw_token_logprob_backward, "adamw_token_logprob_backward", dev, _byref(rows), t.data_ptr(), ignore_index, _scale(temperature),
           stats.data_ptr(), _ptr(ent), dl.data_ptr(), _ptr(dh), _byref(_rows(d)))
     return d
 
@@ -255,9 +254,11 @@ def token_logprob_backward(logits: torch.Tensor, targets: torch.Tensor, result: 
 
 def _tokens(shape, offsets, mask, device):
     """(adamw_tokens_t, sequences, what must stay alive) of token arrays."""
-    n = 1
-    for k in shape:
-        n *= k
+    n = shape.numel()
+    if offsets is None and mask is not None and mask.dtype is torch.bool and mask.shape == shape \
+            and mask.device == device and mask.is_contiguous():
+        sequences = shape[0] if len(shape) > 1 else 1
+        return A.adamw_tokens_t(n, sequences, None, mask.data_ptr()), sequences, mask
     keep = []
     if offsets is not None:
         if offsets.dtype != torch.int64 or offsets.device != device or offsets.dim() != 1 or offsets.numel() < 1:
@@ -275,6 +276,10 @@ def _tokens(shape, offsets, mask, device):
         mask = mask if mask.is_contiguous() else mask.contiguous()
         keep.append(mask)
     return A.adamw_tokens_t(n, sequences, _ptr(offsets), _ptr(mask)), sequences, keep
+
+
+def _detached(t):
+    return t.detach() if t.requires_grad else t
 
 
 def _advantages(a, shape, sequences, device):
@@ -307,10 +312,10 @@ def policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Te
     dev, shape = logp.device, logp.shape
     if not logp.is_cuda:
         raise TypeError("want CUDA tensors")
-    logp = _floats("logp", logp.detach(), shape, dev)
+    logp = _floats("logp", _detached(logp), shape, dev)
     old = _floats("old_logp", old_logp, shape, dev)
     ref = None if ref_logp is None else _floats("ref_logp", ref_logp, shape, dev)
-    ent = None if entropy is None else _floats("entropy", entropy.detach(), shape, dev)
+    ent = None if entropy is None else _floats("entropy", _detached(entropy), shape, dev)
     if kl_coef != 0.0 and ref is None:
         raise ValueError("a KL term needs ref_logp")
     if entropy_coef != 0.0 and ent is None:
@@ -319,12 +324,13 @@ def policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Te
     adv, per_token = _advantages(advantages, shape, sequences, dev)
     policy = _policy(clip_low, clip_high, dual_clip, kl, kl_coef, entropy_coef, reduce, divisor, grad_scale,
                      per_token)
-    stats = torch.empty(6, dtype=torch.float32, device=dev)
+    stats = torch.empty(6, dtype=_F32, device=dev)
     counts = torch.empty(2, dtype=torch.int64, device=dev)
-    d_logp = torch.empty(shape, dtype=torch.float32, device=dev)
-    d_entropy = torch.empty(shape, dtype=torch.float32, device=dev) if ent is not None else None
-    work = torch.empty(A.load().adamw_policy_workspace(tokens.n, sequences), dtype=torch.uint8, device=dev)
-    _call("adamw_policy_loss", dev, _byref(tokens), _byref(policy), logp.data_ptr(), old.data_ptr(), _ptr(ref),
+    d_logp = torch.empty(shape, dtype=_F32, device=dev)
+    d_entropy = torch.empty(shape, dtype=_F32, device=dev) if ent is not None else None
+    lib = A.load()
+    work = torch.empty(lib.adamw_policy_workspace(tokens.n, sequences), dtype=torch.uint8, device=dev)
+    _call(lib.adamw_policy_loss, "adamw_policy_loss", dev, _byref(tokens), _byref(policy), logp.data_ptr(), old.data_ptr(), _ptr(ref),
           adv.data_ptr(), _ptr(ent), stats.data_ptr(), counts.data_ptr(), d_logp.data_ptr(), _ptr(d_entropy),
           work.data_ptr())
     return PolicyLoss(stats, counts, d_logp, d_entropy)
@@ -342,7 +348,7 @@ def policy_loss_logits(logits: torch.Tensor, targets: torch.Tensor, old_logp: to
     (to ``out``, which may be the logits themselves).  Tokens whose target is
     ``ignore_index`` do not count.  ``entropy`` asks for the entropy (implied
     by ``entropy_coef``)."""
-    logits = logits.detach()
+    logits = _detached(logits)
     rows, t = _rows(logits), _targets(targets, logits)
     dev, shape = logits.device, targets.shape
     old = _floats("old_logp", old_logp, shape, dev)
@@ -355,13 +361,14 @@ def policy_loss_logits(logits: torch.Tensor, targets: torch.Tensor, old_logp: to
                      per_token)
     d = _out_rows(out, logits)
     if out is not None:
-        d = d.detach()
-    stats = torch.empty(6, dtype=torch.float32, device=dev)
+        d = _detached(d)
+    stats = torch.empty(6, dtype=_F32, device=dev)
     counts = torch.empty(2, dtype=torch.int64, device=dev)
-    logp = torch.empty(shape, dtype=torch.float32, device=dev)
-    ent = torch.empty(shape, dtype=torch.float32, device=dev) if entropy or entropy_coef != 0.0 else None
-    work = torch.empty(A.load().adamw_policy_logits_workspace(tokens.n, sequences), dtype=torch.uint8, device=dev)
-    _call("adamw_policy_loss_logits", dev, _byref(rows), t.data_ptr(), ignore_index, _scale(temperature),
+    logp = torch.empty(shape, dtype=_F32, device=dev)
+    ent = torch.empty(shape, dtype=_F32, device=dev) if entropy or entropy_coef != 0.0 else None
+    lib = A.load()
+    work = torch.empty(lib.adamw_policy_logits_workspace(tokens.n, sequences), dtype=torch.uint8, device=dev)
+    _call(lib.adamw_policy_loss_logits, "adamw_policy_loss_logits", dev, _byref(rows), t.data_ptr(), ignore_index, _scale(temperature),
           _byref(tokens), _byref(policy), old.data_ptr(), _ptr(ref), adv.data_ptr(), stats.data_ptr(),
           counts.data_ptr(), logp.data_ptr(), _ptr(ent), _byref(_rows(d)), work.data_ptr())
     return PolicyLogits(stats, counts, logp, ent, d)
@@ -382,7 +389,7 @@ def preference_loss(logp: torch.Tensor, ref_logp: Optional[torch.Tensor] = None,
         raise TypeError("want CUDA tensors")
     if kind not in A.PREFERENCE:
         raise ValueError('want kind "sigmoid", "hinge" or "ipo"')
-    logp = _floats("logp", logp.detach(), shape, dev)
+    logp = _floats("logp", _detached(logp), shape, dev)
     tokens, sequences, _keep = _tokens(shape, offsets, mask, dev)
     if sequences < 2 or sequences % 2:
         raise ValueError("want an even number of sequences, the preferred ones first")
@@ -393,11 +400,10 @@ def preference_loss(logp: torch.Tensor, ref_logp: Optional[torch.Tensor] = None,
         ref = _floats("ref_logp", ref_logp, shape if how == A.REF_TOKEN else (sequences,), dev)
     pref = A.adamw_preference_t(beta, margin, label_smoothing, grad_scale, A.PREFERENCE[kind],
                                 1 if length_average else 0, how)
-    stats = torch.empty(3, dtype=torch.float32, device=dev)
-    losses = torch.empty(pairs, dtype=torch.float32, device=dev)
-    rewards = torch.empty(sequences, dtype=torch.float32, device=dev)
-    d_logp = torch.empty(shape, dtype=torch.float32, device=dev)
-    work = torch.empty(A.load().adamw_preference_workspace(pairs), dtype=torch.uint8, device=dev)
-    _call("adamw_preference_loss", dev, _byref(tokens), _byref(pref), logp.data_ptr(), _ptr(ref),
-          stats.data_ptr(), losses.data_ptr(), rewards.data_ptr(), d_logp.data_ptr(), work.data_ptr())
+    stats = torch.empty(3, dtype=_F32, device=dev)
+    losses = torch.empty(pairs, dtype=_F32, device=dev)
+    rewards = torch.empty(sequences, dtype=_F32, device=dev)
+    d_logp = torch.empty(shape, dtype=_F32, device=dev)
+    _call(A.load().adamw_preference_loss, "adamw_preference_loss", dev, _byref(tokens), _byref(pref), logp.data_ptr(), _ptr(ref),
+          stats.data_ptr(), losses.data_ptr(), rewards.data_ptr(), d_logp.data_ptr())
     return PreferenceLoss(stats, losses, rewards, d_logp)

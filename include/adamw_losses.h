@@ -209,14 +209,11 @@ typedef struct {
  * stats: fp32 [3]: loss, share of pairs with D > 0, mean of h.
  * losses: fp32 [B].  rewards: fp32 [2 B], beta S.  d_logp: fp32 [n].
  * A sequence with no token that counts has S = 0 (less its reference's sum).
- * workspace: adamw_preference_workspace(pairs) bytes of device memory,
- *   16-byte aligned.
  * Errors: INVALID_ARG (an odd or zero number of sequences among them),
  * MISALIGNED, TOO_LARGE, CUDA. */
 int adamw_preference_loss(const adamw_tokens_t* tokens, const adamw_preference_t* pref,
                           const float* logp, const float* ref_logp, float* stats, float* losses,
-                          float* rewards, float* d_logp, void* workspace, adamw_stream_t stream);
-int64_t adamw_preference_workspace(int64_t pairs);
+                          float* rewards, float* d_logp, adamw_stream_t stream);
 
 /* One gradient of a list to clip.  src is read; dst receives the clipped
  * gradient, rounded to dst_dtype: another buffer, src itself (in place; then
