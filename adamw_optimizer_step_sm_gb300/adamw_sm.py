@@ -601,7 +601,7 @@ class ClipPlan:
             raise ValueError('norm must be "l2" or "max"')
         if not max_norm > 0:
             raise ValueError("want max_norm > 0")
-        st = stream.cuda_stream if stream is not None else torch.cuda.current_stream(self.device).cuda_stream
+        st = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self.device.index)
         adamw_clip_grads(self.handle, max_norm, NORM[norm], self._at, st)
         return self.result
 

@@ -602,7 +602,8 @@ int launch_policy(const adamw_tokens_t* t, const adamw_policy_t* p, const int64_
 
 extern "C" int64_t adamw_policy_workspace(int64_t n, int64_t sequences) {
     if (n < 0 || sequences < 0 || n > kMaxCount || sequences > kMaxCount) return 0;
-    return counts_bytes(sequences) + int64_t(kMaxGrid) * kSums * int64_t(sizeof(float2));
+    const adamw_tokens_t t = {n, sequences, nullptr, nullptr};
+    return counts_bytes(sequences) + (in_one_cluster(&t) ? 0 : int64_t(kMaxGrid) * kSums * int64_t(sizeof(float2)));
 }
 
 extern "C" int adamw_policy_loss(const adamw_tokens_t* tokens, const adamw_policy_t* policy,
