@@ -22,6 +22,42 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInf = std::numeric_limits<float>::infinity();
 
+// ------------------------------------------------------- pairs of floats --
+
+// Two floats in a 64-bit register, for the packed fp32 instructions (sm_100
+// and later): one instruction does both.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
+}
+__device__ __forceinline__ float low(Pair p) { return __uint_as_float(uint32_t(p)); }
+__device__ __forceinline__ float high(Pair p) { return __uint_as_float(uint32_t(p >> 32)); }
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// A 32-bit register as two 16-bit floats.
+template <typename T>
+__device__ __forceinline__ T word(uint32_t w) {
+    T t;
+    memcpy(&t, &w, 4);
+    return t;
+}
+
 // ------------------------------------------------------- element types ----
 
 template <int DT>
@@ -51,6 +87,31 @@ struct Elem<ADAMW_DTYPE_BF16> {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const __nv_bfloat162 r = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            memcpy(&w[i], &r, 4);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // the vector as pairs of floats, and the larger of each pair's halves
+    __device__ static void pairs(uint4 v, Pair* x) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    }
+    template <int U>
+    __device__ static float largest(const uint4 (&v)[U]) {
+        __nv_bfloat162 m = word<__nv_bfloat162>(v[0].x);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            m = __hmax2(m, __hmax2(word<__nv_bfloat162>(v[u].x), word<__nv_bfloat162>(v[u].y)));
+            m = __hmax2(m, __hmax2(word<__nv_bfloat162>(v[u].z), word<__nv_bfloat162>(v[u].w)));
+        }
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+    __device__ static uint4 pack_pairs(const Pair* x) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 r = __floats2bfloat162_rn(low(x[i]), high(x[i]));
             memcpy(&w[i], &r, 4);
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
@@ -88,6 +149,33 @@ struct Elem<ADAMW_DTYPE_FP16> {
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
+    __device__ static void pairs(uint4 v, Pair* x) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(word<__half2>(w[i]));
+            x[i] = pair(f.x, f.y);
+        }
+    }
+    template <int U>
+    __device__ static float largest(const uint4 (&v)[U]) {
+        __half2 m = word<__half2>(v[0].x);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            m = __hmax2(m, __hmax2(word<__half2>(v[u].x), word<__half2>(v[u].y)));
+            m = __hmax2(m, __hmax2(word<__half2>(v[u].z), word<__half2>(v[u].w)));
+        }
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+    __device__ static uint4 pack_pairs(const Pair* x) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2 r = __floats2half2_rn(low(x[i]), high(x[i]));
+            memcpy(&w[i], &r, 4);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
 };
 
 template <>
@@ -106,6 +194,23 @@ struct Elem<ADAMW_DTYPE_FP32> {
     __device__ static uint4 pack(const float* x) {
         return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
                           __float_as_uint(x[3]));
+    }
+    __device__ static void pairs(uint4 v, Pair* x) {
+        x[0] = pair(__uint_as_float(v.x), __uint_as_float(v.y));
+        x[1] = pair(__uint_as_float(v.z), __uint_as_float(v.w));
+    }
+    template <int U>
+    __device__ static float largest(const uint4 (&v)[U]) {
+        float m = __uint_as_float(v[0].x);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            m = fmaxf(fmaxf(fmaxf(m, __uint_as_float(v[u].x)), fmaxf(__uint_as_float(v[u].y), __uint_as_float(v[u].z))),
+                      __uint_as_float(v[u].w));
+        return m;
+    }
+    __device__ static uint4 pack_pairs(const Pair* x) {
+        return make_uint4(__float_as_uint(low(x[0])), __float_as_uint(high(x[0])), __float_as_uint(low(x[1])),
+                          __float_as_uint(high(x[1])));
     }
 };
 
@@ -198,27 +303,40 @@ __device__ __forceinline__ Sum2 warp_sum(Sum2 a) {
 
 // -------------------------------------------------------- online softmax --
 
-// Over the elements x seen so far: m their largest, s = sum exp(scale(x - m)),
-// t = sum exp(scale(x - m)) (x - m) (for the entropy).  -inf elements (and an
-// empty record) leave m at -inf and add nothing.
+// Exponentials are taken in base 2: with c = scale log2(e), exp(scale x) is
+// 2^(c x).  Over the elements x seen so far, m is their largest, and
+//     s = sum 2^(c x - r),  t = sum 2^(c x - r) (c x - r)  (for the entropy)
+// with r = c m as rounded to fp32, so that each exponent is one fused
+// multiply-add, rounded once.  -inf elements (and an empty record) leave m at
+// -inf and add nothing; r is then 0, so that -inf - (-inf) does not arise.
+// Where c m is near or past fp32's range (rows masked throughout by the
+// type's lowest value) the exponents are (x - m) c instead.
 struct Online {
     float m, s, t;
 };
 
-// The largest element, or 0 where there is none: what exponents are taken
-// relative to, so that -inf - (-inf) does not arise.
-__device__ __forceinline__ float reference_of(float m) { return m == -kInf ? 0.0f : m; }
+__device__ __forceinline__ bool extreme(float m, float c) { return m != -kInf && !(fabsf(m) * c < 1e38f); }
+__device__ __forceinline__ float reference(float m, float c) { return m == -kInf ? 0.0f : m * c; }
 
-// Moves a record's reference to M >= o.m.  c = scale * log2(e).
+// The exponent of an element, whatever m.
+__device__ __forceinline__ float exponent(float x, float m, float c) {
+    return extreme(m, c) ? (x - m) * c : fmaf(x, c, -reference(m, c));
+}
+
+// Moves a record's reference to that of M >= o.m.
 template <bool ENT>
 __device__ __forceinline__ void rebase(Online& o, float M, float c) {
     if (o.m == M) return;
-    const float d = o.m - M;  // < 0; -inf for an empty record
-    const float f = exp2_fast(d * c);
+    if (o.m == -kInf) {   // s is 0, or NaN when it saw a NaN, which stays
+        o.m = M;
+        return;
+    }
+    float d = extreme(o.m, c) || extreme(M, c) ? (o.m - M) * c : o.m * c - M * c;
+    d = fmaxf(d, -1e30f);
+    const float f = exp2_fast(d);
     // d f before s: both d s and f's smallness may pass fp32's range
-    if (ENT) o.t = o.m == -kInf ? 0.0f : fmaf(d * f, o.s, o.t * f);
-    // an empty record holds s = 0, or NaN when it saw a NaN, which stays
-    o.s = o.m == -kInf ? o.s : o.s * f;
+    if (ENT) o.t = fmaf(d * f, o.s, o.t * f);
+    o.s *= f;
     o.m = M;
 }
 
@@ -231,28 +349,47 @@ __device__ __forceinline__ void join(Online& a, Online b, float c) {
     if (ENT) a.t += b.t;
 }
 
-// Adds N elements.
-template <bool ENT, int N>
-__device__ __forceinline__ void absorb(Online& o, const float* x, float c) {
-    float m = x[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i) m = fmaxf(m, x[i]);
+template <bool ENT>
+__device__ __forceinline__ void absorb_one(Online& o, float x, float c) {
+    if (x > o.m) rebase<ENT>(o, x, c);
+    const float d = exponent(x, o.m, c);
+    const float e = exp2_fast(d);
+    o.s += e;
+    if (ENT) o.t = fmaf(e, fmaxf(d, -1e30f), o.t);   // -inf: 0 * (large), not 0 * inf
+}
+
+// Adds the elements of U vectors.
+template <int DT, bool ENT, int U>
+__device__ __forceinline__ void absorb(Online& o, const uint4 (&v)[U], float c) {
+    using E = Elem<DT>;
+    const float m = E::largest(v);
     if (m > o.m) rebase<ENT>(o, m, c);
-    const float ref = reference_of(o.m);
-    float s0 = 0.0f, s1 = 0.0f, t0 = 0.0f, t1 = 0.0f;
+    if (extreme(o.m, c)) {
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-        const float d0 = x[i] - ref, d1 = x[i + 1] - ref;
-        const float e0 = exp2_fast(d0 * c), e1 = exp2_fast(d1 * c);
-        s0 += e0;
-        s1 += e1;
-        if (ENT) {  // a -inf element: 0 * (large), not 0 * inf
-            t0 = fmaf(e0, fmaxf(d0, -1e30f), t0);
-            t1 = fmaf(e1, fmaxf(d1, -1e30f), t1);
+        for (int u = 0; u < U; ++u) {
+            float x[E::kVec];
+            E::unpack(v[u], x);
+            for (int i = 0; i < E::kVec; ++i) absorb_one<ENT>(o, x[i], c);
+        }
+        return;
+    }
+    const float r = -reference(o.m, c);
+    const Pair c2 = pair(c, c), r2 = pair(r, r);
+    Pair s = pair(0.0f, 0.0f), t = s;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        Pair x[E::kVec / 2];
+        E::pairs(v[u], x);
+#pragma unroll
+        for (int i = 0; i < E::kVec / 2; ++i) {
+            const Pair d = fma2(x[i], c2, r2);
+            const Pair e = pair(exp2_fast(low(d)), exp2_fast(high(d)));
+            s = add2(s, e);
+            if (ENT) t = fma2(e, pair(fmaxf(low(d), -1e30f), fmaxf(high(d), -1e30f)), t);
         }
     }
-    o.s += s0 + s1;
-    if (ENT) o.t += t0 + t1;
+    o.s += low(s) + high(s);
+    if (ENT) o.t += low(t) + high(t);
 }
 
 template <bool ENT>
@@ -269,45 +406,60 @@ __device__ __forceinline__ Online warp_join(Online o, float c) {
     return o;
 }
 
-// What the row's softmax comes to.
+constexpr float kLn2 = 0.6931471805599453f;
+
+// What a row's softmax comes to: m and s as in Online, with s = +inf for a
+// row without a distribution, or not read.
 struct RowStats {
-    float m;      // its largest logit (0 where it has no distribution)
-    float log_s;  // log of the sum; +inf: no distribution, or not read
-    float entropy;
+    float m, s, log_s, entropy;
 };
 
 template <bool ENT>
-__device__ __forceinline__ RowStats row_stats(const Online& o, float scale) {
-    RowStats r;
-    if (o.m == -kInf && o.s == 0.0f) {
-        r.m = 0.0f;
-        r.log_s = kInf;
-        r.entropy = 0.0f;
-        return r;
-    }
-    r.m = reference_of(o.m);
-    r.log_s = logf(o.s);
-    r.entropy = ENT ? r.log_s - scale * (o.t / o.s) : 0.0f;
-    return r;
+__device__ __forceinline__ RowStats row_stats(const Online& o) {
+    if (o.m == -kInf && o.s == 0.0f) return {0.0f, kInf, kInf, 0.0f};
+    const float log_s = logf(o.s);
+    return {o.m, o.s, log_s, ENT ? log_s - kLn2 * (o.t / o.s) : 0.0f};
 }
 
 // log-probability of a logit x under the row.
-__device__ __forceinline__ float logp_of(const RowStats& r, float x, float scale) {
-    if (r.log_s == kInf) return -kInf;
-    return (x - r.m) * scale - r.log_s;
+__device__ __forceinline__ float logp_of(const RowStats& r, float x, float scale, float c) {
+    if (r.s == kInf) return -kInf;
+    const float d = exponent(x, r.m, c);
+    // an exponent past fp32's range: the type's lowest value in an ordinary row
+    return (d == -kInf ? (x - r.m) * scale : kLn2 * d) - r.log_s;
 }
 
-// The gradient of one element, without the target's term:
-//   -p (a + b (log p + H)),  a = scale d_logp, b = scale d_entropy
-template <bool ENT>
-__device__ __forceinline__ float logit_grad(float x, float m, float log_s, float log2_s, float scale,
-                                            float c, float a, float b, float H) {
-    const float d = x - m;
-    const float p = exp2_fast(fmaf(d, c, -log2_s));
-    if (!ENT) return -a * p;
-    const float lp = fmaxf(fmaf(d, scale, -log_s), -1e30f);
-    return -p * fmaf(b, lp + H, a);
-}
+// The gradient of an element, without the target's term a:
+//     -p (a + b (log p + H)) = 2^d (A + B d),  d its exponent,
+//     a = scale d_logp, b = scale d_entropy
+struct Gradient {
+    float m, c, A, B, a;
+    bool extreme_row;
+    __device__ __forceinline__ Gradient(float m, float s, float log_s, float c, float a, float b, float H)
+        : m(m), c(c), A(-(a + b * (H - log_s)) / s), B(-b * kLn2 / s), a(a), extreme_row(extreme(m, c)) {}
+
+    template <bool ENT>
+    __device__ __forceinline__ float of(float x) const {
+        const float d = exponent(x, m, c), e = exp2_fast(d);
+        return ENT ? e * fmaf(B, fmaxf(d, -1e30f), A) : e * A;
+    }
+    // of a vector of an ordinary row
+    template <int DT, bool ENT>
+    __device__ __forceinline__ uint4 of(uint4 v) const {
+        using E = Elem<DT>;
+        const float r = -reference(m, c);
+        const Pair c2 = pair(c, c), r2 = pair(r, r), A2 = pair(A, A), B2 = pair(B, B);
+        Pair x[E::kVec / 2];
+        E::pairs(v, x);
+#pragma unroll
+        for (int i = 0; i < E::kVec / 2; ++i) {
+            const Pair d = fma2(x[i], c2, r2);
+            const Pair e = pair(exp2_fast(low(d)), exp2_fast(high(d)));
+            x[i] = mul2(e, ENT ? fma2(B2, pair(fmaxf(low(d), -1e30f), fmaxf(high(d), -1e30f)), A2) : A2);
+        }
+        return E::pack_pairs(x);
+    }
+};
 
 // ----------------------------------------------------------------- rows ----
 

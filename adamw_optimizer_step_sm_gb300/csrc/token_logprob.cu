@@ -98,54 +98,75 @@ logprob_kernel(Rows logits, uint32_t rows, int cols, const int64_t* targets, int
 
     Online o = {-kInf, 0.0f, 0.0f};
     const int extra = extra_element<DT>(sp, lane, rank == 0, rank == size - 1);
-    float x2[2] = {extra >= 0 ? E::load(row, extra) : -kInf, -kInf};
-    for (int base = first + lane; base < end; base += kUnroll * width) {
+    if (extra >= 0) absorb_one<ENT>(o, E::load(row, extra), c);
+    int base = first + lane;
+    for (; base + (kUnroll - 1) * width < end; base += kUnroll * width) {
         uint4 v[kUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            v[u] = base + u * width < end
-                       ? load16(body + base + u * width)
-                       : make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf);
-        float x[kUnroll * E::kVec];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) E::unpack(v[u], x + u * E::kVec);
-        absorb<ENT, kUnroll * E::kVec>(o, x, c);
+        for (int u = 0; u < kUnroll; ++u) v[u] = load16(body + base + u * width);
+        absorb<DT, ENT>(o, v, c);
     }
-    absorb<ENT, 2>(o, x2, c);
+    for (; base < end; base += width) {
+        const uint4 v[1] = {load16(body + base)};
+        absorb<DT, ENT>(o, v, c);
+    }
     o = group_join<ENT, WARP>(o, c);
     if (!writer) return;
     const bool bad = t < 0 || t >= cols;
-    RowStats rs = row_stats<ENT>(o, scale);
-    if (bad) rs.m = rs.log_s = rs.entropy = __int_as_float(0x7fc00000);
-    logp[r] = logp_of(rs, bad ? 0.0f : E::load(row, t), scale);
+    RowStats rs = row_stats<ENT>(o);
+    if (bad) rs.m = rs.s = rs.log_s = rs.entropy = __int_as_float(0x7fc00000);
+    logp[r] = logp_of(rs, bad ? 0.0f : E::load(row, t), scale, c);
     if (entropy) entropy[r] = rs.entropy;
-    if (stats) reinterpret_cast<float2*>(stats)[r] = make_float2(rs.m, rs.log_s);
+    if (stats) reinterpret_cast<float2*>(stats)[r] = make_float2(rs.m, rs.s);
 }
 
 // --------------------------------------------------------------- backward --
 
-// Writes the gradients of the vector at `elem` (its first element's index).
-template <int DT, bool ENT>
-__device__ __forceinline__ void grad_vector(uint4 v, char* out, bool vector_out, int elem, int64_t t,
-                                            float m, float log_s, float log2_s, float scale, float c,
-                                            float a, float b, float H) {
+// Writes the gradients of the vectors lane, lane + width, .. of n, the first
+// of them element `elem` of the row: from v(i), the vector's logits.
+template <int DT, bool ENT, int U, typename Load>
+__device__ __forceinline__ void grad_vectors(const Gradient& G, const Load& v, int n, int lane, int width,
+                                             char* out, bool vector_out, int elem) {
     using E = Elem<DT>;
-    float x[E::kVec];
-    E::unpack(v, x);
+    if (vector_out && !G.extreme_row) {
+        uint4* to = reinterpret_cast<uint4*>(out + int64_t(elem) * E::kSize);
+        int i = lane;
+        for (; i + (U - 1) * width < n; i += U * width) {
+            uint4 x[U];
 #pragma unroll
-    for (int j = 0; j < E::kVec; ++j) x[j] = logit_grad<ENT>(x[j], m, log_s, log2_s, scale, c, a, b, H);
-    const int64_t at = t - elem;
-    if (at >= 0 && at < E::kVec) {
+            for (int u = 0; u < U; ++u) x[u] = v(i + u * width);
 #pragma unroll
-        for (int j = 0; j < E::kVec; ++j)
-            if (j == at) x[j] += a;
+            for (int u = 0; u < U; ++u) store16(to + i + u * width, G.of<DT, ENT>(x[u]));
+        }
+        if (i < n) {
+            uint4 x[U];
+#pragma unroll
+            for (int u = 0; u < U - 1; ++u)
+                if (i + u * width < n) x[u] = v(i + u * width);
+#pragma unroll
+            for (int u = 0; u < U - 1; ++u)
+                if (i + u * width < n) store16(to + i + u * width, G.of<DT, ENT>(x[u]));
+        }
+    } else {  // rows whose addresses differ modulo 16, and rows of extreme logits
+        for (int i = lane; i < n; i += width) {
+            float x[E::kVec];
+            E::unpack(v(i), x);
+#pragma unroll
+            for (int j = 0; j < E::kVec; ++j) E::store(out, int64_t(elem) + i * E::kVec + j, G.of<ENT>(x[j]));
+        }
     }
-    if (vector_out) {
-        store16(out + int64_t(elem) * E::kSize, E::pack(x));
-    } else {
-#pragma unroll
-        for (int j = 0; j < E::kVec; ++j) E::store(out, elem + j, x[j]);
-    }
+}
+
+// The target's element, by the thread that wrote it above: its vector is one
+// of that thread's, or it is the thread's extra element.
+template <int DT, bool ENT>
+__device__ __forceinline__ void grad_target(const Gradient& G, char* out, const RowSplit<DT>& sp, int64_t t,
+                                            float xt, int first, int end, int lane, int width, int extra) {
+    using E = Elem<DT>;
+    const int64_t at = t - sp.head, i = at / E::kVec - first;
+    const bool in_vectors = at >= 0 && at < int64_t(sp.vecs) * E::kVec;
+    const bool mine = in_vectors ? i >= 0 && i < end - first && int(i) % width == lane : t == extra;
+    if (mine) E::store(out, t, G.of<ENT>(xt) + G.a);
 }
 
 // Zeros in the vectors [first, end) and the extra element of a row.
@@ -187,31 +208,22 @@ logprob_backward_kernel(Rows logits, Rows grad, uint32_t rows, uint32_t pieces, 
     const int extra = extra_element<DT>(sp, lane, piece == 0, piece == pieces - 1);
 
     const float2 st = reinterpret_cast<const float2*>(stats)[r];
+    const int64_t t = targets[r];
+    const float a = scale * d_logp[r];
+    const float b = ENT ? scale * d_entropy[r] : 0.0f;
+    const float H = ENT ? entropy[r] : 0.0f;
     if (st.y == kInf) {  // ignored, or without a distribution
         zero_row<DT>(out, vector_out, sp, first, end, lane, width, extra);
         return;
     }
-    const int64_t t = targets[r];
-    const float c = scale * kLog2e, log2_s = st.y * kLog2e;
-    const float a = scale * d_logp[r];
-    const float b = ENT ? scale * d_entropy[r] : 0.0f;
-    const float H = ENT ? entropy[r] : 0.0f;
-    const uint4* body = reinterpret_cast<const uint4*>(row + int64_t(sp.head) * E::kSize);
+    const float xt = t >= 0 && t < cols ? E::load(row, t) : 0.0f;
+    const Gradient G(st.x, st.y, ENT ? logf(st.y) : 0.0f, scale * kLog2e, a, b, H);
+    const uint4* body = reinterpret_cast<const uint4*>(row + int64_t(sp.head) * E::kSize) + first;
     const float xe = extra >= 0 ? E::load(row, extra) : 0.0f;
-    for (int base = first + lane; base < end; base += kUnroll * width) {
-        uint4 v[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            if (base + u * width < end) v[u] = load16(body + base + u * width);
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            if (base + u * width < end)
-                grad_vector<DT, ENT>(v[u], out, vector_out, sp.head + (base + u * width) * E::kVec, t, st.x,
-                                     st.y, log2_s, scale, c, a, b, H);
-    }
-    if (extra >= 0)
-        E::store(out, extra,
-                 logit_grad<ENT>(xe, st.x, st.y, log2_s, scale, c, a, b, H) + (extra == t ? a : 0.0f));
+    grad_vectors<DT, ENT, kUnroll>(G, [body](int i) { return load16(body + i); }, end - first, lane, width, out,
+                                   vector_out, sp.head + first * E::kVec);
+    if (extra >= 0) E::store(out, extra, G.of<ENT>(xe));
+    grad_target<DT, ENT>(G, out, sp, t, xt, first, end, lane, width, extra);
 }
 
 // ------------------------------------------------------ fused policy loss --
@@ -301,43 +313,42 @@ policy_rows_kernel(Rows logits, Rows grad, Tokens tokens, int cols, float scale,
                                            a.counts->sequence[seq]) * P.grad_scale;
 
     Online o = {-kInf, 0.0f, 0.0f};
+    if (extra >= 0) absorb_one<ENT>(o, xe, c);
     for (int base = lane; base < n; base += kUnroll * width) {
         copy_wait<kDepth - 1>();
-        float x[kUnroll * E::kVec];
+        if (base + (kUnroll - 1) * width < n) {
+            uint4 v[kUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            E::unpack(base + u * width < n ? slice[base + u * width]
-                                           : make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf),
-                      x + u * E::kVec);
-        absorb<ENT, kUnroll * E::kVec>(o, x, c);
+            for (int u = 0; u < kUnroll; ++u) v[u] = slice[base + u * width];
+            absorb<DT, ENT>(o, v, c);
+        } else {
+            for (int i = base; i < n; i += width) {
+                const uint4 v[1] = {slice[i]};
+                absorb<DT, ENT>(o, v, c);
+            }
+        }
         ask();
     }
-    const float x2[2] = {xe, -kInf};
-    absorb<ENT, 2>(o, x2, c);
     o = group_join<ENT, WARP>(o, c);
 
-    RowStats rs = row_stats<ENT>(o, scale);
-    if (bad) rs.m = rs.log_s = rs.entropy = __int_as_float(0x7fc00000);
-    const float lp = logp_of(rs, xt, scale);
+    RowStats rs = row_stats<ENT>(o);
+    if (bad) rs.m = rs.s = rs.log_s = rs.entropy = __int_as_float(0x7fc00000);
+    const float lp = logp_of(rs, xt, scale, c);
     if (writer) {
         a.logp[r] = lp;
         if (a.entropy) a.entropy[r] = rs.entropy;
     }
     const PolicyToken k = policy_token(P, lp, old, a.ref_logp != nullptr, ref, A);
-    if (rs.log_s == kInf || seq < 0) {
+    if (rs.s == kInf || seq < 0) {
         zero_row<DT>(out, vector_out, sp, first, end, lane, width, extra);
         return;
     }
-    const float ga = scale * w * k.grad, gb = ENT ? -scale * w * P.entropy_coef : 0.0f;
-    const float log2_s = rs.log_s * kLog2e;
-#pragma unroll 4
-    for (int i = lane; i < n; i += width)
-        grad_vector<DT, ENT>(slice[i], out, vector_out, sp.head + (first + i) * E::kVec, t, rs.m, rs.log_s,
-                             log2_s, scale, c, ga, gb, rs.entropy);
-    if (extra >= 0)
-        E::store(out, extra,
-                 logit_grad<ENT>(xe, rs.m, rs.log_s, log2_s, scale, c, ga, gb, rs.entropy) +
-                     (extra == t ? ga : 0.0f));
+    const Gradient G(rs.m, rs.s, rs.log_s, c, scale * w * k.grad, ENT ? -scale * w * P.entropy_coef : 0.0f,
+                     rs.entropy);
+    grad_vectors<DT, ENT, kUnroll>(G, [slice](int i) { return slice[i]; }, n, lane, width, out, vector_out,
+                                   sp.head + first * E::kVec);
+    if (extra >= 0) E::store(out, extra, G.of<ENT>(xe));
+    grad_target<DT, ENT>(G, out, sp, t, xt, first, end, lane, width, extra);
 }
 
 // ------------------------------------------------------------------- host --

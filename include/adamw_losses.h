@@ -60,7 +60,8 @@ typedef struct {
  * largest x_j and s = sum_j exp(x_j - m):
  *     logp[r]    = x_t - m - log(s),  t = targets[r]
  *     entropy[r] = log(s) - sum_j exp(x_j - m) (x_j - m) / s
- *     stats[r]   = {m / scale, log(s)}, what the backward pass needs.
+ *     stats[r]   = what the backward pass needs: the row's largest logit and
+ *                  its sum relative to it.
  * targets: device int64, one per row.  A row whose target is ignore_index is
  *   not read: logp 0, entropy 0, no gradient.  A target outside [0, cols)
  *   gives NaN for the row and its gradient (a step whose gradients hold NaN
