@@ -9,14 +9,13 @@
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-// Rows of up to this many elements are taken by a warp each, eight to a CTA;
+// Threads of a CTA and 16-byte vectors in flight per thread, by kernel.
+constexpr int kForwardThreads = 128, kForwardUnroll = 8;
+constexpr int kBackwardThreads = 128, kBackwardUnroll = 8;
+constexpr int kPolicyThreads = 128, kPolicyUnroll = 8;
+// Rows of up to this many elements are taken by a warp each;
 // longer ones by a CTA or a cluster of them.
 constexpr int kWarpCols = 1024;
-// 16-byte vectors in flight per thread.
-constexpr int kUnroll = 4;
-
 // The elements of the row outside its vectors, at most one per thread of the
 // group: the head's by threads 0.. of the first CTA, the tail's by threads
 // 8.. of the last one.  -1: none.
@@ -29,13 +28,14 @@ __device__ __forceinline__ int extra_element(const RowSplit<DT>& sp, int lane, b
 
 // Joins the records of a group of threads: a warp, or a cluster of CTAs (one
 // or more).  Every thread gets the same record.
-template <bool ENT, bool WARP>
+template <bool ENT, bool WARP, int THREADS>
 __device__ __forceinline__ Online group_join(Online o, float c) {
     o = warp_join<ENT>(o, c);
     if (WARP) {
         __syncwarp();
         return o;
     }
+    constexpr int kWarps = THREADS / 32;
     __shared__ Online part[kWarps];
     __shared__ Online whole;
     const int warp = threadIdx.x / 32;
@@ -67,7 +67,7 @@ __device__ __forceinline__ Online group_join(Online o, float c) {
 // CTAs, each streaming its share of the row once, with the running maximum
 // and sums in registers).
 template <int DT, bool ENT, bool WARP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kForwardThreads)
 logprob_kernel(Rows logits, uint32_t rows, int cols, const int64_t* targets, int64_t ignore,
                float scale, float* logp, float* entropy, float* stats) {
     using E = Elem<DT>;
@@ -76,8 +76,8 @@ logprob_kernel(Rows logits, uint32_t rows, int cols, const int64_t* targets, int
     const uint32_t size = WARP ? 1 : cluster_size();
     const uint32_t rank = WARP ? 0 : cluster_rank();
     const int lane = WARP ? threadIdx.x % 32 : threadIdx.x;
-    constexpr int width = WARP ? 32 : kThreads;
-    const uint32_t r = WARP ? blockIdx.x * kWarps + threadIdx.x / 32 : blockIdx.x / size;
+    constexpr int width = WARP ? 32 : kForwardThreads;
+    const uint32_t r = WARP ? blockIdx.x * (kForwardThreads / 32) + threadIdx.x / 32 : blockIdx.x / size;
     if (r >= rows) return;  // whole warps only: the CTA form's grid is exact
     const int64_t t = targets[r];
     const bool writer = lane == 0 && rank == 0;
@@ -100,17 +100,21 @@ logprob_kernel(Rows logits, uint32_t rows, int cols, const int64_t* targets, int
     const int extra = extra_element<DT>(sp, lane, rank == 0, rank == size - 1);
     if (extra >= 0) absorb_one<ENT>(o, E::load(row, extra), c);
     int base = first + lane;
-    for (; base + (kUnroll - 1) * width < end; base += kUnroll * width) {
-        uint4 v[kUnroll];
+    for (; base + (kForwardUnroll - 1) * width < end; base += kForwardUnroll * width) {
+        uint4 v[kForwardUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) v[u] = load16(body + base + u * width);
+        for (int u = 0; u < kForwardUnroll; ++u) v[u] = load16(body + base + u * width);
         absorb<DT, ENT>(o, v, c);
     }
-    for (; base < end; base += width) {
-        const uint4 v[1] = {load16(body + base)};
+    if (base < end) {  // the last few, beside -inf
+        uint4 v[kForwardUnroll];
+#pragma unroll
+        for (int u = 0; u < kForwardUnroll; ++u)
+            v[u] = base + u * width < end ? load16(body + base + u * width)
+                                          : make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf);
         absorb<DT, ENT>(o, v, c);
     }
-    o = group_join<ENT, WARP>(o, c);
+    o = group_join<ENT, WARP, kForwardThreads>(o, c);
     if (!writer) return;
     const bool bad = t < 0 || t >= cols;
     RowStats rs = row_stats<ENT>(o);
@@ -187,7 +191,7 @@ __device__ __forceinline__ void zero_row(char* out, bool vector_out, const RowSp
 
 // One CTA per piece of a row (or a warp per row): elementwise.
 template <int DT, bool ENT, bool WARP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kBackwardThreads)
 logprob_backward_kernel(Rows logits, Rows grad, uint32_t rows, uint32_t pieces, int cols,
                         const int64_t* targets, float scale, const float* stats, const float* entropy,
                         const float* d_logp, const float* d_entropy) {
@@ -195,8 +199,8 @@ logprob_backward_kernel(Rows logits, Rows grad, uint32_t rows, uint32_t pieces, 
     dependency_trigger();
     dependency_wait();
     const int lane = WARP ? threadIdx.x % 32 : threadIdx.x;
-    constexpr int width = WARP ? 32 : kThreads;
-    const uint32_t r = WARP ? blockIdx.x * kWarps + threadIdx.x / 32 : blockIdx.x / pieces;
+    constexpr int width = WARP ? 32 : kBackwardThreads;
+    const uint32_t r = WARP ? blockIdx.x * (kBackwardThreads / 32) + threadIdx.x / 32 : blockIdx.x / pieces;
     const uint32_t piece = WARP ? 0 : blockIdx.x - r * pieces;
     if (r >= rows) return;
     const char* row = logits.at(r);
@@ -220,7 +224,7 @@ logprob_backward_kernel(Rows logits, Rows grad, uint32_t rows, uint32_t pieces, 
     const Gradient G(st.x, st.y, ENT ? logf(st.y) : 0.0f, scale * kLog2e, a, b, H);
     const uint4* body = reinterpret_cast<const uint4*>(row + int64_t(sp.head) * E::kSize) + first;
     const float xe = extra >= 0 ? E::load(row, extra) : 0.0f;
-    grad_vectors<DT, ENT, kUnroll>(G, [body](int i) { return load16(body + i); }, end - first, lane, width, out,
+    grad_vectors<DT, ENT, kBackwardUnroll>(G, [body](int i) { return load16(body + i); }, end - first, lane, width, out,
                                    vector_out, sp.head + first * E::kVec);
     if (extra >= 0) E::store(out, extra, G.of<ENT>(xe));
     grad_target<DT, ENT>(G, out, sp, t, xt, first, end, lane, width, extra);
@@ -246,7 +250,7 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
 }
 
-// Groups of kUnroll vectors per thread that are on their way at a time.
+// Groups of kPolicyUnroll vectors per thread that are on their way at a time.
 constexpr int kDepth = 4;
 
 // The policy loss of one token per group, from its row of logits to their
@@ -256,7 +260,7 @@ constexpr int kDepth = 4;
 // copy: one read and one write of HBM.  A thread reads only the vectors that
 // it copied itself, so the copies need no barrier.
 template <int DT, bool ENT, bool WARP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kPolicyThreads)
 policy_rows_kernel(Rows logits, Rows grad, Tokens tokens, int cols, float scale, Policy P, PolicyRows a) {
     using E = Elem<DT>;
     extern __shared__ uint4 slices[];
@@ -265,8 +269,8 @@ policy_rows_kernel(Rows logits, Rows grad, Tokens tokens, int cols, float scale,
     const uint32_t size = WARP ? 1 : cluster_size();
     const uint32_t rank = WARP ? 0 : cluster_rank();
     const int lane = WARP ? threadIdx.x % 32 : threadIdx.x;
-    constexpr int width = WARP ? 32 : kThreads;
-    const uint32_t r = WARP ? blockIdx.x * kWarps + threadIdx.x / 32 : blockIdx.x / size;
+    constexpr int width = WARP ? 32 : kPolicyThreads;
+    const uint32_t r = WARP ? blockIdx.x * (kPolicyThreads / 32) + threadIdx.x / 32 : blockIdx.x / size;
     if (r >= tokens.n) return;
     const char* row = logits.at(r);
     char* out = grad.at(r);
@@ -292,9 +296,9 @@ policy_rows_kernel(Rows logits, Rows grad, Tokens tokens, int cols, float scale,
     int asked = lane;
     auto ask = [&] {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
+        for (int u = 0; u < kPolicyUnroll; ++u)
             if (asked + u * width < n) copy_async16(slice + asked + u * width, body + asked + u * width);
-        asked += kUnroll * width;
+        asked += kPolicyUnroll * width;
         copy_commit();
     };
 #pragma unroll
@@ -314,12 +318,12 @@ policy_rows_kernel(Rows logits, Rows grad, Tokens tokens, int cols, float scale,
 
     Online o = {-kInf, 0.0f, 0.0f};
     if (extra >= 0) absorb_one<ENT>(o, xe, c);
-    for (int base = lane; base < n; base += kUnroll * width) {
+    for (int base = lane; base < n; base += kPolicyUnroll * width) {
         copy_wait<kDepth - 1>();
-        if (base + (kUnroll - 1) * width < n) {
-            uint4 v[kUnroll];
+        if (base + (kPolicyUnroll - 1) * width < n) {
+            uint4 v[kPolicyUnroll];
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) v[u] = slice[base + u * width];
+            for (int u = 0; u < kPolicyUnroll; ++u) v[u] = slice[base + u * width];
             absorb<DT, ENT>(o, v, c);
         } else {
             for (int i = base; i < n; i += width) {
@@ -329,7 +333,7 @@ policy_rows_kernel(Rows logits, Rows grad, Tokens tokens, int cols, float scale,
         }
         ask();
     }
-    o = group_join<ENT, WARP>(o, c);
+    o = group_join<ENT, WARP, kPolicyThreads>(o, c);
 
     RowStats rs = row_stats<ENT>(o);
     if (bad) rs.m = rs.s = rs.log_s = rs.entropy = __int_as_float(0x7fc00000);
@@ -345,7 +349,7 @@ policy_rows_kernel(Rows logits, Rows grad, Tokens tokens, int cols, float scale,
     }
     const Gradient G(rs.m, rs.s, rs.log_s, c, scale * w * k.grad, ENT ? -scale * w * P.entropy_coef : 0.0f,
                      rs.entropy);
-    grad_vectors<DT, ENT, kUnroll>(G, [slice](int i) { return slice[i]; }, n, lane, width, out, vector_out,
+    grad_vectors<DT, ENT, kPolicyUnroll>(G, [slice](int i) { return slice[i]; }, n, lane, width, out, vector_out,
                                    sp.head + first * E::kVec);
     if (extra >= 0) E::store(out, extra, G.of<ENT>(xe));
     grad_target<DT, ENT>(G, out, sp, t, xt, first, end, lane, width, extra);
@@ -429,11 +433,14 @@ bool good_scale(float s) { return s > 0.0f && std::isfinite(s * kLog2e); }
 
 // CTAs per row: one where there are rows enough to keep the GPU busy, else up
 // to eight, each with at least two turns of its threads' vectors.
-int cluster_for(int64_t rows, int64_t vecs, int at_least) {
+int cluster_for(int64_t rows, int64_t vecs, int threads, int at_least) {
     int c = at_least;
-    while (c < kMaxCluster && rows * c < kBusyCtas && vecs >= int64_t(2) * c * 2 * kThreads) c *= 2;
+    while (c < kMaxCluster && rows * c < kBusyCtas && vecs >= int64_t(2) * c * 2 * threads) c *= 2;
     return c;
 }
+
+// The grid of the warp form: a row to each warp.
+uint32_t warp_grid(uint32_t rows, int threads) { return (rows + uint32_t(threads / 32) - 1) / uint32_t(threads / 32); }
 
 uint32_t grid_of(int64_t groups) { return groups > 0 && groups <= kMaxCount ? uint32_t(groups) : 0; }
 
@@ -444,14 +451,14 @@ cudaError_t forward(const adamw_rows_t* x, const int64_t* targets, int64_t ignor
     const uint32_t n = uint32_t(x->rows);
     if (x->cols <= kWarpCols) {
         auto k = entropy ? logprob_kernel<DT, true, true> : logprob_kernel<DT, false, true>;
-        return launch(k, (n + kWarps - 1) / kWarps, kThreads, 1, 0, st, rows, n, x->cols, targets, ignore,
+        return launch(k, warp_grid(n, kForwardThreads), kForwardThreads, 1, 0, st, rows, n, x->cols, targets, ignore,
                       scale, logp, entropy, stats);
     }
-    const int c = cluster_for(x->rows, x->cols / Elem<DT>::kVec, 1);
+    const int c = cluster_for(x->rows, x->cols / Elem<DT>::kVec, kForwardThreads, 1);
     auto k = entropy ? logprob_kernel<DT, true, false> : logprob_kernel<DT, false, false>;
     const uint32_t grid = grid_of(x->rows * c);
     if (!grid) return cudaErrorInvalidConfiguration;
-    return launch(k, grid, kThreads, c, 0, st, rows, n, x->cols, targets, ignore, scale, logp, entropy, stats);
+    return launch(k, grid, kForwardThreads, c, 0, st, rows, n, x->cols, targets, ignore, scale, logp, entropy, stats);
 }
 
 template <int DT>
@@ -462,15 +469,16 @@ cudaError_t backward(const adamw_rows_t* x, const int64_t* targets, float scale,
     const uint32_t n = uint32_t(x->rows);
     if (x->cols <= kWarpCols) {
         auto k = d_entropy ? logprob_backward_kernel<DT, true, true> : logprob_backward_kernel<DT, false, true>;
-        return launch(k, (n + kWarps - 1) / kWarps, kThreads, 1, 0, st, in, out, n, 1u, x->cols, targets,
+        return launch(k, warp_grid(n, kBackwardThreads), kBackwardThreads, 1, 0, st, in, out, n, 1u, x->cols, targets,
                       scale, stats, entropy, d_logp, d_entropy);
     }
-    const int64_t per = int64_t(kThreads) * kUnroll * Elem<DT>::kVec;
+    // two turns of its threads' vectors to a piece
+    const int64_t per = 2 * int64_t(kBackwardThreads) * kBackwardUnroll * Elem<DT>::kVec;
     const uint32_t pieces = uint32_t((x->cols + per - 1) / per);
     auto k = d_entropy ? logprob_backward_kernel<DT, true, false> : logprob_backward_kernel<DT, false, false>;
     const uint32_t grid = grid_of(x->rows * pieces);
     if (!grid) return cudaErrorInvalidConfiguration;
-    return launch(k, grid, kThreads, 1, 0, st, in, out, n, pieces, x->cols, targets, scale, stats, entropy,
+    return launch(k, grid, kBackwardThreads, 1, 0, st, in, out, n, pieces, x->cols, targets, scale, stats, entropy,
                   d_logp, d_entropy);
 }
 
@@ -497,9 +505,9 @@ cudaError_t policy_rows(const adamw_rows_t* x, const adamw_rows_t* dx, const Tok
     const Rows in = rows_of(x), out = rows_of(dx);
     const int64_t vecs = x->cols / Elem<DT>::kVec;
     if (x->cols <= kWarpCols) {
-        // a CTA's eight rows: at most 8 * 1024 * 4 bytes
-        return launch(policy_rows_kernel<DT, ENT, true>, (tokens.n + kWarps - 1) / kWarps, kThreads, 1,
-                      size_t(vecs) * 16 * kWarps, st, in, out, tokens, x->cols, scale, P, a);
+        // a CTA's rows: at most 1024 * 4 bytes each
+        return launch(policy_rows_kernel<DT, ENT, true>, warp_grid(tokens.n, kPolicyThreads), kPolicyThreads, 1,
+                      size_t(vecs) * 16 * (kPolicyThreads / 32), st, in, out, tokens, x->cols, scale, P, a);
     }
     auto k = policy_rows_kernel<DT, ENT, false>;
     static std::atomic<uint64_t> done{0};
@@ -507,10 +515,10 @@ cudaError_t policy_rows(const adamw_rows_t* x, const adamw_rows_t* dx, const Tok
     if (e != cudaSuccess) return e;
     int c = 1;
     while (c < kMaxCluster && (vecs + c - 1) / c * 16 > kWantSmem) c *= 2;
-    c = cluster_for(x->rows, vecs, c);
+    c = cluster_for(x->rows, vecs, kPolicyThreads, c);
     const uint32_t grid = grid_of(x->rows * c);
     if (!grid) return cudaErrorInvalidConfiguration;
-    return launch(k, grid, kThreads, c, size_t((vecs + c - 1) / c) * 16, st, in, out, tokens, x->cols,
+    return launch(k, grid, kPolicyThreads, c, size_t((vecs + c - 1) / c) * 16, st, in, out, tokens, x->cols,
                   scale, P, a);
 }
 
