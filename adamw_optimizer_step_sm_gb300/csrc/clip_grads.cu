@@ -5,6 +5,7 @@
 // after the last element, read again to be scaled (a list that fits the
 // 129 MB L2 comes from there the second time).
 #include <new>
+#include <type_traits>
 #include <vector>
 
 #include "losses_common.cuh"
@@ -30,13 +31,10 @@ struct alignas(16) Tile {
 };
 static_assert(sizeof(Tile) == 32, "tile layout");
 
-// The coefficient in two factors, the second a power of two: a coefficient
-// below fp32's normal range (a norm above 1e38 times the limit) keeps its
-// digits in the first.  {1, 1} when nothing is scaled.
-struct ClipState {
-    uint32_t ticket;
-    int32_t pad_;
-    float2 coef;
+// One CTA's part of the norm: the value x 2^exponent.  The exponent is 0 but
+// for sums that leave fp32's range.
+struct Partial {
+    float x, exponent;
 };
 
 // The squares of one thread's elements.  Groups of elements are summed in
@@ -135,91 +133,153 @@ __device__ __forceinline__ void norm_tile(const Tile& t, Acc& acc) {
     for (int i = done + threadIdx.x; i < t.len; i += kThreads) acc.add(E::load(t.src, i));
 }
 
-template <bool MAX>
-struct NormOf;
-template <>
-struct NormOf<false> {
-    using Acc = SquareSum;
-    __device__ static double value(const Acc& a) { return double(a.sum.hi) + double(a.sum.lo) + a.rare; }
-    __device__ static double join(double a, double b) { return a + b; }
-    __device__ static double norm(double a) { return sqrt(a); }
-};
-template <>
-struct NormOf<true> {
-    using Acc = MaxBits;
-    __device__ static double value(const Acc& a) { return double(__uint_as_float(a.bits)); }
-    __device__ static double join(double a, double b) { return a != a || a > b ? a : b; }
-    __device__ static double norm(double a) { return a; }
-};
+// The larger of two magnitudes, NaN above infinity.
+__device__ __forceinline__ float larger(float a, float b) {
+    return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
+}
 
-// The CTA's joined value, in thread 0.
+// The CTA's joined value, in every thread: a tree in fp32 (eight roundings of
+// a CTA's value; the CTAs' own average out in the total).
 template <bool MAX>
-__device__ __forceinline__ double cta_join(double v) {
-    using N = NormOf<MAX>;
-    __shared__ double part[kWarps];
+__device__ __forceinline__ float cta_join(float v, float* part) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v = N::join(v, __shfl_down_sync(0xffffffffu, v, d));
+    for (int d = 16; d > 0; d >>= 1) {
+        const float o = __shfl_xor_sync(0xffffffffu, v, d);
+        v = MAX ? larger(v, o) : v + o;
+    }
     if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
     __syncthreads();
-    if (threadIdx.x == 0)
-        for (int w = 1; w < kWarps; ++w) v = N::join(v, part[w]);
+    v = part[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) v = MAX ? larger(v, part[w]) : v + part[w];
     return v;
 }
 
-// The norm: tiles dealt round-robin to a resident grid, each CTA's value left
-// in partial[]; the last CTA to finish joins them in order and writes the
-// result.
+__device__ __forceinline__ Partial cta_value(const MaxBits& a) {
+    __shared__ float part[kWarps];
+    return {cta_join<true>(__uint_as_float(a.bits), part), 0.0f};
+}
+__device__ __forceinline__ Partial cta_value(const SquareSum& a) {
+    __shared__ float part[kWarps];
+    const bool rare = __syncthreads_or(a.rare != 0.0);
+    if (!rare) return {cta_join<false>(a.sum.value(), part), 0.0f};
+    __shared__ double wide[kThreads];
+    wide[threadIdx.x] = double(a.sum.hi) + double(a.sum.lo) + a.rare;
+    __syncthreads();
+    double v = 0.0;
+    if (threadIdx.x == 0)
+        for (int k = 0; k < kThreads; ++k) v += wide[k];
+    if (!isfinite(v)) return {float(v), 0.0f};
+    int e;
+    const double m = frexp(v, &e);
+    return {float(m), float(e)};
+}
+
+// The norm's partial values: tiles dealt round-robin to a resident grid.  The
+// next kernel may start once every CTA here has passed its wait, so it may
+// read what this one reads before its own.
 template <bool MAX>
 __global__ void __launch_bounds__(kThreads, 4)
-grad_norm_kernel(const Tile* tiles, int32_t n, float max_norm, double* partial, ClipState* state,
-                 adamw_clip_result_t* result) {
-    using N = NormOf<MAX>;
-    dependency_trigger();
+grad_norm_kernel(const Tile* tiles, int32_t n, Partial* partial) {
+    Tile t = {};
+    if (int32_t(blockIdx.x) < n) t = tiles[blockIdx.x];
     dependency_wait();
-    typename N::Acc acc = {};
+    dependency_trigger();
+    typename std::conditional<MAX, MaxBits, SquareSum>::type acc = {};
     for (int32_t k = blockIdx.x; k < n; k += gridDim.x) {
-        const Tile t = tiles[k];
+        if (k != int32_t(blockIdx.x)) t = tiles[k];
         switch (t.src_type) {
             case ADAMW_DTYPE_BF16: norm_tile<ADAMW_DTYPE_BF16>(t, acc); break;
             case ADAMW_DTYPE_FP16: norm_tile<ADAMW_DTYPE_FP16>(t, acc); break;
             default: norm_tile<ADAMW_DTYPE_FP32>(t, acc); break;
         }
     }
-    __shared__ bool last;
-    double v = cta_join<MAX>(N::value(acc));
+    const Partial p = cta_value(acc);
+    if (threadIdx.x == 0) partial[blockIdx.x] = p;
+}
+
+// What a call's later kernels need of the norm.
+struct Clip {
+    const Partial* partial;
+    int32_t n;
+    int32_t max;   // ADAMW_NORM_MAX
+    float max_norm;
+    adamw_clip_result_t* result;   // NULL: another kernel of the call writes it
+};
+
+// Joins the partial values in their order, the same in every CTA, and gives
+// the coefficient in two factors, the second a power of two: a coefficient
+// below fp32's normal range (a norm above 1e38 times the limit) keeps its
+// digits in the first.  {1, 1} when nothing is scaled.
+__device__ __forceinline__ float2 clip_coefficient(const Clip& c) {
+    __shared__ Sum2 part[kWarps];
+    __shared__ float2 coef;
+    Sum2 s = {};
+    float top = 0.0f;
+    bool wide = false;
+    for (int32_t k = threadIdx.x; k < c.n; k += kThreads) {
+        const Partial p = c.partial[k];
+        s.add(p.x);
+        top = larger(top, p.x);
+        wide |= p.exponent != 0.0f;
+    }
+    if (c.max) s = {top, 0.0f};
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        const float h = __shfl_down_sync(0xffffffffu, s.hi, d), l = __shfl_down_sync(0xffffffffu, s.lo, d);
+        if (c.max) s.hi = larger(s.hi, h); else s.join(h, l);
+    }
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = s;
+    wide = __syncthreads_or(wide);
     if (threadIdx.x == 0) {
-        partial[blockIdx.x] = v;
-        __threadfence();
-        last = atomicAdd(&state->ticket, 1) == gridDim.x - 1;
+        for (int w = 1; w < kWarps; ++w) {
+            if (c.max) s.hi = larger(s.hi, part[w].hi); else s.join(part[w].hi, part[w].lo);
+        }
+        const float v = c.max ? s.hi : s.value();
+        adamw_clip_result_t r = {0.0f, 1.0f, 0, 0};
+        float2 two = make_float2(1.0f, 1.0f);
+        bool done = false;
+        if (!wide && (v == 0.0f || (v > 1e-30f && v < 1e30f))) {
+            r.norm = c.max ? v : sqrtf(v);
+            const float q = c.max_norm / (r.norm + 1e-6f);
+            r.coef = two.x = q < 1.0f ? q : 1.0f;
+            done = r.coef >= 0x1p-100f;
+        }
+        if (!done) {  // out of fp32's reach
+            double sum = v;
+            if (!c.max) {
+                sum = 0.0;
+                for (int32_t k = 0; k < c.n; ++k)
+                    sum += ldexp(double(c.partial[k].x), int(c.partial[k].exponent));
+                sum = sqrt(sum);
+            }
+            const double q = double(c.max_norm) / (sum + 1e-6);
+            r.norm = float(sum);
+            r.nonfinite = isfinite(sum) ? 0 : 1;
+            const bool scaled = isfinite(sum) && q < 1.0;
+            r.coef = scaled ? float(q) : 1.0f;
+            two = scaled && q < 0x1p-100 ? make_float2(float(q * 0x1p64), 0x1p-64f) : make_float2(r.coef, 1.0f);
+        }
+        coef = two;
+        if (c.result && blockIdx.x == 0) *c.result = r;
     }
     __syncthreads();
-    if (!last) return;
-    __threadfence();
-    v = 0.0;
-    for (uint32_t b = threadIdx.x; b < gridDim.x; b += kThreads) v = N::join(v, __ldcg(&partial[b]));
-    v = cta_join<MAX>(v);
-    if (threadIdx.x == 0) {
-        const double norm = N::norm(v);
-        const bool finite = isfinite(norm);
-        const double coef = double(max_norm) / (norm + 1e-6);
-        adamw_clip_result_t r;
-        r.norm = float(norm);
-        r.coef = finite && coef < 1.0 ? float(coef) : 1.0f;
-        r.nonfinite = finite ? 0 : 1;
-        r.pad_ = 0;
-        *result = r;
-        const bool tiny = r.coef < 0x1p-100f;   // by at most 2^-160 or so
-        state->coef = make_float2(tiny ? float(coef * 0x1p64) : r.coef, tiny ? 0x1p-64f : 1.0f);
-        state->ticket = 0;
-    }
+    return coef;
+}
+
+__global__ void __launch_bounds__(kThreads) clip_result_kernel(Clip clip) {
+    dependency_trigger();
+    dependency_wait();
+    clip_coefficient(clip);
 }
 
 // dst = coef * src for the tiles [first, first + n), all of the kernel's pair
 // of types.  In reverse: those that the norm pass read last are the likeliest
 // to be in L2 still.
+// A CTA's first loads go out before it waits for the norm.
 template <int SRC, int DST>
 __global__ void __launch_bounds__(kThreads, 4)
-grad_scale_kernel(const Tile* tiles, int32_t n, const ClipState* state) {
+grad_scale_kernel(const Tile* tiles, int32_t n, Clip clip) {
     using S = Elem<SRC>;
     using D = Elem<DST>;
     // elements per step: whole 16-byte vectors on both sides
@@ -227,48 +287,53 @@ grad_scale_kernel(const Tile* tiles, int32_t n, const ClipState* state) {
     constexpr int kIn = K / S::kVec, kOut = K / D::kVec;
     constexpr int U = kScaleVecs / kIn;
     dependency_trigger();
-    dependency_wait();
-    const float2 coef = state->coef;
-    auto scaled = [&](uint4 (&v)[kIn], char* dst) {
-        float x[K];
+    uint4 v[U][kIn];
+    auto load = [&](const Tile& t, int base, int steps) {
 #pragma unroll
-        for (int j = 0; j < kIn; ++j) S::unpack(v[j], x + j * S::kVec);
+        for (int u = 0; u < U; ++u)
+            if (base + u * kThreads < steps) {
 #pragma unroll
-        for (int j = 0; j < K; ++j) x[j] = x[j] * coef.x * coef.y;
-#pragma unroll
-        for (int j = 0; j < kOut; ++j) store16(dst + j * 16, D::pack(x + j * D::kVec));
+                for (int j = 0; j < kIn; ++j) v[u][j] = load16(t.src + ((base + u * kThreads) * kIn + j) * 16);
+            }
     };
-    for (int32_t k = n - 1 - int32_t(blockIdx.x); k >= 0; k -= gridDim.x) {
-        const Tile t = tiles[k];
-        if (coef.x == 1.0f && t.dst == t.src) continue;
-        int done = 0;
-        if (t.vector) {
-            const int steps = t.len / K;
-            int base = threadIdx.x;
-            for (; base + (U - 1) * kThreads < steps; base += U * kThreads) {
-                uint4 v[U][kIn];
+    int32_t k = n - 1 - int32_t(blockIdx.x);   // the grid is at most n
+    Tile t = tiles[k];
+    if (t.vector) load(t, threadIdx.x, t.len / K);
+    dependency_wait();
+    const float2 coef = clip_coefficient(clip);
+    for (bool loaded = true;; loaded = false) {
+        if (coef.x != 1.0f || t.dst != t.src) {
+            int done = 0;
+            if (t.vector) {
+                const int steps = t.len / K;
+                for (int base = threadIdx.x; base < steps; base += U * kThreads) {
+                    if (!loaded) load(t, base, steps);
+                    loaded = false;
 #pragma unroll
-                for (int u = 0; u < U; ++u)
+                    for (int u = 0; u < U; ++u) {
+                        if (base + u * kThreads >= steps) break;
+                        float x[K];
 #pragma unroll
-                    for (int j = 0; j < kIn; ++j)
-                        v[u][j] = load16(t.src + ((base + u * kThreads) * kIn + j) * 16);
+                        for (int j = 0; j < kIn; ++j) S::unpack(v[u][j], x + j * S::kVec);
 #pragma unroll
-                for (int u = 0; u < U; ++u) scaled(v[u], t.dst + (base + u * kThreads) * kOut * 16);
+                        for (int j = 0; j < K; ++j) x[j] = x[j] * coef.x * coef.y;
+#pragma unroll
+                        for (int j = 0; j < kOut; ++j)
+                            store16(t.dst + ((base + u * kThreads) * kOut + j) * 16, D::pack(x + j * D::kVec));
+                    }
+                }
+                done = steps * K;
             }
-            for (; base < steps; base += kThreads) {
-                uint4 v[kIn];
-#pragma unroll
-                for (int j = 0; j < kIn; ++j) v[j] = load16(t.src + (base * kIn + j) * 16);
-                scaled(v, t.dst + base * kOut * 16);
-            }
-            done = steps * K;
+            for (int i = done + threadIdx.x; i < t.len; i += kThreads)
+                D::store(t.dst, i, S::load(t.src, i) * coef.x * coef.y);
         }
-        for (int i = done + threadIdx.x; i < t.len; i += kThreads)
-            D::store(t.dst, i, S::load(t.src, i) * coef.x * coef.y);
+        k -= int32_t(gridDim.x);
+        if (k < 0) return;
+        t = tiles[k];
     }
 }
 
-using ScaleKernel = void (*)(const Tile*, int32_t, const ClipState*);
+using ScaleKernel = void (*)(const Tile*, int32_t, Clip);
 
 template <int SRC>
 ScaleKernel scale_kernel(int32_t dst) {
@@ -350,10 +415,9 @@ struct adamw_clip_plan {
         int32_t first, n, grid;
     };
     std::vector<Group> groups;
-    void* block = nullptr;           // tiles, then partials, then the state
+    void* block = nullptr;           // tiles, then partial values
     Tile* tiles = nullptr;
-    double* partial = nullptr;
-    ClipState* state = nullptr;
+    Partial* partial = nullptr;
 };
 
 namespace {
@@ -415,13 +479,11 @@ int create(const adamw_grad_t* table, int32_t n, adamw_clip_plan* P) {
         P->norm_grid[k] = int32_t(g < P->n_tiles ? g : P->n_tiles > 0 ? P->n_tiles : 1);
     }
     const size_t tile_bytes = sizeof(Tile) * tiles.size();
-    if (!launched(cudaMalloc(&P->block, tile_bytes + kMaxGrid * sizeof(double) + sizeof(ClipState)), "cudaMalloc"))
+    if (!launched(cudaMalloc(&P->block, tile_bytes + kMaxGrid * sizeof(Partial)), "cudaMalloc"))
         return ADAMW_ERR_CUDA;
     P->tiles = static_cast<Tile*>(P->block);
-    P->partial = reinterpret_cast<double*>(static_cast<char*>(P->block) + tile_bytes);
-    P->state = reinterpret_cast<ClipState*>(P->partial + kMaxGrid);
+    P->partial = reinterpret_cast<Partial*>(static_cast<char*>(P->block) + tile_bytes);
     const bool ok = (tiles.empty() || launched(cudaMemcpy(P->tiles, tiles.data(), tile_bytes, cudaMemcpyHostToDevice), "cudaMemcpy(tiles)")) &&
-                    launched(cudaMemset(P->state, 0, sizeof(ClipState)), "cudaMemset") &&
                     launched(cudaStreamSynchronize(nullptr), "cudaStreamSynchronize");
     return ok ? ADAMW_OK : ADAMW_ERR_CUDA;
 }
@@ -461,14 +523,20 @@ extern "C" int adamw_clip_grads(adamw_clip_plan_t plan, float max_norm, int32_t 
         return ADAMW_ERR_CUDA;
     }
     auto kernel = norm == ADAMW_NORM_MAX ? grad_norm_kernel<true> : grad_norm_kernel<false>;
-    if (!launched(launch(kernel, uint32_t(plan->norm_grid[norm]), kThreads, 1, 0, st, static_cast<const Tile*>(plan->tiles), plan->n_tiles,
-                         max_norm, plan->partial, plan->state, result), "grad_norm launch"))
+    const int32_t grid = plan->norm_grid[norm];
+    if (!launched(launch(kernel, uint32_t(grid), kThreads, 1, 0, st, static_cast<const Tile*>(plan->tiles),
+                         plan->n_tiles, plan->partial), "grad_norm launch"))
         return ADAMW_ERR_CUDA;
-    for (auto g = plan->groups.rbegin(); g != plan->groups.rend(); ++g)
+    Clip clip = {plan->partial, grid, norm, max_norm, result};
+    if (plan->groups.empty())
+        return launched(launch(clip_result_kernel, 1u, kThreads, 1, 0, st, clip), "clip_result launch")
+                   ? ADAMW_OK : ADAMW_ERR_CUDA;
+    for (auto g = plan->groups.rbegin(); g != plan->groups.rend(); ++g) {
         if (!launched(launch(g->kernel, uint32_t(g->grid), kThreads, 1, 0, st,
-                             static_cast<const Tile*>(plan->tiles + g->first), g->n,
-                             static_cast<const ClipState*>(plan->state)), "grad_scale launch"))
+                             static_cast<const Tile*>(plan->tiles + g->first), g->n, clip), "grad_scale launch"))
             return ADAMW_ERR_CUDA;
+        clip.result = nullptr;   // written
+    }
     return ADAMW_OK;
 }
 

@@ -531,22 +531,11 @@ struct Tokens {
         return int64_t(i) >= offsets[lo] && int64_t(i) < offsets[lo + 1] ? int32_t(lo) : -1;
     }
 
-    // The sequences of the N tokens from `first` on, for every lane of a warp
-    // whose lane 0 starts at `base` and which covers [base, base + 32 N).
-    // Called by whole warps.
-    template <int N>
-    __device__ __forceinline__ void sequences_of(uint32_t base, uint32_t first, int32_t (&seq)[N]) const {
-        if (!offsets) {
-            uint32_t q = first / length, r = first - q * length;
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                seq[j] = int32_t(q);
-                if (++r == length) { r = 0; ++q; }
-            }
-            return;
-        }
-        // how many of the sequences + 1 offsets are <= base: each round the
-        // lanes probe 32 points of what is left, so 2048 take three loads
+    // How many of the sequences + 1 offsets are at or before token `base`, the
+    // same for a whole warp, which calls together: each round the lanes probe
+    // 32 points of what is left, so 2048 offsets take three loads.
+    __device__ __forceinline__ uint32_t starts_until(uint32_t base) const {
+        if (!offsets) return 0;
         const uint32_t lane = threadIdx.x % 32;
         uint32_t lo = 0, hi = sequences + 1;  // offsets[0, lo) <= base < offsets[hi, ..)
         while (lo < hi) {
@@ -560,8 +549,25 @@ struct Tokens {
             lo = lo + (k - 1) * step + 1;
             hi = next < hi ? next : hi;
         }
+        return lo;
+    }
+
+    // The sequences of the N tokens from `first` on, for every lane of a warp
+    // that covers [base, base + 32 N), with lo = starts_until(base).  Called
+    // by whole warps.
+    template <int N>
+    __device__ __forceinline__ void sequences_of(uint32_t lo, uint32_t base, uint32_t first, int32_t (&seq)[N]) const {
+        if (!offsets) {
+            uint32_t q = first / length, r = first - q * length;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                seq[j] = int32_t(q);
+                if (++r == length) { r = 0; ++q; }
+            }
+            return;
+        }
         // the offsets inside the warp's tokens, in the lanes
-        const uint32_t at = lo + lane;
+        const uint32_t at = lo + threadIdx.x % 32;
         const int64_t past = int64_t(base) + 32 * N;
         const int64_t mine = at <= sequences ? offsets[at] : past;
         const int count = __popc(__ballot_sync(0xffffffffu, mine < past));
@@ -664,13 +670,16 @@ __device__ __forceinline__ PolicyToken policy_token(const Policy& P, float logp,
                                                     float ref, float A) {
     PolicyToken o;
     const float d = logp - old;
-    const float r = expf(d);
-    const float rc = d > P.d_high ? P.r_high : d < P.d_low ? P.r_low : r;
-    const bool capped = A < 0.0f && d > P.d_dual;
-    const bool off = capped || (A > 0.0f && d > P.d_high) || (A < 0.0f && d < P.d_low);
-    // fmaxf would drop a NaN: the two agree in their NaN (both hold A, r)
-    const float u = -A * r, v = -A * rc;
-    o.pg = capped ? -A * P.dual : (u < v ? v : u);
+    const float r = exp2_fast(d * kLog2e);
+    // Outside [low, high] the clipped branch holds; inside, -A r is the larger
+    // of the two: where r is past a limit there, it is past it on the side
+    // that makes -A r larger.
+    const bool up = A > 0.0f;
+    const float high = up ? P.d_high : P.d_dual, low = up ? -kInf : P.d_low;
+    const bool off = A != 0.0f && (d > high || d < low);
+    const float bound = up ? P.r_high : d < low ? P.r_low : P.dual;
+    const float u = -A * r;
+    o.pg = off ? -A * bound : u;
     o.off = off ? 1.0f : 0.0f;
     o.old_kl = exp_beyond_linear(d, r);
     o.grad = off ? 0.0f : u;
@@ -685,7 +694,7 @@ __device__ __forceinline__ PolicyToken policy_token(const Policy& P, float logp,
             o.kl = 0.5f * k * k;
             dk = k;
         } else {
-            o.kl = exp_beyond_linear(-k, expf(-k));
+            o.kl = exp_beyond_linear(-k, exp2_fast(-k * kLog2e));
             dk = k - o.kl;   // 1 - exp(-k)
         }
         // without a coefficient the estimate is reported only, and a

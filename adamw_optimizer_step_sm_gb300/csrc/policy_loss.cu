@@ -13,7 +13,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kPerLane = 4;    // consecutive tokens of a lane
 constexpr int kChunk = 32 * kPerLane;  // and of a warp
 constexpr int kMaxGrid = 1216; // 8 CTAs for each of 152 SMs
-constexpr int kCountGrid = 608;
+constexpr int kCountGrid = 1216;
 constexpr int kSums = 5;       // pg, KL, entropy, clipped, old KL
 
 uint32_t token_grid(int64_t n, int64_t most) {
@@ -32,11 +32,16 @@ uint32_t cluster_ctas(int64_t n) {
     return c;
 }
 
+// The workspace: the counts; and unless one cluster does the call, the starts
+// of the warps' tokens and the CTAs' sums.
 int64_t counts_bytes(int64_t sequences) { return (16 + 4 * sequences + 15) / 16 * 16; }
+int64_t starts_bytes(int64_t n) { return ((n + kChunk - 1) / kChunk * 4 + 15) / 16 * 16; }
 
 // Counts tokens by sequence (integers: any order gives the same), CTA `cta`
-// of `ctas`.  A warp takes 128 consecutive tokens, four to a lane.
-__device__ __forceinline__ void count_tokens(const Tokens& t, Counts* out, uint32_t cta, uint32_t ctas) {
+// of `ctas`.  A warp takes 128 consecutive tokens, four to a lane, and leaves
+// what it found of their sequences in starts[] (NULL: nowhere).
+__device__ __forceinline__ void count_tokens(const Tokens& t, Counts* out, uint32_t* starts, uint32_t cta,
+                                             uint32_t ctas) {
     const uint32_t lane = threadIdx.x % 32;
     uint32_t tokens = 0, filled = 0;
     const uint64_t step = uint64_t(ctas) * kWarps * kChunk;
@@ -44,7 +49,9 @@ __device__ __forceinline__ void count_tokens(const Tokens& t, Counts* out, uint3
         const uint32_t base = uint32_t(at), first = base + lane * kPerLane;
         uint32_t bits = t.counting<kPerLane>(first);
         int32_t seq[kPerLane];
-        t.sequences_of<kPerLane>(base, first, seq);
+        const uint32_t lo = t.starts_until(base);
+        if (starts && lane == 0) starts[base / kChunk] = lo;
+        t.sequences_of<kPerLane>(lo, base, first, seq);
         // run by run of the lane's tokens; one atomic where the whole warp is
         // in one sequence
         const int32_t s0 = __shfl_sync(0xffffffffu, seq[0], 0);
@@ -93,10 +100,10 @@ __device__ __forceinline__ void count_tokens(const Tokens& t, Counts* out, uint3
     }
 }
 
-__global__ void __launch_bounds__(kThreads) count_kernel(Tokens t, Counts* out) {
+__global__ void __launch_bounds__(kThreads) count_kernel(Tokens t, Counts* out, uint32_t* starts) {
     dependency_trigger();
     dependency_wait();
-    count_tokens(t, out, blockIdx.x, gridDim.x);
+    count_tokens(t, out, starts, blockIdx.x, gridDim.x);
 }
 
 // The same by one cluster, which zeroes the counts first.
@@ -105,7 +112,7 @@ __device__ __forceinline__ void count_in_cluster(const Tokens& t, Counts* out, u
     const uint32_t n = 4 + t.sequences;
     for (uint32_t i = rank * kThreads + threadIdx.x; i < n; i += size * kThreads) words[i] = 0;
     cluster_sync();
-    count_tokens(t, out, rank, size);
+    count_tokens(t, out, nullptr, rank, size);
     cluster_sync();
 }
 __global__ void __launch_bounds__(kThreads) count_cluster_kernel(Tokens t, Counts* out) {
@@ -145,11 +152,11 @@ __device__ __forceinline__ void store4(float* p, uint32_t first, uint32_t n, boo
 
 // Loss terms and gradients of CTA `cta` of `ctas`, 128 tokens to a warp: a
 // lane's loads are all on their way before it looks for its tokens'
-// sequences.  Threads below kSums return the CTA's sums.  aligned: every
+// sequences (from starts[], where the count left them).  Threads below kSums return the CTA's sums.  aligned: every
 // array is 16-byte aligned.
 __device__ __forceinline__ Sum2 policy_tokens(const Tokens& t, const Policy& P, const PolicyTokens& a,
-                                              const Counts* counts, uint32_t tokens, uint32_t filled,
-                                              bool aligned, uint32_t cta, uint32_t ctas) {
+                                              const Counts* counts, const uint32_t* starts,
+                                              uint32_t tokens, uint32_t filled, bool aligned, uint32_t cta, uint32_t ctas) {
     const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     Sum2 sum[kSums] = {};
     const uint64_t step = uint64_t(ctas) * kWarps * kChunk;
@@ -164,18 +171,32 @@ __device__ __forceinline__ Sum2 policy_tokens(const Tokens& t, const Policy& P, 
         if (P.per_token) load4(a.advantages, first, t.n, vector, adv);
         const uint32_t bits = t.counting<kPerLane>(first);
         int32_t seq[kPerLane];
-        t.sequences_of<kPerLane>(base, first, seq);
+        t.sequences_of<kPerLane>(starts ? starts[base / kChunk] : t.starts_until(base), base, first, seq);
+        // the weights and advantages of the lane's sequences, mostly one
+        float weight[kPerLane], value[kPerLane];
+        const bool one = __all_sync(0xffffffffu, seq[0] == seq[kPerLane - 1]);
+#pragma unroll
+        for (int j = 0; j < kPerLane; ++j) {
+            if (j > 0 && one) {
+                weight[j] = weight[0];
+                value[j] = value[0];
+                continue;
+            }
+            const bool in = seq[j] >= 0 && first + j < t.n;
+            const uint32_t q = in ? uint32_t(seq[j]) : 0u;
+            const uint32_t count = P.reduce == ADAMW_REDUCE_SEQUENCE && in ? __ldcg(&counts->sequence[q]) : 1u;
+            weight[j] = token_weight(P.reduce, P.inv_divisor, tokens, filled, count);
+            value[j] = !P.per_token && in ? a.advantages[q] : 0.0f;
+        }
         float g[kPerLane], gh[kPerLane], v[kSums] = {};
         // every token alike, whether it counts or not: its results are then
         // taken or left, never multiplied (they may be anything)
 #pragma unroll
         for (int j = 0; j < kPerLane; ++j) {
             const bool on = (bits >> j & 1) && seq[j] >= 0;
-            const uint32_t q = on ? uint32_t(seq[j]) : 0u;
-            const uint32_t in_sequence = P.reduce == ADAMW_REDUCE_SEQUENCE && on ? __ldcg(&counts->sequence[q]) : 1u;
-            const float w = on ? token_weight(P.reduce, P.inv_divisor, tokens, filled, in_sequence) : 0.0f;
-            const float A = P.per_token ? adv[j] : on ? a.advantages[q] : 0.0f;
-            const PolicyToken k = policy_token(P, logp[j], old[j], a.ref_logp != nullptr, ref[j], A);
+            const float w = on ? weight[j] : 0.0f;
+            const PolicyToken k = policy_token(P, logp[j], old[j], a.ref_logp != nullptr, ref[j],
+                                               P.per_token ? adv[j] : value[j]);
             v[0] = fmaf(w, on ? k.pg : 0.0f, v[0]);
             v[1] = fmaf(w, on ? k.kl : 0.0f, v[1]);
             v[2] = fmaf(w, on ? ent[j] : 0.0f, v[2]);
@@ -220,12 +241,13 @@ __device__ __forceinline__ void policy_result(const Policy& P, const PolicyToken
 // Over a grid: each CTA leaves its five sums and the last one to finish adds
 // them up in the CTAs' order.
 __global__ void __launch_bounds__(kThreads)
-policy_kernel(Tokens t, Policy P, PolicyTokens a, Counts* counts, float2* partial, bool aligned) {
+policy_kernel(Tokens t, Policy P, PolicyTokens a, Counts* counts, const uint32_t* starts, float2* partial,
+              bool aligned) {
     dependency_trigger();
     dependency_wait();
     const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const uint32_t tokens = counts->tokens, filled = counts->filled;
-    const Sum2 mine = policy_tokens(t, P, a, counts, tokens, filled, aligned, blockIdx.x, gridDim.x);
+    const Sum2 mine = policy_tokens(t, P, a, counts, starts, tokens, filled, aligned, blockIdx.x, gridDim.x);
     __shared__ bool last;
     if (threadIdx.x < kSums) {
         partial[blockIdx.x * kSums + threadIdx.x] = make_float2(mine.hi, mine.lo);
@@ -269,7 +291,7 @@ policy_cluster_kernel(Tokens t, Policy P, PolicyTokens a, Counts* counts, bool a
     const uint32_t rank = cluster_rank(), size = cluster_size();
     if (COUNT) count_in_cluster(t, counts, rank, size);
     const uint32_t tokens = __ldcg(&counts->tokens), filled = __ldcg(&counts->filled);
-    const Sum2 mine = policy_tokens(t, P, a, counts, tokens, filled, aligned, rank, size);
+    const Sum2 mine = policy_tokens(t, P, a, counts, nullptr, tokens, filled, aligned, rank, size);
     __shared__ float whole[kSums][2];
     __shared__ float mean[kSums];
     if (threadIdx.x < kSums) {
@@ -566,7 +588,8 @@ int launch_counts(const adamw_tokens_t* t, const int64_t* targets, int64_t ignor
                    ? ADAMW_OK : ADAMW_ERR_CUDA;
     if (!launched(cudaMemsetAsync(c, 0, size_t(counts_bytes(t->sequences)), st), "counts memset"))
         return ADAMW_ERR_CUDA;
-    return launched(launch(count_kernel, token_grid(t->n, kCountGrid), kThreads, 1, 0, st, k, c), "count launch")
+    uint32_t* starts = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + counts_bytes(t->sequences));
+    return launched(launch(count_kernel, token_grid(t->n, kCountGrid), kThreads, 1, 0, st, k, c, starts), "count launch")
                ? ADAMW_OK : ADAMW_ERR_CUDA;
 }
 
@@ -592,9 +615,10 @@ int launch_policy(const adamw_tokens_t* t, const adamw_policy_t* p, const int64_
         const int rc = launch_counts(t, targets, ignore, workspace, st);
         if (rc != ADAMW_OK) return rc;
     }
-    float2* partial = reinterpret_cast<float2*>(static_cast<char*>(workspace) + counts_bytes(t->sequences));
-    return launched(launch(policy_kernel, token_grid(t->n, kMaxGrid), kThreads, 1, 0, st, k, P, a, c, partial,
-                           all_aligned), "policy launch")
+    char* rest = static_cast<char*>(workspace) + counts_bytes(t->sequences);
+    return launched(launch(policy_kernel, token_grid(t->n, kMaxGrid), kThreads, 1, 0, st, k, P, a, c,
+                           reinterpret_cast<const uint32_t*>(rest),
+                           reinterpret_cast<float2*>(rest + starts_bytes(t->n)), all_aligned), "policy launch")
                ? ADAMW_OK : ADAMW_ERR_CUDA;
 }
 
@@ -603,7 +627,7 @@ int launch_policy(const adamw_tokens_t* t, const adamw_policy_t* p, const int64_
 extern "C" int64_t adamw_policy_workspace(int64_t n, int64_t sequences) {
     if (n < 0 || sequences < 0 || n > kMaxCount || sequences > kMaxCount) return 0;
     const adamw_tokens_t t = {n, sequences, nullptr, nullptr};
-    return counts_bytes(sequences) + (in_one_cluster(&t) ? 0 : int64_t(kMaxGrid) * kSums * int64_t(sizeof(float2)));
+    return counts_bytes(sequences) + (in_one_cluster(&t) ? 0 : starts_bytes(n) + int64_t(kMaxGrid) * kSums * int64_t(sizeof(float2)));
 }
 
 extern "C" int adamw_policy_loss(const adamw_tokens_t* tokens, const adamw_policy_t* policy,

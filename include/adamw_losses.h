@@ -219,8 +219,9 @@ int adamw_preference_loss(const adamw_tokens_t* tokens, const adamw_preference_t
 /* One gradient of a list to clip.  src is read; dst receives the clipped
  * gradient, rounded to dst_dtype: another buffer, src itself (in place; then
  * the types must be equal), or NULL (only the norm is wanted).  numel may be
- * 0.  Buffers are aligned to their element size; tensors whose src and dst
- * are 16-byte aligned take 16-byte accesses. */
+ * 0.  Buffers of different entries must not overlap.  They are aligned to
+ * their element size; tensors whose src and dst are 16-byte aligned take
+ * 16-byte accesses. */
 typedef struct {
     const void* src;
     void* dst;
