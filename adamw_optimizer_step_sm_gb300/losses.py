@@ -90,9 +90,9 @@ def _geometry(x: torch.Tensor):
     shape, stride = x.shape, x.stride()
     nd = len(shape)
     if nd == 2:
-        return shape[0], max(1, shape[0]), 0, stride[0]
+        return shape[0], shape[0] or 1, 0, stride[0]
     if nd == 3:
-        return shape[0] * shape[1], max(1, shape[1]), stride[0], stride[1]
+        return shape[0] * shape[1], shape[1] or 1, stride[0], stride[1]
     if nd == 1:
         return 1, 1, 0, 0
     levels = []
@@ -152,27 +152,31 @@ def _like_rows(x: torch.Tensor) -> torch.Tensor:
     phase = x.data_ptr() % 16 // x.element_size()
     if phase == 0 and x.is_contiguous():
         return torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    n = x.numel()
-    if n:
-        apart = sorted((s, k) for s, k in zip(x.stride(), x.shape) if k > 1)
-        span = 1
-        for s, k in apart:
-            if s < span:   # overlapping rows (an expanded tensor)
+    shape, stride, n = x.shape, x.stride(), x.numel()
+    span = 1   # elements from the first to the last, so far
+    for s, k in zip(reversed(stride), reversed(shape)):
+        if k > 1:
+            if s < span:   # overlapping rows (an expanded tensor), or dimensions in another order
                 break
             span += s * (k - 1)
-        else:
-            if span <= n + n // 4 + 64 * x.shape[-1]:
-                return torch.empty(span + phase, dtype=x.dtype, device=x.device).as_strided(
-                    x.shape, x.stride(), phase)
-    return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    else:
+        if n and span <= n + n // 4 + 64 * shape[-1]:
+            return torch.empty(span + phase, dtype=x.dtype, device=x.device).as_strided(shape, stride, phase)
+    if x.dim() == 3 and n and stride[0] < stride[1]:   # [batch, tokens] stored as [tokens, batch]
+        return _like_rows(x.transpose(0, 1)).transpose(0, 1)
+    return torch.empty(shape, dtype=x.dtype, device=x.device)
 
 
-def _out_rows(out: Optional[torch.Tensor], x: torch.Tensor) -> torch.Tensor:
+def _out_rows(out: Optional[torch.Tensor], x: torch.Tensor, rows: A.adamw_rows_t):
+    """The tensor for the gradient of x, and its adamw_rows_t."""
     if out is None:
-        return _like_rows(x)
-    if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
+        out = _like_rows(x)
+    elif out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
         raise ValueError("out must have the logits' shape, type and device")
-    return out
+    if out.stride() == x.stride():
+        return out, A.adamw_rows_t(out.data_ptr(), rows.rows, rows.inner, rows.outer_stride, rows.row_stride,
+                                   rows.cols, rows.dtype)
+    return out, _rows(out)
 
 
 def _scale(temperature: float) -> float:
@@ -244,9 +248,9 @@ def token_logprob_backward(logits: torch.Tensor, targets: torch.Tensor, result: 
             raise ValueError("a gradient of the entropy needs the forward pass's entropy")
         dh = _floats("d_entropy", d_entropy, shape, dev)
         ent = _floats("entropy", result.entropy, shape, dev)
-    d = _out_rows(out, logits)
+    d, d_rows = _out_rows(out, logits, rows)
     _call(A.load().adamw_token_logprob_backward, "adamw_token_logprob_backward", dev, _byref(rows), t.data_ptr(), ignore_index, _scale(temperature),
-          stats.data_ptr(), _ptr(ent), dl.data_ptr(), _ptr(dh), _byref(_rows(d)))
+          stats.data_ptr(), _ptr(ent), dl.data_ptr(), _ptr(dh), _byref(d_rows))
     return d
 
 
@@ -359,9 +363,7 @@ def policy_loss_logits(logits: torch.Tensor, targets: torch.Tensor, old_logp: to
     adv, per_token = _advantages(advantages, shape, sequences, dev)
     policy = _policy(clip_low, clip_high, dual_clip, kl, kl_coef, entropy_coef, reduce, divisor, grad_scale,
                      per_token)
-    d = _out_rows(out, logits)
-    if out is not None:
-        d = _detached(d)
+    d, d_rows = _out_rows(None if out is None else _detached(out), logits, rows)
     stats = torch.empty(6, dtype=_F32, device=dev)
     counts = torch.empty(2, dtype=torch.int64, device=dev)
     logp = torch.empty(shape, dtype=_F32, device=dev)
@@ -370,7 +372,7 @@ def policy_loss_logits(logits: torch.Tensor, targets: torch.Tensor, old_logp: to
     work = torch.empty(lib.adamw_policy_logits_workspace(tokens.n, sequences), dtype=torch.uint8, device=dev)
     _call(lib.adamw_policy_loss_logits, "adamw_policy_loss_logits", dev, _byref(rows), t.data_ptr(), ignore_index, _scale(temperature),
           _byref(tokens), _byref(policy), old.data_ptr(), _ptr(ref), adv.data_ptr(), stats.data_ptr(),
-          counts.data_ptr(), logp.data_ptr(), _ptr(ent), _byref(_rows(d)), work.data_ptr())
+          counts.data_ptr(), logp.data_ptr(), _ptr(ent), _byref(d_rows), work.data_ptr())
     return PolicyLogits(stats, counts, logp, ent, d)
 
 
