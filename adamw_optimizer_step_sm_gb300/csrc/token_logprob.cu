@@ -200,9 +200,11 @@ logprob_backward_kernel(Rows logits, Rows grad, uint32_t rows, uint32_t pieces, 
     dependency_wait();
     const int lane = WARP ? threadIdx.x % 32 : threadIdx.x;
     constexpr int width = WARP ? 32 : kBackwardThreads;
-    const uint32_t r = WARP ? blockIdx.x * (kBackwardThreads / 32) + threadIdx.x / 32 : blockIdx.x / pieces;
-    const uint32_t piece = WARP ? 0 : blockIdx.x - r * pieces;
-    if (r >= rows) return;
+    // the last rows first: a forward pass just before left them in L2
+    const uint32_t back = WARP ? blockIdx.x * (kBackwardThreads / 32) + threadIdx.x / 32 : blockIdx.x / pieces;
+    const uint32_t piece = WARP ? 0 : blockIdx.x - back * pieces;
+    if (back >= rows) return;
+    const uint32_t r = rows - 1 - back;
     const char* row = logits.at(r);
     char* out = grad.at(r);
     const RowSplit<DT> sp(row, cols);
