@@ -14,9 +14,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-// Elements of a tile, the piece of a tensor that a CTA takes at a time: the
-// largest that gives every resident CTA one, in [2048, 16384].
-constexpr int kMaxTile = 16384, kMinTile = 2048;
+// Elements of a tile, the piece of a tensor that a CTA takes at a time: 16384,
+// 8192 for lists that give fewer than two of those to each SM.  Measured (bf16
+// list, us, largest tile / this rule / at least 2048): 1M elements 4.8 / 4.7 /
+// 5.4, 4M 6.8 / 6.2 / 7.9, 16M and above the same; a 1.3B list 1904 with tiles
+// of 32768, 1910 of 16384, 1936 of 8192.
+constexpr int kMaxTile = 16384, kMinTile = 8192;
 constexpr int kNormUnroll = 8;   // 16-byte vectors in flight per thread
 constexpr int kScaleVecs = 8;    // likewise, when scaling
 constexpr int kMaxGrid = 1216;   // CTAs of the norm pass at most: its partials
@@ -438,7 +441,7 @@ int create(const adamw_grad_t* table, int32_t n, adamw_clip_plan* P) {
         total += g.numel;
     }
     int64_t tile = kMaxTile;
-    while (tile > kMinTile && total < tile * sms * 4) tile /= 2;
+    while (tile > kMinTile && total < tile * sms * 2) tile /= 2;
     // pair by pair of types, tensors that are only read first
     std::vector<Tile> tiles;
     for (int pair = -1; pair < 9; ++pair) {

@@ -21,8 +21,12 @@ uint32_t token_grid(int64_t n, int64_t most) {
     return uint32_t(g < 1 ? 1 : g > most ? most : g);
 }
 
-// Up to here one cluster does a whole call in one launch.
-constexpr int64_t kClusterTokens = 32768, kClusterSequences = 8192, kClusterPairs = 16;
+// Up to here one cluster does a whole call in one launch.  Measured (us, one
+// cluster / a grid): policy loss of 1024 tokens 4.2 / 9.4, 8192 6.6 / 10.5,
+// 16384 8.7 / 10.5, 32768 13.4 / 10.6; preference loss of 8 pairs and 1024
+// tokens 4.6 / 4.4 (and one launch less for the host), 8192 5.0 / 5.6, 32768
+// 7.5 / 7.7; of 16 pairs and 16384 tokens, two to a CTA, 7.5 / 5.7.
+constexpr int64_t kClusterTokens = 16384, kClusterSequences = 8192, kClusterPairs = 8;
 bool in_one_cluster(const adamw_tokens_t* t) {
     return t->n <= kClusterTokens && t->sequences <= kClusterSequences;
 }
@@ -678,8 +682,11 @@ extern "C" int adamw_preference_loss(const adamw_tokens_t* tokens, const adamw_p
                           pref->kind, pref->length_average, pref->ref};
     const Tokens k = tokens_of(tokens, nullptr, 0);
     const int64_t per_pair = tokens->n / pairs;
+    // Larger CTAs where a pair is long.  Measured (us, grown at 8 / 16 tokens
+    // a thread / never): 1024 pairs of 2048 tokens 17.1 / 13.3 / 13.2, 4 of
+    // 65536 12.2 / 12.2 / 14.4.
     int block = kThreads;
-    while (block < 1024 && per_pair >= 8 * block) block *= 2;
+    while (block < 1024 && per_pair >= 16 * block) block *= 2;
     if (pairs <= kClusterPairs && tokens->n <= kClusterTokens) {
         int ctas = 1;
         while (ctas < 8 && ctas < pairs) ctas *= 2;

@@ -13,9 +13,15 @@ namespace {
 constexpr int kForwardThreads = 128, kForwardUnroll = 8;
 constexpr int kBackwardThreads = 128, kBackwardUnroll = 8;
 constexpr int kPolicyThreads = 128, kPolicyUnroll = 8;
-// Rows of up to this many elements are taken by a warp each;
-// longer ones by a CTA or a cluster of them.
-constexpr int kWarpCols = 1024;
+// Rows of up to this many 16-byte vectors are taken by a warp each, longer ones
+// by a CTA or a cluster of them: a short row keeps few loads of a CTA in flight
+// between its start and its join.  Measured (bf16, us, warp / CTA), 16384 rows
+// of 2048: forward 9.9 / 40.5, with the backward pass 29 / 74, policy 34 / 79;
+// of 4096: 22.9 / 42.6, 58 / 85, 53 / 88; of 8192: 41.8 / 47.4, 123 / 121,
+// 99 / 99; 64 rows of 4096: 3.0 / 3.8, 5.7 / 6.1, 9.1 / 9.5; of 8192: 4.0 /
+// 4.4, 7.7 / 7.2, 10.0 / 10.0.
+constexpr int kForwardWarpVecs = 1024, kBackwardWarpVecs = 512, kPolicyWarpVecs = 512;
+
 // The elements of the row outside its vectors, at most one per thread of the
 // group: the head's by threads 0.. of the first CTA, the tail's by threads
 // 8.. of the last one.  -1: none.
@@ -359,8 +365,12 @@ policy_rows_kernel(Rows logits, Rows grad, Tokens tokens, int cols, float scale,
 
 // ------------------------------------------------------------------- host --
 
-// Fewest CTAs that keep the GPU busy: rows below it are split over clusters.
-constexpr int64_t kBusyCtas = 304;
+// Fewest CTAs that keep the GPU busy: where there are fewer rows, each is
+// split over a cluster.  Measured (50272 elements, us, split / not): forward
+// of 1 row 4.7 / 5.8, of 32 5.3 / 6.0, of 76 5.7 / 6.0, of 152 6.1 / 6.3;
+// policy of 1 row 11.6 / 13.7, of 32 12.0 / 13.7, of 76 13.3 / 13.9, of 152
+// 15.5 / 15.3.  Splitting further, up to 608 CTAs, costs 1 to 2 us.
+constexpr int64_t kBusyCtas = 152;
 constexpr int kMaxCluster = 8;
 constexpr int64_t kMaxSmem = 200 * 1024;    // a CTA's share of a row, at most
 constexpr int64_t kWantSmem = 108 * 1024;   // two CTAs to an SM
@@ -451,7 +461,7 @@ cudaError_t forward(const adamw_rows_t* x, const int64_t* targets, int64_t ignor
                     float* logp, float* entropy, float* stats, cudaStream_t st) {
     const Rows rows = rows_of(x);
     const uint32_t n = uint32_t(x->rows);
-    if (x->cols <= kWarpCols) {
+    if (x->cols / Elem<DT>::kVec <= kForwardWarpVecs) {
         auto k = entropy ? logprob_kernel<DT, true, true> : logprob_kernel<DT, false, true>;
         return launch(k, warp_grid(n, kForwardThreads), kForwardThreads, 1, 0, st, rows, n, x->cols, targets, ignore,
                       scale, logp, entropy, stats);
@@ -469,7 +479,7 @@ cudaError_t backward(const adamw_rows_t* x, const int64_t* targets, float scale,
                      const adamw_rows_t* dx, cudaStream_t st) {
     const Rows in = rows_of(x), out = rows_of(dx);
     const uint32_t n = uint32_t(x->rows);
-    if (x->cols <= kWarpCols) {
+    if (x->cols / Elem<DT>::kVec <= kBackwardWarpVecs) {
         auto k = d_entropy ? logprob_backward_kernel<DT, true, true> : logprob_backward_kernel<DT, false, true>;
         return launch(k, warp_grid(n, kBackwardThreads), kBackwardThreads, 1, 0, st, in, out, n, 1u, x->cols, targets,
                       scale, stats, entropy, d_logp, d_entropy);
@@ -506,14 +516,12 @@ cudaError_t policy_rows(const adamw_rows_t* x, const adamw_rows_t* dx, const Tok
                         const Policy& P, const PolicyRows& a, cudaStream_t st) {
     const Rows in = rows_of(x), out = rows_of(dx);
     const int64_t vecs = x->cols / Elem<DT>::kVec;
-    if (x->cols <= kWarpCols) {
-        // a CTA's rows: at most 1024 * 4 bytes each
+    if (vecs <= kPolicyWarpVecs)   // at most 8 KB to a warp
         return launch(policy_rows_kernel<DT, ENT, true>, warp_grid(tokens.n, kPolicyThreads), kPolicyThreads, 1,
                       size_t(vecs) * 16 * (kPolicyThreads / 32), st, in, out, tokens, x->cols, scale, P, a);
-    }
     auto k = policy_rows_kernel<DT, ENT, false>;
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), done);
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), done);
     if (e != cudaSuccess) return e;
     int c = 1;
     while (c < kMaxCluster && (vecs + c - 1) / c * 16 > kWantSmem) c *= 2;

@@ -34,7 +34,11 @@ import torch
 
 from . import adamw_sm as A
 
+# names looked up once: small calls are mostly host time
 _byref = ctypes.byref
+_empty = torch.empty
+_rows_t, _tokens_t = A.adamw_rows_t, A.adamw_tokens_t
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 _F32 = torch.float32
 _CODES = {torch.bfloat16: A.DTYPE_BF16, torch.float16: A.DTYPE_FP16, torch.float32: A.DTYPE_FP32}
 
@@ -69,17 +73,16 @@ class PreferenceLoss(NamedTuple):
 
 # ---------------------------------------------------------------- checking --
 
-# A call on small arrays is mostly host time: the checks below take the usual
-# case first, in one condition.
+# The checks take the usual case first, in one condition.
 
 def _call(f, name: str, device: torch.device, *args) -> None:
     """One library call on the device's current stream."""
     index = device.index
-    if index == torch._C._cuda_getDevice():
-        rc = f(*args, torch._C._cuda_getCurrentRawStream(index))
+    if index == _current_device():
+        rc = f(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            rc = f(*args, torch._C._cuda_getCurrentRawStream(index))
+            rc = f(*args, _raw_stream(index))
     if rc:
         raise A.AdamWError(rc, name)
 
@@ -110,20 +113,26 @@ def _geometry(x: torch.Tensor):
 
 
 def _rows(x: torch.Tensor) -> A.adamw_rows_t:
-    if not x.is_cuda:
-        raise TypeError("want CUDA tensors")
-    code = _CODES.get(x.dtype)
-    if code is None:
-        raise TypeError(f"want bfloat16, float16 or float32 logits, not {x.dtype}")
-    if x.dim() < 1 or x.shape[-1] < 1:
-        raise ValueError("want logits of [..., vocabulary]")
-    if x.stride(-1) != 1 and x.shape[-1] > 1:
+    code, shape, stride = _CODES.get(x.dtype), x.shape, x.stride()
+    nd = len(shape)
+    if code is None or not x.is_cuda or nd == 0 or shape[-1] < 1 or (stride[-1] != 1 and shape[-1] > 1):
+        if not x.is_cuda:
+            raise TypeError("want CUDA tensors")
+        if code is None:
+            raise TypeError(f"want bfloat16, float16 or float32 logits, not {x.dtype}")
+        if nd == 0 or shape[-1] < 1:
+            raise ValueError("want logits of [..., vocabulary]")
         raise ValueError("the elements of a row of logits must be consecutive")
-    rows, inner, outer, row = _geometry(x)
-    return A.adamw_rows_t(x.data_ptr(), rows, inner, outer, row, x.shape[-1], code)
+    if nd == 2:
+        return _rows_t(x.data_ptr(), shape[0], shape[0] or 1, 0, stride[0], shape[1], code)
+    if nd == 3:
+        return _rows_t(x.data_ptr(), shape[0] * shape[1], shape[1] or 1, stride[0], stride[1], shape[2], code)
+    return _rows_t(x.data_ptr(), *_geometry(x), shape[-1], code)
 
 
 def _targets(t: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
+    if t.dtype is torch.int64 and t.device == logits.device and t.shape == logits.shape[:-1] and t.is_contiguous():
+        return t
     if t.dtype != torch.int64 or t.device != logits.device:
         raise TypeError("want int64 targets on the logits' device")
     if t.shape != logits.shape[:-1]:
@@ -151,7 +160,7 @@ def _like_rows(x: torch.Tensor) -> torch.Tensor:
     accesses whatever the vocabulary's size), unless x is spread too thin."""
     phase = x.data_ptr() % 16 // x.element_size()
     if phase == 0 and x.is_contiguous():
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        return _empty(x.shape, dtype=x.dtype, device=x.device)
     shape, stride, n = x.shape, x.stride(), x.numel()
     span = 1   # elements from the first to the last, so far
     for s, k in zip(reversed(stride), reversed(shape)):
@@ -161,10 +170,10 @@ def _like_rows(x: torch.Tensor) -> torch.Tensor:
             span += s * (k - 1)
     else:
         if n and span <= n + n // 4 + 64 * shape[-1]:
-            return torch.empty(span + phase, dtype=x.dtype, device=x.device).as_strided(shape, stride, phase)
+            return _empty(span + phase, dtype=x.dtype, device=x.device).as_strided(shape, stride, phase)
     if x.dim() == 3 and n and stride[0] < stride[1]:   # [batch, tokens] stored as [tokens, batch]
         return _like_rows(x.transpose(0, 1)).transpose(0, 1)
-    return torch.empty(shape, dtype=x.dtype, device=x.device)
+    return _empty(shape, dtype=x.dtype, device=x.device)
 
 
 def _out_rows(out: Optional[torch.Tensor], x: torch.Tensor, rows: A.adamw_rows_t):
@@ -174,7 +183,7 @@ def _out_rows(out: Optional[torch.Tensor], x: torch.Tensor, rows: A.adamw_rows_t
     elif out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
         raise ValueError("out must have the logits' shape, type and device")
     if out.stride() == x.stride():
-        return out, A.adamw_rows_t(out.data_ptr(), rows.rows, rows.inner, rows.outer_stride, rows.row_stride,
+        return out, _rows_t(out.data_ptr(), rows.rows, rows.inner, rows.outer_stride, rows.row_stride,
                                    rows.cols, rows.dtype)
     return out, _rows(out)
 
@@ -190,9 +199,9 @@ def _scale(temperature: float) -> float:
 def _token_logprob(logits, targets, ignore_index, temperature, entropy) -> TokenLogprob:
     rows, t = _rows(logits), _targets(targets, logits)
     dev, shape = logits.device, targets.shape
-    logp = torch.empty(shape, dtype=_F32, device=dev)
-    ent = torch.empty(shape, dtype=_F32, device=dev) if entropy else None
-    stats = torch.empty((*shape, 2), dtype=_F32, device=dev)
+    logp = _empty(shape, dtype=_F32, device=dev)
+    ent = _empty(shape, dtype=_F32, device=dev) if entropy else None
+    stats = _empty((*shape, 2), dtype=_F32, device=dev)
     _call(A.load().adamw_token_logprob, "adamw_token_logprob", dev, _byref(rows), t.data_ptr(), ignore_index, _scale(temperature),
           logp.data_ptr(), _ptr(ent), stats.data_ptr())
     return TokenLogprob(logp, ent, stats)
@@ -262,7 +271,7 @@ def _tokens(shape, offsets, mask, device):
     if offsets is None and mask is not None and mask.dtype is torch.bool and mask.shape == shape \
             and mask.device == device and mask.is_contiguous():
         sequences = shape[0] if len(shape) > 1 else 1
-        return A.adamw_tokens_t(n, sequences, None, mask.data_ptr()), sequences, mask
+        return _tokens_t(n, sequences, None, mask.data_ptr()), sequences, mask
     keep = []
     if offsets is not None:
         if offsets.dtype != torch.int64 or offsets.device != device or offsets.dim() != 1 or offsets.numel() < 1:
@@ -279,7 +288,7 @@ def _tokens(shape, offsets, mask, device):
             raise ValueError(f"mask {tuple(mask.shape)} does not match {tuple(shape)}")
         mask = mask if mask.is_contiguous() else mask.contiguous()
         keep.append(mask)
-    return A.adamw_tokens_t(n, sequences, _ptr(offsets), _ptr(mask)), sequences, keep
+    return _tokens_t(n, sequences, _ptr(offsets), _ptr(mask)), sequences, keep
 
 
 def _detached(t):
@@ -328,12 +337,12 @@ def policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Te
     adv, per_token = _advantages(advantages, shape, sequences, dev)
     policy = _policy(clip_low, clip_high, dual_clip, kl, kl_coef, entropy_coef, reduce, divisor, grad_scale,
                      per_token)
-    stats = torch.empty(6, dtype=_F32, device=dev)
-    counts = torch.empty(2, dtype=torch.int64, device=dev)
-    d_logp = torch.empty(shape, dtype=_F32, device=dev)
-    d_entropy = torch.empty(shape, dtype=_F32, device=dev) if ent is not None else None
+    stats = _empty(6, dtype=_F32, device=dev)
+    counts = _empty(2, dtype=torch.int64, device=dev)
+    d_logp = _empty(shape, dtype=_F32, device=dev)
+    d_entropy = _empty(shape, dtype=_F32, device=dev) if ent is not None else None
     lib = A.load()
-    work = torch.empty(lib.adamw_policy_workspace(tokens.n, sequences), dtype=torch.uint8, device=dev)
+    work = _empty(lib.adamw_policy_workspace(tokens.n, sequences), dtype=torch.uint8, device=dev)
     _call(lib.adamw_policy_loss, "adamw_policy_loss", dev, _byref(tokens), _byref(policy), logp.data_ptr(), old.data_ptr(), _ptr(ref),
           adv.data_ptr(), _ptr(ent), stats.data_ptr(), counts.data_ptr(), d_logp.data_ptr(), _ptr(d_entropy),
           work.data_ptr())
@@ -364,12 +373,12 @@ def policy_loss_logits(logits: torch.Tensor, targets: torch.Tensor, old_logp: to
     policy = _policy(clip_low, clip_high, dual_clip, kl, kl_coef, entropy_coef, reduce, divisor, grad_scale,
                      per_token)
     d, d_rows = _out_rows(None if out is None else _detached(out), logits, rows)
-    stats = torch.empty(6, dtype=_F32, device=dev)
-    counts = torch.empty(2, dtype=torch.int64, device=dev)
-    logp = torch.empty(shape, dtype=_F32, device=dev)
-    ent = torch.empty(shape, dtype=_F32, device=dev) if entropy or entropy_coef != 0.0 else None
+    stats = _empty(6, dtype=_F32, device=dev)
+    counts = _empty(2, dtype=torch.int64, device=dev)
+    logp = _empty(shape, dtype=_F32, device=dev)
+    ent = _empty(shape, dtype=_F32, device=dev) if entropy or entropy_coef != 0.0 else None
     lib = A.load()
-    work = torch.empty(lib.adamw_policy_logits_workspace(tokens.n, sequences), dtype=torch.uint8, device=dev)
+    work = _empty(lib.adamw_policy_logits_workspace(tokens.n, sequences), dtype=torch.uint8, device=dev)
     _call(lib.adamw_policy_loss_logits, "adamw_policy_loss_logits", dev, _byref(rows), t.data_ptr(), ignore_index, _scale(temperature),
           _byref(tokens), _byref(policy), old.data_ptr(), _ptr(ref), adv.data_ptr(), stats.data_ptr(),
           counts.data_ptr(), logp.data_ptr(), _ptr(ent), _byref(d_rows), work.data_ptr())
@@ -402,10 +411,10 @@ def preference_loss(logp: torch.Tensor, ref_logp: Optional[torch.Tensor] = None,
         ref = _floats("ref_logp", ref_logp, shape if how == A.REF_TOKEN else (sequences,), dev)
     pref = A.adamw_preference_t(beta, margin, label_smoothing, grad_scale, A.PREFERENCE[kind],
                                 1 if length_average else 0, how)
-    stats = torch.empty(3, dtype=_F32, device=dev)
-    losses = torch.empty(pairs, dtype=_F32, device=dev)
-    rewards = torch.empty(sequences, dtype=_F32, device=dev)
-    d_logp = torch.empty(shape, dtype=_F32, device=dev)
+    stats = _empty(3, dtype=_F32, device=dev)
+    losses = _empty(pairs, dtype=_F32, device=dev)
+    rewards = _empty(sequences, dtype=_F32, device=dev)
+    d_logp = _empty(shape, dtype=_F32, device=dev)
     _call(A.load().adamw_preference_loss, "adamw_preference_loss", dev, _byref(tokens), _byref(pref), logp.data_ptr(), _ptr(ref),
           stats.data_ptr(), losses.data_ptr(), rewards.data_ptr(), d_logp.data_ptr())
     return PreferenceLoss(stats, losses, rewards, d_logp)

@@ -94,8 +94,8 @@ def _close_grad(got, want, dtype):
 
 # ------------------------------------------------------- log-probabilities
 
-SHAPES = [(1, 1), (3, 2), (5, 7), (9, 31), (2, 33), (70, 257), (11, 1000), (8, 1024), (7, 1025), (5, 4097),
-          (3, 50257), (2, 50272), (1, 131072)]
+SHAPES = [(1, 1), (3, 2), (5, 7), (9, 31), (2, 33), (70, 257), (11, 1000), (8, 1024), (7, 1025), (6, 4096),
+          (5, 4097), (4, 8192), (3, 8193), (3, 50257), (2, 50272), (1, 131072)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
@@ -416,8 +416,8 @@ def test_policy_loss_edges():
 # ------------------------------------------------------ policy loss from logits
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
-@pytest.mark.parametrize("b,s,v", [(1, 1, 5), (2, 3, 60), (3, 40, 1000), (2, 9, 1025), (3, 7, 7001), (2, 5, 50257),
-                                   (40, 13, 3000), (1, 2, 200000)])
+@pytest.mark.parametrize("b,s,v", [(1, 1, 5), (2, 3, 60), (3, 40, 1000), (2, 9, 1025), (2, 3, 4096), (2, 3, 4099),
+                                   (3, 7, 7001), (2, 5, 50257), (40, 13, 3000), (1, 2, 200000)])
 def test_policy_loss_logits(b, s, v, dtype):
     n = b * s
     g = _gen(v + n)
