@@ -682,11 +682,13 @@ extern "C" int adamw_preference_loss(const adamw_tokens_t* tokens, const adamw_p
                           pref->kind, pref->length_average, pref->ref};
     const Tokens k = tokens_of(tokens, nullptr, 0);
     const int64_t per_pair = tokens->n / pairs;
-    // Larger CTAs where a pair is long.  Measured (us, grown at 8 / 16 tokens
-    // a thread / never): 1024 pairs of 2048 tokens 17.1 / 13.3 / 13.2, 4 of
-    // 65536 12.2 / 12.2 / 14.4.
-    int block = kThreads;
-    while (block < 1024 && per_pair >= 16 * block) block *= 2;
+    // Larger CTAs where a pair is long, 12 tokens to a thread and more.
+    // Measured (us, CTAs of 128 / 256): 4096 pairs of 128 tokens 16.1 / 22.8,
+    // of 1024 21.1 / 32.0, 1024 ragged pairs of 2048 on average 23.1 / 19.5;
+    // 1024 pairs of 2048, 256 / grown at 8 tokens 13.3 / 17.1; 4 of 65536,
+    // grown / 256 12.2 / 14.4.
+    int block = 128;
+    while (block < 1024 && per_pair >= 12 * block) block *= 2;
     if (pairs <= kClusterPairs && tokens->n <= kClusterTokens) {
         int ctas = 1;
         while (ctas < 8 && ctas < pairs) ctas *= 2;
@@ -694,7 +696,9 @@ extern "C" int adamw_preference_loss(const adamw_tokens_t* tokens, const adamw_p
                                losses, rewards, d_logp, stats), "preference launch")
                    ? ADAMW_OK : ADAMW_ERR_CUDA;
     }
-    // CTAs per pair: more where pairs are few and long
+    // CTAs per pair: more where pairs are few and long (clusters for a grid
+    // that is busy without them cost: 1024 pairs of 2048 tokens 37 us by two
+    // CTAs, 13 by one)
     int cluster = 1;
     while (cluster < 8 && pairs * cluster < 304 && per_pair >= cluster * 4 * block) cluster *= 2;
     if (pairs * cluster > kMaxCount) return ADAMW_ERR_TOO_LARGE;
