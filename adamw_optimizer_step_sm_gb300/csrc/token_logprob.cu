@@ -1,8 +1,10 @@
 // token_logprob.cu -- per-token log-probabilities from logits over the
 // vocabulary, their gradient, and the policy loss fused with both.
 //
-// All three are bound by HBM: a bf16 logit costs about six instructions and
-// one exponential against two bytes.
+// All three are bound by HBM when rows are long or many: a bf16 logit costs
+// about five instructions and one exponential (on packed pairs) a pass against
+// two bytes.  Few or short rows are bound by latency: a call of one row takes
+// 4.7 us.
 #include <atomic>
 
 #include "losses_common.cuh"
@@ -10,6 +12,11 @@
 namespace {
 
 // Threads of a CTA and 16-byte vectors in flight per thread, by kernel.
+// Measured with 50272 bf16 logits to a row (us): the forward pass of 8184 rows
+// 128 x 8 93.4, 128 x 12 92.5, 128 x 4 94.6, 64 x 8 97.7, 256 x 4 98.4; forward
+// and backward of 4092 rows, by the backward's, 128 x 8 165, 256 x 4 165, 128 x
+// 4 166, 64 x 8 171; policy of 16376 rows 128 x 8 500, 192 x 4 514, 256 x 4
+// 520, 128 x 4 533, 256 x 8 535, 64 x 8 672.
 constexpr int kForwardThreads = 128, kForwardUnroll = 8;
 constexpr int kBackwardThreads = 128, kBackwardUnroll = 8;
 constexpr int kPolicyThreads = 128, kPolicyUnroll = 8;
@@ -71,7 +78,8 @@ __device__ __forceinline__ Online group_join(Online o, float c) {
 
 // Log-probability and entropy of one row per group (a warp; or a cluster of
 // CTAs, each streaming its share of the row once, with the running maximum
-// and sums in registers).
+// and sums in registers).  One read of the logits: 8184 rows of 50272 bf16, a
+// quarter of them ignored, 94 us, 6.5 TB/s (98 % of this GPU's copy rate).
 template <int DT, bool ENT, bool WARP>
 __global__ void __launch_bounds__(kForwardThreads)
 logprob_kernel(Rows logits, uint32_t rows, int cols, const int64_t* targets, int64_t ignore,
@@ -195,7 +203,9 @@ __device__ __forceinline__ void zero_row(char* out, bool vector_out, const RowSp
     if (extra >= 0) E::store(out, extra, 0.0f);
 }
 
-// One CTA per piece of a row (or a warp per row): elementwise.
+// Elementwise from the row's maximum and sum, one CTA per piece of a row (or a
+// warp per row).  4092 rows of 50272 bf16, a quarter of them ignored, after
+// their forward pass: 109 us, 6.6 TB/s over one read and one write.
 template <int DT, bool ENT, bool WARP>
 __global__ void __launch_bounds__(kBackwardThreads)
 logprob_backward_kernel(Rows logits, Rows grad, uint32_t rows, uint32_t pieces, int cols,
@@ -266,7 +276,12 @@ constexpr int kDepth = 4;
 // the maximum and sums taken as it arrives, the group joins them, every
 // thread works out the token's loss, and the gradient is written from the
 // copy: one read and one write of HBM.  A thread reads only the vectors that
-// it copied itself, so the copies need no barrier.
+// it copied itself, so the copies need no barrier.  With the count before and
+// the statistics after it, 16376 rows of 50272 bf16 (a quarter of them ignored,
+// with the entropy) take 498 us, 5.8 TB/s; without the entropy and with none
+// ignored 16384 rows take 549 us, 6.0 TB/s.  Two rows are on an SM, eight
+// warps, which issue in 41 % of the cycles: latency keeps it from the copy
+// rate (thirds of rows in registers, three rows to an SM, gave 0 to 2 %).
 template <int DT, bool ENT, bool WARP>
 __global__ void __launch_bounds__(kPolicyThreads)
 policy_rows_kernel(Rows logits, Rows grad, Tokens tokens, int cols, float scale, Policy P, PolicyRows a) {

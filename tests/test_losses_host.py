@@ -153,6 +153,7 @@ def test_clip_list_is_checked():
     assert make((P, P, 10, f32, bf16)) == BAD            # in place with two types
     assert make((P, P + 36, 10, f32, f32)) == BAD        # overlapping
     assert make((P + 18, P, 10, bf16, bf16)) == BAD
+    assert make((P, None, (1 << 40) + 1, bf16, bf16)) == BIG
     lib = A.load()
     assert lib.adamw_clip_plan_create(None, 1, ctypes.byref(ctypes.c_void_p())) == BAD
     assert lib.adamw_clip_plan_create(None, 0, None) == BAD
