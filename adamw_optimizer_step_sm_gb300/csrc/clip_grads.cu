@@ -445,6 +445,7 @@ int create(const adamw_grad_t* table, int32_t n, adamw_clip_plan* P) {
         if (rc == ADAMW_OK && g.dst) rc = check_access(g.dst, P->device, pageable);
         if (rc != ADAMW_OK) return rc;
         total += g.numel;
+        if (total > kMaxTiles * kMaxTile) return ADAMW_ERR_TOO_LARGE;   // before it can overflow
     }
     int64_t tile = kMaxTile;
     while (tile > kMinTile && total < tile * sms * 2) tile /= 2;

@@ -253,8 +253,8 @@ typedef struct adamw_clip_plan* adamw_clip_plan_t;
  * plan must not overlap on the GPU.
  * Errors: INVALID_ARG (NULL out or table with n > 0, n < 0, numel < 0, NULL
  * src with numel > 0, unknown dtype, dst overlapping src without being it, in
- * place with two types), MISALIGNED, NOT_ACCESSIBLE, TOO_LARGE (an entry of
- * more than 2^40 elements, a list of more than 2^39), CUDA. */
+ * place with two types), MISALIGNED, NOT_ACCESSIBLE, TOO_LARGE (more than
+ * 2^40 elements), CUDA. */
 int adamw_clip_plan_create(const adamw_grad_t* host_table, int32_t n, adamw_clip_plan_t* out);
 
 /* Clips the plan's gradients by their global norm: dst = coef * src for every
