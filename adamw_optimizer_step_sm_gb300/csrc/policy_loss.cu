@@ -20,12 +20,11 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kPerLane = 4;    // consecutive tokens of a lane
 constexpr int kChunk = 32 * kPerLane;  // and of a warp
 constexpr int kMaxGrid = 1216; // 8 CTAs for each of 152 SMs
-constexpr int kCountGrid = 1216;
 constexpr int kSums = 5;       // pg, KL, entropy, clipped, old KL
 
-uint32_t token_grid(int64_t n, int64_t most) {
+uint32_t token_grid(int64_t n) {
     const int64_t g = (n + kWarps * kChunk - 1) / (kWarps * kChunk);
-    return uint32_t(g < 1 ? 1 : g > most ? most : g);
+    return uint32_t(g < 1 ? 1 : g > kMaxGrid ? kMaxGrid : g);
 }
 
 // Up to here one cluster does a whole call in one launch.  Measured (us, one
@@ -163,11 +162,12 @@ __device__ __forceinline__ void store4(float* p, uint32_t first, uint32_t n, boo
 
 // Loss terms and gradients of CTA `cta` of `ctas`, 128 tokens to a warp: a
 // lane's loads are all on their way before it looks for its tokens'
-// sequences (from starts[], where the count left them).  Threads below kSums return the CTA's sums.  aligned: every
-// array is 16-byte aligned.
+// sequences (from starts[], where the count left them).  Threads below kSums
+// return the CTA's sums.  aligned: every array is 16-byte aligned.
 __device__ __forceinline__ Sum2 policy_tokens(const Tokens& t, const Policy& P, const PolicyTokens& a,
                                               const Counts* counts, const uint32_t* starts,
-                                              uint32_t tokens, uint32_t filled, bool aligned, uint32_t cta, uint32_t ctas) {
+                                              uint32_t tokens, uint32_t filled, bool aligned, uint32_t cta,
+                                              uint32_t ctas) {
     const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     Sum2 sum[kSums] = {};
     const uint64_t step = uint64_t(ctas) * kWarps * kChunk;
@@ -600,7 +600,7 @@ int launch_counts(const adamw_tokens_t* t, const int64_t* targets, int64_t ignor
     if (!launched(cudaMemsetAsync(c, 0, size_t(counts_bytes(t->sequences)), st), "counts memset"))
         return ADAMW_ERR_CUDA;
     uint32_t* starts = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + counts_bytes(t->sequences));
-    return launched(launch(count_kernel, token_grid(t->n, kCountGrid), kThreads, 1, 0, st, k, c, starts), "count launch")
+    return launched(launch(count_kernel, token_grid(t->n), kThreads, 1, 0, st, k, c, starts), "count launch")
                ? ADAMW_OK : ADAMW_ERR_CUDA;
 }
 
@@ -627,7 +627,7 @@ int launch_policy(const adamw_tokens_t* t, const adamw_policy_t* p, const int64_
         if (rc != ADAMW_OK) return rc;
     }
     char* rest = static_cast<char*>(workspace) + counts_bytes(t->sequences);
-    return launched(launch(policy_kernel, token_grid(t->n, kMaxGrid), kThreads, 1, 0, st, k, P, a, c,
+    return launched(launch(policy_kernel, token_grid(t->n), kThreads, 1, 0, st, k, P, a, c,
                            reinterpret_cast<const uint32_t*>(rest),
                            reinterpret_cast<float2*>(rest + starts_bytes(t->n)), all_aligned), "policy launch")
                ? ADAMW_OK : ADAMW_ERR_CUDA;
