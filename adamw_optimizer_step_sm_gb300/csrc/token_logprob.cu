@@ -254,50 +254,9 @@ struct PolicyRows {
     const int64_t* targets;
     int64_t ignore;
     const float *old_logp, *ref_logp, *advantages;
-    const Counts* counts;   // NULL: each group counts the tokens itself
+    const Counts* counts;
     float *logp, *entropy;
 };
-
-// The weight of a token of sequence `seq` from all the targets, by one group
-// (a warp or a CTA) for itself: sequences of the tokens' length, few tokens.
-template <bool WARP, int THREADS>
-__device__ __forceinline__ float weight_here(const Tokens& t, const Policy& P, uint32_t seq) {
-    if (P.reduce == ADAMW_REDUCE_FIXED) return P.inv_divisor;
-    const uint32_t lane = threadIdx.x % 32;
-    const uint32_t warp = WARP ? 0 : threadIdx.x / 32, warps = WARP ? 1 : THREADS / 32;
-    uint32_t tokens = 0, filled = 0, mine = 0;
-    if (P.reduce == ADAMW_REDUCE_TOKEN) {
-#pragma unroll 4
-        for (uint32_t i = warp * 32 + lane; i < t.n; i += warps * 32) tokens += t.targets[i] != t.ignore;
-        tokens = __reduce_add_sync(0xffffffffu, tokens);
-    } else {
-        for (uint32_t s = warp; s < t.sequences; s += warps) {
-            uint32_t k = 0;
-#pragma unroll 4
-            for (uint32_t i = lane; i < t.length; i += 32) k += t.targets[s * t.length + i] != t.ignore;
-            k = __reduce_add_sync(0xffffffffu, k);
-            filled += k > 0;
-            if (s == seq) mine = k;
-        }
-    }
-    if (!WARP) {
-        __shared__ uint32_t part[3][THREADS / 32];
-        if (lane == 0) {
-            part[0][warp] = tokens;
-            part[1][warp] = filled;
-            part[2][warp] = mine;
-        }
-        __syncthreads();
-        tokens = filled = mine = 0;
-#pragma unroll
-        for (int w = 0; w < THREADS / 32; ++w) {
-            tokens += part[0][w];
-            filled += part[1][w];
-            mine += part[2][w];
-        }
-    }
-    return token_weight(P.reduce, 0.0f, tokens, filled, mine);
-}
 
 __device__ __forceinline__ void copy_async16(uint4* smem, const uint4* global) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
@@ -376,12 +335,9 @@ policy_rows_kernel(Rows logits, Rows grad, Tokens tokens, int cols, float scale,
     const float ref = a.ref_logp ? a.ref_logp[r] : 0.0f;
     const int32_t seq = tokens.sequence(r);
     const float A = seq < 0 ? 0.0f : a.advantages[P.per_token ? r : uint32_t(seq)];
-    float w = 0.0f;
-    if (!a.counts)   // without offsets, so that every token has a sequence
-        w = weight_here<WARP, kPolicyThreads>(tokens, P, uint32_t(seq)) * P.grad_scale;
-    else if (seq >= 0)
-        w = token_weight(P.reduce, P.inv_divisor, a.counts->tokens, a.counts->filled, a.counts->sequence[seq]) *
-            P.grad_scale;
+    const float w = seq < 0 ? 0.0f
+                            : token_weight(P.reduce, P.inv_divisor, a.counts->tokens, a.counts->filled,
+                                           a.counts->sequence[seq]) * P.grad_scale;
 
     Online o = {-kInf, 0.0f, 0.0f};
     if (extra >= 0) absorb_one<ENT>(o, xe, c);
@@ -433,9 +389,6 @@ constexpr int64_t kBusyCtas = 152;
 constexpr int kMaxCluster = 8;
 constexpr int64_t kMaxSmem = 200 * 1024;    // a CTA's share of a row, at most
 constexpr int64_t kWantSmem = 108 * 1024;   // two CTAs to an SM
-
-// Up to here policy_rows_kernel counts the tokens itself.
-constexpr int64_t kAloneTokens = 1024, kAloneSequences = 32;
 
 int vec_of(int32_t dt) { return dt == ADAMW_DTYPE_FP32 ? 4 : 8; }
 
@@ -685,20 +638,14 @@ extern "C" int adamw_policy_loss_logits(const adamw_rows_t* logits, const int64_
         !aligned(workspace, 16))
         return ADAMW_ERR_MISALIGNED;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const bool fits = tokens->n == 0 || fits_cluster(logits);
-    // few tokens are counted by every row for itself, one launch less
-    const bool alone = fits && tokens->n <= kAloneTokens && !tokens->offsets &&
-                       (policy->reduce != ADAMW_REDUCE_SEQUENCE || tokens->sequences <= kAloneSequences);
-    if (!alone) {
-        rc = adamw::launch_counts(tokens, targets, ignore_index, workspace, st);
-        if (rc != ADAMW_OK) return rc;
-    }
-    if (fits) {
+    rc = adamw::launch_counts(tokens, targets, ignore_index, workspace, st);
+    if (rc != ADAMW_OK) return rc;
+    if (tokens->n == 0 || fits_cluster(logits)) {
         if (tokens->n > 0) {
             const Tokens t = tokens_of(tokens, targets, ignore_index);
             const Policy P = policy_of(policy);
             const PolicyRows a = {targets, ignore_index, old_logp, ref_logp, advantages,
-                                  alone ? nullptr : static_cast<const Counts*>(workspace), logp, entropy};
+                                  static_cast<const Counts*>(workspace), logp, entropy};
             cudaError_t e;
             switch (logits->dtype) {
                 case ADAMW_DTYPE_BF16: e = policy_rows<ADAMW_DTYPE_BF16>(logits, d_logits, t, scale, P, a, st); break;
@@ -707,7 +654,7 @@ extern "C" int adamw_policy_loss_logits(const adamw_rows_t* logits, const int64_
             }
             if (!launched(e, "policy_loss_logits launch")) return ADAMW_ERR_CUDA;
         }
-        return adamw::launch_policy(tokens, policy, targets, ignore_index, !alone, logp, old_logp, ref_logp,
+        return adamw::launch_policy(tokens, policy, targets, ignore_index, true, logp, old_logp, ref_logp,
                                     advantages, entropy, stats, counts, nullptr, nullptr, workspace, st);
     }
     char* w = static_cast<char*>(workspace) + round16(adamw_policy_workspace(tokens->n, tokens->sequences));
