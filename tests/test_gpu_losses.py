@@ -381,6 +381,68 @@ def test_policy_loss(n, rows, packed, reduce):
     _check_policy(got, want, False)
 
 
+@pytest.mark.parametrize("n,rows", [(40000, 15000), (40000, 3000), (3000, 2500), (17000, 9000)])
+@pytest.mark.parametrize("reduce", ["token", "sequence"])
+def test_policy_loss_many_short_sequences(n, rows, reduce):
+    """More sequences than lanes among a warp's tokens, empty ones, and tokens
+    before the first and after the last."""
+    logp, old, ref, ent, on, starts, g = _policy_inputs(n, rows, n - rows, True)
+    starts = [min(max(s, 100), n - 50) for s in starts]
+    adv = torch.randn(rows, generator=g) + 0.2
+    o = dict(clip_low=0.2, clip_high=0.28, dual=0.0, kl="k3", kl_coef=0.05, entropy_coef=0.01, reduce=reduce,
+             divisor=1.0, per_token=False)
+    want = _policy64(logp, old, adv, ref, ent, on, starts, o)
+    d = lambda v: v.to(DEV)
+    got = L.policy_loss(d(logp), d(old), d(adv), ref_logp=d(ref), entropy=d(ent), mask=d(on),
+                        offsets=torch.tensor(starts, device=DEV), clip_low=0.2, clip_high=0.28, kl_coef=0.05,
+                        entropy_coef=0.01, reduce=reduce)
+    _check_policy(got, want, True)
+    assert (got.d_logp[:100] == 0).all() and (got.d_logp[n - 50:] == 0).all()
+    # targets in place of the mask: the fused form counts the same tokens
+    x = torch.randn(n, 8, generator=g).to(DEV)
+    t = torch.where(on, torch.randint(0, 8, (n,), generator=g), -100).to(DEV)
+    lp = L.token_logprob(x, t)
+    r = L.policy_loss_logits(x, t, d(old), d(adv), offsets=torch.tensor(starts, device=DEV), reduce=reduce)
+    p = L.policy_loss(lp.logp, d(old), d(adv), mask=d(on), offsets=torch.tensor(starts, device=DEV), reduce=reduce)
+    assert torch.equal(r.counts, got.counts) and torch.equal(r.logp, lp.logp)
+    assert (r.stats - p.stats).abs().max() <= 1e-6 * p.stats.abs().max() + 1e-7
+    back = L.token_logprob_backward(x, t, lp, p.d_logp)
+    assert (r.d_logits - back).abs().max() <= 1e-6 * back.abs().max()
+
+
+@pytest.mark.parametrize("n", [1000, 40000])
+def test_losses_replayed_and_on_two_streams(n):
+    """Counts, tickets and sums start afresh in every replay, and calls on two
+    streams do not share them."""
+    logp, old, ref, ent, on, starts, g = _policy_inputs(n, 50, n, False)
+    args = [v.to(DEV).view(50, n // 50) for v in (logp, old)]
+    adv = [torch.randn(50, generator=g).to(DEV) for _ in range(2)]
+    mask = on.to(DEV).view(50, -1)
+    call = lambda k: (L.policy_loss(*args, adv[k], mask=mask, reduce="sequence"), L.preference_loss(args[k], args[1 - k]))
+    flat = lambda rs: [v for r in rs for v in r if v is not None]
+    want = [[v.clone() for v in flat(call(k))] for k in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(10):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[k].append(flat(call(k)))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for r in got[k]:
+            assert all(torch.equal(a, b) for a, b in zip(r, want[k]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r = flat(call(0))
+    for _ in range(3):
+        for v in r:
+            v.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(r, want[0]))
+
+
 def test_policy_loss_edges():
     t = lambda *v: torch.tensor(v, device=DEV)
     # nothing counts: zeros, no division by zero
