@@ -670,7 +670,7 @@ __device__ __forceinline__ PolicyToken policy_token(const Policy& P, float logp,
                                                     float ref, float A) {
     PolicyToken o;
     const float d = logp - old;
-    const float r = exp2_fast(d * kLog2e);
+    const float r = expf(d);
     // Outside [low, high] the clipped branch holds; inside, -A r is the larger
     // of the two: where r is past a limit there, it is past it on the side
     // that makes -A r larger.
@@ -694,7 +694,7 @@ __device__ __forceinline__ PolicyToken policy_token(const Policy& P, float logp,
             o.kl = 0.5f * k * k;
             dk = k;
         } else {
-            o.kl = exp_beyond_linear(-k, exp2_fast(-k * kLog2e));
+            o.kl = exp_beyond_linear(-k, expf(-k));
             dk = k - o.kl;   // 1 - exp(-k)
         }
         // without a coefficient the estimate is reported only, and a

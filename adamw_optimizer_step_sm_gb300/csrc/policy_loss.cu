@@ -164,6 +164,7 @@ __device__ __forceinline__ void store4(float* p, uint32_t first, uint32_t n, boo
 // lane's loads are all on their way before it looks for its tokens'
 // sequences (from starts[], where the count left them).  Threads below kSums
 // return the CTA's sums.  aligned: every array is 16-byte aligned.
+template <bool EXACT>
 __device__ __forceinline__ Sum2 policy_tokens(const Tokens& t, const Policy& P, const PolicyTokens& a,
                                               const Counts* counts, const uint32_t* starts,
                                               uint32_t tokens, uint32_t filled, bool aligned, uint32_t cta,
@@ -208,33 +209,42 @@ __device__ __forceinline__ Sum2 policy_tokens(const Tokens& t, const Policy& P, 
             const float w = on ? weight[j] : 0.0f;
             const PolicyToken k = policy_token(P, logp[j], old[j], a.ref_logp != nullptr, ref[j],
                                                P.per_token ? adv[j] : value[j]);
-            v[0] = fmaf(w, on ? k.pg : 0.0f, v[0]);
-            v[1] = fmaf(w, on ? k.kl : 0.0f, v[1]);
-            v[2] = fmaf(w, on ? ent[j] : 0.0f, v[2]);
-            v[3] = fmaf(w, k.off, v[3]);
-            v[4] = fmaf(w, on ? k.old_kl : 0.0f, v[4]);
+            const float term[kSums] = {on ? k.pg : 0.0f, on ? k.kl : 0.0f, on ? ent[j] : 0.0f, k.off,
+                                       on ? k.old_kl : 0.0f};
+#pragma unroll
+            for (int i = 0; i < kSums; ++i) {
+                if (EXACT) sum[i].add(w * term[i]); else v[i] = fmaf(w, term[i], v[i]);
+            }
             g[j] = on ? w * P.grad_scale * k.grad : 0.0f;
             gh[j] = on ? -w * P.grad_scale * P.entropy_coef : 0.0f;
         }
+        if (!EXACT) {
 #pragma unroll
-        for (int k = 0; k < kSums; ++k) sum[k].add(v[k]);
+            for (int k = 0; k < kSums; ++k) sum[k].add(v[k]);
+        }
         if (a.d_logp) store4(a.d_logp, first, t.n, vector, g);
         if (a.d_entropy) store4(a.d_entropy, first, t.n, vector, gh);
     }
-    // the lanes' sums as a tree in fp32 (five roundings), the warps' and the
-    // CTAs' error-free
-    __shared__ float part[kSums][kWarps];
+    // EXACT: error-free throughout; else the lanes' sums as a tree in fp32 (five
+    // roundings, which average out over many warps), the warps' and the CTAs'
+    // error-free
+    __shared__ float2 part[kSums][kWarps];
 #pragma unroll
     for (int k = 0; k < kSums; ++k) {
-        float s = sum[k].value();
+        Sum2 s = sum[k];
+        if (EXACT) {
+            s = warp_sum(s);
+        } else {
+            s = {s.value(), 0.0f};
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        if (lane == 0) part[k][warp] = s;
+            for (int d = 16; d > 0; d >>= 1) s.hi += __shfl_xor_sync(0xffffffffu, s.hi, d);
+        }
+        if (lane == 0) part[k][warp] = make_float2(s.hi, s.lo);
     }
     __syncthreads();
     Sum2 s = {};
     if (threadIdx.x < kSums)
-        for (int w = 0; w < kWarps; ++w) s.add(part[threadIdx.x][w]);
+        for (int w = 0; w < kWarps; ++w) s.join(part[threadIdx.x][w].x, part[threadIdx.x][w].y);
     return s;
 }
 
@@ -258,7 +268,7 @@ policy_kernel(Tokens t, Policy P, PolicyTokens a, Counts* counts, const uint32_t
     dependency_wait();
     const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const uint32_t tokens = counts->tokens, filled = counts->filled;
-    const Sum2 mine = policy_tokens(t, P, a, counts, starts, tokens, filled, aligned, blockIdx.x, gridDim.x);
+    const Sum2 mine = policy_tokens<false>(t, P, a, counts, starts, tokens, filled, aligned, blockIdx.x, gridDim.x);
     __shared__ bool last;
     if (threadIdx.x < kSums) {
         partial[blockIdx.x * kSums + threadIdx.x] = make_float2(mine.hi, mine.lo);
@@ -302,7 +312,7 @@ policy_cluster_kernel(Tokens t, Policy P, PolicyTokens a, Counts* counts, bool a
     const uint32_t rank = cluster_rank(), size = cluster_size();
     if (COUNT) count_in_cluster(t, counts, rank, size);
     const uint32_t tokens = __ldcg(&counts->tokens), filled = __ldcg(&counts->filled);
-    const Sum2 mine = policy_tokens(t, P, a, counts, nullptr, tokens, filled, aligned, rank, size);
+    const Sum2 mine = policy_tokens<true>(t, P, a, counts, nullptr, tokens, filled, aligned, rank, size);
     __shared__ float whole[kSums][2];
     __shared__ float mean[kSums];
     if (threadIdx.x < kSums) {
