@@ -4,10 +4,10 @@
 // Bound by HBM: the list is read for the norm and, its coefficient known only
 // after the last element, read again to be scaled (a list that fits the
 // 129 MB L2 comes from there the second time).  The OPT-1.3b list, 1.3B fp32
-// gradients into bf16: 1.90 ms, 6.9 TB/s over its two reads and one write (the
+// gradients into bf16: 1.89 ms, 7.0 TB/s over its two reads and one write (the
 // copy rate measured on this GPU is 6.67); the OPT-125m list 182 us from fp32,
 // 114 us from bf16.  Small lists are bound by the two kernels' latency: a
-// million elements in 37 tensors of two types take 6.9 us.
+// million elements in 37 tensors of two types take 6.8 us.
 #include <exception>
 #include <new>
 #include <type_traits>

@@ -4,9 +4,9 @@
 //
 // Both touch a few floats per token (policy 12 to 28 bytes, preference 9 to
 // 13).  Small batches are bound by the latency of their one launch (policy
-// loss of 1000 tokens 5.0 us, preference loss of 4 pairs 4.6 us).  Large ones
+// loss of 1000 tokens 5.7 us, preference loss of 4 pairs 4.4 us).  Large ones
 // are not yet bound by HBM: 2.1M ragged tokens with a reference, entropies and
-// per-token advantages take 26 us (61 MB, 2.3 TB/s; count, loss and the zeroing
+// per-token advantages take 27 us (61 MB, 2.3 TB/s; count, loss and the zeroing
 // before them), 2.1M even ones with less 20 us: about 680 instructions for 128
 // tokens issue in half of the cycles, between chains of dependent loads (a
 // warp's sequences, then their counts).  1024 pairs of 2048 tokens take 13 us
