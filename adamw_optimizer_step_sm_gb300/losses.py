@@ -179,12 +179,20 @@ def _like_rows(x: torch.Tensor) -> torch.Tensor:
 def _out_rows(out: Optional[torch.Tensor], x: torch.Tensor, rows: A.adamw_rows_t):
     """The tensor for the gradient of x, and its adamw_rows_t."""
     if out is None:
+        size = 4 if rows.dtype == A.DTYPE_FP32 else 2
+        if ((rows.data or 0) | (rows.row_stride | rows.outer_stride | rows.cols) * size) % 16 == 0:
+            # every row starts at a 16-byte boundary: so do a contiguous tensor's
+            out = _empty(x.shape, dtype=x.dtype, device=x.device)
+            d = _rows_t.from_buffer_copy(rows)
+            d.data, d.row_stride, d.outer_stride = out.data_ptr(), rows.cols, rows.inner * rows.cols
+            return out, d
         out = _like_rows(x)
     elif out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
         raise ValueError("out must have the logits' shape, type and device")
     if out.stride() == x.stride():
-        return out, _rows_t(out.data_ptr(), rows.rows, rows.inner, rows.outer_stride, rows.row_stride,
-                                   rows.cols, rows.dtype)
+        d = _rows_t.from_buffer_copy(rows)
+        d.data = out.data_ptr()
+        return out, d
     return out, _rows(out)
 
 

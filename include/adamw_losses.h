@@ -73,7 +73,8 @@ typedef struct {
  *   device fp32 [rows][2], 8-byte aligned, or NULL when no backward follows.
  * Errors: INVALID_ARG (NULL logits, targets or logp with rows > 0, negative
  * or inconsistent sizes or strides, unknown dtype, scale not positive and
- * finite), MISALIGNED, CUDA. */
+ * finite), MISALIGNED, TOO_LARGE (rows above 2^31 - 1, a stride above 2^40),
+ * CUDA. */
 int adamw_token_logprob(const adamw_rows_t* logits, const int64_t* targets, int64_t ignore_index,
                         float scale, float* logp, float* entropy, float* stats,
                         adamw_stream_t stream);

@@ -125,7 +125,7 @@ def test_logprob_and_gradient(n, v, dtype):
     assert torch.equal(e, d)
 
 
-@pytest.mark.parametrize("v", [50, 1501, 5003])
+@pytest.mark.parametrize("v", [50, 64, 1501, 5003, 9000])
 @pytest.mark.parametrize("view", ["shift", "tail", "pad", "batch_second", "odd_start"])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_logprob_strides(view, v, dtype):
