@@ -158,22 +158,21 @@ def _like_rows(x: torch.Tensor) -> torch.Tensor:
     """A new tensor for the gradient of x, its rows at the same strides and the
     same distance from a 16-byte boundary (both sides then take 16-byte
     accesses whatever the vocabulary's size), unless x is spread too thin."""
-    phase = x.data_ptr() % 16 // x.element_size()
-    if phase == 0 and x.is_contiguous():
-        return _empty(x.shape, dtype=x.dtype, device=x.device)
     shape, stride, n = x.shape, x.stride(), x.numel()
+    if len(shape) == 3 and n and stride[0] < stride[1]:   # [batch, tokens] stored as [tokens, batch]
+        return _like_rows(x.transpose(0, 1)).transpose(0, 1)
     span = 1   # elements from the first to the last, so far
     for s, k in zip(reversed(stride), reversed(shape)):
         if k > 1:
             if s < span:   # overlapping rows (an expanded tensor), or dimensions in another order
-                break
+                return _empty(shape, dtype=x.dtype, device=x.device)
             span += s * (k - 1)
-    else:
-        if n and span <= n + n // 4 + 64 * shape[-1]:
-            return _empty(span + phase, dtype=x.dtype, device=x.device).as_strided(shape, stride, phase)
-    if x.dim() == 3 and n and stride[0] < stride[1]:   # [batch, tokens] stored as [tokens, batch]
-        return _like_rows(x.transpose(0, 1)).transpose(0, 1)
-    return _empty(shape, dtype=x.dtype, device=x.device)
+    if n == 0 or span > n + n // 4 + 64 * shape[-1]:
+        return _empty(shape, dtype=x.dtype, device=x.device)
+    phase = x.data_ptr() % 16 // x.element_size()
+    if phase == 0:
+        return torch.empty_strided(shape, stride, dtype=x.dtype, device=x.device)
+    return _empty(span + phase, dtype=x.dtype, device=x.device).as_strided(shape, stride, phase)
 
 
 def _out_rows(out: Optional[torch.Tensor], x: torch.Tensor, rows: A.adamw_rows_t):
