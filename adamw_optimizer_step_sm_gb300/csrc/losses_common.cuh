@@ -589,6 +589,17 @@ struct Tokens {
         }
     }
 
+    // Whether N neighbouring tokens are all of sequence `s`.  All are compared:
+    // -1 stands on both sides of the sequences, so the ends may agree where
+    // the middle differs.
+    template <int N>
+    __device__ __forceinline__ static bool all_of(const int32_t (&seq)[N], int32_t s) {
+        bool same = true;
+#pragma unroll
+        for (int j = 0; j < N; ++j) same = same && seq[j] == s;
+        return same;
+    }
+
     // Which of the N <= 4 tokens from `first` on count, as bits.
     template <int N>
     __device__ __forceinline__ uint32_t counting(uint32_t first) const {

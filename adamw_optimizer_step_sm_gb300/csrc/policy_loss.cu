@@ -65,7 +65,7 @@ __device__ __forceinline__ void count_tokens(const Tokens& t, Counts* out, uint3
         // run by run of the lane's tokens; one atomic where the whole warp is
         // in one sequence
         const int32_t s0 = __shfl_sync(0xffffffffu, seq[0], 0);
-        const bool one = seq[0] == s0 && seq[kPerLane - 1] == s0;
+        const bool one = Tokens::all_of(seq, s0);
         if (__all_sync(0xffffffffu, one || bits == 0)) {
             const uint32_t k = __reduce_add_sync(0xffffffffu, uint32_t(__popc(bits)));
             if (lane == 0 && k && s0 >= 0) {
@@ -186,7 +186,7 @@ __device__ __forceinline__ Sum2 policy_tokens(const Tokens& t, const Policy& P, 
         t.sequences_of<kPerLane>(starts ? starts[base / kChunk] : t.starts_until(base), base, first, seq);
         // the weights and advantages of the lane's sequences, mostly one
         float weight[kPerLane], value[kPerLane];
-        const bool one = __all_sync(0xffffffffu, seq[0] == seq[kPerLane - 1]);
+        const bool one = __all_sync(0xffffffffu, Tokens::all_of(seq, seq[0]));
 #pragma unroll
         for (int j = 0; j < kPerLane; ++j) {
             if (j > 0 && one) {
