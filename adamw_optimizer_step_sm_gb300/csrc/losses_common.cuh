@@ -336,7 +336,9 @@ struct Online {
 };
 
 __device__ __forceinline__ bool extreme(float m, float c) { return m != -kInf && !(fabsf(m) * c < 1e38f); }
-__device__ __forceinline__ float reference(float m, float c) { return m == -kInf ? 0.0f : m * c; }
+// Rounded in every use alike: the compiler may not fuse the product into an
+// addition, where it would stay unrounded.
+__device__ __forceinline__ float reference(float m, float c) { return m == -kInf ? 0.0f : __fmul_rn(m, c); }
 
 // The exponent of an element, whatever m.
 __device__ __forceinline__ float exponent(float x, float m, float c) {
@@ -351,7 +353,7 @@ __device__ __forceinline__ void rebase(Online& o, float M, float c) {
         o.m = M;
         return;
     }
-    float d = extreme(o.m, c) || extreme(M, c) ? (o.m - M) * c : o.m * c - M * c;
+    float d = extreme(o.m, c) || extreme(M, c) ? (o.m - M) * c : __fsub_rn(reference(o.m, c), reference(M, c));
     d = fmaxf(d, -1e30f);
     const float f = exp2_fast(d);
     // d f before s: both d s and f's smallness may pass fp32's range

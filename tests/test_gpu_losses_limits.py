@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from adamw_optimizer_step_sm_gb300 import losses as L
-from test_gpu_losses import DEV, _check_policy, _policy64, _policy_inputs
+from test_gpu_losses import DEV, _check_policy, _close_logp, _gen, _policy64, _policy_inputs, _rows64
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +45,18 @@ def test_few_tokens_between_tokens_outside(n, at, reduce):
                 back = L.token_logprob_backward(data[4], data[5], lp, p.d_logp)
                 assert torch.isfinite(back).all() and back.abs().max() > 0
                 assert (r.d_logits - back).abs().max() <= 1e-6 * back.abs().max()
+
+
+# ------------------------------------------------------- maxima along a row
+
+@pytest.mark.parametrize("offset", [1000.0, -1000.0, 8000.0])
+@pytest.mark.parametrize("n,v", [(3, 4096), (160, 50272)])
+def test_maxima_that_rise_along_a_row(n, v, offset):
+    """Every batch of a thread has a new maximum, far from 0: the products of
+    maximum and scale round, and a record moves by what they rounded to."""
+    x = torch.linspace(0, 8, v) + 0.1 * torch.rand(n, v, generator=_gen(v)) + offset
+    t = torch.randint(0, v, (n,), generator=_gen(n))
+    want = _rows64(x, t, 1.0)
+    r = L.token_logprob(x.to(DEV), t.to(DEV), entropy=True)
+    _close_logp(r.logp, want[0])
+    _close_logp(r.entropy, want[1])
