@@ -21,6 +21,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInf = std::numeric_limits<float>::infinity();
+constexpr float kMaxFloat = std::numeric_limits<float>::max();
 
 // ------------------------------------------------------- pairs of floats --
 
@@ -96,7 +97,8 @@ struct Elem<ADAMW_DTYPE_BF16> {
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
     // -inf to -1e30 before the arithmetic, two elements to an instruction
-    // (what above() does after it); NaN stays
+    // (what above() does after it); NaN stays.  For elements beside a maximum
+    // that is not extreme: what it raises to -1e30 has probability 0 there.
     static constexpr bool kClamps = true;
     __device__ static uint32_t clamped(uint32_t w) {
         const __nv_bfloat162 r = __hmax2_nan(word<__nv_bfloat162>(w), __float2bfloat162_rn(-1e30f));
@@ -329,16 +331,24 @@ __device__ __forceinline__ Sum2 warp_sum(Sum2 a) {
 // with r = c m as rounded to fp32, so that each exponent is one fused
 // multiply-add, rounded once.  -inf elements (and an empty record) leave m at
 // -inf and add nothing; r is then 0, so that -inf - (-inf) does not arise.
-// Where c m is near or past fp32's range (rows masked throughout by the
-// type's lowest value) the exponents are (x - m) c instead.
+// The largest element's own exponent is what r was rounded by: up to 32 where
+// |c m| < 2^30.  Beyond that ("extreme": masks by large finite numbers) it soon
+// leaves fp32's range, but there neighbouring floats are 64 and more apart in
+// the exponent: nothing below such a maximum counts beside it.  So a record
+// with an extreme maximum holds no sums (s is NaN where it saw a NaN, else
+// unspecified); they are dropped when a larger element comes, and a row whose
+// largest element is extreme counts the elements equal to it (row_join).
 struct Online {
     float m, s, t;
 };
 
-__device__ __forceinline__ bool extreme(float m, float c) { return m != -kInf && !(fabsf(m) * c < 1e38f); }
+__device__ __forceinline__ bool extreme(float m, float c) { return m != -kInf && !(fabsf(m) * c < 0x1p30f); }
 // Rounded in every use alike: the compiler may not fuse the product into an
-// addition, where it would stay unrounded.
-__device__ __forceinline__ float reference(float m, float c) { return m == -kInf ? 0.0f : __fmul_rn(m, c); }
+// addition, where it would stay unrounded.  Not -inf where m is finite: a -inf
+// element less that would be NaN.
+__device__ __forceinline__ float reference(float m, float c) {
+    return m == -kInf ? 0.0f : fmaxf(__fmul_rn(m, c), -kMaxFloat);
+}
 
 // The exponent of an element, whatever m.
 __device__ __forceinline__ float exponent(float x, float m, float c) {
@@ -353,8 +363,13 @@ __device__ __forceinline__ void rebase(Online& o, float M, float c) {
         o.m = M;
         return;
     }
-    float d = extreme(o.m, c) || extreme(M, c) ? (o.m - M) * c : __fsub_rn(reference(o.m, c), reference(M, c));
-    d = fmaxf(d, -1e30f);
+    if (extreme(o.m, c)) {
+        o.s = o.s == o.s ? 0.0f : o.s;
+        if (ENT) o.t = 0.0f;
+        o.m = M;
+        return;
+    }
+    const float d = fmaxf(__fsub_rn(reference(o.m, c), reference(M, c)), -1e30f);
     const float f = exp2_fast(d);
     // d f before s: both d s and f's smallness may pass fp32's range
     if (ENT) o.t = fmaf(d * f, o.s, o.t * f);
@@ -386,15 +401,6 @@ __device__ __forceinline__ void absorb(Online& o, const uint4 (&v)[U], float c) 
     using E = Elem<DT>;
     const float m = E::largest(v);
     if (m > o.m) rebase<ENT>(o, m, c);
-    if (extreme(o.m, c)) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float x[E::kVec];
-            E::unpack(v[u], x);
-            for (int i = 0; i < E::kVec; ++i) absorb_one<ENT>(o, x[i], c);
-        }
-        return;
-    }
     const float r = -reference(o.m, c);
     const Pair c2 = pair(c, c), r2 = pair(r, r);
     Pair s = pair(0.0f, 0.0f), t = s;

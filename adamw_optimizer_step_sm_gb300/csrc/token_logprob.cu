@@ -74,6 +74,28 @@ __device__ __forceinline__ Online group_join(Online o, float c) {
     return o;
 }
 
+// The record of a group's row: group_join, and where its largest element is
+// extreme, how many are equal to it (a second pass, over such rows only).
+// v(i): the i-th of the CTA's n vectors.  xe: the thread's extra element, or
+// -inf.
+template <int DT, bool ENT, bool WARP, int THREADS, typename Load>
+__device__ __forceinline__ Online row_join(Online o, float c, const Load& v, int n, int lane, float xe) {
+    using E = Elem<DT>;
+    constexpr int width = WARP ? 32 : THREADS;
+    o = group_join<ENT, WARP, THREADS>(o, c);
+    if (!extreme(o.m, c) || o.s != o.s) return o;   // the whole group
+    float count = xe == o.m ? 1.0f : 0.0f;
+#pragma unroll 1
+    for (int i = lane; i < n; i += width) {
+        float x[E::kVec];
+        E::unpack(v(i), x);
+#pragma unroll
+        for (int j = 0; j < E::kVec; ++j) count += x[j] == o.m ? 1.0f : 0.0f;
+    }
+    if (!WARP) __syncthreads();   // the first join's records have been read
+    return group_join<false, WARP, THREADS>({o.m, count, 0.0f}, c);
+}
+
 // ---------------------------------------------------------------- forward --
 
 // Log-probability and entropy of one row per group (a warp; or a cluster of
@@ -112,7 +134,8 @@ logprob_kernel(Rows logits, uint32_t rows, int cols, const int64_t* targets, int
 
     Online o = {-kInf, 0.0f, 0.0f};
     const int extra = extra_element<DT>(sp, lane, rank == 0, rank == size - 1);
-    if (extra >= 0) absorb_one<ENT>(o, E::load(row, extra), c);
+    const float xe = extra >= 0 ? E::load(row, extra) : -kInf;
+    if (extra >= 0) absorb_one<ENT>(o, xe, c);
     int base = first + lane;
     for (; base + (kForwardUnroll - 1) * width < end; base += kForwardUnroll * width) {
         uint4 v[kForwardUnroll];
@@ -128,7 +151,13 @@ logprob_kernel(Rows logits, uint32_t rows, int cols, const int64_t* targets, int
                                           : make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf);
         absorb<DT, ENT>(o, v, c);
     }
-    o = group_join<ENT, WARP, kForwardThreads>(o, c);
+    // for a second pass the row is found again: five registers less over the
+    // first, a CTA more on an SM
+    auto again = [&](int i) {
+        const char* row = logits.at(r);
+        return load16(row + int64_t(RowSplit<DT>(row, cols).head) * E::kSize + (int64_t(first) + i) * 16);
+    };
+    o = row_join<DT, ENT, WARP, kForwardThreads>(o, c, again, end - first, lane, xe);
     if (!writer) return;
     const bool bad = t < 0 || t >= cols;
     RowStats rs = row_stats<ENT>(o);
@@ -356,7 +385,7 @@ policy_rows_kernel(Rows logits, Rows grad, Tokens tokens, int cols, float scale,
         }
         ask();
     }
-    o = group_join<ENT, WARP, kPolicyThreads>(o, c);
+    o = row_join<DT, ENT, WARP, kPolicyThreads>(o, c, [slice](int i) { return slice[i]; }, n, lane, xe);
 
     RowStats rs = row_stats<ENT>(o);
     if (bad) rs.m = rs.s = rs.log_s = rs.entropy = __int_as_float(0x7fc00000);

@@ -7,7 +7,8 @@ import pytest
 import torch
 
 from adamw_optimizer_step_sm_gb300 import losses as L
-from test_gpu_losses import DEV, _check_policy, _close_logp, _gen, _policy64, _policy_inputs, _rows64
+from test_gpu_losses import (DEV, ROUND, TYPES, _check_policy, _close_grad, _close_logp, _gen, _grad64, _policy64,
+                             _policy_inputs, _rows64)
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +61,84 @@ def test_maxima_that_rise_along_a_row(n, v, offset):
     r = L.token_logprob(x.to(DEV), t.to(DEV), entropy=True)
     _close_logp(r.logp, want[0])
     _close_logp(r.entropy, want[1])
+
+
+# -------------------------------------------------- masks by finite numbers
+
+def _masked_rows(v, dtype, mask):
+    """Rows masked by `mask`: throughout, in a leading stretch, all but a few,
+    in isolated aligned groups, and not; with their targets."""
+    x = (torch.randn(6, v, generator=_gen(v)) * 3).to(TYPES[dtype])
+    t = torch.tensor([v // 2, v - 1, v - 2, v - 3, 1, v // 3])
+    x[0] = mask
+    x[1, : v * 3 // 4] = mask
+    keep = x[2, v - 5:].clone()
+    x[2] = mask
+    x[2, v - 5:] = keep
+    for k in range(0, v - 32, 64):
+        x[3, k:k + 8] = mask
+    x[4] = mask
+    x[4, 2] = 2 * mask if mask > torch.finfo(TYPES[dtype]).min / 2 else mask   # one entry below the others
+    return x, t
+
+
+MASKS = [("fp32", 1.0, m) for m in (-1e8, -1e9, -1e10, -1e12, -1e30, -1e37)] + \
+        [("fp32", 1.0, torch.finfo(torch.float32).min), ("fp32", 6.0, torch.finfo(torch.float32).min)] + \
+        [("bf16", 1.0, m) for m in (-1e9, -1e10, -1e30, -1e32, -1e37)] + \
+        [("bf16", 6.0, torch.finfo(torch.bfloat16).min), ("bf16", 0.7, -1e10), ("fp16", 1e-3, -60000.0)]
+
+
+@pytest.mark.parametrize("dtype,temperature,mask", MASKS)
+@pytest.mark.parametrize("v", [40, 1000, 3001, 9000, 50272])
+def test_masks_by_large_finite_numbers(v, dtype, temperature, mask):
+    x, t = _masked_rows(v, dtype, mask)
+    n, scale = x.shape[0], 1 / temperature
+    want = _rows64(x, t, scale)
+    xd, td = x.to(DEV), t.to(DEV)
+    _close_logp(L.token_logprob(xd, td, temperature=temperature).logp, want[0])
+    r = L.token_logprob(xd, td, temperature=temperature, entropy=True)
+    _close_logp(r.logp, want[0])
+    _close_logp(r.entropy, want[1])
+    g = _gen(1)
+    dl, dh = torch.randn(n, generator=g), 0.3 * torch.randn(n, generator=g)
+    for h in (None, dh):
+        d = L.token_logprob_backward(xd, td, r, dl.to(DEV), None if h is None else h.to(DEV), temperature=temperature)
+        w = _grad64(want, t, dl.double(), None if h is None else h.double(), scale)
+        # as _close_grad, and where the target's probability is near 1 its
+        # gradient is a difference of numbers of size scale |dl|: 4 u of that
+        tol = 1e-5 * w.abs().amax(1, keepdim=True) + 2.4e-7 * scale * dl.abs()[:, None].double() \
+            + ROUND[dtype] * w.abs() + (2.0 ** -25 if dtype == "fp16" else 1e-38)
+        assert ((d.cpu().double() - w).abs() <= tol).all()
+    # and from logits: ratio 1, so the gradient is that of -A logp - 0.1 entropy, a token's weight 1 / n
+    old = r.logp
+    adv = torch.randn(n, generator=g)
+    p = L.policy_loss_logits(xd, td, old, adv.to(DEV), entropy_coef=0.1, temperature=temperature)
+    _close_logp(p.logp, want[0])
+    _close_logp(p.entropy, want[1])
+    w = _grad64(want, t, -adv.double() / n, torch.full((n,), -0.1 / n, dtype=torch.float64), scale)
+    # the ratio is 1 to within the difference of the two calls' logp, two ulps of each
+    top = w.abs().amax(1, keepdim=True)
+    tol = (3e-5 + 5e-7 * want[0].abs()[:, None]) * (top + scale / n) + ROUND[dtype] * w.abs() + (2.0 ** -25 if dtype == "fp16" else 1e-38)
+    assert ((p.d_logits.cpu().double() - w).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("v", [256, 4096, 50272])
+@pytest.mark.parametrize("center,step,offset", [(46516320.0, 4, 2), (744261120.0, 64, 32)])
+def test_logits_where_their_product_with_the_scale_is_coarse(v, sign, center, step, offset):
+    """Rising logits around 2^26 / log2 e and 2^30 / log2 e, fp32's spacing there
+    apart.  The row's largest element may have an exponent of its own, up to
+    `offset`: what is added and taken off again for it costs 4 u of it."""
+    steps = torch.linspace(-30, 0, v).round() + torch.randint(-3, 4, (5, v), generator=_gen(v)).float()
+    x = sign * center + step * steps
+    t = torch.randint(0, v, (5,), generator=_gen(3))
+    want = _rows64(x, t, 1.0)
+    r = L.token_logprob(x.to(DEV), t.to(DEV), entropy=True)
+    for got, exact in ((r.logp, want[0]), (r.entropy, want[1])):
+        tol = 4e-6 + 2e-6 * exact.abs() + 2.4e-7 * offset
+        assert ((got.cpu().double() - exact).abs() <= tol).all()
+    dl = torch.randn(5, generator=_gen(4))
+    d = L.token_logprob_backward(x.to(DEV), t.to(DEV), r, dl.to(DEV))
+    w = _grad64(want, t, dl.double(), None, 1.0)
+    tol = 1e-5 * w.abs().amax(1, keepdim=True) + 2.4e-7 * dl.abs()[:, None].double()
+    assert ((d.cpu().double() - w).abs() <= tol).all()
