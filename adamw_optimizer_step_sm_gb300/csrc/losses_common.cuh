@@ -51,9 +51,11 @@ __device__ __forceinline__ Pair mul2(Pair a, Pair b) {
     return d;
 }
 
-// -inf to a number whose product with a vanished exponential is 0; NaN to
-// itself or to that number (its exponential is NaN already).
-__device__ __forceinline__ Pair above(Pair d) { return pair(fmaxf(low(d), -1e30f), fmaxf(high(d), -1e30f)); }
+// Exponents that vanish all the same, to one whose product with the vanished
+// exponential is 0 (not 0 * inf) and stays finite times a gradient; NaN to itself
+// or to that number (its exponential is NaN already).
+constexpr float kVanished = -1e4f;
+__device__ __forceinline__ Pair above(Pair d) { return pair(fmaxf(low(d), kVanished), fmaxf(high(d), kVanished)); }
 
 // A 32-bit register as two 16-bit floats.
 template <typename T>
@@ -96,19 +98,6 @@ struct Elem<ADAMW_DTYPE_BF16> {
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    // -inf to -1e30 before the arithmetic, two elements to an instruction
-    // (what above() does after it); NaN stays.  For elements beside a maximum
-    // that is not extreme: what it raises to -1e30 has probability 0 there.
-    static constexpr bool kClamps = true;
-    __device__ static uint32_t clamped(uint32_t w) {
-        const __nv_bfloat162 r = __hmax2_nan(word<__nv_bfloat162>(w), __float2bfloat162_rn(-1e30f));
-        uint32_t u;
-        memcpy(&u, &r, 4);
-        return u;
-    }
-    __device__ static uint4 clamped(uint4 v) {
-        return make_uint4(clamped(v.x), clamped(v.y), clamped(v.z), clamped(v.w));
-    }
     // the vector as pairs of floats; the largest element of some vectors
     __device__ static void pairs(uint4 v, Pair* x) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -141,8 +130,6 @@ struct Elem<ADAMW_DTYPE_FP16> {
     static constexpr int kSize = 2, kVec = 8;
     static constexpr uint32_t kNegInf = 0xfc00fc00u;
     static constexpr uint32_t kSigns = 0x80008000u;
-    static constexpr bool kClamps = false;  // it has no such number
-    __device__ static uint4 clamped(uint4 v) { return v; }
     __device__ static float load(const void* p, int64_t i) {
         return __half2float(static_cast<const __half*>(p)[i]);
     }
@@ -203,8 +190,6 @@ struct Elem<ADAMW_DTYPE_FP32> {
     static constexpr int kSize = 4, kVec = 4;
     static constexpr uint32_t kNegInf = 0xff800000u;
     static constexpr uint32_t kSigns = 0x80000000u;
-    static constexpr bool kClamps = false;  // no packed maximum
-    __device__ static uint4 clamped(uint4 v) { return v; }
     __device__ static float load(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
     __device__ static void store(void* p, int64_t i, float x) { static_cast<float*>(p)[i] = x; }
     __device__ static void unpack(uint4 v, float* x) {
@@ -392,7 +377,7 @@ __device__ __forceinline__ void absorb_one(Online& o, float x, float c) {
     const float d = exponent(x, o.m, c);
     const float e = exp2_fast(d);
     o.s += e;
-    if (ENT) o.t = fmaf(e, fmaxf(d, -1e30f), o.t);   // -inf: 0 * (large), not 0 * inf
+    if (ENT) o.t = fmaf(e, fmaxf(d, kVanished), o.t);
 }
 
 // Adds the elements of U vectors.
@@ -407,13 +392,13 @@ __device__ __forceinline__ void absorb(Online& o, const uint4 (&v)[U], float c) 
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         Pair x[E::kVec / 2];
-        E::pairs(ENT && E::kClamps ? E::clamped(v[u]) : v[u], x);
+        E::pairs(v[u], x);
 #pragma unroll
         for (int i = 0; i < E::kVec / 2; ++i) {
             const Pair d = fma2(x[i], c2, r2);
             const Pair e = pair(exp2_fast(low(d)), exp2_fast(high(d)));
             s = add2(s, e);
-            if (ENT) t = fma2(e, E::kClamps ? d : above(d), t);
+            if (ENT) t = fma2(e, above(d), t);
         }
     }
     o.s += low(s) + high(s);
@@ -469,7 +454,7 @@ struct Gradient {
     template <bool ENT>
     __device__ __forceinline__ float of(float x) const {
         const float d = exponent(x, m, c), e = exp2_fast(d);
-        return ENT ? e * fmaf(B, fmaxf(d, -1e30f), A) : e * A;
+        return ENT ? e * fmaf(B, fmaxf(d, kVanished), A) : e * A;
     }
     // of a vector of an ordinary row
     template <int DT, bool ENT>
@@ -478,12 +463,12 @@ struct Gradient {
         const float r = -reference(m, c);
         const Pair c2 = pair(c, c), r2 = pair(r, r), A2 = pair(A, A), B2 = pair(B, B);
         Pair x[E::kVec / 2];
-        E::pairs(ENT && E::kClamps ? E::clamped(v) : v, x);
+        E::pairs(v, x);
 #pragma unroll
         for (int i = 0; i < E::kVec / 2; ++i) {
             const Pair d = fma2(x[i], c2, r2);
             const Pair e = pair(exp2_fast(low(d)), exp2_fast(high(d)));
-            x[i] = mul2(e, ENT ? fma2(B2, E::kClamps ? d : above(d), A2) : A2);
+            x[i] = mul2(e, ENT ? fma2(B2, above(d), A2) : A2);
         }
         return E::pack_pairs(x);
     }

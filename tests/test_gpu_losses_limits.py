@@ -7,8 +7,8 @@ import pytest
 import torch
 
 from adamw_optimizer_step_sm_gb300 import losses as L
-from test_gpu_losses import (DEV, ROUND, TYPES, _check_policy, _close_grad, _close_logp, _gen, _grad64, _policy64,
-                             _policy_inputs, _rows64)
+from test_gpu_losses import (DEV, INF, ROUND, TYPES, _check_policy, _close_logp, _gen, _grad64,
+                             _policy64, _policy_inputs, _rows64)
 
 pytestmark = pytest.mark.gpu
 
@@ -142,3 +142,44 @@ def test_logits_where_their_product_with_the_scale_is_coarse(v, sign, center, st
     w = _grad64(want, t, dl.double(), None, 1.0)
     tol = 1e-5 * w.abs().amax(1, keepdim=True) + 2.4e-7 * dl.abs()[:, None].double()
     assert ((d.cpu().double() - w).abs() <= tol).all()
+
+
+# ------------------------------------------------------ extreme temperatures
+
+@pytest.mark.parametrize("temperature", [1e-19, 1e-12, 1e-9, 1e-7, 1e-5, 1e22, 1e32])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("v", [40, 3001, 9000])
+def test_extreme_temperatures(v, dtype, temperature):
+    x, t = _rows_with_masks(v, dtype)
+    scale = 1 / temperature
+    want = _rows64(x, t, scale)
+    xd, td = x.to(DEV), t.to(DEV)
+    r = L.token_logprob(xd, td, temperature=temperature, entropy=True)
+    _close_logp(r.logp, want[0])
+    _close_logp(r.entropy, want[1])
+    one = torch.ones(4, device=DEV)
+    d = L.token_logprob_backward(xd, td, r, one, 0.5 * one, temperature=temperature)
+    w = _grad64(want, t, torch.ones(4).double(), torch.full((4,), 0.5).double(), scale)
+    if dtype == "fp16":
+        w = torch.where(w.abs() > 65504, w.sign() * INF, w)   # what does not fit the type
+    got = d.cpu().double()
+    big = torch.isinf(w)
+    assert torch.equal(got[big], w[big])
+    w[big], got[big] = 0.0, 0.0
+    # as _close_grad, and 4 u of what is added and taken off again: the target's
+    # own gradient (its p is 1), and up to 32 times the entropy's for the exponent
+    # of the row's largest element, which is 0 where that is past 2^30
+    slack = 2.4e-7 * scale * (1 + 32 * 0.5) if 15.0625 * 1.4427 * scale < 2 ** 30 else 0.0
+    tol = 1e-5 * w.abs().amax(1, keepdim=True) + slack + ROUND[dtype] * w.abs() + (2.0 ** -25 if dtype == "fp16" else 1e-38)
+    assert ((got - w).abs() <= tol).all()
+
+
+def _rows_with_masks(v, dtype):
+    """Four rows of distinct best logits with some entries masked by -inf (in
+    one a whole leading stretch, in one everything but one)."""
+    x = (torch.randn(4, v, generator=_gen(v)) * 3).to(TYPES[dtype])
+    x[:, ::5] = -INF
+    x[2, : v * 3 // 4] = -INF
+    x[3] = -INF
+    x[:, v - 2] = 15.0625    # the best, and the target
+    return x, torch.full((4,), v - 2)
