@@ -344,6 +344,15 @@ __device__ __forceinline__ float sigmoid(float x) {
     return x >= 0.0f ? 1.0f / (1.0f + e) : e / (1.0f + e);
 }
 
+// s / n as a pair of floats: the rounded quotient and what it leaves.
+__device__ __forceinline__ Sum2 quotient(const Sum2& s, float n) {
+    const float v = s.value(), q = v / n;
+    if (!isfinite(v)) return {q, 0.0f};
+    // v and s - v, both exact, less q n, whose fused difference from v is exact
+    const float rest = __fadd_rn(__fsub_rn(s.hi, v), s.lo);
+    return {q, __fadd_rn(fmaf(-q, n, v), rest) / n};
+}
+
 constexpr int kMaxWarps = 32;
 
 // Tokens of a thread on their way at a time.  Measured (us, 2 / 4 / 8): 4 pairs
@@ -434,7 +443,8 @@ __device__ __forceinline__ PairResult preference_pair(const Tokens& t, const Pre
         whole[threadIdx.x][2] = __uint_as_float(k);
     }
     if (SHARED) cluster_sync(); else __syncthreads();
-    float S[2], share[2];
+    Sum2 S[2];
+    float share[2];
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
         Sum2 s = {};
@@ -449,12 +459,18 @@ __device__ __forceinline__ PairResult preference_pair(const Tokens& t, const Pre
             k = __float_as_uint(whole[side][2]);
         }
         if (P.ref == ADAMW_REF_SEQUENCE) s.add(-ref[pair + (side ? pairs : 0)]);
-        share[side] = P.average ? 1.0f / float(k > 0 ? k : 1) : 1.0f;
-        S[side] = P.average ? s.value() / float(k > 0 ? k : 1) : s.value();
+        const float n = float(k > 0 ? k : 1);
+        share[side] = P.average ? 1.0f / n : 1.0f;
+        S[side] = P.average ? quotient(s, n) : s;
     }
     // the records stay until all have read them
     if (SHARED) cluster_sync(); else __syncthreads();
-    const float D = S[0] - S[1];
+    // the difference of the pairs of floats, rounded once: two long answers'
+    // sums are large and may nearly cancel
+    Sum2 difference = S[0];
+    difference.join(-S[1].hi, -S[1].lo);
+    const float D = difference.value();
+    const float reward[2] = {P.beta * S[0].value(), P.beta * S[1].value()};
     const float h = P.beta * D - P.margin;
     float loss, dD;
     if (P.kind == ADAMW_PREF_SIGMOID) {
@@ -471,8 +487,8 @@ __device__ __forceinline__ PairResult preference_pair(const Tokens& t, const Pre
     }
     if (rank == 0 && threadIdx.x == 0) {
         losses[pair] = loss;
-        rewards[pair] = P.beta * S[0];
-        rewards[pairs + pair] = P.beta * S[1];
+        rewards[pair] = reward[0];
+        rewards[pairs + pair] = reward[1];
     }
     const float g = P.grad_scale * dD / float(pairs);
 #pragma unroll
@@ -489,7 +505,7 @@ __device__ __forceinline__ PairResult preference_pair(const Tokens& t, const Pre
     if (t.offsets && pair == pairs - 1) {
         for (int64_t i = end[1] + me; i < int64_t(t.n); i += width) d_logp[i] = 0.0f;
     }
-    return {loss, P.beta * S[0] - P.beta * S[1]};
+    return {loss, reward[0] - reward[1]};
 }
 
 // A cluster (or CTA) per pair.

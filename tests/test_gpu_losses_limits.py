@@ -8,7 +8,7 @@ import torch
 
 from adamw_optimizer_step_sm_gb300 import losses as L
 from test_gpu_losses import (DEV, INF, ROUND, TYPES, _check_policy, _close_logp, _gen, _grad64,
-                             _policy64, _policy_inputs, _rows64)
+                             _policy64, _policy_inputs, _preference64, _rows64)
 
 pytestmark = pytest.mark.gpu
 
@@ -183,3 +183,41 @@ def _rows_with_masks(v, dtype):
     x[3] = -INF
     x[:, v - 2] = 15.0625    # the best, and the target
     return x, torch.full((4,), v - 2)
+
+
+# --------------------------------------------------------- preference losses
+
+def _long_pairs(pairs, length, seed):
+    """Answers of about `length` tokens and their log-probabilities of about -2,
+    on a grid of 2^-12 (sums are exact in 64 bits), the two sums of a pair close."""
+    g = _gen(seed)
+    grid = lambda v: (v * 4096).round() / 4096
+    logp = -grid(torch.rand(2 * pairs, length, generator=g) * 4)
+    logp[pairs:] = logp[:pairs][:, torch.randperm(length, generator=g)]
+    for i in range(pairs):   # differences of 2^-12 and more, of either sign, and none
+        logp[pairs + i, i % length] += [1, -1, 3, 0, -40, 4096][i % 6] / 4096
+    return logp
+
+
+@pytest.mark.parametrize("pairs,length", [(3, 2500), (12, 4096), (40, 8191), (2, 70001)])
+@pytest.mark.parametrize("kind", ["sigmoid", "hinge", "ipo"])
+@pytest.mark.parametrize("average", [False, True])
+def test_preference_sums_that_nearly_cancel(pairs, length, kind, average):
+    """Long answers without a reference: D is the difference of the unrounded
+    sums.  Their pairs of floats are good to some 2^-46 of the size of what they
+    hold, over thousands of additions and a few joins to 2^-40; then one rounding."""
+    logp = _long_pairs(pairs, length, length)
+    rows = 2 * pairs
+    starts = [i * length for i in range(rows + 1)]
+    o = dict(ref=None, average=average, beta=0.1, margin=0.0, kind=kind, eps=0.0)
+    losses, rewards, grad, D, h = _preference64(logp.reshape(-1), None, torch.ones(rows * length, dtype=torch.bool),
+                                                starts, o)
+    got = L.preference_loss(logp.to(DEV), beta=0.1, kind=kind, length_average=average)
+    size = logp.double().abs().sum(1) / (length if average else 1)
+    dD = 3e-7 * D.abs() + 2.0 ** -40 * (size[:pairs] + size[pairs:])
+    assert ((got.rewards.cpu().double() - rewards).abs() <= 3e-7 * rewards.abs()).all()
+    slope = 2 * (D - 5).abs() if kind == "ipo" else torch.full_like(D, 0.1)
+    assert ((got.losses.cpu().double() - losses).abs() <= slope * dD + dD * dD + 1e-6 * losses.abs()).all()
+    second = {"sigmoid": 0.0025, "hinge": 0.0, "ipo": 2.0}[kind]
+    tol = (second * dD / pairs / (length if average else 1)).repeat(2).repeat_interleave(length)
+    assert ((got.d_logp.cpu().double().reshape(-1) - grad).abs() <= 2e-6 * grad.abs() + tol + 1e-12).all()
