@@ -386,15 +386,37 @@ __device__ __forceinline__ void sum_side(const Tokens& t, bool has_ref, const fl
     }
 }
 
-// h without the margin, from the rewards, which also order the pair.
+// A pair's loss, its h, and the derivative with respect to D.
+struct PairLoss {
+    float loss, h, dD;
+};
+__device__ __forceinline__ PairLoss pair_loss(const Preference& P, float D) {
+    const float h = P.beta * D - P.margin;
+    float loss, dD;
+    if (P.kind == ADAMW_PREF_SIGMOID) {
+        loss = (1.0f - P.smoothing) * softplus(-h) + P.smoothing * softplus(h);
+        dD = P.beta * (P.smoothing * sigmoid(h) - (1.0f - P.smoothing) * sigmoid(-h));
+    } else if (P.kind == ADAMW_PREF_HINGE) {
+        const float u = 1.0f - h;
+        loss = u < 0.0f ? 0.0f : u;  // NaN stays
+        dD = h < 1.0f ? -P.beta : h >= 1.0f ? 0.0f : h;
+    } else {
+        const float u = D - 0.5f / P.beta;
+        loss = u * u;
+        dD = 2.0f * u;
+    }
+    return {loss, h, dD};
+}
+
 struct PairResult {
-    float loss, h;
+    float loss, h, D;
 };
 
 // One pair by a group of CTAs (SHARED: a cluster; else one): each sums its
 // share of the two sequences' log ratios, the group joins them, and every CTA
-// writes its share of the gradient.
-template <bool SHARED>
+// writes its share of the gradient.  losses[pair] receives the loss, or with
+// LATER the pair's D, for the kernel of the statistics to go on from.
+template <bool SHARED, bool LATER>
 __device__ __forceinline__ PairResult preference_pair(const Tokens& t, const Preference& P, const float* logp,
                                                       const float* ref, float* losses, float* rewards,
                                                       float* d_logp, uint32_t pair, uint32_t rank,
@@ -470,27 +492,13 @@ __device__ __forceinline__ PairResult preference_pair(const Tokens& t, const Pre
     Sum2 difference = S[0];
     difference.join(-S[1].hi, -S[1].lo);
     const float D = difference.value();
-    const float reward[2] = {P.beta * S[0].value(), P.beta * S[1].value()};
-    const float h = P.beta * D - P.margin;
-    float loss, dD;
-    if (P.kind == ADAMW_PREF_SIGMOID) {
-        loss = (1.0f - P.smoothing) * softplus(-h) + P.smoothing * softplus(h);
-        dD = P.beta * (P.smoothing * sigmoid(h) - (1.0f - P.smoothing) * sigmoid(-h));
-    } else if (P.kind == ADAMW_PREF_HINGE) {
-        const float u = 1.0f - h;
-        loss = u < 0.0f ? 0.0f : u;  // NaN stays
-        dD = h < 1.0f ? -P.beta : h >= 1.0f ? 0.0f : h;
-    } else {
-        const float u = D - 0.5f / P.beta;
-        loss = u * u;
-        dD = 2.0f * u;
-    }
+    const PairLoss l = pair_loss(P, D);
     if (rank == 0 && threadIdx.x == 0) {
-        losses[pair] = loss;
-        rewards[pair] = reward[0];
-        rewards[pairs + pair] = reward[1];
+        losses[pair] = LATER ? D : l.loss;
+        rewards[pair] = P.beta * S[0].value();
+        rewards[pairs + pair] = P.beta * S[1].value();
     }
-    const float g = P.grad_scale * dD / float(pairs);
+    const float g = P.grad_scale * l.dD / float(pairs);
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
         const float v = (side ? -g : g) * share[side];
@@ -505,7 +513,7 @@ __device__ __forceinline__ PairResult preference_pair(const Tokens& t, const Pre
     if (t.offsets && pair == pairs - 1) {
         for (int64_t i = end[1] + me; i < int64_t(t.n); i += width) d_logp[i] = 0.0f;
     }
-    return {loss, reward[0] - reward[1]};
+    return {l.loss, l.h, D};
 }
 
 // A cluster (or CTA) per pair.
@@ -516,22 +524,23 @@ preference_kernel(Tokens t, Preference P, const float* logp, const float* ref, f
     dependency_trigger();
     dependency_wait();
     const uint32_t size = SHARED ? cluster_size() : 1, rank = SHARED ? cluster_rank() : 0;
-    preference_pair<SHARED>(t, P, logp, ref, losses, rewards, d_logp, blockIdx.x / size, rank, size);
+    preference_pair<SHARED, true>(t, P, logp, ref, losses, rewards, d_logp, blockIdx.x / size, rank, size);
 }
 
-// The statistics over the pairs.
+// The losses and the statistics over the pairs, from each pair's D in losses[].
 __global__ void __launch_bounds__(kThreads)
-preference_stats_kernel(uint32_t pairs, Preference P, const float* losses, const float* rewards,
-                        float* stats) {
+preference_stats_kernel(uint32_t pairs, Preference P, float* losses, float* stats) {
     dependency_trigger();
     dependency_wait();
     Sum2 loss = {}, h = {};
     uint32_t right = 0;
     for (uint32_t i = threadIdx.x; i < pairs; i += kThreads) {
-        const float d = rewards[i] - rewards[pairs + i];
-        loss.add(losses[i]);
-        h.add(d - P.margin);
-        right += d > 0.0f;
+        const float D = losses[i];
+        const PairLoss l = pair_loss(P, D);
+        losses[i] = l.loss;
+        loss.add(l.loss);
+        h.add(l.h);
+        right += D > 0.0f;
     }
     __shared__ float2 part[2][kWarps];
     __shared__ uint32_t rights[kWarps];
@@ -567,10 +576,10 @@ preference_cluster_kernel(Tokens t, Preference P, const float* logp, const float
     Sum2 loss = {}, h = {};
     uint32_t right = 0;
     for (uint32_t pair = rank; pair < pairs; pair += size) {
-        const PairResult r = preference_pair<false>(t, P, logp, ref, losses, rewards, d_logp, pair, 0, 1);
+        const PairResult r = preference_pair<false, false>(t, P, logp, ref, losses, rewards, d_logp, pair, 0, 1);
         loss.add(r.loss);
-        h.add(r.h - P.margin);
-        right += r.h > 0.0f;
+        h.add(r.h);
+        right += r.D > 0.0f;
     }
     __shared__ float mine[5];
     if (threadIdx.x == 0) {
@@ -744,8 +753,7 @@ extern "C" int adamw_preference_loss(const adamw_tokens_t* tokens, const adamw_p
     if (!launched(launch(kernel, uint32_t(pairs * cluster), block, cluster, 0, st, k, P, logp, ref_logp, losses,
                          rewards, d_logp), "preference launch"))
         return ADAMW_ERR_CUDA;
-    return launched(launch(preference_stats_kernel, 1u, kThreads, 1, 0, st, uint32_t(pairs), P,
-                           static_cast<const float*>(losses), static_cast<const float*>(rewards), stats),
+    return launched(launch(preference_stats_kernel, 1u, kThreads, 1, 0, st, uint32_t(pairs), P, losses, stats),
                     "preference statistics launch")
                ? ADAMW_OK : ADAMW_ERR_CUDA;
 }

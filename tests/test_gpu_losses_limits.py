@@ -221,3 +221,28 @@ def test_preference_sums_that_nearly_cancel(pairs, length, kind, average):
     second = {"sigmoid": 0.0025, "hinge": 0.0, "ipo": 2.0}[kind]
     tol = (second * dD / pairs / (length if average else 1)).repeat(2).repeat_interleave(length)
     assert ((got.d_logp.cpu().double().reshape(-1) - grad).abs() <= 2e-6 * grad.abs() + tol + 1e-12).all()
+
+
+@pytest.mark.parametrize("pairs,length", [(7, 1100), (40, 8191), (2, 70001)])
+@pytest.mark.parametrize("average", [False, True])
+def test_preference_statistics_of_close_pairs(pairs, length, average):
+    """The share of pairs with D > 0 goes by D itself, and the mean of h is as
+    good as D."""
+    logp = _long_pairs(pairs, length, length + 1)
+    S = logp.double().sum(1) / (length if average else 1)
+    D = S[:pairs] - S[pairs:]
+    got = L.preference_loss(logp.to(DEV), beta=0.1, margin=0.25, length_average=average)
+    s = got.stats.cpu().double()
+    share = (D > 0).double().mean()
+    assert 0 < share < 1 and abs(float(s[1] - share)) <= 1e-7
+    size = logp.double().abs().sum(1).max() / (length if average else 1)
+    err = 4e-7 * (0.1 * D.abs() + 0.25).mean() + 0.1 * 2.0 ** -39 * size
+    assert abs(float(s[2]) - float((0.1 * D - 0.25).mean())) <= err
+    want = -torch.nn.functional.logsigmoid(0.1 * D - 0.25)
+    assert abs(float(s[0] - want.mean())) <= 1e-6 * float(want.mean()) + err
+
+
+def test_preference_order_of_a_pair():
+    """The first half of the sequences is the preferred one."""
+    r = L.preference_loss(torch.tensor([[2000.0], [-2000.0], [-2000.0], [2000.0]], device=DEV), beta=1.0)
+    assert r.losses.tolist() == [0.0, 4000.0] and r.stats[1] == 0.5
