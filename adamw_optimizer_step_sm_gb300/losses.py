@@ -302,9 +302,21 @@ def _detached(t):
     return t.detach() if t.requires_grad else t
 
 
-def _advantages(a, shape, sequences, device):
+def _per_token(name, v, shape, sequences, offsets, per_token):
+    """Whether v is per token, as said or by its shape; as many packed tokens as
+    sequences fit both, and then have to be told."""
+    if per_token is not None:
+        return bool(per_token)
+    if v.shape != shape:
+        return False
+    if offsets is not None and sequences > 1 and shape == (sequences,):
+        raise ValueError(f"as many sequences as tokens: say {name}_per_token=True or False")
+    return True
+
+
+def _advantages(a, shape, sequences, offsets, per_token, device):
     """(tensor, per token) of advantages."""
-    if a.shape == shape:
+    if _per_token("advantage", a, shape, sequences, offsets, per_token):
         return _floats("advantages", a, shape, device), 1
     return _floats("advantages", a, (sequences,), device), 0
 
@@ -321,14 +333,17 @@ def policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Te
                 mask: Optional[torch.Tensor] = None, offsets: Optional[torch.Tensor] = None,
                 clip_low: float = 0.2, clip_high: float = 0.2, dual_clip: float = 0.0, kl: str = "k3",
                 kl_coef: float = 0.0, entropy_coef: float = 0.0, reduce: str = "token",
-                divisor: float = 1.0, grad_scale: float = 1.0) -> PolicyLoss:
+                divisor: float = 1.0, grad_scale: float = 1.0,
+                advantage_per_token: Optional[bool] = None) -> PolicyLoss:
     """The clipped policy loss of tokens, with a KL term to a reference and an
     entropy bonus, and its gradients with respect to ``logp`` and ``entropy``.
 
-    ``advantages``: per token, or one per sequence.  ``mask``: tokens that
-    count.  ``reduce``: mean over the tokens ("token"), mean over the
-    sequences of their means ("sequence"), or a sum divided by ``divisor``
-    ("fixed").  ``grad_scale`` multiplies the gradients."""
+    ``advantages``: per token, or one per sequence, as their shape says; where
+    it fits both (packed, as many sequences as tokens) ``advantage_per_token``
+    has to say which.  ``mask``: tokens that count.  ``reduce``: mean over the
+    tokens ("token"), mean over the sequences of their means ("sequence"), or a
+    sum divided by ``divisor`` ("fixed").  ``grad_scale`` multiplies the
+    gradients."""
     dev, shape = logp.device, logp.shape
     if not logp.is_cuda:
         raise TypeError("want CUDA tensors")
@@ -341,7 +356,7 @@ def policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Te
     if entropy_coef != 0.0 and ent is None:
         raise ValueError("an entropy term needs the entropy")
     tokens, sequences, _keep = _tokens(shape, offsets, mask, dev)
-    adv, per_token = _advantages(advantages, shape, sequences, dev)
+    adv, per_token = _advantages(advantages, shape, sequences, offsets, advantage_per_token, dev)
     policy = _policy(clip_low, clip_high, dual_clip, kl, kl_coef, entropy_coef, reduce, divisor, grad_scale,
                      per_token)
     stats = _empty(6, dtype=_F32, device=dev)
@@ -362,7 +377,8 @@ def policy_loss_logits(logits: torch.Tensor, targets: torch.Tensor, old_logp: to
                        ignore_index: int = -100, temperature: float = 1.0, clip_low: float = 0.2,
                        clip_high: float = 0.2, dual_clip: float = 0.0, kl: str = "k3", kl_coef: float = 0.0,
                        entropy_coef: float = 0.0, reduce: str = "token", divisor: float = 1.0,
-                       grad_scale: float = 1.0, out: Optional[torch.Tensor] = None) -> PolicyLogits:
+                       grad_scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                       advantage_per_token: Optional[bool] = None) -> PolicyLogits:
     """``token_logprob``, ``policy_loss`` and ``token_logprob_backward`` in one
     pass over the logits: each row is read once, and its gradient written once
     (to ``out``, which may be the logits themselves).  Tokens whose target is
@@ -376,7 +392,7 @@ def policy_loss_logits(logits: torch.Tensor, targets: torch.Tensor, old_logp: to
     if kl_coef != 0.0 and ref is None:
         raise ValueError("a KL term needs ref_logp")
     tokens, sequences, _keep = _tokens(shape, offsets, None, dev)
-    adv, per_token = _advantages(advantages, shape, sequences, dev)
+    adv, per_token = _advantages(advantages, shape, sequences, offsets, advantage_per_token, dev)
     policy = _policy(clip_low, clip_high, dual_clip, kl, kl_coef, entropy_coef, reduce, divisor, grad_scale,
                      per_token)
     d, d_rows = _out_rows(None if out is None else _detached(out), logits, rows)

@@ -3,6 +3,8 @@
 The definitions and tolerances are those of test_gpu_losses.py (in 64 bits, on
 the CPU); what differs is derived at the test.
 """
+import math
+
 import pytest
 import torch
 
@@ -246,3 +248,32 @@ def test_preference_order_of_a_pair():
     """The first half of the sequences is the preferred one."""
     r = L.preference_loss(torch.tensor([[2000.0], [-2000.0], [-2000.0], [2000.0]], device=DEV), beta=1.0)
     assert r.losses.tolist() == [0.0, 4000.0] and r.stats[1] == 0.5
+
+
+# ------------------------------------------------- as many sequences as tokens
+
+def test_advantages_where_both_readings_fit():
+    """Three tokens, three sequences, one of them empty and one of two tokens."""
+    z = torch.zeros(3, device=DEV)
+    off = torch.tensor([0, 2, 2, 3], device=DEV)
+    adv = torch.tensor([1.0, 50.0, 3.0], device=DEV)
+    x, t = torch.zeros(3, 5, device=DEV), torch.zeros(3, dtype=torch.int64, device=DEV)
+    call = lambda **k: L.policy_loss(z, z, adv, offsets=off, reduce="fixed", **k).d_logp.tolist()
+    rows = lambda **k: L.policy_loss_logits(x, t, torch.full((3,), -math.log(5), device=DEV), adv, offsets=off,
+                                            reduce="fixed", **k).d_logits[:, 0]
+    assert call(advantage_per_token=True) == [-1.0, -50.0, -3.0]
+    assert call(advantage_per_token=False) == [-1.0, -1.0, -3.0]
+    for per, want in ((True, (1.0, 50.0, 3.0)), (False, (1.0, 1.0, 3.0))):
+        assert (rows(advantage_per_token=per).cpu() + 0.8 * torch.tensor(want)).abs().max() < 1e-4
+    with pytest.raises(ValueError):
+        call()
+    with pytest.raises(ValueError):
+        rows()
+    # one reading only: as before, and the argument has to agree with the shape
+    assert L.policy_loss(z, z, adv[:2], offsets=off[[0, 1, 3]], reduce="fixed").d_logp.tolist() == [-1.0, -1.0, -50.0]
+    with pytest.raises(ValueError):
+        L.policy_loss(z, z, adv[:2], offsets=off[[0, 1, 3]], advantage_per_token=True)
+    with pytest.raises(ValueError):
+        L.policy_loss(z, z, adv, offsets=off[[0, 1, 3]], advantage_per_token=False)
+    # one token in one sequence: both readings are the same
+    assert L.policy_loss(z[:1], z[:1], adv[:1], offsets=off[[0, 3]] // 3).d_logp.tolist() == [-1.0]
