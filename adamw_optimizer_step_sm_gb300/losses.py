@@ -412,10 +412,12 @@ def preference_loss(logp: torch.Tensor, ref_logp: Optional[torch.Tensor] = None,
                     mask: Optional[torch.Tensor] = None, offsets: Optional[torch.Tensor] = None,
                     beta: float = 0.1, margin: float = 0.0, kind: str = "sigmoid",
                     label_smoothing: float = 0.0, length_average: bool = False,
-                    grad_scale: float = 1.0) -> PreferenceLoss:
+                    grad_scale: float = 1.0, ref_per_token: Optional[bool] = None) -> PreferenceLoss:
     """The preference loss of pairs and its gradient with respect to ``logp``:
     of 2 B sequences, i is preferred over B + i.  ``ref_logp``: the frozen
-    reference's log-probabilities per token, its sums per sequence, or None.
+    reference's log-probabilities per token, its sums per sequence, or None;
+    where its shape fits both (packed, as many sequences as tokens)
+    ``ref_per_token`` has to say which.
     ``kind``: "sigmoid", "hinge" or "ipo".  ``length_average`` takes means
     over a sequence's tokens instead of sums."""
     dev, shape = logp.device, logp.shape
@@ -430,7 +432,7 @@ def preference_loss(logp: torch.Tensor, ref_logp: Optional[torch.Tensor] = None,
     pairs = sequences // 2
     ref, how = None, A.REF_NONE
     if ref_logp is not None:
-        how = A.REF_TOKEN if ref_logp.shape == shape else A.REF_SEQUENCE
+        how = A.REF_TOKEN if _per_token("ref", ref_logp, shape, sequences, offsets, ref_per_token) else A.REF_SEQUENCE
         ref = _floats("ref_logp", ref_logp, shape if how == A.REF_TOKEN else (sequences,), dev)
     pref = A.adamw_preference_t(beta, margin, label_smoothing, grad_scale, A.PREFERENCE[kind],
                                 1 if length_average else 0, how)

@@ -277,3 +277,18 @@ def test_advantages_where_both_readings_fit():
         L.policy_loss(z, z, adv, offsets=off[[0, 1, 3]], advantage_per_token=False)
     # one token in one sequence: both readings are the same
     assert L.policy_loss(z[:1], z[:1], adv[:1], offsets=off[[0, 3]] // 3).d_logp.tolist() == [-1.0]
+
+
+def test_reference_where_both_readings_fit():
+    logp = torch.tensor([-1.0, -2.0], device=DEV)
+    off = torch.tensor([0, 2, 2], device=DEV)     # two tokens preferred to an empty answer
+    ref = torch.tensor([-0.5, -4.0], device=DEV)
+    call = lambda **k: L.preference_loss(logp, ref, offsets=off, beta=0.5, **k).rewards.tolist()
+    assert call(ref_per_token=True) == [0.75, 0.0]
+    assert call(ref_per_token=False) == [-1.25, 2.0]
+    with pytest.raises(ValueError):
+        call()
+    four = torch.zeros(4, device=DEV)
+    for per, size in ((True, 2), (False, 4)):
+        with pytest.raises(ValueError):
+            L.preference_loss(four, torch.zeros(size, device=DEV), offsets=off, ref_per_token=per)
