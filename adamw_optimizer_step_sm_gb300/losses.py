@@ -39,6 +39,9 @@ _byref = ctypes.byref
 _empty = torch.empty
 _rows_t, _tokens_t = A.adamw_rows_t, A.adamw_tokens_t
 _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# what autograd has to be told of a tensor of the caller's that was written, so
+# that a graph which saved its earlier values refuses to go on with the new ones
+_written = torch.autograd.graph.increment_version
 _F32 = torch.float32
 _CODES = {torch.bfloat16: A.DTYPE_BF16, torch.float16: A.DTYPE_FP16, torch.float32: A.DTYPE_FP32}
 
@@ -267,6 +270,8 @@ def token_logprob_backward(logits: torch.Tensor, targets: torch.Tensor, result: 
     d, d_rows = _out_rows(out, logits, rows)
     _call(A.load().adamw_token_logprob_backward, "adamw_token_logprob_backward", dev, _byref(rows), t.data_ptr(), ignore_index, _scale(temperature),
           stats.data_ptr(), _ptr(ent), dl.data_ptr(), _ptr(dh), _byref(d_rows))
+    if out is not None:
+        _written(out)
     return d
 
 
@@ -405,6 +410,8 @@ def policy_loss_logits(logits: torch.Tensor, targets: torch.Tensor, old_logp: to
     _call(lib.adamw_policy_loss_logits, "adamw_policy_loss_logits", dev, _byref(rows), t.data_ptr(), ignore_index, _scale(temperature),
           _byref(tokens), _byref(policy), old.data_ptr(), _ptr(ref), adv.data_ptr(), stats.data_ptr(),
           counts.data_ptr(), logp.data_ptr(), _ptr(ent), _byref(d_rows), work.data_ptr())
+    if out is not None:
+        _written(out)
     return PolicyLogits(stats, counts, logp, ent, d)
 
 

@@ -292,3 +292,20 @@ def test_reference_where_both_readings_fit():
     for per, size in ((True, 2), (False, 4)):
         with pytest.raises(ValueError):
             L.preference_loss(four, torch.zeros(size, device=DEV), offsets=off, ref_per_token=per)
+
+
+# ------------------------------------------------------- what autograd has to know
+
+@pytest.mark.parametrize("which", ["backward", "policy"])
+def test_a_graph_over_logits_that_were_overwritten_is_refused(which):
+    x = torch.randn(4, 33, device=DEV).requires_grad_(True)
+    t = torch.zeros(4, dtype=torch.int64, device=DEV)
+    y = x * 1.0
+    r = L.token_logprob(y, t)
+    d, z = y.detach(), torch.zeros(4, device=DEV)
+    if which == "backward":
+        L.token_logprob_backward(d, t, L.TokenLogprob(*(v if v is None else v.detach() for v in r)), z, out=d)
+    else:
+        L.policy_loss_logits(d, t, z, z, out=d)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        r.logp.sum().backward()
