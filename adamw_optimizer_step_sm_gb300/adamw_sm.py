@@ -589,13 +589,17 @@ class ClipPlan:
         self._result = torch.zeros(4, dtype=torch.float32, device=dev)
         self._at = self._result.data_ptr()
         self.result = ClipResult(self._result[0], self._result[1], self._result.view(torch.int32)[2])
+        # what a clip writes, for autograd: a buffer once for all views of it
+        bases = [] if norm_only else [o if o._base is None else o._base for o in outs]
+        self._written = list({id(b): b for b in [self._result, *bases]}.values())
 
     def clip(self, max_norm: float, norm: str = "l2", stream=None) -> ClipResult:
         """One clip to ``max_norm`` (infinity: only copies or converts) by the
         l2 norm of all elements or their largest magnitude ("max"); returns
-        ``self.result`` without waiting for the GPU.  With a non-finite
-        gradient nothing is scaled: the values reach the optimizer, which
-        skips or reports the step."""
+        ``self.result`` without waiting for the GPU.  To autograd it is an
+        in-place write of the outs.  With a non-finite gradient nothing is
+        scaled: the values reach the optimizer, which skips or reports the
+        step."""
         import torch
         if norm not in NORM:
             raise ValueError('norm must be "l2" or "max"')
@@ -603,6 +607,7 @@ class ClipPlan:
             raise ValueError("want max_norm > 0")
         st = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self.device.index)
         adamw_clip_grads(self.handle, max_norm, NORM[norm], self._at, st)
+        torch.autograd.graph.increment_version(self._written)
         return self.result
 
     def close(self) -> None:

@@ -8,7 +8,9 @@ import math
 import pytest
 import torch
 
+from adamw_optimizer_step_sm_gb300 import adamw_sm as A
 from adamw_optimizer_step_sm_gb300 import losses as L
+from adamw_optimizer_step_sm_gb300.optim import AnyPrecisionAdamW, GlobalClip
 from test_gpu_losses import (DEV, INF, ROUND, TYPES, _check_policy, _close_logp, _gen, _grad64,
                              _policy64, _policy_inputs, _preference64, _rows64)
 
@@ -309,3 +311,30 @@ def test_a_graph_over_logits_that_were_overwritten_is_refused(which):
         L.policy_loss_logits(d, t, z, z, out=d)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         r.logp.sum().backward()
+
+
+def test_a_graph_over_clipped_tensors_is_refused():
+    a = torch.randn(100, device=DEV).requires_grad_(True)
+    for in_place in (True, False):
+        g, o = torch.randn(100, device=DEV), torch.zeros(100, device=DEV)
+        y = (a * (g if in_place else o)).sum()
+        A.ClipPlan([g], None if in_place else [o]).clip(0.1)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+    g = torch.randn(100, device=DEV)
+    y = (a * g).sum()
+    A.ClipPlan([g], norm_only=True).clip(0.1)     # writes no gradient
+    y.backward()
+
+
+def test_a_graph_over_an_optimizers_gradients_is_refused():
+    p = torch.nn.Parameter(torch.randn(40, device=DEV).bfloat16())
+    opt = AnyPrecisionAdamW([p], lr=1e-3)
+    clip = GlobalClip(opt)
+    opt.zero_grad()
+    p.grad.fill_(1.0)
+    x = torch.randn(40, device=DEV).bfloat16().requires_grad_(True)
+    y = (x * p.grad).sum()
+    clip(0.1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
