@@ -42,6 +42,7 @@ _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurre
 # what autograd has to be told of a tensor of the caller's that was written, so
 # that a graph which saved its earlier values refuses to go on with the new ones
 _written = torch.autograd.graph.increment_version
+_tangent = torch.autograd.forward_ad.unpack_dual
 _F32 = torch.float32
 _CODES = {torch.bfloat16: A.DTYPE_BF16, torch.float16: A.DTYPE_FP16, torch.float32: A.DTYPE_FP32}
 
@@ -245,8 +246,8 @@ def token_logprob(logits: torch.Tensor, targets: torch.Tensor, *, ignore_index: 
     """log softmax(logits / temperature) at the targets, and with ``entropy``
     the softmax's entropy; fp32.  Tokens whose target is ``ignore_index`` are
     not read and give 0.  Differentiable (logp and entropy) when the logits
-    require a gradient."""
-    if logits.requires_grad and torch.is_grad_enabled():
+    require a gradient; forward mode has no rule and is refused."""
+    if logits.requires_grad and torch.is_grad_enabled() or _tangent(logits).tangent is not None:
         return TokenLogprob(*_TokenLogprob.apply(logits, targets, ignore_index, temperature, entropy))
     return _token_logprob(logits, targets, ignore_index, temperature, entropy)
 

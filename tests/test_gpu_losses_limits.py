@@ -338,3 +338,12 @@ def test_a_graph_over_an_optimizers_gradients_is_refused():
     clip(0.1)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.backward()
+
+
+def test_forward_mode_is_refused():
+    import torch.autograd.forward_ad as fwd
+    x, t = torch.randn(4, 33, device=DEV), torch.zeros(4, dtype=torch.int64, device=DEV)
+    with fwd.dual_level():
+        assert L.token_logprob(x, t).logp.shape == (4,)
+        with pytest.raises(NotImplementedError):
+            L.token_logprob(fwd.make_dual(x, torch.ones_like(x)), t)
