@@ -682,7 +682,8 @@ __device__ __forceinline__ PolicyToken policy_token(const Policy& P, float logp,
     const float high = up ? P.d_high : P.d_dual, low = up ? -kInf : P.d_low;
     const bool off = A != 0.0f && (d > high || d < low);
     const float bound = up ? P.r_high : d < low ? P.r_low : P.dual;
-    const float u = -A * r;
+    // advantage 0: nothing, past fp32's range of ratios too (0 * inf)
+    const float u = A == 0.0f && r == kInf ? 0.0f : -A * r;
     o.pg = off ? -A * bound : u;
     o.off = off ? 1.0f : 0.0f;
     o.old_kl = exp_beyond_linear(d, r);

@@ -347,3 +347,25 @@ def test_forward_mode_is_refused():
         assert L.token_logprob(x, t).logp.shape == (4,)
         with pytest.raises(NotImplementedError):
             L.token_logprob(fwd.make_dual(x, torch.ones_like(x)), t)
+
+
+# -------------------------------------------------------- ratios past fp32
+
+@pytest.mark.parametrize("n", [6, 20000])
+def test_ratios_past_fp32(n):
+    """A token whose old log-probability is the type's lowest value or -inf has
+    an infinite ratio: with advantage 0 it adds nothing."""
+    old = torch.zeros(n, device=DEV)
+    old[1], old[2], old[3] = -200.0, torch.finfo(torch.float32).min, -INF
+    adv = torch.zeros(n, device=DEV)
+    adv[4] = 1.0
+    r = L.policy_loss(torch.zeros(n, device=DEV), old, adv, mask=torch.arange(n, device=DEV) < 5, reduce="fixed")
+    assert r.stats[0] == -1.0 and r.stats[4] == 0.0
+    assert r.d_logp[:5].tolist() == [0.0, 0.0, 0.0, 0.0, -1.0]
+    x, t = torch.zeros(n, 3, device=DEV), torch.zeros(n, dtype=torch.int64, device=DEV)
+    r = L.policy_loss_logits(x, t, old - math.log(3), adv, reduce="fixed")
+    assert abs(float(r.stats[0]) + 1.0) < 1e-6
+    assert (r.d_logits[:4] == 0).all() and (r.d_logits[4].cpu() - torch.tensor([-2 / 3, 1 / 3, 1 / 3])).abs().max() < 1e-5
+    # a NaN is seen all the same
+    nan = torch.full((2,), float("nan"), device=DEV)
+    assert torch.isnan(L.policy_loss(nan, nan, torch.zeros(1, device=DEV)).stats[0])
