@@ -699,8 +699,11 @@ __device__ __forceinline__ PolicyToken policy_token(const Policy& P, float logp,
             o.kl = 0.5f * k * k;
             dk = k;
         } else {
-            o.kl = exp_beyond_linear(-k, expf(-k));
-            dk = k - o.kl;   // 1 - exp(-k)
+            const float e = expf(-k);
+            o.kl = exp_beyond_linear(-k, e);
+            // 1 - exp(-k): from the estimate where that is small, not where k
+            // would round it away
+            dk = fabsf(k) < 0.7f ? k - o.kl : 1.0f - e;
         }
         // without a coefficient the estimate is reported only, and a
         // reference that is -inf somewhere does not reach the gradient

@@ -369,3 +369,15 @@ def test_ratios_past_fp32(n):
     # a NaN is seen all the same
     nan = torch.full((2,), float("nan"), device=DEV)
     assert torch.isnan(L.policy_loss(nan, nan, torch.zeros(1, device=DEV)).stats[0])
+
+
+@pytest.mark.parametrize("n", [12, 20000])
+def test_kl_gradient_of_far_references(n):
+    """d KL / d logp of k3 is 1 - exp(-k): exp is good to 2 ulps, the rest rounds."""
+    k = torch.tensor([1e-3, 0.3, 0.69, 0.71, 1.0, 10.0, 1e3, 1e6, 1e8, 1e12, INF])
+    logp, ref = torch.zeros(n), torch.zeros(n)
+    ref[:11] = -k
+    r = L.policy_loss(logp.to(DEV), logp.to(DEV), torch.zeros(1, device=DEV), ref_logp=ref.to(DEV), kl_coef=0.5,
+                      mask=torch.arange(n, device=DEV) < 11, reduce="fixed")
+    want = -0.5 * torch.expm1(-k.double())
+    assert ((r.d_logp[:11].cpu().double() - want).abs() <= 1e-6 * want).all()
