@@ -664,7 +664,7 @@ __device__ __forceinline__ float exp_beyond_linear(float x, float e) {
     s = fmaf(s, x, 1.0f / 24.0f);
     s = fmaf(s, x, 1.0f / 6.0f);
     s = fmaf(s, x, 0.5f);
-    const float far = (e - 1.0f) - x;
+    const float far = (e - 1.0f) - fminf(x, kMaxFloat);   // not inf - inf
     return fabsf(x) < 0.7f ? s * x * x : far;
 }
 

@@ -381,3 +381,12 @@ def test_kl_gradient_of_far_references(n):
                       mask=torch.arange(n, device=DEV) < 11, reduce="fixed")
     want = -0.5 * torch.expm1(-k.double())
     assert ((r.d_logp[:11].cpu().double() - want).abs() <= 1e-6 * want).all()
+
+
+def test_kl_to_a_reference_that_the_policy_left():
+    """logp -inf: the k3 estimate and the KL from the old policy are +inf, not NaN."""
+    t = lambda *v: torch.tensor(v, device=DEV)
+    r = L.policy_loss(t(-INF, 0.0), t(-1.0, 0.0), t(1.0), ref_logp=t(-1.0, 0.0))
+    assert r.stats[2] == INF and r.stats[5] == INF
+    r = L.policy_loss(t(0.0, 0.0), t(-INF, 0.0), t(1.0), ref_logp=t(0.0, 0.0))
+    assert r.stats[5] == INF and r.stats[2] == 0
