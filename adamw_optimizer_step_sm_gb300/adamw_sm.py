@@ -559,8 +559,8 @@ class ClipPlan:
     ``grads``: contiguous CUDA tensors of one device.  ``outs``: where the
     clipped gradients go, tensors of the same sizes and any of the three
     types (for example the bf16 gradients that an optimizer reads, from fp32
-    accumulators); None clips in place.  ``norm_only``: nothing is written
-    but the result.  The tensors must stay alive and in place for the plan's
+    accumulators); None clips in place.  No tensor twice, and none that reaches
+    into another.  ``norm_only``: nothing is written but the result.  The tensors must stay alive and in place for the plan's
     lifetime (the plan holds references to them); calls on one plan must not
     overlap on the GPU."""
 

@@ -379,6 +379,8 @@ class GlobalClip:
     def __init__(self, *optimizers: _FlatAdamW):
         if not optimizers or not all(isinstance(o, _FlatAdamW) for o in optimizers):
             raise TypeError("want one or more optimizers of this module")
+        if len({id(o) for o in optimizers}) < len(optimizers):
+            raise ValueError("an optimizer is listed twice")
         self.optimizers = optimizers
         self._plan, self._of = None, None
 

@@ -220,7 +220,8 @@ int adamw_preference_loss(const adamw_tokens_t* tokens, const adamw_preference_t
 /* One gradient of a list to clip.  src is read; dst receives the clipped
  * gradient, rounded to dst_dtype: another buffer, src itself (in place; then
  * the types must be equal), or NULL (only the norm is wanted).  numel may be
- * 0.  Buffers of different entries must not overlap.  They are aligned to
+ * 0.  Buffers of different entries must not overlap, those that are only read
+ * among them (a gradient listed twice would count twice).  They are aligned to
  * their element size; tensors whose src and dst are 16-byte aligned take
  * 16-byte accesses. */
 typedef struct {
@@ -254,7 +255,7 @@ typedef struct adamw_clip_plan* adamw_clip_plan_t;
  * plan must not overlap on the GPU.
  * Errors: INVALID_ARG (NULL out or table with n > 0, n < 0, numel < 0, NULL
  * src with numel > 0, unknown dtype, dst overlapping src without being it, in
- * place with two types), MISALIGNED, NOT_ACCESSIBLE, TOO_LARGE (more than
+ * place with two types, buffers of two entries that overlap), MISALIGNED, NOT_ACCESSIBLE, TOO_LARGE (more than
  * 2^40 elements), CUDA. */
 int adamw_clip_plan_create(const adamw_grad_t* host_table, int32_t n, adamw_clip_plan_t* out);
 
