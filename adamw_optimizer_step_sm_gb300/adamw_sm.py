@@ -587,6 +587,9 @@ class ClipPlan:
         with torch.cuda.device(dev):
             self.handle = adamw_clip_plan_create(entries)
         self._result = torch.zeros(4, dtype=torch.float32, device=dev)
+        # the memory may still be in use on the stream current here, by its zeroing
+        # if nothing else, and the first clip may be on another
+        torch.cuda.current_stream(dev).synchronize()
         self._at = self._result.data_ptr()
         self.result = ClipResult(self._result[0], self._result[1], self._result.view(torch.int32)[2])
         # what a clip writes, for autograd: a buffer once for all views of it
