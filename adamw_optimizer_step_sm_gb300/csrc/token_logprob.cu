@@ -233,13 +233,14 @@ __device__ __forceinline__ void zero_row(char* out, bool vector_out, const RowSp
 }
 
 // Elementwise from the row's maximum and sum, one CTA per piece of a row (or a
-// warp per row).  4092 rows of 50272 bf16, a quarter of them ignored, after
+// warp per row).  zeros: a row whose gradients are 0 is not used (it may hold
+// anything) and gets 0.  4092 rows of 50272 bf16, a quarter of them ignored, after
 // their forward pass: 109 us, 6.6 TB/s over one read and one write.
 template <int DT, bool ENT, bool WARP>
 __global__ void __launch_bounds__(kBackwardThreads)
 logprob_backward_kernel(Rows logits, Rows grad, uint32_t rows, uint32_t pieces, int cols,
                         const int64_t* targets, float scale, const float* stats, const float* entropy,
-                        const float* d_logp, const float* d_entropy) {
+                        const float* d_logp, const float* d_entropy, bool zeros) {
     using E = Elem<DT>;
     dependency_trigger();
     dependency_wait();
@@ -263,7 +264,8 @@ logprob_backward_kernel(Rows logits, Rows grad, uint32_t rows, uint32_t pieces, 
     const float a = scale * d_logp[r];
     const float b = ENT ? scale * d_entropy[r] : 0.0f;
     const float H = ENT ? entropy[r] : 0.0f;
-    if (st.y == kInf) {  // ignored, or without a distribution
+    // ignored, without a distribution, or of a token that does not count
+    if (st.y == kInf || (zeros && a == 0.0f && b == 0.0f)) {
         zero_row<DT>(out, vector_out, sp, first, end, lane, width, extra);
         return;
     }
@@ -519,14 +521,14 @@ cudaError_t forward(const adamw_rows_t* x, const int64_t* targets, int64_t ignor
 
 template <int DT>
 cudaError_t backward(const adamw_rows_t* x, const int64_t* targets, float scale, const float* stats,
-                     const float* entropy, const float* d_logp, const float* d_entropy,
+                     const float* entropy, const float* d_logp, const float* d_entropy, bool zeros,
                      const adamw_rows_t* dx, cudaStream_t st) {
     const Rows in = rows_of(x), out = rows_of(dx);
     const uint32_t n = uint32_t(x->rows);
     if (x->cols / Elem<DT>::kVec <= kBackwardWarpVecs) {
         auto k = d_entropy ? logprob_backward_kernel<DT, true, true> : logprob_backward_kernel<DT, false, true>;
         return launch(k, warp_grid(n, kBackwardThreads), kBackwardThreads, 1, 0, st, in, out, n, 1u, x->cols, targets,
-                      scale, stats, entropy, d_logp, d_entropy);
+                      scale, stats, entropy, d_logp, d_entropy, zeros);
     }
     // two turns of its threads' vectors to a piece
     const int64_t per = 2 * int64_t(kBackwardThreads) * kBackwardUnroll * Elem<DT>::kVec;
@@ -535,7 +537,19 @@ cudaError_t backward(const adamw_rows_t* x, const int64_t* targets, float scale,
     const uint32_t grid = grid_of(x->rows * pieces);
     if (!grid) return cudaErrorInvalidConfiguration;
     return launch(k, grid, kBackwardThreads, 1, 0, st, in, out, n, pieces, x->cols, targets, scale, stats, entropy,
-                  d_logp, d_entropy);
+                  d_logp, d_entropy, zeros);
+}
+
+int launch_backward(const adamw_rows_t* x, const int64_t* targets, float scale, const float* stats,
+                    const float* entropy, const float* d_logp, const float* d_entropy, bool zeros,
+                    const adamw_rows_t* dx, cudaStream_t st) {
+    cudaError_t e;
+    switch (x->dtype) {
+        case ADAMW_DTYPE_BF16: e = backward<ADAMW_DTYPE_BF16>(x, targets, scale, stats, entropy, d_logp, d_entropy, zeros, dx, st); break;
+        case ADAMW_DTYPE_FP16: e = backward<ADAMW_DTYPE_FP16>(x, targets, scale, stats, entropy, d_logp, d_entropy, zeros, dx, st); break;
+        default: e = backward<ADAMW_DTYPE_FP32>(x, targets, scale, stats, entropy, d_logp, d_entropy, zeros, dx, st); break;
+    }
+    return launched(e, "token_logprob_backward launch") ? ADAMW_OK : ADAMW_ERR_CUDA;
 }
 
 // Allows a kernel its dynamic shared memory, once per device.
@@ -624,14 +638,8 @@ extern "C" int adamw_token_logprob_backward(const adamw_rows_t* logits, const in
     if (!aligned(targets, 8) || !aligned(stats, 8) || !aligned(d_logp, 4) || !aligned(d_entropy, 4) ||
         !aligned(entropy, 4))
         return ADAMW_ERR_MISALIGNED;
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    switch (logits->dtype) {
-        case ADAMW_DTYPE_BF16: e = backward<ADAMW_DTYPE_BF16>(logits, targets, scale, stats, entropy, d_logp, d_entropy, d_logits, st); break;
-        case ADAMW_DTYPE_FP16: e = backward<ADAMW_DTYPE_FP16>(logits, targets, scale, stats, entropy, d_logp, d_entropy, d_logits, st); break;
-        default: e = backward<ADAMW_DTYPE_FP32>(logits, targets, scale, stats, entropy, d_logp, d_entropy, d_logits, st); break;
-    }
-    return launched(e, "token_logprob_backward launch") ? ADAMW_OK : ADAMW_ERR_CUDA;
+    return launch_backward(logits, targets, scale, stats, entropy, d_logp, d_entropy, false, d_logits,
+                           reinterpret_cast<cudaStream_t>(stream));
 }
 
 // The workspace: the policy loss's, then (used for rows too long for a
@@ -695,6 +703,5 @@ extern "C" int adamw_policy_loss_logits(const adamw_rows_t* logits, const int64_
     rc = adamw::launch_policy(tokens, policy, targets, ignore_index, true, logp, old_logp, ref_logp, advantages,
                               entropy, stats, counts, d_logp, d_entropy, workspace, st);
     if (rc != ADAMW_OK) return rc;
-    return adamw_token_logprob_backward(logits, targets, ignore_index, scale, row_stats, entropy, d_logp,
-                                        d_entropy, d_logits, stream);
+    return launch_backward(logits, targets, scale, row_stats, entropy, d_logp, d_entropy, true, d_logits, st);
 }

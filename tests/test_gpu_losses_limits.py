@@ -390,3 +390,19 @@ def test_kl_to_a_reference_that_the_policy_left():
     assert r.stats[2] == INF and r.stats[5] == INF
     r = L.policy_loss(t(0.0, 0.0), t(-INF, 0.0), t(1.0), ref_logp=t(0.0, 0.0))
     assert r.stats[5] == INF and r.stats[2] == 0
+
+
+@pytest.mark.parametrize("v", [33, 3000, 450001])
+def test_rows_outside_every_sequence_are_not_used(v):
+    """Whatever they hold, in rows of a warp, a CTA, and too long for a cluster."""
+    x = torch.randn(4, v, generator=_gen(v))
+    x[0, v // 2] = float("nan")
+    x[3] = INF
+    t = torch.tensor([1, 2, 3, v])   # the last target is outside the vocabulary, too
+    off = torch.tensor([1, 3], device=DEV)
+    old = torch.full((4,), -10.0, device=DEV)
+    r = L.policy_loss_logits(x.to(DEV), t.to(DEV), old, torch.ones(1, device=DEV), offsets=off, entropy_coef=0.1)
+    assert r.counts.tolist() == [2, 1] and torch.isfinite(r.stats).all()
+    d = r.d_logits
+    assert (d[0] == 0).all() and (d[3] == 0).all()
+    assert torch.isfinite(d[1:3]).all() and d[1].abs().max() > 0
