@@ -438,8 +438,9 @@ __device__ __forceinline__ RowStats row_stats(const Online& o) {
 __device__ __forceinline__ float logp_of(const RowStats& r, float x, float scale, float c) {
     if (r.s == kInf) return -kInf;
     const float d = exponent(x, r.m, c);
-    // an exponent past fp32's range: the type's lowest value in an ordinary row
-    return (d == -kInf ? (x - r.m) * scale : kLn2 * d) - r.log_s;
+    // an exponent past fp32's range: the type's lowest value in an ordinary row,
+    // or beside its largest (half the difference is a number of the type)
+    return (d == -kInf ? (0.5f * x - 0.5f * r.m) * (2.0f * scale) : kLn2 * d) - r.log_s;
 }
 
 // The gradient of an element, without the target's term a:

@@ -406,3 +406,21 @@ def test_rows_outside_every_sequence_are_not_used(v):
     d = r.d_logits
     assert (d[0] == 0).all() and (d[3] == 0).all()
     assert torch.isfinite(d[1:3]).all() and d[1].abs().max() > 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("v", [40, 9000])
+def test_log_probabilities_near_the_types_range(v, dtype):
+    """A target of the lowest value beside the largest one: their difference is
+    not a number of the type, its product with the scale is."""
+    top = torch.finfo(TYPES[dtype]).max
+    x = torch.full((6, v), -INF, dtype=TYPES[dtype])
+    x[:, 0] = torch.tensor([top, top, top / 4, 0.0, -top / 2, -top])
+    x[:, 1] = torch.tensor([-top, -top / 2, -top, -top, -top, -INF])
+    t = torch.ones(6, dtype=torch.int64)
+    for temperature in (1e-3, 0.7, 1.5, 6.0, 1e3):
+        r = L.token_logprob(x.to(DEV), t.to(DEV), temperature=temperature)
+        want = _rows64(x, t, 1 / temperature)[0]
+        fits, over = want.abs() < 3.40e38, want.abs() > 3.41e38   # at the limit itself either
+        got = r.logp.cpu().double()
+        assert ((got - want).abs() <= 4e-7 * want.abs())[fits].all() and (got[over] == -INF).all()
