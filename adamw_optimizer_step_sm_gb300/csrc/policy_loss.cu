@@ -534,13 +534,25 @@ preference_stats_kernel(uint32_t pairs, Preference P, float* losses, float* stat
     dependency_wait();
     Sum2 loss = {}, h = {};
     uint32_t right = 0;
-    for (uint32_t i = threadIdx.x; i < pairs; i += kThreads) {
-        const float D = losses[i];
-        const PairLoss l = pair_loss(P, D);
-        losses[i] = l.loss;
-        loss.add(l.loss);
-        h.add(l.h);
-        right += D > 0.0f;
+    // four pairs of a thread on their way at a time: the loads before the stores
+    constexpr int kPairs = 4;
+    for (uint64_t at = threadIdx.x; at < pairs; at += kPairs * kThreads) {
+        float D[kPairs];
+#pragma unroll
+        for (int u = 0; u < kPairs; ++u) {
+            const uint64_t i = at + u * kThreads;
+            D[u] = i < pairs ? losses[i] : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < kPairs; ++u) {
+            const uint64_t i = at + u * kThreads;
+            if (i >= pairs) break;
+            const PairLoss l = pair_loss(P, D[u]);
+            losses[i] = l.loss;
+            loss.add(l.loss);
+            h.add(l.h);
+            right += D[u] > 0.0f;
+        }
     }
     __shared__ float2 part[2][kWarps];
     __shared__ uint32_t rights[kWarps];
