@@ -7,7 +7,7 @@
 // loss of 1000 tokens 5.7 us, preference loss of 4 pairs 4.4 us).  Large ones
 // are not yet bound by HBM: 2.1M ragged tokens with a reference, entropies and
 // per-token advantages take 27 us (61 MB, 2.3 TB/s; count, loss and the zeroing
-// before them), 2.1M even ones with less 20 us: about 680 instructions for 128
+// before them), 2.1M even ones with less 20 us: about 760 instructions for 128
 // tokens issue in half of the cycles, between chains of dependent loads (a
 // warp's sequences, then their counts).  1024 pairs of 2048 tokens take 13 us
 // (27 MB, 2.0 TB/s), 19 us where ragged: the longest pair's CTA ends last.
@@ -19,7 +19,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPerLane = 4;    // consecutive tokens of a lane
 constexpr int kChunk = 32 * kPerLane;  // and of a warp
-constexpr int kMaxGrid = 1216; // 8 CTAs for each of 152 SMs
+constexpr int kMaxGrid = 1216; // 8 CTAs for each of a GB300's 152 SMs
 constexpr int kSums = 5;       // pg, KL, entropy, clipped, old KL
 
 uint32_t token_grid(int64_t n) {
@@ -31,7 +31,12 @@ uint32_t token_grid(int64_t n) {
 // cluster / a grid): policy loss of 1024 tokens 4.2 / 9.4, 8192 6.6 / 10.5,
 // 16384 8.7 / 10.5, 32768 13.4 / 10.6; preference loss of 8 pairs and 1024
 // tokens 4.6 / 4.4 (and one launch less for the host), 8192 5.0 / 5.6, 32768
-// 7.5 / 7.7; of 16 pairs and 16384 tokens, two to a CTA, 7.5 / 5.7.
+// 7.5 / 7.7; of 16 pairs and 16384 tokens, two to a CTA, 7.5 / 5.7.  By ragged
+// sequences, policy loss with a weight per sequence: 16384 tokens in 64 11.7 /
+// 12.3, in 1024 13.9 / 11.1, in 8192 33 / 20; 8192 tokens in 8192 20 / 21; 1024
+// tokens in 1024 13.9 / 17.6, in 8192 19.5 / 24, in 16384 22 / 26: the limit on
+// the sequences bounds what the cluster zeroes and counts, a limit on their
+// ratio to the tokens would serve the case of many of both better.
 constexpr int64_t kClusterTokens = 16384, kClusterSequences = 8192, kClusterPairs = 8;
 bool in_one_cluster(const adamw_tokens_t* t) {
     return t->n <= kClusterTokens && t->sequences <= kClusterSequences;
@@ -755,9 +760,14 @@ extern "C" int adamw_preference_loss(const adamw_tokens_t* tokens, const adamw_p
                                losses, rewards, d_logp, stats), "preference launch")
                    ? ADAMW_OK : ADAMW_ERR_CUDA;
     }
-    // CTAs per pair: more where pairs are few and long (clusters for a grid
-    // that is busy without them cost: 1024 pairs of 2048 tokens 37 us by two
-    // CTAs, 13 by one)
+    // CTAs per pair: more where pairs are few and long: up to twice the 152 SMs,
+    // each with four tokens to a thread and more.  Clusters for a grid that is
+    // busy without them cost: 1024 pairs of 2048 tokens 37 us by two CTAs, 13 by
+    // one; with a limit of 1216 in place of 304 200 pairs of 8192 take 81 us for
+    // 18.  Measured (us, by at least 1 / 4 / 16 tokens to a thread): 2 pairs of
+    // 16384 9.8 / 9.8 / 8.4, 16 of 4096 15.4 / 8.0 / 7.2, 40 of 4096 23 / 11.7 /
+    // 7.4, 100 of 8192 17.1 / 17.1 / 12.3, 200 of 8192 17.8 in each: 16 would be the
+    // better limit of the three.
     int cluster = 1;
     while (cluster < 8 && pairs * cluster < 304 && per_pair >= cluster * 4 * block) cluster *= 2;
     if (pairs * cluster > kMaxCount) return ADAMW_ERR_TOO_LARGE;

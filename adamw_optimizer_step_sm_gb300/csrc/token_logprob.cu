@@ -309,9 +309,9 @@ constexpr int kDepth = 4;
 // copy: one read and one write of HBM.  A thread reads only the vectors that
 // it copied itself, so the copies need no barrier.  With the count before and
 // the statistics after it, 16376 rows of 50272 bf16 (a quarter of them ignored,
-// with the entropy) take 498 us, 5.8 TB/s; without the entropy and with none
+// with the entropy) take 502 us, 5.7 TB/s; without the entropy and with none
 // ignored 16384 rows take 549 us, 6.0 TB/s, where a 16-byte copy kernel reaches
-// 6.26.  Two rows are on an SM, eight warps, which issue in 41 % of the cycles
+// 6.26.  Two rows are on an SM, eight warps, which issue in 46 % of the cycles
 // (thirds of rows in registers, three rows to an SM, gave 0 to 2 %).
 template <int DT, bool ENT, bool WARP>
 __global__ void __launch_bounds__(kPolicyThreads)
@@ -412,7 +412,8 @@ policy_rows_kernel(Rows logits, Rows grad, Tokens tokens, int cols, float scale,
 // ------------------------------------------------------------------- host --
 
 // Fewest CTAs that keep the GPU busy: where there are fewer rows, each is
-// split over a cluster.  Measured (50272 elements, us, split / not): forward
+// split over a cluster: one for each of the 152 SMs of a GB300, for which this
+// library is built.  Measured (50272 elements, us, split / not): forward
 // of 1 row 4.7 / 5.8, of 32 5.3 / 6.0, of 76 5.7 / 6.0, of 152 6.1 / 6.3;
 // policy of 1 row 11.6 / 13.7, of 32 12.0 / 13.7, of 76 13.3 / 13.9, of 152
 // 15.5 / 15.3.  Splitting further, up to 608 CTAs, costs 1 to 2 us.

@@ -161,7 +161,9 @@ def _ptr(t: Optional[torch.Tensor]):
 def _like_rows(x: torch.Tensor) -> torch.Tensor:
     """A new tensor for the gradient of x, its rows at the same strides and the
     same distance from a 16-byte boundary (both sides then take 16-byte
-    accesses whatever the vocabulary's size), unless x is spread too thin."""
+    accesses whatever the vocabulary's size), unless x is spread too thin: more
+    than a quarter beyond its own size, and 64 rows that a short batch may skip
+    (``logits[:, :-1]`` of a few tokens), would be memory for nothing."""
     shape, stride, n = x.shape, x.stride(), x.numel()
     if len(shape) == 3 and n and stride[0] < stride[1]:   # [batch, tokens] stored as [tokens, batch]
         return _like_rows(x.transpose(0, 1)).transpose(0, 1)

@@ -67,7 +67,8 @@ typedef struct {
  *   gives NaN for the row and its gradient (a step whose gradients hold NaN
  *   is what the optimizer's non-finite flag reports).
  * Logits of -inf (masked entries) have probability 0 and take no part in the
- *   entropy.  A row that is -inf throughout has no distribution: logp -inf,
+ *   entropy; masks by finite numbers are ordinary logits, a row of one such
+ *   number throughout is uniform.  A row that is -inf throughout has no distribution: logp -inf,
  *   entropy 0, gradient 0.  A +inf or NaN logit gives NaN.
  * logp: device fp32 [rows].  entropy: device fp32 [rows] or NULL.  stats:
  *   device fp32 [rows][2], 8-byte aligned, or NULL when no backward follows.
@@ -130,7 +131,8 @@ typedef struct {
  *     loss = sum w (pg + kl_coef KL - entropy_coef entropy)
  * The comparisons are on d, so the gradient is 0 exactly where the clipped
  * branch holds: A > 0 and d > log(1 + clip_high), A < 0 and d < log(1 -
- * clip_low), A < 0 and d > log(c). */
+ * clip_low), A < 0 and d > log(c).  A token with A = 0 has pg = 0, past fp32's
+ * range of r too. */
 typedef struct {
     float clip_low;     /* in [0, 1]                                   */
     float clip_high;    /* >= 0                                        */
@@ -209,6 +211,7 @@ typedef struct {
  * mean (length_average); D = S_i - S_{B+i}, h = beta D - margin; the loss is
  * the mean over the B pairs.
  * stats: fp32 [3]: loss, share of pairs with D > 0, mean of h.
+ * D is the difference of the error-free sums, rounded once.
  * losses: fp32 [B].  rewards: fp32 [2 B], beta S.  d_logp: fp32 [n].
  * A sequence with no token that counts has S = 0 (less its reference's sum).
  * Errors: INVALID_ARG (an odd or zero number of sequences among them),
