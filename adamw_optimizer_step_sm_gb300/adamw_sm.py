@@ -1,5 +1,5 @@
-"""Python binding of the adamw_sm C ABI (include/adamw_sm.h and
-include/adamw_losses.h).
+"""Python binding of the adamw_sm C ABI (include/adamw_sm.h,
+include/adamw_losses.h and include/adamw_matrix.h).
 
 Argument marshalling only: every step of the optimizer runs in the library's
 CUDA kernels.  The functions keep the C names; a non-zero status raises
@@ -62,6 +62,9 @@ REF_NONE = 0
 REF_TOKEN = 1
 REF_SEQUENCE = 2
 NORM = {"l2": 0, "max": 1}
+
+# the matrix operators (include/adamw_matrix.h)
+MUON_SCALE = {"spectral": 0, "rms": 1}
 
 
 class AdamWError(RuntimeError):
@@ -128,6 +131,33 @@ class adamw_grad_t(ctypes.Structure):
                 ("src_dtype", ctypes.c_int32), ("dst_dtype", ctypes.c_int32)]
 
 
+class adamw_matrices_t(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_int64), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("batch_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("pad_", ctypes.c_int32)]
+
+
+class adamw_ortho_t(ctypes.Structure):
+    _fields_ = [("steps", ctypes.c_int32), ("n_coefficients", ctypes.c_int32),
+                ("coefficients", ctypes.POINTER(ctypes.c_float)), ("eps", ctypes.c_float)]
+
+
+class adamw_muon_tensor_t(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("momentum", ctypes.c_void_p),
+                ("master", ctypes.c_void_p), ("batch", ctypes.c_int64), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64)]
+
+
+class adamw_muon_options_t(ctypes.Structure):
+    _fields_ = [("ortho", adamw_ortho_t), ("nesterov", ctypes.c_int32), ("scale", ctypes.c_int32),
+                ("momentum_dtype", ctypes.c_int32)]
+
+
+class adamw_muon_hparams_t(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("pad_", ctypes.c_float)]
+
+
 _lock = threading.Lock()
 _lib: ctypes.CDLL | None = None
 
@@ -181,6 +211,18 @@ def load() -> ctypes.CDLL:
             for name in ("adamw_policy_workspace", "adamw_policy_logits_workspace"):
                 getattr(L, name).argtypes = [i64, i64]
                 getattr(L, name).restype = i64
+            mats = P(adamw_matrices_t)
+            L.adamw_orthogonalize.argtypes = [mats, mats, P(adamw_ortho_t), vp, vp]
+            L.adamw_orthogonalize_workspace.argtypes = [i64, i64, i64]
+            L.adamw_orthogonalize_workspace.restype = i64
+            L.adamw_muon_plan_create.argtypes = [P(adamw_muon_tensor_t), i32, P(adamw_muon_options_t), P(vp)]
+            L.adamw_muon_step.argtypes = [vp, vp, vp, vp]
+            L.adamw_muon_plan_destroy.argtypes = [vp]
+            L.adamw_expert_rows.argtypes = [mats, mats, i32, vp, mats, vp, vp]
+            L.adamw_expert_outer.argtypes = [mats, mats, vp, mats, i32, vp, vp]
+            L.adamw_expert_workspace.argtypes = [mats, mats]
+            L.adamw_expert_workspace.restype = i64
+            L.adamw_matrix_status.argtypes = [P(i32)]
             L.adamw_status_string.argtypes = [ctypes.c_int]
             L.adamw_status_string.restype = ctypes.c_char_p
             for name in ("adamw_plan_create", "adamw_step", "adamw_grad_norm", "adamw_step_device",
@@ -191,7 +233,10 @@ def load() -> ctypes.CDLL:
                          "adamw_plan_test_skew_barrier", "adamw_plan_test_corrupt_chunk",
                          "adamw_token_logprob", "adamw_token_logprob_backward",
                          "adamw_policy_loss", "adamw_policy_loss_logits", "adamw_preference_loss",
-                         "adamw_clip_plan_create", "adamw_clip_grads", "adamw_clip_plan_destroy"):
+                         "adamw_clip_plan_create", "adamw_clip_grads", "adamw_clip_plan_destroy",
+                         "adamw_orthogonalize", "adamw_muon_plan_create", "adamw_muon_step",
+                         "adamw_muon_plan_destroy", "adamw_expert_rows", "adamw_expert_outer",
+                         "adamw_matrix_status"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
         return _lib
@@ -410,6 +455,76 @@ def adamw_clip_grads(plan: int, max_norm: float, norm: int, result: int, stream:
 
 def adamw_clip_plan_destroy(plan: int) -> None:
     _check(load().adamw_clip_plan_destroy(plan), "adamw_clip_plan_destroy")
+
+
+# The C functions of adamw_matrix.h; matrix.py has them over torch tensors.
+
+def ortho_options(steps: int, coefficients, eps: float) -> adamw_ortho_t:
+    """coefficients: (a, b, c), or a sequence of them, one for each step (the
+    last one for the steps beyond)."""
+    rows = [coefficients] if not hasattr(coefficients[0], "__len__") else list(coefficients)
+    if any(len(r) != 3 for r in rows):
+        raise ValueError("want three coefficients a step")
+    flat = (ctypes.c_float * (3 * len(rows)))(*[float(x) for r in rows for x in r])
+    return adamw_ortho_t(steps, len(rows), flat, eps)
+
+
+def adamw_orthogonalize(src: adamw_matrices_t, dst: adamw_matrices_t, ortho: adamw_ortho_t, workspace: int,
+                        stream: int = 0) -> None:
+    rc = load().adamw_orthogonalize(ctypes.byref(src), ctypes.byref(dst), ctypes.byref(ortho), workspace or None,
+                                    stream or None)
+    _check(rc, "adamw_orthogonalize")
+
+
+def adamw_orthogonalize_workspace(batch: int, rows: int, cols: int) -> int:
+    return load().adamw_orthogonalize_workspace(batch, rows, cols)
+
+
+def adamw_muon_plan_create(entries, options: adamw_muon_options_t) -> int:
+    """entries: adamw_muon_tensor_t or (param, grad, momentum, master, batch,
+    rows, cols) tuples.  Returns the plan handle."""
+    entries = list(entries)
+    arr = (adamw_muon_tensor_t * max(1, len(entries)))()
+    for i, e in enumerate(entries):
+        arr[i] = e if isinstance(e, adamw_muon_tensor_t) else adamw_muon_tensor_t(*e)
+    out = ctypes.c_void_p()
+    rc = load().adamw_muon_plan_create(arr, len(entries), ctypes.byref(options), ctypes.byref(out))
+    _check(rc, "adamw_muon_plan_create")
+    return out.value
+
+
+def adamw_muon_step(plan: int, d_hparams: int, d_nonfinite: int, stream: int = 0) -> None:
+    _check(load().adamw_muon_step(plan, d_hparams, d_nonfinite, stream or None), "adamw_muon_step")
+
+
+def adamw_muon_plan_destroy(plan: int) -> None:
+    _check(load().adamw_muon_plan_destroy(plan), "adamw_muon_plan_destroy")
+
+
+def adamw_expert_rows(x: adamw_matrices_t, w: adamw_matrices_t, transposed: int, offsets: int, y: adamw_matrices_t,
+                      workspace: int = 0, stream: int = 0) -> None:
+    rc = load().adamw_expert_rows(ctypes.byref(x), ctypes.byref(w), transposed, offsets, ctypes.byref(y),
+                                  workspace or None, stream or None)
+    _check(rc, "adamw_expert_rows")
+
+
+def adamw_expert_outer(dy: adamw_matrices_t, x: adamw_matrices_t, offsets: int, dw: adamw_matrices_t,
+                       accumulate: int = 0, workspace: int = 0, stream: int = 0) -> None:
+    rc = load().adamw_expert_outer(ctypes.byref(dy), ctypes.byref(x), offsets, ctypes.byref(dw), accumulate,
+                                   workspace or None, stream or None)
+    _check(rc, "adamw_expert_outer")
+
+
+def adamw_expert_workspace(a: adamw_matrices_t, b: adamw_matrices_t) -> int:
+    return load().adamw_expert_workspace(ctypes.byref(a), ctypes.byref(b))
+
+
+def adamw_matrix_status() -> int:
+    """Reads and clears the current device's status word of the matrix
+    operators (1: a bounded wait ran out)."""
+    out = ctypes.c_int32(0)
+    _check(load().adamw_matrix_status(ctypes.byref(out)), "adamw_matrix_status")
+    return out.value
 
 
 def hparams(lr=2e-4, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1,

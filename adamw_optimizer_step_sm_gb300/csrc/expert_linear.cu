@@ -1,0 +1,503 @@
+// expert_linear.cu -- products grouped by expert, and the gradient of the
+// experts' matrices.
+//
+// The sizes of the groups are device data: every CTA reads the offsets, and
+// works out the list of tiles from them, so that no call waits for the host.
+#include "adamw_matrix.h"
+#include "tensor_product.cuh"
+
+namespace {
+
+constexpr int kMaxExperts = 1024;
+
+// Ends of the groups of rows: [0, first offset) and [last offset, rows) belong
+// to no expert and are the first and the last group.
+//   bounds[g] .. bounds[g + 1]: rows of group g = 0 .. experts + 1
+//   tiles[g]: tiles before group g
+struct Groups {
+    int32_t bounds[kMaxExperts + 3];
+    int32_t tiles[kMaxExperts + 3];
+};
+
+// One warp.  row_tile: rows of a tile; per: tiles for each of them.
+__device__ void build_groups(Groups* g, const int64_t* offsets, int32_t experts, int64_t rows, int32_t row_tile, int32_t per) {
+    const int lane = int(threadIdx.x) % 32;
+    int32_t top = 0, sum = 0;   // the largest offset, and the tiles, so far
+    if (lane == 0) g->bounds[0] = 0;
+    for (int base = 0; base <= experts + 1; base += 32) {
+        const int i = base + lane;
+        int32_t end = 0;   // of group i
+        if (i <= experts) {
+            const int64_t v = offsets[i];
+            end = int32_t(v < 0 ? 0 : v > rows ? rows : v);
+        } else {
+            end = int32_t(rows);
+        }
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int32_t o = __shfl_up_sync(0xffffffffu, end, d);
+            if (lane >= d && o > end) end = o;
+        }
+        if (top > end) end = top;
+        int32_t begin = __shfl_up_sync(0xffffffffu, end, 1);
+        if (lane == 0) begin = top;
+        int32_t n = i <= experts + 1 ? (end - begin + row_tile - 1) / row_tile * per : 0;
+        const int32_t mine = n;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int32_t o = __shfl_up_sync(0xffffffffu, n, d);
+            if (lane >= d) n += o;
+        }
+        if (i <= experts + 1) {
+            g->bounds[i + 1] = end;
+            g->tiles[i] = sum + n - mine;
+            if (i == experts + 1) g->tiles[i + 1] = sum + n;
+        }
+        top = __shfl_sync(0xffffffffu, end, 31);
+        sum += __shfl_sync(0xffffffffu, n, 31);
+    }
+}
+
+// The group that tile t is of.
+__device__ __forceinline__ int group_of(const Groups* g, int32_t experts, int32_t t) {
+    int low = 0, high = experts + 2;   // tiles[low] <= t < tiles[high]
+    while (high - low > 1) {
+        const int mid = (low + high) / 2;
+        if (g->tiles[mid] <= t) low = mid; else high = mid;
+    }
+    return low;
+}
+
+// Eight elements to rows of any type.
+struct RowsAt {
+    char* data;
+    int64_t ld;
+    int32_t cols, dtype;
+    int32_t vector;   // 16-byte accesses
+};
+
+template <int DT>
+__device__ __forceinline__ void store8(char* at, const float (&v)[8], int n, bool vector) {
+    using E = Elem<DT>;
+    if (vector && n >= 8) {
+        *reinterpret_cast<uint4*>(at) = E::pack(v);
+        if (E::kVec == 4) *reinterpret_cast<uint4*>(at + 16) = E::pack(v + 4);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) E::store(at, i, v[i]);
+    }
+}
+template <int DT>
+__device__ __forceinline__ void load8(const char* at, float (&v)[8], int n, bool vector) {
+    using E = Elem<DT>;
+    if (vector && n >= 8) {
+        E::unpack(*reinterpret_cast<const uint4*>(at), v);
+        if (E::kVec == 4) E::unpack(*reinterpret_cast<const uint4*>(at + 16), v + 4);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? E::load(at, i) : 0.0f;
+    }
+}
+__device__ __forceinline__ void store_rows(const RowsAt& r, int64_t row, int col, const float (&v)[8]) {
+    const int64_t at = row * r.ld + col;
+    const int n = r.cols - col;
+    if (r.dtype == ADAMW_DTYPE_BF16) store8<ADAMW_DTYPE_BF16>(r.data + at * 2, v, n, r.vector);
+    else if (r.dtype == ADAMW_DTYPE_FP16) store8<ADAMW_DTYPE_FP16>(r.data + at * 2, v, n, r.vector);
+    else store8<ADAMW_DTYPE_FP32>(r.data + at * 4, v, n, r.vector);
+}
+__device__ __forceinline__ void load_rows(const RowsAt& r, int64_t row, int col, float (&v)[8]) {
+    const int64_t at = row * r.ld + col;
+    const int n = r.cols - col;
+    if (r.dtype == ADAMW_DTYPE_BF16) load8<ADAMW_DTYPE_BF16>(r.data + at * 2, v, n, r.vector);
+    else if (r.dtype == ADAMW_DTYPE_FP16) load8<ADAMW_DTYPE_FP16>(r.data + at * 2, v, n, r.vector);
+    else load8<ADAMW_DTYPE_FP32>(r.data + at * 4, v, n, r.vector);
+}
+
+// Tile (m, n) number i of a group of tm x tn: bands of eight tiles of rows, so
+// that tiles worked on at a time share rows of both operands in L2.
+__device__ __forceinline__ void banded(int32_t i, int32_t tm, int32_t tn, int32_t* m, int32_t* n) {
+    const int32_t band = i / (8 * tn), left = tm - band * 8, h = left < 8 ? left : 8;
+    i -= band * 8 * tn;
+    *m = band * 8 + i % h;
+    *n = i / h;
+}
+
+// y = x w^T by groups of rows: A is x (K-major), B the expert's matrix.
+template <class S>
+struct ExpertRows {
+    struct Params {
+        CUtensorMap x, w;
+        const int64_t* offsets;
+        int64_t rows;
+        int32_t experts, k, tiles_n;
+        bool is_bf16, w_mn;
+        RowsAt y;
+    };
+    static constexpr bool kTail = false;
+    static constexpr size_t kTable = sizeof(Groups);
+    struct Extra {};
+    struct Out {
+        int64_t row, end;   // first row of the CTA's part, end of the group
+        int32_t col;
+    };
+    __device__ static bool bf16(const Params& p) { return p.is_bf16; }
+    __device__ static void prepare(const Params& p, unsigned char* table) {
+        if (threadIdx.x < 32)
+            build_groups(reinterpret_cast<Groups*>(table), p.offsets, p.experts, p.rows, S::kRows, p.tiles_n);
+    }
+    __device__ static int tiles(const Params& p, const unsigned char* table) {
+        return reinterpret_cast<const Groups*>(table)->tiles[p.experts + 2];
+    }
+    __device__ static int find(const Params& p, const unsigned char* table, int t, int32_t* m, int32_t* n) {
+        const Groups* g = reinterpret_cast<const Groups*>(table);
+        const int k = group_of(g, p.experts, t);
+        banded(t - g->tiles[k], (g->bounds[k + 1] - g->bounds[k] + S::kRows - 1) / S::kRows, p.tiles_n, m, n);
+        return k;
+    }
+    __device__ static void loads(const Params& p, const unsigned char* table, int t, TileLoads& w) {
+        int32_t m, n;
+        const int k = find(p, table, t, &m, &n);
+        const Groups* g = reinterpret_cast<const Groups*>(table);
+        w.a = &p.x;
+        w.b = &p.w;
+        w.a_at = g->bounds[k] + m * S::kRows;
+        w.b_at = n * S::kCols;
+        w.a_z = 0;
+        w.b_z = k - 1;
+        w.k_at = 0;
+        w.k_len = k == 0 || k == p.experts + 1 ? 0 : p.k;
+        w.a_mn = false;
+        w.b_mn = p.w_mn;
+    }
+    template <class>
+    __device__ static Out out(const Params& p, const unsigned char* table, int t, uint32_t rank) {
+        int32_t m, n;
+        const int k = find(p, table, t, &m, &n);
+        const Groups* g = reinterpret_cast<const Groups*>(table);
+        return {int64_t(g->bounds[k]) + m * S::kRows + int64_t(rank) * kRowsOfCta, g->bounds[k + 1], n * S::kCols};
+    }
+    __device__ static bool wanted(const Params& p, const Out& o, int row, int col) {
+        return o.row + row < o.end && o.col + col < p.y.cols;
+    }
+    __device__ static bool mirrored(const Out&) { return false; }
+    __device__ static void fetch(const Params&, const Out&, int, int, Extra&) {}
+    __device__ static void store(const Params& p, const Out& o, int row, int col, const Extra&, float (&v)[8]) {
+        if (o.row + row < o.end && o.col + col < p.y.cols) store_rows(p.y, o.row + row, o.col + col, v);
+    }
+    __device__ static void mirror(const Params&, const Out&, int, int, const float (&)[8]) {}
+};
+
+// dw[e] = dy^T x over the expert's rows: both operands MN-major.
+template <class S, bool ADD>
+struct ExpertOuter {
+    struct Params {
+        CUtensorMap dy, x;
+        const int64_t* offsets;
+        int64_t rows;
+        int32_t experts, n, tiles_m, tiles_n;
+        bool is_bf16;
+        int64_t stride;   // of dw's matrices
+        RowsAt dw;
+    };
+    static constexpr bool kTail = true;
+    static constexpr size_t kTable = sizeof(Groups);
+    struct Extra {
+        float v[ADD ? 8 : 1];
+    };
+    struct Out {
+        char* data;
+        int32_t row, col;
+        bool skip;
+    };
+    __device__ static bool bf16(const Params& p) { return p.is_bf16; }
+    __device__ static void prepare(const Params& p, unsigned char* table) {
+        if (threadIdx.x < 32) build_groups(reinterpret_cast<Groups*>(table), p.offsets, p.experts, p.rows, 1, 0);
+    }
+    __device__ static int tiles(const Params& p, const unsigned char*) { return p.experts * p.tiles_m * p.tiles_n; }
+    __device__ static void loads(const Params& p, const unsigned char* table, int t, TileLoads& w) {
+        const int32_t per = p.tiles_m * p.tiles_n, e = t / per;
+        int32_t m, n;
+        banded(t - e * per, p.tiles_m, p.tiles_n, &m, &n);
+        const Groups* g = reinterpret_cast<const Groups*>(table);
+        w.a = &p.dy;
+        w.b = &p.x;
+        w.a_at = m * S::kRows;
+        w.b_at = n * S::kCols;
+        w.a_z = w.b_z = 0;
+        w.k_at = g->bounds[e + 1];
+        w.k_len = g->bounds[e + 2] - g->bounds[e + 1];
+        w.a_mn = w.b_mn = true;
+    }
+    template <class>
+    __device__ static Out out(const Params& p, const unsigned char* table, int t, uint32_t rank) {
+        const int32_t per = p.tiles_m * p.tiles_n, e = t / per;
+        int32_t m, n;
+        banded(t - e * per, p.tiles_m, p.tiles_n, &m, &n);
+        const Groups* g = reinterpret_cast<const Groups*>(table);
+        const int size = p.dw.dtype == ADAMW_DTYPE_FP32 ? 4 : 2;
+        return {p.dw.data + e * p.stride * size, m * S::kRows + int32_t(rank) * kRowsOfCta, n * S::kCols,
+                ADD && g->bounds[e + 2] == g->bounds[e + 1]};
+    }
+    __device__ static bool inside(const Params& p, const Out& o, int row, int col) {
+        return o.row + row < p.n && o.col + col < p.dw.cols;
+    }
+    __device__ static bool wanted(const Params& p, const Out& o, int row, int col) { return !o.skip && inside(p, o, row, col); }
+    __device__ static bool mirrored(const Out&) { return false; }
+    __device__ static RowsAt rows(const Params& p, const Out& o) {
+        RowsAt r = p.dw;
+        r.data = o.data;
+        return r;
+    }
+    __device__ static void fetch(const Params& p, const Out& o, int row, int col, Extra& x) {
+        if constexpr (ADD) {
+            if (inside(p, o, row, col)) load_rows(rows(p, o), o.row + row, o.col + col, x.v);
+        }
+    }
+    __device__ static void store(const Params& p, const Out& o, int row, int col, const Extra& x, float (&v)[8]) {
+        if (!inside(p, o, row, col)) return;
+        if constexpr (ADD) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += x.v[i];
+        }
+        store_rows(rows(p, o), o.row + row, o.col + col, v);
+    }
+    __device__ static void mirror(const Params&, const Out&, int, int, const float (&)[8]) {}
+};
+
+// A batch of matrices of 16-bit elements, at any strides, into rows of `ld`.
+__global__ void __launch_bounds__(256) pad_kernel(const uint16_t* src, uint16_t* dst, int64_t total, int32_t rows, int32_t cols,
+                                                  int64_t row_stride, int64_t batch_stride, int32_t ld) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int32_t per = ld / 8;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
+        const int64_t line = i / per;
+        const int32_t col = int32_t(i - line * per) * 8, row = int32_t(line % rows);
+        const uint16_t* s = src + line / rows * batch_stride + row * row_stride + col;
+        uint16_t v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = col + k < cols ? s[k] : 0;
+        uint4 w;
+        memcpy(&w, v, 16);
+        reinterpret_cast<uint4*>(dst)[i] = w;
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// ------------------------------------------------------------------- host --
+
+bool sixteen(int32_t dt) { return dt == ADAMW_DTYPE_BF16 || dt == ADAMW_DTYPE_FP16; }
+constexpr int64_t kMaxSide = int64_t(1) << 30;
+
+int check(const adamw_matrices_t* m, bool operand) {
+    if (!m) return ADAMW_ERR_INVALID_ARG;
+    if (m->batch < 0 || m->rows < 0 || m->cols < 0 || m->batch_stride < 0 || m->row_stride < 0 || dtype_size(m->dtype) == 0 ||
+        (operand && !sixteen(m->dtype)))
+        return ADAMW_ERR_INVALID_ARG;
+    if (m->rows > kMaxSide || m->cols > kMaxSide || m->row_stride > (int64_t(1) << 40) || m->batch_stride > (int64_t(1) << 40))
+        return ADAMW_ERR_TOO_LARGE;
+    const bool any = m->batch > 0 && m->rows > 0 && m->cols > 0;
+    if (any && !m->data) return ADAMW_ERR_INVALID_ARG;
+    if (any && m->rows > 1 && m->row_stride < m->cols && !operand) return ADAMW_ERR_INVALID_ARG;   // rows written overlap
+    if (!aligned(m->data, uintptr_t(dtype_size(m->dtype)))) return ADAMW_ERR_MISALIGNED;
+    return ADAMW_OK;
+}
+
+// TMA reads it as it is.
+bool direct(const adamw_matrices_t& m) {
+    return aligned(m.data, 16) && (m.rows <= 1 || (m.row_stride % 8 == 0 && m.row_stride >= m.cols)) &&
+           (m.batch <= 1 || m.batch_stride % 8 == 0);
+}
+int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
+int64_t copy_bytes(const adamw_matrices_t& m) {
+    if (direct(m) || m.cols == 0) return 0;
+    return (m.batch * m.rows * padded(m.cols) * 2 + 255) / 256 * 256;
+}
+
+// The operand where TMA can read it: itself, or a copy at *workspace, which is
+// moved on.
+bool readable(adamw_matrices_t* m, char** workspace, cudaStream_t st) {
+    if (m->batch * m->rows * m->cols == 0) return true;
+    if (direct(*m)) {
+        if (m->rows <= 1) m->row_stride = padded(m->cols);
+        if (m->batch <= 1) m->batch_stride = m->row_stride * (m->rows > 0 ? m->rows : 1);
+        return true;
+    }
+    const int64_t ld = padded(m->cols), total = m->batch * m->rows * (ld / 8);
+    const int64_t want = (total + 255) / 256;
+    const uint32_t grid = uint32_t(want < 152 * 8 ? want : 152 * 8);
+    char* at = *workspace;
+    *workspace += copy_bytes(*m);
+    if (!launched(launch(pad_kernel, grid, 256, 1, 0, st, static_cast<const uint16_t*>(m->data), reinterpret_cast<uint16_t*>(at),
+                         total, int32_t(m->rows), int32_t(m->cols), m->row_stride, m->batch_stride, int32_t(ld)), "pad launch"))
+        return false;
+    m->data = at;
+    m->row_stride = ld;
+    m->batch_stride = ld * m->rows;
+    return true;
+}
+
+bool map_of(CUtensorMap* map, const adamw_matrices_t& m, bool mn) {
+    return tensor_map(map, m.dtype == ADAMW_DTYPE_BF16, m.data, m.batch, m.rows, m.cols, m.row_stride, m.batch_stride,
+                      mn ? kStepK : kRowsOfCta);
+}
+
+RowsAt rows_of(const adamw_matrices_t& m) {
+    const int size = dtype_size(m.dtype);
+    return {static_cast<char*>(m.data), m.row_stride, int32_t(m.cols), m.dtype,
+            aligned(m.data, 16) && (m.rows <= 1 || m.row_stride * size % 16 == 0) && (m.batch <= 1 || m.batch_stride * size % 16 == 0)};
+}
+
+template <class P>
+cudaError_t units_of(TileUnits* u) {
+    static thread_local int known = -1;
+    static thread_local TileUnits units;
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    if (known != device) {
+        if ((e = cudaFuncSetAttribute(tile_kernel<P, PairTile>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      int(tile_smem(P::kTable)))) != cudaSuccess) return e;
+        if ((e = tile_units<P>(&units, tile_smem(P::kTable))) != cudaSuccess) return e;
+        known = device;
+    }
+    *u = units;
+    return cudaSuccess;
+}
+
+template <class P, class S>
+bool run(const typename P::Params& p, int64_t tiles, int units, cudaStream_t st) {
+    const uint32_t grid = uint32_t(tiles < units ? tiles : units) * S::kPair;
+    static thread_local int known = -1;
+    int device = 0;
+    if (!launched(cudaGetDevice(&device), "cudaGetDevice")) return false;
+    if (known != device) {
+        if (!launched(cudaFuncSetAttribute(tile_kernel<P, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           int(tile_smem(P::kTable))), "cudaFuncSetAttribute"))
+            return false;
+        known = device;
+    }
+    return launched(launch(tile_kernel<P, S>, grid, kTileThreads, S::kPair, tile_smem(P::kTable), st, p), "product launch");
+}
+
+int64_t up(int64_t n, int64_t by) { return (n + by - 1) / by; }
+
+template <class S>
+int rows_call(const adamw_matrices_t& x, const adamw_matrices_t& w, bool transposed, const int64_t* offsets,
+              const adamw_matrices_t& y, int64_t tiles, int units, cudaStream_t st) {
+    using P = ExpertRows<S>;
+    typename P::Params p;
+    memset(&p, 0, sizeof p);
+    // sums of nothing read no operand
+    if (x.cols > 0 && (!map_of(&p.x, x, false) || !map_of(&p.w, w, transposed))) return ADAMW_ERR_CUDA;
+    p.offsets = offsets;
+    p.rows = x.rows;
+    p.experts = int32_t(w.batch);
+    p.k = int32_t(x.cols);
+    p.tiles_n = int32_t(up(y.cols, S::kCols));
+    p.is_bf16 = x.dtype == ADAMW_DTYPE_BF16;
+    p.w_mn = transposed;
+    p.y = rows_of(y);
+    return run<P, S>(p, tiles, units, st) ? ADAMW_OK : ADAMW_ERR_CUDA;
+}
+
+template <class S, bool ADD>
+int outer_call(const adamw_matrices_t& dy, const adamw_matrices_t& x, const int64_t* offsets, const adamw_matrices_t& dw,
+               int64_t tiles, int units, cudaStream_t st) {
+    using P = ExpertOuter<S, ADD>;
+    typename P::Params p;
+    memset(&p, 0, sizeof p);
+    if (x.rows > 0 && (!map_of(&p.dy, dy, true) || !map_of(&p.x, x, true))) return ADAMW_ERR_CUDA;
+    p.offsets = offsets;
+    p.rows = x.rows;
+    p.experts = int32_t(dw.batch);
+    p.n = int32_t(dw.rows);
+    p.tiles_m = int32_t(up(dw.rows, S::kRows));
+    p.tiles_n = int32_t(up(dw.cols, S::kCols));
+    p.is_bf16 = x.dtype == ADAMW_DTYPE_BF16;
+    p.stride = dw.batch_stride;
+    p.dw = rows_of(dw);
+    return run<P, S>(p, tiles, units, st) ? ADAMW_OK : ADAMW_ERR_CUDA;
+}
+
+}  // namespace
+
+namespace adamw {
+int expert_status(int32_t* out) {
+    int32_t v = 0;
+    const int32_t zero = 0;
+    if (!launched(cudaMemcpyFromSymbol(&v, g_tile_status, 4), "cudaMemcpyFromSymbol") ||
+        !launched(cudaMemcpyToSymbol(g_tile_status, &zero, 4), "cudaMemcpyToSymbol"))
+        return ADAMW_ERR_CUDA;
+    *out |= v;
+    return ADAMW_OK;
+}
+}  // namespace adamw
+
+extern "C" int64_t adamw_expert_workspace(const adamw_matrices_t* a, const adamw_matrices_t* b) {
+    if (check(a, true) != ADAMW_OK || check(b, true) != ADAMW_OK) return 0;
+    return copy_bytes(*a) + copy_bytes(*b);
+}
+
+extern "C" int adamw_expert_rows(const adamw_matrices_t* x, const adamw_matrices_t* w, int32_t transposed,
+                                 const int64_t* offsets, const adamw_matrices_t* y, void* workspace, adamw_stream_t stream) {
+    int rc;
+    if ((rc = check(x, true)) != ADAMW_OK || (rc = check(w, true)) != ADAMW_OK || (rc = check(y, false)) != ADAMW_OK) return rc;
+    const int64_t n = transposed ? w->cols : w->rows, k = transposed ? w->rows : w->cols;
+    if (x->batch != 1 || y->batch != 1 || x->dtype != w->dtype || x->cols != k || y->cols != n || y->rows != x->rows ||
+        w->batch < 1 || (transposed != 0 && transposed != 1))
+        return ADAMW_ERR_INVALID_ARG;
+    if (w->batch > kMaxExperts) return ADAMW_ERR_TOO_LARGE;
+    if (y->rows == 0 || y->cols == 0) return ADAMW_OK;
+    if (!offsets) return ADAMW_ERR_INVALID_ARG;
+    if (!aligned(offsets, 8)) return ADAMW_ERR_MISALIGNED;
+    const int64_t bytes = copy_bytes(*x) + copy_bytes(*w);
+    if (bytes > 0 && !workspace) return ADAMW_ERR_INVALID_ARG;
+    if (bytes > 0 && !aligned(workspace, 256)) return ADAMW_ERR_MISALIGNED;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    // at most: every group's last tile is a partial one
+    const int64_t groups = w->batch + 2;
+    const int64_t pair_tiles = (x->rows / PairTile::kRows + groups) * up(n, PairTile::kCols);
+    const int64_t single_tiles = (x->rows / SingleTile::kRows + groups) * up(n, SingleTile::kCols);
+    if (single_tiles > kMaxCount) return ADAMW_ERR_TOO_LARGE;
+    TileUnits units;
+    if (!launched(units_of<ExpertRows<PairTile>>(&units), "tile units")) return ADAMW_ERR_CUDA;
+    adamw_matrices_t a = *x, b = *w;
+    char* at = static_cast<char*>(workspace);
+    if (!readable(&a, &at, st) || !readable(&b, &at, st)) return ADAMW_ERR_CUDA;
+    // few rows for each expert leave most of a pair's tile empty, and few tiles leave SMs idle
+    const bool pair = x->rows >= w->batch * 128 && pair_tiles - groups * up(n, PairTile::kCols) >= units.pairs;
+    return pair ? rows_call<PairTile>(a, b, transposed != 0, offsets, *y, pair_tiles, units.pairs, st)
+                : rows_call<SingleTile>(a, b, transposed != 0, offsets, *y, single_tiles, units.sms, st);
+}
+
+extern "C" int adamw_expert_outer(const adamw_matrices_t* dy, const adamw_matrices_t* x, const int64_t* offsets,
+                                  const adamw_matrices_t* dw, int32_t accumulate, void* workspace, adamw_stream_t stream) {
+    int rc;
+    if ((rc = check(dy, true)) != ADAMW_OK || (rc = check(x, true)) != ADAMW_OK || (rc = check(dw, false)) != ADAMW_OK) return rc;
+    if (dy->batch != 1 || x->batch != 1 || dy->dtype != x->dtype || dy->rows != x->rows || dw->rows != dy->cols ||
+        dw->cols != x->cols || dw->batch < 1 || (accumulate != 0 && accumulate != 1) ||
+        (dw->batch > 1 && dw->rows > 0 && dw->cols > 0 && dw->batch_stride < (dw->rows - 1) * dw->row_stride + dw->cols))
+        return ADAMW_ERR_INVALID_ARG;
+    if (dw->batch > kMaxExperts) return ADAMW_ERR_TOO_LARGE;
+    if (dw->rows == 0 || dw->cols == 0) return ADAMW_OK;
+    if (!offsets) return ADAMW_ERR_INVALID_ARG;
+    if (!aligned(offsets, 8)) return ADAMW_ERR_MISALIGNED;
+    const int64_t bytes = copy_bytes(*dy) + copy_bytes(*x);
+    if (bytes > 0 && !workspace) return ADAMW_ERR_INVALID_ARG;
+    if (bytes > 0 && !aligned(workspace, 256)) return ADAMW_ERR_MISALIGNED;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int64_t pair_tiles = dw->batch * up(dw->rows, PairTile::kRows) * up(dw->cols, PairTile::kCols);
+    const int64_t single_tiles = dw->batch * up(dw->rows, SingleTile::kRows) * up(dw->cols, SingleTile::kCols);
+    if (single_tiles > kMaxCount) return ADAMW_ERR_TOO_LARGE;
+    TileUnits units;
+    if (!launched(units_of<ExpertOuter<PairTile, false>>(&units), "tile units")) return ADAMW_ERR_CUDA;
+    adamw_matrices_t a = *dy, b = *x;
+    char* at = static_cast<char*>(workspace);
+    if (!readable(&a, &at, st) || !readable(&b, &at, st)) return ADAMW_ERR_CUDA;
+    if (pair_tiles >= units.pairs)
+        return accumulate ? outer_call<PairTile, true>(a, b, offsets, *dw, pair_tiles, units.pairs, st)
+                          : outer_call<PairTile, false>(a, b, offsets, *dw, pair_tiles, units.pairs, st);
+    return accumulate ? outer_call<SingleTile, true>(a, b, offsets, *dw, single_tiles, units.sms, st)
+                      : outer_call<SingleTile, false>(a, b, offsets, *dw, single_tiles, units.sms, st);
+}

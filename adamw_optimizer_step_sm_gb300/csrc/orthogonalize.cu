@@ -1,0 +1,1016 @@
+// orthogonalize.cu -- Newton-Schulz orthogonalisation of lists of matrices, and
+// the Muon step around it.
+//
+// A call is: the norms of the matrices, their scaled copies in fp16, and three
+// products a step,
+//     gram   G = X X^T             (symmetric: the tiles on and below the diagonal)
+//     poly   Q = b G + c G G       (likewise)
+//     apply  X <- a X + Q X
+// all matrices of a list in one launch each.  A matrix with more rows than
+// columns takes X^T X and X Q: its operands are then read along the other
+// dimension, and nothing is transposed.
+//
+// Numbers.  Everything between the products is fp16 at 2^12 times its value:
+// X's singular values stay below 1.3, so |X| and |G| are below 2, |Q| below 4
+// with the usual coefficients (16 would overflow), and the small entries of
+// large matrices (2^-12 of the norm in a 4096 x 4096 one) stay normal numbers.
+// fp16's 11 bits carry an eighth of bf16's rounding errors: bf16 was 1e-2 (random
+// matrices) to 2e-1 (rank 64 of 768) off the exact iteration, this is 2e-4 to
+// 1.6e-3.  X is kept as hi + lo, two fp16: each step multiplies an error of X in
+// a direction without singular value by a = 3.44, and a rounding of X itself
+// would be such an error; the rounding of the products' operands (hi alone) is
+// multiplied by Q, which vanishes in such directions.
+#include <algorithm>
+#include <exception>
+#include <new>
+#include <vector>
+
+#include "adamw_matrix.h"
+#include "tensor_product.cuh"
+
+namespace {
+
+constexpr float kScale = 4096.0f, kUnscale = 1.0f / 4096.0f;
+constexpr float kLow = 2048.0f;   // lo is kept times this
+
+using Fp16 = Elem<ADAMW_DTYPE_FP16>;
+
+// Matrices of one shape, whose working copies lie one after the other.
+struct Shape {
+    int64_t stride, small_stride;   // elements between matrices (of X, of G)
+    int32_t rows, cols, ld;         // ld: cols up to a multiple of 8
+    int32_t side, small_ld;         // of G
+    int32_t count, first;           // matrices, and the first one's number in the list
+};
+
+constexpr int kMaxShapes = 8;   // in a launch
+
+// ------------------------------------------------------- norms and copies --
+
+// Where a plan's matrices are.
+struct MuonMatrix {
+    uint16_t* param;
+    const uint16_t* grad;
+    void* momentum;
+    float* master;
+};
+
+// The matrices of a call without a plan.
+struct Batch {
+    char* data;
+    int64_t batch_stride, row_stride;
+    int32_t dtype;
+    int32_t vector;   // 16-byte accesses
+};
+
+constexpr int kNormThreads = 256;
+constexpr int kPieceVecs = 2048;   // vectors of eight elements that a CTA takes
+
+struct CopyShape {
+    Shape s;
+    uint16_t *hi, *lo;
+    int32_t pieces;        // of a matrix
+    int32_t first_piece;   // of the shape, in the launch
+    int32_t first_sum;     // of the shape, in the list
+};
+
+template <bool MUON>
+struct CopyParams {
+    CopyShape shapes[kMaxShapes];
+    int32_t n;
+    double* sums;      // by piece
+    float eps;
+    // without a plan
+    Batch src;
+    // a plan's
+    const MuonMatrix* table;
+    const adamw_muon_hparams_t* hp;
+    int32_t* nonfinite;
+    int32_t nesterov, momentum_bf16;
+};
+
+__device__ __forceinline__ void load8_any(const char* data, int64_t at, int32_t dtype, bool vector, int n, float (&v)[8]) {
+    if (dtype == ADAMW_DTYPE_FP32) {
+        using E = Elem<ADAMW_DTYPE_FP32>;
+        if (vector && n >= 8) {
+            E::unpack(*reinterpret_cast<const uint4*>(data + at * 4), v);
+            E::unpack(*reinterpret_cast<const uint4*>(data + at * 4 + 16), v + 4);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = i < n ? E::load(data, at + i) : 0.0f;
+        }
+    } else if (dtype == ADAMW_DTYPE_BF16) {
+        using E = Elem<ADAMW_DTYPE_BF16>;
+        if (vector && n >= 8) E::unpack(*reinterpret_cast<const uint4*>(data + at * 2), v);
+        else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = i < n ? E::load(data, at + i) : 0.0f;
+        }
+    } else {
+        if (vector && n >= 8) Fp16::unpack(*reinterpret_cast<const uint4*>(data + at * 2), v);
+        else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = i < n ? Fp16::load(data, at + i) : 0.0f;
+        }
+    }
+}
+__device__ __forceinline__ void store8_any(char* data, int64_t at, int32_t dtype, bool vector, int n, const float (&v)[8]) {
+    if (dtype == ADAMW_DTYPE_FP32) {
+        using E = Elem<ADAMW_DTYPE_FP32>;
+        if (vector && n >= 8) {
+            *reinterpret_cast<uint4*>(data + at * 4) = E::pack(v);
+            *reinterpret_cast<uint4*>(data + at * 4 + 16) = E::pack(v + 4);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < n) E::store(data, at + i, v[i]);
+        }
+    } else if (dtype == ADAMW_DTYPE_BF16) {
+        using E = Elem<ADAMW_DTYPE_BF16>;
+        if (vector && n >= 8) *reinterpret_cast<uint4*>(data + at * 2) = E::pack(v);
+        else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < n) E::store(data, at + i, v[i]);
+        }
+    } else {
+        if (vector && n >= 8) *reinterpret_cast<uint4*>(data + at * 2) = Fp16::pack(v);
+        else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < n) Fp16::store(data, at + i, v[i]);
+        }
+    }
+}
+
+// Eight elements of what is orthogonalised: the source, or the step's update
+// of gradient and momentum (then the new momentum in `m`).
+template <bool MUON>
+struct Source {
+    const CopyParams<MUON>& p;
+    const CopyShape& c;
+    MuonMatrix t;
+    const char* data;
+    float mu;
+    bool vector;
+    __device__ Source(const CopyParams<MUON>& p, const CopyShape& c, int matrix) : p(p), c(c) {
+        if (MUON) {
+            t = p.table[c.s.first + matrix];
+            mu = p.hp->momentum;
+            vector = c.s.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(t.grad) | reinterpret_cast<uintptr_t>(t.momentum)) % 16 == 0;
+        } else {
+            const int size = p.src.dtype == ADAMW_DTYPE_FP32 ? 4 : 2;
+            data = p.src.data + matrix * p.src.batch_stride * size;
+            vector = p.src.vector != 0;
+        }
+    }
+    __device__ __forceinline__ void get(int row, int col, float (&u)[8], float (&m)[8]) const {
+        const int n = c.s.cols - col;
+        if (MUON) {
+            const int64_t at = int64_t(row) * c.s.cols + col;
+            load8_any(reinterpret_cast<const char*>(t.grad), at, ADAMW_DTYPE_BF16, vector, n, u);
+            load8_any(static_cast<const char*>(t.momentum), at, p.momentum_bf16 ? ADAMW_DTYPE_BF16 : ADAMW_DTYPE_FP32, vector, n, m);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                m[i] = fmaf(1.0f - mu, u[i] - m[i], m[i]);
+                u[i] = p.nesterov ? fmaf(mu, m[i] - u[i], u[i]) : m[i];
+            }
+        } else {
+            load8_any(data, row * p.src.row_stride + col, p.src.dtype, vector, n, u);
+        }
+    }
+    __device__ __forceinline__ void put(int row, int col, const float (&m)[8]) const {
+        if (MUON)
+            store8_any(static_cast<char*>(t.momentum), int64_t(row) * c.s.cols + col,
+                       p.momentum_bf16 ? ADAMW_DTYPE_BF16 : ADAMW_DTYPE_FP32, vector, c.s.cols - col, m);
+    }
+};
+
+// The shape and the matrix of piece i, which becomes its number in the matrix.
+template <bool MUON>
+__device__ __forceinline__ const CopyShape& piece_of(const CopyParams<MUON>& p, int32_t* i, int32_t* matrix) {
+    int k = 0;
+    while (k + 1 < p.n && p.shapes[k + 1].first_piece <= *i) ++k;
+    const CopyShape& c = p.shapes[k];
+    *i -= c.first_piece;
+    *matrix = *i / c.pieces;
+    *i -= *matrix * c.pieces;
+    return c;
+}
+
+// Sum of squares of each piece.  Eight squares are summed in fp32 and added in
+// fp64; squares that leave fp32's comfortable range are taken in fp64.
+template <bool MUON>
+__global__ void __launch_bounds__(kNormThreads) norm_kernel(const __grid_constant__ CopyParams<MUON> p) {
+    __shared__ double part[kNormThreads / 32];
+    int32_t i = int32_t(blockIdx.x), matrix;
+    const CopyShape& c = piece_of(p, &i, &matrix);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const Source<MUON> src(p, c, matrix);
+    const int32_t per = c.s.ld / 8;
+    const int64_t total = int64_t(c.s.rows) * per, first = int64_t(i) * kPieceVecs;
+    double sum = 0.0;
+#pragma unroll 4
+    for (int k = int(threadIdx.x); k < kPieceVecs; k += kNormThreads) {
+        const int64_t v = first + k;
+        if (v >= total) continue;
+        const int32_t row = int32_t(v / per), col = int32_t(v - int64_t(row) * per) * 8;
+        float u[8], m[8];
+        src.get(row, col, u, m);
+        float s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(u[e], u[e], s);
+        if (s >= 0x1p-100f && s <= 0x1p100f) {
+            sum += double(s);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum += double(u[e]) * double(u[e]);
+        }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double s = 0.0;
+        for (int k = 0; k < kNormThreads / 32; ++k) s += part[k];
+        p.sums[c.first_sum + matrix * c.pieces + i] = s;
+        if (MUON && !(s <= 1.7976931348623157e308)) atomicOr(p.nonfinite, 1);
+    }
+}
+
+// x at 2^12 times its value, as two fp16.
+__device__ __forceinline__ void split8(const float (&x)[8], uint4* hi, uint4* lo) {
+    *hi = Fp16::pack(x);
+    float h[8], l[8];
+    Fp16::unpack(*hi, h);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) l[e] = (x[e] - h[e]) * kLow;
+    *lo = Fp16::pack(l);
+}
+
+// The scaled copies; a plan's new momentum.
+template <bool MUON>
+__global__ void __launch_bounds__(kNormThreads) copy_kernel(const __grid_constant__ CopyParams<MUON> p) {
+    __shared__ double part[kNormThreads / 32];
+    int32_t i = int32_t(blockIdx.x), matrix;
+    const CopyShape& c = piece_of(p, &i, &matrix);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const bool skip = MUON && *p.nonfinite != 0;
+    // the matrix's norm, by every CTA
+    double sum = 0.0;
+    for (int k = int(threadIdx.x); k < c.pieces; k += kNormThreads) sum += p.sums[c.first_sum + matrix * c.pieces + k];
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = sum;
+    __syncthreads();
+    sum = 0.0;
+    for (int k = 0; k < kNormThreads / 32; ++k) sum += part[k];
+    const double norm = sqrt(sum);
+    // NaN for a sum that is not finite: the matrix has no direction
+    const float by = sum <= 1.7976931348623157e308 ? float(double(kScale) / (norm > p.eps ? norm : double(p.eps))) : sqrtf(-1.0f);
+    const Source<MUON> src(p, c, matrix);
+    const int32_t per = c.s.ld / 8;
+    const int64_t total = int64_t(c.s.rows) * per, first = int64_t(i) * kPieceVecs;
+    uint4* hi = reinterpret_cast<uint4*>(c.hi + matrix * c.s.stride);
+    uint4* lo = reinterpret_cast<uint4*>(c.lo + matrix * c.s.stride);
+#pragma unroll 4
+    for (int k = int(threadIdx.x); k < kPieceVecs; k += kNormThreads) {
+        const int64_t v = first + k;
+        if (v >= total) continue;
+        const int32_t row = int32_t(v / per), col = int32_t(v - int64_t(row) * per) * 8;
+        float u[8], m[8];
+        src.get(row, col, u, m);
+        if (MUON && !skip) src.put(row, col, m);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] *= by;
+        uint4 h, l;
+        split8(u, &h, &l);
+        hi[v] = h;   // rows of `per` vectors, as the copy has
+        lo[v] = l;
+    }
+}
+
+// ---------------------------------------------------------------- products --
+
+enum Kind { kGram, kPoly, kApply, kResult, kUpdate };
+
+struct ProductShape {
+    CUtensorMap a, b;
+    Shape s;
+    int32_t m, n, k;                   // the product's own
+    int32_t tiles_m, tiles_n, per;     // tiles of a matrix
+    int32_t first_tile;
+    bool a_mn, b_mn;
+    uint16_t* out;                     // G, Q or the next hi
+    const uint16_t* hi;                // X, or G for Q
+    uint16_t* lo;
+    float rate;                        // of the update
+};
+
+struct ProductParams {
+    ProductShape shapes[kMaxShapes];
+    int32_t n, tiles;
+    float a, b, c;
+    Batch dst;
+    const MuonMatrix* table;
+    const adamw_muon_hparams_t* hp;
+    const int32_t* nonfinite;
+};
+
+template <int KIND, class S>
+struct Product {
+    using Params = ProductParams;
+    static constexpr bool kTail = false;
+    static constexpr size_t kTable = 0;
+    static constexpr bool kSymmetric = KIND == kGram || KIND == kPoly;
+    static_assert(!kSymmetric || S::kRows == S::kCols, "symmetric products take square tiles");
+
+    // what the epilogue adds to the product
+    struct Extra {
+        uint4 hi, lo;
+        float w[KIND == kUpdate ? 8 : 1];
+    };
+    struct Out {
+        const ProductShape* p;
+        int32_t matrix, row, col;   // of the CTA's part
+        bool mirrored, vector, skip;
+        uint16_t *out, *lo;
+        const uint16_t* hi;
+        MuonMatrix t;
+        float decay, rate;
+    };
+    __device__ static bool bf16(const Params&) { return false; }
+    __device__ static void prepare(const Params&, unsigned char*) {}
+    __device__ static int tiles(const Params& p, const unsigned char*) { return p.tiles; }
+    __device__ static const ProductShape& find(const Params& p, int t, int32_t* matrix, int32_t* m, int32_t* n) {
+        int k = 0;
+        while (k + 1 < p.n && p.shapes[k + 1].first_tile <= t) ++k;
+        const ProductShape& c = p.shapes[k];
+        t -= c.first_tile;
+        *matrix = t / c.per;
+        t -= *matrix * c.per;
+        if (kSymmetric) {
+            // row by row of the lower triangle: row r has r + 1 tiles
+            int32_t r = int32_t((sqrtf(8.0f * float(t) + 1.0f) - 1.0f) * 0.5f);
+            while (r * (r + 1) / 2 > t) --r;
+            while ((r + 1) * (r + 2) / 2 <= t) ++r;
+            *m = r;
+            *n = t - r * (r + 1) / 2;
+        } else {
+            // bands of eight tiles of rows, for reuse in L2
+            const int32_t band = t / (8 * c.tiles_n), left = c.tiles_m - band * 8, h = left < 8 ? left : 8;
+            t -= band * 8 * c.tiles_n;
+            *m = band * 8 + t % h;
+            *n = t / h;
+        }
+        return c;
+    }
+    __device__ static void loads(const Params& p, const unsigned char*, int t, TileLoads& w) {
+        int32_t m, n;
+        const ProductShape& c = find(p, t, &w.a_z, &m, &n);
+        w.b_z = w.a_z;
+        w.a = &c.a;
+        w.b = &c.b;
+        w.a_at = m * S::kRows;
+        w.b_at = n * S::kCols;
+        w.k_at = 0;
+        w.k_len = c.k;
+        w.a_mn = c.a_mn;
+        w.b_mn = c.b_mn;
+    }
+    template <class>
+    __device__ static Out out(const Params& p, const unsigned char*, int t, uint32_t rank) {
+        Out o;
+        int32_t m, n;
+        const ProductShape& c = find(p, t, &o.matrix, &m, &n);
+        o.p = &c;
+        o.row = m * S::kRows + int32_t(rank) * kRowsOfCta;
+        o.col = n * S::kCols;
+        o.mirrored = kSymmetric && m != n;
+        o.skip = false;
+        const int64_t at = o.matrix * (kSymmetric ? c.s.small_stride : c.s.stride);
+        o.out = c.out + at;
+        o.hi = c.hi + at;
+        o.lo = c.lo + at;
+        if constexpr (KIND == kUpdate) {
+            o.t = p.table[c.s.first + o.matrix];
+            o.vector = c.s.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(o.t.master) | reinterpret_cast<uintptr_t>(o.t.param)) % 16 == 0;
+            o.skip = *p.nonfinite != 0;
+            const float lr = p.hp->lr;
+            o.decay = 1.0f - lr * p.hp->weight_decay;
+            o.rate = lr * c.rate * kUnscale;
+        }
+        return o;
+    }
+    __device__ static int ld(const Out& o) { return kSymmetric ? o.p->s.small_ld : o.p->s.ld; }
+    __device__ static bool wanted(const Params&, const Out& o, int row, int col) {
+        return !o.skip && o.row + row < o.p->m && o.col + col < o.p->n;
+    }
+    __device__ static bool mirrored(const Out& o) { return o.mirrored; }
+    __device__ static void fetch(const Params& p, const Out& o, int row, int col, Extra& x) {
+        if (KIND == kGram || !wanted(p, o, row, col)) return;
+        const int64_t at = int64_t(o.row + row) * ld(o) + o.col + col;
+        x.hi = *reinterpret_cast<const uint4*>(o.hi + at);
+        if (!kSymmetric) x.lo = *reinterpret_cast<const uint4*>(o.lo + at);
+        if constexpr (KIND == kUpdate)
+            load8_any(reinterpret_cast<const char*>(o.t.master), int64_t(o.row + row) * o.p->s.cols + o.col + col,
+                      ADAMW_DTYPE_FP32, o.vector, o.p->s.cols - o.col - col, x.w);
+    }
+    __device__ static void store(const Params& p, const Out& o, int row, int col, const Extra& x, float (&v)[8]) {
+        const bool here = wanted(p, o, row, col);
+        const int64_t at = int64_t(o.row + row) * ld(o) + o.col + col;
+        if constexpr (kSymmetric) {
+            float g[8];
+            if (KIND == kPoly && here) Fp16::unpack(x.hi, g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = KIND == kPoly ? (here ? fmaf(p.b, g[e], p.c * kUnscale * v[e]) : 0.0f) : v[e] * kUnscale;
+            if (here) *reinterpret_cast<uint4*>(o.out + at) = Fp16::pack(v);
+        } else if (here) {
+            float h[8], l[8];
+            Fp16::unpack(x.hi, h);
+            Fp16::unpack(x.lo, l);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = fmaf(p.a, fmaf(l[e], 1.0f / kLow, h[e]), v[e] * kUnscale);
+            if constexpr (KIND == kApply) {
+                uint4 hi, lo;
+                split8(v, &hi, &lo);
+                *reinterpret_cast<uint4*>(o.out + at) = hi;
+                *reinterpret_cast<uint4*>(o.lo + at) = lo;
+            } else if constexpr (KIND == kResult) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] *= kUnscale;
+                const int64_t to = o.matrix * p.dst.batch_stride + int64_t(o.row + row) * p.dst.row_stride + o.col + col;
+                store8_any(p.dst.data, to, p.dst.dtype, p.dst.vector, o.p->s.cols - o.col - col, v);
+            } else {
+                const int64_t to = int64_t(o.row + row) * o.p->s.cols + o.col + col;
+                const int n = o.p->s.cols - o.col - col;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = fmaf(-o.rate, v[e], o.decay * x.w[e]);
+                store8_any(reinterpret_cast<char*>(o.t.master), to, ADAMW_DTYPE_FP32, o.vector, n, v);
+                store8_any(reinterpret_cast<char*>(o.t.param), to, ADAMW_DTYPE_BF16, o.vector, n, v);
+            }
+        }
+    }
+    // rows row .. row + 7 of column col, as a row of the mirrored tile
+    __device__ static void mirror(const Params&, const Out& o, int col, int row, const float (&v)[8]) {
+        if (!kSymmetric || o.col + col >= o.p->n || o.row + row >= o.p->m) return;
+        *reinterpret_cast<uint4*>(o.out + int64_t(o.col + col) * ld(o) + o.row + row) = Fp16::pack(v);
+    }
+};
+
+// -------------------------------------------------------------------- host --
+
+constexpr int64_t kMaxSide = int64_t(1) << 20;
+constexpr int64_t kMaxElems = int64_t(1) << 40, kMaxMatrices = int64_t(1) << 20;
+
+int64_t up(int64_t n, int64_t by) { return (n + by - 1) / by * by; }
+
+Shape shape_of(int64_t rows, int64_t cols) {
+    Shape s = {};
+    s.rows = int32_t(rows);
+    s.cols = int32_t(cols);
+    s.ld = int32_t(up(cols, 8));
+    s.stride = up(rows * s.ld, 8);
+    s.side = s.rows <= s.cols ? s.rows : s.cols;
+    s.small_ld = int32_t(up(s.side, 8));
+    s.small_stride = int64_t(s.side) * s.small_ld;
+    return s;
+}
+int64_t pieces_of(const Shape& s) { return (int64_t(s.rows) * (s.ld / 8) + kPieceVecs - 1) / kPieceVecs; }
+
+// The working copies of a shape.
+struct Buffers {
+    uint16_t *x[2], *lo, *gram, *poly;
+};
+// A shape's buffers at `at`, each at a multiple of 256 bytes; the bytes they take.
+int64_t place(const Shape& s, char* at, Buffers* b) {
+    const int64_t big = up(s.stride * s.count * 2, 256), small = up(s.small_stride * s.count * 2, 256);
+    if (b) {
+        b->x[0] = reinterpret_cast<uint16_t*>(at);
+        b->x[1] = reinterpret_cast<uint16_t*>(at + big);
+        b->lo = reinterpret_cast<uint16_t*>(at + 2 * big);
+        b->gram = reinterpret_cast<uint16_t*>(at + 3 * big);
+        b->poly = reinterpret_cast<uint16_t*>(at + 3 * big + small);
+    }
+    return 3 * big + 2 * small;
+}
+
+// The products of one group of shapes: at most kMaxShapes.
+struct Group {
+    int n = 0;
+    Shape shapes[kMaxShapes];
+    Buffers buffers[kMaxShapes];
+    float rate[kMaxShapes];
+};
+
+// The products' arguments, but for the coefficients.  which: X's buffer.
+template <class S>
+bool fill(const Group& g, int kind, int which, ProductParams* p) {
+    memset(p, 0, sizeof *p);
+    p->n = g.n;
+    int64_t tiles = 0;
+    for (int i = 0; i < g.n; ++i) {
+        const Shape& s = g.shapes[i];
+        const Buffers& b = g.buffers[i];
+        ProductShape& q = p->shapes[i];
+        q.s = s;
+        q.rate = g.rate[i];
+        const bool wide = s.rows <= s.cols;
+        bool ok;
+        if (kind == kGram) {
+            q.a_mn = q.b_mn = !wide;
+            q.m = q.n = s.side;
+            q.k = wide ? s.cols : s.rows;
+            ok = tensor_map(&q.a, false, b.x[which], s.count, s.rows, s.cols, s.ld, s.stride, wide ? kRowsOfCta : kStepK);
+            q.b = q.a;
+            q.out = b.gram;
+        } else if (kind == kPoly) {
+            q.m = q.n = q.k = s.side;
+            ok = tensor_map(&q.a, false, b.gram, s.count, s.side, s.side, s.small_ld, s.small_stride, kRowsOfCta);
+            q.b = q.a;
+            q.hi = b.gram;
+            q.out = b.poly;
+        } else {
+            q.m = s.rows;
+            q.n = s.cols;
+            q.k = s.side;
+            q.b_mn = wide;
+            ok = tensor_map(wide ? &q.b : &q.a, false, b.x[which], s.count, s.rows, s.cols, s.ld, s.stride, wide ? kStepK : kRowsOfCta) &&
+                 tensor_map(wide ? &q.a : &q.b, false, b.poly, s.count, s.side, s.side, s.small_ld, s.small_stride, kRowsOfCta);
+            q.hi = b.x[which];
+            q.lo = b.lo;
+            q.out = b.x[which ^ 1];
+        }
+        if (!ok) return false;
+        q.tiles_m = int32_t(up(q.m, S::kRows) / S::kRows);
+        q.tiles_n = int32_t(up(q.n, S::kCols) / S::kCols);
+        const int64_t per = kind == kGram || kind == kPoly ? int64_t(q.tiles_m) * (q.tiles_m + 1) / 2 : int64_t(q.tiles_m) * q.tiles_n;
+        q.per = int32_t(per);
+        q.first_tile = int32_t(tiles);
+        tiles += per * s.count;
+        if (tiles > kMaxCount) return false;
+    }
+    p->tiles = int32_t(tiles);
+    return true;
+}
+
+struct Device {
+    int sms = 0, pairs = 0;
+};
+
+template <int KIND, class S>
+bool allow() {
+    using P = Product<KIND, S>;
+    return launched(cudaFuncSetAttribute(tile_kernel<P, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         int(tile_smem(P::kTable))), "cudaFuncSetAttribute");
+}
+
+// The current device's units; allows the kernels' shared memory there.
+bool device_units(Device* d) {
+    static thread_local int known = -1;
+    static thread_local Device units;
+    int device = 0;
+    if (!launched(cudaGetDevice(&device), "cudaGetDevice")) return false;
+    if (known != device) {
+        if (!allow<kGram, PairTile>() || !allow<kPoly, PairTile>() || !allow<kApply, PairTile>() || !allow<kResult, PairTile>() ||
+            !allow<kUpdate, PairTile>() || !allow<kGram, SingleTile>() || !allow<kPoly, SingleTile>() || !allow<kApply, SingleTile>() ||
+            !allow<kResult, SingleTile>() || !allow<kUpdate, SingleTile>())
+            return false;
+        TileUnits u;
+        if (!launched(tile_units<Product<kApply, PairTile>>(&u, tile_smem(0)), "tile units")) return false;
+        units.sms = u.sms;
+        units.pairs = u.pairs;
+        known = device;
+    }
+    *d = units;
+    return true;
+}
+
+template <int KIND, class S>
+bool launch_product(const ProductParams& p, int units, cudaStream_t st) {
+    const uint32_t grid = uint32_t(p.tiles < units ? p.tiles : units) * S::kPair;
+    using P = Product<KIND, S>;
+    return launched(launch(tile_kernel<P, S>, grid, kTileThreads, S::kPair, tile_smem(P::kTable), st, p), "product launch");
+}
+template <class S>
+bool launch_kind(int kind, const ProductParams& p, int units, cudaStream_t st) {
+    switch (kind) {
+        case kGram: return launch_product<kGram, S>(p, units, st);
+        case kPoly: return launch_product<kPoly, S>(p, units, st);
+        case kApply: return launch_product<kApply, S>(p, units, st);
+        case kResult: return launch_product<kResult, S>(p, units, st);
+        default: return launch_product<kUpdate, S>(p, units, st);
+    }
+}
+
+// The steps of one group, whose copies have been made.  last: kResult or
+// kUpdate, with what it needs in `with`.
+bool run_steps(const Group& g, const adamw_ortho_t& o, const float* coefs, int last, const ProductParams& with, const Device& d,
+               cudaStream_t st) {
+    // pairs where their tiles fill the GPU
+    int64_t pair_tiles = 0;
+    for (int i = 0; i < g.n; ++i)
+        pair_tiles += g.shapes[i].count * (up(g.shapes[i].rows, 256) / 256) * (up(g.shapes[i].cols, 256) / 256);
+    const bool pair = pair_tiles * 2 >= d.pairs;
+    for (int k = 0; k < o.steps; ++k) {
+        const float* c = coefs + 3 * (k < o.n_coefficients ? k : o.n_coefficients - 1);
+        for (int kind = kGram; kind <= kApply; ++kind) {
+            const int which = kind == kApply && k + 1 == o.steps ? last : kind;
+            ProductParams p;
+            if (!(pair ? fill<PairTile>(g, kind, k & 1, &p) : fill<SingleTile>(g, kind, k & 1, &p))) return false;
+            p.a = c[0];
+            p.b = c[1];
+            p.c = c[2];
+            p.dst = with.dst;
+            p.table = with.table;
+            p.hp = with.hp;
+            p.nonfinite = with.nonfinite;
+            if (!(pair ? launch_kind<PairTile>(which, p, d.pairs, st) : launch_kind<SingleTile>(which, p, d.sms, st))) return false;
+        }
+    }
+    return true;
+}
+
+int check_ortho(const adamw_ortho_t* o) {
+    if (!o || o->steps < 1 || o->steps > 32 || o->n_coefficients < 1 || o->n_coefficients > 32 || !o->coefficients ||
+        !(o->eps > 0.0f) || !std::isfinite(o->eps))
+        return ADAMW_ERR_INVALID_ARG;
+    for (int i = 0; i < 3 * o->n_coefficients; ++i)
+        if (!std::isfinite(o->coefficients[i])) return ADAMW_ERR_INVALID_ARG;
+    return ADAMW_OK;
+}
+
+bool sizes_fit(int64_t batch, int64_t rows, int64_t cols) {
+    return batch >= 0 && rows >= 0 && cols >= 0 && rows <= kMaxSide && cols <= kMaxSide && batch <= kMaxMatrices &&
+           (rows == 0 || cols == 0 || batch <= kMaxElems / (rows * cols));
+}
+
+int check_matrices(const adamw_matrices_t* m, bool written) {
+    if (!m || m->batch < 0 || m->rows < 0 || m->cols < 0 || m->batch_stride < 0 || m->row_stride < 0 || dtype_size(m->dtype) == 0)
+        return ADAMW_ERR_INVALID_ARG;
+    if (!sizes_fit(m->batch, m->rows, m->cols) || m->row_stride > (int64_t(1) << 40) || m->batch_stride > (int64_t(1) << 40))
+        return ADAMW_ERR_TOO_LARGE;
+    if (m->batch * m->rows * m->cols == 0) return ADAMW_OK;
+    if (!m->data) return ADAMW_ERR_INVALID_ARG;
+    if (written && ((m->rows > 1 && m->row_stride < m->cols) ||
+                    (m->batch > 1 && m->batch_stride < (m->rows - 1) * m->row_stride + m->cols)))
+        return ADAMW_ERR_INVALID_ARG;
+    return aligned(m->data, uintptr_t(dtype_size(m->dtype))) ? ADAMW_OK : ADAMW_ERR_MISALIGNED;
+}
+
+Batch batch_of(const adamw_matrices_t& m) {
+    const int size = dtype_size(m.dtype);
+    return {static_cast<char*>(m.data), m.batch_stride, m.row_stride, m.dtype,
+            aligned(m.data, 16) && (m.rows <= 1 || m.row_stride * size % 16 == 0) && (m.batch <= 1 || m.batch_stride * size % 16 == 0)};
+}
+
+// Pieces of the shapes of a launch, from the list's sum number `sum` on.
+template <bool MUON>
+int64_t fill_copies(const Group& g, const int32_t* first_sum, CopyParams<MUON>* p) {
+    int64_t pieces = 0;
+    p->n = g.n;
+    for (int i = 0; i < g.n; ++i) {
+        CopyShape& c = p->shapes[i];
+        c.s = g.shapes[i];
+        c.hi = g.buffers[i].x[0];
+        c.lo = g.buffers[i].lo;
+        c.pieces = int32_t(pieces_of(c.s));
+        c.first_piece = int32_t(pieces);
+        c.first_sum = first_sum[i];
+        pieces += int64_t(c.pieces) * c.s.count;
+    }
+    return pieces;
+}
+
+}  // namespace
+
+namespace adamw {
+int ortho_status(int32_t* out) {
+    int32_t v = 0;
+    const int32_t zero = 0;
+    if (!launched(cudaMemcpyFromSymbol(&v, g_tile_status, 4), "cudaMemcpyFromSymbol") ||
+        !launched(cudaMemcpyToSymbol(g_tile_status, &zero, 4), "cudaMemcpyToSymbol"))
+        return ADAMW_ERR_CUDA;
+    *out |= v;
+    return ADAMW_OK;
+}
+int expert_status(int32_t* out);
+}  // namespace adamw
+
+extern "C" int adamw_matrix_status(int32_t* out) {
+    if (!out) return ADAMW_ERR_INVALID_ARG;
+    *out = 0;
+    if (!launched(cudaDeviceSynchronize(), "cudaDeviceSynchronize")) return ADAMW_ERR_CUDA;
+    const int rc = adamw::ortho_status(out);
+    return rc != ADAMW_OK ? rc : adamw::expert_status(out);
+}
+
+extern "C" int64_t adamw_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols) {
+    if (!sizes_fit(batch, rows, cols) || batch * rows * cols == 0) return 0;
+    Shape s = shape_of(rows, cols);
+    s.count = int32_t(batch);
+    return up(pieces_of(s) * batch * int64_t(sizeof(double)), 256) + place(s, nullptr, nullptr);
+}
+
+extern "C" int adamw_orthogonalize(const adamw_matrices_t* src, const adamw_matrices_t* dst, const adamw_ortho_t* ortho,
+                                   void* workspace, adamw_stream_t stream) {
+    int rc;
+    if ((rc = check_ortho(ortho)) != ADAMW_OK || (rc = check_matrices(src, false)) != ADAMW_OK ||
+        (rc = check_matrices(dst, true)) != ADAMW_OK)
+        return rc;
+    if (src->batch != dst->batch || src->rows != dst->rows || src->cols != dst->cols) return ADAMW_ERR_INVALID_ARG;
+    if (src->batch * src->rows * src->cols == 0) return ADAMW_OK;
+    if (!workspace) return ADAMW_ERR_INVALID_ARG;
+    if (!aligned(workspace, 256)) return ADAMW_ERR_MISALIGNED;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    Device d;
+    if (!device_units(&d)) return ADAMW_ERR_CUDA;
+    Group g;
+    g.n = 1;
+    Shape& s = g.shapes[0];
+    s = shape_of(src->rows, src->cols);
+    s.count = int32_t(src->batch);
+    const int64_t pieces = pieces_of(s) * s.count;
+    if (pieces > kMaxCount) return ADAMW_ERR_TOO_LARGE;
+    place(s, static_cast<char*>(workspace) + up(pieces * int64_t(sizeof(double)), 256), &g.buffers[0]);
+    CopyParams<false> c;
+    memset(&c, 0, sizeof c);
+    const int32_t first_sum = 0;
+    fill_copies(g, &first_sum, &c);
+    c.sums = static_cast<double*>(workspace);
+    c.eps = ortho->eps;
+    c.src = batch_of(*src);
+    if (!launched(launch(norm_kernel<false>, uint32_t(pieces), kNormThreads, 1, 0, st, c), "norm launch") ||
+        !launched(launch(copy_kernel<false>, uint32_t(pieces), kNormThreads, 1, 0, st, c), "copy launch"))
+        return ADAMW_ERR_CUDA;
+    ProductParams with;
+    memset(&with, 0, sizeof with);
+    with.dst = batch_of(*dst);
+    return run_steps(g, *ortho, ortho->coefficients, kResult, with, d, st) ? ADAMW_OK : ADAMW_ERR_CUDA;
+}
+
+// -------------------------------------------------------------- Muon plan --
+
+struct adamw_muon_plan {
+    int device = 0;
+    adamw_ortho_t ortho = {};
+    std::vector<float> coefs;
+    int32_t nesterov = 0, momentum_bf16 = 0;
+    std::vector<Group> rounds;                 // one after the other, in the same workspace
+    std::vector<std::vector<int32_t>> sums;    // each shape's first sum, by round
+    void* block = nullptr;                     // table, sums, workspace
+    MuonMatrix* table = nullptr;
+    double* d_sums = nullptr;
+    char* work = nullptr;
+};
+
+namespace {
+
+// Workspace of a round: large enough that a round's products fill the GPU many
+// times over, small enough beside a model.
+constexpr int64_t kRoundBytes = int64_t(2) << 30;
+
+// Makes a device current for the scope, restoring the caller's.
+struct Current {
+    int prev = -1;
+    bool ok = true;
+    explicit Current(int device) {
+        if (cudaGetDevice(&prev) != cudaSuccess) { ok = false; return; }
+        if (prev != device) ok = cudaSetDevice(device) == cudaSuccess; else prev = -1;
+    }
+    ~Current() {
+        if (prev >= 0) cudaSetDevice(prev);
+    }
+};
+
+int check_muon(const adamw_muon_tensor_t* table, int32_t n, const adamw_muon_options_t* o) {
+    if (n < 0 || (n > 0 && !table) || !o) return ADAMW_ERR_INVALID_ARG;
+    const int rc = check_ortho(&o->ortho);
+    if (rc != ADAMW_OK) return rc;
+    if ((o->nesterov != 0 && o->nesterov != 1) || (o->scale != ADAMW_MUON_SPECTRAL && o->scale != ADAMW_MUON_RMS) ||
+        (o->momentum_dtype != ADAMW_DTYPE_FP32 && o->momentum_dtype != ADAMW_DTYPE_BF16))
+        return ADAMW_ERR_INVALID_ARG;
+    int64_t matrices = 0;
+    for (int32_t k = 0; k < n; ++k) {
+        const adamw_muon_tensor_t& t = table[k];
+        if (t.batch < 0 || t.rows < 0 || t.cols < 0) return ADAMW_ERR_INVALID_ARG;
+        if (!sizes_fit(t.batch, t.rows, t.cols)) return ADAMW_ERR_TOO_LARGE;
+        if (t.batch * t.rows * t.cols == 0) continue;
+        if (!t.param || !t.grad || !t.momentum || !t.master) return ADAMW_ERR_INVALID_ARG;
+        if (!aligned(t.param, 2) || !aligned(t.grad, 2) || !aligned(t.master, 4) ||
+            !aligned(t.momentum, o->momentum_dtype == ADAMW_DTYPE_FP32 ? 4 : 2))
+            return ADAMW_ERR_MISALIGNED;
+        matrices += t.batch;
+        if (matrices > kMaxMatrices) return ADAMW_ERR_TOO_LARGE;
+    }
+    return ADAMW_OK;
+}
+
+// No buffer of the list reaches into another: two CTAs would write one place,
+// or read what is being written.
+int check_apart(const adamw_muon_tensor_t* table, int32_t n, int momentum_size) {
+    std::vector<std::pair<uintptr_t, uintptr_t>> spans;
+    for (int32_t k = 0; k < n; ++k) {
+        const adamw_muon_tensor_t& t = table[k];
+        const int64_t numel = t.batch * t.rows * t.cols;
+        if (numel == 0) continue;
+        const void* at[] = {t.param, t.grad, t.momentum, t.master};
+        const int size[] = {2, 2, momentum_size, 4};
+        for (int b = 0; b < 4; ++b) {
+            const uintptr_t p = reinterpret_cast<uintptr_t>(at[b]);
+            spans.emplace_back(p, p + uintptr_t(numel) * uintptr_t(size[b]));
+        }
+    }
+    std::sort(spans.begin(), spans.end());
+    for (size_t k = 1; k < spans.size(); ++k)
+        if (spans[k].first < spans[k - 1].second) return ADAMW_ERR_INVALID_ARG;
+    return ADAMW_OK;
+}
+
+int check_device(const void* p, int device, int pageable) {
+    cudaPointerAttributes a{};
+    if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+        adamw::set_cuda_error("cudaPointerGetAttributes", cudaGetErrorString(cudaGetLastError()));
+        return ADAMW_ERR_NOT_ACCESSIBLE;
+    }
+    const bool ok = a.type == cudaMemoryTypeDevice ? a.device == device
+                    : a.type == cudaMemoryTypeManaged ? true
+                    : a.type == cudaMemoryTypeHost    ? a.devicePointer == p
+                                                      : pageable != 0;
+    return ok ? ADAMW_OK : ADAMW_ERR_NOT_ACCESSIBLE;
+}
+
+float rate_of(int32_t scale, int64_t rows, int64_t cols) {
+    const double r = double(rows), c = double(cols);
+    return float(scale == ADAMW_MUON_RMS ? 0.2 * std::sqrt(std::max(r, c)) : std::sqrt(std::max(1.0, r / c)));
+}
+
+int create(const adamw_muon_tensor_t* table, int32_t n, const adamw_muon_options_t* o, adamw_muon_plan* P) {
+    if (!launched(cudaGetDevice(&P->device), "cudaGetDevice")) return ADAMW_ERR_CUDA;
+    int pageable = 0;
+    if (!launched(cudaDeviceGetAttribute(&pageable, cudaDevAttrPageableMemoryAccess, P->device), "cudaDeviceGetAttribute"))
+        return ADAMW_ERR_CUDA;
+    Device d;
+    if (!device_units(&d)) return ADAMW_ERR_CUDA;
+    P->ortho = o->ortho;
+    P->coefs.assign(o->ortho.coefficients, o->ortho.coefficients + 3 * o->ortho.n_coefficients);
+    P->ortho.coefficients = nullptr;
+    P->nesterov = o->nesterov;
+    P->momentum_bf16 = o->momentum_dtype == ADAMW_DTYPE_BF16;
+    const int size = P->momentum_bf16 ? 2 : 4;
+    // the list's matrices, those of one shape together
+    struct Entry {
+        int64_t rows, cols;
+        int32_t tensor;
+    };
+    std::vector<Entry> order;
+    for (int32_t k = 0; k < n; ++k) {
+        const adamw_muon_tensor_t& t = table[k];
+        if (t.batch * t.rows * t.cols == 0) continue;
+        for (const void* p : {static_cast<const void*>(t.param), t.grad, static_cast<const void*>(t.momentum),
+                              static_cast<const void*>(t.master)}) {
+            const int rc = check_device(p, P->device, pageable);
+            if (rc != ADAMW_OK) return rc;
+        }
+        order.push_back({t.rows, t.cols, k});
+    }
+    std::stable_sort(order.begin(), order.end(), [](const Entry& a, const Entry& b) {
+        return a.rows * a.cols != b.rows * b.cols ? a.rows * a.cols > b.rows * b.cols : a.rows > b.rows;
+    });
+    std::vector<MuonMatrix> matrices;
+    std::vector<Shape> shapes;
+    for (const Entry& e : order) {
+        const adamw_muon_tensor_t& t = table[e.tensor];
+        if (shapes.empty() || shapes.back().rows != t.rows || shapes.back().cols != t.cols) {
+            shapes.push_back(shape_of(t.rows, t.cols));
+            shapes.back().first = int32_t(matrices.size());
+        }
+        for (int64_t b = 0; b < t.batch; ++b) {
+            const int64_t at = b * t.rows * t.cols;
+            matrices.push_back({static_cast<uint16_t*>(t.param) + at, static_cast<const uint16_t*>(t.grad) + at,
+                                static_cast<char*>(t.momentum) + at * size, t.master + at});
+            ++shapes.back().count;
+        }
+    }
+    // rounds: as many matrices as the workspace holds, of at most kMaxShapes shapes
+    int64_t sums = 0, work = 0, used = 0;
+    for (const Shape& s : shapes) {
+        for (int32_t done = 0; done < s.count;) {
+            Shape part = s;
+            part.first = s.first + done;
+            part.count = 1;
+            const int64_t one = place(part, nullptr, nullptr);
+            if (P->rounds.empty() || P->rounds.back().n == kMaxShapes || (used > 0 && used + one > kRoundBytes)) {
+                P->rounds.emplace_back();
+                P->sums.emplace_back();
+                used = 0;
+            }
+            const int64_t room = (kRoundBytes - used) / one;
+            part.count = int32_t(std::min<int64_t>(s.count - done, std::max<int64_t>(room, 1)));
+            Group& g = P->rounds.back();
+            g.shapes[g.n] = part;
+            g.rate[g.n] = rate_of(o->scale, part.rows, part.cols);
+            ++g.n;
+            P->sums.back().push_back(int32_t(sums));
+            sums += pieces_of(part) * part.count;
+            if (sums > kMaxCount) return ADAMW_ERR_TOO_LARGE;
+            used += place(part, nullptr, nullptr);
+            work = std::max(work, used);
+            done += part.count;
+        }
+    }
+    if (matrices.empty()) return ADAMW_OK;
+    const int64_t table_bytes = up(int64_t(matrices.size() * sizeof(MuonMatrix)), 256), sum_bytes = up(sums * int64_t(sizeof(double)), 256);
+    if (!launched(cudaMalloc(&P->block, size_t(table_bytes + sum_bytes + work)), "cudaMalloc")) return ADAMW_ERR_CUDA;
+    P->table = static_cast<MuonMatrix*>(P->block);
+    P->d_sums = reinterpret_cast<double*>(static_cast<char*>(P->block) + table_bytes);
+    P->work = static_cast<char*>(P->block) + table_bytes + sum_bytes;
+    for (Group& g : P->rounds) {
+        char* at = P->work;
+        for (int i = 0; i < g.n; ++i) at += place(g.shapes[i], at, &g.buffers[i]);
+    }
+    const bool ok = launched(cudaMemcpy(P->table, matrices.data(), matrices.size() * sizeof(MuonMatrix), cudaMemcpyHostToDevice),
+                             "cudaMemcpy(table)") &&
+                    launched(cudaStreamSynchronize(nullptr), "cudaStreamSynchronize");
+    return ok ? ADAMW_OK : ADAMW_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" int adamw_muon_plan_create(const adamw_muon_tensor_t* host_table, int32_t n, const adamw_muon_options_t* options,
+                                      adamw_muon_plan_t* out) {
+    if (!out) return ADAMW_ERR_INVALID_ARG;
+    *out = nullptr;
+    int rc = check_muon(host_table, n, options);
+    if (rc != ADAMW_OK) return rc;
+    adamw_muon_plan* P = new (std::nothrow) adamw_muon_plan;
+    if (!P) return ADAMW_ERR_TOO_LARGE;
+    try {
+        rc = check_apart(host_table, n, options->momentum_dtype == ADAMW_DTYPE_FP32 ? 4 : 2);
+        if (rc == ADAMW_OK) rc = create(host_table, n, options, P);
+    } catch (const std::exception&) {   // the host has no room for a table
+        rc = ADAMW_ERR_TOO_LARGE;
+    }
+    if (rc != ADAMW_OK) {
+        if (P->block) cudaFree(P->block);
+        delete P;
+        return rc;
+    }
+    *out = P;
+    return ADAMW_OK;
+}
+
+extern "C" int adamw_muon_step(adamw_muon_plan_t plan, const adamw_muon_hparams_t* hparams, int32_t* nonfinite,
+                               adamw_stream_t stream) {
+    if (!plan || !hparams || !nonfinite) return ADAMW_ERR_INVALID_ARG;
+    if (!aligned(hparams, 16) || !aligned(nonfinite, 4)) return ADAMW_ERR_MISALIGNED;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    Current guard(plan->device);
+    if (!guard.ok) {
+        adamw::set_cuda_error("cudaSetDevice", cudaGetErrorString(cudaGetLastError()));
+        return ADAMW_ERR_CUDA;
+    }
+    Device d;
+    if (!device_units(&d)) return ADAMW_ERR_CUDA;
+    if (!launched(cudaMemsetAsync(nonfinite, 0, sizeof(int32_t), st), "cudaMemsetAsync")) return ADAMW_ERR_CUDA;
+    CopyParams<true> c;
+    memset(&c, 0, sizeof c);
+    c.sums = plan->d_sums;
+    c.eps = plan->ortho.eps;
+    c.table = plan->table;
+    c.hp = hparams;
+    c.nonfinite = nonfinite;
+    c.nesterov = plan->nesterov;
+    c.momentum_bf16 = plan->momentum_bf16;
+    // every norm first: one gradient that is not finite stops the whole step
+    for (size_t r = 0; r < plan->rounds.size(); ++r) {
+        const int64_t pieces = fill_copies(plan->rounds[r], plan->sums[r].data(), &c);
+        if (!launched(launch(norm_kernel<true>, uint32_t(pieces), kNormThreads, 1, 0, st, c), "norm launch")) return ADAMW_ERR_CUDA;
+    }
+    ProductParams with;
+    memset(&with, 0, sizeof with);
+    with.table = plan->table;
+    with.hp = hparams;
+    with.nonfinite = nonfinite;
+    for (size_t r = 0; r < plan->rounds.size(); ++r) {
+        const int64_t pieces = fill_copies(plan->rounds[r], plan->sums[r].data(), &c);
+        if (!launched(launch(copy_kernel<true>, uint32_t(pieces), kNormThreads, 1, 0, st, c), "copy launch")) return ADAMW_ERR_CUDA;
+        if (!run_steps(plan->rounds[r], plan->ortho, plan->coefs.data(), kUpdate, with, d, st)) return ADAMW_ERR_CUDA;
+    }
+    return ADAMW_OK;
+}
+
+extern "C" int adamw_muon_plan_destroy(adamw_muon_plan_t plan) {
+    if (!plan) return ADAMW_OK;
+    Current guard(plan->device);
+    bool ok = guard.ok;
+    if (plan->block) {
+        ok = ok && launched(cudaDeviceSynchronize(), "cudaDeviceSynchronize");
+        ok = launched(cudaFree(plan->block), "cudaFree") && ok;
+    }
+    delete plan;
+    return ok ? ADAMW_OK : ADAMW_ERR_CUDA;
+}

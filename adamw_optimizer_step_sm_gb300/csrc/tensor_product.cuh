@@ -1,0 +1,541 @@
+// tensor_product.cuh -- the main loop of the matrix operators: products of
+// 16-bit tiles on the tensor cores with fp32 accumulators, as a persistent
+// kernel over a list of tiles that a policy describes.
+//
+//     D[i][j] = sum_k A(i, k) B(j, k)
+//
+// Each operand lies in memory either with consecutive k ("K-major": rows of
+// k) or with consecutive i or j ("MN-major"), which the tensor cores read
+// alike, so that no operand is ever transposed.
+//
+// A unit (one CTA, or a pair on two neighbouring SMs) computes a tile of
+// kRows x kCols in steps of 64 k.  Roles, a warp each: TMA loads into a ring
+// of stages; one thread issues tcgen05.mma into one of two accumulators in
+// tensor memory; four warps read the other one out and hand it to the policy
+// in vectors of eight columns; and where k ends inside a step at an element
+// that the next group owns (the ragged sums over tokens), one warp zeroes the
+// rest of the step in shared memory.
+//
+// Bounds: a 256 x 256 x 64 step of a pair takes its SMs 256 cycles and 64 KB of
+// loads.  The pair shares each operand's loads (128 rows of A and 128 of B by
+// each SM), which halves the shared-memory traffic of B against two single
+// tiles; the single form is for products with too few tiles to fill the GPU.
+//
+// No wait is endless: after about two seconds it gives up, sets the device's
+// status word, and every role leaves.
+#pragma once
+
+#include <cuda.h>
+
+#include "losses_common.cuh"
+
+namespace {
+
+constexpr int kTileThreads = 256;
+constexpr int kStepK = 64;                  // elements of k in a stage: 128 bytes, one swizzle row
+constexpr int kRowsOfCta = 128;             // accumulator rows of a CTA: the lanes of tensor memory
+constexpr uint32_t kStageRoom = 196608;     // bytes of the ring
+constexpr uint32_t kStagingRoom = 16384;    // four epilogue warps x 32 x 32 fp32
+constexpr uint32_t kControlRoom = 1024;
+constexpr long long kGiveUp = 4000000000ll; // cycles
+
+// ------------------------------------------------------------------ PTX ---
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return uint32_t(__cvta_generic_to_shared(p)); }
+
+// The address of the same shared variable in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ uint32_t cta_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void sync_cluster() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void barrier_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ bool barrier_test(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+    return done != 0;
+}
+// `bar` is a cluster address: this CTA's own or another's.
+__device__ __forceinline__ void barrier_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void barrier_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+
+// A box of a three-dimensional tensor into this CTA's shared memory; its bytes
+// count at `bar`, which may be the other CTA's of the pair.
+template <int PAIR>
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    if (PAIR == 2)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3, %4}], [%5];"
+            ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3, %4}], [%5];"
+            ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+
+template <int PAIR>
+__device__ __forceinline__ void tmem_alloc(uint32_t where, uint32_t columns) {
+    if (PAIR == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(where), "r"(columns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(where), "r"(columns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+}
+template <int PAIR>
+__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t columns) {
+    if (PAIR == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
+}
+template <int PAIR>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add) {
+    if (PAIR == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(kind), "r"(uint32_t(add)) : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(kind), "r"(uint32_t(add)) : "memory");
+}
+// Arrives at `bar` (in both CTAs of a pair) once this thread's products so far
+// have been done.
+template <int PAIR>
+__device__ __forceinline__ void commit(uint32_t bar) {
+    if (PAIR == 2)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+            ::"r"(bar), "h"(uint16_t(3)) : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+
+// 32 columns of this warp's 32 lanes: v[c] is column c of the thread's lane.
+__device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(at) : "memory");
+}
+
+// ------------------------------------------------- operands in shared memory
+
+// A stage's operand of R rows (of i or j) and 64 k.  K-major: R rows of 128
+// bytes, one box.  MN-major: R / 64 boxes of 64 k-rows of 128 bytes.  128-byte
+// swizzle in both (16-byte units of a row XORed with the row's number modulo
+// 8), which TMA writes and the tensor cores read.  The descriptor: address,
+// distance of the 64-wide boxes (MN-major only), distance of groups of eight
+// 128-byte rows, version 1, swizzle mode 2 (128 bytes).
+__device__ __forceinline__ uint64_t operand(uint32_t addr, bool mn) {
+    const uint64_t lead = mn ? (64 * 128) >> 4 : 1;
+    return uint64_t((addr & 0x3ffff) >> 4) | lead << 16 | uint64_t(1024 >> 4) << 32 | uint64_t(1) << 46 | uint64_t(2) << 61;
+}
+// What 16 further k add to the descriptor: 32 bytes of each row, or 16 rows.
+__device__ __forceinline__ uint64_t operand_step(bool mn) { return mn ? (16 * 128) >> 4 : 32 >> 4; }
+
+// The instruction descriptor: fp32 accumulators, both operands of the type
+// (0: fp16, 1: bf16), their layouts, the tile's shape.
+__host__ __device__ constexpr uint32_t mma_kind(int bf16, bool a_mn, bool b_mn, int rows, int cols) {
+    return 1u << 4 | uint32_t(bf16) << 7 | uint32_t(bf16) << 10 | uint32_t(a_mn) << 15 | uint32_t(b_mn) << 16 |
+           uint32_t(cols / 8) << 17 | uint32_t(rows / 16) << 24;
+}
+
+// ------------------------------------------------------------- the kernel --
+
+// What a tile needs of its policy.
+struct TileLoads {
+    const CUtensorMap *a, *b;
+    int32_t a_at, b_at;   // first row (of i, of j) of the unit's tile
+    int32_t a_z, b_z;     // third coordinate
+    int32_t k_at, k_len;  // range of k; k_len 0: the tile is zeros
+    bool a_mn, b_mn;      // layouts
+};
+
+struct Control {
+    uint64_t full[16], empty[16], tail[16];
+    uint64_t acc_full[2], acc_empty[2];
+    uint32_t tmem;
+    int32_t failed;
+};
+static_assert(sizeof(Control) <= kControlRoom, "control block");
+
+// One word a device, OR-ed by kernels whose waits ran out.
+__device__ int32_t g_tile_status;
+
+struct Waiter {
+    Control* c;
+    // the same answer for all of a warp
+    __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity) const {
+        return __all_sync(0xffffffffu, (*this)(bar, parity));
+    }
+    // false: given up (here or elsewhere in the CTA)
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+        if (barrier_test(bar, parity)) return true;
+        const long long start = clock64();
+        for (;;) {
+#pragma unroll 1
+            for (int k = 0; k < 64; ++k)
+                if (barrier_test(bar, parity)) return true;
+            if (*static_cast<volatile int32_t*>(&c->failed)) return false;
+            if (clock64() - start > kGiveUp) {
+                *static_cast<volatile int32_t*>(&c->failed) = 1;
+                atomicOr(&g_tile_status, 1);
+                return false;
+            }
+        }
+    }
+};
+
+template <int PAIR_, int COLS_>
+struct TileShape {
+    static constexpr int kPair = PAIR_, kCols = COLS_, kRows = kRowsOfCta * PAIR_;
+    static constexpr int kBRows = kCols / kPair;   // rows of B that each CTA loads
+    static constexpr uint32_t kABytes = kRowsOfCta * 128, kBBytes = kBRows * 128;
+    static constexpr uint32_t kStageBytes = kABytes + kBBytes;
+    static constexpr int kStages = int(kStageRoom / kStageBytes);
+    static constexpr uint32_t kColumns = 2 * kCols;   // of tensor memory
+    static_assert(kStages <= 16 && kColumns <= 512 && (kColumns & (kColumns - 1)) == 0, "tile shape");
+};
+using PairTile = TileShape<2, 256>;
+using SingleTile = TileShape<1, 128>;
+
+constexpr size_t tile_smem(size_t table) { return 1024 + kStageRoom + kStagingRoom + kControlRoom + table; }
+
+// A policy P over a tile shape S:
+//   P::Params       kernel arguments;  P::kTail: k may end inside a step
+//   P::kTable       bytes of shared memory for its tables
+//   prepare(p, table)                    all threads, before the first tile
+//   tiles(p, table)                      number of tiles
+//   loads(p, table, tile, TileLoads&)    operands
+//   bf16(p)                              type of the operands
+//   Out: what the epilogue keeps of a tile; out<S>(p, table, tile, rank)
+//   wanted(p, out, row, col): whether the 32 x 32 block there has anything to store
+//   Extra, fetch(p, out, row, col, Extra&): what store will want of memory
+//   store(p, out, row, col, extra, float (&v)[8]): eight columns from `col` of
+//        row `row` of the CTA's 128 x kCols part; leaves in v what the
+//        mirrored tile holds
+//   mirrored(out), mirror(p, out, col, row, v): eight rows from `row` of column
+//        `col`, for the transposed tile.
+template <class P, class S>
+__global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_constant__ typename P::Params p) {
+    constexpr int PAIR = S::kPair;
+    extern __shared__ unsigned char raw[];
+    // 1024-byte boundary: the swizzle goes by address bits; the same in both CTAs
+    unsigned char* base = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
+    unsigned char* ring = base;
+    float* staging = reinterpret_cast<float*>(base + kStageRoom);
+    Control* ctl = reinterpret_cast<Control*>(base + kStageRoom + kStagingRoom);
+    unsigned char* table = base + kStageRoom + kStagingRoom + kControlRoom;
+
+    const int warp = int(threadIdx.x) / 32, lane = int(threadIdx.x) % 32;
+    const uint32_t rank = PAIR == 2 ? cta_rank() : 0;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S::kStages; ++s) {
+            barrier_init(smem_addr(&ctl->full[s]), PAIR);
+            barrier_init(smem_addr(&ctl->empty[s]), 1);
+            barrier_init(smem_addr(&ctl->tail[s]), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            barrier_init(smem_addr(&ctl->acc_full[a]), 1);
+            barrier_init(smem_addr(&ctl->acc_empty[a]), 4 * PAIR);
+        }
+        ctl->failed = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 2) tmem_alloc<PAIR>(smem_addr(&ctl->tmem), S::kColumns);
+    tmem_before();
+    if (PAIR == 2) sync_cluster();
+    __syncthreads();
+    tmem_after();
+    const uint32_t tmem = *static_cast<volatile uint32_t*>(&ctl->tmem);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    P::prepare(p, table);
+    __syncthreads();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    const int first = int(blockIdx.x) / PAIR, units = int(gridDim.x) / PAIR;
+    const int tiles = P::tiles(p, table);
+    const Waiter wait = {ctl};
+
+    if (warp == 0 && lane == 0) {
+        // ---- loads
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = first; t < tiles && ok; t += units) {
+            TileLoads w;
+            P::loads(p, table, t, w);
+            const bool a_mn = w.a_mn, b_mn = w.b_mn;
+            const int a_at = w.a_at + int(rank) * kRowsOfCta, b_at = w.b_at + int(rank) * S::kBRows;
+            for (int k = 0; k < w.k_len; k += kStepK, ++it) {
+                const uint32_t s = it % S::kStages;
+                if (!(ok = wait(smem_addr(&ctl->empty[s]), (it / S::kStages & 1) ^ 1))) break;
+                const bool tail = P::kTail && k + kStepK > w.k_len;
+                const uint32_t own = smem_addr(tail ? &ctl->tail[s] : &ctl->full[s]);
+                const uint32_t bar = PAIR == 2 && !tail ? in_cta(own, 0) : own;
+                barrier_expect(PAIR == 2 && tail ? in_cta(own, rank) : bar, S::kStageBytes);
+                const uint32_t a = smem_addr(ring) + s * S::kStageBytes, b = a + S::kABytes;
+                const int at = w.k_at + k;
+                if (a_mn) {
+#pragma unroll
+                    for (int i = 0; i < kRowsOfCta / 64; ++i)
+                        load_box<PAIR>(a + i * 8192, w.a, a_at + i * 64, at, w.a_z, bar);
+                } else {
+                    load_box<PAIR>(a, w.a, at, a_at, w.a_z, bar);
+                }
+                if (b_mn) {
+#pragma unroll
+                    for (int i = 0; i < S::kBRows / 64; ++i)
+                        load_box<PAIR>(b + i * 8192, w.b, b_at + i * 64, at, w.b_z, bar);
+                } else {
+                    load_box<PAIR>(b, w.b, at, b_at, w.b_z, bar);
+                }
+            }
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // ---- products
+        uint32_t it = 0, n = 0;
+        bool ok = true;
+        for (int t = first; t < tiles && ok; t += units) {
+            TileLoads w;
+            P::loads(p, table, t, w);
+            if (w.k_len == 0) continue;
+            const bool a_mn = w.a_mn, b_mn = w.b_mn;
+            const uint32_t kind = mma_kind(P::bf16(p), a_mn, b_mn, S::kRows, S::kCols);
+            const uint32_t acc = n & 1;
+            if (!(ok = wait(smem_addr(&ctl->acc_empty[acc]), (n >> 1 & 1) ^ 1))) break;
+            tmem_after();
+            for (int k = 0; k < w.k_len; k += kStepK, ++it) {
+                const uint32_t s = it % S::kStages;
+                if (!(ok = wait(smem_addr(&ctl->full[s]), it / S::kStages & 1))) break;
+                tmem_after();
+                const uint32_t at = smem_addr(ring) + s * S::kStageBytes;
+                const uint64_t a = operand(at, a_mn), b = operand(at + S::kABytes, b_mn);
+                const uint64_t da = operand_step(a_mn), db = operand_step(b_mn);
+                // the last step: only as many 16s of k as it has
+                const int parts = w.k_len - k >= kStepK ? kStepK / 16 : (w.k_len - k + 15) / 16;
+                for (int i = 0; i < parts; ++i)
+                    mma<PAIR>(tmem + acc * S::kCols, a + i * da, b + i * db, kind, k + i > 0);
+                commit<PAIR>(smem_addr(&ctl->empty[s]));
+            }
+            if (ok) commit<PAIR>(smem_addr(&ctl->acc_full[acc]));
+            ++n;
+        }
+    } else if (P::kTail && warp == 2) {
+        // ---- the last step of a tile whose k ends inside it: rows of k
+        // beyond the end (another group's, or anything) become zeros in both
+        // operands, as 0 x NaN would reach the sum.  MN-major operands only.
+        uint32_t it = 0, turns = 0;   // turns: parity of each stage's next tail
+        bool ok = true;
+        for (int t = first; t < tiles && ok; t += units) {
+            TileLoads w;
+            P::loads(p, table, t, w);
+            const int steps = (w.k_len + kStepK - 1) / kStepK, rest = w.k_len % kStepK;
+            it += uint32_t(steps);
+            if (rest == 0) continue;
+            const uint32_t s = (it - 1) % S::kStages;
+            if (!(ok = wait.warp(smem_addr(&ctl->tail[s]), turns >> s & 1))) break;
+            turns ^= 1u << s;
+            const int end = (rest + 15) / 16 * 16;   // what the products read
+            unsigned char* at = ring + s * S::kStageBytes;
+            const int boxes = int(S::kStageBytes / 8192), units16 = (end - rest) * 8;
+            for (int i = lane; i < boxes * units16; i += 32)
+                *reinterpret_cast<uint4*>(at + i / units16 * 8192 + rest * 128 + i % units16 * 16) = make_uint4(0, 0, 0, 0);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) barrier_arrive(in_cta(smem_addr(&ctl->full[s]), 0));
+        }
+    } else if (warp >= 4) {
+        // ---- results
+        float* mine = staging + (warp - 4) * 1024;
+        uint32_t n = 0;
+        bool ok = true;
+        // element (row, col) of the 32 x 32 block, its 16-byte units swizzled
+        auto place = [&](int row, int col) { return mine + row * 32 + (((col >> 2) ^ (row & 7)) << 2) + (col & 3); };
+        for (int t = first; t < tiles && ok; t += units) {
+            TileLoads w;
+            P::loads(p, table, t, w);
+            const typename P::Out out = P::template out<S>(p, table, t, rank);
+            const uint32_t acc = n & 1;
+            const int row0 = (warp - 4) * 32;
+            // what the epilogue reads of memory is fetched a block ahead
+            typename P::Extra next[4];
+            if (P::wanted(p, out, row0, 0)) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) P::fetch(p, out, row0 + i * 8 + lane / 4, lane % 4 * 8, next[i]);
+            }
+            if (w.k_len > 0) {
+                if (!(ok = wait.warp(smem_addr(&ctl->acc_full[acc]), n >> 1 & 1))) break;
+                tmem_after();
+            }
+            for (int c = 0; c < S::kCols; c += 32) {
+                if (!P::wanted(p, out, row0, c)) continue;
+                typename P::Extra now[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) now[i] = next[i];
+                if (c + 32 < S::kCols && P::wanted(p, out, row0, c + 32)) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) P::fetch(p, out, row0 + i * 8 + lane / 4, c + 32 + lane % 4 * 8, next[i]);
+                }
+                uint32_t v[32];
+                if (w.k_len > 0) {
+                    tmem_load(tmem + (uint32_t(row0) << 16) + acc * S::kCols + uint32_t(c), v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0;
+                }
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    *reinterpret_cast<uint4*>(place(lane, i)) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                __syncwarp();
+                const bool mirrored = P::mirrored(out);
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    const int r = i + lane / 4, q = lane % 4 * 8;
+                    float x[8];
+                    *reinterpret_cast<float4*>(x) = *reinterpret_cast<float4*>(place(r, q));
+                    *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<float4*>(place(r, q + 4));
+                    P::store(p, out, row0 + r, c + q, now[i / 8], x);
+                    if (mirrored) {
+                        *reinterpret_cast<float4*>(place(r, q)) = *reinterpret_cast<float4*>(x);
+                        *reinterpret_cast<float4*>(place(r, q + 4)) = *reinterpret_cast<float4*>(x + 4);
+                    }
+                }
+                __syncwarp();
+                if (mirrored) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        const int j = i + lane / 4, q = lane % 4 * 8;
+                        float x[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = *place(q + e, j);
+                        P::mirror(p, out, c + j, row0 + q, x);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (w.k_len > 0) {
+                tmem_before();
+                __syncwarp();
+                if (lane == 0) barrier_arrive(in_cta(smem_addr(&ctl->acc_empty[acc]), 0));
+                ++n;
+            }
+        }
+    }
+    __syncwarp();
+    __syncthreads();
+    if (*static_cast<volatile int32_t*>(&ctl->failed)) {
+        // copies and products in flight land within microseconds: a
+        // millisecond for them before the memory is given back
+        for (int k = 0; k < 1000; ++k) __nanosleep(1000);
+    }
+    tmem_before();
+    if (PAIR == 2) sync_cluster();   // the other CTA's arrivals, and its reads of this one's memory
+    __syncthreads();
+    tmem_after();
+    if (warp == 2) tmem_free<PAIR>(tmem, S::kColumns);
+}
+
+// -------------------------------------------------------------------- host --
+
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+
+inline EncodeTiled encode_tiled() {
+    static EncodeTiled f = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult how = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &how) != cudaSuccess ||
+            how != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return f;
+}
+
+// The map of a batch of matrices [batch][rows][cols] of 16-bit elements, rows
+// `ld` and matrices `stride` elements apart, for boxes of 64 columns and
+// `box_rows` rows.  Base 16-byte aligned; ld and stride multiples of 8.
+inline bool tensor_map(CUtensorMap* map, bool bf16, const void* data, int64_t batch, int64_t rows, int64_t cols,
+                       int64_t ld, int64_t stride, int box_rows) {
+    const EncodeTiled f = encode_tiled();
+    if (!f) {
+        adamw::set_cuda_error("cuTensorMapEncodeTiled", "not found in the driver");
+        return false;
+    }
+    const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(batch)};
+    const cuuint64_t strides[2] = {cuuint64_t(ld) * 2, cuuint64_t(stride > 0 ? stride : ld) * 2};
+    const cuuint32_t box[3] = {cuuint32_t(kStepK), cuuint32_t(box_rows), 1};
+    const cuuint32_t step[3] = {1, 1, 1};
+    const CUresult r = f(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                         const_cast<void*>(data), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) return true;
+    adamw::set_cuda_error("cuTensorMapEncodeTiled", "refused the layout");
+    return false;
+}
+
+// SMs of the current device, and how many pairs of CTAs run at a time.
+struct TileUnits {
+    int sms = 0, pairs = 0;
+};
+
+template <class P>
+cudaError_t tile_units(TileUnits* u, size_t smem) {
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&u->sms, cudaDevAttrMultiProcessorCount, device)) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(u->sms / 2 * 2));
+    cfg.blockDim = dim3(kTileThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if ((e = cudaOccupancyMaxActiveClusters(&n, tile_kernel<P, PairTile>, &cfg)) != cudaSuccess) return e;
+    u->pairs = n > 0 ? n : 1;
+    return cudaSuccess;
+}
+
+}  // namespace

@@ -1,0 +1,264 @@
+"""Matrix operators of a training step, over torch tensors.
+
+    orthogonalize           Newton-Schulz orthogonalisation of matrices
+    expert_linear           products grouped by expert, of ragged sizes
+    expert_linear_backward  the gradients of both factors
+
+Every function is one or a few calls into the library (include/adamw_matrix.h
+has the formulas) on the current stream of the tensors' device, and waits for
+nothing.  ``optim.Muon`` is the optimizer whose step orthogonalises.
+
+Experts: rows offsets[e] to offsets[e + 1] - 1 of [tokens, features] belong to
+expert e; ``offsets`` is int64 [experts + 1] on the device, as for packed
+sequences, so that no call waits for the router's counts.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import adamw_sm as A
+from .losses import _call, _tangent, _written
+
+_byref = ctypes.byref
+_empty = torch.empty
+_matrices_t = A.adamw_matrices_t
+_CODES = {torch.bfloat16: A.DTYPE_BF16, torch.float16: A.DTYPE_FP16, torch.float32: A.DTYPE_FP32}
+_HALVES = (torch.bfloat16, torch.float16)
+
+COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def _matrices(x: torch.Tensor) -> A.adamw_matrices_t:
+    """x, [rows, cols] or [batch, rows, cols] with consecutive elements in a row."""
+    s, d = x.stride(), x.shape
+    if len(d) == 2:
+        return _matrices_t(x.data_ptr(), 1, d[0], d[1], 0, s[0], _CODES[x.dtype])
+    return _matrices_t(x.data_ptr(), d[0], d[1], d[2], s[0], s[1], _CODES[x.dtype])
+
+
+def _workspace(nbytes: int, device) -> Optional[torch.Tensor]:
+    # torch's allocations start at multiples of 512 bytes
+    return _empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+# ------------------------------------------------------- orthogonalisation --
+
+_options: dict = {}
+
+
+def _ortho(steps, coefficients, eps):
+    key = (steps, coefficients if isinstance(coefficients[0], float) else tuple(map(tuple, coefficients)), eps) \
+        if isinstance(coefficients, tuple) else None
+    o = _options.get(key) if key else None
+    if o is None:
+        if not 1 <= steps <= 32:
+            raise ValueError("want 1 to 32 steps")
+        if not eps > 0:
+            raise ValueError("want eps > 0")
+        o = A.ortho_options(steps, coefficients, eps)
+        if not 1 <= o.n_coefficients <= 32:
+            raise ValueError("want coefficients (a, b, c), or up to 32 of them")
+        if key and len(_options) < 64:
+            _options[key] = o
+    return o
+
+
+def orthogonalize(x: torch.Tensor, *, steps: int = 5, coefficients=COEFFICIENTS, eps: float = 1e-7,
+                  dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The Newton-Schulz iteration of each matrix of x ([..., rows, cols], bf16,
+    fp16 or fp32): X / max(norm, eps), then ``steps`` times a X + (b G + c G G) X
+    with G = X X^T.  ``coefficients``: (a, b, c), or one such triple a step (the
+    last for the steps beyond).  The result is of ``dtype``, or written to
+    ``out`` (which may be x).  A matrix holding inf or NaN gives NaN, a zero
+    matrix zeros.  Not differentiable: it is what optimizers do to gradients."""
+    if not x.is_cuda:
+        raise TypeError("want CUDA tensors")
+    if x.dtype not in _CODES:
+        raise TypeError(f"want bfloat16, float16 or float32 matrices, not {x.dtype}")
+    if x.dim() < 2:
+        raise ValueError("want matrices [..., rows, cols]")
+    if (x.requires_grad and torch.is_grad_enabled()) or _tangent(x).tangent is not None:
+        raise RuntimeError("orthogonalize has no gradient: detach its input")
+    if out is None:
+        if dtype not in _CODES:
+            raise TypeError(f"want a result in bfloat16, float16 or float32, not {dtype}")
+        out = _empty(x.shape, dtype=dtype, device=x.device)
+        given = None
+    else:
+        if out.shape != x.shape or out.device != x.device or out.dtype not in _CODES:
+            raise ValueError("out must have x's shape and device, in bfloat16, float16 or float32")
+        if (out.requires_grad and torch.is_grad_enabled()):
+            raise RuntimeError("out requires a gradient")
+        given = out
+        if not out.is_contiguous():
+            raise ValueError("out must be contiguous")
+    src = x.detach()
+    if src.dim() != 3:
+        src = src.reshape(-1, *src.shape[-2:]) if src.dim() > 3 else src[None]
+    rows, cols = src.shape[-2:]
+    if src.numel() == 0:
+        return out
+    if src.stride(-1) != 1 and cols > 1:
+        if src.stride(-2) == 1 and given is None and rows > 1:
+            # a transposed view: the transpose's result, transposed
+            dense = src.mT
+            t = _empty(dense.shape, dtype=out.dtype, device=x.device)
+            _run_ortho(dense, t, steps, coefficients, eps)
+            return t.mT.reshape(x.shape) if x.dim() > 3 else t.mT.view(x.shape)
+        src = src.contiguous()
+    _run_ortho(src, out.view(src.shape), steps, coefficients, eps)
+    if given is not None:
+        _written(given)
+    return out
+
+
+def _run_ortho(src, dst, steps, coefficients, eps):
+    lib = A.load()
+    nbytes = lib.adamw_orthogonalize_workspace(*src.shape)
+    work = _workspace(nbytes, src.device)
+    _call(lib.adamw_orthogonalize, "adamw_orthogonalize", src.device, _byref(_matrices(src)), _byref(_matrices(dst)),
+          _byref(_ortho(steps, coefficients, eps)), _ptr(work))
+
+
+# ----------------------------------------------------------------- experts --
+
+def _tokens_of(name: str, x: torch.Tensor) -> torch.Tensor:
+    if not x.is_cuda:
+        raise TypeError("want CUDA tensors")
+    if x.dtype not in _HALVES:
+        raise TypeError(f"want bfloat16 or float16 {name}, not {x.dtype}")
+    if x.dim() != 2:
+        raise ValueError(f"want {name} [tokens, features]")
+    return x if x.stride(1) == 1 or x.shape[1] <= 1 else x.contiguous()
+
+
+def _weight_of(w: torch.Tensor, x: torch.Tensor):
+    """(the experts' matrices with consecutive elements in a row, whether they
+    are the transposes of w's)"""
+    if w.dtype != x.dtype or w.device != x.device:
+        raise TypeError("want weights of the tokens' type and device")
+    if w.dim() != 3 or w.shape[0] < 1:
+        raise ValueError("want weights [experts, out features, in features]")
+    if w.stride(2) == 1 or w.shape[2] <= 1:
+        return w, 0
+    if w.stride(1) == 1:
+        return w.mT, 1
+    return w.contiguous(), 0
+
+
+def _offsets_of(offsets: torch.Tensor, experts: int, device) -> torch.Tensor:
+    if offsets.dtype != torch.int64 or offsets.device != device:
+        raise TypeError("want int64 offsets on the tokens' device")
+    if offsets.shape != (experts + 1,):
+        raise ValueError(f"want {experts + 1} offsets for {experts} experts, not {tuple(offsets.shape)}")
+    return offsets if offsets.is_contiguous() else offsets.contiguous()
+
+
+def _rows_product(x, w, transposed, offsets, y):
+    lib = A.load()
+    a, b = _matrices(x), _matrices(w)
+    work = _workspace(lib.adamw_expert_workspace(_byref(a), _byref(b)), x.device)
+    _call(lib.adamw_expert_rows, "adamw_expert_rows", x.device, _byref(a), _byref(b), transposed, offsets.data_ptr(),
+          _byref(_matrices(y)), _ptr(work))
+    return y
+
+
+def _expert_linear(x, weight, offsets, out):
+    x = _tokens_of("tokens", x)
+    w, transposed = _weight_of(weight, x)
+    if weight.shape[2] != x.shape[1]:
+        raise ValueError(f"weights {tuple(weight.shape)} do not match tokens {tuple(x.shape)}")
+    offsets = _offsets_of(offsets, w.shape[0], x.device)
+    shape = (x.shape[0], weight.shape[1])
+    if out is None:
+        out = _empty(shape, dtype=x.dtype, device=x.device)
+    elif out.shape != shape or out.device != x.device or out.dtype not in _CODES or (shape[1] > 1 and out.stride(1) != 1):
+        raise ValueError("out must be [tokens, out features] on the tokens' device, rows of consecutive elements")
+    return _rows_product(x, w, transposed, offsets, out)
+
+
+class _ExpertLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, offsets):
+        ctx.save_for_backward(x, weight, offsets)
+        return _expert_linear(x, weight, offsets, None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, weight, offsets = ctx.saved_tensors
+        dx, dw = expert_linear_backward(dy, x, weight, offsets, need=ctx.needs_input_grad[:2])
+        return dx, dw, None
+
+
+def expert_linear(x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor, *,
+                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y[t] = weight[e] x[t] for every token t of expert e: x [tokens, in],
+    weight [experts, out, in] (or a transposed view of [experts, in, out]),
+    bf16 or fp16; sums in fp32, rounded once.  Tokens of no expert give zeros.
+    Differentiable in x and weight; forward mode has no rule and is refused.
+    ``out`` (bf16, fp16 or fp32) takes the result where no gradient is wanted."""
+    wanted = torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad)
+    if wanted or _tangent(x).tangent is not None or _tangent(weight).tangent is not None:
+        if out is not None:
+            raise RuntimeError("out= takes no part in autograd")
+        return _ExpertLinear.apply(x, weight, offsets)
+    y = _expert_linear(x, weight, offsets, out)
+    if out is not None:
+        _written(out)
+    return y
+
+
+def expert_linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor, *,
+                           need=(True, True), d_weight: Optional[torch.Tensor] = None, accumulate: bool = False):
+    """(gradient of x, gradient of weight) of ``expert_linear``; ``need`` says
+    which are wanted (None for the other).  ``d_weight``: where the weights'
+    gradient goes, [experts, out, in] in bf16, fp16 or fp32 (for example an
+    optimizer's own gradient buffer); with ``accumulate`` it is added there, in
+    fp32 before the rounding."""
+    dy, x = _tokens_of("gradients", dy.detach()), _tokens_of("tokens", x.detach())
+    weight = weight.detach()
+    w, transposed = _weight_of(weight, x)
+    if dy.dtype != x.dtype or dy.device != x.device:
+        raise TypeError("want gradients of the tokens' type and device")
+    if dy.shape != (x.shape[0], weight.shape[1]) or weight.shape[2] != x.shape[1]:
+        raise ValueError(f"gradients {tuple(dy.shape)}, tokens {tuple(x.shape)} and weights {tuple(weight.shape)} do not match")
+    offsets = _offsets_of(offsets, w.shape[0], x.device)
+    dx = dw = None
+    if need[0]:
+        dx = _rows_product(dy, w, 1 - transposed, offsets, _empty(x.shape, dtype=x.dtype, device=x.device))
+    if accumulate and d_weight is None:
+        raise ValueError("accumulate needs d_weight")
+    if need[1]:
+        given = d_weight is not None
+        if given:
+            if d_weight.requires_grad and torch.is_grad_enabled():
+                raise RuntimeError("d_weight requires a gradient")
+            if d_weight.shape != weight.shape or d_weight.device != x.device or d_weight.dtype not in _CODES:
+                raise ValueError("d_weight must have the weights' shape and device, in bfloat16, float16 or float32")
+            dw = d_weight
+        else:
+            # laid out as the weights are
+            dw = _empty(w.shape, dtype=w.dtype, device=x.device)
+            dw = dw.mT if transposed else dw
+        if dw.stride(2) == 1 or dw.shape[2] <= 1:
+            a, b, d = dy, x, dw
+        elif dw.stride(1) == 1:
+            a, b, d = x, dy, dw.mT   # the transposed sum
+        else:
+            raise ValueError("d_weight needs consecutive elements along one of its last two dimensions")
+        lib = A.load()
+        ma, mb = _matrices(a), _matrices(b)
+        work = _workspace(lib.adamw_expert_workspace(_byref(ma), _byref(mb)), x.device)
+        _call(lib.adamw_expert_outer, "adamw_expert_outer", x.device, _byref(ma), _byref(mb), offsets.data_ptr(),
+              _byref(_matrices(d)), int(accumulate), _ptr(work))
+        if given:
+            _written(dw)
+    return dx, dw
