@@ -21,7 +21,7 @@
 // each SM), which halves the shared-memory traffic of B against two single
 // tiles; the single form is for products with too few tiles to fill the GPU.
 //
-// No wait is endless: after about two seconds it gives up, sets the device's
+// No wait is endless: after about half a second it gives up, sets the device's
 // status word, and every role leaves.
 #pragma once
 
@@ -37,7 +37,7 @@ constexpr int kRowsOfCta = 128;             // accumulator rows of a CTA: the la
 constexpr uint32_t kStageRoom = 196608;     // bytes of the ring
 constexpr uint32_t kStagingRoom = 16384;    // four epilogue warps x 32 x 32 fp32
 constexpr uint32_t kControlRoom = 1024;
-constexpr long long kGiveUp = 4000000000ll; // cycles
+constexpr long long kGiveUp = 1000000000ll; // cycles
 
 // ------------------------------------------------------------------ PTX ---
 
@@ -64,17 +64,20 @@ __device__ __forceinline__ bool barrier_test(uint32_t bar, uint32_t parity) {
     uint32_t done;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.b32 %0, 1, 0, p;\n\t}"
         : "=r"(done) : "r"(bar), "r"(parity) : "memory");
     return done != 0;
 }
-// `bar` is a cluster address: this CTA's own or another's.
+// `bar` is a cluster address: this CTA's own or another's.  What these order
+// beyond the barrier goes through the asynchronous proxy or tensor memory, which
+// have fences of their own: at cluster scope, waits and arrivals would each
+// order all of the thread's memory (measured: 790 instead of FAST TFLOP/s).
 __device__ __forceinline__ void barrier_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void barrier_expect(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
 }
 
@@ -134,6 +137,18 @@ __device__ __forceinline__ void commit(uint32_t bar) {
             ::"r"(bar), "h"(uint16_t(3)) : "memory");
     else
         asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// True in one lane of a converged warp.  The instructions for one thread take
+// their operands from uniform registers; under a branch on this the compiler
+// knows that there is one.
+__device__ __forceinline__ bool elected() {
+    uint32_t yes;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(yes));
+    return yes != 0;
 }
 __device__ __forceinline__ void tmem_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -291,7 +306,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
     const int tiles = P::tiles(p, table);
     const Waiter wait = {ctl};
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         // ---- loads
         uint32_t it = 0;
         bool ok = true;
@@ -302,7 +317,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             const int a_at = w.a_at + int(rank) * kRowsOfCta, b_at = w.b_at + int(rank) * S::kBRows;
             for (int k = 0; k < w.k_len; k += kStepK, ++it) {
                 const uint32_t s = it % S::kStages;
-                if (!(ok = wait(smem_addr(&ctl->empty[s]), (it / S::kStages & 1) ^ 1))) break;
+                if (!(ok = wait.warp(smem_addr(&ctl->empty[s]), (it / S::kStages & 1) ^ 1))) break;
+                if (!elected()) continue;
                 const bool tail = P::kTail && k + kStepK > w.k_len;
                 const uint32_t own = smem_addr(tail ? &ctl->tail[s] : &ctl->full[s]);
                 const uint32_t bar = PAIR == 2 && !tail ? in_cta(own, 0) : own;
@@ -325,7 +341,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                 }
             }
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // The products' last arrivals: one that came after this CTA's end would
+        // reach the barriers of the next kernel's.
+        const uint32_t left = it < uint32_t(S::kStages) ? it : uint32_t(S::kStages);
+        for (uint32_t k = it - left; k < it && ok; ++k) ok = wait.warp(smem_addr(&ctl->empty[k % S::kStages]), k / S::kStages & 1);
+    } else if (warp == 1 && rank == 0) {
         // ---- products
         uint32_t it = 0, n = 0;
         bool ok = true;
@@ -336,24 +356,30 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             const bool a_mn = w.a_mn, b_mn = w.b_mn;
             const uint32_t kind = mma_kind(P::bf16(p), a_mn, b_mn, S::kRows, S::kCols);
             const uint32_t acc = n & 1;
-            if (!(ok = wait(smem_addr(&ctl->acc_empty[acc]), (n >> 1 & 1) ^ 1))) break;
+            if (!(ok = wait.warp(smem_addr(&ctl->acc_empty[acc]), (n >> 1 & 1) ^ 1))) break;
             tmem_after();
             for (int k = 0; k < w.k_len; k += kStepK, ++it) {
                 const uint32_t s = it % S::kStages;
-                if (!(ok = wait(smem_addr(&ctl->full[s]), it / S::kStages & 1))) break;
+                if (!(ok = wait.warp(smem_addr(&ctl->full[s]), it / S::kStages & 1))) break;
                 tmem_after();
                 const uint32_t at = smem_addr(ring) + s * S::kStageBytes;
                 const uint64_t a = operand(at, a_mn), b = operand(at + S::kABytes, b_mn);
                 const uint64_t da = operand_step(a_mn), db = operand_step(b_mn);
                 // the last step: only as many 16s of k as it has
                 const int parts = w.k_len - k >= kStepK ? kStepK / 16 : (w.k_len - k + 15) / 16;
-                for (int i = 0; i < parts; ++i)
-                    mma<PAIR>(tmem + acc * S::kCols, a + i * da, b + i * db, kind, k + i > 0);
-                commit<PAIR>(smem_addr(&ctl->empty[s]));
+                if (elected()) {
+#pragma unroll
+                    for (int i = 0; i < kStepK / 16; ++i)
+                        if (i < parts) mma<PAIR>(tmem + acc * S::kCols, a + i * da, b + i * db, kind, k + i > 0);
+                    commit<PAIR>(smem_addr(&ctl->empty[s]));
+                    if (k + kStepK >= w.k_len) commit<PAIR>(smem_addr(&ctl->acc_full[acc]));
+                }
+                __syncwarp();
             }
-            if (ok) commit<PAIR>(smem_addr(&ctl->acc_full[acc]));
             ++n;
         }
+        // the epilogues' last arrivals
+        for (uint32_t k = n < 2 ? 0 : n - 2; k < n && ok; ++k) ok = wait.warp(smem_addr(&ctl->acc_empty[k & 1]), k >> 1 & 1);
     } else if (P::kTail && warp == 2) {
         // ---- the last step of a tile whose k ends inside it: rows of k
         // beyond the end (another group's, or anything) become zeros in both
