@@ -738,3 +738,63 @@ class ClipPlan:
             self.close()
         except Exception:
             pass
+
+
+class MuonPlan:
+    """The Muon step over lists of torch CUDA tensors of one device: params and
+    grads bf16, momenta fp32 or bf16 (all of one type), masters fp32, each
+    contiguous [..., rows, cols] (leading dimensions are a batch of matrices).
+    No buffer may reach into another.  The tensors must stay alive and in place
+    for the plan's lifetime (the plan holds references to them); steps of one
+    plan must not overlap on the GPU."""
+
+    def __init__(self, params, grads, momenta, masters, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),
+                 eps: float = 1e-7, nesterov: bool = True, scale: str = "rms"):
+        import torch
+        lists = [list(x) for x in (params, grads, momenta, masters)]
+        if any(len(x) != len(lists[0]) for x in lists):
+            raise ValueError("tensor lists differ in length")
+        if not lists[0]:
+            raise ValueError("empty parameter list")
+        if scale not in MUON_SCALE:
+            raise ValueError('want scale "rms" or "spectral"')
+        dev, mdt = lists[0][0].device, lists[2][0].dtype
+        if mdt not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"want fp32 or bf16 momenta, not {mdt}")
+        want = (torch.bfloat16, torch.bfloat16, mdt, torch.float32)
+        entries = []
+        for k, ts in enumerate(zip(*lists)):
+            shape = ts[0].shape
+            if len(shape) < 2:
+                raise ValueError(f"tensor {k}: want [..., rows, cols]")
+            for t, dt in zip(ts, want):
+                if not t.is_cuda or t.device != dev or t.dtype != dt or not t.is_contiguous() or t.shape != shape:
+                    raise TypeError(f"tensor {k}: want contiguous CUDA {dt} {tuple(shape)} of one device")
+            entries.append(adamw_muon_tensor_t(*(t.data_ptr() or None for t in ts), shape[:-2].numel(), *shape[-2:]))
+        self._keep = lists
+        self.device = dev
+        self._options = adamw_muon_options_t(ortho_options(steps, coefficients, eps), int(nesterov), MUON_SCALE[scale],
+                                             DTYPE_FP32 if mdt == torch.float32 else DTYPE_BF16)
+        with torch.cuda.device(dev):
+            self.handle = adamw_muon_plan_create(entries, self._options)
+
+    def step(self, d_hparams, nonfinite, stream=None) -> None:
+        """d_hparams: CUDA fp32 [4]: lr, momentum, weight decay, unused;
+        nonfinite: CUDA int32 [1], 1 after a step that wrote nothing."""
+        import torch
+        for name, t, dt, n in (("d_hparams", d_hparams, torch.float32, 4), ("nonfinite", nonfinite, torch.int32, 1)):
+            if t.dtype != dt or t.device != self.device or t.numel() < n or not t.is_contiguous():
+                raise TypeError(f"want {name} contiguous {dt} [{n}] on {self.device}")
+        st = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self.device.index)
+        adamw_muon_step(self.handle, d_hparams.data_ptr(), nonfinite.data_ptr(), st)
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            adamw_muon_plan_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass

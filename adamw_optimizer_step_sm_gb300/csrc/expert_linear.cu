@@ -136,6 +136,8 @@ struct ExpertRows {
     };
     static constexpr bool kTail = false;
     static constexpr size_t kTable = sizeof(Groups);
+    static constexpr int kWarps = 4;
+    struct Late {};
     struct Extra {};
     struct Out {
         int64_t row, end;   // first row of the CTA's part, end of the group
@@ -182,9 +184,10 @@ struct ExpertRows {
     }
     __device__ static bool mirrored(const Out&) { return false; }
     __device__ static void fetch(const Params&, const Out&, int, int, Extra&) {}
-    __device__ static void store(const Params& p, const Out& o, int row, int col, const Extra&, float (&v)[8]) {
+    __device__ static void store(const Params& p, const Out& o, int row, int col, const Extra&, const Late&, float (&v)[8]) {
         if (o.row + row < o.end && o.col + col < p.y.cols) store_rows(p.y, o.row + row, o.col + col, v);
     }
+    __device__ static void fetch_late(const Params&, const Out&, int, int, Late&) {}
     __device__ static void mirror(const Params&, const Out&, int, int, const float (&)[8]) {}
 };
 
@@ -202,6 +205,8 @@ struct ExpertOuter {
     };
     static constexpr bool kTail = true;
     static constexpr size_t kTable = sizeof(Groups);
+    static constexpr int kWarps = 4;
+    struct Late {};
     struct Extra {
         float v[ADD ? 8 : 1];
     };
@@ -254,7 +259,7 @@ struct ExpertOuter {
             if (inside(p, o, row, col)) load_rows(rows(p, o), o.row + row, o.col + col, x.v);
         }
     }
-    __device__ static void store(const Params& p, const Out& o, int row, int col, const Extra& x, float (&v)[8]) {
+    __device__ static void store(const Params& p, const Out& o, int row, int col, const Extra& x, const Late&, float (&v)[8]) {
         if (!inside(p, o, row, col)) return;
         if constexpr (ADD) {
 #pragma unroll
@@ -262,6 +267,7 @@ struct ExpertOuter {
         }
         store_rows(rows(p, o), o.row + row, o.col + col, v);
     }
+    __device__ static void fetch_late(const Params&, const Out&, int, int, Late&) {}
     __device__ static void mirror(const Params&, const Out&, int, int, const float (&)[8]) {}
 };
 
@@ -357,8 +363,8 @@ cudaError_t units_of(TileUnits* u) {
     if (e != cudaSuccess) return e;
     if (known != device) {
         if ((e = cudaFuncSetAttribute(tile_kernel<P, PairTile>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      int(tile_smem(P::kTable)))) != cudaSuccess) return e;
-        if ((e = tile_units<P>(&units, tile_smem(P::kTable))) != cudaSuccess) return e;
+                                      int(tile_smem<P>()))) != cudaSuccess) return e;
+        if ((e = tile_units<P>(&units)) != cudaSuccess) return e;
         known = device;
     }
     *u = units;
@@ -373,11 +379,11 @@ bool run(const typename P::Params& p, int64_t tiles, int units, cudaStream_t st)
     if (!launched(cudaGetDevice(&device), "cudaGetDevice")) return false;
     if (known != device) {
         if (!launched(cudaFuncSetAttribute(tile_kernel<P, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           int(tile_smem(P::kTable))), "cudaFuncSetAttribute"))
+                                           int(tile_smem<P>())), "cudaFuncSetAttribute"))
             return false;
         known = device;
     }
-    return launched(launch(tile_kernel<P, S>, grid, kTileThreads, S::kPair, tile_smem(P::kTable), st, p), "product launch");
+    return launched(launch(tile_kernel<P, S>, grid, tile_threads<P>(), S::kPair, tile_smem<P>(), st, p), "product launch");
 }
 
 int64_t up(int64_t n, int64_t by) { return (n + by - 1) / by; }

@@ -198,8 +198,27 @@ __device__ __forceinline__ const CopyShape& piece_of(const CopyParams<MUON>& p, 
     return c;
 }
 
-// Sum of squares of each piece.  Eight squares are summed in fp32 and added in
-// fp64; squares that leave fp32's comfortable range are taken in fp64.
+// Where the vectors of piece i lie: rows of ld / 8 vectors, one after the other.
+struct Walk {
+    uint32_t per, first_col, n;
+    int32_t first_row;
+    __device__ Walk(const Shape& s, int32_t i) {
+        per = uint32_t(s.ld) / 8;
+        const int64_t first = int64_t(i) * kPieceVecs, left = int64_t(s.rows) * per - first;
+        first_row = int32_t(first / per);
+        first_col = uint32_t(first - int64_t(first_row) * per);
+        n = uint32_t(left < kPieceVecs ? left : kPieceVecs);
+    }
+    __device__ __forceinline__ bool at(int k, int32_t* row, int32_t* col) const {
+        const uint32_t v = first_col + uint32_t(k), r = v / per;
+        *row = first_row + int32_t(r);
+        *col = int32_t(v - r * per) * 8;
+        return uint32_t(k) < n;
+    }
+};
+
+// Sum of squares of each piece.  Eight squares are summed in fp32 and added
+// error-free; squares that leave fp32's comfortable range are taken in fp64.
 template <bool MUON>
 __global__ void __launch_bounds__(kNormThreads) norm_kernel(const __grid_constant__ CopyParams<MUON> p) {
     __shared__ double part[kNormThreads / 32];
@@ -208,26 +227,41 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const __grid_constan
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Source<MUON> src(p, c, matrix);
-    const int32_t per = c.s.ld / 8;
-    const int64_t total = int64_t(c.s.rows) * per, first = int64_t(i) * kPieceVecs;
+    const Walk walk(c.s, i);
+    Sum2 total = {0.0f, 0.0f};
     double sum = 0.0;
-#pragma unroll 4
-    for (int k = int(threadIdx.x); k < kPieceVecs; k += kNormThreads) {
-        const int64_t v = first + k;
-        if (v >= total) continue;
-        const int32_t row = int32_t(v / per), col = int32_t(v - int64_t(row) * per) * 8;
-        float u[8], m[8];
-        src.get(row, col, u, m);
-        float s = 0.0f;
+    constexpr int kBatch = MUON ? 2 : 4;   // vectors in flight
+#pragma unroll 1
+    for (int k = 0; k < kPieceVecs / kNormThreads; k += kBatch) {
+        float u[kBatch][8], m[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s = fmaf(u[e], u[e], s);
-        if (s >= 0x1p-100f && s <= 0x1p100f) {
-            sum += double(s);
-        } else {
+        for (int b = 0; b < kBatch; ++b) {
+            int32_t row, col;
+            if (walk.at((k + b) * kNormThreads + int(threadIdx.x), &row, &col)) {
+                src.get(row, col, u[b], m);
+            } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum += double(u[e]) * double(u[e]);
+                for (int e = 0; e < 8; ++e) u[b][e] = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            float s = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s = fmaf(u[b][e], u[b][e], s);
+            if (s >= 0x1p-100f && s <= 0x1p100f) {
+                total.add(s);
+            } else {
+                float any = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) any = any == 0.0f ? u[b][e] : any;
+                if (any == 0.0f) continue;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum += double(u[b][e]) * double(u[b][e]);
+            }
         }
     }
+    sum += double(total.hi) + double(total.lo);
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = sum;
@@ -272,24 +306,32 @@ __global__ void __launch_bounds__(kNormThreads) copy_kernel(const __grid_constan
     // NaN for a sum that is not finite: the matrix has no direction
     const float by = sum <= 1.7976931348623157e308 ? float(double(kScale) / (norm > p.eps ? norm : double(p.eps))) : sqrtf(-1.0f);
     const Source<MUON> src(p, c, matrix);
-    const int32_t per = c.s.ld / 8;
-    const int64_t total = int64_t(c.s.rows) * per, first = int64_t(i) * kPieceVecs;
-    uint4* hi = reinterpret_cast<uint4*>(c.hi + matrix * c.s.stride);
-    uint4* lo = reinterpret_cast<uint4*>(c.lo + matrix * c.s.stride);
-#pragma unroll 4
-    for (int k = int(threadIdx.x); k < kPieceVecs; k += kNormThreads) {
-        const int64_t v = first + k;
-        if (v >= total) continue;
-        const int32_t row = int32_t(v / per), col = int32_t(v - int64_t(row) * per) * 8;
-        float u[8], m[8];
-        src.get(row, col, u, m);
-        if (MUON && !skip) src.put(row, col, m);
+    const Walk walk(c.s, i);
+    uint4* hi = reinterpret_cast<uint4*>(c.hi + matrix * c.s.stride) + int64_t(i) * kPieceVecs;
+    uint4* lo = reinterpret_cast<uint4*>(c.lo + matrix * c.s.stride) + int64_t(i) * kPieceVecs;
+    constexpr int kBatch = MUON ? 2 : 4;
+#pragma unroll 1
+    for (int k = 0; k < kPieceVecs / kNormThreads; k += kBatch) {
+        float u[kBatch][8], m[MUON ? kBatch : 1][8];
+        int32_t row[kBatch], col[kBatch];
+        bool in[kBatch];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) u[e] *= by;
-        uint4 h, l;
-        split8(u, &h, &l);
-        hi[v] = h;   // rows of `per` vectors, as the copy has
-        lo[v] = l;
+        for (int b = 0; b < kBatch; ++b) {
+            in[b] = walk.at((k + b) * kNormThreads + int(threadIdx.x), &row[b], &col[b]);
+            if (in[b]) src.get(row[b], col[b], u[b], m[MUON ? b : 0]);
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            if (!in[b]) continue;
+            if (MUON && !skip) src.put(row[b], col[b], m[b]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[b][e] *= by;
+            uint4 h, l;
+            split8(u[b], &h, &l);
+            const int at = (k + b) * kNormThreads + int(threadIdx.x);   // the copy's rows are whole vectors
+            hi[at] = h;
+            lo[at] = l;
+        }
     }
 }
 
@@ -325,13 +367,18 @@ struct Product {
     using Params = ProductParams;
     static constexpr bool kTail = false;
     static constexpr size_t kTable = 0;
+    // Eight warps: with four, the reads of X (a microsecond each) made a tile's
+    // epilogue longer than its products.
+    static constexpr int kWarps = 8;
     static constexpr bool kSymmetric = KIND == kGram || KIND == kPoly;
     static_assert(!kSymmetric || S::kRows == S::kCols, "symmetric products take square tiles");
 
     // what the epilogue adds to the product
     struct Extra {
         uint4 hi, lo;
-        float w[KIND == kUpdate ? 8 : 1];
+    };
+    struct Late {
+        float w[KIND == kUpdate ? 8 : 1];   // the master
     };
     struct Out {
         const ProductShape* p;
@@ -415,11 +462,15 @@ struct Product {
         const int64_t at = int64_t(o.row + row) * ld(o) + o.col + col;
         x.hi = *reinterpret_cast<const uint4*>(o.hi + at);
         if (!kSymmetric) x.lo = *reinterpret_cast<const uint4*>(o.lo + at);
-        if constexpr (KIND == kUpdate)
-            load8_any(reinterpret_cast<const char*>(o.t.master), int64_t(o.row + row) * o.p->s.cols + o.col + col,
-                      ADAMW_DTYPE_FP32, o.vector, o.p->s.cols - o.col - col, x.w);
     }
-    __device__ static void store(const Params& p, const Out& o, int row, int col, const Extra& x, float (&v)[8]) {
+    __device__ static void fetch_late(const Params& p, const Out& o, int row, int col, Late& x) {
+        if constexpr (KIND == kUpdate) {
+            if (wanted(p, o, row, col))
+                load8_any(reinterpret_cast<const char*>(o.t.master), int64_t(o.row + row) * o.p->s.cols + o.col + col,
+                          ADAMW_DTYPE_FP32, o.vector, o.p->s.cols - o.col - col, x.w);
+        }
+    }
+    __device__ static void store(const Params& p, const Out& o, int row, int col, const Extra& x, const Late& y, float (&v)[8]) {
         const bool here = wanted(p, o, row, col);
         const int64_t at = int64_t(o.row + row) * ld(o) + o.col + col;
         if constexpr (kSymmetric) {
@@ -448,7 +499,7 @@ struct Product {
                 const int64_t to = int64_t(o.row + row) * o.p->s.cols + o.col + col;
                 const int n = o.p->s.cols - o.col - col;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = fmaf(-o.rate, v[e], o.decay * x.w[e]);
+                for (int e = 0; e < 8; ++e) v[e] = fmaf(-o.rate, v[e], o.decay * y.w[e]);
                 store8_any(reinterpret_cast<char*>(o.t.master), to, ADAMW_DTYPE_FP32, o.vector, n, v);
                 store8_any(reinterpret_cast<char*>(o.t.param), to, ADAMW_DTYPE_BF16, o.vector, n, v);
             }
@@ -565,7 +616,7 @@ template <int KIND, class S>
 bool allow() {
     using P = Product<KIND, S>;
     return launched(cudaFuncSetAttribute(tile_kernel<P, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         int(tile_smem(P::kTable))), "cudaFuncSetAttribute");
+                                         int(tile_smem<P>())), "cudaFuncSetAttribute");
 }
 
 // The current device's units; allows the kernels' shared memory there.
@@ -580,7 +631,7 @@ bool device_units(Device* d) {
             !allow<kResult, SingleTile>() || !allow<kUpdate, SingleTile>())
             return false;
         TileUnits u;
-        if (!launched(tile_units<Product<kApply, PairTile>>(&u, tile_smem(0)), "tile units")) return false;
+        if (!launched(tile_units<Product<kApply, PairTile>>(&u), "tile units")) return false;
         units.sms = u.sms;
         units.pairs = u.pairs;
         known = device;
@@ -593,7 +644,7 @@ template <int KIND, class S>
 bool launch_product(const ProductParams& p, int units, cudaStream_t st) {
     const uint32_t grid = uint32_t(p.tiles < units ? p.tiles : units) * S::kPair;
     using P = Product<KIND, S>;
-    return launched(launch(tile_kernel<P, S>, grid, kTileThreads, S::kPair, tile_smem(P::kTable), st, p), "product launch");
+    return launched(launch(tile_kernel<P, S>, grid, tile_threads<P>(), S::kPair, tile_smem<P>(), st, p), "product launch");
 }
 template <class S>
 bool launch_kind(int kind, const ProductParams& p, int units, cudaStream_t st) {

@@ -11,7 +11,7 @@
 // A unit (one CTA, or a pair on two neighbouring SMs) computes a tile of
 // kRows x kCols in steps of 64 k.  Roles, a warp each: TMA loads into a ring
 // of stages; one thread issues tcgen05.mma into one of two accumulators in
-// tensor memory; four warps read the other one out and hand it to the policy
+// tensor memory; four or eight warps read the other one out and hand it to the policy
 // in vectors of eight columns; and where k ends inside a step at an element
 // that the next group owns (the ragged sums over tokens), one warp zeroes the
 // rest of the step in shared memory.
@@ -31,11 +31,10 @@
 
 namespace {
 
-constexpr int kTileThreads = 256;
 constexpr int kStepK = 64;                  // elements of k in a stage: 128 bytes, one swizzle row
 constexpr int kRowsOfCta = 128;             // accumulator rows of a CTA: the lanes of tensor memory
 constexpr uint32_t kStageRoom = 196608;     // bytes of the ring
-constexpr uint32_t kStagingRoom = 16384;    // four epilogue warps x 32 x 32 fp32
+constexpr uint32_t kStagingOfWarp = 4096;   // 32 x 32 fp32
 constexpr uint32_t kControlRoom = 1024;
 constexpr long long kGiveUp = 1000000000ll; // cycles
 
@@ -248,33 +247,44 @@ struct TileShape {
 using PairTile = TileShape<2, 256>;
 using SingleTile = TileShape<1, 128>;
 
-constexpr size_t tile_smem(size_t table) { return 1024 + kStageRoom + kStagingRoom + kControlRoom + table; }
+template <class P>
+constexpr size_t tile_smem() {
+    static_assert(P::kWarps == 4 || P::kWarps == 8, "epilogue warps");
+    constexpr size_t n = 1024 + kStageRoom + P::kWarps * kStagingOfWarp + kControlRoom + P::kTable;
+    static_assert(n <= 232448, "shared memory of a CTA");
+    return n;
+}
+template <class P>
+constexpr int tile_threads() { return 128 + 32 * P::kWarps; }
 
 // A policy P over a tile shape S:
 //   P::Params       kernel arguments;  P::kTail: k may end inside a step
 //   P::kTable       bytes of shared memory for its tables
+//   P::kWarps       epilogue warps, 4 or 8: each 32 of the CTA's 128 rows, all
+//                   columns or every second block of 32
 //   prepare(p, table)                    all threads, before the first tile
 //   tiles(p, table)                      number of tiles
 //   loads(p, table, tile, TileLoads&)    operands
 //   bf16(p)                              type of the operands
 //   Out: what the epilogue keeps of a tile; out<S>(p, table, tile, rank)
 //   wanted(p, out, row, col): whether the 32 x 32 block there has anything to store
-//   Extra, fetch(p, out, row, col, Extra&): what store will want of memory
-//   store(p, out, row, col, extra, float (&v)[8]): eight columns from `col` of
+//   Extra, fetch(p, out, row, col, Extra&): what store will want of memory,
+//        fetched a block ahead;  Late, fetch_late: the same, of the block itself
+//   store(p, out, row, col, extra, late, float (&v)[8]): eight columns from `col` of
 //        row `row` of the CTA's 128 x kCols part; leaves in v what the
 //        mirrored tile holds
 //   mirrored(out), mirror(p, out, col, row, v): eight rows from `row` of column
 //        `col`, for the transposed tile.
 template <class P, class S>
-__global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_constant__ typename P::Params p) {
+__global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid_constant__ typename P::Params p) {
     constexpr int PAIR = S::kPair;
     extern __shared__ unsigned char raw[];
     // 1024-byte boundary: the swizzle goes by address bits; the same in both CTAs
     unsigned char* base = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
     unsigned char* ring = base;
     float* staging = reinterpret_cast<float*>(base + kStageRoom);
-    Control* ctl = reinterpret_cast<Control*>(base + kStageRoom + kStagingRoom);
-    unsigned char* table = base + kStageRoom + kStagingRoom + kControlRoom;
+    Control* ctl = reinterpret_cast<Control*>(base + kStageRoom + P::kWarps * kStagingOfWarp);
+    unsigned char* table = reinterpret_cast<unsigned char*>(ctl) + kControlRoom;
 
     const int warp = int(threadIdx.x) / 32, lane = int(threadIdx.x) % 32;
     const uint32_t rank = PAIR == 2 ? cta_rank() : 0;
@@ -286,7 +296,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
         }
         for (int a = 0; a < 2; ++a) {
             barrier_init(smem_addr(&ctl->acc_full[a]), 1);
-            barrier_init(smem_addr(&ctl->acc_empty[a]), 4 * PAIR);
+            barrier_init(smem_addr(&ctl->acc_empty[a]), P::kWarps * PAIR);
         }
         ctl->failed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -416,26 +426,32 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
             P::loads(p, table, t, w);
             const typename P::Out out = P::template out<S>(p, table, t, rank);
             const uint32_t acc = n & 1;
-            const int row0 = (warp - 4) * 32;
+            // a warp reaches the 32 lanes of tensor memory of its number modulo 4
+            const int row0 = warp % 4 * 32;
+            constexpr int kNext = P::kWarps * 8;   // columns to the warp's next block
+            const int c0 = (warp - 4) / 4 * 32;
             // what the epilogue reads of memory is fetched a block ahead
             typename P::Extra next[4];
-            if (P::wanted(p, out, row0, 0)) {
+            if (P::wanted(p, out, row0, c0)) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) P::fetch(p, out, row0 + i * 8 + lane / 4, lane % 4 * 8, next[i]);
+                for (int i = 0; i < 4; ++i) P::fetch(p, out, row0 + i * 8 + lane / 4, c0 + lane % 4 * 8, next[i]);
             }
             if (w.k_len > 0) {
                 if (!(ok = wait.warp(smem_addr(&ctl->acc_full[acc]), n >> 1 & 1))) break;
                 tmem_after();
             }
-            for (int c = 0; c < S::kCols; c += 32) {
+            for (int c = c0; c < S::kCols; c += kNext) {
                 if (!P::wanted(p, out, row0, c)) continue;
                 typename P::Extra now[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) now[i] = next[i];
-                if (c + 32 < S::kCols && P::wanted(p, out, row0, c + 32)) {
+                if (c + kNext < S::kCols && P::wanted(p, out, row0, c + kNext)) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) P::fetch(p, out, row0 + i * 8 + lane / 4, c + 32 + lane % 4 * 8, next[i]);
+                    for (int i = 0; i < 4; ++i) P::fetch(p, out, row0 + i * 8 + lane / 4, c + kNext + lane % 4 * 8, next[i]);
                 }
+                typename P::Late late[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) P::fetch_late(p, out, row0 + i * 8 + lane / 4, c + lane % 4 * 8, late[i]);
                 uint32_t v[32];
                 if (w.k_len > 0) {
                     tmem_load(tmem + (uint32_t(row0) << 16) + acc * S::kCols + uint32_t(c), v);
@@ -454,7 +470,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(const __grid_cons
                     float x[8];
                     *reinterpret_cast<float4*>(x) = *reinterpret_cast<float4*>(place(r, q));
                     *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<float4*>(place(r, q + 4));
-                    P::store(p, out, row0 + r, c + q, now[i / 8], x);
+                    P::store(p, out, row0 + r, c + q, now[i / 8], late[i / 8], x);
                     if (mirrored) {
                         *reinterpret_cast<float4*>(place(r, q)) = *reinterpret_cast<float4*>(x);
                         *reinterpret_cast<float4*>(place(r, q + 4)) = *reinterpret_cast<float4*>(x + 4);
@@ -542,15 +558,15 @@ struct TileUnits {
 };
 
 template <class P>
-cudaError_t tile_units(TileUnits* u, size_t smem) {
+cudaError_t tile_units(TileUnits* u) {
     int device = 0;
     cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&u->sms, cudaDevAttrMultiProcessorCount, device)) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(u->sms / 2 * 2));
-    cfg.blockDim = dim3(kTileThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.blockDim = dim3(tile_threads<P>());
+    cfg.dynamicSmemBytes = tile_smem<P>();
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;

@@ -1,8 +1,9 @@
-"""``AnyPrecisionAdamW`` and ``MasterWeightAdamW``: ``torch.optim``
+"""``AnyPrecisionAdamW``, ``MasterWeightAdamW`` and ``Muon``: ``torch.optim``
 optimizers whose step is one call into the adamw_sm library
-(``adamw_step_device``) per parameter group.  ``MasterWeightAdamW`` is the
-fp32-master update (see its docstring); the rest of this note is about
-``AnyPrecisionAdamW`` and holds for both where it concerns the layout and
+(``adamw_step_device``, ``adamw_muon_step``) per parameter group.
+``MasterWeightAdamW`` is the fp32-master update and ``Muon`` the
+orthogonalised momentum (see their docstrings); the rest of this note is about
+``AnyPrecisionAdamW`` and holds for all where it concerns the layout and
 the step.
 
 It takes the options the pure-bf16 recipe passes to its optimizer ("[pure
@@ -119,9 +120,60 @@ class _GroupBuffers:
         self.hp_key = None
 
 
-class _FlatAdamW(torch.optim.Optimizer):
-    """The shared machinery: flat buffers per group, one device-resident
-    library step per group, checkpoints into the optimizer's own buffers."""
+class _FlatOptimizer(torch.optim.Optimizer):
+    """What the optimizers of this module share: a flat gradient buffer per
+    group that the parameters' gradients are views of, and masters that follow
+    the model's parameters."""
+
+    def add_param_group(self, param_group):
+        super().add_param_group(param_group)
+        if hasattr(self, "_buffers"):
+            self._buffers_of(self.param_groups[-1])
+
+    def _gather(self, group, b) -> None:
+        """Brings gradients found outside the group's buffer into it."""
+        for k, (p, g) in enumerate(zip(group["params"], b.grads)):
+            if p.grad is None:
+                raise RuntimeError(f"parameter {k} of a group has no gradient; "
+                                   f"{type(self).__name__} steps every parameter")
+            if p.grad.data_ptr() != g.data_ptr():
+                g.copy_(p.grad)
+                p.grad = g
+
+    def zero_grad(self, set_to_none: bool = True):
+        """Zeroes the gradient buffers in place; ``set_to_none`` is ignored
+        (the gradients stay views of the optimizer's buffer)."""
+        for group in self.param_groups:
+            b = self._buffers_of(group)
+            b.grad.zero_()
+            for p, g in zip(group["params"], b.grads):
+                p.grad = g
+
+    @property
+    def last_nonfinite(self) -> list[torch.Tensor]:
+        """Per group, 1 when the last step's gradients held inf or NaN, else 0
+        (int32, device).  With clipping, and always with ``Muon``, such a step
+        wrote nothing (an AdamW's counter stayed); without clipping the values
+        went through."""
+        return [self._buffers_of(g).nonfinite for g in self.param_groups]
+
+    @torch.no_grad()
+    def sync_master(self) -> None:
+        """Re-derives every master copy from the model's current bf16
+        parameters (fp32 master = the parameter's value; remainder = 0).
+        ``step`` does this by itself for a parameter changed in place (a
+        model ``load_state_dict``, ``p.copy_``); call it after changing a
+        parameter through ``p.data``, which ``step`` cannot see."""
+        for group in self.param_groups:
+            b = self._buffers_of(group)
+            for k, p in enumerate(group["params"]):
+                self._sync_master(b, k, p, force=True)
+
+
+class _FlatAdamW(_FlatOptimizer):
+    """The AdamW optimizers' machinery: flat buffers per group, one
+    device-resident library step per group, checkpoints into the optimizer's
+    own buffers."""
     _aux_name = "compensation"
 
     def __init__(self, params, mode: int, lr: float, betas, eps: float, weight_decay: float,
@@ -170,11 +222,6 @@ class _FlatAdamW(torch.optim.Optimizer):
             self._buffers[key] = b
         return b
 
-    def add_param_group(self, param_group):
-        super().add_param_group(param_group)
-        if hasattr(self, "_buffers"):
-            self._buffers_of(self.param_groups[-1])
-
     # -- the master copy (MasterWeightAdamW) ----------------------------------
     def _sync_master(self, b: _GroupBuffers, k: int, p, force: bool) -> None:
         """Makes parameter k's master agree with the model parameter p again.
@@ -196,29 +243,7 @@ class _FlatAdamW(torch.optim.Optimizer):
             if p._version != b.versions[k]:
                 self._sync_master(b, k, p, force=False)
 
-    @torch.no_grad()
-    def sync_master(self) -> None:
-        """Re-derives every master copy from the model's current bf16
-        parameters (fp32 master = the parameter's value; remainder = 0).
-        ``step`` does this by itself for a parameter changed in place (a
-        model ``load_state_dict``, ``p.copy_``); call it after changing a
-        parameter through ``p.data``, which ``step`` cannot see."""
-        for group in self.param_groups:
-            b = self._buffers_of(group)
-            for k, p in enumerate(group["params"]):
-                self._sync_master(b, k, p, force=True)
-
     # -- the step -----------------------------------------------------------
-    def _gather(self, group, b: _GroupBuffers) -> None:
-        """Brings gradients found outside the group's buffer into it."""
-        for k, (p, g) in enumerate(zip(group["params"], b.grads)):
-            if p.grad is None:
-                raise RuntimeError(f"parameter {k} of a group has no gradient; "
-                                   f"{type(self).__name__} steps every parameter")
-            if p.grad.data_ptr() != g.data_ptr():
-                g.copy_(p.grad)
-                p.grad = g
-
     @torch.no_grad()
     def step(self, closure=None):
         loss = None
@@ -248,28 +273,12 @@ class _FlatAdamW(torch.optim.Optimizer):
                                grad_norm=b.grad_norm if norm else None, nonfinite=b.nonfinite)
         return loss
 
-    def zero_grad(self, set_to_none: bool = True):
-        """Zeroes the gradient buffers in place; ``set_to_none`` is ignored
-        (the gradients stay views of the optimizer's buffer)."""
-        for group in self.param_groups:
-            b = self._buffers_of(group)
-            b.grad.zero_()
-            for p, g in zip(group["params"], b.grads):
-                p.grad = g
-
     # -- observation and checkpoints ----------------------------------------
     @property
     def last_grad_norm(self) -> list[torch.Tensor]:
         """Per group, the global gradient norm of the last step (fp64, device;
         computed when clipping or with ``track_grad_norm``)."""
         return [self._buffers_of(g).grad_norm for g in self.param_groups]
-
-    @property
-    def last_nonfinite(self) -> list[torch.Tensor]:
-        """Per group, 1 when the last step's gradients held inf or NaN, else 0
-        (int32, device).  With clipping on such a step wrote nothing and the
-        step counter stayed; without clipping the values went through."""
-        return [self._buffers_of(g).nonfinite for g in self.param_groups]
 
     def load_state_dict(self, state_dict):
         """Loads hyperparameters and state into this optimizer's own buffers
@@ -363,6 +372,162 @@ class MasterWeightAdamW(_FlatAdamW):
                          track_grad_norm)
 
 
+class _MuonBuffers:
+    """A group's flat buffers, views, plan and step state."""
+
+    def __init__(self, params, momentum_dtype, options):
+        dev = params[0].device
+        offs, n = [], 0
+        for p in params:
+            offs.append(n)
+            n += -(-p.numel() // _ALIGN) * _ALIGN
+        n = max(n, 1)
+        flat = lambda dt: torch.zeros(n, dtype=dt, device=dev)
+        views = lambda buf: [buf[o:o + p.numel()].view(p.shape) for p, o in zip(params, offs)]
+        self.grad, self.momentum, self.master = flat(torch.bfloat16), flat(momentum_dtype), flat(torch.float32)
+        self.grads, self.momenta, self.masters = views(self.grad), views(self.momentum), views(self.master)
+        for m, p in zip(self.masters, params):
+            m.copy_(p.detach())
+        self.versions = [p._version for p in params]
+        self.nonfinite = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.d_hp = torch.zeros(4, dtype=torch.float32, device=dev)
+        self.hp_key = None
+        self.plan = A.MuonPlan(params, self.grads, self.momenta, self.masters, **options)
+
+
+class Muon(_FlatOptimizer):
+    """Momentum, orthogonalised matrix by matrix, for the matrix parameters of
+    a model (the rest, and embeddings and output layers, stay with an AdamW):
+
+        M <- M + (1 - momentum) (G - M),  U = G + momentum (M - G) (nesterov) or M
+        W <- W (1 - lr weight_decay) - lr scale orthogonalize(U)
+
+    Parameters are bf16 CUDA tensors of two or more dimensions, [..., rows,
+    cols]: leading dimensions are a batch of matrices (experts).  The update
+    goes to an fp32 master, from which the parameter is rounded; the momentum
+    is fp32 or bf16.  ``scale``: "rms", 0.2 sqrt(max(rows, cols)), which makes
+    the update as large as an AdamW's, so that both take the same rate; or
+    "spectral", sqrt(max(1, rows / cols)).  ``steps``, ``coefficients`` and
+    ``eps`` are ``matrix.orthogonalize``'s.
+
+    One library call per group, no host synchronisation; the rates live on the
+    device, so that a captured step follows a schedule (call ``step`` once more
+    outside the capture, or write ``lr`` before each replay through
+    ``push_rates``).  A step whose gradients hold inf or NaN writes nothing and
+    is reported by ``last_nonfinite``.  Gradients, masters and checkpoints
+    behave as ``MasterWeightAdamW``'s; ``GlobalClip`` takes both kinds."""
+
+    def __init__(self, params, lr: float = 2e-4, momentum: float = 0.95, nesterov: bool = True,
+                 weight_decay: float = 0.1, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),
+                 eps: float = 1e-7, scale: str = "rms", momentum_dtype: torch.dtype = torch.float32):
+        if scale not in A.MUON_SCALE:
+            raise ValueError('want scale "rms" or "spectral"')
+        if momentum_dtype not in _DTYPES:
+            raise ValueError(f"momentum_dtype must be torch.bfloat16 or torch.float32, not {momentum_dtype}")
+        self._momentum_dtype = momentum_dtype
+        self._options = dict(steps=steps, coefficients=coefficients, eps=eps, nesterov=nesterov, scale=scale)
+        A.ortho_options(steps, coefficients, eps)
+        self._buffers: dict[int, _MuonBuffers] = {}
+        super().__init__(params, dict(lr=lr, momentum=momentum, weight_decay=weight_decay))
+        for group in self.param_groups:
+            self._buffers_of(group)
+
+    @staticmethod
+    def _rates(group):
+        # plain floats (a scheduler may keep lr as a tensor)
+        lr, momentum, decay = (float(group[k]) for k in ("lr", "momentum", "weight_decay"))
+        if not (0.0 <= lr < float("inf")) or not 0.0 <= momentum < 1.0 or not (0.0 <= decay < float("inf")):
+            raise ValueError("want lr >= 0, momentum in [0, 1) and weight_decay >= 0")
+        return lr, momentum, decay
+
+    def _buffers_of(self, group) -> _MuonBuffers:
+        key = id(group)
+        b = self._buffers.get(key)
+        if b is None:
+            params = group["params"]
+            if not params:
+                raise ValueError("empty parameter group")
+            self._rates(group)
+            dev = params[0].device
+            for p in params:
+                if not p.is_cuda or p.dtype != torch.bfloat16 or not p.is_contiguous() or p.device != dev:
+                    raise TypeError("Muon steps contiguous bf16 CUDA parameters of one device")
+                if p.dim() < 2:
+                    raise ValueError("Muon steps matrices; give vectors to another optimizer")
+            with torch.cuda.device(dev):
+                b = _MuonBuffers(params, self._momentum_dtype, self._options)
+            for k, (p, g) in enumerate(zip(params, b.grads)):
+                if p.grad is not None:
+                    g.copy_(p.grad)
+                p.grad = g
+                self.state[p]["momentum"] = b.momenta[k]
+                self.state[p]["master"] = b.masters[k]
+            self._buffers[key] = b
+        return b
+
+    def _sync_master(self, b: _MuonBuffers, k: int, p, force: bool) -> None:
+        """Makes parameter k's master agree with the model parameter p again;
+        kept when p is its round-to-nearest-even bf16 value."""
+        m = b.masters[k]
+        if force or not torch.equal(m.to(torch.bfloat16), p.detach()):
+            m.copy_(p.detach())
+        b.versions[k] = p._version
+
+    @torch.no_grad()
+    def push_rates(self) -> None:
+        """Writes each group's lr, momentum and weight decay to the device, for
+        the next step (``step`` does it by itself; replays of a captured step
+        do not)."""
+        for group in self.param_groups:
+            b = self._buffers_of(group)
+            key = self._rates(group)
+            if key != b.hp_key:
+                b.d_hp.copy_(torch.tensor([*key, 0.0], dtype=torch.float32).pin_memory(), non_blocking=True)
+                b.hp_key = key
+
+    @torch.no_grad()
+    def step(self, closure=None):
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        self.push_rates()
+        for group in self.param_groups:
+            b = self._buffers_of(group)
+            for k, p in enumerate(group["params"]):
+                if p._version != b.versions[k]:
+                    self._sync_master(b, k, p, force=False)
+            self._gather(group, b)
+            b.plan.step(b.d_hp, b.nonfinite)
+        return loss
+
+    def load_state_dict(self, state_dict):
+        """Loads rates and state into this optimizer's own buffers (values are
+        copied, each in its buffer's type)."""
+        groups = state_dict["param_groups"]
+        if len(groups) != len(self.param_groups):
+            raise ValueError("loaded state has a different number of parameter groups")
+        saved = state_dict["state"]
+        for group, sg in zip(self.param_groups, groups):
+            if len(sg["params"]) != len(group["params"]):
+                raise ValueError("loaded state has a different group size")
+            for name in ("lr", "momentum", "weight_decay"):
+                if name in sg:
+                    group[name] = sg[name]
+            b = self._buffers_of(group)
+            for k, (idx, p) in enumerate(zip(sg["params"], group["params"])):
+                s = saved.get(idx) or {}
+                if "momentum" in s:
+                    self.state[p]["momentum"].copy_(s["momentum"])
+                if "master" in s:
+                    self.state[p]["master"].copy_(s["master"])
+                    # the loaded master is authoritative for the parameter as it stands now
+                    b.versions[k] = p._version
+                else:
+                    with torch.no_grad():
+                        self._sync_master(b, k, p, force=True)
+
+
 class GlobalClip:
     """Clips the gradients of every parameter group of one or more of this
     module's optimizers by one norm over them all, in place, before their
@@ -376,8 +541,8 @@ class GlobalClip:
     device tensors of the plan).  Non-finite gradients are passed on
     unscaled: the optimizers report them (``last_nonfinite``)."""
 
-    def __init__(self, *optimizers: _FlatAdamW):
-        if not optimizers or not all(isinstance(o, _FlatAdamW) for o in optimizers):
+    def __init__(self, *optimizers: _FlatOptimizer):
+        if not optimizers or not all(isinstance(o, _FlatOptimizer) for o in optimizers):
             raise TypeError("want one or more optimizers of this module")
         if len({id(o) for o in optimizers}) < len(optimizers):
             raise ValueError("an optimizer is listed twice")
