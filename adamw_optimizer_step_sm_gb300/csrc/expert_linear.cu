@@ -76,10 +76,17 @@ struct RowsAt {
     int32_t vector;   // 16-byte accesses
 };
 
+// The rows from (row, col) on.
+__device__ __forceinline__ RowsAt part_of(RowsAt r, int64_t row, int32_t col) {
+    r.data += (row * r.ld + col) * (r.dtype == ADAMW_DTYPE_FP32 ? 4 : 2);
+    r.cols -= col;
+    return r;
+}
+
 template <int DT>
-__device__ __forceinline__ void store8(char* at, const float (&v)[8], int n, bool vector) {
+__device__ __forceinline__ void store8(char* at, const float (&v)[8], int n) {
     using E = Elem<DT>;
-    if (vector && n >= 8) {
+    if (n >= 8) {
         *reinterpret_cast<uint4*>(at) = E::pack(v);
         if (E::kVec == 4) *reinterpret_cast<uint4*>(at + 16) = E::pack(v + 4);
     } else {
@@ -89,9 +96,9 @@ __device__ __forceinline__ void store8(char* at, const float (&v)[8], int n, boo
     }
 }
 template <int DT>
-__device__ __forceinline__ void load8(const char* at, float (&v)[8], int n, bool vector) {
+__device__ __forceinline__ void load8(const char* at, float (&v)[8], int n) {
     using E = Elem<DT>;
-    if (vector && n >= 8) {
+    if (n >= 8) {
         E::unpack(*reinterpret_cast<const uint4*>(at), v);
         if (E::kVec == 4) E::unpack(*reinterpret_cast<const uint4*>(at + 16), v + 4);
     } else {
@@ -99,19 +106,32 @@ __device__ __forceinline__ void load8(const char* at, float (&v)[8], int n, bool
         for (int i = 0; i < 8; ++i) v[i] = i < n ? E::load(at, i) : 0.0f;
     }
 }
-__device__ __forceinline__ void store_rows(const RowsAt& r, int64_t row, int col, const float (&v)[8]) {
+// of rows of whole vectors
+__device__ __forceinline__ void store_rows(const RowsAt& r, int row, int col, const float (&v)[8]) {
     const int64_t at = row * r.ld + col;
     const int n = r.cols - col;
-    if (r.dtype == ADAMW_DTYPE_BF16) store8<ADAMW_DTYPE_BF16>(r.data + at * 2, v, n, r.vector);
-    else if (r.dtype == ADAMW_DTYPE_FP16) store8<ADAMW_DTYPE_FP16>(r.data + at * 2, v, n, r.vector);
-    else store8<ADAMW_DTYPE_FP32>(r.data + at * 4, v, n, r.vector);
+    if (r.dtype == ADAMW_DTYPE_BF16) store8<ADAMW_DTYPE_BF16>(r.data + at * 2, v, n);
+    else if (r.dtype == ADAMW_DTYPE_FP16) store8<ADAMW_DTYPE_FP16>(r.data + at * 2, v, n);
+    else store8<ADAMW_DTYPE_FP32>(r.data + at * 4, v, n);
 }
-__device__ __forceinline__ void load_rows(const RowsAt& r, int64_t row, int col, float (&v)[8]) {
+__device__ __forceinline__ void load_rows(const RowsAt& r, int row, int col, float (&v)[8]) {
     const int64_t at = row * r.ld + col;
     const int n = r.cols - col;
-    if (r.dtype == ADAMW_DTYPE_BF16) load8<ADAMW_DTYPE_BF16>(r.data + at * 2, v, n, r.vector);
-    else if (r.dtype == ADAMW_DTYPE_FP16) load8<ADAMW_DTYPE_FP16>(r.data + at * 2, v, n, r.vector);
-    else load8<ADAMW_DTYPE_FP32>(r.data + at * 4, v, n, r.vector);
+    if (r.dtype == ADAMW_DTYPE_BF16) load8<ADAMW_DTYPE_BF16>(r.data + at * 2, v, n);
+    else if (r.dtype == ADAMW_DTYPE_FP16) load8<ADAMW_DTYPE_FP16>(r.data + at * 2, v, n);
+    else load8<ADAMW_DTYPE_FP32>(r.data + at * 4, v, n);
+}
+// of any rows
+__device__ __forceinline__ void store_as(const RowsAt& r, int row, int col, float v) {
+    const int64_t at = row * r.ld + col;
+    if (r.dtype == ADAMW_DTYPE_BF16) Elem<ADAMW_DTYPE_BF16>::store(r.data, at, v);
+    else if (r.dtype == ADAMW_DTYPE_FP16) Elem<ADAMW_DTYPE_FP16>::store(r.data, at, v);
+    else Elem<ADAMW_DTYPE_FP32>::store(r.data, at, v);
+}
+__device__ __forceinline__ float load_as(const RowsAt& r, int row, int col) {
+    const int64_t at = row * r.ld + col;
+    return r.dtype == ADAMW_DTYPE_BF16 ? Elem<ADAMW_DTYPE_BF16>::load(r.data, at)
+           : r.dtype == ADAMW_DTYPE_FP16 ? Elem<ADAMW_DTYPE_FP16>::load(r.data, at) : Elem<ADAMW_DTYPE_FP32>::load(r.data, at);
 }
 
 // Tile (m, n) number i of a group of tm x tn: bands of eight tiles of rows, so
@@ -140,8 +160,8 @@ struct ExpertRows {
     struct Late {};
     struct Extra {};
     struct Out {
-        int64_t row, end;   // first row of the CTA's part, end of the group
-        int32_t col;
+        RowsAt y;       // from the first row and column of the CTA's part
+        int32_t rows;   // of the group, from there (0 or less: none)
     };
     __device__ static bool bf16(const Params& p) { return p.is_bf16; }
     __device__ static void prepare(const Params& p, unsigned char* table) {
@@ -177,15 +197,18 @@ struct ExpertRows {
         int32_t m, n;
         const int k = find(p, table, t, &m, &n);
         const Groups* g = reinterpret_cast<const Groups*>(table);
-        return {int64_t(g->bounds[k]) + m * S::kRows + int64_t(rank) * kRowsOfCta, g->bounds[k + 1], n * S::kCols};
+        const int64_t row = int64_t(g->bounds[k]) + int64_t(m) * S::kRows + int64_t(rank) * kRowsOfCta;
+        return {part_of(p.y, row, n * S::kCols), int32_t(g->bounds[k + 1] - row)};
     }
-    __device__ static bool wanted(const Params& p, const Out& o, int row, int col) {
-        return o.row + row < o.end && o.col + col < p.y.cols;
-    }
+    __device__ static bool wanted(const Params&, const Out& o, int row, int col) { return row < o.rows && col < o.y.cols; }
     __device__ static bool mirrored(const Out&) { return false; }
+    __device__ static bool scalar(const Out& o) { return !o.y.vector; }
     __device__ static void fetch(const Params&, const Out&, int, int, Extra&) {}
     __device__ static void store(const Params& p, const Out& o, int row, int col, const Extra&, const Late&, float (&v)[8]) {
-        if (o.row + row < o.end && o.col + col < p.y.cols) store_rows(p.y, o.row + row, o.col + col, v);
+        if (o.y.vector && wanted(p, o, row, col)) store_rows(o.y, row, col, v);
+    }
+    __device__ static void store_one(const Params& p, const Out& o, int row, int col, float v) {
+        if (wanted(p, o, row, col)) store_as(o.y, row, col, v);
     }
     __device__ static void fetch_late(const Params&, const Out&, int, int, Late&) {}
     __device__ static void mirror(const Params&, const Out&, int, int, const float (&)[8]) {}
@@ -211,9 +234,8 @@ struct ExpertOuter {
         float v[ADD ? 8 : 1];
     };
     struct Out {
-        char* data;
-        int32_t row, col;
-        bool skip;
+        RowsAt dw;      // from the first row and column of the CTA's part
+        int32_t rows;   // of dw, from there
     };
     __device__ static bool bf16(const Params& p) { return p.is_bf16; }
     __device__ static void prepare(const Params& p, unsigned char* table) {
@@ -240,32 +262,33 @@ struct ExpertOuter {
         int32_t m, n;
         banded(t - e * per, p.tiles_m, p.tiles_n, &m, &n);
         const Groups* g = reinterpret_cast<const Groups*>(table);
-        const int size = p.dw.dtype == ADAMW_DTYPE_FP32 ? 4 : 2;
-        return {p.dw.data + e * p.stride * size, m * S::kRows + int32_t(rank) * kRowsOfCta, n * S::kCols,
-                ADD && g->bounds[e + 2] == g->bounds[e + 1]};
-    }
-    __device__ static bool inside(const Params& p, const Out& o, int row, int col) {
-        return o.row + row < p.n && o.col + col < p.dw.cols;
-    }
-    __device__ static bool wanted(const Params& p, const Out& o, int row, int col) { return !o.skip && inside(p, o, row, col); }
-    __device__ static bool mirrored(const Out&) { return false; }
-    __device__ static RowsAt rows(const Params& p, const Out& o) {
         RowsAt r = p.dw;
-        r.data = o.data;
-        return r;
+        r.data += e * p.stride * (r.dtype == ADAMW_DTYPE_FP32 ? 4 : 2);
+        const int32_t row = m * S::kRows + int32_t(rank) * kRowsOfCta;
+        // nothing to add: the sums stay as they are
+        const bool skip = ADD && g->bounds[e + 2] == g->bounds[e + 1];
+        return {part_of(r, row, n * S::kCols), skip ? 0 : p.n - row};
     }
+    __device__ static bool wanted(const Params&, const Out& o, int row, int col) { return row < o.rows && col < o.dw.cols; }
+    __device__ static bool mirrored(const Out&) { return false; }
+    __device__ static bool scalar(const Out& o) { return !o.dw.vector; }
     __device__ static void fetch(const Params& p, const Out& o, int row, int col, Extra& x) {
         if constexpr (ADD) {
-            if (inside(p, o, row, col)) load_rows(rows(p, o), o.row + row, o.col + col, x.v);
+            if (o.dw.vector && wanted(p, o, row, col)) load_rows(o.dw, row, col, x.v);
         }
     }
     __device__ static void store(const Params& p, const Out& o, int row, int col, const Extra& x, const Late&, float (&v)[8]) {
-        if (!inside(p, o, row, col)) return;
+        if (!o.dw.vector || !wanted(p, o, row, col)) return;
         if constexpr (ADD) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] += x.v[i];
         }
-        store_rows(rows(p, o), o.row + row, o.col + col, v);
+        store_rows(o.dw, row, col, v);
+    }
+    __device__ static void store_one(const Params& p, const Out& o, int row, int col, float v) {
+        if (!wanted(p, o, row, col)) return;
+        if constexpr (ADD) v += load_as(o.dw, row, col);
+        store_as(o.dw, row, col, v);
     }
     __device__ static void fetch_late(const Params&, const Out&, int, int, Late&) {}
     __device__ static void mirror(const Params&, const Out&, int, int, const float (&)[8]) {}
@@ -343,9 +366,10 @@ bool readable(adamw_matrices_t* m, char** workspace, cudaStream_t st) {
     return true;
 }
 
-bool map_of(CUtensorMap* map, const adamw_matrices_t& m, bool mn) {
+// rows: what a CTA loads of a K-major operand at a time.
+bool map_of(CUtensorMap* map, const adamw_matrices_t& m, bool mn, int rows) {
     return tensor_map(map, m.dtype == ADAMW_DTYPE_BF16, m.data, m.batch, m.rows, m.cols, m.row_stride, m.batch_stride,
-                      mn ? kStepK : kRowsOfCta);
+                      mn ? kStepK : rows);
 }
 
 RowsAt rows_of(const adamw_matrices_t& m) {
@@ -395,7 +419,7 @@ int rows_call(const adamw_matrices_t& x, const adamw_matrices_t& w, bool transpo
     typename P::Params p;
     memset(&p, 0, sizeof p);
     // sums of nothing read no operand
-    if (x.cols > 0 && (!map_of(&p.x, x, false) || !map_of(&p.w, w, transposed))) return ADAMW_ERR_CUDA;
+    if (x.cols > 0 && (!map_of(&p.x, x, false, kRowsOfCta) || !map_of(&p.w, w, transposed, S::kBRows))) return ADAMW_ERR_CUDA;
     p.offsets = offsets;
     p.rows = x.rows;
     p.experts = int32_t(w.batch);
@@ -413,7 +437,7 @@ int outer_call(const adamw_matrices_t& dy, const adamw_matrices_t& x, const int6
     using P = ExpertOuter<S, ADD>;
     typename P::Params p;
     memset(&p, 0, sizeof p);
-    if (x.rows > 0 && (!map_of(&p.dy, dy, true) || !map_of(&p.x, x, true))) return ADAMW_ERR_CUDA;
+    if (x.rows > 0 && (!map_of(&p.dy, dy, true, 0) || !map_of(&p.x, x, true, 0))) return ADAMW_ERR_CUDA;
     p.offsets = offsets;
     p.rows = x.rows;
     p.experts = int32_t(dw.batch);
@@ -461,20 +485,28 @@ extern "C" int adamw_expert_rows(const adamw_matrices_t* x, const adamw_matrices
     if (bytes > 0 && !workspace) return ADAMW_ERR_INVALID_ARG;
     if (bytes > 0 && !aligned(workspace, 256)) return ADAMW_ERR_MISALIGNED;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    // at most: every group's last tile is a partial one
+    // the grid covers the most tiles that the groups can have: one partial in each
     const int64_t groups = w->batch + 2;
-    const int64_t pair_tiles = (x->rows / PairTile::kRows + groups) * up(n, PairTile::kCols);
-    const int64_t single_tiles = (x->rows / SingleTile::kRows + groups) * up(n, SingleTile::kCols);
-    if (single_tiles > kMaxCount) return ADAMW_ERR_TOO_LARGE;
+    auto most = [&](int rows, int cols) { return (x->rows / rows + groups) * up(n, cols); };
+    if (most(SingleTile::kRows, SingleTile::kCols) > kMaxCount) return ADAMW_ERR_TOO_LARGE;
     TileUnits units;
     if (!launched(units_of<ExpertRows<PairTile>>(&units), "tile units")) return ADAMW_ERR_CUDA;
     adamw_matrices_t a = *x, b = *w;
     char* at = static_cast<char*>(workspace);
     if (!readable(&a, &at, st) || !readable(&b, &at, st)) return ADAMW_ERR_CUDA;
-    // few rows for each expert leave most of a pair's tile empty, and few tiles leave SMs idle
-    const bool pair = x->rows >= w->batch * 128 && pair_tiles - groups * up(n, PairTile::kCols) >= units.pairs;
-    return pair ? rows_call<PairTile>(a, b, transposed != 0, offsets, *y, pair_tiles, units.pairs, st)
-                : rows_call<SingleTile>(a, b, transposed != 0, offsets, *y, single_tiles, units.sms, st);
+    // what groups of one size would have
+    const int64_t each = up(x->rows, w->batch), used = std::min(w->batch, x->rows);
+    auto likely = [&](int rows, int cols) { return used * up(each, rows) * up(n, cols); };
+    const TileChoice choice = {{likely(PairTile::kRows, PairTile::kCols), likely(HalfTile::kRows, HalfTile::kCols),
+                                likely(SingleTile::kRows, SingleTile::kCols)}};
+    switch (choose_shape(choice, up(k, kStepK), units.pairs, units.sms)) {
+        case kPairShape:
+            return rows_call<PairTile>(a, b, transposed != 0, offsets, *y, most(PairTile::kRows, PairTile::kCols), units.pairs, st);
+        case kHalfShape:
+            return rows_call<HalfTile>(a, b, transposed != 0, offsets, *y, most(HalfTile::kRows, HalfTile::kCols), units.pairs, st);
+        default:
+            return rows_call<SingleTile>(a, b, transposed != 0, offsets, *y, most(SingleTile::kRows, SingleTile::kCols), units.sms, st);
+    }
 }
 
 extern "C" int adamw_expert_outer(const adamw_matrices_t* dy, const adamw_matrices_t* x, const int64_t* offsets,
@@ -493,17 +525,23 @@ extern "C" int adamw_expert_outer(const adamw_matrices_t* dy, const adamw_matric
     if (bytes > 0 && !workspace) return ADAMW_ERR_INVALID_ARG;
     if (bytes > 0 && !aligned(workspace, 256)) return ADAMW_ERR_MISALIGNED;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const int64_t pair_tiles = dw->batch * up(dw->rows, PairTile::kRows) * up(dw->cols, PairTile::kCols);
-    const int64_t single_tiles = dw->batch * up(dw->rows, SingleTile::kRows) * up(dw->cols, SingleTile::kCols);
-    if (single_tiles > kMaxCount) return ADAMW_ERR_TOO_LARGE;
+    auto tiles = [&](int rows, int cols) { return dw->batch * up(dw->rows, rows) * up(dw->cols, cols); };
+    if (tiles(SingleTile::kRows, SingleTile::kCols) > kMaxCount) return ADAMW_ERR_TOO_LARGE;
     TileUnits units;
     if (!launched(units_of<ExpertOuter<PairTile, false>>(&units), "tile units")) return ADAMW_ERR_CUDA;
     adamw_matrices_t a = *dy, b = *x;
     char* at = static_cast<char*>(workspace);
     if (!readable(&a, &at, st) || !readable(&b, &at, st)) return ADAMW_ERR_CUDA;
-    if (pair_tiles >= units.pairs)
-        return accumulate ? outer_call<PairTile, true>(a, b, offsets, *dw, pair_tiles, units.pairs, st)
-                          : outer_call<PairTile, false>(a, b, offsets, *dw, pair_tiles, units.pairs, st);
-    return accumulate ? outer_call<SingleTile, true>(a, b, offsets, *dw, single_tiles, units.sms, st)
-                      : outer_call<SingleTile, false>(a, b, offsets, *dw, single_tiles, units.sms, st);
+    const TileChoice choice = {{tiles(PairTile::kRows, PairTile::kCols), tiles(HalfTile::kRows, HalfTile::kCols),
+                                tiles(SingleTile::kRows, SingleTile::kCols)}};
+    const int shape = choose_shape(choice, up(up(dy->rows, dw->batch), kStepK), units.pairs, units.sms);
+    const int64_t n = choice.tiles[shape];
+    if (shape == kPairShape)
+        return accumulate ? outer_call<PairTile, true>(a, b, offsets, *dw, n, units.pairs, st)
+                          : outer_call<PairTile, false>(a, b, offsets, *dw, n, units.pairs, st);
+    if (shape == kHalfShape)
+        return accumulate ? outer_call<HalfTile, true>(a, b, offsets, *dw, n, units.pairs, st)
+                          : outer_call<HalfTile, false>(a, b, offsets, *dw, n, units.pairs, st);
+    return accumulate ? outer_call<SingleTile, true>(a, b, offsets, *dw, n, units.sms, st)
+                      : outer_call<SingleTile, false>(a, b, offsets, *dw, n, units.sms, st);
 }

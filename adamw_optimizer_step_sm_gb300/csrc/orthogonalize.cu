@@ -64,7 +64,8 @@ struct Batch {
 };
 
 constexpr int kNormThreads = 256;
-constexpr int kPieceVecs = 2048;   // vectors of eight elements that a CTA takes
+constexpr int kPieceVecs = 4096;   // vectors of eight elements that a CTA takes
+constexpr int kBatch = 4;          // of them in flight in a thread
 
 struct CopyShape {
     Shape s;
@@ -86,33 +87,13 @@ struct CopyParams {
     const MuonMatrix* table;
     const adamw_muon_hparams_t* hp;
     int32_t* nonfinite;
-    int32_t nesterov, momentum_bf16;
+    int32_t nesterov;
 };
 
-__device__ __forceinline__ void load8_any(const char* data, int64_t at, int32_t dtype, bool vector, int n, float (&v)[8]) {
-    if (dtype == ADAMW_DTYPE_FP32) {
-        using E = Elem<ADAMW_DTYPE_FP32>;
-        if (vector && n >= 8) {
-            E::unpack(*reinterpret_cast<const uint4*>(data + at * 4), v);
-            E::unpack(*reinterpret_cast<const uint4*>(data + at * 4 + 16), v + 4);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = i < n ? E::load(data, at + i) : 0.0f;
-        }
-    } else if (dtype == ADAMW_DTYPE_BF16) {
-        using E = Elem<ADAMW_DTYPE_BF16>;
-        if (vector && n >= 8) E::unpack(*reinterpret_cast<const uint4*>(data + at * 2), v);
-        else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = i < n ? E::load(data, at + i) : 0.0f;
-        }
-    } else {
-        if (vector && n >= 8) Fp16::unpack(*reinterpret_cast<const uint4*>(data + at * 2), v);
-        else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = i < n ? Fp16::load(data, at + i) : 0.0f;
-        }
-    }
+__device__ __forceinline__ void store_as(char* data, int64_t at, int32_t dtype, float v) {
+    if (dtype == ADAMW_DTYPE_FP32) Elem<ADAMW_DTYPE_FP32>::store(data, at, v);
+    else if (dtype == ADAMW_DTYPE_BF16) Elem<ADAMW_DTYPE_BF16>::store(data, at, v);
+    else Fp16::store(data, at, v);
 }
 __device__ __forceinline__ void store8_any(char* data, int64_t at, int32_t dtype, bool vector, int n, const float (&v)[8]) {
     if (dtype == ADAMW_DTYPE_FP32) {
@@ -143,46 +124,90 @@ __device__ __forceinline__ void store8_any(char* data, int64_t at, int32_t dtype
     }
 }
 
+// What eight elements are read as, so that several vectors' loads are in flight
+// before the first is looked at: the source (DT), or the gradient in c and the
+// momentum (DT) in a and b.
+struct Raw {
+    uint4 a, b, c;
+};
+
+template <int DT>
+__device__ __forceinline__ void load_raw(const char* data, int64_t at, bool vector, int n, uint4* a, uint4* b) {
+    using E = Elem<DT>;
+    const char* p = data + at * E::kSize;
+    if (vector) {
+        *a = *reinterpret_cast<const uint4*>(p);
+        if (E::kSize == 4) *b = *reinterpret_cast<const uint4*>(p + 16);
+        return;
+    }
+    if (E::kSize == 4) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = i < n ? reinterpret_cast<const uint32_t*>(p)[i] : 0;
+        *a = make_uint4(w[0], w[1], w[2], w[3]);
+        *b = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = i < n ? reinterpret_cast<const uint16_t*>(p)[i] : 0;
+        *a = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+    }
+}
+template <int DT>
+__device__ __forceinline__ void unpack_raw(uint4 a, uint4 b, float (&v)[8]) {
+    Elem<DT>::unpack(a, v);
+    if (Elem<DT>::kSize == 4) Elem<DT>::unpack(b, v + 4);
+}
+
 // Eight elements of what is orthogonalised: the source, or the step's update
 // of gradient and momentum (then the new momentum in `m`).
-template <bool MUON>
+template <bool MUON, int DT>
 struct Source {
-    const CopyParams<MUON>& p;
-    const CopyShape& c;
-    MuonMatrix t;
-    const char* data;
+    const char *data, *grad;
+    int64_t ld;
+    int32_t cols;
     float mu;
-    bool vector;
-    __device__ Source(const CopyParams<MUON>& p, const CopyShape& c, int matrix) : p(p), c(c) {
+    bool vector, nesterov;
+    __device__ Source(const CopyParams<MUON>& p, const CopyShape& c, int matrix) {
+        cols = c.s.cols;
         if (MUON) {
-            t = p.table[c.s.first + matrix];
+            const MuonMatrix t = p.table[c.s.first + matrix];
+            data = static_cast<const char*>(t.momentum);
+            grad = reinterpret_cast<const char*>(t.grad);
+            ld = cols;
             mu = p.hp->momentum;
-            vector = c.s.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(t.grad) | reinterpret_cast<uintptr_t>(t.momentum)) % 16 == 0;
+            nesterov = p.nesterov != 0;
+            vector = cols % 8 == 0 && (reinterpret_cast<uintptr_t>(data) | reinterpret_cast<uintptr_t>(grad)) % 16 == 0;
         } else {
-            const int size = p.src.dtype == ADAMW_DTYPE_FP32 ? 4 : 2;
-            data = p.src.data + matrix * p.src.batch_stride * size;
+            data = p.src.data + matrix * p.src.batch_stride * Elem<DT>::kSize;
+            ld = p.src.row_stride;
             vector = p.src.vector != 0;
         }
     }
-    __device__ __forceinline__ void get(int row, int col, float (&u)[8], float (&m)[8]) const {
-        const int n = c.s.cols - col;
+    // a row's last vector may be a part of one
+    __device__ __forceinline__ Raw load(int row, int col) const {
+        Raw r;
+        const int64_t at = row * ld + col;
+        const int n = cols - col;
+        load_raw<DT>(data, at, vector && n >= 8, n, &r.a, &r.b);
+        if (MUON) load_raw<ADAMW_DTYPE_BF16>(grad, at, vector, n, &r.c, &r.c);
+        return r;
+    }
+    __device__ __forceinline__ void value(const Raw& r, float (&u)[8], float (&m)[8]) const {
         if (MUON) {
-            const int64_t at = int64_t(row) * c.s.cols + col;
-            load8_any(reinterpret_cast<const char*>(t.grad), at, ADAMW_DTYPE_BF16, vector, n, u);
-            load8_any(static_cast<const char*>(t.momentum), at, p.momentum_bf16 ? ADAMW_DTYPE_BF16 : ADAMW_DTYPE_FP32, vector, n, m);
+            unpack_raw<DT>(r.a, r.b, m);
+            unpack_raw<ADAMW_DTYPE_BF16>(r.c, r.c, u);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 m[i] = fmaf(1.0f - mu, u[i] - m[i], m[i]);
-                u[i] = p.nesterov ? fmaf(mu, m[i] - u[i], u[i]) : m[i];
+                u[i] = nesterov ? fmaf(mu, m[i] - u[i], u[i]) : m[i];
             }
         } else {
-            load8_any(data, row * p.src.row_stride + col, p.src.dtype, vector, n, u);
+            unpack_raw<DT>(r.a, r.b, u);
         }
     }
     __device__ __forceinline__ void put(int row, int col, const float (&m)[8]) const {
-        if (MUON)
-            store8_any(static_cast<char*>(t.momentum), int64_t(row) * c.s.cols + col,
-                       p.momentum_bf16 ? ADAMW_DTYPE_BF16 : ADAMW_DTYPE_FP32, vector, c.s.cols - col, m);
+        if (MUON) store8_any(const_cast<char*>(data), row * ld + col, DT, vector, cols - col, m);
     }
 };
 
@@ -219,46 +244,44 @@ struct Walk {
 
 // Sum of squares of each piece.  Eight squares are summed in fp32 and added
 // error-free; squares that leave fp32's comfortable range are taken in fp64.
-template <bool MUON>
+template <bool MUON, int DT>
 __global__ void __launch_bounds__(kNormThreads) norm_kernel(const __grid_constant__ CopyParams<MUON> p) {
     __shared__ double part[kNormThreads / 32];
     int32_t i = int32_t(blockIdx.x), matrix;
     const CopyShape& c = piece_of(p, &i, &matrix);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Source<MUON> src(p, c, matrix);
+    const Source<MUON, DT> src(p, c, matrix);
     const Walk walk(c.s, i);
     Sum2 total = {0.0f, 0.0f};
     double sum = 0.0;
-    constexpr int kBatch = MUON ? 2 : 4;   // vectors in flight
 #pragma unroll 1
     for (int k = 0; k < kPieceVecs / kNormThreads; k += kBatch) {
-        float u[kBatch][8], m[8];
+        Raw raw[kBatch];
+        bool in[kBatch];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             int32_t row, col;
-            if (walk.at((k + b) * kNormThreads + int(threadIdx.x), &row, &col)) {
-                src.get(row, col, u[b], m);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) u[b][e] = 0.0f;
-            }
+            in[b] = walk.at((k + b) * kNormThreads + int(threadIdx.x), &row, &col);
+            if (in[b]) raw[b] = src.load(row, col);
         }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            float s = 0.0f;
+            if (!in[b]) continue;
+            float u[8], m[8];
+            src.value(raw[b], u, m);
+            float s = 0.0f, any = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s = fmaf(u[b][e], u[b][e], s);
+            for (int e = 0; e < 8; ++e) s = fmaf(u[e], u[e], s);
             if (s >= 0x1p-100f && s <= 0x1p100f) {
                 total.add(s);
-            } else {
-                float any = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) any = any == 0.0f ? u[b][e] : any;
-                if (any == 0.0f) continue;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum += double(u[b][e]) * double(u[b][e]);
+                continue;
             }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) any = any == 0.0f ? u[e] : any;
+            if (any == 0.0f) continue;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum += double(u[e]) * double(u[e]);
         }
     }
     sum += double(total.hi) + double(total.lo);
@@ -285,7 +308,7 @@ __device__ __forceinline__ void split8(const float (&x)[8], uint4* hi, uint4* lo
 }
 
 // The scaled copies; a plan's new momentum.
-template <bool MUON>
+template <bool MUON, int DT>
 __global__ void __launch_bounds__(kNormThreads) copy_kernel(const __grid_constant__ CopyParams<MUON> p) {
     __shared__ double part[kNormThreads / 32];
     int32_t i = int32_t(blockIdx.x), matrix;
@@ -305,34 +328,49 @@ __global__ void __launch_bounds__(kNormThreads) copy_kernel(const __grid_constan
     const double norm = sqrt(sum);
     // NaN for a sum that is not finite: the matrix has no direction
     const float by = sum <= 1.7976931348623157e308 ? float(double(kScale) / (norm > p.eps ? norm : double(p.eps))) : sqrtf(-1.0f);
-    const Source<MUON> src(p, c, matrix);
+    const Source<MUON, DT> src(p, c, matrix);
     const Walk walk(c.s, i);
     uint4* hi = reinterpret_cast<uint4*>(c.hi + matrix * c.s.stride) + int64_t(i) * kPieceVecs;
     uint4* lo = reinterpret_cast<uint4*>(c.lo + matrix * c.s.stride) + int64_t(i) * kPieceVecs;
-    constexpr int kBatch = MUON ? 2 : 4;
 #pragma unroll 1
     for (int k = 0; k < kPieceVecs / kNormThreads; k += kBatch) {
-        float u[kBatch][8], m[MUON ? kBatch : 1][8];
+        Raw raw[kBatch];
         int32_t row[kBatch], col[kBatch];
         bool in[kBatch];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             in[b] = walk.at((k + b) * kNormThreads + int(threadIdx.x), &row[b], &col[b]);
-            if (in[b]) src.get(row[b], col[b], u[b], m[MUON ? b : 0]);
+            if (in[b]) raw[b] = src.load(row[b], col[b]);
         }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             if (!in[b]) continue;
-            if (MUON && !skip) src.put(row[b], col[b], m[b]);
+            float u[8], m[8];
+            src.value(raw[b], u, m);
+            if (MUON && !skip) src.put(row[b], col[b], m);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) u[b][e] *= by;
+            for (int e = 0; e < 8; ++e) u[e] *= by;
             uint4 h, l;
-            split8(u[b], &h, &l);
+            split8(u, &h, &l);
             const int at = (k + b) * kNormThreads + int(threadIdx.x);   // the copy's rows are whole vectors
             hi[at] = h;
             lo[at] = l;
         }
     }
+}
+
+// By the type of the source, or of the momentum.
+template <bool MUON>
+using CopyKernel = void (*)(CopyParams<MUON>);
+template <bool MUON>
+CopyKernel<MUON> norm_of(int32_t dtype) {
+    return dtype == ADAMW_DTYPE_FP32 ? norm_kernel<MUON, ADAMW_DTYPE_FP32>
+           : dtype == ADAMW_DTYPE_BF16 ? norm_kernel<MUON, ADAMW_DTYPE_BF16> : norm_kernel<MUON, MUON ? ADAMW_DTYPE_BF16 : ADAMW_DTYPE_FP16>;
+}
+template <bool MUON>
+CopyKernel<MUON> copy_of(int32_t dtype) {
+    return dtype == ADAMW_DTYPE_FP32 ? copy_kernel<MUON, ADAMW_DTYPE_FP32>
+           : dtype == ADAMW_DTYPE_BF16 ? copy_kernel<MUON, ADAMW_DTYPE_BF16> : copy_kernel<MUON, MUON ? ADAMW_DTYPE_BF16 : ADAMW_DTYPE_FP16>;
 }
 
 // ---------------------------------------------------------------- products --
@@ -371,23 +409,28 @@ struct Product {
     // epilogue longer than its products.
     static constexpr int kWarps = 8;
     static constexpr bool kSymmetric = KIND == kGram || KIND == kPoly;
-    static_assert(!kSymmetric || S::kRows == S::kCols, "symmetric products take square tiles");
+    // tiles of columns to a tile of rows
+    static constexpr int kRatio = S::kRows / S::kCols;
 
     // what the epilogue adds to the product
     struct Extra {
         uint4 hi, lo;
     };
     struct Late {
-        float w[KIND == kUpdate ? 8 : 1];   // the master
+        float4 w[KIND == kUpdate ? 2 : 1];   // the master
     };
     struct Out {
-        const ProductShape* p;
+        // by value: read through a pointer to the arguments, each of these cost
+        // a trip to L1 in every vector
+        int32_t m, n, ld, cols;
         int32_t matrix, row, col;   // of the CTA's part
         bool mirrored, vector, skip;
         uint16_t *out, *lo;
         const uint16_t* hi;
-        MuonMatrix t;
-        float decay, rate;
+        char *dst, *param;          // the result, or the master and the parameter
+        int64_t dst_ld;
+        int32_t dst_type;
+        float decay, rate, a, b, c;
     };
     __device__ static bool bf16(const Params&) { return false; }
     __device__ static void prepare(const Params&, unsigned char*) {}
@@ -400,12 +443,13 @@ struct Product {
         *matrix = t / c.per;
         t -= *matrix * c.per;
         if (kSymmetric) {
-            // row by row of the lower triangle: row r has r + 1 tiles
-            int32_t r = int32_t((sqrtf(8.0f * float(t) + 1.0f) - 1.0f) * 0.5f);
-            while (r * (r + 1) / 2 > t) --r;
-            while ((r + 1) * (r + 2) / 2 <= t) ++r;
+            // row by row of the lower triangle, its diagonal in squares: row r
+            // has kRatio (r + 1) tiles
+            int32_t r = int32_t((sqrtf(8.0f / kRatio * float(t) + 1.0f) - 1.0f) * 0.5f);
+            while (kRatio * r * (r + 1) / 2 > t) --r;
+            while (kRatio * (r + 1) * (r + 2) / 2 <= t) ++r;
             *m = r;
-            *n = t - r * (r + 1) / 2;
+            *n = t - kRatio * r * (r + 1) / 2;
         } else {
             // bands of eight tiles of rows, for reuse in L2
             const int32_t band = t / (8 * c.tiles_n), left = c.tiles_m - band * 8, h = left < 8 ? left : 8;
@@ -433,18 +477,33 @@ struct Product {
         Out o;
         int32_t m, n;
         const ProductShape& c = find(p, t, &o.matrix, &m, &n);
-        o.p = &c;
+        o.m = c.m;
+        o.n = c.n;
+        o.ld = kSymmetric ? c.s.small_ld : c.s.ld;
+        o.cols = c.s.cols;
         o.row = m * S::kRows + int32_t(rank) * kRowsOfCta;
         o.col = n * S::kCols;
-        o.mirrored = kSymmetric && m != n;
+        o.mirrored = kSymmetric && m != n / kRatio;
         o.skip = false;
+        o.vector = true;
+        o.a = p.a;
+        o.b = p.b;
+        o.c = p.c * kUnscale;
         const int64_t at = o.matrix * (kSymmetric ? c.s.small_stride : c.s.stride);
         o.out = c.out + at;
         o.hi = c.hi + at;
         o.lo = c.lo + at;
-        if constexpr (KIND == kUpdate) {
-            o.t = p.table[c.s.first + o.matrix];
-            o.vector = c.s.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(o.t.master) | reinterpret_cast<uintptr_t>(o.t.param)) % 16 == 0;
+        if constexpr (KIND == kResult) {
+            o.dst_type = p.dst.dtype;
+            o.dst = p.dst.data + o.matrix * p.dst.batch_stride * (o.dst_type == ADAMW_DTYPE_FP32 ? 4 : 2);
+            o.dst_ld = p.dst.row_stride;
+            o.vector = p.dst.vector != 0;
+        } else if constexpr (KIND == kUpdate) {
+            const MuonMatrix t = p.table[c.s.first + o.matrix];
+            o.dst = reinterpret_cast<char*>(t.master);
+            o.param = reinterpret_cast<char*>(t.param);
+            o.dst_ld = c.s.cols;
+            o.vector = c.s.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(t.master) | reinterpret_cast<uintptr_t>(t.param)) % 16 == 0;
             o.skip = *p.nonfinite != 0;
             const float lr = p.hp->lr;
             o.decay = 1.0f - lr * p.hp->weight_decay;
@@ -452,39 +511,48 @@ struct Product {
         }
         return o;
     }
-    __device__ static int ld(const Out& o) { return kSymmetric ? o.p->s.small_ld : o.p->s.ld; }
     __device__ static bool wanted(const Params&, const Out& o, int row, int col) {
-        return !o.skip && o.row + row < o.p->m && o.col + col < o.p->n;
+        return !o.skip && o.row + row < o.m && o.col + col < o.n;
     }
     __device__ static bool mirrored(const Out& o) { return o.mirrored; }
     __device__ static void fetch(const Params& p, const Out& o, int row, int col, Extra& x) {
         if (KIND == kGram || !wanted(p, o, row, col)) return;
-        const int64_t at = int64_t(o.row + row) * ld(o) + o.col + col;
+        const int64_t at = int64_t(o.row + row) * o.ld + o.col + col;
         x.hi = *reinterpret_cast<const uint4*>(o.hi + at);
         if (!kSymmetric) x.lo = *reinterpret_cast<const uint4*>(o.lo + at);
     }
     __device__ static void fetch_late(const Params& p, const Out& o, int row, int col, Late& x) {
         if constexpr (KIND == kUpdate) {
-            if (wanted(p, o, row, col))
-                load8_any(reinterpret_cast<const char*>(o.t.master), int64_t(o.row + row) * o.p->s.cols + o.col + col,
-                          ADAMW_DTYPE_FP32, o.vector, o.p->s.cols - o.col - col, x.w);
+            if (o.vector && wanted(p, o, row, col)) {
+                const float4* w = reinterpret_cast<const float4*>(o.dst + (int64_t(o.row + row) * o.dst_ld + o.col + col) * 4);
+                x.w[0] = w[0];
+                x.w[1] = w[1];
+            }
         }
     }
+    // Results whose rows are not whole vectors go element by element.
+    __device__ static bool scalar(const Out& o) { return (KIND == kResult || KIND == kUpdate) && !o.vector; }
     __device__ static void store(const Params& p, const Out& o, int row, int col, const Extra& x, const Late& y, float (&v)[8]) {
         const bool here = wanted(p, o, row, col);
-        const int64_t at = int64_t(o.row + row) * ld(o) + o.col + col;
-        if constexpr (kSymmetric) {
-            float g[8];
-            if (KIND == kPoly && here) Fp16::unpack(x.hi, g);
+        const int64_t at = int64_t(o.row + row) * o.ld + o.col + col;
+        if constexpr (KIND == kGram) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = KIND == kPoly ? (here ? fmaf(p.b, g[e], p.c * kUnscale * v[e]) : 0.0f) : v[e] * kUnscale;
+            for (int e = 0; e < 8; ++e) v[e] *= kUnscale;
             if (here) *reinterpret_cast<uint4*>(o.out + at) = Fp16::pack(v);
-        } else if (here) {
+        } else if constexpr (KIND == kPoly) {
+            if (!here) return;   // rows beyond the matrix: nothing mirrors them
+            float g[8];
+            Fp16::unpack(x.hi, g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = fmaf(o.b, g[e], o.c * v[e]);
+            *reinterpret_cast<uint4*>(o.out + at) = Fp16::pack(v);
+        } else {
+            if (!here) return;
             float h[8], l[8];
             Fp16::unpack(x.hi, h);
             Fp16::unpack(x.lo, l);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = fmaf(p.a, fmaf(l[e], 1.0f / kLow, h[e]), v[e] * kUnscale);
+            for (int e = 0; e < 8; ++e) v[e] = fmaf(o.a, fmaf(l[e], 1.0f / kLow, h[e]), v[e] * kUnscale);
             if constexpr (KIND == kApply) {
                 uint4 hi, lo;
                 split8(v, &hi, &lo);
@@ -493,22 +561,34 @@ struct Product {
             } else if constexpr (KIND == kResult) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] *= kUnscale;
-                const int64_t to = o.matrix * p.dst.batch_stride + int64_t(o.row + row) * p.dst.row_stride + o.col + col;
-                store8_any(p.dst.data, to, p.dst.dtype, p.dst.vector, o.p->s.cols - o.col - col, v);
-            } else {
-                const int64_t to = int64_t(o.row + row) * o.p->s.cols + o.col + col;
-                const int n = o.p->s.cols - o.col - col;
+                if (o.vector)
+                    store8_any(o.dst, int64_t(o.row + row) * o.dst_ld + o.col + col, o.dst_type, true, o.cols - o.col - col, v);
+            } else if (o.vector) {
+                const float* w = reinterpret_cast<const float*>(y.w);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = fmaf(-o.rate, v[e], o.decay * y.w[e]);
-                store8_any(reinterpret_cast<char*>(o.t.master), to, ADAMW_DTYPE_FP32, o.vector, n, v);
-                store8_any(reinterpret_cast<char*>(o.t.param), to, ADAMW_DTYPE_BF16, o.vector, n, v);
+                for (int e = 0; e < 8; ++e) v[e] = fmaf(-o.rate, v[e], o.decay * w[e]);
+                const int64_t to = int64_t(o.row + row) * o.dst_ld + o.col + col;
+                store8_any(o.dst, to, ADAMW_DTYPE_FP32, true, 8, v);
+                store8_any(o.param, to, ADAMW_DTYPE_BF16, true, 8, v);
             }
+        }
+    }
+    __device__ static void store_one(const Params& p, const Out& o, int row, int col, float v) {
+        if (!wanted(p, o, row, col)) return;
+        const int64_t to = int64_t(o.row + row) * o.dst_ld + o.col + col;
+        if constexpr (KIND == kResult) {
+            store_as(o.dst, to, o.dst_type, v);
+        } else if constexpr (KIND == kUpdate) {
+            float* w = reinterpret_cast<float*>(o.dst) + to;
+            v = fmaf(-o.rate, v, o.decay * *w);
+            *w = v;
+            store_as(o.param, to, ADAMW_DTYPE_BF16, v);
         }
     }
     // rows row .. row + 7 of column col, as a row of the mirrored tile
     __device__ static void mirror(const Params&, const Out& o, int col, int row, const float (&v)[8]) {
-        if (!kSymmetric || o.col + col >= o.p->n || o.row + row >= o.p->m) return;
-        *reinterpret_cast<uint4*>(o.out + int64_t(o.col + col) * ld(o) + o.row + row) = Fp16::pack(v);
+        if (!kSymmetric || o.col + col >= o.n || o.row + row >= o.m) return;
+        *reinterpret_cast<uint4*>(o.out + int64_t(o.col + col) * o.ld + o.row + row) = Fp16::pack(v);
     }
 };
 
@@ -557,6 +637,15 @@ struct Group {
     float rate[kMaxShapes];
 };
 
+// Tiles of a matrix.
+template <class S>
+int64_t tiles_of(const Shape& s, int kind) {
+    const int64_t side = s.side;
+    if (kind != kGram && kind != kPoly) return (up(s.rows, S::kRows) / S::kRows) * (up(s.cols, S::kCols) / S::kCols);
+    const int64_t m = up(side, S::kRows) / S::kRows, n = up(side, S::kCols) / S::kCols, ratio = S::kRows / S::kCols;
+    return ratio * m * (m + 1) / 2 - (ratio * m - n);   // the last row may end earlier
+}
+
 // The products' arguments, but for the coefficients.  which: X's buffer.
 template <class S>
 bool fill(const Group& g, int kind, int which, ProductParams* p) {
@@ -575,13 +664,13 @@ bool fill(const Group& g, int kind, int which, ProductParams* p) {
             q.a_mn = q.b_mn = !wide;
             q.m = q.n = s.side;
             q.k = wide ? s.cols : s.rows;
-            ok = tensor_map(&q.a, false, b.x[which], s.count, s.rows, s.cols, s.ld, s.stride, wide ? kRowsOfCta : kStepK);
-            q.b = q.a;
+            ok = tensor_map(&q.a, false, b.x[which], s.count, s.rows, s.cols, s.ld, s.stride, wide ? kRowsOfCta : kStepK) &&
+                 tensor_map(&q.b, false, b.x[which], s.count, s.rows, s.cols, s.ld, s.stride, wide ? S::kBRows : kStepK);
             q.out = b.gram;
         } else if (kind == kPoly) {
             q.m = q.n = q.k = s.side;
-            ok = tensor_map(&q.a, false, b.gram, s.count, s.side, s.side, s.small_ld, s.small_stride, kRowsOfCta);
-            q.b = q.a;
+            ok = tensor_map(&q.a, false, b.gram, s.count, s.side, s.side, s.small_ld, s.small_stride, kRowsOfCta) &&
+                 tensor_map(&q.b, false, b.gram, s.count, s.side, s.side, s.small_ld, s.small_stride, S::kBRows);
             q.hi = b.gram;
             q.out = b.poly;
         } else {
@@ -590,7 +679,8 @@ bool fill(const Group& g, int kind, int which, ProductParams* p) {
             q.k = s.side;
             q.b_mn = wide;
             ok = tensor_map(wide ? &q.b : &q.a, false, b.x[which], s.count, s.rows, s.cols, s.ld, s.stride, wide ? kStepK : kRowsOfCta) &&
-                 tensor_map(wide ? &q.a : &q.b, false, b.poly, s.count, s.side, s.side, s.small_ld, s.small_stride, kRowsOfCta);
+                 tensor_map(wide ? &q.a : &q.b, false, b.poly, s.count, s.side, s.side, s.small_ld, s.small_stride,
+                            wide ? kRowsOfCta : S::kBRows);
             q.hi = b.x[which];
             q.lo = b.lo;
             q.out = b.x[which ^ 1];
@@ -598,7 +688,7 @@ bool fill(const Group& g, int kind, int which, ProductParams* p) {
         if (!ok) return false;
         q.tiles_m = int32_t(up(q.m, S::kRows) / S::kRows);
         q.tiles_n = int32_t(up(q.n, S::kCols) / S::kCols);
-        const int64_t per = kind == kGram || kind == kPoly ? int64_t(q.tiles_m) * (q.tiles_m + 1) / 2 : int64_t(q.tiles_m) * q.tiles_n;
+        const int64_t per = tiles_of<S>(s, kind);
         q.per = int32_t(per);
         q.first_tile = int32_t(tiles);
         tiles += per * s.count;
@@ -619,6 +709,11 @@ bool allow() {
                                          int(tile_smem<P>())), "cudaFuncSetAttribute");
 }
 
+template <class S>
+bool allow_all() {
+    return allow<kGram, S>() && allow<kPoly, S>() && allow<kApply, S>() && allow<kResult, S>() && allow<kUpdate, S>();
+}
+
 // The current device's units; allows the kernels' shared memory there.
 bool device_units(Device* d) {
     static thread_local int known = -1;
@@ -626,10 +721,7 @@ bool device_units(Device* d) {
     int device = 0;
     if (!launched(cudaGetDevice(&device), "cudaGetDevice")) return false;
     if (known != device) {
-        if (!allow<kGram, PairTile>() || !allow<kPoly, PairTile>() || !allow<kApply, PairTile>() || !allow<kResult, PairTile>() ||
-            !allow<kUpdate, PairTile>() || !allow<kGram, SingleTile>() || !allow<kPoly, SingleTile>() || !allow<kApply, SingleTile>() ||
-            !allow<kResult, SingleTile>() || !allow<kUpdate, SingleTile>())
-            return false;
+        if (!allow_all<PairTile>() || !allow_all<HalfTile>() || !allow_all<SingleTile>()) return false;
         TileUnits u;
         if (!launched(tile_units<Product<kApply, PairTile>>(&u), "tile units")) return false;
         units.sms = u.sms;
@@ -661,17 +753,27 @@ bool launch_kind(int kind, const ProductParams& p, int units, cudaStream_t st) {
 // kUpdate, with what it needs in `with`.
 bool run_steps(const Group& g, const adamw_ortho_t& o, const float* coefs, int last, const ProductParams& with, const Device& d,
                cudaStream_t st) {
-    // pairs where their tiles fill the GPU
-    int64_t pair_tiles = 0;
-    for (int i = 0; i < g.n; ++i)
-        pair_tiles += g.shapes[i].count * (up(g.shapes[i].rows, 256) / 256) * (up(g.shapes[i].cols, 256) / 256);
-    const bool pair = pair_tiles * 2 >= d.pairs;
     for (int k = 0; k < o.steps; ++k) {
         const float* c = coefs + 3 * (k < o.n_coefficients ? k : o.n_coefficients - 1);
         for (int kind = kGram; kind <= kApply; ++kind) {
             const int which = kind == kApply && k + 1 == o.steps ? last : kind;
+            TileChoice choice = {{0, 0, 0}};
+            int64_t steps = 0;
+            for (int i = 0; i < g.n; ++i) {
+                const Shape& s = g.shapes[i];
+                choice.tiles[kPairShape] += tiles_of<PairTile>(s, kind) * s.count;
+                choice.tiles[kHalfShape] += tiles_of<HalfTile>(s, kind) * s.count;
+                choice.tiles[kSingleShape] += tiles_of<SingleTile>(s, kind) * s.count;
+                // the list's average
+                steps += up(kind == kGram ? std::max(s.rows, s.cols) : s.side, kStepK) / kStepK * tiles_of<PairTile>(s, kind) * s.count;
+            }
+            steps /= choice.tiles[kPairShape];
+            const int shape = choose_shape(choice, steps, d.pairs, d.sms);
             ProductParams p;
-            if (!(pair ? fill<PairTile>(g, kind, k & 1, &p) : fill<SingleTile>(g, kind, k & 1, &p))) return false;
+            if (!(shape == kPairShape   ? fill<PairTile>(g, kind, k & 1, &p)
+                  : shape == kHalfShape ? fill<HalfTile>(g, kind, k & 1, &p)
+                                        : fill<SingleTile>(g, kind, k & 1, &p)))
+                return false;
             p.a = c[0];
             p.b = c[1];
             p.c = c[2];
@@ -679,7 +781,10 @@ bool run_steps(const Group& g, const adamw_ortho_t& o, const float* coefs, int l
             p.table = with.table;
             p.hp = with.hp;
             p.nonfinite = with.nonfinite;
-            if (!(pair ? launch_kind<PairTile>(which, p, d.pairs, st) : launch_kind<SingleTile>(which, p, d.sms, st))) return false;
+            if (!(shape == kPairShape   ? launch_kind<PairTile>(which, p, d.pairs, st)
+                  : shape == kHalfShape ? launch_kind<HalfTile>(which, p, d.pairs, st)
+                                        : launch_kind<SingleTile>(which, p, d.sms, st)))
+                return false;
         }
     }
     return true;
@@ -794,8 +899,8 @@ extern "C" int adamw_orthogonalize(const adamw_matrices_t* src, const adamw_matr
     c.sums = static_cast<double*>(workspace);
     c.eps = ortho->eps;
     c.src = batch_of(*src);
-    if (!launched(launch(norm_kernel<false>, uint32_t(pieces), kNormThreads, 1, 0, st, c), "norm launch") ||
-        !launched(launch(copy_kernel<false>, uint32_t(pieces), kNormThreads, 1, 0, st, c), "copy launch"))
+    if (!launched(launch(norm_of<false>(src->dtype), uint32_t(pieces), kNormThreads, 1, 0, st, c), "norm launch") ||
+        !launched(launch(copy_of<false>(src->dtype), uint32_t(pieces), kNormThreads, 1, 0, st, c), "copy launch"))
         return ADAMW_ERR_CUDA;
     ProductParams with;
     memset(&with, 0, sizeof with);
@@ -1035,11 +1140,10 @@ extern "C" int adamw_muon_step(adamw_muon_plan_t plan, const adamw_muon_hparams_
     c.hp = hparams;
     c.nonfinite = nonfinite;
     c.nesterov = plan->nesterov;
-    c.momentum_bf16 = plan->momentum_bf16;
     // every norm first: one gradient that is not finite stops the whole step
     for (size_t r = 0; r < plan->rounds.size(); ++r) {
         const int64_t pieces = fill_copies(plan->rounds[r], plan->sums[r].data(), &c);
-        if (!launched(launch(norm_kernel<true>, uint32_t(pieces), kNormThreads, 1, 0, st, c), "norm launch")) return ADAMW_ERR_CUDA;
+        if (!launched(launch(norm_of<true>(plan->momentum_bf16 ? ADAMW_DTYPE_BF16 : ADAMW_DTYPE_FP32), uint32_t(pieces), kNormThreads, 1, 0, st, c), "norm launch")) return ADAMW_ERR_CUDA;
     }
     ProductParams with;
     memset(&with, 0, sizeof with);
@@ -1048,7 +1152,7 @@ extern "C" int adamw_muon_step(adamw_muon_plan_t plan, const adamw_muon_hparams_
     with.nonfinite = nonfinite;
     for (size_t r = 0; r < plan->rounds.size(); ++r) {
         const int64_t pieces = fill_copies(plan->rounds[r], plan->sums[r].data(), &c);
-        if (!launched(launch(copy_kernel<true>, uint32_t(pieces), kNormThreads, 1, 0, st, c), "copy launch")) return ADAMW_ERR_CUDA;
+        if (!launched(launch(copy_of<true>(plan->momentum_bf16 ? ADAMW_DTYPE_BF16 : ADAMW_DTYPE_FP32), uint32_t(pieces), kNormThreads, 1, 0, st, c), "copy launch")) return ADAMW_ERR_CUDA;
         if (!run_steps(plan->rounds[r], plan->ortho, plan->coefs.data(), kUpdate, with, d, st)) return ADAMW_ERR_CUDA;
     }
     return ADAMW_OK;

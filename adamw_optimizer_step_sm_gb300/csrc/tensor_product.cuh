@@ -27,7 +27,18 @@
 
 #include <cuda.h>
 
+#include <algorithm>
+
 #include "losses_common.cuh"
+
+#ifndef TILE_STEP0
+#define TILE_STEP0 512
+#define TILE_STEP1 384
+#define TILE_STEP2 512
+#define TILE_REST0 4000
+#define TILE_REST1 2500
+#define TILE_REST2 2500
+#endif
 
 namespace {
 
@@ -244,8 +255,35 @@ struct TileShape {
     static constexpr uint32_t kColumns = 2 * kCols;   // of tensor memory
     static_assert(kStages <= 16 && kColumns <= 512 && (kColumns & (kColumns - 1)) == 0, "tile shape");
 };
-using PairTile = TileShape<2, 256>;
-using SingleTile = TileShape<1, 128>;
+using PairTile = TileShape<2, 256>;     // 256 x 256
+using HalfTile = TileShape<2, 128>;     // 256 x 128
+using SingleTile = TileShape<1, 128>;   // 128 x 128
+
+// Which shape a product takes: the one whose list of tiles is done first by
+// this estimate, in cycles.  A step's time is that of shared memory (each SM
+// writes and reads what it loads of it, 128 bytes a cycle): 512 for PairTile,
+// 384 for HalfTile, 512 for SingleTile, against 512, 256 and 256 of the tensor
+// cores; the last tile's epilogue is not hidden.
+struct TileChoice {
+    int64_t tiles[3];   // of each shape; 0: not to be taken
+};
+constexpr int kPairShape = 0, kHalfShape = 1, kSingleShape = 2;
+inline int choose_shape(const TileChoice& c, int64_t steps, int pairs, int sms) {
+    const int64_t step[3] = {TILE_STEP0, TILE_STEP1, TILE_STEP2}, rest[3] = {TILE_REST0, TILE_REST1, TILE_REST2};
+    const int units[3] = {pairs, pairs, sms};
+    int best = -1;
+    int64_t least = 0;
+    for (int k = 0; k < 3; ++k) {
+        if (c.tiles[k] <= 0) continue;
+        const int64_t waves = (c.tiles[k] + units[k] - 1) / units[k];
+        const int64_t t = waves * std::max(steps * step[k], rest[k]) + rest[k];
+        if (best < 0 || t < least) {
+            best = k;
+            least = t;
+        }
+    }
+    return best < 0 ? kSingleShape : best;
+}
 
 template <class P>
 constexpr size_t tile_smem() {
@@ -274,7 +312,9 @@ constexpr int tile_threads() { return 128 + 32 * P::kWarps; }
 //        row `row` of the CTA's 128 x kCols part; leaves in v what the
 //        mirrored tile holds
 //   mirrored(out), mirror(p, out, col, row, v): eight rows from `row` of column
-//        `col`, for the transposed tile.
+//        `col`, for the transposed tile
+//   scalar(out), store_one(p, out, row, col, v): whether results go element by
+//        element (rows that are not whole vectors), neighbours by neighbouring lanes
 template <class P, class S>
 __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid_constant__ typename P::Params p) {
     constexpr int PAIR = S::kPair;
@@ -463,7 +503,7 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
                 for (int i = 0; i < 32; i += 4)
                     *reinterpret_cast<uint4*>(place(lane, i)) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                 __syncwarp();
-                const bool mirrored = P::mirrored(out);
+                const bool mirrored = P::mirrored(out), scalar = P::scalar(out);
 #pragma unroll
                 for (int i = 0; i < 32; i += 8) {
                     const int r = i + lane / 4, q = lane % 4 * 8;
@@ -471,7 +511,7 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
                     *reinterpret_cast<float4*>(x) = *reinterpret_cast<float4*>(place(r, q));
                     *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<float4*>(place(r, q + 4));
                     P::store(p, out, row0 + r, c + q, now[i / 8], late[i / 8], x);
-                    if (mirrored) {
+                    if (mirrored || scalar) {
                         *reinterpret_cast<float4*>(place(r, q)) = *reinterpret_cast<float4*>(x);
                         *reinterpret_cast<float4*>(place(r, q + 4)) = *reinterpret_cast<float4*>(x + 4);
                     }
@@ -486,6 +526,11 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
                         for (int e = 0; e < 8; ++e) x[e] = *place(q + e, j);
                         P::mirror(p, out, c + j, row0 + q, x);
                     }
+                    __syncwarp();
+                }
+                if (scalar) {
+#pragma unroll 4
+                    for (int r = 0; r < 32; ++r) P::store_one(p, out, row0 + r, c + lane, *place(r, lane));
                     __syncwarp();
                 }
             }
