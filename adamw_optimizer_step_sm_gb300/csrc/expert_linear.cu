@@ -68,12 +68,12 @@ __device__ __forceinline__ int group_of(const Groups* g, int32_t experts, int32_
     return low;
 }
 
-// Eight elements to rows of any type.
+// Rows of any type.
 struct RowsAt {
     char* data;
     int64_t ld;
     int32_t cols, dtype;
-    int32_t vector;   // 16-byte accesses
+    int32_t vector;   // every row at a multiple of 32 bytes
 };
 
 // The rows from (row, col) on.
@@ -81,57 +81,6 @@ __device__ __forceinline__ RowsAt part_of(RowsAt r, int64_t row, int32_t col) {
     r.data += (row * r.ld + col) * (r.dtype == ADAMW_DTYPE_FP32 ? 4 : 2);
     r.cols -= col;
     return r;
-}
-
-template <int DT>
-__device__ __forceinline__ void store8(char* at, const float (&v)[8], int n) {
-    using E = Elem<DT>;
-    if (n >= 8) {
-        *reinterpret_cast<uint4*>(at) = E::pack(v);
-        if (E::kVec == 4) *reinterpret_cast<uint4*>(at + 16) = E::pack(v + 4);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) E::store(at, i, v[i]);
-    }
-}
-template <int DT>
-__device__ __forceinline__ void load8(const char* at, float (&v)[8], int n) {
-    using E = Elem<DT>;
-    if (n >= 8) {
-        E::unpack(*reinterpret_cast<const uint4*>(at), v);
-        if (E::kVec == 4) E::unpack(*reinterpret_cast<const uint4*>(at + 16), v + 4);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? E::load(at, i) : 0.0f;
-    }
-}
-// of rows of whole vectors
-__device__ __forceinline__ void store_rows(const RowsAt& r, int row, int col, const float (&v)[8]) {
-    const int64_t at = row * r.ld + col;
-    const int n = r.cols - col;
-    if (r.dtype == ADAMW_DTYPE_BF16) store8<ADAMW_DTYPE_BF16>(r.data + at * 2, v, n);
-    else if (r.dtype == ADAMW_DTYPE_FP16) store8<ADAMW_DTYPE_FP16>(r.data + at * 2, v, n);
-    else store8<ADAMW_DTYPE_FP32>(r.data + at * 4, v, n);
-}
-__device__ __forceinline__ void load_rows(const RowsAt& r, int row, int col, float (&v)[8]) {
-    const int64_t at = row * r.ld + col;
-    const int n = r.cols - col;
-    if (r.dtype == ADAMW_DTYPE_BF16) load8<ADAMW_DTYPE_BF16>(r.data + at * 2, v, n);
-    else if (r.dtype == ADAMW_DTYPE_FP16) load8<ADAMW_DTYPE_FP16>(r.data + at * 2, v, n);
-    else load8<ADAMW_DTYPE_FP32>(r.data + at * 4, v, n);
-}
-// of any rows
-__device__ __forceinline__ void store_as(const RowsAt& r, int row, int col, float v) {
-    const int64_t at = row * r.ld + col;
-    if (r.dtype == ADAMW_DTYPE_BF16) Elem<ADAMW_DTYPE_BF16>::store(r.data, at, v);
-    else if (r.dtype == ADAMW_DTYPE_FP16) Elem<ADAMW_DTYPE_FP16>::store(r.data, at, v);
-    else Elem<ADAMW_DTYPE_FP32>::store(r.data, at, v);
-}
-__device__ __forceinline__ float load_as(const RowsAt& r, int row, int col) {
-    const int64_t at = row * r.ld + col;
-    return r.dtype == ADAMW_DTYPE_BF16 ? Elem<ADAMW_DTYPE_BF16>::load(r.data, at)
-           : r.dtype == ADAMW_DTYPE_FP16 ? Elem<ADAMW_DTYPE_FP16>::load(r.data, at) : Elem<ADAMW_DTYPE_FP32>::load(r.data, at);
 }
 
 // Tile (m, n) number i of a group of tm x tn: bands of eight tiles of rows, so
@@ -157,7 +106,6 @@ struct ExpertRows {
     static constexpr bool kTail = false;
     static constexpr size_t kTable = sizeof(Groups);
     static constexpr int kWarps = 4;
-    struct Late {};
     struct Extra {};
     struct Out {
         RowsAt y;       // from the first row and column of the CTA's part
@@ -204,14 +152,14 @@ struct ExpertRows {
     __device__ static bool mirrored(const Out&) { return false; }
     __device__ static bool scalar(const Out& o) { return !o.y.vector; }
     __device__ static void fetch(const Params&, const Out&, int, int, Extra&) {}
-    __device__ static void store(const Params& p, const Out& o, int row, int col, const Extra&, const Late&, float (&v)[8]) {
-        if (o.y.vector && wanted(p, o, row, col)) store_rows(o.y, row, col, v);
+    __device__ static void store(const Params& p, const Out& o, int row, int col, const Extra&, float (&v)[32]) {
+        if (o.y.vector && row < o.rows)
+            store_row(o.y.data + (row * o.y.ld + col) * (o.y.dtype == ADAMW_DTYPE_FP32 ? 4 : 2), o.y.dtype, v, o.y.cols - col);
     }
     __device__ static void store_one(const Params& p, const Out& o, int row, int col, float v) {
-        if (wanted(p, o, row, col)) store_as(o.y, row, col, v);
+        if (wanted(p, o, row, col)) store_as(o.y.data, row * o.y.ld + col, o.y.dtype, v);
     }
-    __device__ static void fetch_late(const Params&, const Out&, int, int, Late&) {}
-    __device__ static void mirror(const Params&, const Out&, int, int, const float (&)[8]) {}
+    __device__ static void mirror(const Params&, const Out&, int, int, const float (&)[32]) {}
 };
 
 // dw[e] = dy^T x over the expert's rows: both operands MN-major.
@@ -229,10 +177,7 @@ struct ExpertOuter {
     static constexpr bool kTail = true;
     static constexpr size_t kTable = sizeof(Groups);
     static constexpr int kWarps = 4;
-    struct Late {};
-    struct Extra {
-        float v[ADD ? 8 : 1];
-    };
+    struct Extra {};
     struct Out {
         RowsAt dw;      // from the first row and column of the CTA's part
         int32_t rows;   // of dw, from there
@@ -272,26 +217,25 @@ struct ExpertOuter {
     __device__ static bool wanted(const Params&, const Out& o, int row, int col) { return row < o.rows && col < o.dw.cols; }
     __device__ static bool mirrored(const Out&) { return false; }
     __device__ static bool scalar(const Out& o) { return !o.dw.vector; }
-    __device__ static void fetch(const Params& p, const Out& o, int row, int col, Extra& x) {
+    __device__ static void fetch(const Params&, const Out&, int, int, Extra&) {}
+    __device__ static void store(const Params& p, const Out& o, int row, int col, const Extra&, float (&v)[32]) {
+        if (!o.dw.vector || row >= o.rows) return;
+        char* at = o.dw.data + (row * o.dw.ld + col) * (o.dw.dtype == ADAMW_DTYPE_FP32 ? 4 : 2);
         if constexpr (ADD) {
-            if (o.dw.vector && wanted(p, o, row, col)) load_rows(o.dw, row, col, x.v);
-        }
-    }
-    __device__ static void store(const Params& p, const Out& o, int row, int col, const Extra& x, const Late&, float (&v)[8]) {
-        if (!o.dw.vector || !wanted(p, o, row, col)) return;
-        if constexpr (ADD) {
+            float sum[32];
+            load_row(at, o.dw.dtype, sum, o.dw.cols - col);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += x.v[i];
+            for (int i = 0; i < 32; ++i) v[i] += sum[i];
         }
-        store_rows(o.dw, row, col, v);
+        store_row(at, o.dw.dtype, v, o.dw.cols - col);
     }
     __device__ static void store_one(const Params& p, const Out& o, int row, int col, float v) {
         if (!wanted(p, o, row, col)) return;
-        if constexpr (ADD) v += load_as(o.dw, row, col);
-        store_as(o.dw, row, col, v);
+        const int64_t at = row * o.dw.ld + col;
+        if constexpr (ADD) v += load_as(o.dw.data, at, o.dw.dtype);
+        store_as(o.dw.data, at, o.dw.dtype, v);
     }
-    __device__ static void fetch_late(const Params&, const Out&, int, int, Late&) {}
-    __device__ static void mirror(const Params&, const Out&, int, int, const float (&)[8]) {}
+    __device__ static void mirror(const Params&, const Out&, int, int, const float (&)[32]) {}
 };
 
 // A batch of matrices of 16-bit elements, at any strides, into rows of `ld`.
@@ -375,7 +319,7 @@ bool map_of(CUtensorMap* map, const adamw_matrices_t& m, bool mn, int rows) {
 RowsAt rows_of(const adamw_matrices_t& m) {
     const int size = dtype_size(m.dtype);
     return {static_cast<char*>(m.data), m.row_stride, int32_t(m.cols), m.dtype,
-            aligned(m.data, 16) && (m.rows <= 1 || m.row_stride * size % 16 == 0) && (m.batch <= 1 || m.batch_stride * size % 16 == 0)};
+            aligned(m.data, 32) && (m.rows <= 1 || m.row_stride * size % 32 == 0) && (m.batch <= 1 || m.batch_stride * size % 32 == 0)};
 }
 
 template <class P>
@@ -488,7 +432,7 @@ extern "C" int adamw_expert_rows(const adamw_matrices_t* x, const adamw_matrices
     // the grid covers the most tiles that the groups can have: one partial in each
     const int64_t groups = w->batch + 2;
     auto most = [&](int rows, int cols) { return (x->rows / rows + groups) * up(n, cols); };
-    if (most(SingleTile::kRows, SingleTile::kCols) > kMaxCount) return ADAMW_ERR_TOO_LARGE;
+    if (most(SmallTile::kRows, SmallTile::kCols) > kMaxCount) return ADAMW_ERR_TOO_LARGE;
     TileUnits units;
     if (!launched(units_of<ExpertRows<PairTile>>(&units), "tile units")) return ADAMW_ERR_CUDA;
     adamw_matrices_t a = *x, b = *w;
@@ -497,15 +441,15 @@ extern "C" int adamw_expert_rows(const adamw_matrices_t* x, const adamw_matrices
     // what groups of one size would have
     const int64_t each = up(x->rows, w->batch), used = std::min(w->batch, x->rows);
     auto likely = [&](int rows, int cols) { return used * up(each, rows) * up(n, cols); };
-    const TileChoice choice = {{likely(PairTile::kRows, PairTile::kCols), likely(HalfTile::kRows, HalfTile::kCols),
-                                likely(SingleTile::kRows, SingleTile::kCols)}};
+    const TileChoice choice = {{likely(PairTile::kRows, PairTile::kCols), likely(WideTile::kRows, WideTile::kCols),
+                                likely(SmallTile::kRows, SmallTile::kCols)}};
     switch (choose_shape(choice, up(k, kStepK), units.pairs, units.sms)) {
         case kPairShape:
             return rows_call<PairTile>(a, b, transposed != 0, offsets, *y, most(PairTile::kRows, PairTile::kCols), units.pairs, st);
-        case kHalfShape:
-            return rows_call<HalfTile>(a, b, transposed != 0, offsets, *y, most(HalfTile::kRows, HalfTile::kCols), units.pairs, st);
+        case kWideShape:
+            return rows_call<WideTile>(a, b, transposed != 0, offsets, *y, most(WideTile::kRows, WideTile::kCols), units.sms, st);
         default:
-            return rows_call<SingleTile>(a, b, transposed != 0, offsets, *y, most(SingleTile::kRows, SingleTile::kCols), units.sms, st);
+            return rows_call<SmallTile>(a, b, transposed != 0, offsets, *y, most(SmallTile::kRows, SmallTile::kCols), units.sms, st);
     }
 }
 
@@ -526,22 +470,22 @@ extern "C" int adamw_expert_outer(const adamw_matrices_t* dy, const adamw_matric
     if (bytes > 0 && !aligned(workspace, 256)) return ADAMW_ERR_MISALIGNED;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     auto tiles = [&](int rows, int cols) { return dw->batch * up(dw->rows, rows) * up(dw->cols, cols); };
-    if (tiles(SingleTile::kRows, SingleTile::kCols) > kMaxCount) return ADAMW_ERR_TOO_LARGE;
+    if (tiles(SmallTile::kRows, SmallTile::kCols) > kMaxCount) return ADAMW_ERR_TOO_LARGE;
     TileUnits units;
     if (!launched(units_of<ExpertOuter<PairTile, false>>(&units), "tile units")) return ADAMW_ERR_CUDA;
     adamw_matrices_t a = *dy, b = *x;
     char* at = static_cast<char*>(workspace);
     if (!readable(&a, &at, st) || !readable(&b, &at, st)) return ADAMW_ERR_CUDA;
-    const TileChoice choice = {{tiles(PairTile::kRows, PairTile::kCols), tiles(HalfTile::kRows, HalfTile::kCols),
-                                tiles(SingleTile::kRows, SingleTile::kCols)}};
+    const TileChoice choice = {{tiles(PairTile::kRows, PairTile::kCols), tiles(WideTile::kRows, WideTile::kCols),
+                                tiles(SmallTile::kRows, SmallTile::kCols)}};
     const int shape = choose_shape(choice, up(up(dy->rows, dw->batch), kStepK), units.pairs, units.sms);
     const int64_t n = choice.tiles[shape];
     if (shape == kPairShape)
         return accumulate ? outer_call<PairTile, true>(a, b, offsets, *dw, n, units.pairs, st)
                           : outer_call<PairTile, false>(a, b, offsets, *dw, n, units.pairs, st);
-    if (shape == kHalfShape)
-        return accumulate ? outer_call<HalfTile, true>(a, b, offsets, *dw, n, units.pairs, st)
-                          : outer_call<HalfTile, false>(a, b, offsets, *dw, n, units.pairs, st);
-    return accumulate ? outer_call<SingleTile, true>(a, b, offsets, *dw, n, units.sms, st)
-                      : outer_call<SingleTile, false>(a, b, offsets, *dw, n, units.sms, st);
+    if (shape == kWideShape)
+        return accumulate ? outer_call<WideTile, true>(a, b, offsets, *dw, n, units.sms, st)
+                          : outer_call<WideTile, false>(a, b, offsets, *dw, n, units.sms, st);
+    return accumulate ? outer_call<SmallTile, true>(a, b, offsets, *dw, n, units.sms, st)
+                      : outer_call<SmallTile, false>(a, b, offsets, *dw, n, units.sms, st);
 }

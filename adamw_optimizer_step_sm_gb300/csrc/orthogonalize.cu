@@ -38,7 +38,7 @@ using Fp16 = Elem<ADAMW_DTYPE_FP16>;
 // Matrices of one shape, whose working copies lie one after the other.
 struct Shape {
     int64_t stride, small_stride;   // elements between matrices (of X, of G)
-    int32_t rows, cols, ld;         // ld: cols up to a multiple of 8
+    int32_t rows, cols, ld;         // ld: cols up to a multiple of 16
     int32_t side, small_ld;         // of G
     int32_t count, first;           // matrices, and the first one's number in the list
 };
@@ -60,7 +60,8 @@ struct Batch {
     char* data;
     int64_t batch_stride, row_stride;
     int32_t dtype;
-    int32_t vector;   // 16-byte accesses
+    int32_t vector;   // every row at a multiple of 16 bytes
+    int32_t sectors;  // of 32
 };
 
 constexpr int kNormThreads = 256;
@@ -90,11 +91,6 @@ struct CopyParams {
     int32_t nesterov;
 };
 
-__device__ __forceinline__ void store_as(char* data, int64_t at, int32_t dtype, float v) {
-    if (dtype == ADAMW_DTYPE_FP32) Elem<ADAMW_DTYPE_FP32>::store(data, at, v);
-    else if (dtype == ADAMW_DTYPE_BF16) Elem<ADAMW_DTYPE_BF16>::store(data, at, v);
-    else Fp16::store(data, at, v);
-}
 __device__ __forceinline__ void store8_any(char* data, int64_t at, int32_t dtype, bool vector, int n, const float (&v)[8]) {
     if (dtype == ADAMW_DTYPE_FP32) {
         using E = Elem<ADAMW_DTYPE_FP32>;
@@ -400,7 +396,8 @@ struct ProductParams {
     const int32_t* nonfinite;
 };
 
-template <int KIND, class S>
+// LOW_IN, LOW_OUT: X has its second fp16, the next X gets one.
+template <int KIND, class S, bool LOW_IN = false, bool LOW_OUT = false>
 struct Product {
     using Params = ProductParams;
     static constexpr bool kTail = false;
@@ -409,15 +406,12 @@ struct Product {
     // epilogue longer than its products.
     static constexpr int kWarps = 8;
     static constexpr bool kSymmetric = KIND == kGram || KIND == kPoly;
-    // tiles of columns to a tile of rows
-    static constexpr int kRatio = S::kRows / S::kCols;
+    // tiles of rows to a tile of columns
+    static constexpr int kRatio = S::kCols / S::kRows;
 
     // what the epilogue adds to the product
     struct Extra {
-        uint4 hi, lo;
-    };
-    struct Late {
-        float4 w[KIND == kUpdate ? 2 : 1];   // the master
+        Sector hi[KIND == kGram ? 1 : 2], lo[LOW_IN ? 2 : 1];
     };
     struct Out {
         // by value: read through a pointer to the arguments, each of these cost
@@ -443,13 +437,14 @@ struct Product {
         *matrix = t / c.per;
         t -= *matrix * c.per;
         if (kSymmetric) {
-            // row by row of the lower triangle, its diagonal in squares: row r
-            // has kRatio (r + 1) tiles
+            // the lower triangle, its diagonal in squares of kCols: the kRatio
+            // rows of square r have r + 1 tiles each
             int32_t r = int32_t((sqrtf(8.0f / kRatio * float(t) + 1.0f) - 1.0f) * 0.5f);
             while (kRatio * r * (r + 1) / 2 > t) --r;
             while (kRatio * (r + 1) * (r + 2) / 2 <= t) ++r;
-            *m = r;
-            *n = t - kRatio * r * (r + 1) / 2;
+            t -= kRatio * r * (r + 1) / 2;
+            *m = r * kRatio + t / (r + 1);
+            *n = t % (r + 1);
         } else {
             // bands of eight tiles of rows, for reuse in L2
             const int32_t band = t / (8 * c.tiles_n), left = c.tiles_m - band * 8, h = left < 8 ? left : 8;
@@ -483,7 +478,7 @@ struct Product {
         o.cols = c.s.cols;
         o.row = m * S::kRows + int32_t(rank) * kRowsOfCta;
         o.col = n * S::kCols;
-        o.mirrored = kSymmetric && m != n / kRatio;
+        o.mirrored = kSymmetric && m / kRatio != n;
         o.skip = false;
         o.vector = true;
         o.a = p.a;
@@ -497,13 +492,13 @@ struct Product {
             o.dst_type = p.dst.dtype;
             o.dst = p.dst.data + o.matrix * p.dst.batch_stride * (o.dst_type == ADAMW_DTYPE_FP32 ? 4 : 2);
             o.dst_ld = p.dst.row_stride;
-            o.vector = p.dst.vector != 0;
+            o.vector = p.dst.sectors != 0;
         } else if constexpr (KIND == kUpdate) {
             const MuonMatrix t = p.table[c.s.first + o.matrix];
             o.dst = reinterpret_cast<char*>(t.master);
             o.param = reinterpret_cast<char*>(t.param);
             o.dst_ld = c.s.cols;
-            o.vector = c.s.cols % 8 == 0 && (reinterpret_cast<uintptr_t>(t.master) | reinterpret_cast<uintptr_t>(t.param)) % 16 == 0;
+            o.vector = c.s.cols % 16 == 0 && (reinterpret_cast<uintptr_t>(t.master) | reinterpret_cast<uintptr_t>(t.param)) % 32 == 0;
             o.skip = *p.nonfinite != 0;
             const float lr = p.hp->lr;
             o.decay = 1.0f - lr * p.hp->weight_decay;
@@ -515,61 +510,76 @@ struct Product {
         return !o.skip && o.row + row < o.m && o.col + col < o.n;
     }
     __device__ static bool mirrored(const Out& o) { return o.mirrored; }
-    __device__ static void fetch(const Params& p, const Out& o, int row, int col, Extra& x) {
-        if (KIND == kGram || !wanted(p, o, row, col)) return;
+    __device__ static void fetch(const Params&, const Out& o, int row, int col, Extra& x) {
+        if (KIND == kGram || o.row + row >= o.m) return;
         const int64_t at = int64_t(o.row + row) * o.ld + o.col + col;
-        x.hi = *reinterpret_cast<const uint4*>(o.hi + at);
-        if (!kSymmetric) x.lo = *reinterpret_cast<const uint4*>(o.lo + at);
-    }
-    __device__ static void fetch_late(const Params& p, const Out& o, int row, int col, Late& x) {
-        if constexpr (KIND == kUpdate) {
-            if (o.vector && wanted(p, o, row, col)) {
-                const float4* w = reinterpret_cast<const float4*>(o.dst + (int64_t(o.row + row) * o.dst_ld + o.col + col) * 4);
-                x.w[0] = w[0];
-                x.w[1] = w[1];
-            }
+        const int n = o.ld - o.col - col;   // the working copies' rows are whole sectors
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (i * 16 >= n) break;
+            x.hi[i] = load_sector(o.hi + at + i * 16);
+            if constexpr (LOW_IN) x.lo[i] = load_sector(o.lo + at + i * 16);
         }
     }
-    // Results whose rows are not whole vectors go element by element.
+    // Results whose rows are not whole sectors go element by element.
     __device__ static bool scalar(const Out& o) { return (KIND == kResult || KIND == kUpdate) && !o.vector; }
-    __device__ static void store(const Params& p, const Out& o, int row, int col, const Extra& x, const Late& y, float (&v)[8]) {
-        const bool here = wanted(p, o, row, col);
+    __device__ static void store(const Params&, const Out& o, int row, int col, const Extra& x, float (&v)[32]) {
+        if (o.row + row >= o.m) return;
         const int64_t at = int64_t(o.row + row) * o.ld + o.col + col;
-        if constexpr (KIND == kGram) {
+        const int n = o.ld - o.col - col;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= kUnscale;
-            if (here) *reinterpret_cast<uint4*>(o.out + at) = Fp16::pack(v);
-        } else if constexpr (KIND == kPoly) {
-            if (!here) return;   // rows beyond the matrix: nothing mirrors them
-            float g[8];
-            Fp16::unpack(x.hi, g);
+        for (int i = 0; i < 2; ++i) {
+            if (i * 16 >= n) break;
+            float* y = v + i * 16;
+            if constexpr (KIND == kGram) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = fmaf(o.b, g[e], o.c * v[e]);
-            *reinterpret_cast<uint4*>(o.out + at) = Fp16::pack(v);
-        } else {
-            if (!here) return;
-            float h[8], l[8];
-            Fp16::unpack(x.hi, h);
-            Fp16::unpack(x.lo, l);
+                for (int e = 0; e < 16; ++e) y[e] *= kUnscale;
+                store_sector(o.out + at + i * 16, pack_sector<ADAMW_DTYPE_FP16>(y));
+            } else {
+                float h[16];
+                unpack_sector<ADAMW_DTYPE_FP16>(x.hi[i], h);
+                if constexpr (KIND == kPoly) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = fmaf(o.a, fmaf(l[e], 1.0f / kLow, h[e]), v[e] * kUnscale);
-            if constexpr (KIND == kApply) {
-                uint4 hi, lo;
-                split8(v, &hi, &lo);
-                *reinterpret_cast<uint4*>(o.out + at) = hi;
-                *reinterpret_cast<uint4*>(o.lo + at) = lo;
-            } else if constexpr (KIND == kResult) {
+                    for (int e = 0; e < 16; ++e) y[e] = fmaf(o.b, h[e], o.c * y[e]);
+                    store_sector(o.out + at + i * 16, pack_sector<ADAMW_DTYPE_FP16>(y));
+                } else {
+                    if constexpr (LOW_IN) {
+                        float l[16];
+                        unpack_sector<ADAMW_DTYPE_FP16>(x.lo[i], l);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= kUnscale;
-                if (o.vector)
-                    store8_any(o.dst, int64_t(o.row + row) * o.dst_ld + o.col + col, o.dst_type, true, o.cols - o.col - col, v);
-            } else if (o.vector) {
-                const float* w = reinterpret_cast<const float*>(y.w);
+                        for (int e = 0; e < 16; ++e) h[e] = fmaf(l[e], 1.0f / kLow, h[e]);
+                    }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = fmaf(-o.rate, v[e], o.decay * w[e]);
-                const int64_t to = int64_t(o.row + row) * o.dst_ld + o.col + col;
-                store8_any(o.dst, to, ADAMW_DTYPE_FP32, true, 8, v);
-                store8_any(o.param, to, ADAMW_DTYPE_BF16, true, 8, v);
+                    for (int e = 0; e < 16; ++e) y[e] = fmaf(o.a, h[e], y[e] * kUnscale);
+                    if constexpr (KIND == kApply) {
+                        const Sector hi = pack_sector<ADAMW_DTYPE_FP16>(y);
+                        store_sector(o.out + at + i * 16, hi);
+                        if constexpr (LOW_OUT) {
+                            unpack_sector<ADAMW_DTYPE_FP16>(hi, h);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) y[e] = (y[e] - h[e]) * kLow;
+                            store_sector(o.lo + at + i * 16, pack_sector<ADAMW_DTYPE_FP16>(y));
+                        }
+                    } else if constexpr (KIND == kResult) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) y[e] *= kUnscale;
+                    }
+                }
+            }
+        }
+        if constexpr (KIND == kResult || KIND == kUpdate) {
+            if (!o.vector) return;
+            const int64_t to = int64_t(o.row + row) * o.dst_ld + o.col + col;
+            const int left = o.cols - o.col - col;
+            if constexpr (KIND == kResult) {
+                store_row(o.dst + to * (o.dst_type == ADAMW_DTYPE_FP32 ? 4 : 2), o.dst_type, v, left);
+            } else {
+                float w[32];
+                load_row<ADAMW_DTYPE_FP32>(o.dst + to * 4, w, left);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = fmaf(-o.rate, v[e], o.decay * w[e]);
+                store_row<ADAMW_DTYPE_FP32>(o.dst + to * 4, v, left);
+                store_row<ADAMW_DTYPE_BF16>(o.param + to * 2, v, left);
             }
         }
     }
@@ -585,10 +595,12 @@ struct Product {
             store_as(o.param, to, ADAMW_DTYPE_BF16, v);
         }
     }
-    // rows row .. row + 7 of column col, as a row of the mirrored tile
-    __device__ static void mirror(const Params&, const Out& o, int col, int row, const float (&v)[8]) {
-        if (!kSymmetric || o.col + col >= o.n || o.row + row >= o.m) return;
-        *reinterpret_cast<uint4*>(o.out + int64_t(o.col + col) * o.ld + o.row + row) = Fp16::pack(v);
+    __device__ static void mirror(const Params&, const Out& o, int row, int col, const float (&v)[32]) {
+        if (!kSymmetric || o.row + row >= o.m) return;
+        __half* at = reinterpret_cast<__half*>(o.out) + int64_t(o.col + col) * o.ld + o.row + row;
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (o.col + col + e < o.n) at[int64_t(e) * o.ld] = __float2half_rn(v[e]);
     }
 };
 
@@ -603,10 +615,10 @@ Shape shape_of(int64_t rows, int64_t cols) {
     Shape s = {};
     s.rows = int32_t(rows);
     s.cols = int32_t(cols);
-    s.ld = int32_t(up(cols, 8));
-    s.stride = up(rows * s.ld, 8);
+    s.ld = int32_t(up(cols, 16));   // whole 32-byte sectors
+    s.stride = rows * s.ld;
     s.side = s.rows <= s.cols ? s.rows : s.cols;
-    s.small_ld = int32_t(up(s.side, 8));
+    s.small_ld = int32_t(up(s.side, 16));
     s.small_stride = int64_t(s.side) * s.small_ld;
     return s;
 }
@@ -642,8 +654,8 @@ template <class S>
 int64_t tiles_of(const Shape& s, int kind) {
     const int64_t side = s.side;
     if (kind != kGram && kind != kPoly) return (up(s.rows, S::kRows) / S::kRows) * (up(s.cols, S::kCols) / S::kCols);
-    const int64_t m = up(side, S::kRows) / S::kRows, n = up(side, S::kCols) / S::kCols, ratio = S::kRows / S::kCols;
-    return ratio * m * (m + 1) / 2 - (ratio * m - n);   // the last row may end earlier
+    const int64_t m = up(side, S::kRows) / S::kRows, n = up(side, S::kCols) / S::kCols, ratio = S::kCols / S::kRows;
+    return ratio * n * (n + 1) / 2 - (ratio * n - m) * n;   // the last square may have fewer rows
 }
 
 // The products' arguments, but for the coefficients.  which: X's buffer.
@@ -702,16 +714,17 @@ struct Device {
     int sms = 0, pairs = 0;
 };
 
-template <int KIND, class S>
+template <class P, class S>
 bool allow() {
-    using P = Product<KIND, S>;
     return launched(cudaFuncSetAttribute(tile_kernel<P, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          int(tile_smem<P>())), "cudaFuncSetAttribute");
 }
 
 template <class S>
 bool allow_all() {
-    return allow<kGram, S>() && allow<kPoly, S>() && allow<kApply, S>() && allow<kResult, S>() && allow<kUpdate, S>();
+    return allow<Product<kGram, S>, S>() && allow<Product<kPoly, S>, S>() && allow<Product<kApply, S>, S>() &&
+           allow<Product<kApply, S, true>, S>() && allow<Product<kApply, S, true, true>, S>() && allow<Product<kResult, S>, S>() &&
+           allow<Product<kResult, S, true>, S>() && allow<Product<kUpdate, S>, S>() && allow<Product<kUpdate, S, true>, S>();
 }
 
 // The current device's units; allows the kernels' shared memory there.
@@ -721,7 +734,7 @@ bool device_units(Device* d) {
     int device = 0;
     if (!launched(cudaGetDevice(&device), "cudaGetDevice")) return false;
     if (known != device) {
-        if (!allow_all<PairTile>() || !allow_all<HalfTile>() || !allow_all<SingleTile>()) return false;
+        if (!allow_all<PairTile>() || !allow_all<WideTile>() || !allow_all<SmallTile>()) return false;
         TileUnits u;
         if (!launched(tile_units<Product<kApply, PairTile>>(&u), "tile units")) return false;
         units.sms = u.sms;
@@ -732,20 +745,24 @@ bool device_units(Device* d) {
     return true;
 }
 
-template <int KIND, class S>
+template <class P, class S>
 bool launch_product(const ProductParams& p, int units, cudaStream_t st) {
     const uint32_t grid = uint32_t(p.tiles < units ? p.tiles : units) * S::kPair;
-    using P = Product<KIND, S>;
     return launched(launch(tile_kernel<P, S>, grid, tile_threads<P>(), S::kPair, tile_smem<P>(), st, p), "product launch");
 }
 template <class S>
-bool launch_kind(int kind, const ProductParams& p, int units, cudaStream_t st) {
+bool launch_kind(int kind, bool low_in, bool low_out, const ProductParams& p, int units, cudaStream_t st) {
     switch (kind) {
-        case kGram: return launch_product<kGram, S>(p, units, st);
-        case kPoly: return launch_product<kPoly, S>(p, units, st);
-        case kApply: return launch_product<kApply, S>(p, units, st);
-        case kResult: return launch_product<kResult, S>(p, units, st);
-        default: return launch_product<kUpdate, S>(p, units, st);
+        case kGram: return launch_product<Product<kGram, S>, S>(p, units, st);
+        case kPoly: return launch_product<Product<kPoly, S>, S>(p, units, st);
+        case kApply:
+            return !low_in    ? launch_product<Product<kApply, S>, S>(p, units, st)
+                   : !low_out ? launch_product<Product<kApply, S, true>, S>(p, units, st)
+                              : launch_product<Product<kApply, S, true, true>, S>(p, units, st);
+        case kResult:
+            return low_in ? launch_product<Product<kResult, S, true>, S>(p, units, st) : launch_product<Product<kResult, S>, S>(p, units, st);
+        default:
+            return low_in ? launch_product<Product<kUpdate, S, true>, S>(p, units, st) : launch_product<Product<kUpdate, S>, S>(p, units, st);
     }
 }
 
@@ -753,8 +770,16 @@ bool launch_kind(int kind, const ProductParams& p, int units, cudaStream_t st) {
 // kUpdate, with what it needs in `with`.
 bool run_steps(const Group& g, const adamw_ortho_t& o, const float* coefs, int last, const ProductParams& with, const Device& d,
                cudaStream_t st) {
+    auto row = [&](int k) { return coefs + 3 * (k < o.n_coefficients ? k : o.n_coefficients - 1); };
+    bool low_in = true;   // X starts as two fp16
     for (int k = 0; k < o.steps; ++k) {
-        const float* c = coefs + 3 * (k < o.n_coefficients ? k : o.n_coefficients - 1);
+        // by how much the steps after this one multiply an error of X in a
+        // direction without singular value; up to 16, eleven bits of X are enough
+        // (5e-4 of the result at worst, a matrix of few directions)
+        double later = 1.0;
+        for (int i = k + 1; i < o.steps; ++i) later *= std::fabs(double(row(i)[0]));
+        const bool low_out = low_in && later > 16.0;
+        const float* c = row(k);
         for (int kind = kGram; kind <= kApply; ++kind) {
             const int which = kind == kApply && k + 1 == o.steps ? last : kind;
             TileChoice choice = {{0, 0, 0}};
@@ -762,8 +787,8 @@ bool run_steps(const Group& g, const adamw_ortho_t& o, const float* coefs, int l
             for (int i = 0; i < g.n; ++i) {
                 const Shape& s = g.shapes[i];
                 choice.tiles[kPairShape] += tiles_of<PairTile>(s, kind) * s.count;
-                choice.tiles[kHalfShape] += tiles_of<HalfTile>(s, kind) * s.count;
-                choice.tiles[kSingleShape] += tiles_of<SingleTile>(s, kind) * s.count;
+                choice.tiles[kWideShape] += tiles_of<WideTile>(s, kind) * s.count;
+                choice.tiles[kSmallShape] += tiles_of<SmallTile>(s, kind) * s.count;
                 // the list's average
                 steps += up(kind == kGram ? std::max(s.rows, s.cols) : s.side, kStepK) / kStepK * tiles_of<PairTile>(s, kind) * s.count;
             }
@@ -771,8 +796,8 @@ bool run_steps(const Group& g, const adamw_ortho_t& o, const float* coefs, int l
             const int shape = choose_shape(choice, steps, d.pairs, d.sms);
             ProductParams p;
             if (!(shape == kPairShape   ? fill<PairTile>(g, kind, k & 1, &p)
-                  : shape == kHalfShape ? fill<HalfTile>(g, kind, k & 1, &p)
-                                        : fill<SingleTile>(g, kind, k & 1, &p)))
+                  : shape == kWideShape ? fill<WideTile>(g, kind, k & 1, &p)
+                                        : fill<SmallTile>(g, kind, k & 1, &p)))
                 return false;
             p.a = c[0];
             p.b = c[1];
@@ -781,11 +806,12 @@ bool run_steps(const Group& g, const adamw_ortho_t& o, const float* coefs, int l
             p.table = with.table;
             p.hp = with.hp;
             p.nonfinite = with.nonfinite;
-            if (!(shape == kPairShape   ? launch_kind<PairTile>(which, p, d.pairs, st)
-                  : shape == kHalfShape ? launch_kind<HalfTile>(which, p, d.pairs, st)
-                                        : launch_kind<SingleTile>(which, p, d.sms, st)))
+            if (!(shape == kPairShape   ? launch_kind<PairTile>(which, low_in, low_out, p, d.pairs, st)
+                  : shape == kWideShape ? launch_kind<WideTile>(which, low_in, low_out, p, d.sms, st)
+                                        : launch_kind<SmallTile>(which, low_in, low_out, p, d.sms, st)))
                 return false;
         }
+        low_in = low_out;
     }
     return true;
 }
@@ -819,8 +845,11 @@ int check_matrices(const adamw_matrices_t* m, bool written) {
 
 Batch batch_of(const adamw_matrices_t& m) {
     const int size = dtype_size(m.dtype);
-    return {static_cast<char*>(m.data), m.batch_stride, m.row_stride, m.dtype,
-            aligned(m.data, 16) && (m.rows <= 1 || m.row_stride * size % 16 == 0) && (m.batch <= 1 || m.batch_stride * size % 16 == 0)};
+    auto whole = [&](int bytes) {
+        return aligned(m.data, uintptr_t(bytes)) && (m.rows <= 1 || m.row_stride * size % bytes == 0) &&
+               (m.batch <= 1 || m.batch_stride * size % bytes == 0);
+    };
+    return {static_cast<char*>(m.data), m.batch_stride, m.row_stride, m.dtype, whole(16), whole(32)};
 }
 
 // Pieces of the shapes of a launch, from the list's sum number `sum` on.

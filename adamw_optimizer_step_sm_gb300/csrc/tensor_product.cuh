@@ -33,10 +33,10 @@
 
 #ifndef TILE_STEP0
 #define TILE_STEP0 512
-#define TILE_STEP1 384
-#define TILE_STEP2 512
+#define TILE_STEP1 540
+#define TILE_STEP2 500
 #define TILE_REST0 4000
-#define TILE_REST1 2500
+#define TILE_REST1 4000
 #define TILE_REST2 2500
 #endif
 
@@ -164,17 +164,105 @@ __device__ __forceinline__ void tmem_after() { asm volatile("tcgen05.fence::afte
 __device__ __forceinline__ void tmem_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
 // 32 columns of this warp's 32 lanes: v[c] is column c of the thread's lane.
-__device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&v)[32]) {
+__device__ __forceinline__ void tmem_load(uint32_t at, float (&v)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
         "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
-          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
-          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+          "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+          "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
         : "r"(at) : "memory");
+}
+
+// A sector of 32 bytes, at a multiple of 32.
+struct Sector {
+    uint32_t w[8];
+};
+__device__ __forceinline__ Sector load_sector(const void* p) {
+    Sector s;
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(s.w[0]), "=r"(s.w[1]), "=r"(s.w[2]), "=r"(s.w[3]), "=r"(s.w[4]), "=r"(s.w[5]), "=r"(s.w[6]), "=r"(s.w[7])
+                 : "l"(__cvta_generic_to_global(p)) : "memory");
+    return s;
+}
+__device__ __forceinline__ void store_sector(void* p, const Sector& s) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(__cvta_generic_to_global(p)), "r"(s.w[0]),
+                 "r"(s.w[1]), "r"(s.w[2]), "r"(s.w[3]), "r"(s.w[4]), "r"(s.w[5]), "r"(s.w[6]), "r"(s.w[7])
+                 : "memory");
+}
+// Sixteen values of 16 bits, or eight fp32, in a sector.
+template <int DT>
+__device__ __forceinline__ Sector pack_sector(const float* v) {
+    Sector s;
+    if (DT == ADAMW_DTYPE_FP32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s.w[i] = __float_as_uint(v[i]);
+    } else {
+        const uint4 a = Elem<DT>::pack(v), b = Elem<DT>::pack(v + 8);
+        s.w[0] = a.x, s.w[1] = a.y, s.w[2] = a.z, s.w[3] = a.w;
+        s.w[4] = b.x, s.w[5] = b.y, s.w[6] = b.z, s.w[7] = b.w;
+    }
+    return s;
+}
+template <int DT>
+__device__ __forceinline__ void unpack_sector(const Sector& s, float* v) {
+    if (DT == ADAMW_DTYPE_FP32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(s.w[i]);
+    } else {
+        Elem<DT>::unpack(make_uint4(s.w[0], s.w[1], s.w[2], s.w[3]), v);
+        Elem<DT>::unpack(make_uint4(s.w[4], s.w[5], s.w[6], s.w[7]), v + 8);
+    }
+}
+// 32 values, of which the first n are there, to a row at a multiple of 32 bytes.
+template <int DT>
+__device__ __forceinline__ void store_row(char* at, const float (&v)[32], int n) {
+    constexpr int k = 32 / Elem<DT>::kSize;   // values of a sector
+#pragma unroll
+    for (int i = 0; i < 32; i += k) {
+        if (i + k <= n) {
+            store_sector(at + i * Elem<DT>::kSize, pack_sector<DT>(v + i));
+        } else {
+#pragma unroll
+            for (int e = i; e < i + k; ++e)
+                if (e < n) Elem<DT>::store(at, e, v[e]);
+        }
+    }
+}
+template <int DT>
+__device__ __forceinline__ void load_row(const char* at, float (&v)[32], int n) {
+    constexpr int k = 32 / Elem<DT>::kSize;
+#pragma unroll
+    for (int i = 0; i < 32; i += k) {
+        if (i + k <= n) {
+            unpack_sector<DT>(load_sector(at + i * Elem<DT>::kSize), v + i);
+        } else {
+#pragma unroll
+            for (int e = i; e < i + k; ++e) v[e] = e < n ? Elem<DT>::load(at, e) : 0.0f;
+        }
+    }
+}
+__device__ __forceinline__ void store_row(char* at, int32_t dtype, const float (&v)[32], int n) {
+    if (dtype == ADAMW_DTYPE_BF16) store_row<ADAMW_DTYPE_BF16>(at, v, n);
+    else if (dtype == ADAMW_DTYPE_FP16) store_row<ADAMW_DTYPE_FP16>(at, v, n);
+    else store_row<ADAMW_DTYPE_FP32>(at, v, n);
+}
+__device__ __forceinline__ void load_row(const char* at, int32_t dtype, float (&v)[32], int n) {
+    if (dtype == ADAMW_DTYPE_BF16) load_row<ADAMW_DTYPE_BF16>(at, v, n);
+    else if (dtype == ADAMW_DTYPE_FP16) load_row<ADAMW_DTYPE_FP16>(at, v, n);
+    else load_row<ADAMW_DTYPE_FP32>(at, v, n);
+}
+__device__ __forceinline__ void store_as(char* at, int64_t i, int32_t dtype, float v) {
+    if (dtype == ADAMW_DTYPE_BF16) Elem<ADAMW_DTYPE_BF16>::store(at, i, v);
+    else if (dtype == ADAMW_DTYPE_FP16) Elem<ADAMW_DTYPE_FP16>::store(at, i, v);
+    else Elem<ADAMW_DTYPE_FP32>::store(at, i, v);
+}
+__device__ __forceinline__ float load_as(const char* at, int64_t i, int32_t dtype) {
+    return dtype == ADAMW_DTYPE_BF16   ? Elem<ADAMW_DTYPE_BF16>::load(at, i)
+           : dtype == ADAMW_DTYPE_FP16 ? Elem<ADAMW_DTYPE_FP16>::load(at, i) : Elem<ADAMW_DTYPE_FP32>::load(at, i);
 }
 
 // ------------------------------------------------- operands in shared memory
@@ -255,22 +343,20 @@ struct TileShape {
     static constexpr uint32_t kColumns = 2 * kCols;   // of tensor memory
     static_assert(kStages <= 16 && kColumns <= 512 && (kColumns & (kColumns - 1)) == 0, "tile shape");
 };
-using PairTile = TileShape<2, 256>;     // 256 x 256
-using HalfTile = TileShape<2, 128>;     // 256 x 128
-using SingleTile = TileShape<1, 128>;   // 128 x 128
+using PairTile = TileShape<2, 256>;     // 256 x 256 by a pair
+using WideTile = TileShape<1, 256>;     // 128 x 256 by one CTA
+using SmallTile = TileShape<1, 128>;    // 128 x 128 by one CTA
 
 // Which shape a product takes: the one whose list of tiles is done first by
-// this estimate, in cycles.  A step's time is that of shared memory (each SM
-// writes and reads what it loads of it, 128 bytes a cycle): 512 for PairTile,
-// 384 for HalfTile, 512 for SingleTile, against 512, 256 and 256 of the tensor
-// cores; the last tile's epilogue is not hidden.
+// this estimate, in cycles: a step of 64 k takes TILE_STEP, and what a tile's
+// epilogue takes beyond its neighbour's products TILE_REST.
 struct TileChoice {
     int64_t tiles[3];   // of each shape; 0: not to be taken
 };
-constexpr int kPairShape = 0, kHalfShape = 1, kSingleShape = 2;
+constexpr int kPairShape = 0, kWideShape = 1, kSmallShape = 2;
 inline int choose_shape(const TileChoice& c, int64_t steps, int pairs, int sms) {
     const int64_t step[3] = {TILE_STEP0, TILE_STEP1, TILE_STEP2}, rest[3] = {TILE_REST0, TILE_REST1, TILE_REST2};
-    const int units[3] = {pairs, pairs, sms};
+    const int units[3] = {pairs, sms, sms};
     int best = -1;
     int64_t least = 0;
     for (int k = 0; k < 3; ++k) {
@@ -282,7 +368,7 @@ inline int choose_shape(const TileChoice& c, int64_t steps, int pairs, int sms) 
             least = t;
         }
     }
-    return best < 0 ? kSingleShape : best;
+    return best < 0 ? kSmallShape : best;
 }
 
 template <class P>
@@ -306,15 +392,17 @@ constexpr int tile_threads() { return 128 + 32 * P::kWarps; }
 //   bf16(p)                              type of the operands
 //   Out: what the epilogue keeps of a tile; out<S>(p, table, tile, rank)
 //   wanted(p, out, row, col): whether the 32 x 32 block there has anything to store
-//   Extra, fetch(p, out, row, col, Extra&): what store will want of memory,
-//        fetched a block ahead;  Late, fetch_late: the same, of the block itself
-//   store(p, out, row, col, extra, late, float (&v)[8]): eight columns from `col` of
-//        row `row` of the CTA's 128 x kCols part; leaves in v what the
-//        mirrored tile holds
-//   mirrored(out), mirror(p, out, col, row, v): eight rows from `row` of column
-//        `col`, for the transposed tile
+//   Extra, fetch(p, out, row, col, Extra&): what store wants of memory for 32
+//        columns from `col` of row `row` of the CTA's part, fetched a block ahead
+//   store(p, out, row, col, extra, float (&v)[32]): the results there; leaves
+//        in v what mirror or store_one store
+//   mirrored(out), mirror(p, out, row, col, v): the transposed tile's elements;
+//        neighbouring lanes have neighbouring rows
 //   scalar(out), store_one(p, out, row, col, v): whether results go element by
 //        element (rows that are not whole vectors), neighbours by neighbouring lanes
+// A thread has a row, and reads and writes whole 32-byte sectors of it: no
+// shared memory between tensor memory and the results, and a tenth of the
+// instructions of an epilogue that regroups them (1.7 us a block before).
 template <class P, class S>
 __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid_constant__ typename P::Params p) {
     constexpr int PAIR = S::kPair;
@@ -470,65 +558,30 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
             const int row0 = warp % 4 * 32;
             constexpr int kNext = P::kWarps * 8;   // columns to the warp's next block
             const int c0 = (warp - 4) / 4 * 32;
-            // what the epilogue reads of memory is fetched a block ahead
-            typename P::Extra next[4];
-            if (P::wanted(p, out, row0, c0)) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) P::fetch(p, out, row0 + i * 8 + lane / 4, c0 + lane % 4 * 8, next[i]);
-            }
+            const int row = row0 + lane;
+            typename P::Extra next;
+            if (P::wanted(p, out, row0, c0)) P::fetch(p, out, row, c0, next);
             if (w.k_len > 0) {
                 if (!(ok = wait.warp(smem_addr(&ctl->acc_full[acc]), n >> 1 & 1))) break;
                 tmem_after();
             }
             for (int c = c0; c < S::kCols; c += kNext) {
                 if (!P::wanted(p, out, row0, c)) continue;
-                typename P::Extra now[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) now[i] = next[i];
-                if (c + kNext < S::kCols && P::wanted(p, out, row0, c + kNext)) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) P::fetch(p, out, row0 + i * 8 + lane / 4, c + kNext + lane % 4 * 8, next[i]);
-                }
-                typename P::Late late[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) P::fetch_late(p, out, row0 + i * 8 + lane / 4, c + lane % 4 * 8, late[i]);
-                uint32_t v[32];
+                const typename P::Extra now = next;
+                if (c + kNext < S::kCols && P::wanted(p, out, row0, c + kNext)) P::fetch(p, out, row, c + kNext, next);
+                float v[32];
                 if (w.k_len > 0) {
                     tmem_load(tmem + (uint32_t(row0) << 16) + acc * S::kCols + uint32_t(c), v);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0;
+                    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
                 }
+                P::store(p, out, row, c, now, v);
+                if (P::mirrored(out)) P::mirror(p, out, row, c, v);
+                if (P::scalar(out)) {
 #pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                    *reinterpret_cast<uint4*>(place(lane, i)) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                __syncwarp();
-                const bool mirrored = P::mirrored(out), scalar = P::scalar(out);
-#pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                    const int r = i + lane / 4, q = lane % 4 * 8;
-                    float x[8];
-                    *reinterpret_cast<float4*>(x) = *reinterpret_cast<float4*>(place(r, q));
-                    *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<float4*>(place(r, q + 4));
-                    P::store(p, out, row0 + r, c + q, now[i / 8], late[i / 8], x);
-                    if (mirrored || scalar) {
-                        *reinterpret_cast<float4*>(place(r, q)) = *reinterpret_cast<float4*>(x);
-                        *reinterpret_cast<float4*>(place(r, q + 4)) = *reinterpret_cast<float4*>(x + 4);
-                    }
-                }
-                __syncwarp();
-                if (mirrored) {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        const int j = i + lane / 4, q = lane % 4 * 8;
-                        float x[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = *place(q + e, j);
-                        P::mirror(p, out, c + j, row0 + q, x);
-                    }
+                    for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(place(lane, i)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                     __syncwarp();
-                }
-                if (scalar) {
 #pragma unroll 4
                     for (int r = 0; r < 32; ++r) P::store_one(p, out, row0 + r, c + lane, *place(r, lane));
                     __syncwarp();
