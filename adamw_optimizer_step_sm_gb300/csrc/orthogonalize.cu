@@ -202,6 +202,20 @@ struct Source {
             unpack_raw<DT>(r.a, r.b, u);
         }
     }
+    // one element
+    __device__ __forceinline__ float one(int row, int col, float* m) const {
+        const int64_t at = row * ld + col;
+        float u = Elem<DT>::load(data, at);
+        if (MUON) {
+            const float g = Elem<ADAMW_DTYPE_BF16>::load(grad, at);
+            *m = fmaf(1.0f - mu, g - u, u);
+            u = nesterov ? fmaf(mu, *m - g, g) : *m;
+        }
+        return u;
+    }
+    __device__ __forceinline__ void put_one(int row, int col, float m) const {
+        if (MUON) Elem<DT>::store(const_cast<char*>(data), row * ld + col, m);
+    }
     __device__ __forceinline__ void put(int row, int col, const float (&m)[8]) const {
         if (MUON) store8_any(const_cast<char*>(data), row * ld + col, DT, vector, cols - col, m);
     }
@@ -293,6 +307,13 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const __grid_constan
     }
 }
 
+// What brings a matrix of this sum of squares to 2^12 times the norm 1; NaN for
+// a sum that is not finite: the matrix has no direction.
+__device__ __forceinline__ float scale_of(double sum, float eps) {
+    const double norm = sqrt(sum);
+    return sum <= 1.7976931348623157e308 ? float(double(kScale) / (norm > eps ? norm : double(eps))) : sqrtf(-1.0f);
+}
+
 // x at 2^12 times its value, as two fp16.
 __device__ __forceinline__ void split8(const float (&x)[8], uint4* hi, uint4* lo) {
     *hi = Fp16::pack(x);
@@ -321,9 +342,7 @@ __global__ void __launch_bounds__(kNormThreads) copy_kernel(const __grid_constan
     __syncthreads();
     sum = 0.0;
     for (int k = 0; k < kNormThreads / 32; ++k) sum += part[k];
-    const double norm = sqrt(sum);
-    // NaN for a sum that is not finite: the matrix has no direction
-    const float by = sum <= 1.7976931348623157e308 ? float(double(kScale) / (norm > p.eps ? norm : double(p.eps))) : sqrtf(-1.0f);
+    const float by = scale_of(sum, p.eps);
     const Source<MUON, DT> src(p, c, matrix);
     const Walk walk(c.s, i);
     uint4* hi = reinterpret_cast<uint4*>(c.hi + matrix * c.s.stride) + int64_t(i) * kPieceVecs;
@@ -872,6 +891,8 @@ int64_t fill_copies(const Group& g, const int32_t* first_sum, CopyParams<MUON>* 
 
 }  // namespace
 
+#include "orthogonalize_small.cuh"
+
 namespace adamw {
 int ortho_status(int32_t* out) {
     int32_t v = 0;
@@ -924,10 +945,17 @@ extern "C" int adamw_orthogonalize(const adamw_matrices_t* src, const adamw_matr
     CopyParams<false> c;
     memset(&c, 0, sizeof c);
     const int32_t first_sum = 0;
-    fill_copies(g, &first_sum, &c);
     c.sums = static_cast<double*>(workspace);
     c.eps = ortho->eps;
     c.src = batch_of(*src);
+    if (small_ctas(s) > 0) {
+        SmallParams<false> p;
+        memset(&p, 0, sizeof p);
+        p.in = c;
+        p.dst = batch_of(*dst);
+        return launch_small(g, &first_sum, *ortho, ortho->coefficients, src->dtype, d.sms, &p, st) ? ADAMW_OK : ADAMW_ERR_CUDA;
+    }
+    fill_copies(g, &first_sum, &c);
     if (!launched(launch(norm_of<false>(src->dtype), uint32_t(pieces), kNormThreads, 1, 0, st, c), "norm launch") ||
         !launched(launch(copy_of<false>(src->dtype), uint32_t(pieces), kNormThreads, 1, 0, st, c), "copy launch"))
         return ADAMW_ERR_CUDA;
@@ -1062,7 +1090,10 @@ int create(const adamw_muon_tensor_t* table, int32_t n, const adamw_muon_options
         }
         order.push_back({t.rows, t.cols, k});
     }
-    std::stable_sort(order.begin(), order.end(), [](const Entry& a, const Entry& b) {
+    // the small ones, which have a kernel of their own, last
+    auto is_small = [](const Entry& e) { return small_ctas(shape_of(e.rows, e.cols)) > 0; };
+    std::stable_sort(order.begin(), order.end(), [&](const Entry& a, const Entry& b) {
+        if (is_small(a) != is_small(b)) return is_small(b);
         return a.rows * a.cols != b.rows * b.cols ? a.rows * a.cols > b.rows * b.cols : a.rows > b.rows;
     });
     std::vector<MuonMatrix> matrices;
@@ -1088,12 +1119,14 @@ int create(const adamw_muon_tensor_t* table, int32_t n, const adamw_muon_options
             part.first = s.first + done;
             part.count = 1;
             const int64_t one = place(part, nullptr, nullptr);
-            if (P->rounds.empty() || P->rounds.back().n == kMaxShapes || (used > 0 && used + one > kRoundBytes)) {
+            const bool small = small_ctas(part) > 0;
+            if (P->rounds.empty() || P->rounds.back().n == kMaxShapes || (!small && used > 0 && used + one > kRoundBytes) ||
+                (small_ctas(P->rounds.back().shapes[0]) > 0) != small) {
                 P->rounds.emplace_back();
                 P->sums.emplace_back();
                 used = 0;
             }
-            const int64_t room = (kRoundBytes - used) / one;
+            const int64_t room = small ? s.count : (kRoundBytes - used) / one;
             part.count = int32_t(std::min<int64_t>(s.count - done, std::max<int64_t>(room, 1)));
             Group& g = P->rounds.back();
             g.shapes[g.n] = part;
@@ -1102,7 +1135,7 @@ int create(const adamw_muon_tensor_t* table, int32_t n, const adamw_muon_options
             P->sums.back().push_back(int32_t(sums));
             sums += pieces_of(part) * part.count;
             if (sums > kMaxCount) return ADAMW_ERR_TOO_LARGE;
-            used += place(part, nullptr, nullptr);
+            if (!small) used += place(part, nullptr, nullptr);
             work = std::max(work, used);
             done += part.count;
         }
@@ -1115,7 +1148,7 @@ int create(const adamw_muon_tensor_t* table, int32_t n, const adamw_muon_options
     P->work = static_cast<char*>(P->block) + table_bytes + sum_bytes;
     for (Group& g : P->rounds) {
         char* at = P->work;
-        for (int i = 0; i < g.n; ++i) at += place(g.shapes[i], at, &g.buffers[i]);
+        for (int i = 0; i < g.n && small_ctas(g.shapes[i]) == 0; ++i) at += place(g.shapes[i], at, &g.buffers[i]);
     }
     const bool ok = launched(cudaMemcpy(P->table, matrices.data(), matrices.size() * sizeof(MuonMatrix), cudaMemcpyHostToDevice),
                              "cudaMemcpy(table)") &&
@@ -1179,7 +1212,16 @@ extern "C" int adamw_muon_step(adamw_muon_plan_t plan, const adamw_muon_hparams_
     with.table = plan->table;
     with.hp = hparams;
     with.nonfinite = nonfinite;
+    const int32_t dtype = plan->momentum_bf16 ? ADAMW_DTYPE_BF16 : ADAMW_DTYPE_FP32;
     for (size_t r = 0; r < plan->rounds.size(); ++r) {
+        if (small_ctas(plan->rounds[r].shapes[0]) > 0) {
+            SmallParams<true> p;
+            memset(&p, 0, sizeof p);
+            p.in = c;
+            if (!launch_small(plan->rounds[r], plan->sums[r].data(), plan->ortho, plan->coefs.data(), dtype, d.sms, &p, st))
+                return ADAMW_ERR_CUDA;
+            continue;
+        }
         const int64_t pieces = fill_copies(plan->rounds[r], plan->sums[r].data(), &c);
         if (!launched(launch(copy_of<true>(plan->momentum_bf16 ? ADAMW_DTYPE_BF16 : ADAMW_DTYPE_FP32), uint32_t(pieces), kNormThreads, 1, 0, st, c), "copy launch")) return ADAMW_ERR_CUDA;
         if (!run_steps(plan->rounds[r], plan->ortho, plan->coefs.data(), kUpdate, with, d, st)) return ADAMW_ERR_CUDA;

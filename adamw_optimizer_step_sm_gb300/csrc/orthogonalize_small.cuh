@@ -1,0 +1,380 @@
+// orthogonalize_small.cuh -- the whole iteration of small matrices in one
+// kernel: a cluster of up to eight CTAs has a matrix of at most 128 x 1024 (or
+// 1024 x 128), 128 of the long side each, and takes all steps on chip.
+// Included by orthogonalize.cu, whose products take 17 launches for a matrix
+// of any size, each a few microseconds whatever it computes.
+//
+// X stays in registers, in fp32; shared memory holds what the tensor cores
+// read, in fp16 at 2^12 times its value as in the large form: X's part, G and
+// Q. The sum G = X X^T over the cluster goes through distributed shared memory:
+// each CTA adds up its share of G's rows over all parts, in their order, and
+// hands the sums to all. A step is three products one after the other, each
+// about a microsecond from operands in shared memory to results there.
+#pragma once
+
+namespace {
+
+constexpr int kSmallThreads = 256;
+constexpr int kSmallSide = 128, kSmallMost = 8;   // largest side, CTAs of a cluster
+constexpr uint32_t kPlane = 128 * 128;            // 64 columns of 128 rows of fp16
+constexpr uint32_t kSmallBytes = 1024 + 6 * kPlane, kSmallSumBytes = 128 * 128 * 4;
+
+template <bool MUON>
+struct SmallParams {
+    CopyParams<MUON> in;              // shapes, source, norms of a plan
+    int32_t first_cluster[kMaxShapes];
+    float rate[kMaxShapes];
+    float coefs[32][3];
+    int32_t steps;
+    Batch dst;
+};
+
+struct SmallControl {
+    uint64_t done;
+    uint32_t tmem;
+    int32_t failed;
+    double part[kSmallThreads / 32], sum;
+};
+
+// 16-byte unit j (eight columns) of row r in a plane, as the tensor cores read it.
+__device__ __forceinline__ uint32_t unit_at(int r, int j) { return uint32_t(r * 128 + ((j ^ (r & 7)) << 4)); }
+
+// This CTA's share of G's rows, added up over the cluster's parts and handed to
+// all: 16 loads of each thread in flight.
+template <int CTAS>
+__device__ __forceinline__ void add_up(float* sums, unsigned char* gs, uint32_t rank) {
+    float4 v[16 / CTAS][CTAS];
+#pragma unroll
+    for (int i = 0; i < 16 / CTAS; ++i) {
+        const int at = i * kSmallThreads + int(threadIdx.x), row = int(rank) * (128 / CTAS) + at / 32, u = at % 32;
+        const uint32_t from = smem_addr(sums + row * 128 + ((u ^ (row & 31)) << 2));   // four columns
+#pragma unroll
+        for (int o = 0; o < CTAS; ++o)
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(v[i][o].x), "=f"(v[i][o].y), "=f"(v[i][o].z), "=f"(v[i][o].w) : "r"(in_cta(from, uint32_t(o))) : "memory");
+    }
+#pragma unroll
+    for (int i = 0; i < 16 / CTAS; ++i) {
+        const int at = i * kSmallThreads + int(threadIdx.x), row = int(rank) * (128 / CTAS) + at / 32, u = at % 32;
+        float4 t = v[i][0];
+#pragma unroll
+        for (int o = 1; o < CTAS; ++o) t = make_float4(t.x + v[i][o].x, t.y + v[i][o].y, t.z + v[i][o].z, t.w + v[i][o].w);
+        const __half2 lo = __floats2half2_rn(t.x, t.y), hi = __floats2half2_rn(t.z, t.w);
+        uint32_t w[2];
+        memcpy(&w[0], &lo, 4);
+        memcpy(&w[1], &hi, 4);
+        const uint32_t to = smem_addr(gs + (u / 16) * kPlane + unit_at(row, u % 16 / 2) + u % 2 * 8);
+#pragma unroll
+        for (int o = 0; o < CTAS; ++o)
+            asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(in_cta(to, uint32_t(o))), "r"(w[0]), "r"(w[1]) : "memory");
+    }
+}
+
+template <bool MUON, int DT>
+__global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_constant__ SmallParams<MUON> p) {
+    extern __shared__ unsigned char raw[];
+    __shared__ SmallControl ctl;
+    unsigned char* base = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
+    unsigned char *xs = base, *gs = base + 2 * kPlane, *qs = base + 4 * kPlane;
+    float* sums = reinterpret_cast<float*>(base + 6 * kPlane);   // with a cluster only
+
+    const int warp = int(threadIdx.x) / 32, lane = int(threadIdx.x) % 32;
+    const uint32_t rank = cluster_rank(), ctas = cluster_size();
+    const int r = warp % 4 * 32 + lane, h = warp / 4;   // the thread's row, and its 64 columns
+    const uint32_t bar = smem_addr(&ctl.done);
+    if (threadIdx.x == 0) {
+        barrier_init(bar, 1);
+        ctl.failed = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) tmem_alloc<1>(smem_addr(&ctl.tmem), 128);
+    int k = 0;
+    const int cluster = int(blockIdx.x / ctas);
+    while (k + 1 < p.in.n && p.first_cluster[k + 1] <= cluster) ++k;
+    const CopyShape& c = p.in.shapes[k];
+    const int matrix = cluster - p.first_cluster[k];
+    const int rows = c.s.rows, cols = c.s.cols, side = c.s.side;
+    const bool wide = rows <= cols;
+    const int at = int(rank) * 128, length = wide ? cols : rows;
+    const int mine = length - at < 0 ? 0 : length - at < 128 ? length - at : 128;   // of the long side
+    tmem_before();
+    __syncthreads();
+    tmem_after();
+    const uint32_t tmem = *static_cast<volatile uint32_t*>(&ctl.tmem) + (uint32_t(warp % 4 * 32) << 16) + uint32_t(h * 64);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const bool skip = MUON && *p.in.nonfinite != 0;
+
+    // ---- X, unscaled, and its norm
+    const Source<MUON, DT> src(p.in, c, matrix);
+    float x[64];
+    const int valid = r < side ? (mine - h * 64 < 64 ? mine - h * 64 : 64) : 0;   // of the thread's values
+    // all loads of a batch before its first store, which they would wait for
+    if (wide) {
+        Raw w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j * 8 < valid) w[j] = src.load(r, at + h * 64 + j * 8);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float u[8], m[8];
+            if (j * 8 < valid) {
+                src.value(w[j], u, m);
+                if (MUON && !skip) src.put(r, at + h * 64 + j * 8, m);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[j * 8 + e] = j * 8 + e < valid ? u[e] : 0.0f;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 64; i += 32) {
+            float m[MUON ? 32 : 1];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[i + e] = i + e < valid ? src.one(at + h * 64 + i + e, r, m + (MUON ? e : 0)) : 0.0f;
+            if (MUON && !skip) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (i + e < valid) src.put_one(at + h * 64 + i + e, r, m[MUON ? e : 0]);
+            }
+        }
+    }
+    double sum = 0.0;
+    if (MUON) {
+        for (int i = 0; i < c.pieces; ++i) sum += p.in.sums[c.first_sum + matrix * c.pieces + i];
+    } else {
+        Sum2 total = {0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float s = 0.0f, any = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                s = fmaf(x[j * 8 + e], x[j * 8 + e], s);
+                any = any == 0.0f ? x[j * 8 + e] : any;
+            }
+            if (s >= 0x1p-100f && s <= 0x1p100f) {
+                total.add(s);
+            } else if (any != 0.0f) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum += double(x[j * 8 + e]) * double(x[j * 8 + e]);
+            }
+        }
+        sum += double(total.hi) + double(total.lo);
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane == 0) ctl.part[warp] = sum;
+        __syncthreads();
+        sum = 0.0;
+        for (int i = 0; i < kSmallThreads / 32; ++i) sum += ctl.part[i];
+        if (ctas > 1) {
+            if (threadIdx.x == 0) ctl.sum = sum;
+            cluster_sync();
+            sum = 0.0;
+            for (uint32_t i = 0; i < ctas; ++i) {
+                double v;
+                asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(in_cta(smem_addr(&ctl.sum), i)) : "memory");
+                sum += v;
+            }
+        }
+    }
+    const float by = scale_of(sum, p.in.eps);
+#pragma unroll
+    for (int e = 0; e < 64; ++e) x[e] *= by;
+
+    // ---- the steps
+    uint32_t turn = 0;
+    const Waiter wait = {&ctl.failed};
+    const uint32_t xa = smem_addr(xs), ga = smem_addr(gs), qa = smem_addr(qs), out = *static_cast<volatile uint32_t*>(&ctl.tmem);
+    // what is there of k; all 128 rows and columns are computed, zeros beyond the matrix
+    const int side16 = (side + 15) / 16 * 16, mine16 = mine > 0 ? (mine + 15) / 16 * 16 : 16;
+    // D = A B^T over `depth` k; B read K-major, or MN-major (then its rows are k)
+    auto product = [&](uint32_t a, uint32_t b, bool b_mn, int depth) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tmem_before();
+        __syncthreads();
+        tmem_after();
+        if (warp == 0 && elected()) {
+            const uint32_t kind = mma_kind(0, false, b_mn, 128, 128);
+            const uint64_t da = operand(a, false), db = operand(b, b_mn, kPlane);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint64_t along = uint64_t(i / 4) * (kPlane >> 4) + uint64_t(i % 4) * 2;   // 16 k of rows of 128 bytes
+                if (i * 16 < depth) mma<1>(out, da + along, db + (b_mn ? uint64_t(i) * 128 : along), kind, i > 0);
+            }
+            commit<1>(bar);
+        }
+        __syncwarp();
+        wait.warp(bar, turn);   // a failure is in the status word; the cluster stays together
+        turn ^= 1;
+        tmem_after();
+    };
+    for (int step = 0; step < p.steps; ++step) {
+        const float a = p.coefs[step][0], b = p.coefs[step][1], q = p.coefs[step][2] * kUnscale;
+        unsigned char* plane = xs + h * kPlane;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(plane + unit_at(r, j)) = Fp16::pack(x + j * 8);
+        // G
+        product(xa, xa, false, mine16);
+        plane = gs + h * kPlane;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float v[32];
+            tmem_load(tmem + i * 32, v);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] *= kUnscale;
+            if (ctas == 1) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(plane + unit_at(r, i * 4 + j)) = Fp16::pack(v + j * 8);
+            } else {
+                // rows of 512 bytes, their 16-byte units XORed with the row
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<float4*>(sums + r * 128 + (((h * 16 + i * 8 + j) ^ (r & 31)) << 2)) =
+                        make_float4(v[j * 4], v[j * 4 + 1], v[j * 4 + 2], v[j * 4 + 3]);
+            }
+        }
+        if (ctas > 1) {
+            cluster_sync();
+            if (ctas == 2) add_up<2>(sums, gs, rank);
+            else if (ctas == 4) add_up<4>(sums, gs, rank);
+            else add_up<8>(sums, gs, rank);
+            cluster_sync();
+        }
+        // Q
+        product(ga, ga, false, side16);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float v[32];
+            tmem_load(tmem + i * 32, v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float g[8];
+                Fp16::unpack(*reinterpret_cast<const uint4*>(gs + h * kPlane + unit_at(r, i * 4 + j)), g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) g[e] = fmaf(b, g[e], q * v[j * 8 + e]);
+                *reinterpret_cast<uint4*>(qs + h * kPlane + unit_at(r, i * 4 + j)) = Fp16::pack(g);
+            }
+        }
+        // X
+        product(qa, xa, true, side16);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float v[32];
+            tmem_load(tmem + i * 32, v);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[i * 32 + e] = fmaf(a, x[i * 32 + e], v[e] * kUnscale);
+        }
+    }
+
+    // ---- the result, or the update
+    if (valid > 0 && !skip) {
+        char *dst, *param = nullptr;
+        int64_t ld;
+        int32_t type = ADAMW_DTYPE_FP32;
+        float rate = kUnscale, decay = 0.0f;
+        if (MUON) {
+            const MuonMatrix t = p.in.table[c.s.first + matrix];
+            dst = reinterpret_cast<char*>(t.master);
+            param = reinterpret_cast<char*>(t.param);
+            ld = cols;
+            const float lr = p.in.hp->lr;
+            decay = 1.0f - lr * p.in.hp->weight_decay;
+            rate = -lr * p.rate[k] * kUnscale;
+        } else {
+            type = p.dst.dtype;
+            dst = p.dst.data + matrix * p.dst.batch_stride * (type == ADAMW_DTYPE_FP32 ? 4 : 2);
+            ld = p.dst.row_stride;
+        }
+        auto place = [&](int e) { return wide ? int64_t(r) * ld + at + h * 64 + e : int64_t(at + h * 64 + e) * ld + r; };
+        const bool vector = wide && (MUON ? ld % 8 == 0 && (reinterpret_cast<uintptr_t>(dst) | reinterpret_cast<uintptr_t>(param)) % 16 == 0
+                                          : p.dst.vector != 0);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float v[8];
+            if (vector && j * 8 + 8 <= valid) {
+                const int64_t to = place(j * 8);
+                if (MUON) {
+                    *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(dst + to * 4);
+                    *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(dst + to * 4 + 16);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = MUON ? fmaf(rate, x[j * 8 + e], decay * v[e]) : x[j * 8 + e] * rate;
+                store8_any(dst, to, type, true, 8, v);
+                if (MUON) store8_any(param, to, ADAMW_DTYPE_BF16, true, 8, v);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (j * 8 + e >= valid) break;
+                    const int64_t to = place(j * 8 + e);
+                    float w = x[j * 8 + e] * rate;
+                    if (MUON) w = fmaf(rate, x[j * 8 + e], decay * reinterpret_cast<const float*>(dst)[to]);
+                    store_as(dst, to, type, w);
+                    if (MUON) store_as(param, to, ADAMW_DTYPE_BF16, w);
+                }
+            }
+        }
+    }
+    tmem_before();
+    if (ctas > 1) cluster_sync();   // nobody reads this CTA's memory any more
+    __syncthreads();
+    tmem_after();
+    if (warp == 0) tmem_free<1>(out, 128);
+}
+
+template <bool MUON>
+using SmallKernel = void (*)(SmallParams<MUON>);
+template <bool MUON>
+SmallKernel<MUON> small_of(int32_t dtype) {
+    return dtype == ADAMW_DTYPE_FP32 ? small_kernel<MUON, ADAMW_DTYPE_FP32>
+           : dtype == ADAMW_DTYPE_BF16 ? small_kernel<MUON, ADAMW_DTYPE_BF16> : small_kernel<MUON, MUON ? ADAMW_DTYPE_BF16 : ADAMW_DTYPE_FP16>;
+}
+
+// CTAs of a cluster for a shape; 0: too large.
+inline int small_ctas(const Shape& s) {
+    const int length = s.rows > s.cols ? s.rows : s.cols;
+    if (s.side > kSmallSide || length > 128 * kSmallMost) return 0;
+    int n = 1;
+    while (n * 128 < length) n *= 2;
+    return n;
+}
+
+// The shapes of `g`, all small, whose norms (of a plan) begin at `first_sum`.
+template <bool MUON>
+bool launch_small(const Group& g, const int32_t* first_sum, const adamw_ortho_t& o, const float* coefs, int32_t dtype,
+                  int sms, SmallParams<MUON>* p, cudaStream_t st) {
+    p->steps = o.steps;
+    for (int k = 0; k < o.steps; ++k) memcpy(p->coefs[k], coefs + 3 * (k < o.n_coefficients ? k : o.n_coefficients - 1), 12);
+    int most = 1;
+    int64_t matrices = 0;
+    for (int i = 0; i < g.n; ++i) {
+        most = std::max(most, small_ctas(g.shapes[i]));
+        matrices += g.shapes[i].count;
+    }
+    const SmallKernel<MUON> kernel = small_of<MUON>(dtype);
+    // one launch while its CTAs run at a time, though some have nothing to do;
+    // else one for each size of cluster
+    const bool together = matrices * most <= sms;
+    for (int ctas = together ? most : 1; ctas <= most; ctas *= 2) {
+        Group part;
+        int32_t sums[kMaxShapes];
+        int64_t clusters = 0;
+        for (int i = 0; i < g.n; ++i) {
+            if (!together && small_ctas(g.shapes[i]) != ctas) continue;
+            part.shapes[part.n] = g.shapes[i];
+            part.buffers[part.n] = Buffers{};
+            sums[part.n] = first_sum[i];
+            p->rate[part.n] = g.rate[i];
+            p->first_cluster[part.n++] = int32_t(clusters);
+            clusters += g.shapes[i].count;
+        }
+        if (part.n == 0) continue;
+        fill_copies(part, sums, &p->in);
+        const size_t smem = kSmallBytes + (ctas > 1 ? kSmallSumBytes : 0);
+        if (!launched(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmallBytes + kSmallSumBytes)),
+                      "cudaFuncSetAttribute") ||
+            !launched(launch(kernel, uint32_t(clusters * ctas), kSmallThreads, ctas, smem, st, *p), "small launch"))
+            return false;
+    }
+    return true;
+}
+
+}  // namespace

@@ -59,14 +59,6 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ uint32_t cta_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void sync_cluster() {
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
 __device__ __forceinline__ void barrier_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
@@ -273,8 +265,8 @@ __device__ __forceinline__ float load_as(const char* at, int64_t i, int32_t dtyp
 // 8), which TMA writes and the tensor cores read.  The descriptor: address,
 // distance of the 64-wide boxes (MN-major only), distance of groups of eight
 // 128-byte rows, version 1, swizzle mode 2 (128 bytes).
-__device__ __forceinline__ uint64_t operand(uint32_t addr, bool mn) {
-    const uint64_t lead = mn ? (64 * 128) >> 4 : 1;
+__device__ __forceinline__ uint64_t operand(uint32_t addr, bool mn, uint32_t box = 64 * 128) {
+    const uint64_t lead = mn ? box >> 4 : 1;
     return uint64_t((addr & 0x3ffff) >> 4) | lead << 16 | uint64_t(1024 >> 4) << 32 | uint64_t(1) << 46 | uint64_t(2) << 61;
 }
 // What 16 further k add to the descriptor: 32 bytes of each row, or 16 rows.
@@ -310,7 +302,7 @@ static_assert(sizeof(Control) <= kControlRoom, "control block");
 __device__ int32_t g_tile_status;
 
 struct Waiter {
-    Control* c;
+    int32_t* failed;   // the CTA's
     // the same answer for all of a warp
     __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity) const {
         return __all_sync(0xffffffffu, (*this)(bar, parity));
@@ -323,9 +315,9 @@ struct Waiter {
 #pragma unroll 1
             for (int k = 0; k < 64; ++k)
                 if (barrier_test(bar, parity)) return true;
-            if (*static_cast<volatile int32_t*>(&c->failed)) return false;
+            if (*static_cast<volatile int32_t*>(failed)) return false;
             if (clock64() - start > kGiveUp) {
-                *static_cast<volatile int32_t*>(&c->failed) = 1;
+                *static_cast<volatile int32_t*>(failed) = 1;
                 atomicOr(&g_tile_status, 1);
                 return false;
             }
@@ -415,7 +407,7 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
     unsigned char* table = reinterpret_cast<unsigned char*>(ctl) + kControlRoom;
 
     const int warp = int(threadIdx.x) / 32, lane = int(threadIdx.x) % 32;
-    const uint32_t rank = PAIR == 2 ? cta_rank() : 0;
+    const uint32_t rank = PAIR == 2 ? cluster_rank() : 0;
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             barrier_init(smem_addr(&ctl->full[s]), PAIR);
@@ -431,7 +423,7 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
     }
     if (warp == 2) tmem_alloc<PAIR>(smem_addr(&ctl->tmem), S::kColumns);
     tmem_before();
-    if (PAIR == 2) sync_cluster();
+    if (PAIR == 2) cluster_sync();
     __syncthreads();
     tmem_after();
     const uint32_t tmem = *static_cast<volatile uint32_t*>(&ctl->tmem);
@@ -442,7 +434,7 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
 
     const int first = int(blockIdx.x) / PAIR, units = int(gridDim.x) / PAIR;
     const int tiles = P::tiles(p, table);
-    const Waiter wait = {ctl};
+    const Waiter wait = {&ctl->failed};
 
     if (warp == 0) {
         // ---- loads
@@ -603,7 +595,7 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
         for (int k = 0; k < 1000; ++k) __nanosleep(1000);
     }
     tmem_before();
-    if (PAIR == 2) sync_cluster();   // the other CTA's arrivals, and its reads of this one's memory
+    if (PAIR == 2) cluster_sync();   // the other CTA's arrivals, and its reads of this one's memory
     __syncthreads();
     tmem_after();
     if (warp == 2) tmem_free<PAIR>(tmem, S::kColumns);

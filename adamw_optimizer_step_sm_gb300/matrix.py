@@ -27,6 +27,7 @@ _empty = torch.empty
 _matrices_t = A.adamw_matrices_t
 _CODES = {torch.bfloat16: A.DTYPE_BF16, torch.float16: A.DTYPE_FP16, torch.float32: A.DTYPE_FP32}
 _HALVES = (torch.bfloat16, torch.float16)
+_BYTES = torch.uint8
 
 COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 
@@ -39,23 +40,13 @@ def _matrices(x: torch.Tensor) -> A.adamw_matrices_t:
     return _matrices_t(x.data_ptr(), d[0], d[1], d[2], s[0], s[1], _CODES[x.dtype])
 
 
-def _workspace(nbytes: int, device) -> Optional[torch.Tensor]:
-    # torch's allocations start at multiples of 512 bytes
-    return _empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
 # ------------------------------------------------------- orthogonalisation --
 
 _options: dict = {}
 
 
 def _ortho(steps, coefficients, eps):
-    key = (steps, coefficients if isinstance(coefficients[0], float) else tuple(map(tuple, coefficients)), eps) \
-        if isinstance(coefficients, tuple) else None
+    key = (steps, coefficients, eps) if type(coefficients) is tuple and type(coefficients[0]) is float else None
     o = _options.get(key) if key else None
     if o is None:
         if not 1 <= steps <= 32:
@@ -78,108 +69,119 @@ def orthogonalize(x: torch.Tensor, *, steps: int = 5, coefficients=COEFFICIENTS,
     last for the steps beyond).  The result is of ``dtype``, or written to
     ``out`` (which may be x).  A matrix holding inf or NaN gives NaN, a zero
     matrix zeros.  Not differentiable: it is what optimizers do to gradients."""
-    if not x.is_cuda:
-        raise TypeError("want CUDA tensors")
-    if x.dtype not in _CODES:
-        raise TypeError(f"want bfloat16, float16 or float32 matrices, not {x.dtype}")
-    if x.dim() < 2:
+    code, shape = _CODES.get(x.dtype), x.shape
+    nd = len(shape)
+    if code is None or nd < 2 or not x.is_cuda:
+        if not x.is_cuda:
+            raise TypeError("want CUDA tensors")
+        if code is None:
+            raise TypeError(f"want bfloat16, float16 or float32 matrices, not {x.dtype}")
         raise ValueError("want matrices [..., rows, cols]")
-    if (x.requires_grad and torch.is_grad_enabled()) or _tangent(x).tangent is not None:
+    if x.requires_grad and torch.is_grad_enabled() or _tangent(x).tangent is not None:
         raise RuntimeError("orthogonalize has no gradient: detach its input")
-    if out is None:
-        if dtype not in _CODES:
-            raise TypeError(f"want a result in bfloat16, float16 or float32, not {dtype}")
-        out = _empty(x.shape, dtype=dtype, device=x.device)
-        given = None
-    else:
-        if out.shape != x.shape or out.device != x.device or out.dtype not in _CODES:
-            raise ValueError("out must have x's shape and device, in bfloat16, float16 or float32")
-        if (out.requires_grad and torch.is_grad_enabled()):
+    dev = x.device
+    if out is not None:
+        dtype = out.dtype
+        if out.shape != shape or out.device != dev or dtype not in _CODES or not out.is_contiguous():
+            raise ValueError("out must be contiguous, of x's shape and device, in bfloat16, float16 or float32")
+        if out.requires_grad and torch.is_grad_enabled():
             raise RuntimeError("out requires a gradient")
-        given = out
-        if not out.is_contiguous():
-            raise ValueError("out must be contiguous")
-    src = x.detach()
-    if src.dim() != 3:
-        src = src.reshape(-1, *src.shape[-2:]) if src.dim() > 3 else src[None]
-    rows, cols = src.shape[-2:]
-    if src.numel() == 0:
-        return out
-    if src.stride(-1) != 1 and cols > 1:
-        if src.stride(-2) == 1 and given is None and rows > 1:
-            # a transposed view: the transpose's result, transposed
-            dense = src.mT
-            t = _empty(dense.shape, dtype=out.dtype, device=x.device)
-            _run_ortho(dense, t, steps, coefficients, eps)
-            return t.mT.reshape(x.shape) if x.dim() > 3 else t.mT.view(x.shape)
-        src = src.contiguous()
-    _run_ortho(src, out.view(src.shape), steps, coefficients, eps)
-    if given is not None:
-        _written(given)
-    return out
-
-
-def _run_ortho(src, dst, steps, coefficients, eps):
+    elif dtype not in _CODES:
+        raise TypeError(f"want a result in bfloat16, float16 or float32, not {dtype}")
+    ortho = _ortho(steps, coefficients, eps)
+    if x.numel() == 0:
+        return out if out is not None else _empty(shape, dtype=dtype, device=dev)
+    if nd > 3:   # one batch dimension, a copy where the others do not make one
+        x = x.detach().reshape(-1, *shape[-2:])
+    stride = x.stride()
+    rows, cols = shape[-2], shape[-1]
+    turned = False
+    if stride[-1] != 1 and cols > 1:
+        if stride[-2] == 1 and out is None and nd <= 3:
+            turned = True   # a transposed view: the transpose's result, transposed
+        else:
+            x = x.detach().contiguous()
+            stride = x.stride()
+    batch, between = (1, 0) if nd == 2 else (x.shape[0], stride[0])
+    y = out
+    if turned:
+        rows, cols = cols, rows
+        y = _empty((*shape[:-2], rows, cols), dtype=dtype, device=dev)
+    elif y is None:
+        y = _empty(shape, dtype=dtype, device=dev)
     lib = A.load()
-    nbytes = lib.adamw_orthogonalize_workspace(*src.shape)
-    work = _workspace(nbytes, src.device)
-    _call(lib.adamw_orthogonalize, "adamw_orthogonalize", src.device, _byref(_matrices(src)), _byref(_matrices(dst)),
-          _byref(_ortho(steps, coefficients, eps)), _ptr(work))
+    nbytes = lib.adamw_orthogonalize_workspace(batch, rows, cols)
+    # torch's allocations start at multiples of 512 bytes
+    work = _empty(nbytes, dtype=_BYTES, device=dev) if nbytes else None
+    _call(lib.adamw_orthogonalize, "adamw_orthogonalize", dev,
+          _byref(_matrices_t(x.data_ptr(), batch, rows, cols, between, stride[-1] if turned else stride[-2], code)),
+          _byref(_matrices_t(y.data_ptr(), batch, rows, cols, rows * cols, cols, _CODES[dtype])),
+          _byref(ortho), work.data_ptr() if nbytes else None)
+    if out is not None:
+        _written(out)
+    return y.mT if turned else y
 
 
 # ----------------------------------------------------------------- experts --
 
 def _tokens_of(name: str, x: torch.Tensor) -> torch.Tensor:
+    if x.is_cuda and x.dtype in _HALVES and x.dim() == 2 and x.stride(1) == 1:
+        return x
     if not x.is_cuda:
         raise TypeError("want CUDA tensors")
     if x.dtype not in _HALVES:
         raise TypeError(f"want bfloat16 or float16 {name}, not {x.dtype}")
     if x.dim() != 2:
         raise ValueError(f"want {name} [tokens, features]")
-    return x if x.stride(1) == 1 or x.shape[1] <= 1 else x.contiguous()
+    return x if x.shape[1] <= 1 else x.detach().contiguous()
 
 
 def _weight_of(w: torch.Tensor, x: torch.Tensor):
-    """(the experts' matrices with consecutive elements in a row, whether they
-    are the transposes of w's)"""
+    """(the experts' matrices, whether they are the transposes of w's)"""
     if w.dtype != x.dtype or w.device != x.device:
         raise TypeError("want weights of the tokens' type and device")
-    if w.dim() != 3 or w.shape[0] < 1:
+    shape, stride = w.shape, w.stride()
+    if len(shape) != 3 or shape[0] < 1:
         raise ValueError("want weights [experts, out features, in features]")
-    if w.stride(2) == 1 or w.shape[2] <= 1:
-        return w, 0
-    if w.stride(1) == 1:
-        return w.mT, 1
-    return w.contiguous(), 0
+    if stride[2] != 1 and shape[2] > 1:
+        if stride[1] == 1:
+            return _matrices_t(w.data_ptr(), shape[0], shape[2], shape[1], stride[0], stride[2], _CODES[w.dtype]), 1, w
+        w = w.detach().contiguous()
+        stride = w.stride()
+    return _matrices_t(w.data_ptr(), *shape, stride[0], stride[1], _CODES[w.dtype]), 0, w
 
 
 def _offsets_of(offsets: torch.Tensor, experts: int, device) -> torch.Tensor:
+    if offsets.dtype is torch.int64 and offsets.device == device and offsets.shape == (experts + 1,) and offsets.is_contiguous():
+        return offsets
     if offsets.dtype != torch.int64 or offsets.device != device:
         raise TypeError("want int64 offsets on the tokens' device")
     if offsets.shape != (experts + 1,):
         raise ValueError(f"want {experts + 1} offsets for {experts} experts, not {tuple(offsets.shape)}")
-    return offsets if offsets.is_contiguous() else offsets.contiguous()
+    return offsets.contiguous()
 
 
 def _rows_product(x, w, transposed, offsets, y):
     lib = A.load()
-    a, b = _matrices(x), _matrices(w)
-    work = _workspace(lib.adamw_expert_workspace(_byref(a), _byref(b)), x.device)
-    _call(lib.adamw_expert_rows, "adamw_expert_rows", x.device, _byref(a), _byref(b), transposed, offsets.data_ptr(),
-          _byref(_matrices(y)), _ptr(work))
+    a = _byref(_matrices(x))
+    b = _byref(w)
+    nbytes = lib.adamw_expert_workspace(a, b)
+    work = _empty(nbytes, dtype=_BYTES, device=x.device) if nbytes else None
+    _call(lib.adamw_expert_rows, "adamw_expert_rows", x.device, a, b, transposed, offsets.data_ptr(),
+          _byref(_matrices(y)), work.data_ptr() if nbytes else None)
     return y
 
 
 def _expert_linear(x, weight, offsets, out):
     x = _tokens_of("tokens", x)
-    w, transposed = _weight_of(weight, x)
-    if weight.shape[2] != x.shape[1]:
+    w, transposed, _keep = _weight_of(weight, x)
+    experts, n, k = weight.shape
+    if k != x.shape[1]:
         raise ValueError(f"weights {tuple(weight.shape)} do not match tokens {tuple(x.shape)}")
-    offsets = _offsets_of(offsets, w.shape[0], x.device)
-    shape = (x.shape[0], weight.shape[1])
+    offsets = _offsets_of(offsets, experts, x.device)
     if out is None:
-        out = _empty(shape, dtype=x.dtype, device=x.device)
-    elif out.shape != shape or out.device != x.device or out.dtype not in _CODES or (shape[1] > 1 and out.stride(1) != 1):
+        out = _empty((x.shape[0], n), dtype=x.dtype, device=x.device)
+    elif out.shape != (x.shape[0], n) or out.device != x.device or out.dtype not in _CODES or (n > 1 and out.stride(1) != 1):
         raise ValueError("out must be [tokens, out features] on the tokens' device, rows of consecutive elements")
     return _rows_product(x, w, transposed, offsets, out)
 
@@ -223,14 +225,13 @@ def expert_linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tens
     gradient goes, [experts, out, in] in bf16, fp16 or fp32 (for example an
     optimizer's own gradient buffer); with ``accumulate`` it is added there, in
     fp32 before the rounding."""
-    dy, x = _tokens_of("gradients", dy.detach()), _tokens_of("tokens", x.detach())
-    weight = weight.detach()
-    w, transposed = _weight_of(weight, x)
+    dy, x = _tokens_of("gradients", dy), _tokens_of("tokens", x)
+    w, transposed, _keep = _weight_of(weight, x)
     if dy.dtype != x.dtype or dy.device != x.device:
         raise TypeError("want gradients of the tokens' type and device")
     if dy.shape != (x.shape[0], weight.shape[1]) or weight.shape[2] != x.shape[1]:
         raise ValueError(f"gradients {tuple(dy.shape)}, tokens {tuple(x.shape)} and weights {tuple(weight.shape)} do not match")
-    offsets = _offsets_of(offsets, w.shape[0], x.device)
+    offsets = _offsets_of(offsets, weight.shape[0], x.device)
     dx = dw = None
     if need[0]:
         dx = _rows_product(dy, w, 1 - transposed, offsets, _empty(x.shape, dtype=x.dtype, device=x.device))
@@ -246,8 +247,8 @@ def expert_linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tens
             dw = d_weight
         else:
             # laid out as the weights are
-            dw = _empty(w.shape, dtype=w.dtype, device=x.device)
-            dw = dw.mT if transposed else dw
+            e, n, k = weight.shape
+            dw = _empty((e, k, n), dtype=x.dtype, device=x.device).mT if transposed else _empty((e, n, k), dtype=x.dtype, device=x.device)
         if dw.stride(2) == 1 or dw.shape[2] <= 1:
             a, b, d = dy, x, dw
         elif dw.stride(1) == 1:
@@ -255,10 +256,11 @@ def expert_linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tens
         else:
             raise ValueError("d_weight needs consecutive elements along one of its last two dimensions")
         lib = A.load()
-        ma, mb = _matrices(a), _matrices(b)
-        work = _workspace(lib.adamw_expert_workspace(_byref(ma), _byref(mb)), x.device)
-        _call(lib.adamw_expert_outer, "adamw_expert_outer", x.device, _byref(ma), _byref(mb), offsets.data_ptr(),
-              _byref(_matrices(d)), int(accumulate), _ptr(work))
+        ma, mb = _byref(_matrices(a)), _byref(_matrices(b))
+        nbytes = lib.adamw_expert_workspace(ma, mb)
+        work = _empty(nbytes, dtype=_BYTES, device=x.device) if nbytes else None
+        _call(lib.adamw_expert_outer, "adamw_expert_outer", x.device, ma, mb, offsets.data_ptr(),
+              _byref(_matrices(d)), int(accumulate), work.data_ptr() if nbytes else None)
         if given:
             _written(dw)
     return dx, dw

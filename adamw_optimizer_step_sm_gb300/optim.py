@@ -133,6 +133,8 @@ class _FlatOptimizer(torch.optim.Optimizer):
     def _gather(self, group, b) -> None:
         """Brings gradients found outside the group's buffer into it."""
         for k, (p, g) in enumerate(zip(group["params"], b.grads)):
+            if p.grad is g:   # the usual case, without a look at the memory
+                continue
             if p.grad is None:
                 raise RuntimeError(f"parameter {k} of a group has no gradient; "
                                    f"{type(self).__name__} steps every parameter")
