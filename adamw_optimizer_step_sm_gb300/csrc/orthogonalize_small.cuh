@@ -6,7 +6,9 @@
 //
 // X stays in registers, in fp32; shared memory holds what the tensor cores
 // read, in fp16 at 2^12 times its value as in the large form: X's part, G and
-// Q. The sum G = X X^T over the cluster goes through distributed shared memory:
+// Q. Q X takes X and Q as two fp16 each (three products: a microsecond and a half of
+// 19 for 64 x 128): in small matrices the roundings of few numbers do not average
+// out, and with one fp16 each the result was up to 3.5e-3 off, now 2e-3. The sum G = X X^T over the cluster goes through distributed shared memory:
 // each CTA adds up its share of G's rows over all parts, in their order, and
 // hands the sums to all. A step is three products one after the other, each
 // about a microsecond from operands in shared memory to results there.
@@ -17,7 +19,9 @@ namespace {
 constexpr int kSmallThreads = 256;
 constexpr int kSmallSide = 128, kSmallMost = 8;   // largest side, CTAs of a cluster
 constexpr uint32_t kPlane = 128 * 128;            // 64 columns of 128 rows of fp16
-constexpr uint32_t kSmallBytes = 1024 + 6 * kPlane, kSmallSumBytes = 128 * 128 * 4;
+// Two planes each for X, what its fp16 leaves, G and Q; then what Q's fp16
+// leaves, in the place of a cluster's sums.
+constexpr uint32_t kSmallBytes = 1024 + 10 * kPlane, kSmallClusterBytes = 1024 + 8 * kPlane + 128 * 128 * 4;
 
 template <bool MUON>
 struct SmallParams {
@@ -38,6 +42,15 @@ struct SmallControl {
 
 // 16-byte unit j (eight columns) of row r in a plane, as the tensor cores read it.
 __device__ __forceinline__ uint32_t unit_at(int r, int j) { return uint32_t(r * 128 + ((j ^ (r & 7)) << 4)); }
+
+// What fp16 leaves of eight values, in fp16.
+__device__ __forceinline__ uint4 left_of(const float* v) {
+    float h[8];
+    Fp16::unpack(Fp16::pack(v), h);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = v[e] - h[e];
+    return Fp16::pack(h);
+}
 
 // This CTA's share of G's rows, added up over the cluster's parts and handed to
 // all: 16 loads of each thread in flight.
@@ -75,8 +88,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
     extern __shared__ unsigned char raw[];
     __shared__ SmallControl ctl;
     unsigned char* base = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
-    unsigned char *xs = base, *gs = base + 2 * kPlane, *qs = base + 4 * kPlane;
-    float* sums = reinterpret_cast<float*>(base + 6 * kPlane);   // with a cluster only
+    unsigned char *xs = base, *xl = base + 2 * kPlane, *gs = base + 4 * kPlane, *qs = base + 6 * kPlane, *ql = base + 8 * kPlane;
+    float* sums = reinterpret_cast<float*>(ql);   // in a cluster
 
     const int warp = int(threadIdx.x) / 32, lane = int(threadIdx.x) % 32;
     const uint32_t rank = cluster_rank(), ctas = cluster_size();
@@ -183,25 +196,28 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
     // ---- the steps
     uint32_t turn = 0;
     const Waiter wait = {&ctl.failed};
-    const uint32_t xa = smem_addr(xs), ga = smem_addr(gs), qa = smem_addr(qs), out = *static_cast<volatile uint32_t*>(&ctl.tmem);
+    const uint32_t xa = smem_addr(xs), xla = smem_addr(xl), ga = smem_addr(gs), qa = smem_addr(qs), qla = smem_addr(ql), out = *static_cast<volatile uint32_t*>(&ctl.tmem);
     // what is there of k; all 128 rows and columns are computed, zeros beyond the matrix
     const int side16 = (side + 15) / 16 * 16, mine16 = mine > 0 ? (mine + 15) / 16 * 16 : 16;
-    // D = A B^T over `depth` k; B read K-major, or MN-major (then its rows are k)
-    auto product = [&](uint32_t a, uint32_t b, bool b_mn, int depth) {
+    // D (+)= A B^T over `depth` k; B read K-major, or MN-major (then its rows are k)
+    auto issue = [&](uint32_t a, uint32_t b, bool b_mn, int depth, bool add) {
+        const uint32_t kind = mma_kind(0, false, b_mn, 128, 128);
+        const uint64_t da = operand(a, false), db = operand(b, b_mn, kPlane);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint64_t along = uint64_t(i / 4) * (kPlane >> 4) + uint64_t(i % 4) * 2;   // 16 k of rows of 128 bytes
+            if (i * 16 < depth) mma<1>(out, da + along, db + (b_mn ? uint64_t(i) * 128 : along), kind, add || i > 0);
+        }
+    };
+    // what all threads have written is there for the tensor cores
+    auto ready = [&] {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tmem_before();
         __syncthreads();
         tmem_after();
-        if (warp == 0 && elected()) {
-            const uint32_t kind = mma_kind(0, false, b_mn, 128, 128);
-            const uint64_t da = operand(a, false), db = operand(b, b_mn, kPlane);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint64_t along = uint64_t(i / 4) * (kPlane >> 4) + uint64_t(i % 4) * 2;   // 16 k of rows of 128 bytes
-                if (i * 16 < depth) mma<1>(out, da + along, db + (b_mn ? uint64_t(i) * 128 : along), kind, i > 0);
-            }
-            commit<1>(bar);
-        }
+    };
+    auto done = [&] {
+        if (warp == 0 && elected()) commit<1>(bar);
         __syncwarp();
         wait.warp(bar, turn);   // a failure is in the status word; the cluster stays together
         turn ^= 1;
@@ -209,12 +225,17 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
     };
     for (int step = 0; step < p.steps; ++step) {
         const float a = p.coefs[step][0], b = p.coefs[step][1], q = p.coefs[step][2] * kUnscale;
-        unsigned char* plane = xs + h * kPlane;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(plane + unit_at(r, j)) = Fp16::pack(x + j * 8);
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t to = h * kPlane + unit_at(r, j);
+            *reinterpret_cast<uint4*>(xs + to) = Fp16::pack(x + j * 8);
+            *reinterpret_cast<uint4*>(xl + to) = left_of(x + j * 8);
+        }
         // G
-        product(xa, xa, false, mine16);
-        plane = gs + h * kPlane;
+        ready();
+        if (warp == 0 && elected()) issue(xa, xa, false, mine16, false);
+        done();
+        unsigned char* plane = gs + h * kPlane;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             float v[32];
@@ -240,7 +261,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
             cluster_sync();
         }
         // Q
-        product(ga, ga, false, side16);
+        ready();
+        if (warp == 0 && elected()) issue(ga, ga, false, side16, false);
+        done();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             float v[32];
@@ -251,11 +274,19 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
                 Fp16::unpack(*reinterpret_cast<const uint4*>(gs + h * kPlane + unit_at(r, i * 4 + j)), g);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) g[e] = fmaf(b, g[e], q * v[j * 8 + e]);
-                *reinterpret_cast<uint4*>(qs + h * kPlane + unit_at(r, i * 4 + j)) = Fp16::pack(g);
+                const uint32_t to = h * kPlane + unit_at(r, i * 4 + j);
+                *reinterpret_cast<uint4*>(qs + to) = Fp16::pack(g);
+                *reinterpret_cast<uint4*>(ql + to) = left_of(g);
             }
         }
         // X
-        product(qa, xa, true, side16);
+        ready();
+        if (warp == 0 && elected()) {
+            issue(qa, xa, true, side16, false);
+            issue(qa, xla, true, side16, true);
+            issue(qla, xa, true, side16, true);
+        }
+        done();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             float v[32];
@@ -368,8 +399,8 @@ bool launch_small(const Group& g, const int32_t* first_sum, const adamw_ortho_t&
         }
         if (part.n == 0) continue;
         fill_copies(part, sums, &p->in);
-        const size_t smem = kSmallBytes + (ctas > 1 ? kSmallSumBytes : 0);
-        if (!launched(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmallBytes + kSmallSumBytes)),
+        const size_t smem = ctas > 1 ? kSmallClusterBytes : kSmallBytes;
+        if (!launched(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmallClusterBytes)),
                       "cudaFuncSetAttribute") ||
             !launched(launch(kernel, uint32_t(clusters * ctas), kSmallThreads, ctas, smem, st, *p), "small launch"))
             return false;
