@@ -576,7 +576,7 @@ extern "C" int adamw_expert_rows(const adamw_matrices_t* x, const adamw_matrices
     if ((rc = check(x, true)) != ADAMW_OK || (rc = check(w, true)) != ADAMW_OK || (rc = check(y, false)) != ADAMW_OK) return rc;
     const int64_t n = transposed ? w->cols : w->rows, k = transposed ? w->rows : w->cols;
     if (x->batch != 1 || y->batch != 1 || x->dtype != w->dtype || x->cols != k || y->cols != n || y->rows != x->rows ||
-        w->batch < 1 || (transposed != 0 && transposed != 1))
+        w->batch < 1 || (transposed != 0 && transposed != 1) || overlap(*y, *x) || overlap(*y, *w))
         return ADAMW_ERR_INVALID_ARG;
     if (w->batch > kMaxExperts) return ADAMW_ERR_TOO_LARGE;
     if (y->rows == 0 || y->cols == 0) return ADAMW_OK;
@@ -618,7 +618,8 @@ extern "C" int adamw_expert_outer(const adamw_matrices_t* dy, const adamw_matric
     if ((rc = check(dy, true)) != ADAMW_OK || (rc = check(x, true)) != ADAMW_OK || (rc = check(dw, false)) != ADAMW_OK) return rc;
     if (dy->batch != 1 || x->batch != 1 || dy->dtype != x->dtype || dy->rows != x->rows || dw->rows != dy->cols ||
         dw->cols != x->cols || dw->batch < 1 || (accumulate != 0 && accumulate != 1) ||
-        (dw->batch > 1 && dw->rows > 0 && dw->cols > 0 && dw->batch_stride < (dw->rows - 1) * dw->row_stride + dw->cols))
+        (dw->batch > 1 && dw->rows > 0 && dw->cols > 0 && dw->batch_stride < (dw->rows - 1) * dw->row_stride + dw->cols) ||
+        overlap(*dw, *dy) || overlap(*dw, *x))
         return ADAMW_ERR_INVALID_ARG;
     if (dw->batch > kMaxExperts) return ADAMW_ERR_TOO_LARGE;
     if (dw->rows == 0 || dw->cols == 0) return ADAMW_OK;

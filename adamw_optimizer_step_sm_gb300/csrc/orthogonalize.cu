@@ -184,9 +184,10 @@ struct Source {
     __device__ __forceinline__ Raw load(int row, int col) const {
         Raw r;
         const int64_t at = row * ld + col;
-        const int n = cols - col;
-        load_raw<DT>(data, at, vector && n >= 8, n, &r.a, &r.b);
-        if (MUON) load_raw<ADAMW_DTYPE_BF16>(grad, at, vector, n, &r.c, &r.c);
+        const int n = cols - col;   // none of the last one of a row whose copy is wider
+        const bool whole = vector && n >= 8;
+        load_raw<DT>(data, at, whole, n, &r.a, &r.b);
+        if (MUON) load_raw<ADAMW_DTYPE_BF16>(grad, at, whole, n, &r.c, &r.c);
         return r;
     }
     __device__ __forceinline__ void value(const Raw& r, float (&u)[8], float (&m)[8]) const {
@@ -928,6 +929,11 @@ extern "C" int adamw_orthogonalize(const adamw_matrices_t* src, const adamw_matr
         (rc = check_matrices(dst, true)) != ADAMW_OK)
         return rc;
     if (src->batch != dst->batch || src->rows != dst->rows || src->cols != dst->cols) return ADAMW_ERR_INVALID_ARG;
+    // in place: element for element
+    if (overlap(*src, *dst) &&
+        (src->data != dst->data || src->dtype != dst->dtype || (src->rows > 1 && src->row_stride != dst->row_stride) ||
+         (src->batch > 1 && src->batch_stride != dst->batch_stride)))
+        return ADAMW_ERR_INVALID_ARG;
     if (src->batch * src->rows * src->cols == 0) return ADAMW_OK;
     if (!workspace) return ADAMW_ERR_INVALID_ARG;
     if (!aligned(workspace, 256)) return ADAMW_ERR_MISALIGNED;

@@ -29,6 +29,7 @@
 
 #include <algorithm>
 
+#include "adamw_matrix.h"
 #include "losses_common.cuh"
 
 #ifndef TILE_STEP0
@@ -602,6 +603,16 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
 }
 
 // -------------------------------------------------------------------- host --
+
+// Whether two batches of matrices share an address (by their outer ends).
+inline bool overlap(const adamw_matrices_t& a, const adamw_matrices_t& b) {
+    auto end = [](const adamw_matrices_t& m) {
+        return reinterpret_cast<uintptr_t>(m.data) +
+               uintptr_t((m.batch - 1) * m.batch_stride + (m.rows - 1) * m.row_stride + m.cols) * uintptr_t(dtype_size(m.dtype));
+    };
+    if (a.batch == 0 || a.rows == 0 || a.cols == 0 || b.batch == 0 || b.rows == 0 || b.cols == 0) return false;
+    return reinterpret_cast<uintptr_t>(a.data) < end(b) && reinterpret_cast<uintptr_t>(b.data) < end(a);
+}
 
 using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
 

@@ -59,10 +59,12 @@ typedef struct {
  * of small singular values, where each step multiplies errors by a; what is
  * kept of X itself could, and has 22 bits.  Results are 2e-4 to 2e-3 off the
  * iteration in exact arithmetic (2-norm), before their rounding to dst's type.
+ * X loses its second fp16 where the steps left multiply errors by 16 or less.
  * Coefficients are the caller's: entries of b G + c G G above 16 overflow.
  * A zero matrix gives zeros; one with an inf or NaN gives NaN throughout.
  * src: bf16, fp16 or fp32; dst: any of the three, the same batch, rows and
- *   cols, matrices and rows not overlapping.  It may be src itself.
+ *   cols, matrices and rows not overlapping.  It may be src itself (the same
+ *   data, type and strides) but must not overlap it otherwise.
  * workspace: adamw_orthogonalize_workspace(batch, rows, cols) bytes of device
  *   memory, 256-byte aligned, contents undefined before and after.
  * Errors: INVALID_ARG, MISALIGNED (workspace, or data not aligned to its
@@ -144,7 +146,8 @@ int adamw_muon_plan_destroy(adamw_muon_plan_t plan);
  * offsets: device int64 [experts + 1], ascending within [0, rows].  Offsets
  *   outside that range are taken to its ends, one below its predecessor to the
  *   predecessor.
- * y must not overlap x or w.
+ * y must not overlap x or w.  Up to 16 rows the weights are streamed once, at
+ *   any alignment, and need no workspace.
  * workspace: adamw_expert_workspace(x, w) bytes of device memory, 256-byte
  *   aligned; 0 where data are 16-byte aligned and strides multiples of 8
  *   (others are copied there first).
