@@ -105,6 +105,7 @@ struct ExpertRows {
     };
     static constexpr bool kTail = false;
     static constexpr size_t kTable = sizeof(Groups);
+    static constexpr uint32_t kRing = 196608;
     static constexpr int kWarps = 4;
     struct Extra {};
     struct Out {
@@ -176,6 +177,7 @@ struct ExpertOuter {
     };
     static constexpr bool kTail = true;
     static constexpr size_t kTable = sizeof(Groups);
+    static constexpr uint32_t kRing = 196608;
     static constexpr int kWarps = 4;
     struct Extra {};
     struct Out {

@@ -28,6 +28,9 @@
 #include "adamw_matrix.h"
 #include "tensor_product.cuh"
 
+#ifndef RINGB
+#define RINGB 163840
+#endif
 namespace {
 
 constexpr float kScale = 4096.0f, kUnscale = 1.0f / 4096.0f;
@@ -425,6 +428,9 @@ struct Product {
     // Eight warps: with four, the reads of X (a microsecond each) made a tile's
     // epilogue longer than its products.
     static constexpr int kWarps = 8;
+    // One stage less than fits: the epilogues' sectors go through an L1 of what
+    // shared memory leaves (apply of 16 x 2048^2 203 -> 192 us, 32 x 512 x 1024 58 -> 51).
+    static constexpr uint32_t kRing = S::kStageBytes > 32768 ? 196608 : RINGB;
     static constexpr bool kSymmetric = KIND == kGram || KIND == kPoly;
     // tiles of rows to a tile of columns
     static constexpr int kRatio = S::kCols / S::kRows;

@@ -45,7 +45,6 @@ namespace {
 
 constexpr int kStepK = 64;                  // elements of k in a stage: 128 bytes, one swizzle row
 constexpr int kRowsOfCta = 128;             // accumulator rows of a CTA: the lanes of tensor memory
-constexpr uint32_t kStageRoom = 196608;     // bytes of the ring
 constexpr uint32_t kStagingOfWarp = 4096;   // 32 x 32 fp32
 constexpr uint32_t kControlRoom = 1024;
 constexpr long long kGiveUp = 1000000000ll; // cycles
@@ -332,9 +331,8 @@ struct TileShape {
     static constexpr int kBRows = kCols / kPair;   // rows of B that each CTA loads
     static constexpr uint32_t kABytes = kRowsOfCta * 128, kBBytes = kBRows * 128;
     static constexpr uint32_t kStageBytes = kABytes + kBBytes;
-    static constexpr int kStages = int(kStageRoom / kStageBytes);
     static constexpr uint32_t kColumns = 2 * kCols;   // of tensor memory
-    static_assert(kStages <= 16 && kColumns <= 512 && (kColumns & (kColumns - 1)) == 0, "tile shape");
+    static_assert(kColumns <= 512 && (kColumns & (kColumns - 1)) == 0, "tile shape");
 };
 using PairTile = TileShape<2, 256>;     // 256 x 256 by a pair
 using WideTile = TileShape<1, 256>;     // 128 x 256 by one CTA
@@ -367,7 +365,7 @@ inline int choose_shape(const TileChoice& c, int64_t steps, int pairs, int sms) 
 template <class P>
 constexpr size_t tile_smem() {
     static_assert(P::kWarps == 4 || P::kWarps == 8, "epilogue warps");
-    constexpr size_t n = 1024 + kStageRoom + P::kWarps * kStagingOfWarp + kControlRoom + P::kTable;
+    constexpr size_t n = 1024 + P::kRing + P::kWarps * kStagingOfWarp + kControlRoom + P::kTable;
     static_assert(n <= 232448, "shared memory of a CTA");
     return n;
 }
@@ -377,8 +375,9 @@ constexpr int tile_threads() { return 128 + 32 * P::kWarps; }
 // A policy P over a tile shape S:
 //   P::Params       kernel arguments;  P::kTail: k may end inside a step
 //   P::kTable       bytes of shared memory for its tables
+//   P::kRing        bytes of the ring of stages
 //   P::kWarps       epilogue warps, 4 or 8: each 32 of the CTA's 128 rows, all
-//                   columns or every second block of 32
+//                   columns or half of them
 //   prepare(p, table)                    all threads, before the first tile
 //   tiles(p, table)                      number of tiles
 //   loads(p, table, tile, TileLoads&)    operands
@@ -398,19 +397,20 @@ constexpr int tile_threads() { return 128 + 32 * P::kWarps; }
 // instructions of an epilogue that regroups them (1.7 us a block before).
 template <class P, class S>
 __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid_constant__ typename P::Params p) {
-    constexpr int PAIR = S::kPair;
+    constexpr int PAIR = S::kPair, kStages = int(P::kRing / S::kStageBytes);
+    static_assert(kStages >= 3 && kStages <= 16, "stages");
     extern __shared__ unsigned char raw[];
     // 1024-byte boundary: the swizzle goes by address bits; the same in both CTAs
     unsigned char* base = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
     unsigned char* ring = base;
-    float* staging = reinterpret_cast<float*>(base + kStageRoom);
-    Control* ctl = reinterpret_cast<Control*>(base + kStageRoom + P::kWarps * kStagingOfWarp);
+    float* staging = reinterpret_cast<float*>(base + P::kRing);
+    Control* ctl = reinterpret_cast<Control*>(base + P::kRing + P::kWarps * kStagingOfWarp);
     unsigned char* table = reinterpret_cast<unsigned char*>(ctl) + kControlRoom;
 
     const int warp = int(threadIdx.x) / 32, lane = int(threadIdx.x) % 32;
     const uint32_t rank = PAIR == 2 ? cluster_rank() : 0;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < S::kStages; ++s) {
+        for (int s = 0; s < kStages; ++s) {
             barrier_init(smem_addr(&ctl->full[s]), PAIR);
             barrier_init(smem_addr(&ctl->empty[s]), 1);
             barrier_init(smem_addr(&ctl->tail[s]), 1);
@@ -447,8 +447,8 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
             const bool a_mn = w.a_mn, b_mn = w.b_mn;
             const int a_at = w.a_at + int(rank) * kRowsOfCta, b_at = w.b_at + int(rank) * S::kBRows;
             for (int k = 0; k < w.k_len; k += kStepK, ++it) {
-                const uint32_t s = it % S::kStages;
-                if (!(ok = wait.warp(smem_addr(&ctl->empty[s]), (it / S::kStages & 1) ^ 1))) break;
+                const uint32_t s = it % kStages;
+                if (!(ok = wait.warp(smem_addr(&ctl->empty[s]), (it / kStages & 1) ^ 1))) break;
                 if (!elected()) continue;
                 const bool tail = P::kTail && k + kStepK > w.k_len;
                 const uint32_t own = smem_addr(tail ? &ctl->tail[s] : &ctl->full[s]);
@@ -474,8 +474,8 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
         }
         // The products' last arrivals: one that came after this CTA's end would
         // reach the barriers of the next kernel's.
-        const uint32_t left = it < uint32_t(S::kStages) ? it : uint32_t(S::kStages);
-        for (uint32_t k = it - left; k < it && ok; ++k) ok = wait.warp(smem_addr(&ctl->empty[k % S::kStages]), k / S::kStages & 1);
+        const uint32_t left = it < uint32_t(kStages) ? it : uint32_t(kStages);
+        for (uint32_t k = it - left; k < it && ok; ++k) ok = wait.warp(smem_addr(&ctl->empty[k % kStages]), k / kStages & 1);
     } else if (warp == 1 && rank == 0) {
         // ---- products
         uint32_t it = 0, n = 0;
@@ -490,8 +490,8 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
             if (!(ok = wait.warp(smem_addr(&ctl->acc_empty[acc]), (n >> 1 & 1) ^ 1))) break;
             tmem_after();
             for (int k = 0; k < w.k_len; k += kStepK, ++it) {
-                const uint32_t s = it % S::kStages;
-                if (!(ok = wait.warp(smem_addr(&ctl->full[s]), it / S::kStages & 1))) break;
+                const uint32_t s = it % kStages;
+                if (!(ok = wait.warp(smem_addr(&ctl->full[s]), it / kStages & 1))) break;
                 tmem_after();
                 const uint32_t at = smem_addr(ring) + s * S::kStageBytes;
                 const uint64_t a = operand(at, a_mn), b = operand(at + S::kABytes, b_mn);
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
             const int steps = (w.k_len + kStepK - 1) / kStepK, rest = w.k_len % kStepK;
             it += uint32_t(steps);
             if (rest == 0) continue;
-            const uint32_t s = (it - 1) % S::kStages;
+            const uint32_t s = (it - 1) % kStages;
             if (!(ok = wait.warp(smem_addr(&ctl->tail[s]), turns >> s & 1))) break;
             turns ^= 1u << s;
             const int end = (rest + 15) / 16 * 16;   // what the products read
@@ -549,8 +549,8 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
             const uint32_t acc = n & 1;
             // a warp reaches the 32 lanes of tensor memory of its number modulo 4
             const int row0 = warp % 4 * 32;
-            constexpr int kNext = P::kWarps * 8;   // columns to the warp's next block
-            const int c0 = (warp - 4) / 4 * 32;
+            constexpr int kShare = S::kCols / (P::kWarps / 4);   // columns of the warp
+            const int c0 = (warp - 4) / 4 * kShare, c1 = c0 + kShare;
             const int row = row0 + lane;
             typename P::Extra next;
             if (P::wanted(p, out, row0, c0)) P::fetch(p, out, row, c0, next);
@@ -558,10 +558,10 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
                 if (!(ok = wait.warp(smem_addr(&ctl->acc_full[acc]), n >> 1 & 1))) break;
                 tmem_after();
             }
-            for (int c = c0; c < S::kCols; c += kNext) {
+            for (int c = c0; c < c1; c += 32) {
                 if (!P::wanted(p, out, row0, c)) continue;
                 const typename P::Extra now = next;
-                if (c + kNext < S::kCols && P::wanted(p, out, row0, c + kNext)) P::fetch(p, out, row, c + kNext, next);
+                if (c + 32 < c1 && P::wanted(p, out, row0, c + 32)) P::fetch(p, out, row, c + 32, next);
                 float v[32];
                 if (w.k_len > 0) {
                     tmem_load(tmem + (uint32_t(row0) << 16) + acc * S::kCols + uint32_t(c), v);
