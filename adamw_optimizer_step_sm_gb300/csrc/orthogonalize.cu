@@ -28,9 +28,6 @@
 #include "adamw_matrix.h"
 #include "tensor_product.cuh"
 
-#ifndef RINGB
-#define RINGB 163840
-#endif
 namespace {
 
 constexpr float kScale = 4096.0f, kUnscale = 1.0f / 4096.0f;
@@ -63,13 +60,17 @@ struct Batch {
     char* data;
     int64_t batch_stride, row_stride;
     int32_t dtype;
-    int32_t vector;   // every row at a multiple of 16 bytes
-    int32_t sectors;  // of 32
+    int32_t vector;   // kAnyRows, ...
 };
 
 constexpr int kNormThreads = 256;
-constexpr int kPieceVecs = 4096;   // vectors of eight elements that a CTA takes
-constexpr int kBatch = 4;          // of them in flight in a thread
+constexpr int kBatch = 4;   // vectors of eight elements in flight in a thread
+constexpr int kLeastPiece = kNormThreads * kBatch;
+
+// Vectors that a CTA takes of a list of this many: four batches, one where the
+// list would give the GPU fewer than two CTAs an SM (norm and copy of three 515 x
+// 1031 fp32: 25 us with four, 19 with one).
+inline int32_t piece_size(int64_t vecs) { return vecs / (4 * kLeastPiece) >= 304 ? 4 * kLeastPiece : kLeastPiece; }
 
 struct CopyShape {
     Shape s;
@@ -83,6 +84,7 @@ template <bool MUON>
 struct CopyParams {
     CopyShape shapes[kMaxShapes];
     int32_t n;
+    int32_t piece;     // vectors of one
     double* sums;      // by piece
     float eps;
     // without a plan
@@ -241,12 +243,12 @@ __device__ __forceinline__ const CopyShape& piece_of(const CopyParams<MUON>& p, 
 struct Walk {
     uint32_t per, first_col, n;
     int32_t first_row;
-    __device__ Walk(const Shape& s, int32_t i) {
+    __device__ Walk(const Shape& s, int32_t i, int32_t piece) {
         per = uint32_t(s.ld) / 8;
-        const int64_t first = int64_t(i) * kPieceVecs, left = int64_t(s.rows) * per - first;
+        const int64_t first = int64_t(i) * piece, left = int64_t(s.rows) * per - first;
         first_row = int32_t(first / per);
         first_col = uint32_t(first - int64_t(first_row) * per);
-        n = uint32_t(left < kPieceVecs ? left : kPieceVecs);
+        n = uint32_t(left < piece ? left : piece);
     }
     __device__ __forceinline__ bool at(int k, int32_t* row, int32_t* col) const {
         const uint32_t v = first_col + uint32_t(k), r = v / per;
@@ -266,11 +268,11 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const __grid_constan
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Source<MUON, DT> src(p, c, matrix);
-    const Walk walk(c.s, i);
+    const Walk walk(c.s, i, p.piece);
     Sum2 total = {0.0f, 0.0f};
     double sum = 0.0;
 #pragma unroll 1
-    for (int k = 0; k < kPieceVecs / kNormThreads; k += kBatch) {
+    for (int k = 0; k < p.piece / kNormThreads; k += kBatch) {
         Raw raw[kBatch];
         bool in[kBatch];
 #pragma unroll
@@ -348,11 +350,11 @@ __global__ void __launch_bounds__(kNormThreads) copy_kernel(const __grid_constan
     for (int k = 0; k < kNormThreads / 32; ++k) sum += part[k];
     const float by = scale_of(sum, p.eps);
     const Source<MUON, DT> src(p, c, matrix);
-    const Walk walk(c.s, i);
-    uint4* hi = reinterpret_cast<uint4*>(c.hi + matrix * c.s.stride) + int64_t(i) * kPieceVecs;
-    uint4* lo = reinterpret_cast<uint4*>(c.lo + matrix * c.s.stride) + int64_t(i) * kPieceVecs;
+    const Walk walk(c.s, i, p.piece);
+    uint4* hi = reinterpret_cast<uint4*>(c.hi + matrix * c.s.stride) + int64_t(i) * p.piece;
+    uint4* lo = reinterpret_cast<uint4*>(c.lo + matrix * c.s.stride) + int64_t(i) * p.piece;
 #pragma unroll 1
-    for (int k = 0; k < kPieceVecs / kNormThreads; k += kBatch) {
+    for (int k = 0; k < p.piece / kNormThreads; k += kBatch) {
         Raw raw[kBatch];
         int32_t row[kBatch], col[kBatch];
         bool in[kBatch];
@@ -430,7 +432,7 @@ struct Product {
     static constexpr int kWarps = 8;
     // One stage less than fits: the epilogues' sectors go through an L1 of what
     // shared memory leaves (apply of 16 x 2048^2 203 -> 192 us, 32 x 512 x 1024 58 -> 51).
-    static constexpr uint32_t kRing = S::kStageBytes > 32768 ? 196608 : RINGB;
+    static constexpr uint32_t kRing = S::kStageBytes > 32768 ? 196608 : 163840;
     static constexpr bool kSymmetric = KIND == kGram || KIND == kPoly;
     // tiles of rows to a tile of columns
     static constexpr int kRatio = S::kCols / S::kRows;
@@ -444,7 +446,8 @@ struct Product {
         // a trip to L1 in every vector
         int32_t m, n, ld, cols;
         int32_t matrix, row, col;   // of the CTA's part
-        bool mirrored, vector, skip;
+        int32_t vector;             // of the result's rows
+        bool mirrored, skip;
         uint16_t *out, *lo;
         const uint16_t* hi;
         char *dst, *param;          // the result, or the master and the parameter
@@ -506,7 +509,7 @@ struct Product {
         o.col = n * S::kCols;
         o.mirrored = kSymmetric && m / kRatio != n;
         o.skip = false;
-        o.vector = true;
+        o.vector = kSectorRows;
         o.a = p.a;
         o.b = p.b;
         o.c = p.c * kUnscale;
@@ -518,13 +521,14 @@ struct Product {
             o.dst_type = p.dst.dtype;
             o.dst = p.dst.data + o.matrix * p.dst.batch_stride * (o.dst_type == ADAMW_DTYPE_FP32 ? 4 : 2);
             o.dst_ld = p.dst.row_stride;
-            o.vector = p.dst.sectors != 0;
+            o.vector = p.dst.vector;
         } else if constexpr (KIND == kUpdate) {
             const MuonMatrix t = p.table[c.s.first + o.matrix];
             o.dst = reinterpret_cast<char*>(t.master);
             o.param = reinterpret_cast<char*>(t.param);
             o.dst_ld = c.s.cols;
-            o.vector = c.s.cols % 16 == 0 && (reinterpret_cast<uintptr_t>(t.master) | reinterpret_cast<uintptr_t>(t.param)) % 32 == 0;
+            const uintptr_t at32 = reinterpret_cast<uintptr_t>(t.master) | reinterpret_cast<uintptr_t>(t.param) | uintptr_t(c.s.cols) * 2;
+            o.vector = at32 % 32 == 0 ? kSectorRows : at32 % 16 == 0 ? kHalfRows : kAnyRows;
             o.skip = *p.nonfinite != 0;
             const float lr = p.hp->lr;
             o.decay = 1.0f - lr * p.hp->weight_decay;
@@ -598,14 +602,15 @@ struct Product {
             const int64_t to = int64_t(o.row + row) * o.dst_ld + o.col + col;
             const int left = o.cols - o.col - col;
             if constexpr (KIND == kResult) {
-                store_row(o.dst + to * (o.dst_type == ADAMW_DTYPE_FP32 ? 4 : 2), o.dst_type, v, left);
+                store_row(o.dst + to * (o.dst_type == ADAMW_DTYPE_FP32 ? 4 : 2), o.dst_type, v, left, o.vector == kSectorRows);
             } else {
                 float w[32];
-                load_row<ADAMW_DTYPE_FP32>(o.dst + to * 4, w, left);
+                const bool whole = o.vector == kSectorRows;
+                load_row<ADAMW_DTYPE_FP32>(o.dst + to * 4, w, left, whole);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = fmaf(-o.rate, v[e], o.decay * w[e]);
-                store_row<ADAMW_DTYPE_FP32>(o.dst + to * 4, v, left);
-                store_row<ADAMW_DTYPE_BF16>(o.param + to * 2, v, left);
+                store_row<ADAMW_DTYPE_FP32>(o.dst + to * 4, v, left, whole);
+                store_row<ADAMW_DTYPE_BF16>(o.param + to * 2, v, left, whole);
             }
         }
     }
@@ -648,7 +653,8 @@ Shape shape_of(int64_t rows, int64_t cols) {
     s.small_stride = int64_t(s.side) * s.small_ld;
     return s;
 }
-int64_t pieces_of(const Shape& s) { return (int64_t(s.rows) * (s.ld / 8) + kPieceVecs - 1) / kPieceVecs; }
+int64_t vecs_of(const Shape& s) { return int64_t(s.rows) * (s.ld / 8); }
+int64_t pieces_of(const Shape& s, int32_t piece) { return (vecs_of(s) + piece - 1) / piece; }
 
 // The working copies of a shape.
 struct Buffers {
@@ -870,25 +876,21 @@ int check_matrices(const adamw_matrices_t* m, bool written) {
 }
 
 Batch batch_of(const adamw_matrices_t& m) {
-    const int size = dtype_size(m.dtype);
-    auto whole = [&](int bytes) {
-        return aligned(m.data, uintptr_t(bytes)) && (m.rows <= 1 || m.row_stride * size % bytes == 0) &&
-               (m.batch <= 1 || m.batch_stride * size % bytes == 0);
-    };
-    return {static_cast<char*>(m.data), m.batch_stride, m.row_stride, m.dtype, whole(16), whole(32)};
+    return {static_cast<char*>(m.data), m.batch_stride, m.row_stride, m.dtype, rows_at(m)};
 }
 
 // Pieces of the shapes of a launch, from the list's sum number `sum` on.
 template <bool MUON>
-int64_t fill_copies(const Group& g, const int32_t* first_sum, CopyParams<MUON>* p) {
+int64_t fill_copies(const Group& g, const int32_t* first_sum, int32_t piece, CopyParams<MUON>* p) {
     int64_t pieces = 0;
     p->n = g.n;
+    p->piece = piece;
     for (int i = 0; i < g.n; ++i) {
         CopyShape& c = p->shapes[i];
         c.s = g.shapes[i];
         c.hi = g.buffers[i].x[0];
         c.lo = g.buffers[i].lo;
-        c.pieces = int32_t(pieces_of(c.s));
+        c.pieces = int32_t(pieces_of(c.s, piece));
         c.first_piece = int32_t(pieces);
         c.first_sum = first_sum[i];
         pieces += int64_t(c.pieces) * c.s.count;
@@ -925,7 +927,7 @@ extern "C" int64_t adamw_orthogonalize_workspace(int64_t batch, int64_t rows, in
     if (!sizes_fit(batch, rows, cols) || batch * rows * cols == 0) return 0;
     Shape s = shape_of(rows, cols);
     s.count = int32_t(batch);
-    return up(pieces_of(s) * batch * int64_t(sizeof(double)), 256) + place(s, nullptr, nullptr);
+    return up(pieces_of(s, piece_size(vecs_of(s) * batch)) * batch * int64_t(sizeof(double)), 256) + place(s, nullptr, nullptr);
 }
 
 extern "C" int adamw_orthogonalize(const adamw_matrices_t* src, const adamw_matrices_t* dst, const adamw_ortho_t* ortho,
@@ -951,7 +953,8 @@ extern "C" int adamw_orthogonalize(const adamw_matrices_t* src, const adamw_matr
     Shape& s = g.shapes[0];
     s = shape_of(src->rows, src->cols);
     s.count = int32_t(src->batch);
-    const int64_t pieces = pieces_of(s) * s.count;
+    const int32_t piece = piece_size(vecs_of(s) * s.count);
+    const int64_t pieces = pieces_of(s, piece) * s.count;
     if (pieces > kMaxCount) return ADAMW_ERR_TOO_LARGE;
     place(s, static_cast<char*>(workspace) + up(pieces * int64_t(sizeof(double)), 256), &g.buffers[0]);
     CopyParams<false> c;
@@ -965,9 +968,9 @@ extern "C" int adamw_orthogonalize(const adamw_matrices_t* src, const adamw_matr
         memset(&p, 0, sizeof p);
         p.in = c;
         p.dst = batch_of(*dst);
-        return launch_small(g, &first_sum, *ortho, ortho->coefficients, src->dtype, d.sms, &p, st) ? ADAMW_OK : ADAMW_ERR_CUDA;
+        return launch_small(g, &first_sum, *ortho, ortho->coefficients, src->dtype, d.sms, piece, &p, st) ? ADAMW_OK : ADAMW_ERR_CUDA;
     }
-    fill_copies(g, &first_sum, &c);
+    fill_copies(g, &first_sum, piece, &c);
     if (!launched(launch(norm_of<false>(src->dtype), uint32_t(pieces), kNormThreads, 1, 0, st, c), "norm launch") ||
         !launched(launch(copy_of<false>(src->dtype), uint32_t(pieces), kNormThreads, 1, 0, st, c), "copy launch"))
         return ADAMW_ERR_CUDA;
@@ -983,7 +986,7 @@ struct adamw_muon_plan {
     int device = 0;
     adamw_ortho_t ortho = {};
     std::vector<float> coefs;
-    int32_t nesterov = 0, momentum_bf16 = 0;
+    int32_t nesterov = 0, momentum_bf16 = 0, piece = 0;
     std::vector<Group> rounds;                 // one after the other, in the same workspace
     std::vector<std::vector<int32_t>> sums;    // each shape's first sum, by round
     void* block = nullptr;                     // table, sums, workspace
@@ -1123,6 +1126,9 @@ int create(const adamw_muon_tensor_t* table, int32_t n, const adamw_muon_options
             ++shapes.back().count;
         }
     }
+    int64_t vecs = 0;
+    for (const Shape& s : shapes) vecs += vecs_of(s) * s.count;
+    P->piece = piece_size(vecs);
     // rounds: as many matrices as the workspace holds, of at most kMaxShapes shapes
     int64_t sums = 0, work = 0, used = 0;
     for (const Shape& s : shapes) {
@@ -1145,7 +1151,7 @@ int create(const adamw_muon_tensor_t* table, int32_t n, const adamw_muon_options
             g.rate[g.n] = rate_of(o->scale, part.rows, part.cols);
             ++g.n;
             P->sums.back().push_back(int32_t(sums));
-            sums += pieces_of(part) * part.count;
+            sums += pieces_of(part, P->piece) * part.count;
             if (sums > kMaxCount) return ADAMW_ERR_TOO_LARGE;
             if (!small) used += place(part, nullptr, nullptr);
             work = std::max(work, used);
@@ -1216,7 +1222,7 @@ extern "C" int adamw_muon_step(adamw_muon_plan_t plan, const adamw_muon_hparams_
     c.nesterov = plan->nesterov;
     // every norm first: one gradient that is not finite stops the whole step
     for (size_t r = 0; r < plan->rounds.size(); ++r) {
-        const int64_t pieces = fill_copies(plan->rounds[r], plan->sums[r].data(), &c);
+        const int64_t pieces = fill_copies(plan->rounds[r], plan->sums[r].data(), plan->piece, &c);
         if (!launched(launch(norm_of<true>(plan->momentum_bf16 ? ADAMW_DTYPE_BF16 : ADAMW_DTYPE_FP32), uint32_t(pieces), kNormThreads, 1, 0, st, c), "norm launch")) return ADAMW_ERR_CUDA;
     }
     ProductParams with;
@@ -1230,11 +1236,11 @@ extern "C" int adamw_muon_step(adamw_muon_plan_t plan, const adamw_muon_hparams_
             SmallParams<true> p;
             memset(&p, 0, sizeof p);
             p.in = c;
-            if (!launch_small(plan->rounds[r], plan->sums[r].data(), plan->ortho, plan->coefs.data(), dtype, d.sms, &p, st))
+            if (!launch_small(plan->rounds[r], plan->sums[r].data(), plan->ortho, plan->coefs.data(), dtype, d.sms, plan->piece, &p, st))
                 return ADAMW_ERR_CUDA;
             continue;
         }
-        const int64_t pieces = fill_copies(plan->rounds[r], plan->sums[r].data(), &c);
+        const int64_t pieces = fill_copies(plan->rounds[r], plan->sums[r].data(), plan->piece, &c);
         if (!launched(launch(copy_of<true>(plan->momentum_bf16 ? ADAMW_DTYPE_BF16 : ADAMW_DTYPE_FP32), uint32_t(pieces), kNormThreads, 1, 0, st, c), "copy launch")) return ADAMW_ERR_CUDA;
         if (!run_steps(plan->rounds[r], plan->ortho, plan->coefs.data(), kUpdate, with, d, st)) return ADAMW_ERR_CUDA;
     }

@@ -20,8 +20,8 @@ constexpr int kSmallThreads = 256;
 constexpr int kSmallSide = 128, kSmallMost = 8;   // largest side, CTAs of a cluster
 constexpr uint32_t kPlane = 128 * 128;            // 64 columns of 128 rows of fp16
 // Two planes each for X, what its fp16 leaves, G and Q; then what Q's fp16
-// leaves, in the place of a cluster's sums.
-constexpr uint32_t kSmallBytes = 1024 + 10 * kPlane, kSmallClusterBytes = 1024 + 8 * kPlane + 128 * 128 * 4;
+// leaves, in the place of a cluster's parts of G.
+constexpr uint32_t kSmallBytes = 1024 + 10 * kPlane;
 
 template <bool MUON>
 struct SmallParams {
@@ -52,34 +52,39 @@ __device__ __forceinline__ uint4 left_of(const float* v) {
     return Fp16::pack(h);
 }
 
-// This CTA's share of G's rows, added up over the cluster's parts and handed to
-// all: 16 loads of each thread in flight.
+// This CTA's share of G's rows, added up over the cluster's parts (in fp32, from
+// fp16: their roundings together are below that of the sum) and handed to all.
 template <int CTAS>
-__device__ __forceinline__ void add_up(float* sums, unsigned char* gs, uint32_t rank) {
-    float4 v[16 / CTAS][CTAS];
+__device__ __forceinline__ void add_up(const unsigned char* parts, unsigned char* gs, uint32_t rank) {
+    constexpr int kUnits = 8 / CTAS;   // of eight columns, for each thread
+    uint4 v[kUnits][CTAS];
+    uint32_t at[kUnits];
 #pragma unroll
-    for (int i = 0; i < 16 / CTAS; ++i) {
-        const int at = i * kSmallThreads + int(threadIdx.x), row = int(rank) * (128 / CTAS) + at / 32, u = at % 32;
-        const uint32_t from = smem_addr(sums + row * 128 + ((u ^ (row & 31)) << 2));   // four columns
+    for (int i = 0; i < kUnits; ++i) {
+        const int u = i * kSmallThreads + int(threadIdx.x), row = int(rank) * (128 / CTAS) + u / 16;
+        at[i] = uint32_t(u % 16 / 8) * kPlane + unit_at(row, u % 8);
 #pragma unroll
         for (int o = 0; o < CTAS; ++o)
-            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(v[i][o].x), "=f"(v[i][o].y), "=f"(v[i][o].z), "=f"(v[i][o].w) : "r"(in_cta(from, uint32_t(o))) : "memory");
+            asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[i][o].x), "=r"(v[i][o].y), "=r"(v[i][o].z), "=r"(v[i][o].w)
+                         : "r"(in_cta(smem_addr(parts + at[i]), uint32_t(o))) : "memory");
     }
 #pragma unroll
-    for (int i = 0; i < 16 / CTAS; ++i) {
-        const int at = i * kSmallThreads + int(threadIdx.x), row = int(rank) * (128 / CTAS) + at / 32, u = at % 32;
-        float4 t = v[i][0];
+    for (int i = 0; i < kUnits; ++i) {
+        float t[8];
+        Fp16::unpack(v[i][0], t);
 #pragma unroll
-        for (int o = 1; o < CTAS; ++o) t = make_float4(t.x + v[i][o].x, t.y + v[i][o].y, t.z + v[i][o].z, t.w + v[i][o].w);
-        const __half2 lo = __floats2half2_rn(t.x, t.y), hi = __floats2half2_rn(t.z, t.w);
-        uint32_t w[2];
-        memcpy(&w[0], &lo, 4);
-        memcpy(&w[1], &hi, 4);
-        const uint32_t to = smem_addr(gs + (u / 16) * kPlane + unit_at(row, u % 16 / 2) + u % 2 * 8);
+        for (int o = 1; o < CTAS; ++o) {
+            float w[8];
+            Fp16::unpack(v[i][o], w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] += w[e];
+        }
+        const uint4 g = Fp16::pack(t);
 #pragma unroll
         for (int o = 0; o < CTAS; ++o)
-            asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(in_cta(to, uint32_t(o))), "r"(w[0]), "r"(w[1]) : "memory");
+            asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(in_cta(smem_addr(gs + at[i]), uint32_t(o))),
+                         "r"(g.x), "r"(g.y), "r"(g.z), "r"(g.w) : "memory");
     }
 }
 
@@ -89,7 +94,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
     __shared__ SmallControl ctl;
     unsigned char* base = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
     unsigned char *xs = base, *xl = base + 2 * kPlane, *gs = base + 4 * kPlane, *qs = base + 6 * kPlane, *ql = base + 8 * kPlane;
-    float* sums = reinterpret_cast<float*>(ql);   // in a cluster
+    unsigned char* parts = ql;   // of G, in a cluster
 
     const int warp = int(threadIdx.x) / 32, lane = int(threadIdx.x) % 32;
     const uint32_t rank = cluster_rank(), ctas = cluster_size();
@@ -235,29 +240,21 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
         ready();
         if (warp == 0 && elected()) issue(xa, xa, false, mine16, false);
         done();
-        unsigned char* plane = gs + h * kPlane;
+        unsigned char* plane = (ctas == 1 ? gs : parts) + h * kPlane;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             float v[32];
             tmem_load(tmem + i * 32, v);
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] *= kUnscale;
-            if (ctas == 1) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(plane + unit_at(r, i * 4 + j)) = Fp16::pack(v + j * 8);
-            } else {
-                // rows of 512 bytes, their 16-byte units XORed with the row
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<float4*>(sums + r * 128 + (((h * 16 + i * 8 + j) ^ (r & 31)) << 2)) =
-                        make_float4(v[j * 4], v[j * 4 + 1], v[j * 4 + 2], v[j * 4 + 3]);
-            }
+            for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(plane + unit_at(r, i * 4 + j)) = Fp16::pack(v + j * 8);
         }
         if (ctas > 1) {
             cluster_sync();
-            if (ctas == 2) add_up<2>(sums, gs, rank);
-            else if (ctas == 4) add_up<4>(sums, gs, rank);
-            else add_up<8>(sums, gs, rank);
+            if (ctas == 2) add_up<2>(parts, gs, rank);
+            else if (ctas == 4) add_up<4>(parts, gs, rank);
+            else add_up<8>(parts, gs, rank);
             cluster_sync();
         }
         // Q
@@ -371,7 +368,7 @@ inline int small_ctas(const Shape& s) {
 // The shapes of `g`, all small, whose norms (of a plan) begin at `first_sum`.
 template <bool MUON>
 bool launch_small(const Group& g, const int32_t* first_sum, const adamw_ortho_t& o, const float* coefs, int32_t dtype,
-                  int sms, SmallParams<MUON>* p, cudaStream_t st) {
+                  int sms, int32_t piece, SmallParams<MUON>* p, cudaStream_t st) {
     p->steps = o.steps;
     for (int k = 0; k < o.steps; ++k) memcpy(p->coefs[k], coefs + 3 * (k < o.n_coefficients ? k : o.n_coefficients - 1), 12);
     int most = 1;
@@ -398,11 +395,10 @@ bool launch_small(const Group& g, const int32_t* first_sum, const adamw_ortho_t&
             clusters += g.shapes[i].count;
         }
         if (part.n == 0) continue;
-        fill_copies(part, sums, &p->in);
-        const size_t smem = ctas > 1 ? kSmallClusterBytes : kSmallBytes;
-        if (!launched(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmallClusterBytes)),
+        fill_copies(part, sums, piece, &p->in);
+        if (!launched(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmallBytes)),
                       "cudaFuncSetAttribute") ||
-            !launched(launch(kernel, uint32_t(clusters * ctas), kSmallThreads, ctas, smem, st, *p), "small launch"))
+            !launched(launch(kernel, uint32_t(clusters * ctas), kSmallThreads, ctas, kSmallBytes, st, *p), "small launch"))
             return false;
     }
     return true;

@@ -11,15 +11,17 @@
 // A unit (one CTA, or a pair on two neighbouring SMs) computes a tile of
 // kRows x kCols in steps of 64 k.  Roles, a warp each: TMA loads into a ring
 // of stages; one thread issues tcgen05.mma into one of two accumulators in
-// tensor memory; four or eight warps read the other one out and hand it to the policy
-// in vectors of eight columns; and where k ends inside a step at an element
-// that the next group owns (the ragged sums over tokens), one warp zeroes the
-// rest of the step in shared memory.
+// tensor memory; four or eight warps read the other one out and hand it to the
+// policy, 32 columns of a row to a thread; and where k ends inside a step at an
+// element that the next group owns (the ragged sums over tokens), one warp zeroes
+// the rest of the step in shared memory.
 //
-// Bounds: a 256 x 256 x 64 step of a pair takes its SMs 256 cycles and 64 KB of
-// loads.  The pair shares each operand's loads (128 rows of A and 128 of B by
-// each SM), which halves the shared-memory traffic of B against two single
-// tiles; the single form is for products with too few tiles to fill the GPU.
+// Bounds: a 256 x 256 x 64 step of a pair takes the tensor cores of its SMs 512
+// cycles, and 64 KB of loads.  The pair shares the loads (128 rows of A and 128 of
+// B by each SM); tiles of one CTA load half as much again for the same work and
+// are for products with few tiles or groups of few rows.  8192^3 in bf16 takes 551 us
+// (1996 TFLOP/s, 104 % of the measured burst rate of 1911; the library's product
+// 545 us in the same process); larger products are bound by the power limit.
 //
 // No wait is endless: after about half a second it gives up, sets the device's
 // status word, and every role leaves.
@@ -31,15 +33,6 @@
 
 #include "adamw_matrix.h"
 #include "losses_common.cuh"
-
-#ifndef TILE_STEP0
-#define TILE_STEP0 512
-#define TILE_STEP1 540
-#define TILE_STEP2 500
-#define TILE_REST0 4000
-#define TILE_REST1 4000
-#define TILE_REST2 2500
-#endif
 
 namespace {
 
@@ -74,7 +67,7 @@ __device__ __forceinline__ bool barrier_test(uint32_t bar, uint32_t parity) {
 // `bar` is a cluster address: this CTA's own or another's.  What these order
 // beyond the barrier goes through the asynchronous proxy or tensor memory, which
 // have fences of their own: at cluster scope, waits and arrivals would each
-// order all of the thread's memory (measured: 790 instead of FAST TFLOP/s).
+// order all of the thread's memory (measured: 790 instead of 1520 TFLOP/s).
 __device__ __forceinline__ void barrier_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -180,6 +173,15 @@ __device__ __forceinline__ Sector load_sector(const void* p) {
                  : "l"(__cvta_generic_to_global(p)) : "memory");
     return s;
 }
+// The same at a multiple of 16.
+__device__ __forceinline__ Sector load_halves(const void* p) {
+    const uint4 a = static_cast<const uint4*>(p)[0], b = static_cast<const uint4*>(p)[1];
+    return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+}
+__device__ __forceinline__ void store_halves(void* p, const Sector& s) {
+    static_cast<uint4*>(p)[0] = make_uint4(s.w[0], s.w[1], s.w[2], s.w[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(s.w[4], s.w[5], s.w[6], s.w[7]);
+}
 __device__ __forceinline__ void store_sector(void* p, const Sector& s) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(__cvta_generic_to_global(p)), "r"(s.w[0]),
                  "r"(s.w[1]), "r"(s.w[2]), "r"(s.w[3]), "r"(s.w[4]), "r"(s.w[5]), "r"(s.w[6]), "r"(s.w[7])
@@ -209,14 +211,19 @@ __device__ __forceinline__ void unpack_sector(const Sector& s, float* v) {
         Elem<DT>::unpack(make_uint4(s.w[4], s.w[5], s.w[6], s.w[7]), v + 8);
     }
 }
-// 32 values, of which the first n are there, to a row at a multiple of 32 bytes.
+// What rows are a multiple of: nothing that helps, 16 bytes or 32.
+constexpr int32_t kAnyRows = 0, kHalfRows = 1, kSectorRows = 2;
+
+// 32 values, of which the first n are there, to a row at a multiple of 32 bytes
+// (whole) or of 16.
 template <int DT>
-__device__ __forceinline__ void store_row(char* at, const float (&v)[32], int n) {
+__device__ __forceinline__ void store_row(char* at, const float (&v)[32], int n, bool whole) {
     constexpr int k = 32 / Elem<DT>::kSize;   // values of a sector
 #pragma unroll
     for (int i = 0; i < 32; i += k) {
         if (i + k <= n) {
-            store_sector(at + i * Elem<DT>::kSize, pack_sector<DT>(v + i));
+            if (whole) store_sector(at + i * Elem<DT>::kSize, pack_sector<DT>(v + i));
+            else store_halves(at + i * Elem<DT>::kSize, pack_sector<DT>(v + i));
         } else {
 #pragma unroll
             for (int e = i; e < i + k; ++e)
@@ -225,27 +232,28 @@ __device__ __forceinline__ void store_row(char* at, const float (&v)[32], int n)
     }
 }
 template <int DT>
-__device__ __forceinline__ void load_row(const char* at, float (&v)[32], int n) {
+__device__ __forceinline__ void load_row(const char* at, float (&v)[32], int n, bool whole) {
     constexpr int k = 32 / Elem<DT>::kSize;
 #pragma unroll
     for (int i = 0; i < 32; i += k) {
         if (i + k <= n) {
-            unpack_sector<DT>(load_sector(at + i * Elem<DT>::kSize), v + i);
+            const char* p = at + i * Elem<DT>::kSize;
+            unpack_sector<DT>(whole ? load_sector(p) : load_halves(p), v + i);
         } else {
 #pragma unroll
             for (int e = i; e < i + k; ++e) v[e] = e < n ? Elem<DT>::load(at, e) : 0.0f;
         }
     }
 }
-__device__ __forceinline__ void store_row(char* at, int32_t dtype, const float (&v)[32], int n) {
-    if (dtype == ADAMW_DTYPE_BF16) store_row<ADAMW_DTYPE_BF16>(at, v, n);
-    else if (dtype == ADAMW_DTYPE_FP16) store_row<ADAMW_DTYPE_FP16>(at, v, n);
-    else store_row<ADAMW_DTYPE_FP32>(at, v, n);
+__device__ __forceinline__ void store_row(char* at, int32_t dtype, const float (&v)[32], int n, bool whole) {
+    if (dtype == ADAMW_DTYPE_BF16) store_row<ADAMW_DTYPE_BF16>(at, v, n, whole);
+    else if (dtype == ADAMW_DTYPE_FP16) store_row<ADAMW_DTYPE_FP16>(at, v, n, whole);
+    else store_row<ADAMW_DTYPE_FP32>(at, v, n, whole);
 }
-__device__ __forceinline__ void load_row(const char* at, int32_t dtype, float (&v)[32], int n) {
-    if (dtype == ADAMW_DTYPE_BF16) load_row<ADAMW_DTYPE_BF16>(at, v, n);
-    else if (dtype == ADAMW_DTYPE_FP16) load_row<ADAMW_DTYPE_FP16>(at, v, n);
-    else load_row<ADAMW_DTYPE_FP32>(at, v, n);
+__device__ __forceinline__ void load_row(const char* at, int32_t dtype, float (&v)[32], int n, bool whole) {
+    if (dtype == ADAMW_DTYPE_BF16) load_row<ADAMW_DTYPE_BF16>(at, v, n, whole);
+    else if (dtype == ADAMW_DTYPE_FP16) load_row<ADAMW_DTYPE_FP16>(at, v, n, whole);
+    else load_row<ADAMW_DTYPE_FP32>(at, v, n, whole);
 }
 __device__ __forceinline__ void store_as(char* at, int64_t i, int32_t dtype, float v) {
     if (dtype == ADAMW_DTYPE_BF16) Elem<ADAMW_DTYPE_BF16>::store(at, i, v);
@@ -338,15 +346,21 @@ using PairTile = TileShape<2, 256>;     // 256 x 256 by a pair
 using WideTile = TileShape<1, 256>;     // 128 x 256 by one CTA
 using SmallTile = TileShape<1, 128>;    // 128 x 128 by one CTA
 
-// Which shape a product takes: the one whose list of tiles is done first by
-// this estimate, in cycles: a step of 64 k takes TILE_STEP, and what a tile's
-// epilogue takes beyond its neighbour's products TILE_REST.
+// Which shape a product takes: the one whose list of tiles is done first by this
+// estimate, in cycles: a step of 64 k takes `step`, and what a tile's epilogue
+// takes beyond its neighbour's products `rest`.  A 128-column product of 16 k
+// takes the tensor cores of an SM as long as one of 256 columns (125 cycles
+// against 128, measured without loads), so SmallTile has half the rate and wins
+// where its tiles are few or its columns fewer than 128.  Measured: 8192^3 551,
+// 673 and 970 us in the three shapes; the Gram matrix of 515 x 1031 in three
+// matrices 17, 18 and 13 us.  (256 x 128 by a pair took as long as SmallTile
+// for twice its columns, and is not kept.)
 struct TileChoice {
     int64_t tiles[3];   // of each shape; 0: not to be taken
 };
 constexpr int kPairShape = 0, kWideShape = 1, kSmallShape = 2;
 inline int choose_shape(const TileChoice& c, int64_t steps, int pairs, int sms) {
-    const int64_t step[3] = {TILE_STEP0, TILE_STEP1, TILE_STEP2}, rest[3] = {TILE_REST0, TILE_REST1, TILE_REST2};
+    const int64_t step[3] = {512, 540, 500}, rest[3] = {4000, 4000, 2500};
     const int units[3] = {pairs, sms, sms};
     int best = -1;
     int64_t least = 0;
@@ -612,6 +626,16 @@ inline bool overlap(const adamw_matrices_t& a, const adamw_matrices_t& b) {
     };
     if (a.batch == 0 || a.rows == 0 || a.cols == 0 || b.batch == 0 || b.rows == 0 || b.cols == 0) return false;
     return reinterpret_cast<uintptr_t>(a.data) < end(b) && reinterpret_cast<uintptr_t>(b.data) < end(a);
+}
+
+// What the rows of all matrices are a multiple of.
+inline int32_t rows_at(const adamw_matrices_t& m) {
+    const int size = dtype_size(m.dtype);
+    auto whole = [&](int bytes) {
+        return aligned(m.data, uintptr_t(bytes)) && (m.rows <= 1 || m.row_stride * size % bytes == 0) &&
+               (m.batch <= 1 || m.batch_stride * size % bytes == 0);
+    };
+    return whole(32) ? kSectorRows : whole(16) ? kHalfRows : kAnyRows;
 }
 
 using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
