@@ -115,6 +115,8 @@ struct ExpertRows {
     static constexpr size_t kTable = sizeof(Groups);
     static constexpr uint32_t kRing = 196608;
     static constexpr int kWarps = 4;
+    static constexpr uint32_t kStaging = 4096;
+    static constexpr bool kStaged = false;
     struct Extra {};
     struct Out {
         RowsAt y;       // from the first row and column of the CTA's part
@@ -188,6 +190,8 @@ struct ExpertOuter {
     static constexpr size_t kTable = sizeof(Groups);
     static constexpr uint32_t kRing = 196608;
     static constexpr int kWarps = 4;
+    static constexpr uint32_t kStaging = 4096;
+    static constexpr bool kStaged = false;
     struct Extra {};
     struct Out {
         RowsAt dw;      // from the first row and column of the CTA's part

@@ -400,14 +400,14 @@ enum Kind { kGram, kPoly, kApply, kResult, kUpdate };
 
 struct ProductShape {
     CUtensorMap a, b;
+    // blocks of the epilogue, 32 rows of 64: what it reads (X or G, and X's second
+    // fp16), what it writes, and the mirrored result, 64 rows of 32
+    CUtensorMap in, low, result, turned;
     Shape s;
     int32_t m, n, k;                   // the product's own
     int32_t tiles_m, tiles_n, per;     // tiles of a matrix
     int32_t first_tile;
     bool a_mn, b_mn;
-    uint16_t* out;                     // G, Q or the next hi
-    const uint16_t* hi;                // X, or G for Q
-    uint16_t* lo;
     float rate;                        // of the update
 };
 
@@ -427,20 +427,18 @@ struct Product {
     using Params = ProductParams;
     static constexpr bool kTail = false;
     static constexpr size_t kTable = 0;
-    // Eight warps: with four, the reads of X (a microsecond each) made a tile's
-    // epilogue longer than its products.
+    // Eight warps, each with two staged blocks: X, G and their like come and go
+    // by TMA, in rows of 128 bytes.  Sectors by threads made four times the requests,
+    // and the epilogue longer than the products of up to 2048 k (apply of 16 x 2048^2
+    // with both fp16 of X 192 us, of 32 x 512 x 1024 51 us; staged 185 and 41).
     static constexpr int kWarps = 8;
-    // One stage less than fits: the epilogues' sectors go through an L1 of what
-    // shared memory leaves (apply of 16 x 2048^2 203 -> 192 us, 32 x 512 x 1024 58 -> 51).
-    static constexpr uint32_t kRing = S::kStageBytes > 32768 ? 196608 : 163840;
+    static constexpr uint32_t kStaging = 8192;
+    static constexpr bool kStaged = true;
+    static constexpr uint32_t kRing = S::kStageBytes > 32768 ? 147456 : 163840;
     static constexpr bool kSymmetric = KIND == kGram || KIND == kPoly;
     // tiles of rows to a tile of columns
     static constexpr int kRatio = S::kCols / S::kRows;
 
-    // what the epilogue adds to the product
-    struct Extra {
-        Sector hi[KIND == kGram ? 1 : 2], lo[LOW_IN ? 2 : 1];
-    };
     struct Out {
         // by value: read through a pointer to the arguments, each of these cost
         // a trip to L1 in every vector
@@ -448,8 +446,7 @@ struct Product {
         int32_t matrix, row, col;   // of the CTA's part
         int32_t vector;             // of the result's rows
         bool mirrored, skip;
-        uint16_t *out, *lo;
-        const uint16_t* hi;
+        const ProductShape* maps;
         char *dst, *param;          // the result, or the master and the parameter
         int64_t dst_ld;
         int32_t dst_type;
@@ -513,10 +510,7 @@ struct Product {
         o.a = p.a;
         o.b = p.b;
         o.c = p.c * kUnscale;
-        const int64_t at = o.matrix * (kSymmetric ? c.s.small_stride : c.s.stride);
-        o.out = c.out + at;
-        o.hi = c.hi + at;
-        o.lo = c.lo + at;
+        o.maps = &c;
         if constexpr (KIND == kResult) {
             o.dst_type = p.dst.dtype;
             o.dst = p.dst.data + o.matrix * p.dst.batch_stride * (o.dst_type == ADAMW_DTYPE_FP32 ? 4 : 2);
@@ -539,80 +533,126 @@ struct Product {
     __device__ static bool wanted(const Params&, const Out& o, int row, int col) {
         return !o.skip && o.row + row < o.m && o.col + col < o.n;
     }
-    __device__ static bool mirrored(const Out& o) { return o.mirrored; }
-    __device__ static void fetch(const Params&, const Out& o, int row, int col, Extra& x) {
-        if (KIND == kGram || o.row + row >= o.m) return;
-        const int64_t at = int64_t(o.row + row) * o.ld + o.col + col;
-        const int n = o.ld - o.col - col;   // the working copies' rows are whole sectors
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (i * 16 >= n) break;
-            x.hi[i] = load_sector(o.hi + at + i * 16);
-            if constexpr (LOW_IN) x.lo[i] = load_sector(o.lo + at + i * 16);
+    // X or G at the warp's block from column `col`, into its buffers.
+    __device__ static void begin(const Params& p, const Out& o, Staged& s, int col) {
+        if (KIND == kGram || !wanted(p, o, s.row, col)) return;
+        if (elected()) {
+            barrier_expect(s.bar, LOW_IN ? 8192 : 4096);
+            load_box<1>(smem_addr(s.one), &o.maps->in, o.col + col, o.row + s.row, o.matrix, s.bar);
+            if (LOW_IN) load_box<1>(smem_addr(s.two), &o.maps->low, o.col + col, o.row + s.row, o.matrix, s.bar);
         }
+        __syncwarp();
     }
-    // Results whose rows are not whole sectors go element by element.
-    __device__ static bool scalar(const Out& o) { return (KIND == kResult || KIND == kUpdate) && !o.vector; }
-    __device__ static void store(const Params&, const Out& o, int row, int col, const Extra& x, float (&v)[32]) {
-        if (o.row + row >= o.m) return;
-        const int64_t at = int64_t(o.row + row) * o.ld + o.col + col;
-        const int n = o.ld - o.col - col;
+    __device__ static bool finish(const Params& p, const Out& o, Staged& s) {
+        for (int c = s.col; c < s.end; c += kBlock64) {
+            if (!wanted(p, o, s.row, c)) continue;
+            uint4 hi[KIND == kGram ? 1 : 8], low[LOW_IN ? 8 : 1];
+            if constexpr (KIND != kGram) {
+                if (!s.wait.warp(s.bar, s.turn)) return false;
+                s.turn ^= 1;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (i * 16 >= n) break;
-            float* y = v + i * 16;
-            if constexpr (KIND == kGram) {
+                for (int j = 0; j < 8; ++j) {
+                    hi[j] = *unit_of(s.one, s.lane, j);
+                    if constexpr (LOW_IN) low[j] = *unit_of(s.two, s.lane, j);
+                }
+                __syncwarp();
+            }
 #pragma unroll
-                for (int e = 0; e < 16; ++e) y[e] *= kUnscale;
-                store_sector(o.out + at + i * 16, pack_sector<ADAMW_DTYPE_FP16>(y));
-            } else {
-                float h[16];
-                unpack_sector<ADAMW_DTYPE_FP16>(x.hi[i], h);
-                if constexpr (KIND == kPoly) {
+            for (int half = 0; half < 2; ++half) {
+                float v[32];
+                tmem_load(s.acc + uint32_t(c + half * 32), v);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) y[e] = fmaf(o.b, h[e], o.c * y[e]);
-                    store_sector(o.out + at + i * 16, pack_sector<ADAMW_DTYPE_FP16>(y));
-                } else {
-                    if constexpr (LOW_IN) {
-                        float l[16];
-                        unpack_sector<ADAMW_DTYPE_FP16>(x.lo[i], l);
+                for (int j = 0; j < 4; ++j) {
+                    float* y = v + j * 8;
+                    float h[8];
+                    if constexpr (KIND == kGram) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) h[e] = fmaf(l[e], 1.0f / kLow, h[e]);
-                    }
+                        for (int e = 0; e < 8; ++e) y[e] *= kUnscale;
+                    } else if constexpr (KIND == kPoly) {
+                        Fp16::unpack(hi[half * 4 + j], h);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) y[e] = fmaf(o.a, h[e], y[e] * kUnscale);
-                    if constexpr (KIND == kApply) {
-                        const Sector hi = pack_sector<ADAMW_DTYPE_FP16>(y);
-                        store_sector(o.out + at + i * 16, hi);
-                        if constexpr (LOW_OUT) {
-                            unpack_sector<ADAMW_DTYPE_FP16>(hi, h);
+                        for (int e = 0; e < 8; ++e) y[e] = fmaf(o.b, h[e], o.c * y[e]);
+                    } else {
+                        Fp16::unpack(hi[half * 4 + j], h);
+                        if constexpr (LOW_IN) {
+                            float l[8];
+                            Fp16::unpack(low[half * 4 + j], l);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) y[e] = (y[e] - h[e]) * kLow;
-                            store_sector(o.lo + at + i * 16, pack_sector<ADAMW_DTYPE_FP16>(y));
+                            for (int e = 0; e < 8; ++e) h[e] = fmaf(l[e], 1.0f / kLow, h[e]);
                         }
-                    } else if constexpr (KIND == kResult) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) y[e] *= kUnscale;
+                        for (int e = 0; e < 8; ++e) y[e] = fmaf(o.a, h[e], y[e] * kUnscale);
+                    }
+                    if constexpr (KIND <= kApply) {
+                        if constexpr (LOW_OUT) {
+                            uint4 a, b;
+                            split8(*reinterpret_cast<float(*)[8]>(y), &a, &b);
+                            *unit_of(s.one, s.lane, half * 4 + j) = a;
+                            *unit_of(s.two, s.lane, half * 4 + j) = b;
+                        } else {
+                            *unit_of(s.one, s.lane, half * 4 + j) = Fp16::pack(y);
+                        }
                     }
                 }
+                if constexpr (kSymmetric) {
+                    if (o.mirrored) {   // row e of 64 bytes: the block's column
+                        __half* turned = reinterpret_cast<__half*>(s.two) + half * 32 * 32 + s.lane;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) turned[e * 32] = __float2half_rn(v[e]);
+                    }
+                }
+                if constexpr (KIND == kResult || KIND == kUpdate) last(p, o, s, c + half * 32, v);
             }
+            if constexpr (KIND <= kApply) {
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (elected()) {
+                    store_box(&o.maps->result, o.col + c, o.row + s.row, o.matrix, smem_addr(s.one));
+                    if constexpr (LOW_OUT) store_box(&o.maps->low, o.col + c, o.row + s.row, o.matrix, smem_addr(s.two));
+                    if constexpr (kSymmetric) {
+                        if (o.mirrored) store_box(&o.maps->turned, o.row + s.row, o.col + c, o.matrix, smem_addr(s.two));
+                    }
+                    stores_read();
+                }
+                __syncwarp();
+            }
+            if (c + kBlock64 < s.end) begin(p, o, s, c + kBlock64);
         }
-        if constexpr (KIND == kResult || KIND == kUpdate) {
-            if (!o.vector) return;
-            const int64_t to = int64_t(o.row + row) * o.dst_ld + o.col + col;
-            const int left = o.cols - o.col - col;
+        return true;
+    }
+    // 32 columns of the result, or of the update.
+    __device__ static void last(const Params& p, const Out& o, Staged& s, int c, float (&v)[32]) {
+        const int row = s.row + s.lane, left = o.cols - o.col - c;
+        const int64_t to = int64_t(o.row + row) * o.dst_ld + o.col + c;
+        const bool whole = o.vector == kSectorRows;
+        if constexpr (KIND == kResult) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] *= kUnscale;
+        }
+        if (o.vector) {
+            if (o.row + row >= o.m) return;
             if constexpr (KIND == kResult) {
-                store_row(o.dst + to * (o.dst_type == ADAMW_DTYPE_FP32 ? 4 : 2), o.dst_type, v, left, o.vector == kSectorRows);
+                store_row(o.dst + to * (o.dst_type == ADAMW_DTYPE_FP32 ? 4 : 2), o.dst_type, v, left, whole);
             } else {
                 float w[32];
-                const bool whole = o.vector == kSectorRows;
                 load_row<ADAMW_DTYPE_FP32>(o.dst + to * 4, w, left, whole);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = fmaf(-o.rate, v[e], o.decay * w[e]);
                 store_row<ADAMW_DTYPE_FP32>(o.dst + to * 4, v, left, whole);
                 store_row<ADAMW_DTYPE_BF16>(o.param + to * 2, v, left, whole);
             }
+            return;
         }
+        // rows that are not whole vectors: element by element, neighbours by
+        // neighbouring lanes, through the first buffer
+#pragma unroll
+        for (int i = 0; i < 8; ++i) *reinterpret_cast<float4*>(unit_of(s.one, s.lane, i)) = *reinterpret_cast<float4*>(v + i * 4);
+        __syncwarp();
+#pragma unroll 4
+        for (int r = 0; r < 32; ++r)
+            store_one(p, o, s.row + r, c + s.lane, reinterpret_cast<const float*>(unit_of(s.one, r, s.lane / 4))[s.lane % 4]);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the next block comes by TMA
+        __syncwarp();
     }
     __device__ static void store_one(const Params& p, const Out& o, int row, int col, float v) {
         if (!wanted(p, o, row, col)) return;
@@ -625,13 +665,6 @@ struct Product {
             *w = v;
             store_as(o.param, to, ADAMW_DTYPE_BF16, v);
         }
-    }
-    __device__ static void mirror(const Params&, const Out& o, int row, int col, const float (&v)[32]) {
-        if (!kSymmetric || o.row + row >= o.m) return;
-        __half* at = reinterpret_cast<__half*>(o.out) + int64_t(o.col + col) * o.ld + o.row + row;
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-            if (o.col + col + e < o.n) at[int64_t(e) * o.ld] = __float2half_rn(v[e]);
     }
 };
 
@@ -710,13 +743,15 @@ bool fill(const Group& g, int kind, int which, ProductParams* p) {
             q.k = wide ? s.cols : s.rows;
             ok = tensor_map(&q.a, false, b.x[which], s.count, s.rows, s.cols, s.ld, s.stride, wide ? kRowsOfCta : kStepK) &&
                  tensor_map(&q.b, false, b.x[which], s.count, s.rows, s.cols, s.ld, s.stride, wide ? S::kBRows : kStepK);
-            q.out = b.gram;
+            ok = ok && tensor_map(&q.result, false, b.gram, s.count, s.side, s.side, s.small_ld, s.small_stride, 32) &&
+                 tensor_map(&q.turned, false, b.gram, s.count, s.side, s.side, s.small_ld, s.small_stride, 64, 32);
         } else if (kind == kPoly) {
             q.m = q.n = q.k = s.side;
             ok = tensor_map(&q.a, false, b.gram, s.count, s.side, s.side, s.small_ld, s.small_stride, kRowsOfCta) &&
                  tensor_map(&q.b, false, b.gram, s.count, s.side, s.side, s.small_ld, s.small_stride, S::kBRows);
-            q.hi = b.gram;
-            q.out = b.poly;
+            ok = ok && tensor_map(&q.in, false, b.gram, s.count, s.side, s.side, s.small_ld, s.small_stride, 32) &&
+                 tensor_map(&q.result, false, b.poly, s.count, s.side, s.side, s.small_ld, s.small_stride, 32) &&
+                 tensor_map(&q.turned, false, b.poly, s.count, s.side, s.side, s.small_ld, s.small_stride, 64, 32);
         } else {
             q.m = s.rows;
             q.n = s.cols;
@@ -725,9 +760,9 @@ bool fill(const Group& g, int kind, int which, ProductParams* p) {
             ok = tensor_map(wide ? &q.b : &q.a, false, b.x[which], s.count, s.rows, s.cols, s.ld, s.stride, wide ? kStepK : kRowsOfCta) &&
                  tensor_map(wide ? &q.a : &q.b, false, b.poly, s.count, s.side, s.side, s.small_ld, s.small_stride,
                             wide ? kRowsOfCta : S::kBRows);
-            q.hi = b.x[which];
-            q.lo = b.lo;
-            q.out = b.x[which ^ 1];
+            ok = ok && tensor_map(&q.in, false, b.x[which], s.count, s.rows, s.cols, s.ld, s.stride, 32) &&
+                 tensor_map(&q.low, false, b.lo, s.count, s.rows, s.cols, s.ld, s.stride, 32) &&
+                 tensor_map(&q.result, false, b.x[which ^ 1], s.count, s.rows, s.cols, s.ld, s.stride, 32);
         }
         if (!ok) return false;
         q.tiles_m = int32_t(up(q.m, S::kRows) / S::kRows);

@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kStepK = 64;                  // elements of k in a stage: 128 bytes, one swizzle row
 constexpr int kRowsOfCta = 128;             // accumulator rows of a CTA: the lanes of tensor memory
-constexpr uint32_t kStagingOfWarp = 4096;   // 32 x 32 fp32
+constexpr int kBlock64 = 64;                // columns of a staged block: 32 rows of 128 bytes
 constexpr uint32_t kControlRoom = 1024;
 constexpr long long kGiveUp = 1000000000ll; // cycles
 
@@ -91,6 +91,17 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, i
             "[%0], [%1, {%2, %3, %4}], [%5];"
             ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
 }
+
+// A box of this CTA's shared memory into a tensor; what is outside is left out.
+__device__ __forceinline__ void store_box(const CUtensorMap* map, int x, int y, int z, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x), "r"(y),
+                 "r"(z), "r"(src) : "memory");
+}
+// This thread's stores so far have left shared memory / are done.
+__device__ __forceinline__ void stores_read() {
+    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 template <int PAIR>
 __device__ __forceinline__ void tmem_alloc(uint32_t where, uint32_t columns) {
@@ -301,6 +312,7 @@ struct TileLoads {
 struct Control {
     uint64_t full[16], empty[16], tail[16];
     uint64_t acc_full[2], acc_empty[2];
+    uint64_t block[8];   // of the epilogue warps: their staged blocks are there
     uint32_t tmem;
     int32_t failed;
 };
@@ -332,6 +344,20 @@ struct Waiter {
         }
     }
 };
+
+// What a staged epilogue has: a warp's two buffers of 32 rows of 128 bytes, in
+// the swizzle of the operands.
+struct Staged {
+    unsigned char *one, *two;
+    uint32_t bar, turn;   // where boxes to them arrive, and its parity
+    int lane, row, col, end;   // the warp's first row, its columns
+    uint32_t acc;         // its lanes of the accumulator
+    Waiter wait;
+};
+// Unit j (16 bytes) of the thread's row in a buffer.
+__device__ __forceinline__ uint4* unit_of(unsigned char* buffer, int lane, int j) {
+    return reinterpret_cast<uint4*>(buffer + lane * 128 + ((j ^ (lane & 7)) << 4));
+}
 
 template <int PAIR_, int COLS_>
 struct TileShape {
@@ -379,7 +405,7 @@ inline int choose_shape(const TileChoice& c, int64_t steps, int pairs, int sms) 
 template <class P>
 constexpr size_t tile_smem() {
     static_assert(P::kWarps == 4 || P::kWarps == 8, "epilogue warps");
-    constexpr size_t n = 1024 + P::kRing + P::kWarps * kStagingOfWarp + kControlRoom + P::kTable;
+    constexpr size_t n = 1024 + P::kRing + P::kWarps * P::kStaging + kControlRoom + P::kTable;
     static_assert(n <= 232448, "shared memory of a CTA");
     return n;
 }
@@ -398,6 +424,10 @@ constexpr int tile_threads() { return 128 + 32 * P::kWarps; }
 //   bf16(p)                              type of the operands
 //   Out: what the epilogue keeps of a tile; out<S>(p, table, tile, rank)
 //   wanted(p, out, row, col): whether the 32 x 32 block there has anything to store
+//   kStaging        bytes of shared memory of an epilogue warp
+//   kStaged: the policy takes a tile's epilogue as a whole, through Staged:
+//        begin(p, out, staged, col) asks for what the block at `col` reads, before
+//        the products are waited for; finish(p, out, staged) does the rest.  Else:
 //   Extra, fetch(p, out, row, col, Extra&): what store wants of memory for 32
 //        columns from `col` of row `row` of the CTA's part, fetched a block ahead
 //   store(p, out, row, col, extra, float (&v)[32]): the results there; leaves
@@ -406,9 +436,9 @@ constexpr int tile_threads() { return 128 + 32 * P::kWarps; }
 //        neighbouring lanes have neighbouring rows
 //   scalar(out), store_one(p, out, row, col, v): whether results go element by
 //        element (rows that are not whole vectors), neighbours by neighbouring lanes
-// A thread has a row, and reads and writes whole 32-byte sectors of it: no
+// There a thread has a row, and reads and writes whole 32-byte sectors of it: no
 // shared memory between tensor memory and the results, and a tenth of the
-// instructions of an epilogue that regroups them (1.7 us a block before).
+// instructions of an epilogue that regroups them.
 template <class P, class S>
 __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid_constant__ typename P::Params p) {
     constexpr int PAIR = S::kPair, kStages = int(P::kRing / S::kStageBytes);
@@ -417,8 +447,8 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
     // 1024-byte boundary: the swizzle goes by address bits; the same in both CTAs
     unsigned char* base = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
     unsigned char* ring = base;
-    float* staging = reinterpret_cast<float*>(base + P::kRing);
-    Control* ctl = reinterpret_cast<Control*>(base + P::kRing + P::kWarps * kStagingOfWarp);
+    unsigned char* staging = base + P::kRing;
+    Control* ctl = reinterpret_cast<Control*>(base + P::kRing + P::kWarps * P::kStaging);
     unsigned char* table = reinterpret_cast<unsigned char*>(ctl) + kControlRoom;
 
     const int warp = int(threadIdx.x) / 32, lane = int(threadIdx.x) % 32;
@@ -433,6 +463,7 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
             barrier_init(smem_addr(&ctl->acc_full[a]), 1);
             barrier_init(smem_addr(&ctl->acc_empty[a]), P::kWarps * PAIR);
         }
+        for (int k = 0; k < P::kWarps; ++k) barrier_init(smem_addr(&ctl->block[k]), 1);
         ctl->failed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -551,7 +582,9 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
         }
     } else if (warp >= 4) {
         // ---- results
-        float* mine = staging + (warp - 4) * 1024;
+        float* mine = reinterpret_cast<float*>(staging + (warp - 4) * P::kStaging);
+        Staged block = {reinterpret_cast<unsigned char*>(mine), reinterpret_cast<unsigned char*>(mine) + 4096,
+                        smem_addr(&ctl->block[warp - 4]), 0, lane, warp % 4 * 32, 0, 0, 0, wait};
         uint32_t n = 0;
         bool ok = true;
         // element (row, col) of the 32 x 32 block, its 16-byte units swizzled
@@ -565,33 +598,43 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
             const int row0 = warp % 4 * 32;
             constexpr int kShare = S::kCols / (P::kWarps / 4);   // columns of the warp
             const int c0 = (warp - 4) / 4 * kShare, c1 = c0 + kShare;
-            const int row = row0 + lane;
-            typename P::Extra next;
-            if (P::wanted(p, out, row0, c0)) P::fetch(p, out, row, c0, next);
-            if (w.k_len > 0) {
+            if constexpr (P::kStaged) {
+                block.col = c0;
+                block.end = c1;
+                block.acc = tmem + (uint32_t(row0) << 16) + acc * S::kCols;
+                P::begin(p, out, block, c0);
                 if (!(ok = wait.warp(smem_addr(&ctl->acc_full[acc]), n >> 1 & 1))) break;
                 tmem_after();
-            }
-            for (int c = c0; c < c1; c += 32) {
-                if (!P::wanted(p, out, row0, c)) continue;
-                const typename P::Extra now = next;
-                if (c + 32 < c1 && P::wanted(p, out, row0, c + 32)) P::fetch(p, out, row, c + 32, next);
-                float v[32];
+                if (!(ok = P::finish(p, out, block))) break;
+            } else {
+                const int row = row0 + lane;
+                typename P::Extra next;
+                if (P::wanted(p, out, row0, c0)) P::fetch(p, out, row, c0, next);
                 if (w.k_len > 0) {
-                    tmem_load(tmem + (uint32_t(row0) << 16) + acc * S::kCols + uint32_t(c), v);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+                    if (!(ok = wait.warp(smem_addr(&ctl->acc_full[acc]), n >> 1 & 1))) break;
+                    tmem_after();
                 }
-                P::store(p, out, row, c, now, v);
-                if (P::mirrored(out)) P::mirror(p, out, row, c, v);
-                if (P::scalar(out)) {
+                for (int c = c0; c < c1; c += 32) {
+                    if (!P::wanted(p, out, row0, c)) continue;
+                    const typename P::Extra now = next;
+                    if (c + 32 < c1 && P::wanted(p, out, row0, c + 32)) P::fetch(p, out, row, c + 32, next);
+                    float v[32];
+                    if (w.k_len > 0) {
+                        tmem_load(tmem + (uint32_t(row0) << 16) + acc * S::kCols + uint32_t(c), v);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(place(lane, i)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                    __syncwarp();
+                        for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+                    }
+                    P::store(p, out, row, c, now, v);
+                    if (P::mirrored(out)) P::mirror(p, out, row, c, v);
+                    if (P::scalar(out)) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(place(lane, i)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                        __syncwarp();
 #pragma unroll 4
-                    for (int r = 0; r < 32; ++r) P::store_one(p, out, row0 + r, c + lane, *place(r, lane));
-                    __syncwarp();
+                        for (int r = 0; r < 32; ++r) P::store_one(p, out, row0 + r, c + lane, *place(r, lane));
+                        __syncwarp();
+                    }
                 }
             }
             if (w.k_len > 0) {
@@ -601,6 +644,8 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
                 ++n;
             }
         }
+        __syncwarp();
+        if (P::kStaged && elected()) stores_done();
     }
     __syncwarp();
     __syncthreads();
@@ -655,10 +700,10 @@ inline EncodeTiled encode_tiled() {
 }
 
 // The map of a batch of matrices [batch][rows][cols] of 16-bit elements, rows
-// `ld` and matrices `stride` elements apart, for boxes of 64 columns and
-// `box_rows` rows.  Base 16-byte aligned; ld and stride multiples of 8.
+// `ld` and matrices `stride` elements apart, for boxes of 64 columns (swizzled; or
+// fewer, as they are) and `box_rows` rows.  Base 16-byte aligned; ld and stride multiples of 8.
 inline bool tensor_map(CUtensorMap* map, bool bf16, const void* data, int64_t batch, int64_t rows, int64_t cols,
-                       int64_t ld, int64_t stride, int box_rows) {
+                       int64_t ld, int64_t stride, int box_rows, int box_cols = kStepK) {
     const EncodeTiled f = encode_tiled();
     if (!f) {
         adamw::set_cuda_error("cuTensorMapEncodeTiled", "not found in the driver");
@@ -666,11 +711,11 @@ inline bool tensor_map(CUtensorMap* map, bool bf16, const void* data, int64_t ba
     }
     const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(batch)};
     const cuuint64_t strides[2] = {cuuint64_t(ld) * 2, cuuint64_t(stride > 0 ? stride : ld) * 2};
-    const cuuint32_t box[3] = {cuuint32_t(kStepK), cuuint32_t(box_rows), 1};
+    const cuuint32_t box[3] = {cuuint32_t(box_cols), cuuint32_t(box_rows), 1};
     const cuuint32_t step[3] = {1, 1, 1};
     const CUresult r = f(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                          const_cast<void*>(data), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         box_cols == kStepK ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r == CUDA_SUCCESS) return true;
     adamw::set_cuda_error("cuTensorMapEncodeTiled", "refused the layout");
