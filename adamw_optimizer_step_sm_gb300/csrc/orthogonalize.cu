@@ -543,7 +543,7 @@ struct Product {
         }
         __syncwarp();
     }
-    __device__ static bool finish(const Params& p, const Out& o, Staged& s) {
+    __device__ static bool finish(const Params& p, const Out& o, Staged& s, bool) {
         for (int c = s.col; c < s.end; c += kBlock64) {
             if (!wanted(p, o, s.row, c)) continue;
             uint4 hi[KIND == kGram ? 1 : 8], low[LOW_IN ? 8 : 1];

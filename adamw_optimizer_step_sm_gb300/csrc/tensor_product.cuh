@@ -101,6 +101,10 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, int x, int y, 
 __device__ __forceinline__ void stores_read() {
     asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
 }
+// All but the last group of them.
+__device__ __forceinline__ void stores_read_but_one() {
+    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 1;" ::: "memory");
+}
 __device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 template <int PAIR>
@@ -171,6 +175,16 @@ __device__ __forceinline__ void tmem_load(uint32_t at, float (&v)[32]) {
           "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
           "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
         : "r"(at) : "memory");
+}
+
+// The same, zeros where nothing was summed.
+__device__ __forceinline__ void load_acc(uint32_t at, bool any, float (&v)[32]) {
+    if (any) {
+        tmem_load(at, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+    }
 }
 
 // A sector of 32 bytes, at a multiple of 32.
@@ -345,8 +359,8 @@ struct Waiter {
     }
 };
 
-// What a staged epilogue has: a warp's two buffers of 32 rows of 128 bytes, in
-// the swizzle of the operands.
+// What a staged epilogue has: a warp's buffers of 32 rows of 128 bytes, in the
+// swizzle of the operands (one or two of them, by P::kStaging).
 struct Staged {
     unsigned char *one, *two;
     uint32_t bar, turn;   // where boxes to them arrive, and its parity
@@ -427,18 +441,13 @@ constexpr int tile_threads() { return 128 + 32 * P::kWarps; }
 //   kStaging        bytes of shared memory of an epilogue warp
 //   kStaged: the policy takes a tile's epilogue as a whole, through Staged:
 //        begin(p, out, staged, col) asks for what the block at `col` reads, before
-//        the products are waited for; finish(p, out, staged) does the rest.  Else:
-//   Extra, fetch(p, out, row, col, Extra&): what store wants of memory for 32
-//        columns from `col` of row `row` of the CTA's part, fetched a block ahead
-//   store(p, out, row, col, extra, float (&v)[32]): the results there; leaves
-//        in v what mirror or store_one store
-//   mirrored(out), mirror(p, out, row, col, v): the transposed tile's elements;
-//        neighbouring lanes have neighbouring rows
+//        the products are waited for; finish(p, out, staged, any) does the rest
+//        (any: k is not empty).  Else:
+//   store(p, out, row, col, float (&v)[32]): results of 32 columns from `col` of row
+//        `row` of the CTA's part
 //   scalar(out), store_one(p, out, row, col, v): whether results go element by
 //        element (rows that are not whole vectors), neighbours by neighbouring lanes
-// There a thread has a row, and reads and writes whole 32-byte sectors of it: no
-// shared memory between tensor memory and the results, and a tenth of the
-// instructions of an epilogue that regroups them.
+// There a thread has a row, and writes whole 32-byte sectors of it.
 template <class P, class S>
 __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid_constant__ typename P::Params p) {
     constexpr int PAIR = S::kPair, kStages = int(P::kRing / S::kStageBytes);
@@ -603,30 +612,22 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
                 block.end = c1;
                 block.acc = tmem + (uint32_t(row0) << 16) + acc * S::kCols;
                 P::begin(p, out, block, c0);
-                if (!(ok = wait.warp(smem_addr(&ctl->acc_full[acc]), n >> 1 & 1))) break;
-                tmem_after();
-                if (!(ok = P::finish(p, out, block))) break;
+                if (w.k_len > 0) {
+                    if (!(ok = wait.warp(smem_addr(&ctl->acc_full[acc]), n >> 1 & 1))) break;
+                    tmem_after();
+                }
+                if (!(ok = P::finish(p, out, block, w.k_len > 0))) break;
             } else {
                 const int row = row0 + lane;
-                typename P::Extra next;
-                if (P::wanted(p, out, row0, c0)) P::fetch(p, out, row, c0, next);
                 if (w.k_len > 0) {
                     if (!(ok = wait.warp(smem_addr(&ctl->acc_full[acc]), n >> 1 & 1))) break;
                     tmem_after();
                 }
                 for (int c = c0; c < c1; c += 32) {
                     if (!P::wanted(p, out, row0, c)) continue;
-                    const typename P::Extra now = next;
-                    if (c + 32 < c1 && P::wanted(p, out, row0, c + 32)) P::fetch(p, out, row, c + 32, next);
                     float v[32];
-                    if (w.k_len > 0) {
-                        tmem_load(tmem + (uint32_t(row0) << 16) + acc * S::kCols + uint32_t(c), v);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-                    }
-                    P::store(p, out, row, c, now, v);
-                    if (P::mirrored(out)) P::mirror(p, out, row, c, v);
+                    load_acc(tmem + (uint32_t(row0) << 16) + acc * S::kCols + uint32_t(c), w.k_len > 0, v);
+                    P::store(p, out, row, c, v);
                     if (P::scalar(out)) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(place(lane, i)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
