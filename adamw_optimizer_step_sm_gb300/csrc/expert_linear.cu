@@ -151,7 +151,7 @@ struct ExpertRows {
         bool is_bf16, w_mn;
         RowsAt y;
     };
-    static constexpr bool kTail = false;
+    static constexpr bool kTail = false, kParts = false;
     static constexpr size_t kTable = sizeof(Groups);
     static constexpr uint32_t kRing = 196608;
     static constexpr int kWarps = 4;
@@ -231,7 +231,7 @@ struct ExpertOuter {
         int64_t stride;   // of dw's matrices
         RowsAt dw;
     };
-    static constexpr bool kTail = true;
+    static constexpr bool kTail = true, kParts = false;
     static constexpr size_t kTable = sizeof(Groups);
     static constexpr uint32_t kRing = STAGED < 2 ? 196608 : S::kStageBytes > 32768 ? 147456 : 163840;
     static constexpr int kWarps = 4;

@@ -19,7 +19,11 @@
 // 1.6e-3.  X is kept as hi + lo, two fp16: each step multiplies an error of X in
 // a direction without singular value by a = 3.44, and a rounding of X itself
 // would be such an error; the rounding of the products' operands (hi alone) is
-// multiplied by Q, which vanishes in such directions.
+// multiplied by Q, which vanishes in such directions.  lo is as fine as fp16's
+// subnormals: 2^-24 beside entries of 2^12 X.
+// Thin matrices (a side of at most 128) have few singular values, whose errors do
+// not average out: their Q is kept as two fp16 as well, and Q X is three products
+// (sides of 1 to 32: up to 6.7e-3 off without, 3.5e-3 with, 2e-3 and 1e-3 on average).
 #include <algorithm>
 #include <exception>
 #include <new>
@@ -31,7 +35,6 @@
 namespace {
 
 constexpr float kScale = 4096.0f, kUnscale = 1.0f / 4096.0f;
-constexpr float kLow = 2048.0f;   // lo is kept times this
 
 using Fp16 = Elem<ADAMW_DTYPE_FP16>;
 
@@ -40,6 +43,7 @@ struct Shape {
     int64_t stride, small_stride;   // elements between matrices (of X, of G)
     int32_t rows, cols, ld;         // ld: cols up to a multiple of 16
     int32_t side, small_ld;         // of G
+    bool thin;                      // Q is kept as two fp16
     int32_t count, first;           // matrices, and the first one's number in the list
 };
 
@@ -326,7 +330,7 @@ __device__ __forceinline__ void split8(const float (&x)[8], uint4* hi, uint4* lo
     float h[8], l[8];
     Fp16::unpack(*hi, h);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) l[e] = (x[e] - h[e]) * kLow;
+    for (int e = 0; e < 8; ++e) l[e] = x[e] - h[e];
     *lo = Fp16::pack(l);
 }
 
@@ -399,9 +403,10 @@ CopyKernel<MUON> copy_of(int32_t dtype) {
 enum Kind { kGram, kPoly, kApply, kResult, kUpdate };
 
 struct ProductShape {
-    CUtensorMap a, b;
-    // blocks of the epilogue, 32 rows of 64: what it reads (X or G, and X's second
-    // fp16), what it writes, and the mirrored result, 64 rows of 32
+    CUtensorMap a, b, a_low, b_low;
+    // blocks of the epilogue, 32 rows of 64: what it reads (X or G), second fp16 (X's
+    // that it reads and writes, Q's that it writes), what it writes, and the
+    // mirrored result, 64 rows of 32
     CUtensorMap in, low, result, turned;
     Shape s;
     int32_t m, n, k;                   // the product's own
@@ -425,7 +430,7 @@ struct ProductParams {
 template <int KIND, class S, bool LOW_IN = false, bool LOW_OUT = false>
 struct Product {
     using Params = ProductParams;
-    static constexpr bool kTail = false;
+    static constexpr bool kTail = false, kParts = KIND >= kApply;
     static constexpr size_t kTable = 0;
     // Eight warps, each with two staged blocks: X, G and their like come and go
     // by TMA, in rows of 128 bytes.  Sectors by threads made four times the requests,
@@ -442,10 +447,10 @@ struct Product {
     struct Out {
         // by value: read through a pointer to the arguments, each of these cost
         // a trip to L1 in every vector
-        int32_t m, n, ld, cols;
+        int32_t m, n, cols;
         int32_t matrix, row, col;   // of the CTA's part
         int32_t vector;             // of the result's rows
-        bool mirrored, skip;
+        bool mirrored, skip, thin;
         const ProductShape* maps;
         char *dst, *param;          // the result, or the master and the parameter
         int64_t dst_ld;
@@ -492,6 +497,13 @@ struct Product {
         w.k_len = c.k;
         w.a_mn = c.a_mn;
         w.b_mn = c.b_mn;
+        w.part = 0;
+        if (kParts && c.s.thin) {
+            w.a_low = &c.a_low;
+            w.b_low = &c.b_low;
+            w.part = (c.k + kStepK - 1) / kStepK * kStepK;
+            w.k_len = 3 * w.part;
+        }
     }
     template <class>
     __device__ static Out out(const Params& p, const unsigned char*, int t, uint32_t rank) {
@@ -500,12 +512,12 @@ struct Product {
         const ProductShape& c = find(p, t, &o.matrix, &m, &n);
         o.m = c.m;
         o.n = c.n;
-        o.ld = kSymmetric ? c.s.small_ld : c.s.ld;
         o.cols = c.s.cols;
         o.row = m * S::kRows + int32_t(rank) * kRowsOfCta;
         o.col = n * S::kCols;
         o.mirrored = kSymmetric && m / kRatio != n;
         o.skip = false;
+        o.thin = c.s.thin;
         o.vector = kSectorRows;
         o.a = p.a;
         o.b = p.b;
@@ -578,13 +590,13 @@ struct Product {
                             float l[8];
                             Fp16::unpack(low[half * 4 + j], l);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) h[e] = fmaf(l[e], 1.0f / kLow, h[e]);
+                            for (int e = 0; e < 8; ++e) h[e] += l[e];
                         }
 #pragma unroll
                         for (int e = 0; e < 8; ++e) y[e] = fmaf(o.a, h[e], y[e] * kUnscale);
                     }
                     if constexpr (KIND <= kApply) {
-                        if constexpr (LOW_OUT) {
+                        if (LOW_OUT || (KIND == kPoly && o.thin)) {   // a thin Q is one tile, and nothing is mirrored
                             uint4 a, b;
                             split8(*reinterpret_cast<float(*)[8]>(y), &a, &b);
                             *unit_of(s.one, s.lane, half * 4 + j) = a;
@@ -608,7 +620,7 @@ struct Product {
                 __syncwarp();
                 if (elected()) {
                     store_box(&o.maps->result, o.col + c, o.row + s.row, o.matrix, smem_addr(s.one));
-                    if constexpr (LOW_OUT) store_box(&o.maps->low, o.col + c, o.row + s.row, o.matrix, smem_addr(s.two));
+                    if (LOW_OUT || (KIND == kPoly && o.thin)) store_box(&o.maps->low, o.col + c, o.row + s.row, o.matrix, smem_addr(s.two));
                     if constexpr (kSymmetric) {
                         if (o.mirrored) store_box(&o.maps->turned, o.row + s.row, o.col + c, o.matrix, smem_addr(s.two));
                     }
@@ -684,6 +696,7 @@ Shape shape_of(int64_t rows, int64_t cols) {
     s.side = s.rows <= s.cols ? s.rows : s.cols;
     s.small_ld = int32_t(up(s.side, 16));
     s.small_stride = int64_t(s.side) * s.small_ld;
+    s.thin = s.side <= 128;
     return s;
 }
 int64_t vecs_of(const Shape& s) { return int64_t(s.rows) * (s.ld / 8); }
@@ -691,7 +704,7 @@ int64_t pieces_of(const Shape& s, int32_t piece) { return (vecs_of(s) + piece - 
 
 // The working copies of a shape.
 struct Buffers {
-    uint16_t *x[2], *lo, *gram, *poly;
+    uint16_t *x[2], *lo, *gram, *poly, *poly_lo;
 };
 // A shape's buffers at `at`, each at a multiple of 256 bytes; the bytes they take.
 int64_t place(const Shape& s, char* at, Buffers* b) {
@@ -702,8 +715,9 @@ int64_t place(const Shape& s, char* at, Buffers* b) {
         b->lo = reinterpret_cast<uint16_t*>(at + 2 * big);
         b->gram = reinterpret_cast<uint16_t*>(at + 3 * big);
         b->poly = reinterpret_cast<uint16_t*>(at + 3 * big + small);
+        b->poly_lo = s.thin ? reinterpret_cast<uint16_t*>(at + 3 * big + 2 * small) : nullptr;
     }
-    return 3 * big + 2 * small;
+    return 3 * big + (s.thin ? 3 : 2) * small;
 }
 
 // The products of one group of shapes: at most kMaxShapes.
@@ -752,6 +766,7 @@ bool fill(const Group& g, int kind, int which, ProductParams* p) {
             ok = ok && tensor_map(&q.in, false, b.gram, s.count, s.side, s.side, s.small_ld, s.small_stride, 32) &&
                  tensor_map(&q.result, false, b.poly, s.count, s.side, s.side, s.small_ld, s.small_stride, 32) &&
                  tensor_map(&q.turned, false, b.poly, s.count, s.side, s.side, s.small_ld, s.small_stride, 64, 32);
+            if (ok && s.thin) ok = tensor_map(&q.low, false, b.poly_lo, s.count, s.side, s.side, s.small_ld, s.small_stride, 32);
         } else {
             q.m = s.rows;
             q.n = s.cols;
@@ -760,6 +775,10 @@ bool fill(const Group& g, int kind, int which, ProductParams* p) {
             ok = tensor_map(wide ? &q.b : &q.a, false, b.x[which], s.count, s.rows, s.cols, s.ld, s.stride, wide ? kStepK : kRowsOfCta) &&
                  tensor_map(wide ? &q.a : &q.b, false, b.poly, s.count, s.side, s.side, s.small_ld, s.small_stride,
                             wide ? kRowsOfCta : S::kBRows);
+            if (ok && s.thin)
+                ok = tensor_map(wide ? &q.b_low : &q.a_low, false, b.lo, s.count, s.rows, s.cols, s.ld, s.stride, wide ? kStepK : kRowsOfCta) &&
+                     tensor_map(wide ? &q.a_low : &q.b_low, false, b.poly_lo, s.count, s.side, s.side, s.small_ld, s.small_stride,
+                                wide ? kRowsOfCta : S::kBRows);
             ok = ok && tensor_map(&q.in, false, b.x[which], s.count, s.rows, s.cols, s.ld, s.stride, 32) &&
                  tensor_map(&q.low, false, b.lo, s.count, s.rows, s.cols, s.ld, s.stride, 32) &&
                  tensor_map(&q.result, false, b.x[which ^ 1], s.count, s.rows, s.cols, s.ld, s.stride, 32);
@@ -839,13 +858,15 @@ bool run_steps(const Group& g, const adamw_ortho_t& o, const float* coefs, int l
                cudaStream_t st) {
     auto row = [&](int k) { return coefs + 3 * (k < o.n_coefficients ? k : o.n_coefficients - 1); };
     bool low_in = true;   // X starts as two fp16
+    bool thin = false;    // products of thin matrices take both
+    for (int i = 0; i < g.n; ++i) thin = thin || g.shapes[i].thin;
     for (int k = 0; k < o.steps; ++k) {
         // by how much the steps after this one multiply an error of X in a
         // direction without singular value; up to 16, eleven bits of X are enough
         // (5e-4 of the result at worst, a matrix of few directions)
         double later = 1.0;
         for (int i = k + 1; i < o.steps; ++i) later *= std::fabs(double(row(i)[0]));
-        const bool low_out = low_in && later > 16.0;
+        const bool low_out = low_in && (later > 16.0 || (thin && k + 1 < o.steps));
         const float* c = row(k);
         for (int kind = kGram; kind <= kApply; ++kind) {
             const int which = kind == kApply && k + 1 == o.steps ? last : kind;
@@ -1140,10 +1161,14 @@ int create(const adamw_muon_tensor_t* table, int32_t n, const adamw_muon_options
         }
         order.push_back({t.rows, t.cols, k});
     }
-    // the small ones, which have a kernel of their own, last
-    auto is_small = [](const Entry& e) { return small_ctas(shape_of(e.rows, e.cols)) > 0; };
+    // the thin ones, and the small ones that have a kernel of their own, last
+    auto class_of = [](int64_t rows, int64_t cols) {
+        const Shape s = shape_of(rows, cols);
+        return small_ctas(s) > 0 ? 2 : s.thin ? 1 : 0;
+    };
     std::stable_sort(order.begin(), order.end(), [&](const Entry& a, const Entry& b) {
-        if (is_small(a) != is_small(b)) return is_small(b);
+        const int ca = class_of(a.rows, a.cols), cb = class_of(b.rows, b.cols);
+        if (ca != cb) return ca < cb;
         return a.rows * a.cols != b.rows * b.cols ? a.rows * a.cols > b.rows * b.cols : a.rows > b.rows;
     });
     std::vector<MuonMatrix> matrices;
@@ -1172,9 +1197,10 @@ int create(const adamw_muon_tensor_t* table, int32_t n, const adamw_muon_options
             part.first = s.first + done;
             part.count = 1;
             const int64_t one = place(part, nullptr, nullptr);
-            const bool small = small_ctas(part) > 0;
+            const int which = class_of(part.rows, part.cols);
+            const bool small = which == 2;
             if (P->rounds.empty() || P->rounds.back().n == kMaxShapes || (!small && used > 0 && used + one > kRoundBytes) ||
-                (small_ctas(P->rounds.back().shapes[0]) > 0) != small) {
+                class_of(P->rounds.back().shapes[0].rows, P->rounds.back().shapes[0].cols) != which) {
                 P->rounds.emplace_back();
                 P->sums.emplace_back();
                 used = 0;

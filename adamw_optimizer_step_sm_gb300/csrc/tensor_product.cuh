@@ -321,6 +321,10 @@ struct TileLoads {
     int32_t a_z, b_z;     // third coordinate
     int32_t k_at, k_len;  // range of k; k_len 0: the tile is zeros
     bool a_mn, b_mn;      // layouts
+    // Operands of two parts each (P::kParts): `part` > 0 is their k, a multiple of 64,
+    // and k_len three of it: A B, then a_low B, then A b_low.
+    const CUtensorMap *a_low, *b_low;
+    int32_t part;
 };
 
 struct Control {
@@ -427,7 +431,8 @@ template <class P>
 constexpr int tile_threads() { return 128 + 32 * P::kWarps; }
 
 // A policy P over a tile shape S:
-//   P::Params       kernel arguments;  P::kTail: k may end inside a step
+//   P::Params       kernel arguments;  P::kTail: k may end inside a step;
+//                   P::kParts: operands may be sums of two
 //   P::kTable       bytes of shared memory for its tables
 //   P::kRing        bytes of the ring of stages
 //   P::kWarps       epilogue warps, 4 or 8: each 32 of the CTA's 128 rows, all
@@ -509,20 +514,27 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
                 const uint32_t bar = PAIR == 2 && !tail ? in_cta(own, 0) : own;
                 barrier_expect(PAIR == 2 && tail ? in_cta(own, rank) : bar, S::kStageBytes);
                 const uint32_t a = smem_addr(ring) + s * S::kStageBytes, b = a + S::kABytes;
-                const int at = w.k_at + k;
+                int at = w.k_at + k;
+                const CUtensorMap *map_a = w.a, *map_b = w.b;
+                if (P::kParts && w.part > 0) {
+                    const int part = k / w.part;
+                    at -= part * w.part;
+                    if (part == 1) map_a = w.a_low;
+                    if (part == 2) map_b = w.b_low;
+                }
                 if (a_mn) {
 #pragma unroll
                     for (int i = 0; i < kRowsOfCta / 64; ++i)
-                        load_box<PAIR>(a + i * 8192, w.a, a_at + i * 64, at, w.a_z, bar);
+                        load_box<PAIR>(a + i * 8192, map_a, a_at + i * 64, at, w.a_z, bar);
                 } else {
-                    load_box<PAIR>(a, w.a, at, a_at, w.a_z, bar);
+                    load_box<PAIR>(a, map_a, at, a_at, w.a_z, bar);
                 }
                 if (b_mn) {
 #pragma unroll
                     for (int i = 0; i < S::kBRows / 64; ++i)
-                        load_box<PAIR>(b + i * 8192, w.b, b_at + i * 64, at, w.b_z, bar);
+                        load_box<PAIR>(b + i * 8192, map_b, b_at + i * 64, at, w.b_z, bar);
                 } else {
-                    load_box<PAIR>(b, w.b, at, b_at, w.b_z, bar);
+                    load_box<PAIR>(b, map_b, at, b_at, w.b_z, bar);
                 }
             }
         }

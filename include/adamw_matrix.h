@@ -55,11 +55,13 @@ typedef struct {
  * above 1e-3 of the norm to between 0.68 and 1.14.
  * Precision: G and b G + c G G are rounded to fp16 (2^12 times their values),
  * X is kept as a sum of two fp16 numbers, of which the products take the
- * first.  What is rounded away of a product's operand cannot reach directions
- * of small singular values, where each step multiplies errors by a; what is
- * kept of X itself could, and has 22 bits.  Results are 2e-4 to 2e-3 off the
- * iteration in exact arithmetic (2-norm), before their rounding to dst's type.
- * X loses its second fp16 where the steps left multiply errors by 16 or less.
+ * first (both, and two of b G + c G G, where the smaller side is at most 128).
+ * What is rounded away of a product's operand cannot reach directions of small
+ * singular values, where each step multiplies errors by a; what is kept of X
+ * itself could, and has 22 bits, but where the steps left multiply errors by 16 or
+ * less (then 11).  Results are 2e-4 to 2e-3 off the iteration in exact arithmetic
+ * (2-norm; a few times that at worst for sides below 5), before their rounding to
+ * dst's type.
  * Coefficients are the caller's: entries of b G + c G G above 16 overflow.
  * A zero matrix gives zeros; one with an inf or NaN gives NaN throughout.
  * src: bf16, fp16 or fp32; dst: any of the three, the same batch, rows and

@@ -60,7 +60,8 @@ def rand(*shape, dtype=F32, seed=1, scale=1.0, rank=None):
 # both kernels (the small one up to 128 x 1024), one to eight CTAs of a cluster,
 # every tile shape's edges, sides that are no multiple of 8, tall and wide
 SHAPES = [(1, 1), (1, 7), (9, 1), (2, 3), (16, 16), (17, 33), (64, 128), (128, 128), (127, 129), (128, 1024), (1000, 100), (1024, 128),
-          (129, 129), (128, 1025), (130, 2000), (255, 257), (515, 1031), (1031, 515), (300, 1), (1, 1500), (768, 768), (640, 200)]
+          (129, 129), (128, 1025), (130, 2000), (255, 257), (515, 1031), (1031, 515), (300, 1), (1, 1500), (768, 768), (640, 200),
+          (2, 1100), (4, 3000), (8, 5000), (3000, 3), (16, 4096), (2500, 64), (128, 1500), (1100, 127)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
@@ -72,6 +73,16 @@ def test_shapes_and_types(shape, dtype):
         y = M.orthogonalize(x, dtype=out)
         assert y.dtype == out and y.shape == x.shape
         assert off(y, want) < TOL
+
+
+@pytest.mark.parametrize("shape", [(12, 4, 1100), (12, 2000, 8), (6, 128, 64), (8, 3, 50), (5, 100, 1030)], ids=str)
+def test_thin_matrices(shape):
+    """Few singular values, whose errors do not average out: held to half the
+    tolerance, at many scales of them."""
+    for seed in range(4):
+        x = rand(*shape, seed=seed)
+        x *= torch.logspace(0, -2, shape[-1 if shape[-1] < shape[-2] else -2], device="cuda")[(None, slice(None)) if shape[-1] < shape[-2] else (slice(None), None)]
+        assert off(M.orthogonalize(x, dtype=F32), exact(x)) < TOL / 2
 
 
 @pytest.mark.parametrize("shape", [(7, 64, 96), (3, 2, 33, 40), (200, 16, 20), (5, 257, 130), (2, 3, 300, 299)], ids=str)
