@@ -222,6 +222,9 @@ def load() -> ctypes.CDLL:
             L.adamw_expert_outer.argtypes = [mats, mats, vp, mats, i32, vp, vp]
             L.adamw_expert_workspace.argtypes = [mats, mats]
             L.adamw_expert_workspace.restype = i64
+            L.adamw_expert_backward.argtypes = [mats, mats, mats, i32, vp, mats, mats, i32, i32, vp, vp]
+            L.adamw_expert_backward_workspace.argtypes = [mats, mats, mats]
+            L.adamw_expert_backward_workspace.restype = i64
             L.adamw_matrix_status.argtypes = [P(i32)]
             L.adamw_status_string.argtypes = [ctypes.c_int]
             L.adamw_status_string.restype = ctypes.c_char_p
@@ -236,7 +239,7 @@ def load() -> ctypes.CDLL:
                          "adamw_clip_plan_create", "adamw_clip_grads", "adamw_clip_plan_destroy",
                          "adamw_orthogonalize", "adamw_muon_plan_create", "adamw_muon_step",
                          "adamw_muon_plan_destroy", "adamw_expert_rows", "adamw_expert_outer",
-                         "adamw_matrix_status"):
+                         "adamw_expert_backward", "adamw_matrix_status"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
         return _lib
@@ -517,6 +520,19 @@ def adamw_expert_outer(dy: adamw_matrices_t, x: adamw_matrices_t, offsets: int, 
 
 def adamw_expert_workspace(a: adamw_matrices_t, b: adamw_matrices_t) -> int:
     return load().adamw_expert_workspace(ctypes.byref(a), ctypes.byref(b))
+
+
+def adamw_expert_backward(dy: adamw_matrices_t, x: adamw_matrices_t, w: adamw_matrices_t, transposed: int, offsets: int,
+                          dx: adamw_matrices_t | None, dw: adamw_matrices_t | None, dw_transposed: int = 0,
+                          accumulate: int = 0, workspace: int = 0, stream: int = 0) -> None:
+    ref = lambda m: None if m is None else ctypes.byref(m)
+    rc = load().adamw_expert_backward(ref(dy), ref(x), ref(w), transposed, offsets, ref(dx), ref(dw), dw_transposed,
+                                      accumulate, workspace or None, stream or None)
+    _check(rc, "adamw_expert_backward")
+
+
+def adamw_expert_backward_workspace(dy: adamw_matrices_t, x: adamw_matrices_t, w: adamw_matrices_t) -> int:
+    return load().adamw_expert_backward_workspace(ctypes.byref(dy), ctypes.byref(x), ctypes.byref(w))
 
 
 def adamw_matrix_status() -> int:

@@ -433,21 +433,36 @@ __global__ void __launch_bounds__(kStreamThreads, 2) stream_kernel(const __grid_
     }
 }
 
-// A batch of matrices of 16-bit elements, at any strides, into rows of `ld`.
-__global__ void __launch_bounds__(256) pad_kernel(const uint16_t* src, uint16_t* dst, int64_t total, int32_t rows, int32_t cols,
-                                                  int64_t row_stride, int64_t batch_stride, int32_t ld) {
+// Batches of matrices of 16-bit elements, at any strides, into rows of `ld`: what
+// TMA reads in their place. Up to three in a launch (each costs the host 4 us).
+struct PadJob {
+    const uint16_t* src;
+    uint16_t* dst;
+    int64_t total;   // vectors of eight elements
+    int64_t row_stride, batch_stride;
+    int32_t rows, cols, ld;
+};
+struct PadJobs {
+    PadJob job[3];
+    int32_t n;
+};
+
+__global__ void __launch_bounds__(256) pad_kernel(const __grid_constant__ PadJobs jobs) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int32_t per = ld / 8;
-    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
-        const int64_t line = i / per;
-        const int32_t col = int32_t(i - line * per) * 8, row = int32_t(line % rows);
-        const uint16_t* s = src + line / rows * batch_stride + row * row_stride + col;
-        uint16_t v[8];
+    for (int k = 0; k < jobs.n; ++k) {
+        const PadJob& j = jobs.job[k];
+        const int32_t per = j.ld / 8;
+        for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < j.total; i += int64_t(gridDim.x) * 256) {
+            const int64_t line = i / per;
+            const int32_t col = int32_t(i - line * per) * 8, row = int32_t(line % j.rows);
+            const uint16_t* s = j.src + line / j.rows * j.batch_stride + row * j.row_stride + col;
+            uint16_t v[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = col + k < cols ? s[k] : 0;
-        uint4 w;
-        memcpy(&w, v, 16);
-        reinterpret_cast<uint4*>(dst)[i] = w;
+            for (int e = 0; e < 8; ++e) v[e] = col + e < j.cols ? s[e] : 0;
+            uint4 w;
+            memcpy(&w, v, 16);
+            reinterpret_cast<uint4*>(j.dst)[i] = w;
+        }
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -483,27 +498,37 @@ int64_t copy_bytes(const adamw_matrices_t& m) {
     return (m.batch * m.rows * padded(m.cols) * 2 + 255) / 256 * 256;
 }
 
-// The operand where TMA can read it: itself, or a copy at *workspace, which is
-// moved on.
-bool readable(adamw_matrices_t* m, char** workspace, cudaStream_t st) {
-    if (m->batch * m->rows * m->cols == 0) return true;
-    if (direct(*m)) {
-        if (m->rows <= 1) m->row_stride = padded(m->cols);
-        if (m->batch <= 1) m->batch_stride = m->row_stride * (m->rows > 0 ? m->rows : 1);
-        return true;
+// The operands where TMA can read them: themselves, or copies in the workspace.
+bool readable(adamw_matrices_t* const (&operands)[3], void* workspace, cudaStream_t st) {
+    PadJobs jobs;
+    memset(&jobs, 0, sizeof jobs);
+    char* at = static_cast<char*>(workspace);
+    int64_t most = 0;
+    for (adamw_matrices_t* m : operands) {
+        if (!m || m->batch * m->rows * m->cols == 0) continue;
+        if (direct(*m)) {
+            if (m->rows <= 1) m->row_stride = padded(m->cols);
+            if (m->batch <= 1) m->batch_stride = m->row_stride * m->rows;
+            continue;
+        }
+        PadJob& j = jobs.job[jobs.n++];
+        j.src = static_cast<const uint16_t*>(m->data);
+        j.dst = reinterpret_cast<uint16_t*>(at);
+        j.ld = int32_t(padded(m->cols));
+        j.total = m->batch * m->rows * (j.ld / 8);
+        j.row_stride = m->row_stride;
+        j.batch_stride = m->batch_stride;
+        j.rows = int32_t(m->rows);
+        j.cols = int32_t(m->cols);
+        most = std::max(most, j.total);
+        at += copy_bytes(*m);
+        m->data = j.dst;
+        m->row_stride = j.ld;
+        m->batch_stride = j.ld * m->rows;
     }
-    const int64_t ld = padded(m->cols), total = m->batch * m->rows * (ld / 8);
-    const int64_t want = (total + 255) / 256;
-    const uint32_t grid = uint32_t(want < 152 * 8 ? want : 152 * 8);
-    char* at = *workspace;
-    *workspace += copy_bytes(*m);
-    if (!launched(launch(pad_kernel, grid, 256, 1, 0, st, static_cast<const uint16_t*>(m->data), reinterpret_cast<uint16_t*>(at),
-                         total, int32_t(m->rows), int32_t(m->cols), m->row_stride, m->batch_stride, int32_t(ld)), "pad launch"))
-        return false;
-    m->data = at;
-    m->row_stride = ld;
-    m->batch_stride = ld * m->rows;
-    return true;
+    if (jobs.n == 0) return true;
+    const int64_t want = (most + 255) / 256;
+    return launched(launch(pad_kernel, uint32_t(want < 152 * 8 ? want : 152 * 8), 256, 1, 0, st, jobs), "pad launch");
 }
 
 // rows: what a CTA loads of a K-major operand at a time.
@@ -578,8 +603,10 @@ int rows_call(const adamw_matrices_t& x, const adamw_matrices_t& w, bool transpo
     return run<P, S>(p, tiles, units, st) ? ADAMW_OK : ADAMW_ERR_CUDA;
 }
 
-int stream_call(const adamw_matrices_t& x, const adamw_matrices_t& w, const int64_t* offsets, const adamw_matrices_t& y, int sms,
+int stream_call(const adamw_matrices_t& x, const adamw_matrices_t& w, const int64_t* offsets, const adamw_matrices_t& y,
                 cudaStream_t st) {
+    TileUnits units;
+    if (!launched(units_of<ExpertRows<PairTile, true>>(&units), "tile units")) return ADAMW_ERR_CUDA;
     StreamParams p;
     memset(&p, 0, sizeof p);
     p.x = static_cast<const uint16_t*>(x.data);
@@ -600,7 +627,7 @@ int stream_call(const adamw_matrices_t& x, const adamw_matrices_t& w, const int6
     if (!launched(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, kStreamThreads, 0), "occupancy")) return ADAMW_ERR_CUDA;
     // every token in an expert of its own, or in none
     const int64_t most = std::min<int64_t>(x.rows, w.batch + 2) * up(y.cols, kStreamRows);
-    const int64_t grid = std::min<int64_t>(up(most, kStreamThreads / 32), int64_t(sms) * (occ > 0 ? occ : 1));
+    const int64_t grid = std::min<int64_t>(up(most, kStreamThreads / 32), int64_t(units.sms) * (occ > 0 ? occ : 1));
     return launched(launch(kernel, uint32_t(grid), kStreamThreads, 1, 0, st, p), "stream launch") ? ADAMW_OK : ADAMW_ERR_CUDA;
 }
 
@@ -638,13 +665,10 @@ int expert_status(int32_t* out) {
 }
 }  // namespace adamw
 
-extern "C" int64_t adamw_expert_workspace(const adamw_matrices_t* a, const adamw_matrices_t* b) {
-    if (check(a, true) != ADAMW_OK || check(b, true) != ADAMW_OK) return 0;
-    return copy_bytes(*a) + copy_bytes(*b);
-}
+namespace {
 
-extern "C" int adamw_expert_rows(const adamw_matrices_t* x, const adamw_matrices_t* w, int32_t transposed,
-                                 const int64_t* offsets, const adamw_matrices_t* y, void* workspace, adamw_stream_t stream) {
+int check_rows(const adamw_matrices_t* x, const adamw_matrices_t* w, int32_t transposed, const int64_t* offsets,
+               const adamw_matrices_t* y) {
     int rc;
     if ((rc = check(x, true)) != ADAMW_OK || (rc = check(w, true)) != ADAMW_OK || (rc = check(y, false)) != ADAMW_OK) return rc;
     const int64_t n = transposed ? w->cols : w->rows, k = transposed ? w->rows : w->cols;
@@ -655,41 +679,12 @@ extern "C" int adamw_expert_rows(const adamw_matrices_t* x, const adamw_matrices
     if (y->rows == 0 || y->cols == 0) return ADAMW_OK;
     if (!offsets) return ADAMW_ERR_INVALID_ARG;
     if (!aligned(offsets, 8)) return ADAMW_ERR_MISALIGNED;
-    const bool few = !transposed && x->rows <= kStreamTokens && n < (int64_t(1) << 24);
-    const int64_t bytes = few ? 0 : copy_bytes(*x) + copy_bytes(*w);
-    if (bytes > 0 && !workspace) return ADAMW_ERR_INVALID_ARG;
-    if (bytes > 0 && !aligned(workspace, 256)) return ADAMW_ERR_MISALIGNED;
-    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    // the grid covers the most tiles that the groups can have: one partial in each
-    const int64_t groups = w->batch + 2;
-    auto most = [&](int rows, int cols) { return (x->rows / rows + groups) * up(n, cols); };
-    if (most(SmallTile::kRows, SmallTile::kCols) > kMaxCount) return ADAMW_ERR_TOO_LARGE;
-    TileUnits units;
-    if (!launched(units_of<ExpertRows<PairTile, true>>(&units), "tile units")) return ADAMW_ERR_CUDA;
-    if (few) return stream_call(*x, *w, offsets, *y, units.sms, st);
-    adamw_matrices_t a = *x, b = *w;
-    char* at = static_cast<char*>(workspace);
-    if (!readable(&a, &at, st) || !readable(&b, &at, st)) return ADAMW_ERR_CUDA;
-    // what groups of one size would have
-    const int64_t each = up(x->rows, w->batch), used = std::min(w->batch, x->rows);
-    auto likely = [&](int rows, int cols) { return used * up(each, rows) * up(n, cols); };
-    const TileChoice choice = {{likely(PairTile::kRows, PairTile::kCols), likely(WideTile::kRows, WideTile::kCols),
-                                likely(SmallTile::kRows, SmallTile::kCols)}};
-    auto call = [&](auto shape, int u) {
-        using S = decltype(shape);
-        const int64_t tiles = most(S::kRows, S::kCols);
-        return stages(*y) ? rows_call<S, true>(a, b, transposed != 0, offsets, *y, tiles, u, st)
-                          : rows_call<S, false>(a, b, transposed != 0, offsets, *y, tiles, u, st);
-    };
-    switch (choose_shape(choice, up(k, kStepK), units.pairs, units.sms)) {
-        case kPairShape: return call(PairTile(), units.pairs);
-        case kWideShape: return call(WideTile(), units.sms);
-        default: return call(SmallTile(), units.sms);
-    }
+    if ((x->rows / SmallTile::kRows + w->batch + 2) * up(n, SmallTile::kCols) > kMaxCount) return ADAMW_ERR_TOO_LARGE;
+    return ADAMW_OK;
 }
 
-extern "C" int adamw_expert_outer(const adamw_matrices_t* dy, const adamw_matrices_t* x, const int64_t* offsets,
-                                  const adamw_matrices_t* dw, int32_t accumulate, void* workspace, adamw_stream_t stream) {
+int check_outer(const adamw_matrices_t* dy, const adamw_matrices_t* x, const int64_t* offsets, const adamw_matrices_t* dw,
+                int32_t accumulate) {
     int rc;
     if ((rc = check(dy, true)) != ADAMW_OK || (rc = check(x, true)) != ADAMW_OK || (rc = check(dw, false)) != ADAMW_OK) return rc;
     if (dy->batch != 1 || x->batch != 1 || dy->dtype != x->dtype || dy->rows != x->rows || dw->rows != dy->cols ||
@@ -701,32 +696,119 @@ extern "C" int adamw_expert_outer(const adamw_matrices_t* dy, const adamw_matric
     if (dw->rows == 0 || dw->cols == 0) return ADAMW_OK;
     if (!offsets) return ADAMW_ERR_INVALID_ARG;
     if (!aligned(offsets, 8)) return ADAMW_ERR_MISALIGNED;
-    const int64_t bytes = copy_bytes(*dy) + copy_bytes(*x);
+    if (dw->batch * up(dw->rows, SmallTile::kRows) * up(dw->cols, SmallTile::kCols) > kMaxCount) return ADAMW_ERR_TOO_LARGE;
+    return ADAMW_OK;
+}
+
+int check_workspace(int64_t bytes, const void* workspace) {
     if (bytes > 0 && !workspace) return ADAMW_ERR_INVALID_ARG;
-    if (bytes > 0 && !aligned(workspace, 256)) return ADAMW_ERR_MISALIGNED;
-    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    auto tiles = [&](int rows, int cols) { return dw->batch * up(dw->rows, rows) * up(dw->cols, cols); };
-    if (tiles(SmallTile::kRows, SmallTile::kCols) > kMaxCount) return ADAMW_ERR_TOO_LARGE;
+    return bytes > 0 && !aligned(workspace, 256) ? ADAMW_ERR_MISALIGNED : ADAMW_OK;
+}
+
+// Checked and readable, with something to do.
+int launch_rows(const adamw_matrices_t& x, const adamw_matrices_t& w, bool transposed, const int64_t* offsets,
+                const adamw_matrices_t& y, cudaStream_t st) {
+    TileUnits units;
+    if (!launched(units_of<ExpertRows<PairTile, true>>(&units), "tile units")) return ADAMW_ERR_CUDA;
+    const int64_t n = y.cols;
+    // the grid covers the most tiles that the groups can have: one partial in each
+    const int64_t groups = w.batch + 2;
+    auto most = [&](int rows, int cols) { return (x.rows / rows + groups) * up(n, cols); };
+    // what groups of one size would have
+    const int64_t each = up(x.rows, w.batch), used = std::min(w.batch, x.rows);
+    auto likely = [&](int rows, int cols) { return used * up(each, rows) * up(n, cols); };
+    const TileChoice choice = {{likely(PairTile::kRows, PairTile::kCols), likely(WideTile::kRows, WideTile::kCols),
+                                likely(SmallTile::kRows, SmallTile::kCols)}};
+    auto call = [&](auto shape, int u) {
+        using S = decltype(shape);
+        const int64_t tiles = most(S::kRows, S::kCols);
+        return stages(y) ? rows_call<S, true>(x, w, transposed, offsets, y, tiles, u, st)
+                         : rows_call<S, false>(x, w, transposed, offsets, y, tiles, u, st);
+    };
+    switch (choose_shape(choice, up(x.cols, kStepK), units.pairs, units.sms)) {
+        case kPairShape: return call(PairTile(), units.pairs);
+        case kWideShape: return call(WideTile(), units.sms);
+        default: return call(SmallTile(), units.sms);
+    }
+}
+
+int launch_outer(const adamw_matrices_t& dy, const adamw_matrices_t& x, const int64_t* offsets, const adamw_matrices_t& dw,
+                 bool accumulate, cudaStream_t st) {
     TileUnits units;
     if (!launched(units_of<ExpertOuter<PairTile, false, 1>>(&units), "tile units")) return ADAMW_ERR_CUDA;
-    adamw_matrices_t a = *dy, b = *x;
-    char* at = static_cast<char*>(workspace);
-    if (!readable(&a, &at, st) || !readable(&b, &at, st)) return ADAMW_ERR_CUDA;
+    auto tiles = [&](int rows, int cols) { return dw.batch * up(dw.rows, rows) * up(dw.cols, cols); };
     const TileChoice choice = {{tiles(PairTile::kRows, PairTile::kCols), tiles(WideTile::kRows, WideTile::kCols),
                                 tiles(SmallTile::kRows, SmallTile::kCols)}};
-    const int shape = choose_shape(choice, up(up(dy->rows, dw->batch), kStepK), units.pairs, units.sms);
+    const int shape = choose_shape(choice, up(up(dy.rows, dw.batch), kStepK), units.pairs, units.sms);
     // Sums over few tokens are bound by the results: two buffers a warp, for a stage
     // of the ring (32 tokens in each of 16 experts, 8192 x 2048: 83 against 106 us;
     // 200 115 / 124; 640 217 / 198).
-    const bool brief = dy->rows < dw->batch * 256;
+    const bool brief = dy.rows < dw.batch * 256;
     auto call = [&](auto tile, int u) {
         using S = decltype(tile);
         const int64_t n = choice.tiles[shape];
-        return accumulate     ? outer_call<S, true, 0>(a, b, offsets, *dw, n, u, st)
-               : !stages(*dw) ? outer_call<S, false, 0>(a, b, offsets, *dw, n, u, st)
-               : brief        ? outer_call<S, false, 2>(a, b, offsets, *dw, n, u, st)
-                              : outer_call<S, false, 1>(a, b, offsets, *dw, n, u, st);
+        return accumulate    ? outer_call<S, true, 0>(dy, x, offsets, dw, n, u, st)
+               : !stages(dw) ? outer_call<S, false, 0>(dy, x, offsets, dw, n, u, st)
+               : brief       ? outer_call<S, false, 2>(dy, x, offsets, dw, n, u, st)
+                             : outer_call<S, false, 1>(dy, x, offsets, dw, n, u, st);
     };
     return shape == kPairShape ? call(PairTile(), units.pairs)
            : shape == kWideShape ? call(WideTile(), units.sms) : call(SmallTile(), units.sms);
+}
+
+}  // namespace
+
+extern "C" int64_t adamw_expert_workspace(const adamw_matrices_t* a, const adamw_matrices_t* b) {
+    if (check(a, true) != ADAMW_OK || check(b, true) != ADAMW_OK) return 0;
+    return copy_bytes(*a) + copy_bytes(*b);
+}
+
+extern "C" int adamw_expert_rows(const adamw_matrices_t* x, const adamw_matrices_t* w, int32_t transposed,
+                                 const int64_t* offsets, const adamw_matrices_t* y, void* workspace, adamw_stream_t stream) {
+    int rc = check_rows(x, w, transposed, offsets, y);
+    if (rc != ADAMW_OK || y->rows == 0 || y->cols == 0) return rc;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (!transposed && x->rows <= kStreamTokens && y->cols < (int64_t(1) << 24)) return stream_call(*x, *w, offsets, *y, st);
+    if ((rc = check_workspace(copy_bytes(*x) + copy_bytes(*w), workspace)) != ADAMW_OK) return rc;
+    adamw_matrices_t a = *x, b = *w;
+    if (!readable({&a, &b, nullptr}, workspace, st)) return ADAMW_ERR_CUDA;
+    return launch_rows(a, b, transposed != 0, offsets, *y, st);
+}
+
+extern "C" int adamw_expert_outer(const adamw_matrices_t* dy, const adamw_matrices_t* x, const int64_t* offsets,
+                                  const adamw_matrices_t* dw, int32_t accumulate, void* workspace, adamw_stream_t stream) {
+    int rc = check_outer(dy, x, offsets, dw, accumulate);
+    if (rc != ADAMW_OK || dw->rows == 0 || dw->cols == 0) return rc;
+    if ((rc = check_workspace(copy_bytes(*dy) + copy_bytes(*x), workspace)) != ADAMW_OK) return rc;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    adamw_matrices_t a = *dy, b = *x;
+    if (!readable({&a, &b, nullptr}, workspace, st)) return ADAMW_ERR_CUDA;
+    return launch_outer(a, b, offsets, *dw, accumulate != 0, st);
+}
+
+extern "C" int64_t adamw_expert_backward_workspace(const adamw_matrices_t* dy, const adamw_matrices_t* x, const adamw_matrices_t* w) {
+    if (check(dy, true) != ADAMW_OK || check(x, true) != ADAMW_OK || check(w, true) != ADAMW_OK) return 0;
+    return copy_bytes(*dy) + copy_bytes(*x) + copy_bytes(*w);
+}
+
+extern "C" int adamw_expert_backward(const adamw_matrices_t* dy, const adamw_matrices_t* x, const adamw_matrices_t* w,
+                                     int32_t transposed, const int64_t* offsets, const adamw_matrices_t* dx,
+                                     const adamw_matrices_t* dw, int32_t dw_transposed, int32_t accumulate, void* workspace,
+                                     adamw_stream_t stream) {
+    int rc;
+    if (!dy || !x || !w || (dw_transposed != 0 && dw_transposed != 1) || (transposed != 0 && transposed != 1)) return ADAMW_ERR_INVALID_ARG;
+    const adamw_matrices_t *left = dw_transposed ? x : dy, *right = dw_transposed ? dy : x;
+    if (dx && (rc = check_rows(dy, w, !transposed, offsets, dx)) != ADAMW_OK) return rc;
+    if (dw && (rc = check_outer(left, right, offsets, dw, accumulate)) != ADAMW_OK) return rc;
+    if (dx && dw && (dw->batch != w->batch || overlap(*dx, *dw))) return ADAMW_ERR_INVALID_ARG;
+    const bool rows = dx && dx->rows > 0 && dx->cols > 0, outer = dw && dw->rows > 0 && dw->cols > 0;
+    if (!rows && !outer) return ADAMW_OK;
+    const int64_t bytes = copy_bytes(*dy) + (outer ? copy_bytes(*x) : 0) + (rows ? copy_bytes(*w) : 0);
+    if ((rc = check_workspace(bytes, workspace)) != ADAMW_OK) return rc;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    adamw_matrices_t a = *dy, b = *x, c = *w;
+    if (!readable({&a, outer ? &b : nullptr, rows ? &c : nullptr}, workspace, st)) return ADAMW_ERR_CUDA;
+    if (rows && (rc = launch_rows(a, c, transposed == 0, offsets, *dx, st)) != ADAMW_OK) return rc;
+    if (outer) return dw_transposed ? launch_outer(b, a, offsets, *dw, accumulate != 0, st) : launch_outer(a, b, offsets, *dw, accumulate != 0, st);
+    return ADAMW_OK;
 }

@@ -189,15 +189,15 @@ def _expert_linear(x, weight, offsets, out):
 class _ExpertLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, offsets):
+        y = _expert_linear(x, weight, offsets, None)
         ctx.save_for_backward(x, weight, offsets)
-        return _expert_linear(x, weight, offsets, None)
+        return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        x, weight, offsets = ctx.saved_tensors
-        dx, dw = expert_linear_backward(dy, x, weight, offsets, need=ctx.needs_input_grad[:2])
-        return dx, dw, None
+        x, weight, offsets = ctx.saved_tensors   # checked by the forward pass
+        return (*_gradients(dy, x, weight, offsets, ctx.needs_input_grad, None, False), None)
 
 
 def expert_linear(x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor, *,
@@ -225,42 +225,53 @@ def expert_linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tens
     gradient goes, [experts, out, in] in bf16, fp16 or fp32 (for example an
     optimizer's own gradient buffer); with ``accumulate`` it is added there, in
     fp32 before the rounding."""
-    dy, x = _tokens_of("gradients", dy), _tokens_of("tokens", x)
-    w, transposed, _keep = _weight_of(weight, x)
+    x = _tokens_of("tokens", x)
+    w, _, _ = _weight_of(weight, x)
     if dy.dtype != x.dtype or dy.device != x.device:
         raise TypeError("want gradients of the tokens' type and device")
     if dy.shape != (x.shape[0], weight.shape[1]) or weight.shape[2] != x.shape[1]:
         raise ValueError(f"gradients {tuple(dy.shape)}, tokens {tuple(x.shape)} and weights {tuple(weight.shape)} do not match")
     offsets = _offsets_of(offsets, weight.shape[0], x.device)
-    dx = dw = None
-    if need[0]:
-        dx = _rows_product(dy, w, 1 - transposed, offsets, _empty(x.shape, dtype=x.dtype, device=x.device))
     if accumulate and d_weight is None:
         raise ValueError("accumulate needs d_weight")
-    if need[1]:
-        given = d_weight is not None
-        if given:
-            if d_weight.requires_grad and torch.is_grad_enabled():
-                raise RuntimeError("d_weight requires a gradient")
-            if d_weight.shape != weight.shape or d_weight.device != x.device or d_weight.dtype not in _CODES:
-                raise ValueError("d_weight must have the weights' shape and device, in bfloat16, float16 or float32")
-            dw = d_weight
-        else:
-            # laid out as the weights are
-            e, n, k = weight.shape
-            dw = _empty((e, k, n), dtype=x.dtype, device=x.device).mT if transposed else _empty((e, n, k), dtype=x.dtype, device=x.device)
-        if dw.stride(2) == 1 or dw.shape[2] <= 1:
-            a, b, d = dy, x, dw
-        elif dw.stride(1) == 1:
-            a, b, d = x, dy, dw.mT   # the transposed sum
-        else:
+    if d_weight is not None:
+        if d_weight.requires_grad and torch.is_grad_enabled():
+            raise RuntimeError("d_weight requires a gradient")
+        if d_weight.shape != weight.shape or d_weight.device != x.device or d_weight.dtype not in _CODES:
+            raise ValueError("d_weight must have the weights' shape and device, in bfloat16, float16 or float32")
+        s = d_weight.stride()
+        if not (s[2] == 1 or d_weight.shape[2] <= 1 or s[1] == 1):
             raise ValueError("d_weight needs consecutive elements along one of its last two dimensions")
-        lib = A.load()
-        ma, mb = _byref(_matrices(a)), _byref(_matrices(b))
-        nbytes = lib.adamw_expert_workspace(ma, mb)
-        work = _empty(nbytes, dtype=_BYTES, device=x.device) if nbytes else None
-        _call(lib.adamw_expert_outer, "adamw_expert_outer", x.device, ma, mb, offsets.data_ptr(),
-              _byref(_matrices(d)), int(accumulate), work.data_ptr() if nbytes else None)
-        if given:
-            _written(dw)
+    return _gradients(dy, x, weight, offsets, need, d_weight, accumulate)
+
+
+def _gradients(dy, x, weight, offsets, need, dw, accumulate):
+    """Of arguments that fit each other."""
+    dy, x = _tokens_of("gradients", dy), _tokens_of("tokens", x)
+    w, transposed, _keep = _weight_of(weight, x)
+    if not offsets.is_contiguous():
+        offsets = offsets.contiguous()
+    dev, dtype = x.device, x.dtype
+    dx = _empty(x.shape, dtype=dtype, device=dev) if need[0] else None
+    given = dw is not None and need[1]
+    turned, d = 0, None
+    if need[1]:
+        e, n, k = weight.shape
+        if dw is None:   # laid out as the weights are
+            dw = _empty((e, k, n), dtype=dtype, device=dev).mT if transposed else _empty((e, n, k), dtype=dtype, device=dev)
+        s = dw.stride()
+        turned = 0 if s[2] == 1 or k <= 1 else 1
+        d = _matrices_t(dw.data_ptr(), e, k, n, s[0], s[2], _CODES[dw.dtype]) if turned else \
+            _matrices_t(dw.data_ptr(), e, n, k, s[0], s[1], _CODES[dw.dtype])
+    else:
+        dw = None
+    lib = A.load()
+    a, b, c = _byref(_matrices(dy)), _byref(_matrices(x)), _byref(w)
+    nbytes = lib.adamw_expert_backward_workspace(a, b, c)
+    work = _empty(nbytes, dtype=_BYTES, device=dev) if nbytes else None
+    _call(lib.adamw_expert_backward, "adamw_expert_backward", dev, a, b, c, transposed, offsets.data_ptr(),
+          _byref(_matrices(dx)) if need[0] else None, _byref(d) if need[1] else None, turned, int(accumulate),
+          work.data_ptr() if nbytes else None)
+    if given:
+        _written(dw)
     return dx, dw

@@ -52,7 +52,7 @@ typedef struct {
  * (G = X^T X and the products from the right where rows > cols, which is the
  * same polynomial of smaller matrices).  With the coefficients of the Muon
  * optimizer (3.4445, -4.775, 2.0315) five steps bring every singular value
- * above 1e-3 of the norm to between 0.68 and 1.14.
+ * above 2e-3 of the norm to between 0.68 and 1.21.
  * Precision: G and b G + c G G are rounded to fp16 (2^12 times their values),
  * X is kept as a sum of two fp16 numbers, of which the products take the
  * first (both, and two of b G + c G G, where the smaller side is at most 128).
@@ -171,6 +171,18 @@ int adamw_expert_outer(const adamw_matrices_t* dy, const adamw_matrices_t* x,
                        const int64_t* offsets, const adamw_matrices_t* dw, int32_t accumulate,
                        void* workspace, adamw_stream_t stream);
 int64_t adamw_expert_workspace(const adamw_matrices_t* a, const adamw_matrices_t* b);
+
+/* Both gradients of y[r] = w[e] x[r] (w[e]^T x[r] where transposed) in one call:
+ *   dx: as adamw_expert_rows makes it of dy with the other `transposed`, or NULL
+ *   dw: as adamw_expert_outer makes it of dy and x (dw_transposed: of x and dy,
+ *       experts x (x's cols) x (dy's cols)), or NULL
+ * Each is what its own call gives. workspace: adamw_expert_backward_workspace
+ * bytes. dx and dw must not overlap. Errors: as above. */
+int adamw_expert_backward(const adamw_matrices_t* dy, const adamw_matrices_t* x, const adamw_matrices_t* w,
+                          int32_t transposed, const int64_t* offsets, const adamw_matrices_t* dx,
+                          const adamw_matrices_t* dw, int32_t dw_transposed, int32_t accumulate, void* workspace,
+                          adamw_stream_t stream);
+int64_t adamw_expert_backward_workspace(const adamw_matrices_t* dy, const adamw_matrices_t* x, const adamw_matrices_t* w);
 
 /* Reads and clears the current device's status word of these operators: 1 when
  * a kernel's bounded wait ran out (its results are then undefined).

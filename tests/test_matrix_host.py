@@ -182,6 +182,25 @@ def test_expert_outer_is_checked(dy, x, dw, status):
     assert _status(A.adamw_expert_outer, *args) == status
 
 
+def test_expert_backward_is_checked():
+    f, big = A.adamw_expert_backward, 6 << 40
+    dy, x, w = _y(data=4 << 40), _x(), _w()
+    dx, dw = _x(data=W), _w(data=big)
+    o = 5 << 40
+    for bad, status in ((dict(dy=_y(data=4 << 40, rows=41)), BAD), (dict(x=_x(cols=95)), BAD), (dict(w=_w(rows=63)), BAD), (dict(transposed=2), BAD),
+                        (dict(dx=_x(data=W, cols=95)), BAD), (dict(dx=_x(data=4 << 40)), BAD), (dict(dw=_w(data=big, batch=3)), BAD),
+                        (dict(dw=_w(data=W)), BAD), (dict(dw_transposed=1), BAD), (dict(dw_transposed=2), BAD), (dict(accumulate=2), BAD),
+                        (dict(offsets=0), BAD), (dict(offsets=o + 4), MIS), (dict(dw=_w(data=big, batch=1025)), BIG)):
+        args = dict(dy=dy, x=x, w=w, transposed=0, offsets=o, dx=dx, dw=dw, dw_transposed=0, accumulate=0)
+        args.update(bad)
+        assert _status(f, *args.values()) == status, bad
+    odd = _y(data=4 << 40, row_stride=65)
+    assert _status(f, odd, x, w, 0, o, dx, dw) == BAD              # a copy needs the workspace
+    assert _status(f, odd, x, w, 0, o, dx, dw, 0, 0, W + 128) == MIS
+    assert A.adamw_expert_backward_workspace(odd, x, w) == 40 * 64 * 2
+    f(dy, x, w, 0, o, None, None)                                  # nothing wanted
+
+
 def test_expert_workspace():
     ws = A.adamw_expert_workspace
     assert ws(_x(), _w()) == 0
