@@ -800,7 +800,8 @@ extern "C" int adamw_expert_backward(const adamw_matrices_t* dy, const adamw_mat
     const adamw_matrices_t *left = dw_transposed ? x : dy, *right = dw_transposed ? dy : x;
     if (dx && (rc = check_rows(dy, w, !transposed, offsets, dx)) != ADAMW_OK) return rc;
     if (dw && (rc = check_outer(left, right, offsets, dw, accumulate)) != ADAMW_OK) return rc;
-    if (dx && dw && (dw->batch != w->batch || overlap(*dx, *dw))) return ADAMW_ERR_INVALID_ARG;
+    // dx is written before x is read, and w's rows may still be read when dw is written
+    if (dx && dw && (dw->batch != w->batch || overlap(*dx, *dw) || overlap(*dx, *x) || overlap(*dw, *w))) return ADAMW_ERR_INVALID_ARG;
     const bool rows = dx && dx->rows > 0 && dx->cols > 0, outer = dw && dw->rows > 0 && dw->cols > 0;
     if (!rows && !outer) return ADAMW_OK;
     const int64_t bytes = copy_bytes(*dy) + (outer ? copy_bytes(*x) : 0) + (rows ? copy_bytes(*w) : 0);

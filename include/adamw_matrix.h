@@ -177,7 +177,7 @@ int64_t adamw_expert_workspace(const adamw_matrices_t* a, const adamw_matrices_t
  *   dw: as adamw_expert_outer makes it of dy and x (dw_transposed: of x and dy,
  *       experts x (x's cols) x (dy's cols)), or NULL
  * Each is what its own call gives. workspace: adamw_expert_backward_workspace
- * bytes. dx and dw must not overlap. Errors: as above. */
+ * bytes. dx overlaps none of the others, nor does dw. Errors: as above. */
 int adamw_expert_backward(const adamw_matrices_t* dy, const adamw_matrices_t* x, const adamw_matrices_t* w,
                           int32_t transposed, const int64_t* offsets, const adamw_matrices_t* dx,
                           const adamw_matrices_t* dw, int32_t dw_transposed, int32_t accumulate, void* workspace,

@@ -189,7 +189,7 @@ def test_expert_backward_is_checked():
     o = 5 << 40
     for bad, status in ((dict(dy=_y(data=4 << 40, rows=41)), BAD), (dict(x=_x(cols=95)), BAD), (dict(w=_w(rows=63)), BAD), (dict(transposed=2), BAD),
                         (dict(dx=_x(data=W, cols=95)), BAD), (dict(dx=_x(data=4 << 40)), BAD), (dict(dw=_w(data=big, batch=3)), BAD),
-                        (dict(dw=_w(data=W)), BAD), (dict(dw_transposed=1), BAD), (dict(dw_transposed=2), BAD), (dict(accumulate=2), BAD),
+                        (dict(dw=_w(data=W)), BAD), (dict(dx=_x(data=P)), BAD), (dict(dw=_w(data=Q)), BAD), (dict(dw_transposed=1), BAD), (dict(dw_transposed=2), BAD), (dict(accumulate=2), BAD),
                         (dict(offsets=0), BAD), (dict(offsets=o + 4), MIS), (dict(dw=_w(data=big, batch=1025)), BIG)):
         args = dict(dy=dy, x=x, w=w, transposed=0, offsets=o, dx=dx, dw=dw, dw_transposed=0, accumulate=0)
         args.update(bad)
