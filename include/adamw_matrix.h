@@ -60,7 +60,7 @@ typedef struct {
  * singular values, where each step multiplies errors by a; what is kept of X
  * itself could, and has 22 bits, but where the steps left multiply errors by 16 or
  * less (then 11).  Results are 2e-4 to 2e-3 off the iteration in exact arithmetic
- * (2-norm; a few times that at worst for sides below 5), before their rounding to
+ * (2-norm; for sides of 2 to 4, whose errors do not average out, up to 1e-2), before their rounding to
  * dst's type.
  * Coefficients are the caller's: entries of b G + c G G above 16 overflow.
  * A zero matrix gives zeros; one with an inf or NaN gives NaN throughout.
