@@ -23,8 +23,9 @@
 // subnormals: 2^-24 beside entries of 2^12 X.
 // Thin matrices (a side of at most 128) have few singular values, whose errors do
 // not average out: their Q is kept as two fp16 as well, and Q X is three products
-// (sides of 1 to 32: up to 6.7e-3 off without and 3.5e-3 with, 2e-3 and 1e-3 on
-// average; the worst of thousands of matrices of 2 x 3 and the like is 1e-2).
+// (a small sample of sides of 1 to 4: up to 6.7e-3 off without, 3.5e-3 with).  G is
+// still one fp16; the worst of 16800 random matrices of a side was 8.9e-3 for
+// 2, 7.4e-3 for 3, 6.5e-3 for 4, 5.4e-3 for 5, and of 7920 of a side of 32, 2.1e-3.
 #include <algorithm>
 #include <exception>
 #include <new>

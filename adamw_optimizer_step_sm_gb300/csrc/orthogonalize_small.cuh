@@ -7,10 +7,10 @@
 // X stays in registers, in fp32; shared memory holds what the tensor cores
 // read, in fp16 at 2^12 times its value as in the large form: X's part, G and Q.
 // Q X takes X and Q as two fp16 each (three products: 22 against 17 us for 64 x 128):
-// in small matrices the roundings of few numbers do not average out, and with one
-// fp16 each the result was up to 3.5e-3 off. The sum G = X X^T over the cluster goes
-// through distributed shared memory: each CTA adds up its share of G's rows over
-// all parts, in their order, and hands the sums to all.
+// in small matrices the roundings of few numbers do not average out (figures in
+// orthogonalize.cu). The sum G = X X^T over the cluster goes through distributed
+// shared memory: each CTA adds up its share of G's rows over all parts, in their
+// order, and hands the sums to all.
 //
 // Bound by latency: a step is three products one after the other, each half a
 // microsecond of tensor cores and as much between their operands and results in

@@ -60,8 +60,10 @@ typedef struct {
  * singular values, where each step multiplies errors by a; what is kept of X
  * itself could, and has 22 bits, but where the steps left multiply errors by 16 or
  * less (then 11).  Results are 2e-4 to 2e-3 off the iteration in exact arithmetic
- * (2-norm; for sides of 2 to 4, whose errors do not average out, up to 1e-2), before their rounding to
- * dst's type.
+ * (2-norm) before their rounding to dst's type.  The errors of few singular
+ * values do not average out: the worst of 16800 random matrices of each smaller
+ * side, in fp32 after five steps, was 8.9e-3 for a side of 2, 7.4e-3 for 3, 6.5e-3
+ * for 4, 5.4e-3 for 5, 4.2e-3 for 6, 3.1e-3 for 1; of 14400 for 8, 3.3e-3.
  * Coefficients are the caller's: entries of b G + c G G above 16 overflow.
  * A zero matrix gives zeros; one with an inf or NaN gives NaN throughout.
  * src: bf16, fp16 or fp32; dst: any of the three, the same batch, rows and
