@@ -23,9 +23,12 @@
 // subnormals: 2^-24 beside entries of 2^12 X.
 // Thin matrices (a side of at most 128) have few singular values, whose errors do
 // not average out: their Q is kept as two fp16 as well, and Q X is three products
-// (a small sample of sides of 1 to 4: up to 6.7e-3 off without, 3.5e-3 with).  G is
-// still one fp16; the worst of 16800 random matrices of a side was 8.9e-3 for
-// 2, 7.4e-3 for 3, 6.5e-3 for 4, 5.4e-3 for 5, and of 7920 of a side of 32, 2.1e-3.
+// (a small sample of sides of 1 to 4: up to 6.7e-3 off without, 3.5e-3 with).  Up to a
+// side of 32 (kFineSide) G is formed from both fp16 of X and kept as two as well;
+// in one it left up to 8.9e-3 (the worst of 16800 random matrices of a side of 2;
+// 5, 5.4e-3; 8, 3.3e-3; 32, 2.1e-3), in two 8.5e-5.  It costs 8 x 128 19 -> 26 us, 32 x
+// 1000 32 -> 53, and a long Gram product thrice its steps (16 x 8192 243 -> 615), so
+// sides above, whose worst is below bf16's rounding, keep one.
 #include <algorithm>
 #include <exception>
 #include <new>
@@ -46,10 +49,12 @@ struct Shape {
     int32_t rows, cols, ld;         // ld: cols up to a multiple of 16
     int32_t side, small_ld;         // of G
     bool thin;                      // Q is kept as two fp16
+    bool fine;                      // and G, from both of X's
     int32_t count, first;           // matrices, and the first one's number in the list
 };
 
 constexpr int kMaxShapes = 8;   // in a launch
+constexpr int kFineSide = 32;   // up to which G is two fp16, from both of X's
 
 // ------------------------------------------------------- norms and copies --
 
@@ -428,11 +433,12 @@ struct ProductParams {
     const int32_t* nonfinite;
 };
 
-// LOW_IN, LOW_OUT: X has its second fp16, the next X gets one.
+// LOW_IN, LOW_OUT: X has its second fp16, the next X gets one.  Of G and Q, LOW_IN:
+// there are fine shapes (a flag at run time alone slowed all others by 2 to 5 %).
 template <int KIND, class S, bool LOW_IN = false, bool LOW_OUT = false>
 struct Product {
     using Params = ProductParams;
-    static constexpr bool kTail = false, kParts = KIND >= kApply;
+    static constexpr bool kTail = false, kParts = KIND >= kApply || LOW_IN;
     static constexpr size_t kTable = 0;
     // Eight warps, each with two staged blocks: X, G and their like come and go
     // by TMA, in rows of 128 bytes.  Sectors by threads made four times the requests,
@@ -452,7 +458,7 @@ struct Product {
         int32_t m, n, cols;
         int32_t matrix, row, col;   // of the CTA's part
         int32_t vector;             // of the result's rows
-        bool mirrored, skip, thin;
+        bool mirrored, skip, thin, fine;
         const ProductShape* maps;
         char *dst, *param;          // the result, or the master and the parameter
         int64_t dst_ld;
@@ -500,7 +506,7 @@ struct Product {
         w.a_mn = c.a_mn;
         w.b_mn = c.b_mn;
         w.part = 0;
-        if (kParts && c.s.thin) {
+        if (kParts && (KIND >= kApply ? c.s.thin : c.s.fine)) {
             w.a_low = &c.a_low;
             w.b_low = &c.b_low;
             w.part = (c.k + kStepK - 1) / kStepK * kStepK;
@@ -520,6 +526,7 @@ struct Product {
         o.mirrored = kSymmetric && m / kRatio != n;
         o.skip = false;
         o.thin = c.s.thin;
+        o.fine = LOW_IN && c.s.fine;
         o.vector = kSectorRows;
         o.a = p.a;
         o.b = p.b;
@@ -547,27 +554,30 @@ struct Product {
     __device__ static bool wanted(const Params&, const Out& o, int row, int col) {
         return !o.skip && o.row + row < o.m && o.col + col < o.n;
     }
+    // Is the result two fp16?  A thin G or Q is one tile, nothing of it is mirrored.
+    __device__ static bool split(const Out& o) { return LOW_OUT || (KIND == kPoly && o.thin) || (KIND == kGram && LOW_IN && o.fine); }
     // X or G at the warp's block from column `col`, into its buffers.
     __device__ static void begin(const Params& p, const Out& o, Staged& s, int col) {
         if (KIND == kGram || !wanted(p, o, s.row, col)) return;
         if (elected()) {
-            barrier_expect(s.bar, LOW_IN ? 8192 : 4096);
+            const bool two = LOW_IN && (KIND != kPoly || o.fine);
+            barrier_expect(s.bar, two ? 8192 : 4096);
             load_box<1>(smem_addr(s.one), &o.maps->in, o.col + col, o.row + s.row, o.matrix, s.bar);
-            if (LOW_IN) load_box<1>(smem_addr(s.two), &o.maps->low, o.col + col, o.row + s.row, o.matrix, s.bar);
+            if (two) load_box<1>(smem_addr(s.two), &o.maps->low, o.col + col, o.row + s.row, o.matrix, s.bar);
         }
         __syncwarp();
     }
     __device__ static bool finish(const Params& p, const Out& o, Staged& s, bool) {
         for (int c = s.col; c < s.end; c += kBlock64) {
             if (!wanted(p, o, s.row, c)) continue;
-            uint4 hi[KIND == kGram ? 1 : 8], low[LOW_IN ? 8 : 1];
+            uint4 hi[KIND == kGram ? 1 : 8], low[LOW_IN && KIND >= kApply ? 8 : 1];
             if constexpr (KIND != kGram) {
                 if (!s.wait.warp(s.bar, s.turn)) return false;
                 s.turn ^= 1;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     hi[j] = *unit_of(s.one, s.lane, j);
-                    if constexpr (LOW_IN) low[j] = *unit_of(s.two, s.lane, j);
+                    if constexpr (LOW_IN && KIND >= kApply) low[j] = *unit_of(s.two, s.lane, j);
                 }
                 __syncwarp();
             }
@@ -584,6 +594,12 @@ struct Product {
                         for (int e = 0; e < 8; ++e) y[e] *= kUnscale;
                     } else if constexpr (KIND == kPoly) {
                         Fp16::unpack(hi[half * 4 + j], h);
+                        if (LOW_IN && o.fine) {   // still there: it is overwritten below, unit by unit
+                            float l[8];
+                            Fp16::unpack(*unit_of(s.two, s.lane, half * 4 + j), l);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) h[e] += l[e];
+                        }
 #pragma unroll
                         for (int e = 0; e < 8; ++e) y[e] = fmaf(o.b, h[e], o.c * y[e]);
                     } else {
@@ -598,7 +614,7 @@ struct Product {
                         for (int e = 0; e < 8; ++e) y[e] = fmaf(o.a, h[e], y[e] * kUnscale);
                     }
                     if constexpr (KIND <= kApply) {
-                        if (LOW_OUT || (KIND == kPoly && o.thin)) {   // a thin Q is one tile, and nothing is mirrored
+                        if (split(o)) {
                             uint4 a, b;
                             split8(*reinterpret_cast<float(*)[8]>(y), &a, &b);
                             *unit_of(s.one, s.lane, half * 4 + j) = a;
@@ -622,7 +638,7 @@ struct Product {
                 __syncwarp();
                 if (elected()) {
                     store_box(&o.maps->result, o.col + c, o.row + s.row, o.matrix, smem_addr(s.one));
-                    if (LOW_OUT || (KIND == kPoly && o.thin)) store_box(&o.maps->low, o.col + c, o.row + s.row, o.matrix, smem_addr(s.two));
+                    if (split(o)) store_box(&o.maps->low, o.col + c, o.row + s.row, o.matrix, smem_addr(s.two));
                     if constexpr (kSymmetric) {
                         if (o.mirrored) store_box(&o.maps->turned, o.row + s.row, o.col + c, o.matrix, smem_addr(s.two));
                     }
@@ -699,6 +715,7 @@ Shape shape_of(int64_t rows, int64_t cols) {
     s.small_ld = int32_t(up(s.side, 16));
     s.small_stride = int64_t(s.side) * s.small_ld;
     s.thin = s.side <= 128;
+    s.fine = s.side <= kFineSide;
     return s;
 }
 int64_t vecs_of(const Shape& s) { return int64_t(s.rows) * (s.ld / 8); }
@@ -706,7 +723,8 @@ int64_t pieces_of(const Shape& s, int32_t piece) { return (vecs_of(s) + piece - 
 
 // The working copies of a shape.
 struct Buffers {
-    uint16_t *x[2], *lo, *gram, *poly, *poly_lo;
+    uint16_t *x[2], *lo, *gram, *poly;
+    uint16_t* poly_lo;   // Q's, and before it G's: a thin matrix's is one tile, which reads all of G first
 };
 // A shape's buffers at `at`, each at a multiple of 256 bytes; the bytes they take.
 int64_t place(const Shape& s, char* at, Buffers* b) {
@@ -761,6 +779,10 @@ bool fill(const Group& g, int kind, int which, ProductParams* p) {
                  tensor_map(&q.b, false, b.x[which], s.count, s.rows, s.cols, s.ld, s.stride, wide ? S::kBRows : kStepK);
             ok = ok && tensor_map(&q.result, false, b.gram, s.count, s.side, s.side, s.small_ld, s.small_stride, 32) &&
                  tensor_map(&q.turned, false, b.gram, s.count, s.side, s.side, s.small_ld, s.small_stride, 64, 32);
+            if (ok && s.fine)
+                ok = tensor_map(&q.a_low, false, b.lo, s.count, s.rows, s.cols, s.ld, s.stride, wide ? kRowsOfCta : kStepK) &&
+                     tensor_map(&q.b_low, false, b.lo, s.count, s.rows, s.cols, s.ld, s.stride, wide ? S::kBRows : kStepK) &&
+                     tensor_map(&q.low, false, b.poly_lo, s.count, s.side, s.side, s.small_ld, s.small_stride, 32);
         } else if (kind == kPoly) {
             q.m = q.n = q.k = s.side;
             ok = tensor_map(&q.a, false, b.gram, s.count, s.side, s.side, s.small_ld, s.small_stride, kRowsOfCta) &&
@@ -769,6 +791,9 @@ bool fill(const Group& g, int kind, int which, ProductParams* p) {
                  tensor_map(&q.result, false, b.poly, s.count, s.side, s.side, s.small_ld, s.small_stride, 32) &&
                  tensor_map(&q.turned, false, b.poly, s.count, s.side, s.side, s.small_ld, s.small_stride, 64, 32);
             if (ok && s.thin) ok = tensor_map(&q.low, false, b.poly_lo, s.count, s.side, s.side, s.small_ld, s.small_stride, 32);
+            if (ok && s.fine)
+                ok = tensor_map(&q.a_low, false, b.poly_lo, s.count, s.side, s.side, s.small_ld, s.small_stride, kRowsOfCta) &&
+                     tensor_map(&q.b_low, false, b.poly_lo, s.count, s.side, s.side, s.small_ld, s.small_stride, S::kBRows);
         } else {
             q.m = s.rows;
             q.n = s.cols;
@@ -810,7 +835,8 @@ bool allow() {
 
 template <class S>
 bool allow_all() {
-    return allow<Product<kGram, S>, S>() && allow<Product<kPoly, S>, S>() && allow<Product<kApply, S>, S>() &&
+    return allow<Product<kGram, S>, S>() && allow<Product<kGram, S, true>, S>() && allow<Product<kPoly, S>, S>() &&
+           allow<Product<kPoly, S, true>, S>() && allow<Product<kApply, S>, S>() &&
            allow<Product<kApply, S, true>, S>() && allow<Product<kApply, S, true, true>, S>() && allow<Product<kResult, S>, S>() &&
            allow<Product<kResult, S, true>, S>() && allow<Product<kUpdate, S>, S>() && allow<Product<kUpdate, S, true>, S>();
 }
@@ -839,10 +865,12 @@ bool launch_product(const ProductParams& p, int units, cudaStream_t st) {
     return launched(launch(tile_kernel<P, S>, grid, tile_threads<P>(), S::kPair, tile_smem<P>(), st, p), "product launch");
 }
 template <class S>
-bool launch_kind(int kind, bool low_in, bool low_out, const ProductParams& p, int units, cudaStream_t st) {
+bool launch_kind(int kind, bool fine, bool low_in, bool low_out, const ProductParams& p, int units, cudaStream_t st) {
     switch (kind) {
-        case kGram: return launch_product<Product<kGram, S>, S>(p, units, st);
-        case kPoly: return launch_product<Product<kPoly, S>, S>(p, units, st);
+        case kGram:
+            return fine ? launch_product<Product<kGram, S, true>, S>(p, units, st) : launch_product<Product<kGram, S>, S>(p, units, st);
+        case kPoly:
+            return fine ? launch_product<Product<kPoly, S, true>, S>(p, units, st) : launch_product<Product<kPoly, S>, S>(p, units, st);
         case kApply:
             return !low_in    ? launch_product<Product<kApply, S>, S>(p, units, st)
                    : !low_out ? launch_product<Product<kApply, S, true>, S>(p, units, st)
@@ -861,7 +889,8 @@ bool run_steps(const Group& g, const adamw_ortho_t& o, const float* coefs, int l
     auto row = [&](int k) { return coefs + 3 * (k < o.n_coefficients ? k : o.n_coefficients - 1); };
     bool low_in = true;   // X starts as two fp16
     bool thin = false;    // products of thin matrices take both
-    for (int i = 0; i < g.n; ++i) thin = thin || g.shapes[i].thin;
+    bool fine = false;
+    for (int i = 0; i < g.n; ++i) thin = thin || g.shapes[i].thin, fine = fine || g.shapes[i].fine;
     for (int k = 0; k < o.steps; ++k) {
         // by how much the steps after this one multiply an error of X in a
         // direction without singular value; up to 16, eleven bits of X are enough
@@ -896,9 +925,9 @@ bool run_steps(const Group& g, const adamw_ortho_t& o, const float* coefs, int l
             p.table = with.table;
             p.hp = with.hp;
             p.nonfinite = with.nonfinite;
-            if (!(shape == kPairShape   ? launch_kind<PairTile>(which, low_in, low_out, p, d.pairs, st)
-                  : shape == kWideShape ? launch_kind<WideTile>(which, low_in, low_out, p, d.sms, st)
-                                        : launch_kind<SmallTile>(which, low_in, low_out, p, d.sms, st)))
+            if (!(shape == kPairShape   ? launch_kind<PairTile>(which, fine, low_in, low_out, p, d.pairs, st)
+                  : shape == kWideShape ? launch_kind<WideTile>(which, fine, low_in, low_out, p, d.sms, st)
+                                        : launch_kind<SmallTile>(which, fine, low_in, low_out, p, d.sms, st)))
                 return false;
         }
         low_in = low_out;

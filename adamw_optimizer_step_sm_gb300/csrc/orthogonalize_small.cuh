@@ -23,9 +23,9 @@ namespace {
 constexpr int kSmallThreads = 256;
 constexpr int kSmallSide = 128, kSmallMost = 8;   // largest side, CTAs of a cluster
 constexpr uint32_t kPlane = 128 * 128;            // 64 columns of 128 rows of fp16
-// Two planes each for X, what its fp16 leaves, G and Q; then what Q's fp16
-// leaves, in the place of a cluster's parts of G.
-constexpr uint32_t kSmallBytes = 1024 + 10 * kPlane;
+// Two planes each for X, what its fp16 leaves, G and Q; what Q's fp16 leaves, in
+// the place of a cluster's parts of G (what theirs leaves is in Q's); what G's leaves.
+constexpr uint32_t kSmallBytes = 1024 + 12 * kPlane;
 
 template <bool MUON>
 struct SmallParams {
@@ -92,13 +92,45 @@ __device__ __forceinline__ void add_up(const unsigned char* parts, unsigned char
     }
 }
 
-template <bool MUON, int DT>
+// The same with parts and sum as two fp16 each, for small sides.
+template <int CTAS>
+__device__ __forceinline__ void add_up_fine(const unsigned char* parts, const unsigned char* parts_lo, unsigned char* gs,
+                                            unsigned char* gl, uint32_t rank) {
+#pragma unroll 1
+    for (int i = 0; i < 8 / CTAS; ++i) {
+        const int u = i * kSmallThreads + int(threadIdx.x), row = int(rank) * (128 / CTAS) + u / 16;
+        const uint32_t at = uint32_t(u % 16 / 8) * kPlane + unit_at(row, u % 8);
+        float t[8] = {};
+#pragma unroll
+        for (int o = 0; o < 2 * CTAS; ++o) {
+            uint4 v;
+            asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(in_cta(smem_addr((o % 2 ? parts_lo : parts) + at), uint32_t(o / 2))) : "memory");
+            float w[8];
+            Fp16::unpack(v, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] += w[e];
+        }
+        const uint4 g = Fp16::pack(t), l = left_of(t);
+#pragma unroll
+        for (int o = 0; o < CTAS; ++o) {
+            asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(in_cta(smem_addr(gs + at), uint32_t(o))),
+                         "r"(g.x), "r"(g.y), "r"(g.z), "r"(g.w) : "memory");
+            asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(in_cta(smem_addr(gl + at), uint32_t(o))),
+                         "r"(l.x), "r"(l.y), "r"(l.z), "r"(l.w) : "memory");
+        }
+    }
+}
+
+// FINE: some shape is (as a flag at run time alone: 64 x 128 8 % slower).
+template <bool MUON, int DT, bool FINE>
 __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_constant__ SmallParams<MUON> p) {
     extern __shared__ unsigned char raw[];
     __shared__ SmallControl ctl;
     unsigned char* base = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
-    unsigned char *xs = base, *xl = base + 2 * kPlane, *gs = base + 4 * kPlane, *qs = base + 6 * kPlane, *ql = base + 8 * kPlane;
-    unsigned char* parts = ql;   // of G, in a cluster
+    unsigned char *xs = base, *xl = base + 2 * kPlane, *gs = base + 4 * kPlane, *qs = base + 6 * kPlane, *ql = base + 8 * kPlane, *gl = base + 10 * kPlane;
+    unsigned char *parts = ql, *parts_lo = qs;   // of G, in a cluster
 
     const int warp = int(threadIdx.x) / 32, lane = int(threadIdx.x) % 32;
     const uint32_t rank = cluster_rank(), ctas = cluster_size();
@@ -116,7 +148,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
     const CopyShape& c = p.in.shapes[k];
     const int matrix = cluster - p.first_cluster[k];
     const int rows = c.s.rows, cols = c.s.cols, side = c.s.side;
-    const bool wide = rows <= cols;
+    const bool wide = rows <= cols, fine = FINE && c.s.fine;
     const int at = int(rank) * 128, length = wide ? cols : rows;
     const int mine = length - at < 0 ? 0 : length - at < 128 ? length - at : 128;   // of the long side
     tmem_before();
@@ -205,7 +237,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
     // ---- the steps
     uint32_t turn = 0;
     const Waiter wait = {&ctl.failed};
-    const uint32_t xa = smem_addr(xs), xla = smem_addr(xl), ga = smem_addr(gs), qa = smem_addr(qs), qla = smem_addr(ql), out = *static_cast<volatile uint32_t*>(&ctl.tmem);
+    const uint32_t xa = smem_addr(xs), xla = smem_addr(xl), ga = smem_addr(gs), qa = smem_addr(qs), qla = smem_addr(ql), gla = smem_addr(gl), out = *static_cast<volatile uint32_t*>(&ctl.tmem);
     // what is there of k; all 128 rows and columns are computed, zeros beyond the matrix
     const int side16 = (side + 15) / 16 * 16, mine16 = mine > 0 ? (mine + 15) / 16 * 16 : 16;
     // D (+)= A B^T over `depth` k; B read K-major, or MN-major (then its rows are k)
@@ -242,9 +274,15 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
         }
         // G
         ready();
-        if (warp == 0 && elected()) issue(xa, xa, false, mine16, false);
+        if (warp == 0 && elected()) {
+            issue(xa, xa, false, mine16, false);
+            if (fine) {
+                issue(xa, xla, false, mine16, true);
+                issue(xla, xa, false, mine16, true);
+            }
+        }
         done();
-        unsigned char* plane = (ctas == 1 ? gs : parts) + h * kPlane;
+        unsigned char *plane = (ctas == 1 ? gs : parts) + h * kPlane, *plane_lo = (ctas == 1 ? gl : parts_lo) + h * kPlane;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             float v[32];
@@ -252,18 +290,31 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] *= kUnscale;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(plane + unit_at(r, i * 4 + j)) = Fp16::pack(v + j * 8);
+            for (int j = 0; j < 4; ++j) {
+                *reinterpret_cast<uint4*>(plane + unit_at(r, i * 4 + j)) = Fp16::pack(v + j * 8);
+                if (fine) *reinterpret_cast<uint4*>(plane_lo + unit_at(r, i * 4 + j)) = left_of(v + j * 8);
+            }
         }
         if (ctas > 1) {
             cluster_sync();
-            if (ctas == 2) add_up<2>(parts, gs, rank);
+            if (fine) {
+                if (ctas == 2) add_up_fine<2>(parts, parts_lo, gs, gl, rank);
+                else if (ctas == 4) add_up_fine<4>(parts, parts_lo, gs, gl, rank);
+                else add_up_fine<8>(parts, parts_lo, gs, gl, rank);
+            } else if (ctas == 2) add_up<2>(parts, gs, rank);
             else if (ctas == 4) add_up<4>(parts, gs, rank);
             else add_up<8>(parts, gs, rank);
             cluster_sync();
         }
         // Q
         ready();
-        if (warp == 0 && elected()) issue(ga, ga, false, side16, false);
+        if (warp == 0 && elected()) {
+            issue(ga, ga, false, side16, false);
+            if (fine) {
+                issue(ga, gla, false, side16, true);
+                issue(gla, ga, false, side16, true);
+            }
+        }
         done();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -273,6 +324,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
             for (int j = 0; j < 4; ++j) {
                 float g[8];
                 Fp16::unpack(*reinterpret_cast<const uint4*>(gs + h * kPlane + unit_at(r, i * 4 + j)), g);
+                if (fine) {
+                    float l[8];
+                    Fp16::unpack(*reinterpret_cast<const uint4*>(gl + h * kPlane + unit_at(r, i * 4 + j)), l);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) g[e] += l[e];
+                }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) g[e] = fmaf(b, g[e], q * v[j * 8 + e]);
                 const uint32_t to = h * kPlane + unit_at(r, i * 4 + j);
@@ -355,9 +412,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
 template <bool MUON>
 using SmallKernel = void (*)(SmallParams<MUON>);
 template <bool MUON>
-SmallKernel<MUON> small_of(int32_t dtype) {
-    return dtype == ADAMW_DTYPE_FP32 ? small_kernel<MUON, ADAMW_DTYPE_FP32>
-           : dtype == ADAMW_DTYPE_BF16 ? small_kernel<MUON, ADAMW_DTYPE_BF16> : small_kernel<MUON, MUON ? ADAMW_DTYPE_BF16 : ADAMW_DTYPE_FP16>;
+SmallKernel<MUON> small_of(int32_t dtype, bool fine) {
+    constexpr int kOther = MUON ? ADAMW_DTYPE_BF16 : ADAMW_DTYPE_FP16;
+    if (dtype == ADAMW_DTYPE_FP32) return fine ? small_kernel<MUON, ADAMW_DTYPE_FP32, true> : small_kernel<MUON, ADAMW_DTYPE_FP32, false>;
+    if (dtype == ADAMW_DTYPE_BF16) return fine ? small_kernel<MUON, ADAMW_DTYPE_BF16, true> : small_kernel<MUON, ADAMW_DTYPE_BF16, false>;
+    return fine ? small_kernel<MUON, kOther, true> : small_kernel<MUON, kOther, false>;
 }
 
 // CTAs of a cluster for a shape; 0: too large.
@@ -381,7 +440,6 @@ bool launch_small(const Group& g, const int32_t* first_sum, const adamw_ortho_t&
         most = std::max(most, small_ctas(g.shapes[i]));
         matrices += g.shapes[i].count;
     }
-    const SmallKernel<MUON> kernel = small_of<MUON>(dtype);
     // one launch while its CTAs run at a time, though some have nothing to do;
     // else one for each size of cluster
     const bool together = matrices * most <= sms;
@@ -389,17 +447,20 @@ bool launch_small(const Group& g, const int32_t* first_sum, const adamw_ortho_t&
         Group part;
         int32_t sums[kMaxShapes];
         int64_t clusters = 0;
+        bool fine = false;
         for (int i = 0; i < g.n; ++i) {
             if (!together && small_ctas(g.shapes[i]) != ctas) continue;
             part.shapes[part.n] = g.shapes[i];
             part.buffers[part.n] = Buffers{};
             sums[part.n] = first_sum[i];
+            fine = fine || g.shapes[i].fine;
             p->rate[part.n] = g.rate[i];
             p->first_cluster[part.n++] = int32_t(clusters);
             clusters += g.shapes[i].count;
         }
         if (part.n == 0) continue;
         fill_copies(part, sums, piece, &p->in);
+        const SmallKernel<MUON> kernel = small_of<MUON>(dtype, fine);
         if (!launched(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmallBytes)),
                       "cudaFuncSetAttribute") ||
             !launched(launch(kernel, uint32_t(clusters * ctas), kSmallThreads, ctas, kSmallBytes, st, *p), "small launch"))

@@ -85,6 +85,22 @@ def test_thin_matrices(shape):
         assert off(M.orthogonalize(x, dtype=F32), exact(x)) < TOL / 2
 
 
+@pytest.mark.parametrize("length", [1, 2, 3, 33, 144, 300, 1000, 1030, 2000])
+@pytest.mark.parametrize("side", [1, 2, 3, 5, 8, 17, 32])
+def test_smallest_sides(side, length):
+    """Sides of up to 32, whose few errors do not average out: every operand is two
+    fp16 there, each rounding at most 2^-22 of its value whatever its sign.  Q and the
+    X that it multiplies enter with 2.8 each, G's factors with 4.8 each: 15.2 2^-22 =
+    3.6e-6 a step at most.  A step multiplies an error by a = 3.44 at most, so five
+    leave (1 + 3.44 + ... + 3.44^4) 3.6e-6 = 7.1e-4."""
+    length = max(side, length)
+    for seed, dtype in enumerate((BF, HALF, F32)):
+        for shape in ((200, side, length), (200, length, side)):
+            x = rand(*shape, dtype=dtype, seed=seed)
+            want = exact(x) if shape[1] == side else exact(x.mT).mT   # the same, of the smaller side
+            assert off(M.orthogonalize(x, dtype=F32), want) < 7.1e-4
+
+
 @pytest.mark.parametrize("shape", [(7, 64, 96), (3, 2, 33, 40), (200, 16, 20), (5, 257, 130), (2, 3, 300, 299)], ids=str)
 def test_batches(shape):
     x = rand(*shape, dtype=BF)
