@@ -148,7 +148,7 @@ struct ExpertRows {
         const int64_t* offsets;
         int64_t rows;
         int32_t experts, k, tiles_n;
-        bool is_bf16, w_mn;
+        bool is_bf16, w_mn, shared;   // shared: one matrix for all experts
         RowsAt y;
     };
     static constexpr bool kTail = false, kParts = false;
@@ -185,7 +185,7 @@ struct ExpertRows {
         w.a_at = g->bounds[k] + m * S::kRows;
         w.b_at = n * S::kCols;
         w.a_z = 0;
-        w.b_z = k - 1;
+        w.b_z = p.shared ? 0 : k - 1;
         w.k_at = 0;
         w.k_len = k == 0 || k == p.experts + 1 ? 0 : p.k;
         w.a_mn = false;
@@ -486,14 +486,20 @@ int check(const adamw_matrices_t* m, bool operand) {
     return ADAMW_OK;
 }
 
-// TMA reads it as it is (its strides are below 2^40 bytes).
+// One matrix for all of a batch (a stride of 0) is read as the one that it is.
+adamw_matrices_t single(adamw_matrices_t m) {
+    if (m.batch > 1 && m.batch_stride == 0) m.batch = 1;
+    return m;
+}
+// TMA reads it as it is (its strides are above 0 and below 2^40 bytes).
 bool direct(const adamw_matrices_t& m) {
     constexpr int64_t kMost = int64_t(1) << 38;
     return aligned(m.data, 16) && (m.rows <= 1 || (m.row_stride % 8 == 0 && m.row_stride >= m.cols && m.row_stride <= kMost)) &&
-           (m.batch <= 1 || (m.batch_stride % 8 == 0 && m.batch_stride <= kMost));
+           (m.batch <= 1 || (m.batch_stride % 8 == 0 && m.batch_stride > 0 && m.batch_stride <= kMost));
 }
 int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
-int64_t copy_bytes(const adamw_matrices_t& m) {
+int64_t copy_bytes(const adamw_matrices_t& given) {
+    const adamw_matrices_t m = single(given);
     if (direct(m) || m.cols == 0) return 0;
     return (m.batch * m.rows * padded(m.cols) * 2 + 255) / 256 * 256;
 }
@@ -506,6 +512,7 @@ bool readable(adamw_matrices_t* const (&operands)[3], void* workspace, cudaStrea
     int64_t most = 0;
     for (adamw_matrices_t* m : operands) {
         if (!m || m->batch * m->rows * m->cols == 0) continue;
+        *m = single(*m);
         if (direct(*m)) {
             if (m->rows <= 1) m->row_stride = padded(m->cols);
             if (m->batch <= 1) m->batch_stride = m->row_stride * m->rows;
@@ -584,7 +591,7 @@ bool result_map(CUtensorMap* map, adamw_matrices_t m) {
 }
 
 template <class S, bool STAGED>
-int rows_call(const adamw_matrices_t& x, const adamw_matrices_t& w, bool transposed, const int64_t* offsets,
+int rows_call(const adamw_matrices_t& x, const adamw_matrices_t& w, int64_t experts, bool transposed, const int64_t* offsets,
               const adamw_matrices_t& y, int64_t tiles, int units, cudaStream_t st) {
     using P = ExpertRows<S, STAGED>;
     typename P::Params p;
@@ -594,7 +601,8 @@ int rows_call(const adamw_matrices_t& x, const adamw_matrices_t& w, bool transpo
     if (STAGED && !result_map(&p.result, y)) return ADAMW_ERR_CUDA;
     p.offsets = offsets;
     p.rows = x.rows;
-    p.experts = int32_t(w.batch);
+    p.experts = int32_t(experts);
+    p.shared = w.batch < experts;
     p.k = int32_t(x.cols);
     p.tiles_n = int32_t(up(y.cols, S::kCols));
     p.is_bf16 = x.dtype == ADAMW_DTYPE_BF16;
@@ -620,7 +628,7 @@ int stream_call(const adamw_matrices_t& x, const adamw_matrices_t& w, const int6
     p.n = int32_t(y.cols);
     p.k = int32_t(x.cols);
     p.y = rows_of(y);
-    const bool vec = direct(x) && direct(w) && x.cols % 8 == 0, bf16 = x.dtype == ADAMW_DTYPE_BF16;
+    const bool vec = direct(x) && direct(single(w)) && x.cols % 8 == 0, bf16 = x.dtype == ADAMW_DTYPE_BF16;
     const auto kernel = bf16 ? (vec ? stream_kernel<ADAMW_DTYPE_BF16, true> : stream_kernel<ADAMW_DTYPE_BF16, false>)
                              : (vec ? stream_kernel<ADAMW_DTYPE_FP16, true> : stream_kernel<ADAMW_DTYPE_FP16, false>);
     int occ = 0;
@@ -706,24 +714,24 @@ int check_workspace(int64_t bytes, const void* workspace) {
 }
 
 // Checked and readable, with something to do.
-int launch_rows(const adamw_matrices_t& x, const adamw_matrices_t& w, bool transposed, const int64_t* offsets,
+int launch_rows(const adamw_matrices_t& x, const adamw_matrices_t& w, int64_t experts, bool transposed, const int64_t* offsets,
                 const adamw_matrices_t& y, cudaStream_t st) {
     TileUnits units;
     if (!launched(units_of<ExpertRows<PairTile, true>>(&units), "tile units")) return ADAMW_ERR_CUDA;
     const int64_t n = y.cols;
     // the grid covers the most tiles that the groups can have: one partial in each
-    const int64_t groups = w.batch + 2;
+    const int64_t groups = experts + 2;
     auto most = [&](int rows, int cols) { return (x.rows / rows + groups) * up(n, cols); };
     // what groups of one size would have
-    const int64_t each = up(x.rows, w.batch), used = std::min(w.batch, x.rows);
+    const int64_t each = up(x.rows, experts), used = std::min(experts, x.rows);
     auto likely = [&](int rows, int cols) { return used * up(each, rows) * up(n, cols); };
     const TileChoice choice = {{likely(PairTile::kRows, PairTile::kCols), likely(WideTile::kRows, WideTile::kCols),
                                 likely(SmallTile::kRows, SmallTile::kCols)}};
     auto call = [&](auto shape, int u) {
         using S = decltype(shape);
         const int64_t tiles = most(S::kRows, S::kCols);
-        return stages(y) ? rows_call<S, true>(x, w, transposed, offsets, y, tiles, u, st)
-                         : rows_call<S, false>(x, w, transposed, offsets, y, tiles, u, st);
+        return stages(y) ? rows_call<S, true>(x, w, experts, transposed, offsets, y, tiles, u, st)
+                         : rows_call<S, false>(x, w, experts, transposed, offsets, y, tiles, u, st);
     };
     switch (choose_shape(choice, up(x.cols, kStepK), units.pairs, units.sms)) {
         case kPairShape: return call(PairTile(), units.pairs);
@@ -772,7 +780,7 @@ extern "C" int adamw_expert_rows(const adamw_matrices_t* x, const adamw_matrices
     if ((rc = check_workspace(copy_bytes(*x) + copy_bytes(*w), workspace)) != ADAMW_OK) return rc;
     adamw_matrices_t a = *x, b = *w;
     if (!readable({&a, &b, nullptr}, workspace, st)) return ADAMW_ERR_CUDA;
-    return launch_rows(a, b, transposed != 0, offsets, *y, st);
+    return launch_rows(a, b, w->batch, transposed != 0, offsets, *y, st);
 }
 
 extern "C" int adamw_expert_outer(const adamw_matrices_t* dy, const adamw_matrices_t* x, const int64_t* offsets,
@@ -809,7 +817,7 @@ extern "C" int adamw_expert_backward(const adamw_matrices_t* dy, const adamw_mat
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     adamw_matrices_t a = *dy, b = *x, c = *w;
     if (!readable({&a, outer ? &b : nullptr, rows ? &c : nullptr}, workspace, st)) return ADAMW_ERR_CUDA;
-    if (rows && (rc = launch_rows(a, c, transposed == 0, offsets, *dx, st)) != ADAMW_OK) return rc;
+    if (rows && (rc = launch_rows(a, c, w->batch, transposed == 0, offsets, *dx, st)) != ADAMW_OK) return rc;
     if (outer) return dw_transposed ? launch_outer(b, a, offsets, *dw, accumulate != 0, st) : launch_outer(a, b, offsets, *dw, accumulate != 0, st);
     return ADAMW_OK;
 }

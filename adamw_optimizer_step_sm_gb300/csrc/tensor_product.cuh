@@ -723,7 +723,11 @@ inline bool tensor_map(CUtensorMap* map, bool bf16, const void* data, int64_t ba
         return false;
     }
     const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(batch)};
-    const cuuint64_t strides[2] = {cuuint64_t(ld) * 2, cuuint64_t(stride > 0 ? stride : ld) * 2};
+    if (ld <= 0 || stride <= 0) {   // rows or matrices that are one and the same are the caller's to tell apart
+        adamw::set_cuda_error("tensor map", "strides must be positive");
+        return false;
+    }
+    const cuuint64_t strides[2] = {cuuint64_t(ld) * 2, cuuint64_t(stride) * 2};
     const cuuint32_t box[3] = {cuuint32_t(box_cols), cuuint32_t(box_rows), 1};
     const cuuint32_t step[3] = {1, 1, 1};
     const CUresult r = f(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,

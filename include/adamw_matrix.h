@@ -26,7 +26,8 @@ extern "C" {
 
 /* A batch of matrices: element (b, r, c) is at b * batch_stride + r *
  * row_stride + c of `data`, in elements; a row's elements are consecutive.
- * Strides are not negative; rows and cols up to 2^31 - 1, offsets 64-bit. */
+ * Strides are not negative; of what is read they may be 0 (one matrix for all of
+ * a batch).  Rows and cols up to 2^31 - 1, offsets 64-bit. */
 typedef struct {
     void* data;
     int64_t batch;

@@ -1,0 +1,52 @@
+"""The matrix operators at the ends of what their calls allow: against
+definitions in 64 bits, with the tolerances of test_gpu_experts.py and
+test_gpu_orthogonalize.py unless a test says why it has another."""
+import pytest
+import torch
+
+from adamw_optimizer_step_sm_gb300 import adamw_sm as A
+from adamw_optimizer_step_sm_gb300 import matrix as M
+from test_gpu_experts import _no_wait_ran_out, check, close, offsets_of, outer, products, rand  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+BF, HALF, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+# ------------------------------------------------- one matrix for all experts --
+
+@pytest.mark.parametrize("tokens", [9, 300])
+@pytest.mark.parametrize("dtype", [BF, HALF], ids=str)
+@pytest.mark.parametrize("n,k", [(64, 80), (264, 520), (33, 45)])
+def test_one_matrix_for_all_experts(tokens, dtype, n, k):
+    """A stride of 0 between the experts' matrices, rows that TMA reads in place
+    (strides of 8 elements) or not, and the transposed views of such weights."""
+    offsets = [1, tokens // 3, tokens // 3, tokens // 2, tokens - 1]
+    rows = (k + 7) // 8 * 8
+    for w in (rand(1, n, rows, dtype=dtype, seed=2)[:, :, :k].expand(4, n, k), rand(n, k + 1, dtype=dtype, seed=2)[:, :k].expand(4, n, k),
+              rand(1, k, (n + 7) // 8 * 8, dtype=dtype, seed=2)[:, :, :n].mT.expand(4, n, k)):
+        assert w.stride(0) == 0
+        y, dx, dw = check(tokens, n, k, offsets, dtype=dtype, w=w)
+        again = check(tokens, n, k, offsets, dtype=dtype, w=w.clone(memory_format=torch.contiguous_format))
+        if tokens > 16 and w.stride(2) == 1:   # as of copies of it, to the bit
+            assert all(torch.equal(a, b) for a, b in zip((y, dx, dw), again))
+
+
+def test_gradient_of_one_matrix_for_all_experts():
+    """Through expand: the gradients of the experts are added up."""
+    w = rand(1, 64, 80, seed=2).requires_grad_()
+    x, dy, ends = rand(300, 80), rand(300, 64, seed=3), [0, 100, 120, 300]
+    M.expert_linear(x, w.expand(3, 64, 80), offsets_of(ends)).backward(dy)
+    dw, size = outer(dy, x, ends)
+    # one rounding to bf16 of each, one of their sum; the third for second orders
+    room = dw.abs().sum(0) * 3 * 2.0 ** -8 + size.sum(0) * (300 / 16 + 16) * 2.0 ** -23
+    assert (w.grad[0].double() - dw.sum(0)).abs().le(room).all()
+
+
+@pytest.mark.parametrize("tokens", [9, 300])
+def test_experts_that_alternate_by_rows(tokens):
+    """The matrices' rows by turns: strides between experts smaller than those
+    between rows."""
+    big, turned = rand(64, 4, 80, seed=2), rand(80, 4, 64, seed=3)
+    for w in (big.permute(1, 0, 2), turned.permute(1, 2, 0), big.permute(1, 0, 2)[:, :, 3:77]):
+        check(tokens, 64, w.shape[2], [0, tokens // 4, tokens // 3, tokens // 2, tokens], w=w)

@@ -1,0 +1,19 @@
+"""Host-side checks of the matrix operators at the ends of what their calls
+allow (no GPU; addresses are never dereferenced)."""
+import pytest
+
+from adamw_optimizer_step_sm_gb300 import adamw_sm as A
+from test_matrix_host import BAD, BIG, MIS, P, Q, W, _m, _muon, _muon_options, _options, _status, _w, _x, _y  # noqa: F401
+
+
+def test_one_matrix_for_all_experts_is_copied_once():
+    """Strides of 0 between matrices: one matrix is what the products read, and
+    all that an unaligned one takes of the workspace."""
+    ws, back = A.adamw_expert_workspace, A.adamw_expert_backward_workspace
+    one = 64 * 96 * 2
+    assert ws(_x(), _w(batch_stride=0)) == 0
+    assert ws(_x(), _w(batch_stride=0, row_stride=97)) == one
+    assert ws(_x(), _w(batch_stride=0, data=Q + 2)) == one
+    assert ws(_x(), _w(batch_stride=96, row_stride=97)) == 4 * one
+    assert back(_y(), _x(), _w(batch_stride=0, row_stride=97)) == one
+    assert back(_y(row_stride=65), _x(row_stride=97), _w(batch_stride=0)) == (40 * 64 + 40 * 96) * 2
