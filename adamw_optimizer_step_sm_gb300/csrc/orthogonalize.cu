@@ -325,10 +325,19 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const __grid_constan
 }
 
 // What brings a matrix of this sum of squares to 2^12 times the norm 1; NaN for
-// a sum that is not finite: the matrix has no direction.
-__device__ __forceinline__ float scale_of(double sum, float eps) {
-    const double norm = sqrt(sum);
-    return sum <= 1.7976931348623157e308 ? float(double(kScale) / (norm > eps ? norm : double(eps))) : sqrtf(-1.0f);
+// a sum that is not finite: the matrix has no direction.  Norms of fp32 numbers
+// (1e-45 to 4e44) and eps ask for factors beyond fp32: those come in two, of which
+// the first, a power of two, keeps every element in range.
+struct Scale {
+    float by, again;
+    __device__ __forceinline__ float operator()(float x) const { return x * by * again; }
+};
+__device__ __forceinline__ Scale scale_of(double sum, float eps) {
+    if (!(sum <= 1.7976931348623157e308)) return {sqrtf(-1.0f), 1.0f};
+    const double norm = sqrt(sum), s = double(kScale) / (norm > eps ? norm : double(eps));
+    if (s > 0x1p100) return {0x1p100f, float(s * 0x1p-100)};
+    if (s < 0x1p-100) return {0x1p-100f, float(s * 0x1p100)};
+    return {float(s), 1.0f};
 }
 
 // x at 2^12 times its value, as two fp16.
@@ -359,7 +368,7 @@ __global__ void __launch_bounds__(kNormThreads) copy_kernel(const __grid_constan
     __syncthreads();
     sum = 0.0;
     for (int k = 0; k < kNormThreads / 32; ++k) sum += part[k];
-    const float by = scale_of(sum, p.eps);
+    const Scale scale = scale_of(sum, p.eps);
     const Source<MUON, DT> src(p, c, matrix);
     const Walk walk(c.s, i, p.piece);
     uint4* hi = reinterpret_cast<uint4*>(c.hi + matrix * c.s.stride) + int64_t(i) * p.piece;
@@ -381,7 +390,7 @@ __global__ void __launch_bounds__(kNormThreads) copy_kernel(const __grid_constan
             src.value(raw[b], u, m);
             if (MUON && !skip) src.put(row[b], col[b], m);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) u[e] *= by;
+            for (int e = 0; e < 8; ++e) u[e] = scale(u[e]);
             uint4 h, l;
             split8(u, &h, &l);
             const int at = (k + b) * kNormThreads + int(threadIdx.x);   // the copy's rows are whole vectors

@@ -6,7 +6,9 @@ import torch
 
 from adamw_optimizer_step_sm_gb300 import adamw_sm as A
 from adamw_optimizer_step_sm_gb300 import matrix as M
+from adamw_optimizer_step_sm_gb300 import optim as OPT
 from test_gpu_experts import _no_wait_ran_out, check, close, offsets_of, outer, products, rand  # noqa: F401
+from test_gpu_orthogonalize import TOL, exact, off
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +52,43 @@ def test_experts_that_alternate_by_rows(tokens):
     big, turned = rand(64, 4, 80, seed=2), rand(80, 4, 64, seed=3)
     for w in (big.permute(1, 0, 2), turned.permute(1, 2, 0), big.permute(1, 0, 2)[:, :, 3:77]):
         check(tokens, 64, w.shape[2], [0, tokens // 4, tokens // 3, tokens // 2, tokens], w=w)
+
+
+# --------------------------------------------------------- norms beyond fp32's --
+
+SMALL_AND_LARGE = pytest.mark.parametrize("shape", [(3, 64, 96), (3, 20, 30), (2, 100, 1000), (3, 300, 200), (2, 40, 2000)], ids=str)
+
+
+@SMALL_AND_LARGE
+@pytest.mark.parametrize("eps", [1e-7, 1e-36, 1e-38, 1e-45])
+def test_zero_matrices_give_zeros(shape, eps):
+    """2^12 / eps is beyond fp32 from 1.2e-35 down."""
+    x = rand(*shape, dtype=F32)
+    want = M.orthogonalize(x, eps=eps)
+    x[1] = 0
+    y = M.orthogonalize(x, eps=eps)
+    assert (y[1] == 0).all() and torch.equal(y[0], want[0])
+
+
+@SMALL_AND_LARGE
+def test_norms_of_the_smallest_and_largest_numbers(shape):
+    """Down to subnormal elements, whose few bits are the matrix's own."""
+    for scale in (1e-36, 1e-40, 1e-43):
+        x = rand(*shape, dtype=F32) * scale
+        assert off(M.orthogonalize(x, eps=1e-45, dtype=F32), exact(x, eps=2.0 ** -149)) < TOL
+    x = rand(*shape, dtype=F32) * 1e-36   # below eps: not brought to norm 1
+    assert off(M.orthogonalize(x, eps=1e-32, dtype=F32), exact(x, eps=1e-32)) < TOL
+    x = rand(*shape, dtype=F32).sign() * 3e38
+    assert off(M.orthogonalize(x, dtype=F32), exact(x)) < TOL
+
+
+@pytest.mark.parametrize("eps", [1e-7, 1e-38])
+def test_muon_step_of_no_gradient(eps):
+    """Momentum and update are zeros: the weights only decay, whatever eps."""
+    params = [torch.nn.Parameter(rand(*s, seed=4)) for s in ((64, 96), (300, 200), (2, 40, 1030))]
+    opt = OPT.Muon(params, lr=0.25, weight_decay=0.5, eps=eps)
+    before = [opt.state[p]["master"].clone() for p in params]
+    opt.step()
+    assert int(opt.last_nonfinite[0]) == 0
+    for p, w in zip(params, before):
+        assert torch.equal(opt.state[p]["master"], w * 0.875) and (opt.state[p]["momentum"] == 0).all()
