@@ -413,9 +413,9 @@ class Muon(_FlatOptimizer):
     ``eps`` are ``matrix.orthogonalize``'s.
 
     One library call per group, no host synchronisation; the rates live on the
-    device, so that a captured step follows a schedule (call ``step`` once more
-    outside the capture, or write ``lr`` before each replay through
-    ``push_rates``).  A step whose gradients hold inf or NaN writes nothing and
+    device, so that a captured step follows a schedule: set ``lr`` and call
+    ``push_rates`` before each replay, and before the capture if they have
+    changed since the last step (a capture does not record the rates).  A step whose gradients hold inf or NaN writes nothing and
     is reported by ``last_nonfinite``.  Gradients, masters and checkpoints
     behave as ``MasterWeightAdamW``'s; ``GlobalClip`` takes both kinds."""
 
@@ -479,11 +479,16 @@ class Muon(_FlatOptimizer):
     def push_rates(self) -> None:
         """Writes each group's lr, momentum and weight decay to the device, for
         the next step (``step`` does it by itself; replays of a captured step
-        do not)."""
+        do not).  Refused in a capture where they have changed: every replay
+        would write the recorded rates over those that were pushed for it."""
         for group in self.param_groups:
             b = self._buffers_of(group)
             key = self._rates(group)
             if key != b.hp_key:
+                with torch.cuda.device(b.d_hp.device):
+                    if torch.cuda.is_current_stream_capturing():
+                        raise RuntimeError("rates have changed since they were written to the device: "
+                                           "call push_rates() before the capture")
                 b.d_hp.copy_(torch.tensor([*key, 0.0], dtype=torch.float32).pin_memory(), non_blocking=True)
                 b.hp_key = key
 

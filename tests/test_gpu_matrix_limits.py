@@ -92,3 +92,55 @@ def test_muon_step_of_no_gradient(eps):
     assert int(opt.last_nonfinite[0]) == 0
     for p, w in zip(params, before):
         assert torch.equal(opt.state[p]["master"], w * 0.875) and (opt.state[p]["momentum"] == 0).all()
+
+
+# ------------------------------------------------------ captured steps' rates --
+
+def _two_muons(**kw):
+    out = []
+    for _ in range(2):
+        params = [torch.nn.Parameter(rand(*s, seed=4)) for s in ((64, 48), (300, 200))]
+        out.append((params, OPT.Muon(params, lr=1e-2, **kw)))
+    return out
+
+
+def _grads(params, seed):
+    for k, p in enumerate(params):
+        p.grad.copy_(rand(*p.shape, seed=seed + 100 * k))
+
+
+@pytest.mark.parametrize("warm", [False, True])
+def test_capture_does_not_record_rates(warm):
+    """Rates changed since the last step, or never written: the capture is
+    refused, before anything of the step is recorded; pushed first, the replays
+    take what is pushed for each."""
+    (a, x), (b, y) = _two_muons()
+    if warm:
+        for p, o in ((a, x), (b, y)):
+            _grads(p, 1)
+            o.step()
+        x.param_groups[0]["lr"] = y.param_groups[0]["lr"] = 5e-3
+    before = [p.detach().clone() for p in a]
+    with pytest.raises(RuntimeError, match="push_rates"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            x.step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(a, before))
+    x.push_rates()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        x.step()
+    junk = []
+    for k, lr in enumerate((5e-3, 2e-3, 2e-3, 0.0, 1e-2)):
+        for p, o in ((a, x), (b, y)):
+            _grads(p, 5 + k)
+            o.param_groups[0]["lr"] = lr
+        x.push_rates()
+        junk.append(torch.full((4,), 1e3).pin_memory())   # what a released pinned block may hold next
+        g.replay()
+        y.step()
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+        if k == 2:   # a step between replays
+            for p, o in ((a, x), (b, y)):
+                o.step()
+            assert all(torch.equal(p, q) for p, q in zip(a, b))
