@@ -120,6 +120,14 @@ class _GroupBuffers:
         self.hp_key = None
 
 
+def _refuse_capture(device, instead: str) -> None:
+    """Rates go to the device from pinned memory that is released at once: a
+    graph would copy whatever is there at each replay."""
+    with torch.cuda.device(device):
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("rates have changed since they were written to the device: " + instead)
+
+
 class _FlatOptimizer(torch.optim.Optimizer):
     """What the optimizers of this module share: a flat gradient buffer per
     group that the parameters' gradients are views of, and masters that follow
@@ -266,6 +274,7 @@ class _FlatAdamW(_FlatOptimizer):
                 # refuse out-of-range values here: on the device they would
                 # only make the step skip
                 A.adamw_step_scalars(hp, 1)
+                _refuse_capture(b.d_hp.device, "step once before the capture")
                 host = torch.frombuffer(bytearray(bytes(hp)), dtype=torch.uint8)
                 b.d_hp.copy_(host.pin_memory(), non_blocking=True)
                 b.hp_key = key
@@ -485,10 +494,7 @@ class Muon(_FlatOptimizer):
             b = self._buffers_of(group)
             key = self._rates(group)
             if key != b.hp_key:
-                with torch.cuda.device(b.d_hp.device):
-                    if torch.cuda.is_current_stream_capturing():
-                        raise RuntimeError("rates have changed since they were written to the device: "
-                                           "call push_rates() before the capture")
+                _refuse_capture(b.d_hp.device, "call push_rates() before the capture")
                 b.d_hp.copy_(torch.tensor([*key, 0.0], dtype=torch.float32).pin_memory(), non_blocking=True)
                 b.hp_key = key
 

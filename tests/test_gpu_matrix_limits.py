@@ -144,3 +144,31 @@ def test_capture_does_not_record_rates(warm):
             for p, o in ((a, x), (b, y)):
                 o.step()
             assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_capture_does_not_record_an_adamw_step_rates():
+    """The same of the other optimizers of the module, whose replays keep the
+    rates of the step before the capture."""
+    out = []
+    for _ in range(2):
+        params = [torch.nn.Parameter(rand(40, 50, seed=4)), torch.nn.Parameter(rand(77, seed=5))]
+        out.append((params, OPT.AnyPrecisionAdamW(params, lr=1e-2)))
+    (a, x), (b, y) = out
+    for p, o in out:
+        _grads(p, 1)
+        o.step()
+        o.param_groups[0]["lr"] = 4e-3
+    held = torch.full((64,), 200, dtype=torch.uint8).pin_memory()
+    del held   # a pinned block that could be taken in a capture
+    with pytest.raises(RuntimeError, match="before the capture"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            x.step()
+    x.step()
+    y.step()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        x.step()
+    for _ in range(3):
+        g.replay()
+        y.step()
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
