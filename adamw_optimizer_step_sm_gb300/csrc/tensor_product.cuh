@@ -23,8 +23,9 @@
 // (1996 TFLOP/s, 104 % of the measured burst rate of 1911; the library's product
 // 545 us in the same process); larger products are bound by the power limit.
 //
-// No wait is endless: after about half a second it gives up, sets the device's
-// status word, and every role leaves.
+// No wait is endless: after about half a second (a wait for a tile's products: and
+// 4 us for each of their steps) it gives up, sets the device's status word, and
+// every role leaves.
 #pragma once
 
 #include <cuda.h>
@@ -40,7 +41,10 @@ constexpr int kStepK = 64;                  // elements of k in a stage: 128 byt
 constexpr int kRowsOfCta = 128;             // accumulator rows of a CTA: the lanes of tensor memory
 constexpr int kBlock64 = 64;                // columns of a staged block: 32 rows of 128 bytes
 constexpr uint32_t kControlRoom = 1024;
-constexpr long long kGiveUp = 1000000000ll; // cycles
+// Cycles after which a wait gives up, and what a wait for all products of a tile has
+// besides for each step of 64 k: a step takes 500 to 550 of the tensor cores, about
+// 1500 at an SM's share of HBM.
+constexpr long long kGiveUp = 1000000000ll, kGiveUpStep = 8192;
 
 // ------------------------------------------------------------------ PTX ---
 
@@ -342,19 +346,20 @@ __device__ int32_t g_tile_status;
 struct Waiter {
     int32_t* failed;   // the CTA's
     // the same answer for all of a warp
-    __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity) const {
-        return __all_sync(0xffffffffu, (*this)(bar, parity));
+    __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity, int k = 0) const {
+        return __all_sync(0xffffffffu, (*this)(bar, parity, k));
     }
-    // false: given up (here or elsewhere in the CTA)
-    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+    // false: given up (here or elsewhere in the CTA).  k: of the products that are
+    // waited for
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity, int k) const {
         if (barrier_test(bar, parity)) return true;
         const long long start = clock64();
         for (;;) {
 #pragma unroll 1
-            for (int k = 0; k < 64; ++k)
+            for (int i = 0; i < 64; ++i)
                 if (barrier_test(bar, parity)) return true;
             if (*static_cast<volatile int32_t*>(failed)) return false;
-            if (clock64() - start > kGiveUp) {
+            if (clock64() - start > kGiveUp + k / kStepK * kGiveUpStep) {
                 *static_cast<volatile int32_t*>(failed) = 1;
                 atomicOr(&g_tile_status, 1);
                 return false;
@@ -590,7 +595,7 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
             it += uint32_t(steps);
             if (rest == 0) continue;
             const uint32_t s = (it - 1) % kStages;
-            if (!(ok = wait.warp(smem_addr(&ctl->tail[s]), turns >> s & 1))) break;
+            if (!(ok = wait.warp(smem_addr(&ctl->tail[s]), turns >> s & 1, w.k_len))) break;
             turns ^= 1u << s;
             const int end = (rest + 15) / 16 * 16;   // what the products read
             unsigned char* at = ring + s * S::kStageBytes;
@@ -625,14 +630,14 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
                 block.acc = tmem + (uint32_t(row0) << 16) + acc * S::kCols;
                 P::begin(p, out, block, c0);
                 if (w.k_len > 0) {
-                    if (!(ok = wait.warp(smem_addr(&ctl->acc_full[acc]), n >> 1 & 1))) break;
+                    if (!(ok = wait.warp(smem_addr(&ctl->acc_full[acc]), n >> 1 & 1, w.k_len))) break;
                     tmem_after();
                 }
                 if (!(ok = P::finish(p, out, block, w.k_len > 0))) break;
             } else {
                 const int row = row0 + lane;
                 if (w.k_len > 0) {
-                    if (!(ok = wait.warp(smem_addr(&ctl->acc_full[acc]), n >> 1 & 1))) break;
+                    if (!(ok = wait.warp(smem_addr(&ctl->acc_full[acc]), n >> 1 & 1, w.k_len))) break;
                     tmem_after();
                 }
                 for (int c = c0; c < c1; c += 32) {

@@ -172,3 +172,25 @@ def test_capture_does_not_record_an_adamw_step_rates():
         g.replay()
         y.step()
         assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+# ------------------------------------------------------------- very long sums --
+
+def test_sums_longer_than_a_fixed_wait():
+    """Tiles of 4.2e6 steps of 64 k, about a second of one SM: the epilogue's wait
+    for them has its time for each step.  All but the last rows are zeros, whose
+    sums are exact."""
+    n = 2 ** 28
+    x, dy = (torch.zeros(n + 300, 8, dtype=BF, device="cuda") for _ in range(2))
+    x[-300:], dy[-300:] = rand(300, 8), rand(300, 8, seed=3)
+    w = rand(2, 8, 8, seed=2)
+    _, dw = M.expert_linear_backward(dy, x, w, offsets_of([0, 0, n + 300]), need=(False, True))
+    close(dw[1:], outer(dy[-300:], x[-300:], [0, 300]), 300)
+    assert (dw[0] == 0).all()
+    del x, dy
+    x, w = torch.zeros(17, n, dtype=BF, device="cuda"), torch.zeros(1, 8, n, dtype=BF, device="cuda")
+    x[:, -300:], w[:, :, -300:] = rand(17, 300), rand(1, 8, 300, seed=2)
+    y = M.expert_linear(x, w, offsets_of([0, 17]))
+    close(y, products(x[:, -300:], w[:, :, -300:], [0, 17]), 300)
+    del x, w
+    torch.cuda.empty_cache()
