@@ -330,14 +330,22 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const __grid_constan
 // the first, a power of two, keeps every element in range.
 struct Scale {
     float by, again;
-    __device__ __forceinline__ float operator()(float x) const { return x * by * again; }
+    template <int N>
+    __device__ __forceinline__ void operator()(float (&x)[N]) const {
+#pragma unroll
+        for (int e = 0; e < N; ++e) x[e] *= by;
+        if (again == 1.0f) return;
+#pragma unroll
+        for (int e = 0; e < N; ++e) x[e] *= again;
+    }
 };
 __device__ __forceinline__ Scale scale_of(double sum, float eps) {
     if (!(sum <= 1.7976931348623157e308)) return {sqrtf(-1.0f), 1.0f};
     const double norm = sqrt(sum), s = double(kScale) / (norm > eps ? norm : double(eps));
-    if (s > 0x1p100) return {0x1p100f, float(s * 0x1p-100)};
-    if (s < 0x1p-100) return {0x1p-100f, float(s * 0x1p100)};
-    return {float(s), 1.0f};
+    const float f = float(s);   // compared as fp32: fp64 arithmetic is slow
+    if (f >= 0x1p-100f && f <= 0x1p100f) return {f, 1.0f};
+    if (f > 1.0f) return {0x1p100f, float(s * 0x1p-100)};
+    return {0x1p-100f, float(s * 0x1p100)};
 }
 
 // x at 2^12 times its value, as two fp16.
@@ -389,8 +397,7 @@ __global__ void __launch_bounds__(kNormThreads) copy_kernel(const __grid_constan
             float u[8], m[8];
             src.value(raw[b], u, m);
             if (MUON && !skip) src.put(row[b], col[b], m);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) u[e] = scale(u[e]);
+            scale(u);
             uint4 h, l;
             split8(u, &h, &l);
             const int at = (k + b) * kNormThreads + int(threadIdx.x);   // the copy's rows are whole vectors

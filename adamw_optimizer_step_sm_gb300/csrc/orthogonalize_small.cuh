@@ -231,8 +231,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
         }
     }
     const Scale scale = scale_of(sum, p.in.eps);
-#pragma unroll
-    for (int e = 0; e < 64; ++e) x[e] = scale(x[e]);
+    scale(x);
 
     // ---- the steps
     uint32_t turn = 0;
