@@ -226,6 +226,8 @@ def load() -> ctypes.CDLL:
             L.adamw_expert_backward_workspace.argtypes = [mats, mats, mats]
             L.adamw_expert_backward_workspace.restype = i64
             L.adamw_matrix_status.argtypes = [P(i32)]
+            L.adamw_matrix_test_expire.argtypes = [i32]
+            L.adamw_matrix_test_expire.restype = None
             L.adamw_status_string.argtypes = [ctypes.c_int]
             L.adamw_status_string.restype = ctypes.c_char_p
             for name in ("adamw_plan_create", "adamw_step", "adamw_grad_norm", "adamw_step_device",
@@ -543,6 +545,10 @@ def adamw_matrix_status() -> int:
     return out.value
 
 
+def adamw_matrix_test_expire(on: bool) -> None:
+    load().adamw_matrix_test_expire(int(on))
+
+
 def hparams(lr=2e-4, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1,
             max_grad_norm=0.0) -> adamw_hparams_t:
     return adamw_hparams_t(lr, beta1, beta2, eps, weight_decay, max_grad_norm)
@@ -796,7 +802,8 @@ class MuonPlan:
 
     def step(self, d_hparams, nonfinite, stream=None) -> None:
         """d_hparams: CUDA fp32 [4]: lr, momentum, weight decay, unused;
-        nonfinite: CUDA int32 [1], 1 after a step that wrote nothing."""
+        nonfinite: CUDA int32 [1], 1 after a step that wrote nothing, 2 after one
+        whose results are undefined as a kernel's bounded wait ran out."""
         import torch
         for name, t, dt, n in (("d_hparams", d_hparams, torch.float32, 4), ("nonfinite", nonfinite, torch.int32, 1)):
             if t.dtype != dt or t.device != self.device or t.numel() < n or not t.is_contiguous():

@@ -201,6 +201,8 @@ struct ExpertRows {
     }
     __device__ static bool wanted(const Params&, const Out& o, int row, int col) { return row < o.rows && col < o.y.cols; }
     __device__ static void begin(const Params&, const Out&, Staged&, int) {}
+    __device__ static void gave_up(const Params&) {}
+    __device__ static bool pretend(const Params&) { return false; }
     __device__ static bool finish(const Params& p, const Out& o, Staged& s, bool any) {
         for (int c = s.col; c < s.end && wanted(p, o, s.row, c); c += kBlock64)
             store_block<1>(&p.result, o.y.dtype == ADAMW_DTYPE_BF16, o.y, o.col + c, o.row + s.row, 0, o.rows - s.row, c, s, any);
@@ -276,6 +278,8 @@ struct ExpertOuter {
     }
     __device__ static bool wanted(const Params&, const Out& o, int row, int col) { return row < o.rows && col < o.dw.cols; }
     __device__ static void begin(const Params&, const Out&, Staged&, int) {}
+    __device__ static void gave_up(const Params&) {}
+    __device__ static bool pretend(const Params&) { return false; }
     __device__ static bool finish(const Params& p, const Out& o, Staged& s, bool any) {
         // rows beyond dw's end are left out by TMA
         for (int c = s.col; c < s.end && wanted(p, o, s.row, c); c += kBlock64)

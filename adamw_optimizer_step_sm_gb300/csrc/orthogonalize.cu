@@ -30,6 +30,7 @@
 // 1000 32 -> 53, and a long Gram product thrice its steps (16 x 8192 243 -> 615), so
 // sides above, whose worst is below bf16's rounding, keep one.
 #include <algorithm>
+#include <atomic>
 #include <exception>
 #include <new>
 #include <vector>
@@ -446,8 +447,13 @@ struct ProductParams {
     Batch dst;
     const MuonMatrix* table;
     const adamw_muon_hparams_t* hp;
-    const int32_t* nonfinite;
+    int32_t* nonfinite;   // a step's: a wait that runs out also keeps it from writing what comes after
+    int32_t pretend;      // report as if one had run out
 };
+
+__device__ __forceinline__ void gave_up_on(int32_t* nonfinite) {
+    if (nonfinite) atomicOr(nonfinite, 2);
+}
 
 // LOW_IN, LOW_OUT: X has its second fp16, the next X gets one.  Of G and Q, LOW_IN:
 // there are fine shapes (a flag at run time alone slowed all others by 2 to 5 %).
@@ -482,6 +488,8 @@ struct Product {
         float decay, rate, a, b, c;
     };
     __device__ static bool bf16(const Params&) { return false; }
+    __device__ static void gave_up(const Params& p) { gave_up_on(p.nonfinite); }
+    __device__ static bool pretend(const Params& p) { return p.pretend != 0; }
     __device__ static void prepare(const Params&, unsigned char*) {}
     __device__ static int tiles(const Params& p, const unsigned char*) { return p.tiles; }
     __device__ static const ProductShape& find(const Params& p, int t, int32_t* matrix, int32_t* m, int32_t* n) {
@@ -898,6 +906,8 @@ bool launch_kind(int kind, bool fine, bool low_in, bool low_out, const ProductPa
     }
 }
 
+std::atomic<int32_t> g_pretend{0};   // adamw_matrix_test_expire
+
 // The steps of one group, whose copies have been made.  last: kResult or
 // kUpdate, with what it needs in `with`.
 bool run_steps(const Group& g, const adamw_ortho_t& o, const float* coefs, int last, const ProductParams& with, const Device& d,
@@ -941,6 +951,7 @@ bool run_steps(const Group& g, const adamw_ortho_t& o, const float* coefs, int l
             p.table = with.table;
             p.hp = with.hp;
             p.nonfinite = with.nonfinite;
+            p.pretend = g_pretend;
             if (!(shape == kPairShape   ? launch_kind<PairTile>(which, fine, low_in, low_out, p, d.pairs, st)
                   : shape == kWideShape ? launch_kind<WideTile>(which, fine, low_in, low_out, p, d.sms, st)
                                         : launch_kind<SmallTile>(which, fine, low_in, low_out, p, d.sms, st)))
@@ -1025,6 +1036,8 @@ extern "C" int adamw_matrix_status(int32_t* out) {
     const int rc = adamw::ortho_status(out);
     return rc != ADAMW_OK ? rc : adamw::expert_status(out);
 }
+
+extern "C" void adamw_matrix_test_expire(int32_t on) { g_pretend = on != 0; }
 
 extern "C" int64_t adamw_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols) {
     if (!sizes_fit(batch, rows, cols) || batch * rows * cols == 0) return 0;

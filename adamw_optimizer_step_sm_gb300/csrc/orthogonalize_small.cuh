@@ -33,7 +33,7 @@ struct SmallParams {
     int32_t first_cluster[kMaxShapes];
     float rate[kMaxShapes];
     float coefs[32][3];
-    int32_t steps;
+    int32_t steps, pretend;
     Batch dst;
 };
 
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
     const uint32_t bar = smem_addr(&ctl.done);
     if (threadIdx.x == 0) {
         barrier_init(bar, 1);
-        ctl.failed = 0;
+        ctl.failed = p.pretend ? Waiter::kPretend : 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) tmem_alloc<1>(smem_addr(&ctl.tmem), 128);
@@ -405,7 +405,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
     if (ctas > 1) cluster_sync();   // nobody reads this CTA's memory any more
     __syncthreads();
     tmem_after();
-    if (warp == 0) tmem_free<1>(out, 128);
+    if (*static_cast<volatile int32_t*>(&ctl.failed)) {
+        if (MUON && threadIdx.x == 0) gave_up_on(p.in.nonfinite);
+        let_land();
+    }
+    if (warp == 0) {
+        __syncwarp();
+        tmem_free<1>(out, 128);
+    }
 }
 
 template <bool MUON>
@@ -432,6 +439,7 @@ template <bool MUON>
 bool launch_small(const Group& g, const int32_t* first_sum, const adamw_ortho_t& o, const float* coefs, int32_t dtype,
                   int sms, int32_t piece, SmallParams<MUON>* p, cudaStream_t st) {
     p->steps = o.steps;
+    p->pretend = g_pretend;
     for (int k = 0; k < o.steps; ++k) memcpy(p->coefs[k], coefs + 3 * (k < o.n_coefficients ? k : o.n_coefficients - 1), 12);
     int most = 1;
     int64_t matrices = 0;

@@ -340,11 +340,12 @@ struct Control {
 };
 static_assert(sizeof(Control) <= kControlRoom, "control block");
 
-// One word a device, OR-ed by kernels whose waits ran out.
+// One word a device, set by kernels whose waits ran out.
 __device__ int32_t g_tile_status;
 
 struct Waiter {
-    int32_t* failed;   // the CTA's
+    static constexpr int32_t kPretend = 2;   // to be reported, though no wait has run out
+    int32_t* failed;   // the CTA's: 1, a wait has run out
     // the same answer for all of a warp
     __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity, int k = 0) const {
         return __all_sync(0xffffffffu, (*this)(bar, parity, k));
@@ -358,15 +359,21 @@ struct Waiter {
 #pragma unroll 1
             for (int i = 0; i < 64; ++i)
                 if (barrier_test(bar, parity)) return true;
-            if (*static_cast<volatile int32_t*>(failed)) return false;
+            if (*static_cast<volatile int32_t*>(failed) == 1) return false;
             if (clock64() - start > kGiveUp + k / kStepK * kGiveUpStep) {
                 *static_cast<volatile int32_t*>(failed) = 1;
-                atomicOr(&g_tile_status, 1);
                 return false;
             }
         }
     }
 };
+// A CTA's end after a wait that ran out.
+__device__ __forceinline__ void let_land() {
+    if (threadIdx.x == 0) atomicOr(&g_tile_status, 1);
+    // copies and products in flight land within microseconds: a
+    // millisecond for them before the memory is given back
+    for (int k = 0; k < 1000; ++k) __nanosleep(1000);
+}
 
 // What a staged epilogue has: a warp's buffers of 32 rows of 128 bytes, in the
 // swizzle of the operands (one or two of them, by P::kStaging).
@@ -448,6 +455,8 @@ constexpr int tile_threads() { return 128 + 32 * P::kWarps; }
 //   bf16(p)                              type of the operands
 //   Out: what the epilogue keeps of a tile; out<S>(p, table, tile, rank)
 //   wanted(p, out, row, col): whether the 32 x 32 block there has anything to store
+//   gave_up(p)                           one thread of a CTA, of which a wait ran out
+//   pretend(p)                           whether to say so though none did
 //   kStaging        bytes of shared memory of an epilogue warp
 //   kStaged: the policy takes a tile's epilogue as a whole, through Staged:
 //        begin(p, out, staged, col) asks for what the block at `col` reads, before
@@ -483,7 +492,7 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
             barrier_init(smem_addr(&ctl->acc_empty[a]), P::kWarps * PAIR);
         }
         for (int k = 0; k < P::kWarps; ++k) barrier_init(smem_addr(&ctl->block[k]), 1);
-        ctl->failed = 0;
+        ctl->failed = P::pretend(p) ? Waiter::kPretend : 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2) tmem_alloc<PAIR>(smem_addr(&ctl->tmem), S::kColumns);
@@ -668,9 +677,8 @@ __global__ void __launch_bounds__(tile_threads<P>(), 1) tile_kernel(const __grid
     __syncwarp();
     __syncthreads();
     if (*static_cast<volatile int32_t*>(&ctl->failed)) {
-        // copies and products in flight land within microseconds: a
-        // millisecond for them before the memory is given back
-        for (int k = 0; k < 1000; ++k) __nanosleep(1000);
+        if (threadIdx.x == 0) P::gave_up(p);
+        let_land();
     }
     tmem_before();
     if (PAIR == 2) cluster_sync();   // the other CTA's arrivals, and its reads of this one's memory

@@ -164,7 +164,8 @@ class _FlatOptimizer(torch.optim.Optimizer):
         """Per group, 1 when the last step's gradients held inf or NaN, else 0
         (int32, device).  With clipping, and always with ``Muon``, such a step
         wrote nothing (an AdamW's counter stayed); without clipping the values
-        went through."""
+        went through.  2 (``Muon``): a kernel gave up waiting, and the group's
+        state is undefined: go back to a checkpoint."""
         return [self._buffers_of(g).nonfinite for g in self.param_groups]
 
     @torch.no_grad()

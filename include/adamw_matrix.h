@@ -129,7 +129,9 @@ int adamw_muon_plan_create(const adamw_muon_tensor_t* host_table, int32_t n,
  * hparams: device adamw_muon_hparams_t, 16-byte aligned, so that a captured
  *   step takes other values later.
  * nonfinite: device int32: 1 when a gradient or momentum of the list is inf or
- *   NaN (or their norm beyond fp64); then nothing else is written.  0 otherwise.
+ *   NaN (or their norm beyond fp64); then nothing else is written.  2 added when a
+ *   kernel's bounded wait ran out (adamw_matrix_status says so too): momenta,
+ *   masters and parameters are then undefined.  0 otherwise.
  * No host synchronisation; sums run in a fixed order.
  * Errors: INVALID_ARG, MISALIGNED, CUDA. */
 int adamw_muon_step(adamw_muon_plan_t plan, const adamw_muon_hparams_t* hparams,
@@ -190,6 +192,10 @@ int64_t adamw_expert_backward_workspace(const adamw_matrices_t* dy, const adamw_
  * a kernel's bounded wait ran out (its results are then undefined).
  * Synchronises the device. */
 int adamw_matrix_status(int32_t* out);
+
+/* For tests: while on, the kernels of adamw_orthogonalize and adamw_muon_step
+ * that this process launches report a wait that ran out, though none did. */
+void adamw_matrix_test_expire(int32_t on);
 
 #ifdef __cplusplus
 }

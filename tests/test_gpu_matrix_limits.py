@@ -194,3 +194,45 @@ def test_sums_longer_than_a_fixed_wait():
     close(y, products(x[:, -300:], w[:, :, -300:], [0, 17]), 300)
     del x, w
     torch.cuda.empty_cache()
+
+
+# --------------------------------------------------------- waits that run out --
+
+@pytest.fixture
+def expiring():
+    """Kernels say that a wait of theirs ran out, though none did."""
+    A.adamw_matrix_test_expire(True)
+    yield
+    A.adamw_matrix_test_expire(False)
+    A.adamw_matrix_status()
+
+
+@pytest.mark.parametrize("shapes", [[(64, 48)], [(300, 200)], [(40, 1500), (700, 130)], [(300, 200), (64, 48), (2, 100, 1000)]], ids=str)
+def test_a_step_reports_its_waits(expiring, shapes):
+    """In its own word, without a synchronisation, and in the device's; one whose
+    gradients are not finite besides says both; the next one is as ever."""
+    params = [torch.nn.Parameter(rand(*s, seed=4)) for s in shapes]
+    opt = OPT.Muon(params, lr=1e-2)
+    for bad, word in ((False, 2), (True, 3)):
+        _grads(params, 1)
+        if bad:
+            params[0].grad.view(-1)[0] = float("inf")
+        opt.step()
+        assert int(opt.last_nonfinite[0]) == word
+        assert A.adamw_matrix_status() == 1
+    A.adamw_matrix_test_expire(False)
+    opt.sync_master()
+    _grads(params, 2)
+    opt.step()
+    assert int(opt.last_nonfinite[0]) == 0
+    assert A.adamw_matrix_status() == 0
+
+
+@pytest.mark.parametrize("shape", [(64, 48), (300, 200)], ids=str)
+def test_a_call_reports_its_waits(expiring, shape):
+    x = rand(*shape)
+    y = M.orthogonalize(x)
+    assert A.adamw_matrix_status() == 1
+    A.adamw_matrix_test_expire(False)
+    assert torch.equal(M.orthogonalize(x), y)
+    assert A.adamw_matrix_status() == 0
