@@ -27,7 +27,7 @@
 // side of 32 (kFineSide) G is formed from both fp16 of X and kept as two as well;
 // in one it left up to 8.9e-3 (the worst of 16800 random matrices of a side of 2;
 // 5, 5.4e-3; 8, 3.3e-3; 32, 2.1e-3), in two 8.5e-5.  It costs 8 x 128 19 -> 26 us, 32 x
-// 1000 32 -> 53, and a long Gram product thrice its steps (16 x 8192 243 -> 615), so
+// 1000 27 -> 33, and a long Gram product thrice its steps (16 x 8192 243 -> 615), so
 // sides above, whose worst is below bf16's rounding, keep one.
 #include <algorithm>
 #include <atomic>

@@ -9,13 +9,14 @@
 // Q X takes X and Q as two fp16 each (three products: 22 against 17 us for 64 x 128):
 // in small matrices the roundings of few numbers do not average out (figures in
 // orthogonalize.cu). The sum G = X X^T over the cluster goes through distributed
-// shared memory: each CTA adds up its share of G's rows over all parts, in their
+// shared memory, in fp32: each CTA adds up its share of G over all parts, in their
 // order, and hands the sums to all.
 //
 // Bound by latency: a step is three products one after the other, each half a
 // microsecond of tensor cores and as much between their operands and results in
-// shared memory; a cluster adds two barriers and the exchange, 3 us a step. One
-// 64 x 128 takes 22 us, the Muon step of twelve of 128 x 128 to 512 takes 61.
+// shared memory; a cluster adds two barriers (1.2 us a step) and the exchange (0.3 for a
+// side of 32, 2 for one of 128). One 64 x 128 takes 20 us in a row of them, 64 x 1024 29,
+// 128 x 1024 37, the Muon step of twelve of 128 x 128 to 512 61.
 #pragma once
 
 namespace {
@@ -23,8 +24,8 @@ namespace {
 constexpr int kSmallThreads = 256;
 constexpr int kSmallSide = 128, kSmallMost = 8;   // largest side, CTAs of a cluster
 constexpr uint32_t kPlane = 128 * 128;            // 64 columns of 128 rows of fp16
-// Two planes each for X, what its fp16 leaves, G and Q; what Q's fp16 leaves, in
-// the place of a cluster's parts of G (what theirs leaves is in Q's); what G's leaves.
+// Two planes each for X, what its fp16 leaves, G, Q, what Q's fp16 leaves (a cluster's
+// parts of G, in fp32, have the place of both), and what G's leaves.
 constexpr uint32_t kSmallBytes = 1024 + 12 * kPlane;
 
 template <bool MUON>
@@ -56,70 +57,72 @@ __device__ __forceinline__ uint4 left_of(const float* v) {
     return Fp16::pack(h);
 }
 
-// This CTA's share of G's rows, added up over the cluster's parts (in fp32, from
-// fp16: their roundings together are below that of the sum) and handed to all.
+// A cluster's sums of G go by blocks of 8 x 8, those on and below the diagonal that the
+// matrix has, each in one piece: what eight lanes read or write of another CTA is one row
+// of 128 bytes.  Reads bound this: rows of all of G in fp32 took 41.4 us for 128 x 1024 and 38.1
+// for 64 x 1024; of the half in blocks by 16 bytes 54.2 and 34.6; this 37.0 and 28.5.
+constexpr int kBlocksOfG = 16 * 17 / 2;
+constexpr uint32_t kSums = kBlocksOfG * 256, kSumsLow = kSums + kBlocksOfG * 128;   // behind the parts, in fp32
+static_assert(kSumsLow + (kFineSide / 8) * (kFineSide / 8 + 1) / 2 * 128 <= 4 * kPlane, "in the place of Q");
+
+__device__ __forceinline__ int block_of(int down, int across) { return down * (down + 1) / 2 + across; }
+
+// 16 bytes to the same place of all CTAs of the cluster.
 template <int CTAS>
-__device__ __forceinline__ void add_up(const unsigned char* parts, unsigned char* gs, uint32_t rank) {
-    constexpr int kUnits = 8 / CTAS;   // of eight columns, for each thread
-    uint4 v[kUnits][CTAS];
-    uint32_t at[kUnits];
+__device__ __forceinline__ void hand_out(const unsigned char* at, uint4 g) {
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        const int u = i * kSmallThreads + int(threadIdx.x), row = int(rank) * (128 / CTAS) + u / 16;
-        at[i] = uint32_t(u % 16 / 8) * kPlane + unit_at(row, u % 8);
+    for (int o = 0; o < CTAS; ++o)
+        asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(in_cta(smem_addr(at), uint32_t(o))), "r"(g.x), "r"(g.y),
+                     "r"(g.z), "r"(g.w) : "memory");
+}
+
+// This CTA's share of the blocks, added up over the cluster's parts in their order, and
+// handed to all in fp16, with what that leaves where `fine`.
+template <int CTAS, bool FINE>
+__device__ __forceinline__ void add_up(unsigned char* parts, bool fine, int blocks, uint32_t rank) {
+    const int e = int(threadIdx.x) % 8;
+#pragma unroll 1
+    for (int t = int(rank) + CTAS * (int(threadIdx.x) / 8); t < blocks; t += CTAS * kSmallThreads / 8) {
+        float4 v[CTAS][2];
 #pragma unroll
         for (int o = 0; o < CTAS; ++o)
-            asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(v[i][o].x), "=r"(v[i][o].y), "=r"(v[i][o].z), "=r"(v[i][o].w)
-                         : "r"(in_cta(smem_addr(parts + at[i]), uint32_t(o))) : "memory");
-    }
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-        float t[8];
-        Fp16::unpack(v[i][0], t);
+            for (int half = 0; half < 2; ++half) {
+                float4& w = v[o][half];
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(w.x), "=f"(w.y), "=f"(w.z), "=f"(w.w)
+                             : "r"(in_cta(smem_addr(parts + t * 256 + half * 128 + e * 16), uint32_t(o))) : "memory");
+            }
+        float sum[8];
 #pragma unroll
-        for (int o = 1; o < CTAS; ++o) {
-            float w[8];
-            Fp16::unpack(v[i][o], w);
+        for (int half = 0; half < 2; ++half) {
+            float4 w = v[0][half];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) t[e] += w[e];
+            for (int o = 1; o < CTAS; ++o) w = make_float4(w.x + v[o][half].x, w.y + v[o][half].y, w.z + v[o][half].z, w.w + v[o][half].w);
+            sum[half * 4] = w.x, sum[half * 4 + 1] = w.y, sum[half * 4 + 2] = w.z, sum[half * 4 + 3] = w.w;
         }
-        const uint4 g = Fp16::pack(t);
-#pragma unroll
-        for (int o = 0; o < CTAS; ++o)
-            asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(in_cta(smem_addr(gs + at[i]), uint32_t(o))),
-                         "r"(g.x), "r"(g.y), "r"(g.z), "r"(g.w) : "memory");
+        hand_out<CTAS>(parts + kSums + t * 128 + e * 16, Fp16::pack(sum));
+        if (FINE && fine) hand_out<CTAS>(parts + kSumsLow + t * 128 + e * 16, left_of(sum));
     }
 }
 
-// The same with parts and sum as two fp16 each, for small sides.
-template <int CTAS>
-__device__ __forceinline__ void add_up_fine(const unsigned char* parts, const unsigned char* parts_lo, unsigned char* gs,
-                                            unsigned char* gl, uint32_t rank) {
+// The sums as the tensor cores read them: each block and its transpose.  A warp has two of
+// the n rows of blocks, n even, together as many as any other's, four blocks at a time.
+__device__ __forceinline__ void lay_out(const unsigned char* sums, unsigned char* g, int n) {
+    const int warp = int(threadIdx.x) / 32, lane = int(threadIdx.x) % 32, e = lane % 8;
+    if (warp >= n / 2) return;
 #pragma unroll 1
-    for (int i = 0; i < 8 / CTAS; ++i) {
-        const int u = i * kSmallThreads + int(threadIdx.x), row = int(rank) * (128 / CTAS) + u / 16;
-        const uint32_t at = uint32_t(u % 16 / 8) * kPlane + unit_at(row, u % 8);
-        float t[8] = {};
-#pragma unroll
-        for (int o = 0; o < 2 * CTAS; ++o) {
-            uint4 v;
-            asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                         : "r"(in_cta(smem_addr((o % 2 ? parts_lo : parts) + at), uint32_t(o / 2))) : "memory");
-            float w[8];
-            Fp16::unpack(v, w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) t[e] += w[e];
-        }
-        const uint4 g = Fp16::pack(t), l = left_of(t);
-#pragma unroll
-        for (int o = 0; o < CTAS; ++o) {
-            asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(in_cta(smem_addr(gs + at), uint32_t(o))),
-                         "r"(g.x), "r"(g.y), "r"(g.z), "r"(g.w) : "memory");
-            asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(in_cta(smem_addr(gl + at), uint32_t(o))),
-                         "r"(l.x), "r"(l.y), "r"(l.z), "r"(l.w) : "memory");
-        }
+    for (int i = 0; i <= n; i += 4) {
+        const int q = i + lane / 8 <= n ? i + lane / 8 : n;   // the last one again: the same numbers to the same place
+        const int down = q <= warp ? warp : n - 1 - warp, across = q <= warp ? q : q - warp - 1;
+        const uint32_t from = smem_addr(sums + block_of(down, across) * 128 + e * 16);
+        uint32_t a, b, c, d;
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(from) : "memory");
+        const uint32_t to = smem_addr(g + across / 8 * kPlane + unit_at(down * 8 + e, across % 8));
+        const uint32_t turned = smem_addr(g + down / 8 * kPlane + unit_at(across * 8 + e, down % 8));
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+        __syncwarp();   // a block on the diagonal is written twice
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(turned), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
     }
 }
 
@@ -130,7 +133,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
     __shared__ SmallControl ctl;
     unsigned char* base = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
     unsigned char *xs = base, *xl = base + 2 * kPlane, *gs = base + 4 * kPlane, *qs = base + 6 * kPlane, *ql = base + 8 * kPlane, *gl = base + 10 * kPlane;
-    unsigned char *parts = ql, *parts_lo = qs;   // of G, in a cluster
+    unsigned char* parts = qs;   // of G, in a cluster
 
     const int warp = int(threadIdx.x) / 32, lane = int(threadIdx.x) % 32;
     const uint32_t rank = cluster_rank(), ctas = cluster_size();
@@ -239,6 +242,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
     const uint32_t xa = smem_addr(xs), xla = smem_addr(xl), ga = smem_addr(gs), qa = smem_addr(qs), qla = smem_addr(ql), gla = smem_addr(gl), out = *static_cast<volatile uint32_t*>(&ctl.tmem);
     // what is there of k; all 128 rows and columns are computed, zeros beyond the matrix
     const int side16 = (side + 15) / 16 * 16, mine16 = mine > 0 ? (mine + 15) / 16 * 16 : 16;
+    const int blocks = block_of(side16 / 8, 0);
+    // what a cluster does not add up of G, beyond the matrix
+    if (ctas > 1 && side16 < 128) {
+        for (int i = int(threadIdx.x); i < int(2 * kPlane / 16); i += kSmallThreads) {
+            reinterpret_cast<uint4*>(gs)[i] = make_uint4(0, 0, 0, 0);
+            if (fine) reinterpret_cast<uint4*>(gl)[i] = make_uint4(0, 0, 0, 0);
+        }
+    }
     // D (+)= A B^T over `depth` k; B read K-major, or MN-major (then its rows are k)
     auto issue = [&](uint32_t a, uint32_t b, bool b_mn, int depth, bool add) {
         const uint32_t kind = mma_kind(0, false, b_mn, 128, 128);
@@ -281,7 +292,6 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
             }
         }
         done();
-        unsigned char *plane = (ctas == 1 ? gs : parts) + h * kPlane, *plane_lo = (ctas == 1 ? gl : parts_lo) + h * kPlane;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             float v[32];
@@ -290,20 +300,27 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_kernel(const __grid_co
             for (int e = 0; e < 32; ++e) v[e] *= kUnscale;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                *reinterpret_cast<uint4*>(plane + unit_at(r, i * 4 + j)) = Fp16::pack(v + j * 8);
-                if (fine) *reinterpret_cast<uint4*>(plane_lo + unit_at(r, i * 4 + j)) = left_of(v + j * 8);
+                if (ctas > 1) {
+                    const int across = h * 8 + i * 4 + j;
+                    if (across > r / 8) continue;   // above the diagonal
+                    unsigned char* to = parts + block_of(r / 8, across) * 256 + r % 8 * 16;
+                    *reinterpret_cast<float4*>(to) = *reinterpret_cast<const float4*>(v + j * 8);
+                    *reinterpret_cast<float4*>(to + 128) = *reinterpret_cast<const float4*>(v + j * 8 + 4);
+                    continue;
+                }
+                const uint32_t to = h * kPlane + unit_at(r, i * 4 + j);
+                *reinterpret_cast<uint4*>(gs + to) = Fp16::pack(v + j * 8);
+                if (fine) *reinterpret_cast<uint4*>(gl + to) = left_of(v + j * 8);
             }
         }
         if (ctas > 1) {
             cluster_sync();
-            if (fine) {
-                if (ctas == 2) add_up_fine<2>(parts, parts_lo, gs, gl, rank);
-                else if (ctas == 4) add_up_fine<4>(parts, parts_lo, gs, gl, rank);
-                else add_up_fine<8>(parts, parts_lo, gs, gl, rank);
-            } else if (ctas == 2) add_up<2>(parts, gs, rank);
-            else if (ctas == 4) add_up<4>(parts, gs, rank);
-            else add_up<8>(parts, gs, rank);
+            if (ctas == 2) add_up<2, FINE>(parts, fine, blocks, rank);
+            else if (ctas == 4) add_up<4, FINE>(parts, fine, blocks, rank);
+            else add_up<8, FINE>(parts, fine, blocks, rank);
             cluster_sync();
+            lay_out(parts + kSums, gs, side16 / 8);
+            if (fine) lay_out(parts + kSumsLow, gl, side16 / 8);
         }
         // Q
         ready();

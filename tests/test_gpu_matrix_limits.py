@@ -1,6 +1,8 @@
 """The matrix operators at the ends of what their calls allow: against
 definitions in 64 bits, with the tolerances of test_gpu_experts.py and
 test_gpu_orthogonalize.py unless a test says why it has another."""
+import math
+
 import pytest
 import torch
 
@@ -236,3 +238,53 @@ def test_a_call_reports_its_waits(expiring, shape):
     A.adamw_matrix_test_expire(False)
     assert torch.equal(M.orthogonalize(x), y)
     assert A.adamw_matrix_status() == 0
+
+
+# --------------------------------------------------- sums of G over a cluster --
+
+def _nearly_orthogonal(side, length, seed):
+    """Integers of which every operand of one step is exact in fp16: rows 0 and 1
+    whose product is 1, though its parts over each 128 columns are thousands (more
+    than 11 bits), and row 2, which makes the norm a power of two."""
+    g = torch.Generator().manual_seed(seed)
+    z = torch.zeros(side, length, dtype=torch.int64)
+    z[:2] = torch.randint(-40, 41, (2, length), generator=g)
+    z[0, ::3] = 0   # where the result is the product alone, times row 1
+    z[:2, 3:9] = 0
+    rest = 1 - int(z[0] @ z[1])
+    high = round(rest / 64)
+    z[0, 3], z[1, 3], z[0, 4], z[1, 4] = 1, rest - 64 * high, 64, high
+    size = int((z * z).sum())
+    norm = 1
+    while norm * norm < size:
+        norm *= 2
+    z[2, 5:9] = torch.tensor(_squares(norm * norm - size, 4))
+    assert int((z * z).sum()) == norm * norm and int(z.abs().max()) <= 2048 and int(z[0] @ z[1]) == 1
+    return z, norm
+
+
+def _squares(n, count):
+    """Numbers whose squares add up to n: four always do."""
+    if count == 1:
+        return [math.isqrt(n)] if math.isqrt(n) ** 2 == n else None
+    for a in range(math.isqrt(n), -1, -1):
+        rest = _squares(n - a * a, count - 1)
+        if rest is not None:
+            return [a] + rest
+    return None
+
+
+@pytest.mark.parametrize("side", [33, 64, 128, 20])
+@pytest.mark.parametrize("length", [128, 200, 256, 500, 1000, 1024])
+@pytest.mark.parametrize("turned", [False, True])
+def test_sums_over_a_cluster_are_fp32(side, length, turned):
+    """One step of X <- G X: the sum over the cluster's parts is 1 to the bit, as are
+    the results that consist of it alone (products of integers in fp32)."""
+    for seed in range(4):
+        z, norm = _nearly_orthogonal(side, length, seed)
+        x = z.float().cuda()
+        y = M.orthogonalize(x.mT.contiguous() if turned else x, steps=1, coefficients=(0.0, 1.0, 0.0), dtype=F32)
+        y = (y.mT if turned else y).double().cpu() * float(norm) ** 3
+        alone = (z[0] == 0) & (z[1] != 0)
+        assert int(alone.sum()) > length // 5
+        assert torch.equal(y[0][alone], z[1][alone].double())
