@@ -65,6 +65,7 @@ NORM = {"l2": 0, "max": 1}
 
 # the matrix operators (include/adamw_matrix.h)
 MUON_SCALE = {"spectral": 0, "rms": 1}
+EXPERT_STREAM_ROWS = 16
 
 
 class AdamWError(RuntimeError):

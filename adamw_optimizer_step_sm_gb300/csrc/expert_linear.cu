@@ -315,7 +315,7 @@ struct ExpertOuter {
 // tile kernel streams half as much of zero-padded tokens beside the weights
 // and was slower up to kStreamTokens: 8 tokens through 7 of 16 matrices of
 // 8192 x 2048 (235 MB) 61 us there, 41 here.
-constexpr int kStreamThreads = 256, kStreamRows = 4, kStreamTokens = 16;
+constexpr int kStreamThreads = 256, kStreamRows = 4, kStreamTokens = ADAMW_EXPERT_STREAM_ROWS;
 
 struct StreamParams {
     const uint16_t *x, *w;

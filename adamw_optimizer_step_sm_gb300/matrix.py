@@ -165,7 +165,9 @@ def _rows_product(x, w, transposed, offsets, y):
     lib = A.load()
     a = _byref(_matrices(x))
     b = _byref(w)
-    nbytes = lib.adamw_expert_workspace(a, b)
+    # few tokens are multiplied by the weights as they lie
+    nbytes = 0 if x.shape[0] <= A.EXPERT_STREAM_ROWS and not transposed and y.shape[1] < 1 << 24 \
+        else lib.adamw_expert_workspace(a, b)
     work = _empty(nbytes, dtype=_BYTES, device=x.device) if nbytes else None
     _call(lib.adamw_expert_rows, "adamw_expert_rows", x.device, a, b, transposed, offsets.data_ptr(),
           _byref(_matrices(y)), work.data_ptr() if nbytes else None)

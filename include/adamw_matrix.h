@@ -27,7 +27,7 @@ extern "C" {
 /* A batch of matrices: element (b, r, c) is at b * batch_stride + r *
  * row_stride + c of `data`, in elements; a row's elements are consecutive.
  * Strides are not negative; of what is read they may be 0 (one matrix for all of
- * a batch).  Rows and cols up to 2^31 - 1, offsets 64-bit. */
+ * a batch).  Sizes up to what each call says, offsets 64-bit. */
 typedef struct {
     void* data;
     int64_t batch;
@@ -152,13 +152,15 @@ int adamw_muon_plan_destroy(adamw_muon_plan_t plan);
  * offsets: device int64 [experts + 1], ascending within [0, rows].  Offsets
  *   outside that range are taken to its ends, one below its predecessor to the
  *   predecessor.
- * y must not overlap x or w.  Up to 16 rows the weights are streamed once, at
- *   any alignment, and need no workspace.
+ * y must not overlap x or w.  Up to ADAMW_EXPERT_STREAM_ROWS rows, with transposed = 0
+ *   and y of fewer than 2^24 columns, the weights are streamed once, at any alignment, and
+ *   no workspace is needed, whatever adamw_expert_workspace says.
  * workspace: adamw_expert_workspace(x, w) bytes of device memory, 256-byte
- *   aligned; 0 where data are 16-byte aligned and strides multiples of 8
- *   (others are copied there first).
+ *   aligned; 0 where data are 16-byte aligned, rows do not overlap and strides are
+ *   multiples of 8 (others are copied there first).
  * Errors: INVALID_ARG, MISALIGNED, TOO_LARGE (more than 1024 experts, rows or
  * cols above 2^30), CUDA. */
+#define ADAMW_EXPERT_STREAM_ROWS 16
 int adamw_expert_rows(const adamw_matrices_t* x, const adamw_matrices_t* w, int32_t transposed,
                       const int64_t* offsets, const adamw_matrices_t* y, void* workspace,
                       adamw_stream_t stream);

@@ -288,3 +288,19 @@ def test_sums_over_a_cluster_are_fp32(side, length, turned):
         alone = (z[0] == 0) & (z[1] != 0)
         assert int(alone.sum()) > length // 5
         assert torch.equal(y[0][alone], z[1][alone].double())
+
+
+# ------------------------------------------------------------------ workspaces --
+
+@pytest.mark.parametrize("tokens", [1, A.EXPERT_STREAM_ROWS])
+def test_few_tokens_need_no_copy_of_the_weights(tokens):
+    x, w, at = rand(tokens, 1023), rand(4, 512, 1023, seed=2), offsets_of([0, 0, 1, 1, tokens])
+    M.expert_linear(x, w, at)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    y = M.expert_linear(x, w, at)
+    torch.cuda.synchronize()
+    assert torch.cuda.max_memory_allocated() - before <= 2 * y.numel() * y.element_size() + 4096
+    close(y, products(x, w, [0, 0, 1, 1, tokens]), 1023)
+    check(tokens + 1, 512, 1023, [0, 0, 1, 1, tokens + 1], w=w)   # one more does

@@ -1,6 +1,6 @@
 """Host-side checks of the matrix operators at the ends of what their calls
 allow (no GPU; addresses are never dereferenced)."""
-import pytest
+import torch
 
 from adamw_optimizer_step_sm_gb300 import adamw_sm as A
 from test_matrix_host import BAD, BIG, MIS, P, Q, W, _m, _muon, _muon_options, _options, _status, _w, _x, _y  # noqa: F401
@@ -17,3 +17,16 @@ def test_one_matrix_for_all_experts_is_copied_once():
     assert ws(_x(), _w(batch_stride=96, row_stride=97)) == 4 * one
     assert back(_y(), _x(), _w(batch_stride=0, row_stride=97)) == one
     assert back(_y(row_stride=65), _x(row_stride=97), _w(batch_stride=0)) == (40 * 64 + 40 * 96) * 2
+
+
+def test_few_rows_need_a_workspace_for_the_transposed_product_alone():
+    """Weights that TMA cannot read: streamed up to ADAMW_EXPERT_STREAM_ROWS rows (the
+    call gets as far as the device), copied where they are taken transposed or
+    rows are more."""
+    few = A.EXPERT_STREAM_ROWS
+    odd = _w(row_stride=97)
+    if not torch.cuda.is_available():
+        assert _status(A.adamw_expert_rows, _x(rows=few), odd, 0, 5 << 40, _y(rows=few), 0) == A.ADAMW_ERR_CUDA
+    assert _status(A.adamw_expert_rows, _x(rows=few + 1), odd, 0, 5 << 40, _y(rows=few + 1), 0) == BAD
+    back = _m(data=W, rows=few, cols=96, row_stride=96)
+    assert _status(A.adamw_expert_rows, _m(rows=few, cols=64, row_stride=64), odd, 1, 5 << 40, back, 0) == BAD
