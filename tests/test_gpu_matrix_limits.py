@@ -304,3 +304,62 @@ def test_few_tokens_need_no_copy_of_the_weights(tokens):
     assert torch.cuda.max_memory_allocated() - before <= 2 * y.numel() * y.element_size() + 4096
     close(y, products(x, w, [0, 0, 1, 1, tokens]), 1023)
     check(tokens + 1, 512, 1023, [0, 0, 1, 1, tokens + 1], w=w)   # one more does
+
+
+# ------------------------------------------- the C entry points by themselves --
+
+def _workspace(nbytes):
+    return torch.full((max(nbytes, 1) + 512,), 255, dtype=torch.uint8, device="cuda")   # NaN wherever it is read first
+
+
+@pytest.mark.parametrize("dtype", [BF, HALF, F32], ids=str)
+@pytest.mark.parametrize("n,k", [(64, 96), (33, 45), (300, 264)])
+@pytest.mark.parametrize("tokens", [5, 300])
+def test_outer_is_what_backward_gives(dtype, n, k, tokens):
+    """adamw_expert_outer, with a workspace of exactly its size: the same bits as
+    adamw_expert_backward's gradient, and as sums in 64 bits say; added too, and
+    exchanged (the gradient of transposed weights)."""
+    ends = [0, tokens // 3, tokens // 3, tokens - 1]
+    dy, x, at = rand(tokens, n, seed=3), rand(tokens, k), offsets_of(ends)
+    w = rand(3, n, k, seed=2)
+    nbytes = A.adamw_expert_workspace(M._matrices(dy), M._matrices(x))
+    assert (nbytes > 0) == (n % 8 > 0)
+    work = _workspace(nbytes)
+    stream = torch.cuda.current_stream().cuda_stream
+    for exchanged in (False, True):
+        left, right = (x, dy) if exchanged else (dy, x)
+        dw = torch.full((3, left.shape[1], right.shape[1]), 7.0, dtype=dtype, device="cuda")
+        ref = torch.full_like(dw, 3.0)
+        view = ref.mT if exchanged else ref
+        for accumulate in (0, 1):
+            before = dw.double()
+            A.adamw_expert_outer(M._matrices(left), M._matrices(right), at.data_ptr(), M._matrices(dw), accumulate, work.data_ptr(), stream)
+            M.expert_linear_backward(dy, x, w, at, need=(False, True), d_weight=view, accumulate=bool(accumulate))
+            assert torch.equal(dw, ref)
+            want, size = outer(left, right, ends)
+            close(dw, (want + before, size + before.abs()) if accumulate else (want, size), tokens)
+        assert (work[nbytes:] == 255).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, HALF], ids=str)
+@pytest.mark.parametrize("n,k", [(64, 96), (33, 45), (300, 264)])
+@pytest.mark.parametrize("tokens", [5, 16, 300])
+def test_transposed_rows_are_what_backward_gives(dtype, n, k, tokens):
+    """adamw_expert_rows of the gradient of y, w taken transposed: dx, to the bit."""
+    ends = [1, tokens // 3, tokens // 3, tokens - 1]
+    dy, w, at = rand(tokens, n, dtype=dtype, seed=3), rand(3, n, k, dtype=dtype, seed=2), offsets_of(ends)
+    nbytes = A.adamw_expert_workspace(M._matrices(dy), M._matrices(w))
+    work = _workspace(nbytes)
+    dx = torch.full((tokens, k), 7.0, dtype=dtype, device="cuda")
+    A.adamw_expert_rows(M._matrices(dy), M._matrices(w), 1, at.data_ptr(), M._matrices(dx), work.data_ptr(),
+                        torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(dx, M.expert_linear_backward(dy, rand(tokens, k, dtype=dtype), w, at, need=(True, False))[0])
+    close(dx, products(dy, w.mT, ends), n)
+    assert (work[nbytes:] == 255).all()
+    # and of weights that lie transposed, as they are
+    y = torch.full((tokens, n), 7.0, dtype=F32, device="cuda")
+    turned, x = w.mT.contiguous(), rand(tokens, k, dtype=dtype)
+    work = _workspace(A.adamw_expert_workspace(M._matrices(x), M._matrices(turned)))
+    A.adamw_expert_rows(M._matrices(x), M._matrices(turned), 1, at.data_ptr(), M._matrices(y), work.data_ptr(),
+                        torch.cuda.current_stream().cuda_stream)
+    close(y, products(x, w, ends), k)
