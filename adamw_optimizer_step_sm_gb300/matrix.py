@@ -214,6 +214,8 @@ def expert_linear(x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor, 
         if out is not None:
             raise RuntimeError("out= takes no part in autograd")
         return _ExpertLinear.apply(x, weight, offsets)
+    if out is not None and out.requires_grad and torch.is_grad_enabled():
+        raise RuntimeError("out requires a gradient")
     y = _expert_linear(x, weight, offsets, out)
     if out is not None:
         _written(out)

@@ -363,3 +363,19 @@ def test_transposed_rows_are_what_backward_gives(dtype, n, k, tokens):
     A.adamw_expert_rows(M._matrices(x), M._matrices(turned), 1, at.data_ptr(), M._matrices(y), work.data_ptr(),
                         torch.cuda.current_stream().cuda_stream)
     close(y, products(x, w, ends), k)
+
+
+# --------------------------------------------------------------------- results --
+
+def test_results_that_require_a_gradient_are_refused():
+    """As an in-place write to them is by torch."""
+    x, w, at = rand(6, 8), rand(2, 4, 8, seed=2), offsets_of([0, 3, 6])
+    leaf = torch.zeros(6, 4, dtype=BF, device="cuda").requires_grad_()
+    for out in (leaf, leaf * 1):
+        keep = out.detach().clone()
+        with pytest.raises(RuntimeError, match="gradient"):
+            M.expert_linear(x, w, at, out=out)
+        assert torch.equal(out, keep)
+    with torch.no_grad():
+        M.expert_linear(x, w, at, out=leaf)
+    close(leaf.detach(), products(x, w, [0, 3, 6]), 8)
