@@ -586,8 +586,9 @@ bool run(const typename P::Params& p, int64_t tiles, int units, cudaStream_t st)
 
 int64_t up(int64_t n, int64_t by) { return (n + by - 1) / by; }
 
-// Results that leave by TMA: 16 bits, rows of whole 16 bytes, strides that a map takes.
-bool stages(const adamw_matrices_t& m) { return sixteen(m.dtype) && direct(m); }
+// Results that leave by TMA: 16 bits, rows of whole 16 bytes (it writes whole ones: of a row
+// that ends inside of one, what lies behind it too), strides that a map takes.
+bool stages(const adamw_matrices_t& m) { return sixteen(m.dtype) && m.cols % 8 == 0 && direct(m); }
 bool result_map(CUtensorMap* map, adamw_matrices_t m) {
     if (m.rows <= 1) m.row_stride = padded(m.cols);
     if (m.batch <= 1) m.batch_stride = m.row_stride * m.rows;

@@ -96,7 +96,8 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, i
             ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
 }
 
-// A box of this CTA's shared memory into a tensor; what is outside is left out.
+// A box of this CTA's shared memory into a tensor; what is outside is left out, but for
+// the rest of 16 bytes that a row ends in (measured: it is written).
 __device__ __forceinline__ void store_box(const CUtensorMap* map, int x, int y, int z, uint32_t src) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x), "r"(y),
                  "r"(z), "r"(src) : "memory");

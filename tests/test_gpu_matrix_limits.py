@@ -379,3 +379,51 @@ def test_results_that_require_a_gradient_are_refused():
     with torch.no_grad():
         M.expert_linear(x, w, at, out=leaf)
     close(leaf.detach(), products(x, w, [0, 3, 6]), 8)
+
+
+# --------------------------------------------------- rows that end inside 16 bytes --
+
+@pytest.mark.parametrize("dtype", [BF, HALF, F32], ids=str)
+@pytest.mark.parametrize("cols", [40, 41, 44, 47, 255, 258])
+@pytest.mark.parametrize("tokens", [5, 17, 300])
+def test_what_lies_behind_a_row_stays(dtype, cols, tokens):
+    """Results in views of wider rows, at strides that TMA could take: y, the weights'
+    gradient either way round, and ends of memory."""
+    k, ends = 72, [0, tokens // 2, tokens]
+    x, w, dy, at = rand(tokens, k), rand(2, cols, k, seed=2), rand(tokens, cols, seed=3), offsets_of(ends)
+    wide = (cols + 7) // 8 * 8
+    flat = torch.full((tokens * wide + 64,), 5.0, dtype=dtype, device="cuda")
+    y = flat.as_strided((tokens, cols), (wide, 1))
+    M.expert_linear(x, w, at, out=y)
+    close(y, products(x, w, ends), k)
+    flat.as_strided((tokens, cols), (wide, 1)).fill_(5.0)
+    assert (flat == 5).all()
+    flat = torch.full((2 * 72 * max(wide, 72) * 4 + 64,), 5.0, dtype=dtype, device="cuda")
+    for view in (flat.as_strided((2, k, cols), (k * wide, wide, 1)).mT, flat.as_strided((2, cols, k), (cols * 72, 72, 1))):
+        M.expert_linear_backward(dy, x, w, at, need=(False, True), d_weight=view)
+        close(view, outer(dy, x, ends), tokens)
+        view.fill_(5.0)
+        assert (flat == 5).all()
+    # one row, whose end is the next parameter's beginning
+    M.expert_linear_backward(dy, x[:, :1], w[:1, :, :1], offsets_of([0, tokens]), need=(False, True), d_weight=flat[:cols].view(1, 1, cols).mT)
+    close(flat[:cols].view(1, 1, cols).mT, outer(dy, x[:, :1], [0, tokens]), tokens)
+    assert (flat[cols:] == 5).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, HALF], ids=str)
+@pytest.mark.parametrize("tokens", [9, 300])
+@pytest.mark.parametrize("n,k", [(64, 41), (61, 45), (61, 127), (33, 264)])
+def test_what_lies_behind_a_row_does_not_matter(dtype, tokens, n, k):
+    """NaN between rows of operands that TMA reads as they lie: the same bits as of
+    contiguous ones."""
+    def padded(*shape, seed):
+        t = torch.full((*shape[:-1], (shape[-1] + 7) // 8 * 8 + 8), float("nan"), dtype=dtype, device="cuda")
+        t[..., :shape[-1]] = rand(*shape, dtype=dtype, seed=seed)
+        return t[..., :shape[-1]]
+
+    x, w, dy, at = padded(tokens, k, seed=1), padded(2, n, k, seed=2), padded(tokens, n, seed=3), offsets_of([0, tokens // 2, tokens])
+    args = [t.clone(memory_format=torch.contiguous_format) for t in (dy, x, w)]
+    y, want = M.expert_linear(x, w, at), M.expert_linear(args[1], args[2], at)
+    assert torch.equal(y, want) or tokens <= A.EXPERT_STREAM_ROWS
+    close(y, products(args[1], args[2], [0, tokens // 2, tokens]), k)
+    assert all(torch.equal(a, b) for a, b in zip(M.expert_linear_backward(dy, x, w, at), M.expert_linear_backward(*args, at)))
