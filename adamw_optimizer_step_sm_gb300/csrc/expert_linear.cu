@@ -485,7 +485,7 @@ int check(const adamw_matrices_t* m, bool operand) {
         return ADAMW_ERR_TOO_LARGE;
     const bool any = m->batch > 0 && m->rows > 0 && m->cols > 0;
     if (any && !m->data) return ADAMW_ERR_INVALID_ARG;
-    if (any && m->rows > 1 && m->row_stride < m->cols && !operand) return ADAMW_ERR_INVALID_ARG;   // rows written overlap
+    if (any && !operand && !apart(*m)) return ADAMW_ERR_INVALID_ARG;
     if (!aligned(m->data, uintptr_t(dtype_size(m->dtype)))) return ADAMW_ERR_MISALIGNED;
     return ADAMW_OK;
 }
@@ -702,7 +702,6 @@ int check_outer(const adamw_matrices_t* dy, const adamw_matrices_t* x, const int
     if ((rc = check(dy, true)) != ADAMW_OK || (rc = check(x, true)) != ADAMW_OK || (rc = check(dw, false)) != ADAMW_OK) return rc;
     if (dy->batch != 1 || x->batch != 1 || dy->dtype != x->dtype || dy->rows != x->rows || dw->rows != dy->cols ||
         dw->cols != x->cols || dw->batch < 1 || (accumulate != 0 && accumulate != 1) ||
-        (dw->batch > 1 && dw->rows > 0 && dw->cols > 0 && dw->batch_stride < (dw->rows - 1) * dw->row_stride + dw->cols) ||
         overlap(*dw, *dy) || overlap(*dw, *x))
         return ADAMW_ERR_INVALID_ARG;
     if (dw->batch > kMaxExperts) return ADAMW_ERR_TOO_LARGE;

@@ -983,9 +983,7 @@ int check_matrices(const adamw_matrices_t* m, bool written) {
         return ADAMW_ERR_TOO_LARGE;
     if (m->batch * m->rows * m->cols == 0) return ADAMW_OK;
     if (!m->data) return ADAMW_ERR_INVALID_ARG;
-    if (written && ((m->rows > 1 && m->row_stride < m->cols) ||
-                    (m->batch > 1 && m->batch_stride < (m->rows - 1) * m->row_stride + m->cols)))
-        return ADAMW_ERR_INVALID_ARG;
+    if (written && !apart(*m)) return ADAMW_ERR_INVALID_ARG;
     return aligned(m->data, uintptr_t(dtype_size(m->dtype))) ? ADAMW_OK : ADAMW_ERR_MISALIGNED;
 }
 

@@ -700,6 +700,16 @@ inline bool overlap(const adamw_matrices_t& a, const adamw_matrices_t& b) {
     return reinterpret_cast<uintptr_t>(a.data) < end(b) && reinterpret_cast<uintptr_t>(b.data) < end(a);
 }
 
+// Whether every element of a batch has a place of its own: matrices one after the other,
+// or their rows by turns.
+inline bool apart(const adamw_matrices_t& m) {
+    if (m.batch == 0 || m.rows == 0 || m.cols == 0) return true;
+    if (m.rows > 1 && m.row_stride < m.cols) return false;
+    if (m.batch <= 1) return true;
+    return m.batch_stride >= (m.rows - 1) * m.row_stride + m.cols ||
+           (m.batch_stride >= m.cols && (m.rows == 1 || m.row_stride >= (m.batch - 1) * m.batch_stride + m.cols));
+}
+
 // What the rows of all matrices are a multiple of.
 inline int32_t rows_at(const adamw_matrices_t& m) {
     const int size = dtype_size(m.dtype);

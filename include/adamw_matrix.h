@@ -9,7 +9,8 @@
  * arguments caused.  Buffers belong to the caller and are not kept.  Pointers
  * are not looked up by the calls without a plan: they must be dereferenceable
  * by the current device.  Two calls may run at the same time when they share
- * no output and no workspace.
+ * no output and no workspace.  Whether two arguments overlap goes by their outer
+ * ends.
  *
  * Values: products are summed in fp32 and rounded once, to nearest even, when
  * they are stored (what orthogonalisation keeps between its products is said
@@ -27,7 +28,8 @@ extern "C" {
 /* A batch of matrices: element (b, r, c) is at b * batch_stride + r *
  * row_stride + c of `data`, in elements; a row's elements are consecutive.
  * Strides are not negative; of what is read they may be 0 (one matrix for all of
- * a batch).  Sizes up to what each call says, offsets 64-bit. */
+ * a batch); of what is written no two elements share a place (matrices one after the
+ * other, or their rows by turns).  Sizes up to what each call says, offsets 64-bit. */
 typedef struct {
     void* data;
     int64_t batch;

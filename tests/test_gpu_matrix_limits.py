@@ -427,3 +427,37 @@ def test_what_lies_behind_a_row_does_not_matter(dtype, tokens, n, k):
     assert torch.equal(y, want) or tokens <= A.EXPERT_STREAM_ROWS
     close(y, products(args[1], args[2], [0, tokens // 2, tokens]), k)
     assert all(torch.equal(a, b) for a, b in zip(M.expert_linear_backward(dy, x, w, at), M.expert_linear_backward(*args, at)))
+
+
+@pytest.mark.parametrize("dtype", [BF, HALF, F32], ids=str)
+@pytest.mark.parametrize("n,k", [(64, 96), (33, 45), (300, 264)])
+@pytest.mark.parametrize("room", [0, 3, 8])
+def test_results_whose_rows_alternate(dtype, n, k, room):
+    """Gradients of three experts, row by row in turn, with or without room between
+    them: places between the rows are left as they were."""
+    ends = [0, 130, 131, 297]
+    x, w, dy, at = rand(300, k), rand(3, n, k, seed=2), rand(300, n, seed=3), offsets_of(ends)
+    for turned in (False, True):
+        rows, cols = (k, n) if turned else (n, k)
+        buffer = torch.full((rows, 3, cols + room), 5.0, dtype=dtype, device="cuda")
+        d = buffer.permute(1, 0, 2)[:, :, :cols]
+        d = d.mT if turned else d
+        want, size = outer(dy, x, ends)
+        M.expert_linear_backward(dy, x, w, at, need=(False, True), d_weight=d)
+        close(d, (want, size), 300)
+        first = d.double()
+        M.expert_linear_backward(dy, x, w, at, need=(False, True), d_weight=d, accumulate=True)
+        close(d, (want + first, size + first.abs()), 300)
+        assert (buffer[:, :, cols:] == 5).all()
+
+
+@pytest.mark.parametrize("shape", [(3, 64, 96), (3, 300, 200), (3, 100, 45)], ids=str)
+def test_orthogonalised_rows_that_alternate(shape):
+    x = rand(*shape)
+    want = M.orthogonalize(x)
+    buffer = torch.full((shape[1], 3, shape[2] + 5), 7.0, dtype=BF, device="cuda")
+    y = buffer.permute(1, 0, 2)[:, :, :shape[2]]
+    work = torch.empty(A.adamw_orthogonalize_workspace(*shape), dtype=torch.uint8, device="cuda")
+    A.adamw_orthogonalize(M._matrices(x), M._matrices(y), A.ortho_options(5, M.COEFFICIENTS, 1e-7), work.data_ptr(),
+                          torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(y, want) and (buffer[:, :, shape[2]:] == 7).all()

@@ -30,3 +30,21 @@ def test_few_rows_need_a_workspace_for_the_transposed_product_alone():
     assert _status(A.adamw_expert_rows, _x(rows=few + 1), odd, 0, 5 << 40, _y(rows=few + 1), 0) == BAD
     back = _m(data=W, rows=few, cols=96, row_stride=96)
     assert _status(A.adamw_expert_rows, _m(rows=few, cols=64, row_stride=64), odd, 1, 5 << 40, back, 0) == BAD
+
+
+def test_results_have_places_of_their_own():
+    """Matrices whose rows alternate pass the checks (and get as far as the device);
+    ones that reach into each other do not."""
+    apart = [dict(batch=3, batch_stride=96, row_stride=3 * 96), dict(batch=3, batch_stride=100, row_stride=2 * 100 + 96),
+             dict(batch=3, rows=1, batch_stride=96, row_stride=0)]
+    shared = [dict(batch=3, batch_stride=95, row_stride=3 * 96), dict(batch=3, batch_stride=96, row_stride=3 * 96 - 1),
+              dict(batch=3, batch_stride=0, row_stride=96), dict(batch=2, batch_stride=64 * 96 - 1), dict(batch=3, rows=1, batch_stride=95)]
+    for how, layouts in ((A.ADAMW_ERR_CUDA, apart), (BAD, shared)):
+        if how != BAD and torch.cuda.is_available():
+            continue
+        for layout in layouts:
+            rows = layout.get("rows", 64)
+            src = _m(batch=layout["batch"], rows=rows)
+            assert _status(A.adamw_orthogonalize, src, _m(**dict(layout, data=Q)), _options(), W) == how, layout
+            dy, x = _y(cols=rows, row_stride=64), _x(data=4 << 40)
+            assert _status(A.adamw_expert_outer, dy, x, 5 << 40, _m(**dict(layout, data=Q))) == how, layout
