@@ -15,8 +15,8 @@
 // with the usual coefficients (16 would overflow), and the small entries of
 // large matrices (2^-12 of the norm in a 4096 x 4096 one) stay normal numbers.
 // fp16's 11 bits carry an eighth of bf16's rounding errors: bf16 was 1e-2 (random
-// matrices) to 2e-1 (rank 64 of 768) off the exact iteration, this is 2e-4 to
-// 1.6e-3.  X is kept as hi + lo, two fp16: each step multiplies an error of X in
+// matrices) to 2e-1 (rank 64 of 768) off the exact iteration, this is 5e-4 to
+// 2.5e-3 above a side of 32 (3.3e-3 the worst of 205000).  X is kept as hi + lo, two fp16: each step multiplies an error of X in
 // a direction without singular value by a = 3.44, and a rounding of X itself
 // would be such an error; the rounding of the products' operands (hi alone) is
 // multiplied by Q, which vanishes in such directions.  lo is as fine as fp16's
@@ -28,7 +28,7 @@
 // in one it left up to 8.9e-3 (the worst of 16800 random matrices of a side of 2;
 // 5, 5.4e-3; 8, 3.3e-3; 32, 2.1e-3), in two 8.5e-5.  It costs 8 x 128 19 -> 26 us, 32 x
 // 1000 27 -> 33, and a long Gram product thrice its steps (16 x 8192 243 -> 615), so
-// sides above, whose worst is below bf16's rounding, keep one.
+// sides above, whose worst is below bf16's half step (2^-8), keep one.
 #include <algorithm>
 #include <atomic>
 #include <exception>
@@ -919,8 +919,11 @@ bool run_steps(const Group& g, const adamw_ortho_t& o, const float* coefs, int l
     for (int i = 0; i < g.n; ++i) thin = thin || g.shapes[i].thin, fine = fine || g.shapes[i].fine;
     for (int k = 0; k < o.steps; ++k) {
         // by how much the steps after this one multiply an error of X in a
-        // direction without singular value; up to 16, eleven bits of X are enough
-        // (5e-4 of the result at worst, a matrix of few directions)
+        // direction without singular value; up to 16, X keeps eleven bits.  With both fp16
+        // to the end, sides of 129 to 2048 whose rank is an eighth of them are 0.8e-3 off
+        // instead of 2.5e-3, but random ones 1.4e-3 to 1.8e-3 instead of 1.1e-3 to 1.5e-3 (G
+        // is formed from the first alone, and is then not that of the X it multiplies),
+        // and lists are 1.5 to 5 % slower.
         double later = 1.0;
         for (int i = k + 1; i < o.steps; ++i) later *= std::fabs(double(row(i)[0]));
         const bool low_out = low_in && (later > 16.0 || (thin && k + 1 < o.steps));

@@ -461,3 +461,22 @@ def test_orthogonalised_rows_that_alternate(shape):
     A.adamw_orthogonalize(M._matrices(x), M._matrices(y), A.ortho_options(5, M.COEFFICIENTS, 1e-7), work.data_ptr(),
                           torch.cuda.current_stream().cuda_stream)
     assert torch.equal(y, want) and (buffer[:, :, shape[2]:] == 7).all()
+
+
+# ---------------------------------------------------------- more than five steps --
+
+@pytest.mark.parametrize("shape", [(24, 100), (64, 128), (100, 300), (300, 500), (512, 1024), (1100, 400)], ids=str)
+@pytest.mark.parametrize("steps", [6, 7, 8])
+def test_more_steps_of_the_usual_coefficients(shape, steps):
+    """p(s) = 3.4445 s - 4.775 s^3 + 2.0315 s^5 is no contraction.  After five steps every
+    singular value of these matrices (0.013 of the norm or more, 3.44 times as much a
+    step) is in [0.682, 1.2025], p's extrema; a step takes that to [0.682, 1.134], where
+    |p'| and the differences that a matrix function has in its place, (p(s) -+ p(t)) /
+    (s -+ t), are at most 1.83 (at 1.2025: 3.97, once).  So a step multiplies an error by
+    1.83 (the sixth by 3.97) and adds its own 1.1e-3, beginning at TOL after five, all
+    relative to a norm that is between 0.682 and 1.2025 times the root of the rank."""
+    x = rand(*shape, dtype=F32)
+    room = TOL
+    for k in range(6, steps + 1):
+        room = room * (3.97 if k == 6 else 1.83) + 1.1e-3
+    assert off(M.orthogonalize(x, steps=steps, dtype=F32), exact(x, steps)) < room * 1.2025 / 0.682
