@@ -706,8 +706,9 @@ inline bool apart(const adamw_matrices_t& m) {
     if (m.batch == 0 || m.rows == 0 || m.cols == 0) return true;
     if (m.rows > 1 && m.row_stride < m.cols) return false;
     if (m.batch <= 1) return true;
-    return m.batch_stride >= (m.rows - 1) * m.row_stride + m.cols ||
-           (m.batch_stride >= m.cols && (m.rows == 1 || m.row_stride >= (m.batch - 1) * m.batch_stride + m.cols));
+    using Wide = __int128;   // sizes and strides of any product
+    const Wide rows = Wide(m.rows - 1) * m.row_stride + m.cols, matrices = Wide(m.batch - 1) * m.batch_stride + m.cols;
+    return m.batch_stride >= rows || (m.batch_stride >= m.cols && (m.rows == 1 || m.row_stride >= matrices));
 }
 
 // What the rows of all matrices are a multiple of.

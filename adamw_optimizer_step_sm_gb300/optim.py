@@ -425,9 +425,10 @@ class Muon(_FlatOptimizer):
     One library call per group, no host synchronisation; the rates live on the
     device, so that a captured step follows a schedule: set ``lr`` and call
     ``push_rates`` before each replay, and before the capture if they have
-    changed since the last step (a capture does not record the rates).  A step whose gradients hold inf or NaN writes nothing and
-    is reported by ``last_nonfinite``.  Gradients, masters and checkpoints
-    behave as ``MasterWeightAdamW``'s; ``GlobalClip`` takes both kinds."""
+    changed since the last step (a capture does not record the rates).  A step
+    whose gradients hold inf or NaN writes nothing and is reported by
+    ``last_nonfinite``.  Gradients, masters and checkpoints behave as
+    ``MasterWeightAdamW``'s; ``GlobalClip`` takes both kinds."""
 
     def __init__(self, params, lr: float = 2e-4, momentum: float = 0.95, nesterov: bool = True,
                  weight_decay: float = 0.1, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),

@@ -38,7 +38,7 @@ def test_results_have_places_of_their_own():
     apart = [dict(batch=3, batch_stride=96, row_stride=3 * 96), dict(batch=3, batch_stride=100, row_stride=2 * 100 + 96),
              dict(batch=3, rows=1, batch_stride=96, row_stride=0)]
     shared = [dict(batch=3, batch_stride=95, row_stride=3 * 96), dict(batch=3, batch_stride=96, row_stride=3 * 96 - 1),
-              dict(batch=3, batch_stride=0, row_stride=96), dict(batch=2, batch_stride=64 * 96 - 1), dict(batch=3, rows=1, batch_stride=95)]
+              dict(batch=3, batch_stride=96, row_stride=0), dict(batch=3, batch_stride=0, row_stride=96), dict(batch=2, batch_stride=64 * 96 - 1), dict(batch=3, rows=1, batch_stride=95)]
     for how, layouts in ((A.ADAMW_ERR_CUDA, apart), (BAD, shared)):
         if how != BAD and torch.cuda.is_available():
             continue
@@ -48,3 +48,12 @@ def test_results_have_places_of_their_own():
             assert _status(A.adamw_orthogonalize, src, _m(**dict(layout, data=Q)), _options(), W) == how, layout
             dy, x = _y(cols=rows, row_stride=64), _x(data=4 << 40)
             assert _status(A.adamw_expert_outer, dy, x, 5 << 40, _m(**dict(layout, data=Q))) == how, layout
+
+
+def test_strides_whose_products_pass_64_bits():
+    """Rows of 2^30 at strides of 2^40 reach past 2^64: a batch of them is no less
+    refused where its matrices begin inside each other."""
+    big = dict(batch=2, rows=1 << 30, cols=8, row_stride=1 << 40, batch_stride=1 << 39, data=Q)
+    dy, x = _m(data=4 << 40, rows=4, cols=1 << 30, row_stride=1 << 30), _m(rows=4, cols=8, row_stride=8)
+    assert _status(A.adamw_expert_outer, dy, x, 5 << 40, _m(**dict(big, batch=3, batch_stride=4))) == BAD
+    assert _status(A.adamw_expert_outer, dy, x, 5 << 40, _m(**dict(big, batch=3, batch_stride=1 << 40))) == BAD
