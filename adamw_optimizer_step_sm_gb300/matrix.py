@@ -6,7 +6,9 @@
 
 Every function is one or a few calls into the library (include/adamw_matrix.h
 has the formulas) on the current stream of the tensors' device, and waits for
-nothing.  ``optim.Muon`` is the optimizer whose step orthogonalises.
+nothing.  ``optim.Muon`` is the optimizer whose step orthogonalises.  Every wait
+in a kernel is bounded; one that ran out (results are then undefined) shows in
+``adamw_sm.adamw_matrix_status()``, which synchronises.
 
 Experts: rows offsets[e] to offsets[e + 1] - 1 of [tokens, features] belong to
 expert e; ``offsets`` is int64 [experts + 1] on the device, as for packed
